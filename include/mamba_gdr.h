@@ -1,0 +1,95 @@
+/*
+ * mamba_gdr.h -- C ABI of the gated delta rule: the sequence layer whose state
+ * update first takes back what the state already answers for a key.  It stands
+ * beside mamba_ssd_fwd (mamba_scan.h): the same decay per head, the same
+ * (B, H*P, N) state, the same sequence-fastest layout, and the conventions of
+ * that header (device pointers, host checks before any launch, status codes,
+ * the caller's workspace, graph capture) hold for every call here.
+ *
+ * What the calls compute, per value head h of P channels with state S (P x N)
+ * and key head g = h / (H / G):
+ *     delta_t = softplus(delta_raw[b,h,t] + delta_bias[h]),  a_t = exp(A[h] delta_t)
+ *     b_t     = sigmoid(beta_raw[b,h,t])
+ *     S' = a_t S_(t-1);   u_t = b_t (v_t - S' k_t);   S_t = S' + u_t k_t^T
+ *     y_t = scale * S_t q_t
+ * With MAMBA_FLAG_QK_NORM, q_t and k_t are first divided by
+ * sqrt(their sum of squares + 1e-6).  Without it the keys are taken as they are:
+ * the update is a contraction only while b_t |k_t|^2 <= 2.
+ *
+ * Arguments shared by the calls
+ *   q, k        : (B, G*N, L) in_dtype, channel g*N + n; one key head serves the
+ *                 H / G value heads g*(H/G) .. (g+1)*(H/G) - 1.
+ *   v           : (B, H*P, L) in_dtype, channel h*P + p.
+ *   delta, beta : (B, H, L) in_dtype, raw (before bias and softplus / sigmoid).
+ *   q_stride, k_stride, v_stride : elements from one batch row to the next (at
+ *                 least the row's own size), so that q, k and v may be channel
+ *                 ranges of one convolution's output.
+ *   A           : (H) fp32.  delta_bias : (H) fp32 or NULL (zeros).
+ *   states      : (B, H*P, N) fp32.
+ *   lengths     : (B) int32 on the device, or NULL (every row has L tokens).
+ *                 Row b ends after lengths[b] tokens (values are held to 0 .. L):
+ *                 what its inputs hold behind that is not looked at, be it NaN,
+ *                 its outputs and gradients there are zero, and its final state is
+ *                 the one after lengths[b] tokens.
+ *
+ * Sizes: 1 <= N <= 128; B, H, G, P, L >= 1; H a multiple of G; B*H*P*L and
+ * B*G*N*L < 2^46.  in_dtype and the output dtypes may each be MAMBA_F32 or
+ * MAMBA_BF16.  Alignment: every array to its element size (16 bytes, and sizes that
+ * are multiples of a vector, select vector accesses); workspaces 256 bytes.
+ * State, gates and sums are fp32 or better; the results are deterministic
+ * (sums in a fixed order, no atomics) and do not depend on the other rows of the batch.
+ */
+#ifndef MAMBA_GDR_H_
+#define MAMBA_GDR_H_
+
+#include "mamba_scan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MAMBA_FLAG_QK_NORM 0x4u          /* unit-length queries and keys */
+
+/*
+ * Bytes of workspace mamba_gdr_fwd needs (sizes only; callable without a GPU);
+ * 0 when it needs none, (size_t)-1 for an invalid or unsupported shape.
+ */
+size_t mamba_gdr_workspace_size(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
+                                mamba_dtype_t in_dtype);
+
+/*
+ * The rule over whole sequences.
+ *   initial_state : (B, H*P, N) fp32 or NULL (zeros).
+ *   y             : (B, H*P, L) out_dtype, written.
+ *   final_state   : (B, H*P, N) fp32, written, or NULL.
+ */
+int mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* delta, const void* beta,
+                  const float* A, const float* delta_bias, const float* initial_state,
+                  const int32_t* lengths, void* y, float* final_state,
+                  int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
+                  int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                  mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token for every batch row, on a pool of states updated in place.
+ *   state : (n_slots, H*P, N) fp32.
+ *   slots : (B) int32 on the device: the state of row b is state[slots[b]]; NULL
+ *           takes state[b] (then n_slots >= B is required).  A row whose slot is
+ *           negative or not below n_slots is empty: its y is zero and no state is
+ *           read or written for it.  A slot named by two rows of one call leaves
+ *           that state unspecified (the rows run at the same time).
+ *   q, k  : (B, G*N); v : (B, H*P); delta, beta : (B, H); y : (B, H*P) out_dtype,
+ *           written.  No workspace is used.
+ */
+int mamba_gdr_update(float* state, const int32_t* slots, const void* q, const void* k, const void* v,
+                     const void* delta, const void* beta, const float* A, const float* delta_bias, void* y,
+                     int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t n_slots,
+                     int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                     mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MAMBA_GDR_H_ */

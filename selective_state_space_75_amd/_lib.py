@@ -1,4 +1,5 @@
-"""ctypes binding of libmamba_scan.so (the C ABI of include/mamba_scan.h).
+"""ctypes binding of libmamba_scan.so (the C ABI of include/mamba_scan.h,
+include/mamba_gdr.h and include/mamba_state_cache.h).
 
 Argument marshalling only: tensors are checked (device, dtype, shape,
 contiguity), outputs and the workspace are allocated with torch, and raw
@@ -18,6 +19,7 @@ LIB_PATH = os.path.join(PKG, "libmamba_scan.so")
 MAMBA_F32, MAMBA_BF16 = 0, 1
 FLAG_DELTA_B = 0x1
 FLAG_ACCURATE_EXPM1 = 0x2
+FLAG_QK_NORM = 0x4
 
 STATUS = {
     0: "MAMBA_OK", -1: "MAMBA_ERR_NULL", -2: "MAMBA_ERR_SHAPE", -3: "MAMBA_ERR_DTYPE",
@@ -72,6 +74,17 @@ def lib() -> ctypes.CDLL:
             L.mamba_ssd_fwd.restype = c_int
             L.mamba_ssd_workspace_size.argtypes = [i64] * 5
             L.mamba_ssd_workspace_size.restype = ctypes.c_size_t
+            f32, sz = ctypes.c_float, ctypes.c_size_t
+            L.mamba_gdr_workspace_size.argtypes = [i64] * 6 + [c_int]
+            L.mamba_gdr_workspace_size.restype = sz
+            L.mamba_gdr_fwd.argtypes = [vp] * 11 + [i64] * 9 + [f32, c_int, c_int, u32, vp, sz, vp]
+            L.mamba_gdr_fwd.restype = c_int
+            L.mamba_gdr_update.argtypes = [vp] * 10 + [i64] * 9 + [f32, c_int, c_int, u32, vp]
+            L.mamba_gdr_update.restype = c_int
+            L.mamba_state_cache_write.argtypes = [vp] * 4 + [i64] * 3 + [c_int, vp]
+            L.mamba_state_cache_write.restype = c_int
+            L.mamba_state_cache_read.argtypes = [vp] * 4 + [i64] * 3 + [c_int, vp]
+            L.mamba_state_cache_read.restype = c_int
             L.mamba_scan_kernel.argtypes = [i64, i64, i64, i64]
             L.mamba_scan_kernel.restype = c_int
             L.mamba_set_test_knobs.argtypes = [ctypes.POINTER(TestKnobs)]
@@ -459,4 +472,206 @@ def scan_bwd(u, delta, z, Bt, Ct, A, Dskip, delta_bias, dy, *, grad_dtype=None, 
         _stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_scan_bwd")
+    return out
+
+
+# ----------------------------------------------------------------------------- gated delta rule
+def _check_rows(t, name, shape, dtype, device):
+    """Like _check for (B, C, ...) tensors whose batch rows are each dense: a
+    channel range of a wider tensor is taken as it is.  Returns the row stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    row = 1
+    for n in shape[1:]:
+        row *= n
+    if not t[:1].is_contiguous() or (shape[0] > 1 and t.stride(0) < row):
+        raise ValueError("%s must be dense within each batch row" % name)
+    return t.stride(0) if shape[0] > 1 else row
+
+
+def _gdr_sizes(q, v, delta, groups, dims):
+    """(B, H, G, P, N) from the arguments' shapes."""
+    if q.dim() != dims or v.dim() != dims or delta.dim() != dims:
+        raise ValueError("q, v and delta must have %d dimensions" % dims)
+    B, H = delta.shape[:2]
+    G = H if groups is None else int(groups)
+    if G < 1 or H % G or q.shape[1] % G or v.shape[1] % H or not q.shape[1] or not v.shape[1]:
+        raise ValueError("q has %d channels, v %d and delta %d heads, which do not divide into %d key heads"
+                         % (q.shape[1], v.shape[1], H, G))
+    if q.device.type != "cuda":
+        raise ValueError("inputs must be on a GPU device")
+    _dtype_code(q)
+    return B, H, G, v.shape[1] // H, q.shape[1] // G
+
+
+def _gdr_scale(scale, N):
+    return float(N) ** -0.5 if scale is None else float(scale)
+
+
+def gdr_workspace_size(B: int, H: int, G: int, P: int, N: int, L: int, dtype=None) -> int:
+    """Bytes gdr_fwd needs for these sizes and this input dtype (bfloat16 by default)."""
+    code = MAMBA_F32 if dtype is not None and dtype == _torch().float32 else MAMBA_BF16
+    n = lib().mamba_gdr_workspace_size(B, H, G, P, N, L, code)
+    if n == ctypes.c_size_t(-1).value:
+        raise MambaError(-2, "mamba_gdr_workspace_size")
+    return n
+
+
+def _workspace(workspace, need, dev):
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    if workspace.device != dev:
+        raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def gdr_fwd(q, k, v, delta, beta, A, delta_bias=None, *, groups=None, initial_state=None, lengths=None,
+            qk_norm=False, scale=None, return_final_state=False, out_dtype=None, y=None, final_state=None,
+            workspace=None, stream=None):
+    """Gated delta rule over whole sequences (include/mamba_gdr.h).
+
+    q, k: (B, G*N, L); v: (B, H*P, L); delta, beta: (B, H, L), raw; A, delta_bias: (H)
+    fp32.  groups = G (default H) key heads serve the H heads of delta.  q, k and v may be
+    channel ranges of a wider tensor.  initial_state: (B, H*P, N) fp32; lengths: (B)
+    int32, tokens per row; scale: default N**-0.5.
+
+    Returns y (B, H*P, L), or (y, final_state (B, H*P, N) fp32) when return_final_state.
+    """
+    torch = _torch()
+    B, H, G, P, N = _gdr_sizes(q, v, delta, groups, 3)
+    L, dev, in_dt = q.shape[2], q.device, q.dtype
+    qs = _check_rows(q, "q", (B, G * N, L), in_dt, dev)
+    ks = _check_rows(k, "k", (B, G * N, L), in_dt, dev)
+    vs = _check_rows(v, "v", (B, H * P, L), in_dt, dev)
+    _check(delta, "delta", (B, H, L), in_dt, dev)
+    _check(beta, "beta", (B, H, L), in_dt, dev)
+    _check(A, "A", (H,), torch.float32, dev)
+    _check(delta_bias, "delta_bias", (H,), torch.float32, dev)
+    _check(initial_state, "initial_state", (B, H * P, N), torch.float32, dev)
+    _check(lengths, "lengths", (B,), torch.int32, dev)
+    out_dt = in_dt if out_dtype is None else out_dtype
+    with torch.cuda.device(dev):
+        if y is None:
+            y = torch.empty((B, H * P, L), dtype=out_dt, device=dev)
+        _check(y, "y", (B, H * P, L), out_dt, dev)
+        if return_final_state:
+            if final_state is None:
+                final_state = torch.empty((B, H * P, N), dtype=torch.float32, device=dev)
+            _check(final_state, "final_state", (B, H * P, N), torch.float32, dev)
+        workspace = _workspace(workspace, gdr_workspace_size(B, H, G, P, N, L, in_dt), dev)
+        st = lib().mamba_gdr_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(beta), _ptr(A), _ptr(delta_bias), _ptr(initial_state),
+            _ptr(lengths), _ptr(y), _ptr(final_state if return_final_state else None), B, H, G, P, N, L, qs, ks, vs,
+            _gdr_scale(scale, N), _dtype_code(q), _dtype_code(y), FLAG_QK_NORM if qk_norm else 0,
+            _ptr(workspace), _nbytes(workspace), _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_gdr_fwd")
+    return (y, final_state) if return_final_state else y
+
+
+def gdr_update(state, q, k, v, delta, beta, A, delta_bias=None, *, groups=None, slots=None, qk_norm=False,
+               scale=None, out_dtype=None, y=None, stream=None):
+    """One token of the gated delta rule for every row; `state` (S, H*P, N) fp32 is
+    updated in place at the rows' slots (int32 (B); None: row b has state b; negative:
+    an empty row, y = 0).  q, k: (B, G*N); v: (B, H*P); delta, beta: (B, H).  Returns y
+    (B, H*P)."""
+    torch = _torch()
+    B, H, G, P, N = _gdr_sizes(q, v, delta, groups, 2)
+    dev, in_dt = q.device, q.dtype
+    if state.dim() != 3:
+        raise ValueError("state must be (S, H*P, N)")
+    S = state.shape[0]
+    qs = _check_rows(q, "q", (B, G * N), in_dt, dev)
+    ks = _check_rows(k, "k", (B, G * N), in_dt, dev)
+    vs = _check_rows(v, "v", (B, H * P), in_dt, dev)
+    _check(delta, "delta", (B, H), in_dt, dev)
+    _check(beta, "beta", (B, H), in_dt, dev)
+    _check(A, "A", (H,), torch.float32, dev)
+    _check(delta_bias, "delta_bias", (H,), torch.float32, dev)
+    _check(state, "state", (S, H * P, N), torch.float32, dev)
+    _check(slots, "slots", (B,), torch.int32, dev)
+    out_dt = in_dt if out_dtype is None else out_dtype
+    with torch.cuda.device(dev):
+        if y is None:
+            y = torch.empty((B, H * P), dtype=out_dt, device=dev)
+        _check(y, "y", (B, H * P), out_dt, dev)
+        st = lib().mamba_gdr_update(
+            _ptr(state), _ptr(slots), _ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(beta), _ptr(A), _ptr(delta_bias),
+            _ptr(y), B, H, G, P, N, S, qs, ks, vs, _gdr_scale(scale, N), _dtype_code(q), _dtype_code(y),
+            FLAG_QK_NORM if qk_norm else 0, _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_gdr_update")
+    return y
+
+
+# ----------------------------------------------------------------------------- 8-bit state cache
+CACHE_GROUP = 32
+
+
+def state_cache(n_slots: int, n: int, device):
+    """An empty cache of n_slots rows of n numbers: (codes int8 (n_slots, n), exps uint8
+    (n_slots, ceil(n / 32))).  Every row reads as zeros until it is written."""
+    torch = _torch()
+    return (torch.zeros((n_slots, n), dtype=torch.int8, device=device),
+            torch.zeros((n_slots, (n + CACHE_GROUP - 1) // CACHE_GROUP), dtype=torch.uint8, device=device))
+
+
+def _cache_args(codes, exps, slots, state, what):
+    torch = _torch()
+    if codes.dim() != 2:
+        raise ValueError("codes must be (n_slots, n)")
+    S, n = codes.shape
+    dev = codes.device
+    if dev.type != "cuda":
+        raise ValueError("%s must be on a GPU device" % what)
+    _check(codes, "codes", (S, n), torch.int8, dev)
+    _check(exps, "exps", (S, (n + CACHE_GROUP - 1) // CACHE_GROUP), torch.uint8, dev)
+    if state.dim() < 1 or not state.shape[0] or state.numel() != state.shape[0] * n:
+        raise ValueError("%s has shape %s, expected (rows, ...) with %d numbers a row" % (what, tuple(state.shape), n))
+    _dtype_code(state)
+    _check(state, what, tuple(state.shape), None, dev)
+    _check(slots, "slots", (state.shape[0],), torch.int32, dev)
+    return state.shape[0], n, S, dev
+
+
+def state_cache_write(state, codes, exps, *, slots=None, stream=None):
+    """Keep the rows of `state` (rows, ...) fp32 or bf16 in 8 bits (include/
+    mamba_state_cache.h): row r in slot slots[r] (int32 (rows); None: slot r;
+    negative: not kept) of codes (n_slots, n) int8 and exps (n_slots, ceil(n / 32)) uint8."""
+    rows, n, S, dev = _cache_args(codes, exps, slots, state, "state")
+    with _torch().cuda.device(dev):
+        st = lib().mamba_state_cache_write(_ptr(state), _ptr(slots), _ptr(codes), _ptr(exps), rows, n, S,
+                                           _dtype_code(state), _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_state_cache_write")
+
+
+def state_cache_read(codes, exps, *, slots=None, out=None, dtype=None, stream=None):
+    """Rows of an 8-bit state cache: out[r] = the row kept in slot slots[r] (int32
+    (rows); None: every slot in order; negative: zeros).  `out` (rows, ...) fp32 or bf16
+    is written when given, else a (rows, n) tensor of `dtype` (fp32) is made."""
+    torch = _torch()
+    if out is None:
+        rows = codes.shape[0] if slots is None else slots.shape[0]
+        out = torch.empty((rows, codes.shape[1]), dtype=dtype or torch.float32, device=codes.device)
+    rows, n, S, dev = _cache_args(codes, exps, slots, out, "out")
+    with torch.cuda.device(dev):
+        st = lib().mamba_state_cache_read(_ptr(codes), _ptr(exps), _ptr(slots), _ptr(out), rows, n, S,
+                                          _dtype_code(out), _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_state_cache_read")
     return out

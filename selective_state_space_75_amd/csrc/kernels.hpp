@@ -156,6 +156,35 @@ struct SsdParams {
   int vec;      // L % 8 == 0 and every pointer 16-byte aligned
 };
 
+// Gated delta rule: H value heads of P channels, G key heads of N numbers
+// (head h uses key head h / (H / G)), one P x N state per value head.
+constexpr float kGdrNormEps = 1e-6f;    // added to a key's or query's sum of squares before the root
+
+struct GdrParams {
+  const void *q, *k, *v, *delta, *beta;         // in dtype: q, k (B, G N, L); v (B, H P, L); delta, beta (B, H, L)
+  const float *A, *bias;                        // (H); bias may be null
+  const float* init;                            // (B or n_slots, H P, N) or null (zeros)
+  const int32_t* lengths;                       // (B) or null
+  const int32_t* slots;                         // (B) or null: states of the pool `init` / `final_state`
+  void* y;                                      // (B, H P, L) out dtype
+  float* final_state;                           // like init, or null
+  int64_t B, H, G, P, N, L, n_slots;
+  int64_t q_stride, k_stride, v_stride;         // elements from one batch row to the next
+  float scale;
+  int norm;                                     // q and k scaled to unit length first
+  int state_vec;                                // N % 4 == 0, states 16-byte aligned
+};
+
+// Rows of state in 8 bits.
+struct CacheParams {
+  void* state;              // (rows, n)
+  const int32_t* slots;     // (rows) or null
+  int8_t* codes;            // (n_slots, n)
+  uint8_t* exps;            // (n_slots, groups)
+  int64_t rows, n, groups, n_slots;
+  int vec;                  // n % 4 == 0 and aligned for four numbers at a time
+};
+
 // Each returns hipSuccess or the launch error.
 hipError_t launch_scan_full(const ScanParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_scan_summary(const ScanParams& p, Dt in, hipStream_t s);
@@ -170,5 +199,7 @@ hipError_t launch_scan_bwd(const BwdParams& p, Dt in, Dt grad, hipStream_t s);
 hipError_t launch_conv1d_fwd(const ConvParams& p, Dt in, Dt out, bool vec, hipStream_t s);
 hipError_t launch_conv1d_update(const ConvParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_ssd(const SsdParams& p, Dt out, hipStream_t s);
+hipError_t launch_gdr_step(const GdrParams& p, Dt in, Dt out, hipStream_t s);
+hipError_t launch_state_cache(const CacheParams& p, Dt dt, bool write, hipStream_t s);
 
 }  // namespace mamba

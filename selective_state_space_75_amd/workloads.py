@@ -37,6 +37,7 @@ BLOCK = 1 << 22
 _ID_PARAMS, _ID_DELTA, _ID_U, _ID_Z, _ID_B, _ID_C, _ID_STATE = range(7)
 _ID_CONV_X, _ID_CONV_PARAMS, _ID_CONV_STATE = range(7, 10)
 _ID_SSD_PARAMS, _ID_SSD_X, _ID_SSD_DT, _ID_SSD_Z, _ID_SSD_B, _ID_SSD_C = range(10, 16)
+_ID_GDR_PARAMS, _ID_GDR_Q, _ID_GDR_K, _ID_GDR_V, _ID_GDR_DT, _ID_GDR_BETA, _ID_GDR_S, _ID_GDR_DY = range(16, 24)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -342,4 +343,26 @@ def ssd_inputs(B: int, H: int, P: int, N: int, L: int, seed: int, gate: bool = T
         "Ct": f32_to_bf16_bits(_normal_f32([seed, _ID_SSD_C], B * N * L)).reshape(bc),
         "z": f32_to_bf16_bits(_normal_f32([seed, _ID_SSD_Z], B * D * L)).reshape(big) if gate else None,
     }
+    return out
+
+
+# ----------------------------------------------------------------------------- gated delta rule
+def gdr_inputs(B: int, H: int, G: int, P: int, N: int, L: int, dtype: str, seed: int, unit_qk: bool = False) -> dict:
+    """q, k (B, G N, L), v, dy (B, H P, L), delta_raw, beta_raw (B, H, L) ~ N(0, 1) in
+    `dtype` (bf16 as uint16 bit patterns); q and k scaled to unit length per token when
+    unit_qk; initial_state, dfinal_state (B, H P, N) ~ N(0, 0.1) fp32; A and delta_bias
+    per head as in ssd_inputs."""
+    g = np.random.Generator(np.random.PCG64(np.random.SeedSequence([seed, _ID_GDR_PARAMS])))
+    dt = np.exp(g.uniform(np.log(1e-3), np.log(1e-1), size=H))
+    out = {"delta_bias": np.log(np.expm1(dt)).astype(np.float32),
+           "A": (-g.uniform(1.0, 16.0, size=H)).astype(np.float32)}
+    for name, i, rows in (("q", _ID_GDR_Q, G * N), ("k", _ID_GDR_K, G * N), ("v", _ID_GDR_V, H * P),
+                          ("delta_raw", _ID_GDR_DT, H), ("beta_raw", _ID_GDR_BETA, H), ("dy", _ID_GDR_DY, H * P)):
+        x = _normal_f32([seed, i], B * rows * L).reshape(B, rows, L)
+        if unit_qk and name in ("q", "k"):
+            y = x.reshape(B, G, N, L)
+            x = (y / np.sqrt((y * y).sum(2, keepdims=True) + np.float32(1e-12))).reshape(B, rows, L)
+        out[name] = _store(x, dtype)
+    st = _normal_f32([seed, _ID_GDR_S], 2 * B * H * P * N).reshape(2, B, H * P, N) * np.float32(0.1)
+    out["initial_state"], out["dfinal_state"] = st[0].copy(), st[1].copy()
     return out
