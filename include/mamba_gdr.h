@@ -88,6 +88,17 @@ int mamba_gdr_update(float* state, const int32_t* slots, const void* q, const vo
                      int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
                      mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags, hipStream_t stream);
 
+/*
+ * Test and diagnostic knobs, process-wide like mamba_set_test_knobs: how a call is
+ * carried out, never what it computes (to fp32 rounding).  A workspace size asked
+ * for before a change does not fit a call after it.
+ *   kernel   : 0 the planner's choice; 1 token by token; 2 in chunks.
+ *   segments : > 0: mamba_gdr_fwd in chunks cuts L into this many segments (at most one
+ *              per chunk of 32 tokens); 0: the planner decides.
+ * Returns MAMBA_ERR_SHAPE for other values.
+ */
+int mamba_gdr_set_test_knobs(int kernel, int64_t segments);
+
 #ifdef __cplusplus
 }
 #endif

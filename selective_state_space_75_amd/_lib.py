@@ -81,6 +81,8 @@ def lib() -> ctypes.CDLL:
             L.mamba_gdr_fwd.restype = c_int
             L.mamba_gdr_update.argtypes = [vp] * 10 + [i64] * 9 + [f32, c_int, c_int, u32, vp]
             L.mamba_gdr_update.restype = c_int
+            L.mamba_gdr_set_test_knobs.argtypes = [c_int, i64]
+            L.mamba_gdr_set_test_knobs.restype = c_int
             L.mamba_state_cache_write.argtypes = [vp] * 4 + [i64] * 3 + [c_int, vp]
             L.mamba_state_cache_write.restype = c_int
             L.mamba_state_cache_read.argtypes = [vp] * 4 + [i64] * 3 + [c_int, vp]
@@ -509,6 +511,29 @@ def _gdr_sizes(q, v, delta, groups, dims):
         raise ValueError("inputs must be on a GPU device")
     _dtype_code(q)
     return B, H, G, v.shape[1] // H, q.shape[1] // G
+
+
+GDR_KERNELS = {"planner": 0, "token": 1, "chunk": 2}
+
+
+class gdr_test_knobs:  # noqa: N801 (used as a context manager)
+    """``with gdr_test_knobs(kernel="chunk", segments=3): ...`` sets the gated delta
+    rule's test knobs (mamba_gdr_set_test_knobs) for the block and restores the
+    planner's choices after it."""
+    __test__ = False   # not a pytest test class
+
+    def __init__(self, kernel: str = "planner", segments: int = 0):
+        self.args = (GDR_KERNELS[kernel], segments)
+
+    def __enter__(self):
+        st = lib().mamba_gdr_set_test_knobs(*self.args)
+        if st != 0:
+            raise MambaError(st, "mamba_gdr_set_test_knobs")
+        return self
+
+    def __exit__(self, *exc):
+        lib().mamba_gdr_set_test_knobs(0, 0)
+        return False
 
 
 def _gdr_scale(scale, N):

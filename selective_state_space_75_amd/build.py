@@ -30,10 +30,11 @@ def sources():
 
 FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Wall"]
-# Per-file additions.  ssd.hip: MFMA accumulators in ordinary VGPRs, so the
-# state the SSD kernels update with both MFMA and VALU instructions is not
+# Per-file additions.  ssd.hip, gdr_*.hip: MFMA accumulators in ordinary VGPRs,
+# so the state these kernels update with both MFMA and VALU instructions is not
 # copied between AGPRs and VGPRs every chunk.
-FILE_FLAGS = {"ssd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+_MFMA_VGPR = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+FILE_FLAGS = {"ssd.hip": _MFMA_VGPR, "gdr_chunk.hip": _MFMA_VGPR, "gdr_bwd.hip": _MFMA_VGPR}
 NOISE = "is not a recognized feature for this target"
 
 

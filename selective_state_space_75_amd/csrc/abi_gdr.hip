@@ -1,6 +1,8 @@
 // abi_gdr.hip -- the C ABI declared in include/mamba_gdr.h and
 // include/mamba_state_cache.h: argument checks, workspace plans and launches.
 // Every check runs before any HIP call.
+#include <atomic>
+
 #include "kernels.hpp"
 #include "mamba_gdr.h"
 #include "mamba_state_cache.h"
@@ -55,6 +57,59 @@ mamba::GdrParams gdr_params(const void* q, const void* k, const void* v, const v
   return p;
 }
 
+// Test knobs (mamba_gdr_set_test_knobs), read once per call.
+std::atomic<int> g_kernel{0};
+std::atomic<int64_t> g_segments{0};
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct GdrPlan {
+  bool chunk = false;
+  int64_t n_chunks = 0, S = 1, seg_chunks = 0;
+  size_t off_planes = 0, off_vec = 0, off_M = 0, off_h = 0, off_start = 0, bytes = 0;
+};
+
+// Sizes-only plan of the forward pass.  Up to 24 tokens go token by token (one
+// launch).  In chunks, L is cut into segments when the 16-channel waves of all
+// heads would leave SIMDs idle (there are 1024): the summary launch then adds
+// the N transition rows to the P value rows of every head, so fewer than three
+// segments do not pay.
+GdrPlan make_gdr_plan(int64_t B, int64_t H, int64_t P, int64_t N, int64_t L) {
+  GdrPlan q;
+  const int kernel = g_kernel.load();
+  q.chunk = kernel == 2 || (kernel == 0 && L > 24);
+  if (!q.chunk) return q;
+  q.n_chunks = (L + mamba::kGdrChunk - 1) / mamba::kGdrChunk;
+  const int64_t waves = B * H * ((P + 15) / 16);
+  int64_t S = waves <= 512 ? 2048 / waves : 1;
+  if (S > q.n_chunks / 16) S = q.n_chunks / 16;
+  if (S > 32) S = 32;
+  if (S < 3) S = 1;
+  const int64_t forced = g_segments.load();
+  if (forced > 0) S = forced < q.n_chunks ? forced : q.n_chunks;
+  q.seg_chunks = (q.n_chunks + S - 1) / S;
+  q.S = (q.n_chunks + q.seg_chunks - 1) / q.seg_chunks;
+  const size_t blocks = size_t(B) * H * q.n_chunks;
+  size_t o = 0;
+  q.off_planes = o; o += align256(blocks * 6 * mamba::kGdrPlane * sizeof(uint16_t));
+  q.off_vec = o; o += align256(blocks * mamba::kGdrVec * sizeof(float));
+  if (q.S > 1) {
+    const size_t heads = size_t(B) * H;
+    q.off_M = o; o += align256(heads * (q.S - 1) * N * N * sizeof(float));
+    q.off_h = o; o += align256(heads * (q.S - 1) * P * N * sizeof(float));
+    q.off_start = o; o += align256(heads * q.S * P * N * sizeof(float));
+  }
+  q.bytes = o;
+  return q;
+}
+
+// Workgroups of the largest launch of a plan.
+bool gdr_grid_ok(const GdrPlan& q, int64_t B, int64_t H, int64_t G, int64_t P, int64_t N) {
+  if (!q.chunk) return B * H * ((P + 3) / 4) / 4 + 1 < kMaxGrid;
+  const int64_t slices = (P + 63) / 64 + (q.S > 1 ? (N + 63) / 64 : 0);
+  return B * G < kMaxGrid / q.n_chunks && B * H < kMaxGrid / (q.S * slices) && B * H < kMaxGrid / ((P + 15) / 16);
+}
+
 int check_cache(const void* state, const int32_t* slots, const void* codes, const void* exps, int64_t rows, int64_t n,
                 int64_t n_slots, int dtype) {
   if (!dtype_ok(dtype)) return MAMBA_ERR_DTYPE;
@@ -83,7 +138,7 @@ extern "C" {
 size_t mamba_gdr_workspace_size(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
                                 mamba_dtype_t in_dtype) {
   if (!dtype_ok(in_dtype) || !gdr_sizes_ok(B, H, G, P, N, L) || N > 128) return (size_t)-1;
-  return 0;
+  return make_gdr_plan(B, H, P, N, L).bytes;
 }
 
 int mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* delta, const void* beta, const float* A,
@@ -101,13 +156,30 @@ int mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* delta
   for (const void* ptr : {(const void*)A, (const void*)delta_bias, (const void*)initial_state, (const void*)lengths,
                           (const void*)final_state})
     if (ptr && !aligned(ptr, 4)) return MAMBA_ERR_ALIGN;
-  if (B * H * ((P + 3) / 4) / 4 + 1 >= kMaxGrid) return MAMBA_ERR_SHAPE;
-  (void)workspace;
-  (void)workspace_bytes;
+  const GdrPlan plan = make_gdr_plan(B, H, P, N, L);
+  if (!gdr_grid_ok(plan, B, H, G, P, N)) return MAMBA_ERR_SHAPE;
+  if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return MAMBA_ERR_WORKSPACE;
+  if (plan.bytes && !aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
   mamba::GdrParams p = gdr_params(q, k, v, delta, beta, A, delta_bias, B, H, G, P, N, L, q_stride, k_stride, v_stride,
                                   scale, flags);
   p.init = initial_state; p.lengths = lengths; p.y = y; p.final_state = final_state;
   p.state_vec = N % 4 == 0 && (!initial_state || aligned(initial_state, 16)) && (!final_state || aligned(final_state, 16));
+  if (plan.chunk) {
+    mamba::GdrChunkParams c{};
+    c.g = p;
+    char* ws = static_cast<char*>(workspace);
+    c.planes = reinterpret_cast<uint16_t*>(ws + plan.off_planes);
+    c.vec = reinterpret_cast<float*>(ws + plan.off_vec);
+    c.n_chunks = plan.n_chunks; c.S = plan.S; c.seg_chunks = plan.seg_chunks;
+    if (plan.S > 1) {
+      c.seg_M = reinterpret_cast<float*>(ws + plan.off_M);
+      c.seg_h = reinterpret_cast<float*>(ws + plan.off_h);
+      c.seg_start = reinterpret_cast<float*>(ws + plan.off_start);
+    }
+    c.p_parts = out_dtype == MAMBA_BF16 ? 2 : 3;
+    return mamba::launch_gdr_chunk(c, dt_of(in_dtype), dt_of(out_dtype), stream) == hipSuccess ? MAMBA_OK
+                                                                                              : MAMBA_ERR_HIP;
+  }
   return mamba::launch_gdr_step(p, dt_of(in_dtype), dt_of(out_dtype), stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 
@@ -131,6 +203,13 @@ int mamba_gdr_update(float* state, const int32_t* slots, const void* q, const vo
   p.init = state; p.final_state = state; p.slots = slots; p.n_slots = n_slots; p.y = y;
   p.state_vec = N % 4 == 0 && aligned(state, 16);
   return mamba::launch_gdr_step(p, dt_of(in_dtype), dt_of(out_dtype), stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+}
+
+int mamba_gdr_set_test_knobs(int kernel, int64_t segments) {
+  if (kernel < 0 || kernel > 2 || segments < 0) return MAMBA_ERR_SHAPE;
+  g_kernel.store(kernel);
+  g_segments.store(segments);
+  return MAMBA_OK;
 }
 
 int mamba_state_cache_write(const void* state, const int32_t* slots, int8_t* codes, uint8_t* exps, int64_t rows,

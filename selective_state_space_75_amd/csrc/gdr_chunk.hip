@@ -1,0 +1,534 @@
+// gdr_chunk.hip -- the gated delta rule over sequences, in chunks of C = 32
+// tokens on the matrix cores (gfx950).
+//
+// For a chunk with entering state S0 (P x N), rows k_i, q_i, v_i, cumulated log
+// decay G_i (from the chunk's first token, inclusive) and D_ij = exp(G_i - G_j):
+//   the updates u_i solve u_i = b_i (v_i - exp(G_i) S0 k_i - sum_(j<i) D_ij (k_i . k_j) u_j),
+//   a unit lower-triangular system, so with A_ij = b_i D_ij k_i . k_j (j < i) and
+//   T = (1 + A)^-1 diag(b):
+//     R = V - diag(exp G) K S0^T          (C x P)
+//     U = T R
+//     Y = scale (diag(exp G) Q S0^T + tril(D o Q K^T) U)
+//     S1 = exp(G_C) S0 + (diag(exp(G_C - G)) U)^T K
+// T, the scaled query matrix and the factors do not depend on the state: a first
+// kernel makes them for every (batch row, head, chunk) in parallel; the second runs
+// the chain of chunks.  Differences G_i - G_j are taken in fp64 of sums from the
+// chunk's start, so a hard reset inside a chunk does not cost the later tokens
+// their digits; lengths of unit keys are folded into T, the query matrix and the
+// factors, so that raw bf16 keys stay exact operands.
+//
+// The chain is cut over the P value channels, which are independent: one wave owns
+// 16 channels and their 16 x N state in MFMA accumulators, four waves (64 channels)
+// share the chunk's K and Q tiles in LDS.  Per chunk and wave at N = 128 and bf16:
+// 24 + 16 + 12 + 6 + 24 MFMAs of 16 cycles each (K S0, Q S0, T R, query x U, U K);
+// every result is the next product's operand in place (gdr_mfma.hpp).
+//
+// Few heads over a long L: L is cut into segments.  A summary launch runs every
+// segment but the last from a zero state and, since a segment maps its entering
+// state linearly (S1 = S0 M + h), with N more rows that start as the identity and
+// have no values; they end as M.  A carry kernel chains the segments, and the full
+// launch runs all of them at once.
+#include "gdr_mfma.hpp"
+
+namespace mamba {
+namespace {
+
+constexpr int kC = kGdrChunk;
+
+__device__ __forceinline__ int64_t block_of(const GdrChunkParams& p, int64_t b, int64_t h, int64_t c) {
+  return (b * p.g.H + h) * p.n_chunks + c;
+}
+__device__ __forceinline__ uint16_t* planes_of(const GdrChunkParams& p, int64_t blk) {
+  return p.planes + blk * (int64_t)(3 + p.p_parts) * kGdrPlane;
+}
+
+// A tile of one chunk: kN rows (numbers of a key head) of 32 tokens, one plane per part.
+template <typename T, int kN>
+struct Tile {
+  static constexpr int kParts = GdrIn<T>::kParts;
+  static constexpr int kPlane = kN * kGdrRow;
+  static constexpr int kPieces = kN * 4 / 256;      // eight tokens each, per thread of a workgroup
+  using Raw = typename GdrIn<T>::Raw;
+  Raw raw[kPieces];
+  __device__ __forceinline__ void load(const T* rows, int64_t N, int64_t L, int64_t t0, int64_t end, int tid) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int id = tid + 256 * j;
+      const int64_t n = id >> 2;
+      if (n < N) raw[j].load(rows + n * L, t0 + 8 * (id & 3), end);
+      else raw[j].zero();
+    }
+  }
+  __device__ __forceinline__ void put(uint16_t* tile, int tid) const {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int id = tid + 256 * j;
+      raw[j].template put<kPlane>(tile + (id >> 2) * kGdrRow + 8 * (id & 3));
+    }
+  }
+};
+
+// Orders a wave's LDS accesses across its lanes (no other wave is involved).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <typename T, int kN>
+__device__ __forceinline__ void frags_t(const uint16_t* tile, int row0, int col0, int lane,
+                                        bf16x8 (&f)[GdrIn<T>::kParts]) {
+#pragma unroll
+  for (int s = 0; s < GdrIn<T>::kParts; ++s) f[s] = gdr_frag_t<kGdrRow>(tile + s * kN * kGdrRow, row0, col0, lane);
+}
+
+// ----------------------------------------------------------------------------- preparation
+// One workgroup per (batch row, key head, chunk).  K K^T and Q K^T once for all value
+// heads of the key head (wave w: rows 16 (w & 1) of K or Q), then a wave per value
+// head: gates, the triangular solve, and the operand planes.  The solve is column by
+// column in registers: lane 32 half + c holds rows i = 2 m + half of column c of the
+// inverse; once row j is final, every later row takes its multiple of it, 15 fused
+// multiply-adds at most per lane and step with no dependence among them.
+template <typename T, int kN>
+__global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
+  constexpr int kParts = GdrIn<T>::kParts;
+  constexpr int kTile = kN * kGdrRow * kParts;
+  constexpr int kM = 36;                                   // floats per row of a wave's matrix
+  constexpr int kWaveM = 32 * kM;
+  constexpr size_t kTileBytes = 2 * kTile * 2, kMBytes = 4 * kWaveM * 4;
+  __shared__ __align__(16) char mem[kTileBytes > kMBytes ? kTileBytes : kMBytes];
+  __shared__ float prod[2][32 * 33];                       // K K^T, Q K^T
+  __shared__ float red[2][8][32];
+  __shared__ float rlen[2][32];                            // 1 / |k|, 1 / |q| (1 without normalisation)
+  __shared__ double cums[4][32];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const GdrParams& q = p.g;
+  const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
+  const int64_t c = it % p.n_chunks, bg = it / p.n_chunks, g = bg % q.G, b = bg / q.G;
+  const int64_t len = gdr_length(q, b), t0 = c * kC;
+  if (t0 >= len) return;
+  uint16_t* Kt = reinterpret_cast<uint16_t*>(mem);
+  uint16_t* Qt = Kt + kTile;
+  {
+    Tile<T, kN> tk, tq;
+    tk.load(static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L, q.N, q.L, t0, len, tid);
+    tq.load(static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L, q.N, q.L, t0, len, tid);
+    tk.put(Kt, tid);
+    tq.put(Qt, tid);
+  }
+  __syncthreads();
+  {
+    const uint16_t* src = (w & 2) ? Qt : Kt;
+    const int rt = w & 1;
+    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+    for (int kb = 0; kb < kN / 32; ++kb) {
+      bf16x8 a[kParts], b0[kParts], b1[kParts];
+      frags_t<T, kN>(src, 32 * kb, 16 * rt, lane, a);
+      frags_t<T, kN>(Kt, 32 * kb, 0, lane, b0);
+      acc[0] = gdr_mma<3>(a, b0, acc[0]);
+      frags_t<T, kN>(Kt, 32 * kb, 16, lane, b1);
+      acc[1] = gdr_mma<3>(a, b1, acc[1]);
+    }
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) prod[w >> 1][(16 * rt + 4 * g4 + r) * 33 + 16 * ct + i16] = acc[ct][r];
+  }
+  if (q.norm) {
+    const int t = tid & 31, part = tid >> 5;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const uint16_t* tile = m ? Qt : Kt;
+      float ss = 0.0f;
+      for (int n = part * (kN / 8); n < (part + 1) * (kN / 8); ++n) {
+        float x = 0.0f;
+#pragma unroll
+        for (int s = kParts - 1; s >= 0; --s) x += bf16_to_f32(tile[s * kN * kGdrRow + n * kGdrRow + t]);
+        ss = __builtin_fmaf(x, x, ss);
+      }
+      red[m][part][t] = ss;
+    }
+  }
+  __syncthreads();
+  if (tid < 64) {
+    const int m = tid >> 5, t = tid & 31;
+    float r = 1.0f;
+    if (q.norm) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int part = 0; part < 8; ++part) ss += red[m][part][t];
+      r = gdr_rnorm(ss);
+    }
+    rlen[m][t] = r;
+  }
+  __syncthreads();
+
+  float* M = reinterpret_cast<float*>(mem) + w * kWaveM;    // the tiles are no longer needed
+  const int c32 = lane & 31, half = lane >> 5;
+  const int64_t rep = q.H / q.G;
+  for (int64_t hh = w; hh < rep; hh += 4) {
+    const int64_t h = g * rep + hh, bh = b * q.H + h;
+    const int64_t blk = block_of(p, b, h, c);
+    uint16_t* planes = planes_of(p, blk);
+    float* vec = p.vec + blk * kGdrVec;
+    // gates: base-2 log decay, held at 2^-1000 per token (zero in fp32) so that a
+    // reset by an infinite step leaves differences finite
+    const int64_t t = t0 + c32;
+    double cum = 0.0;
+    float beta = 0.0f;
+    if (t < len) {
+      const float x = gdr_load(static_cast<const T*>(q.delta) + bh * q.L + t) + (q.bias ? q.bias[h] : 0.0f);
+      const float g2 = softplus(x) * q.A[h] * kLog2e;
+      cum = g2 < -1000.0f ? -1000.0 : (double)g2;
+      beta = gdr_sigmoid(gdr_load(static_cast<const T*>(q.beta) + bh * q.L + t));
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const double o = __shfl_up(cum, d, 32);
+      if (c32 >= d) cum += o;
+    }
+    if (half == 0) cums[w][c32] = cum;
+    const double last = __shfl(cum, 31, 32);
+    const float rk = rlen[0][c32], rq = rlen[1][c32] * q.scale;
+    const float dec = hw_exp2((float)cum);
+    if (half == 0) {
+      vec[c32] = dec * rk;
+      vec[32 + c32] = dec * rq;
+      vec[64 + c32] = hw_exp2((float)(last - cum)) * rk;
+      if (c32 == 0) vec[96] = hw_exp2((float)last);
+    }
+    wave_sync();
+    // M[j][i]: column j of the strictly lower-triangular A, its rows i with even i first
+    {
+      const int pos = (c32 & 1) * 16 + (c32 >> 1);
+      const float f = beta * rk;
+#pragma unroll
+      for (int jj = 0; jj < 16; ++jj) {
+        const int j = 2 * jj + half;
+        const float e = hw_exp2((float)(cum - cums[w][j]));
+        M[j * kM + pos] = j < c32 ? f * rlen[0][j] * prod[0][c32 * 33 + j] * e : 0.0f;
+      }
+    }
+    // the query matrix, straight into operand order
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+      const int row = 16 * rt + i16;
+      const double cr = cums[w][row];
+      const float fr = rlen[1][row] * q.scale;
+      f32x4 x[2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int col = (e < 4 ? 0 : 16) + 4 * g4 + (e & 3);
+        const float d = hw_exp2((float)(cr - cums[w][col]));
+        x[e >> 2][e & 3] = col <= row ? fr * rlen[0][col] * prod[1][row * 33 + col] * d : 0.0f;
+      }
+      if (p.p_parts == 2) {
+        bf16x8 f[2];
+        gdr_split<2>(x[0], x[1], f);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          *reinterpret_cast<bf16x8*>(planes + (3 + s) * kGdrPlane + rt * 512 + lane * 8) = f[s];
+      } else {
+        bf16x8 f[3];
+        gdr_split<3>(x[0], x[1], f);
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+          *reinterpret_cast<bf16x8*>(planes + (3 + s) * kGdrPlane + rt * 512 + lane * 8) = f[s];
+      }
+    }
+    wave_sync();
+    // T = (1 + A)^-1: x[m] is row 2 m + half of column c32
+    float x[16];
+#pragma unroll
+    for (int m = 0; m < 16; ++m) x[m] = (2 * m + half == c32) ? 1.0f : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 31; ++j) {
+      // row j to both halves of the wave
+      const auto sw = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x[j >> 1]),
+                                                       __builtin_bit_cast(uint32_t, x[j >> 1]), false, false);
+      const float xj = __builtin_bit_cast(float, (j & 1) ? sw[1] : sw[0]);
+      const float* col = M + j * kM + half * 16;
+#pragma unroll
+      for (int m4 = (j + 1) / 2 & ~3; m4 < 16; m4 += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(col + m4);
+        if (2 * m4 + 1 > j) x[m4] = __builtin_fmaf(-a.x, xj, x[m4]);
+        if (2 * m4 + 3 > j) x[m4 + 1] = __builtin_fmaf(-a.y, xj, x[m4 + 1]);
+        if (2 * m4 + 5 > j) x[m4 + 2] = __builtin_fmaf(-a.z, xj, x[m4 + 2]);
+        if (2 * m4 + 7 > j) x[m4 + 3] = __builtin_fmaf(-a.w, xj, x[m4 + 3]);
+      }
+    }
+    wave_sync();
+#pragma unroll
+    for (int m = 0; m < 16; ++m) M[(2 * m + half) * 33 + c32] = x[m] * beta;
+    wave_sync();
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+      f32x4 y[2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = M[(16 * rt + i16) * 33 + (e < 4 ? 0 : 16) + 4 * g4 + (e & 3)];
+      bf16x8 f[3];
+      gdr_split<3>(y[0], y[1], f);
+#pragma unroll
+      for (int s = 0; s < 3; ++s) *reinterpret_cast<bf16x8*>(planes + s * kGdrPlane + rt * 512 + lane * 8) = f[s];
+    }
+    wave_sync();
+  }
+}
+
+// ----------------------------------------------------------------------------- the chain of chunks
+enum ChainMode { kFull = 0, kSummary = 1 };
+
+template <typename T, typename O, int kN, int kMode>
+__global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
+  constexpr int kParts = GdrIn<T>::kParts;
+  constexpr int kTile = kN * kGdrRow * kParts;
+  constexpr int kNT = kN / 16, kNB = kN / 32;
+  constexpr int kOut = sizeof(O) == 2 ? 2 : 3;            // parts of what only y sees
+  constexpr int kBuf = kParts == 1 ? 2 : 1;               // fp32 tiles take three planes: one buffer
+  __shared__ __align__(16) uint16_t Kt[kBuf][kTile];
+  __shared__ __align__(16) uint16_t Qt[kMode == kFull ? kBuf : 1][kMode == kFull ? kTile : 8];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const GdrParams& q = p.g;
+  const int64_t vslices = (q.P + 63) / 64;
+  const int64_t slices = kMode == kFull ? vslices : vslices + (q.N + 63) / 64;
+  const int64_t segs = kMode == kFull ? p.S : p.S - 1;
+  const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
+  const int64_t slice = it % slices, h = (it / slices) % q.H, bs = it / (slices * q.H);
+  const int64_t seg = bs % segs, b = bs / segs, bh = b * q.H + h, g = h / (q.H / q.G);
+  const bool ident = kMode == kSummary && slice >= vslices;  // rows of the transition
+  const int64_t ch0 = (ident ? slice - vslices : slice) * 64 + 16 * w, ch = ch0 + i16;
+  const int64_t channels = ident ? q.N : q.P;
+  const bool active = ch0 < channels, mine = ch < channels;
+  const int64_t len = gdr_length(q, b);
+  const int64_t c0 = seg * p.seg_chunks, c1 = c0 + p.seg_chunks < p.n_chunks ? c0 + p.seg_chunks : p.n_chunks;
+  const int64_t live = (len + kC - 1) / kC, ce = live < c1 ? live : c1;
+
+  const T* krows = static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L;
+  const T* qrows = static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L;
+  const T* vrow = static_cast<const T*>(q.v) + b * q.v_stride + (h * q.P + (mine && !ident ? ch : 0)) * q.L;
+  O* yrow = static_cast<O*>(q.y) + (bh * q.P + (mine && !ident ? ch : 0)) * q.L;
+  const bool values = mine && !ident;
+
+  f32x4 S[kNT];
+  {
+    const float* src = nullptr;
+    if (mine) {
+      if (kMode == kFull && p.S > 1) src = p.seg_start + ((bs * q.H + h) * q.P + ch) * q.N;
+      else if (kMode == kFull && q.init) src = q.init + (bh * q.P + ch) * q.N;
+    }
+#pragma unroll
+    for (int tn = 0; tn < kNT; ++tn) {
+      S[tn] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (src) S[tn] = gdr_load_state(src, 16 * tn + 4 * g4, q.N, q.state_vec);
+      if (ident) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[tn][r] = (mine && 16 * tn + 4 * g4 + r == ch) ? 1.0f : 0.0f;
+      }
+    }
+  }
+
+  // what a wave needs of one chunk besides the shared tiles, loaded a chunk ahead
+  struct Ahead {
+    bf16x8 tf[2][3], pf[2][kOut];
+    f32x4 v[2], fk[2], fq[2], fu[2];
+    float dec;
+  } nx;
+  Tile<T, kN> tk, tq;
+  auto fetch = [&](int64_t c) {
+    const int64_t t0 = c * kC;
+    tk.load(krows, q.N, q.L, t0, len, tid);
+    if constexpr (kMode == kFull) tq.load(qrows, q.N, q.L, t0, len, tid);
+    if (!active) return;
+    const int64_t blk = block_of(p, b, h, c);
+    const uint16_t* planes = planes_of(p, blk) + lane * 8;
+    const float* vec = p.vec + blk * kGdrVec;
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+#pragma unroll
+      for (int s = 0; s < 3; ++s) nx.tf[rt][s] = *reinterpret_cast<const bf16x8*>(planes + s * kGdrPlane + rt * 512);
+      nx.v[rt] = values ? gdr_load4(vrow, t0 + 16 * rt + 4 * g4, len) : f32x4{0.f, 0.f, 0.f, 0.f};
+      nx.fk[rt] = *reinterpret_cast<const f32x4*>(vec + 16 * rt + 4 * g4);
+      nx.fu[rt] = *reinterpret_cast<const f32x4*>(vec + 64 + 16 * rt + 4 * g4);
+      if constexpr (kMode == kFull) {
+#pragma unroll
+        for (int s = 0; s < kOut; ++s)
+          nx.pf[rt][s] = *reinterpret_cast<const bf16x8*>(planes + (3 + s) * kGdrPlane + rt * 512);
+        nx.fq[rt] = *reinterpret_cast<const f32x4*>(vec + 32 + 16 * rt + 4 * g4);
+      }
+    }
+    nx.dec = vec[96];
+  };
+  auto put = [&](int buf) {
+    tk.put(Kt[buf], tid);
+    if constexpr (kMode == kFull) tq.put(Qt[buf], tid);
+  };
+
+  if (c0 < ce) {
+    fetch(c0);
+    put(0);
+    __syncthreads();
+  }
+  for (int64_t c = c0; c < ce; ++c) {
+    const int buf = kBuf == 2 ? (int)((c - c0) & 1) : 0;
+    const uint16_t* K = Kt[buf];
+    const Ahead cur = nx;
+    if (c + 1 < ce) fetch(c + 1);
+    if (active) {
+      f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}, Y[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+      for (int kb = 0; kb < kNB; ++kb) {
+        bf16x8 sb[3];
+        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+          bf16x8 a[kParts];
+          frags_t<T, kN>(K, 32 * kb, 16 * rt, lane, a);
+          R[rt] = gdr_mma<3>(a, sb, R[rt]);
+          if constexpr (kMode == kFull) {
+            bf16x8 aq[kParts];
+            frags_t<T, kN>(Qt[buf], 32 * kb, 16 * rt, lane, aq);
+            Y[rt] = gdr_mma<kOut>(aq, sb, Y[rt]);
+          }
+        }
+      }
+      bf16x8 rb[3];
+      gdr_split<3>(cur.v[0] - cur.fk[0] * R[0], cur.v[1] - cur.fk[1] * R[1], rb);
+      f32x4 U[2];
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) U[rt] = gdr_mma<3>(cur.tf[rt], rb, f32x4{0.f, 0.f, 0.f, 0.f});
+      bf16x8 wb[3];
+      gdr_split<3>(cur.fu[0] * U[0], cur.fu[1] * U[1], wb);
+#pragma unroll
+      for (int tn = 0; tn < kNT; ++tn) {
+        bf16x8 a[kParts];
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) a[s] = gdr_frag<kGdrRow>(K + s * kN * kGdrRow, 16 * tn, 0, lane);
+        S[tn] = gdr_mma<3>(a, wb, S[tn] * cur.dec);
+      }
+      if constexpr (kMode == kFull) {
+        bf16x8 ub[kOut];
+        gdr_split<kOut>(U[0], U[1], ub);
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+          const f32x4 y = gdr_mma<kOut>(cur.pf[rt], ub, Y[rt] * cur.fq[rt]);
+          if (values) gdr_store4(yrow, c * kC + 16 * rt + 4 * g4, q.L, y);
+        }
+      }
+    }
+    if (c + 1 < ce) {
+      if constexpr (kBuf == 1) __syncthreads();
+      put(kBuf == 2 ? buf ^ 1 : 0);
+      __syncthreads();
+    }
+  }
+
+  if constexpr (kMode == kFull) {
+    // tokens of this segment behind the row's end
+    if (values) {
+      const int64_t from = (ce > c0 ? ce : c0) * kC, to = c1 * kC < q.L ? c1 * kC : q.L;
+      for (int64_t t = from + 4 * g4; t < to; t += 16) gdr_store4(yrow, t, to, f32x4{0.f, 0.f, 0.f, 0.f});
+    }
+    if (q.final_state && seg == p.S - 1 && mine) {
+      float* dst = q.final_state + (bh * q.P + ch) * q.N;
+#pragma unroll
+      for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+    }
+  } else if (mine) {
+    float* dst = ident ? p.seg_M + ((bs * q.H + h) * q.N + ch) * q.N : p.seg_h + ((bs * q.H + h) * q.P + ch) * q.N;
+#pragma unroll
+    for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+  }
+}
+
+// ----------------------------------------------------------------------------- carries
+// start[0] = initial state, start[s + 1] = start[s] M_s + h_s.  The rows of the state
+// are independent: one workgroup per 16 of them, wave w the 16-column tiles w, w + 4.
+// Exact fp32 products (v_mfma_f32_16x16x4_f32): the chain is short and its bytes
+// (one N x N matrix per segment) come from L2.
+__global__ __launch_bounds__(256) void gdr_carry_kernel(GdrChunkParams p) {
+  constexpr int kRow = 132;
+  __shared__ float A[2][16 * kRow];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const GdrParams& q = p.g;
+  const int64_t tiles = (q.P + 15) / 16;
+  const int64_t bh = blockIdx.x / tiles, b = bh / q.H, h = bh % q.H, p0 = (blockIdx.x % tiles) * 16;
+  const int N = (int)q.N;
+  for (int e = tid; e < 16 * 128; e += 256) {
+    const int row = e >> 7, n = e & 127;
+    float x = 0.0f;
+    if (p0 + row < q.P && n < N) {
+      if (q.init) x = q.init[(bh * q.P + p0 + row) * N + n];
+      p.seg_start[(((b * p.S) * q.H + h) * q.P + p0 + row) * N + n] = x;
+    }
+    A[0][row * kRow + n] = x;
+    A[1][row * kRow + n] = 0.0f;       // columns past N meet zeros of M, so they must be finite
+  }
+  __syncthreads();
+  for (int64_t s = 0; s + 1 < p.S; ++s) {
+    const float* a = A[s & 1];
+    const int64_t sm = (b * (p.S - 1) + s) * q.H + h;
+    const float* M = p.seg_M + sm * (int64_t)N * N;
+#pragma unroll
+    for (int t2 = 0; t2 < 2; ++t2) {
+      const int n = 16 * (w + 4 * t2) + i16;
+      if (16 * (w + 4 * t2) >= N) continue;
+      f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+      f32x4 hs = acc;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n < N && p0 + 4 * g4 + r < q.P) hs[r] = p.seg_h[(sm * q.P + p0 + 4 * g4 + r) * N + n];
+      for (int k0 = 0; k0 < N; k0 += 32) {
+        float m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int k = k0 + 4 * j + g4;
+          m[j] = (k < N && n < N) ? M[(int64_t)k * N + n] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i16 * kRow + k0 + 4 * j + g4], m[j], acc, 0, 0, 0);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 4 * g4 + r;
+        const float x = acc[r] + hs[r];
+        A[(s + 1) & 1][row * kRow + n] = x;
+        if (n < N && p0 + row < q.P) p.seg_start[(((b * p.S + s + 1) * q.H + h) * q.P + p0 + row) * N + n] = x;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, typename O, int kN>
+hipError_t chunk_n(const GdrChunkParams& p, hipStream_t s) {
+  const GdrParams& q = p.g;
+  hipLaunchKernelGGL((gdr_prep_kernel<T, kN>), dim3((unsigned)(q.B * q.G * p.n_chunks)), dim3(256), 0, s, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t vslices = (q.P + 63) / 64, islices = (q.N + 63) / 64;
+  if (p.S > 1) {
+    hipLaunchKernelGGL((gdr_chain_kernel<T, O, kN, kSummary>),
+                       dim3((unsigned)(q.B * (p.S - 1) * q.H * (vslices + islices))), dim3(256), 0, s, p);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(gdr_carry_kernel, dim3((unsigned)(q.B * q.H * ((q.P + 15) / 16))), dim3(256), 0, s, p);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((gdr_chain_kernel<T, O, kN, kFull>), dim3((unsigned)(q.B * p.S * q.H * vslices)), dim3(256), 0,
+                     s, p);
+  return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t chunk_t(const GdrChunkParams& p, hipStream_t s) {
+  return p.g.N > 64 ? chunk_n<T, O, 128>(p, s) : chunk_n<T, O, 64>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_gdr_chunk(const GdrChunkParams& p, Dt in, Dt out, hipStream_t s) {
+  if (in == Dt::BF16) return out == Dt::BF16 ? chunk_t<uint16_t, uint16_t>(p, s) : chunk_t<uint16_t, float>(p, s);
+  return out == Dt::BF16 ? chunk_t<float, uint16_t>(p, s) : chunk_t<float, float>(p, s);
+}
+
+}  // namespace mamba

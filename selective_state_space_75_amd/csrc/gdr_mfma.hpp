@@ -1,0 +1,216 @@
+// gdr_mfma.hpp -- matrix-core building blocks of the gated delta rule's chunk
+// kernels (gfx950).
+//
+// Every product is v_mfma_f32_16x16x32_bf16 with fp32 accumulators.  Lane l of a
+// wave (i = l & 15, g = l >> 4) holds
+//   of A (16 x 32): row i, eight of the 32 contraction indices;
+//   of B (32 x 16): column i, the same eight;
+//   of the result (16 x 16): column i, rows 4 g .. 4 g + 3.
+// Which eight is free as long as A and B agree.  All kernels here take, for lane
+// group g, indices 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3: exactly the rows
+// that a lane holds of two results stacked on each other.  A result therefore is
+// the B operand of the next product as it lies in the registers, and the chain
+// state -> residual -> update -> state of a chunk never moves between lanes.
+//
+// fp32 operands are split into bf16 parts that are multiplied separately.  Three
+// parts by truncation hold an fp32 number exactly (8 + 8 + 8 bits), so products of
+// parts i and j with i + j < 3 leave out only terms below 2^-24 of the largest:
+// fp32 accuracy at three products for a bf16 operand (exact in one part) times an
+// fp32 one and six for two fp32 ones, on units 16 times as fast as the fp32 MFMA.
+// Results that are rounded to bf16 at once take two parts (2^-16).
+#pragma once
+
+#include "gdr.hpp"
+
+namespace mamba {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 gdr_mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// c += sum over parts i, j with i + j < kOrd of a[i] b[j], small terms first
+template <int kOrd, int kA, int kB>
+__device__ __forceinline__ f32x4 gdr_mma(const bf16x8 (&a)[kA], const bf16x8 (&b)[kB], f32x4 c) {
+#pragma unroll
+  for (int o = kOrd - 1; o >= 0; --o)
+#pragma unroll
+    for (int i = 0; i < kA; ++i)
+      if (o - i >= 0 && o - i < kB) c = gdr_mfma(a[i], b[o - i], c);
+  return c;
+}
+
+// Eight fp32 numbers (the rows of two stacked results) -> kParts bf16 operands.
+template <int kParts>
+__device__ __forceinline__ void gdr_split(f32x4 x, f32x4 y, bf16x8 (&out)[kParts]) {
+  float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+  for (int s = 0; s < kParts; ++s) {
+    uint32_t w[4];
+    if (s == kParts - 1) {           // the last part is rounded (exact for the third)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = __builtin_bit_cast(uint32_t, v[2 * j]), b = __builtin_bit_cast(uint32_t, v[2 * j + 1]);
+        w[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);          // both upper halves
+        v[2 * j] -= __builtin_bit_cast(float, a & 0xffff0000u);
+        v[2 * j + 1] -= __builtin_bit_cast(float, b & 0xffff0000u);
+      }
+    }
+    out[s] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+
+// Operand tiles in LDS: rows of 32 tokens (or of other bf16 numbers), 40 apart.
+// 80 bytes put the 16 rows that a ds_read_b64 pair of one lane group touches on
+// different banks.
+constexpr int kGdrRow = 40;
+
+// A or B operand whose row (column) index runs along the stored row: lane i takes
+// column col0 + i of rows row0 + 4 g .. + 3 and row0 + 16 + 4 g .. + 3.  The
+// transposing read hands lane i of a 16-lane group column i of the 4 x 16 block
+// that the group's addresses cover, row r at lanes 4 r .. 4 r + 3.
+template <int kStride>
+__device__ __forceinline__ bf16x8 gdr_frag_t(const uint16_t* tile, int row0, int col0, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  const uint16_t* p = tile + (row0 + 4 * g + (i >> 2)) * kStride + col0 + 4 * (i & 3);
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * kStride));
+  const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
+  return __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
+}
+
+// A or B operand whose contraction index runs along the stored row: lane i takes
+// row row0 + i, numbers col0 + 4 g .. + 3 and col0 + 16 + 4 g .. + 3.
+template <int kStride>
+__device__ __forceinline__ bf16x8 gdr_frag(const uint16_t* tile, int row0, int col0, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  const uint16_t* p = tile + (row0 + i) * kStride + col0 + 4 * g;
+  const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(p + 16);
+  return __builtin_bit_cast(bf16x8, make_uint4(x.x, x.y, y.x, y.y));
+}
+
+// Vectors at any element-aligned global address (the hardware takes unaligned
+// dword accesses; rows of odd length start anywhere).
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight consecutive numbers of a row from token t, zeros from token `end` on.
+struct GdrRaw16 {
+  uint4 v;
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const uint16_t* row, int64_t t, int64_t end) {
+    if (t + 8 <= end) {
+      const u32x4_u x = *reinterpret_cast<const u32x4_u*>(row + t);
+      v = make_uint4(x[0], x[1], x[2], x[3]);
+    } else {
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = t + j < end ? (uint32_t)row[t + j] : 0u;
+      v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+  }
+  // into the plane(s) of a tile
+  template <int kPlaneStride>
+  __device__ __forceinline__ void put(uint16_t* dst) const { *reinterpret_cast<uint4*>(dst) = v; }
+};
+
+struct GdrRaw32 {
+  f32x4 a, b;
+  __device__ __forceinline__ void zero() { a = b = f32x4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ void load(const float* row, int64_t t, int64_t end) {
+    if (t + 8 <= end) {
+      a = *reinterpret_cast<const f32x4_u*>(row + t);
+      b = *reinterpret_cast<const f32x4_u*>(row + t + 4);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[j] = t + j < end ? row[t + j] : 0.0f;
+        b[j] = t + 4 + j < end ? row[t + 4 + j] : 0.0f;
+      }
+    }
+  }
+  template <int kPlaneStride>
+  __device__ __forceinline__ void put(uint16_t* dst) const {
+    bf16x8 part[3];
+    gdr_split<3>(a, b, part);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) *reinterpret_cast<uint4*>(dst + s * kPlaneStride) = __builtin_bit_cast(uint4, part[s]);
+  }
+};
+
+template <typename T> struct GdrIn;
+template <> struct GdrIn<uint16_t> { using Raw = GdrRaw16; static constexpr int kParts = 1; };
+template <> struct GdrIn<float> { using Raw = GdrRaw32; static constexpr int kParts = 3; };
+
+// Four consecutive numbers of a row from token t as fp32, zeros from `end` on.
+__device__ __forceinline__ f32x4 gdr_load4(const uint16_t* row, int64_t t, int64_t end) {
+  if (t + 4 <= end) {
+    const u32x2_u x = *reinterpret_cast<const u32x2_u*>(row + t);
+    return f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
+  }
+  f32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = t + j < end ? bf16_to_f32(row[t + j]) : 0.0f;
+  return r;
+}
+__device__ __forceinline__ f32x4 gdr_load4(const float* row, int64_t t, int64_t end) {
+  if (t + 4 <= end) return *reinterpret_cast<const f32x4_u*>(row + t);
+  f32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = t + j < end ? row[t + j] : 0.0f;
+  return r;
+}
+__device__ __forceinline__ void gdr_store4(uint16_t* row, int64_t t, int64_t end, f32x4 x) {
+  if (t + 4 <= end) {
+    *reinterpret_cast<u32x2_u*>(row + t) = u32x2_u{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (t + j < end) row[t + j] = f32_to_bf16(x[j]);
+}
+__device__ __forceinline__ void gdr_store4(float* row, int64_t t, int64_t end, f32x4 x) {
+  if (t + 4 <= end) {
+    *reinterpret_cast<f32x4_u*>(row + t) = x;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (t + j < end) row[t + j] = x[j];
+}
+
+// Four numbers n .. n + 3 of a state row of N (zeros behind it).
+__device__ __forceinline__ f32x4 gdr_load_state(const float* row, int64_t n, int64_t N, bool vec) {
+  if (vec) return n < N ? *reinterpret_cast<const f32x4*>(row + n) : f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = n + j < N ? row[n + j] : 0.0f;
+  return r;
+}
+__device__ __forceinline__ void gdr_store_state(float* row, int64_t n, int64_t N, bool vec, f32x4 x) {
+  if (vec) {
+    if (n < N) *reinterpret_cast<f32x4*>(row + n) = x;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n + j < N) row[n + j] = x[j];
+}
+
+// Work item of workgroup `id` of `n` so that each of the 8 XCDs (workgroups go
+// round them) gets a contiguous range: workgroups of one head, which read the
+// same keys, then share an L2.
+__device__ __forceinline__ int64_t gdr_xcd_item(int64_t id, int64_t n) {
+  const int64_t per = n / 8;
+  return id >= 8 * per ? id : (id % 8) * per + id / 8;
+}
+
+}  // namespace mamba

@@ -175,6 +175,23 @@ struct GdrParams {
   int state_vec;                                // N % 4 == 0, states 16-byte aligned
 };
 
+// The rule in chunks of kGdrChunk tokens (gdr_chunk.hip).  A preparation kernel
+// leaves, per (batch row, head, chunk), what does not depend on the state.
+constexpr int kGdrChunk = 32;
+constexpr int kGdrPlane = 1024;                 // bf16 numbers of one 32 x 32 operand plane
+constexpr int kGdrVec = 128;                    // floats of per-token factors per block
+
+struct GdrChunkParams {
+  GdrParams g;
+  uint16_t* planes;        // per block: 3 planes of T, then p_parts of the query matrix
+  float* vec;              // per block: factors of k (32), of q (32), of u (32), the chunk's decay
+  float* seg_M;            // (B, S - 1, H, N, N) transition of each segment but the last (S > 1)
+  float* seg_h;            // (B, S - 1, H, P, N) its end state from a zero start
+  float* seg_start;        // (B, S, H, P, N) state entering each segment
+  int64_t n_chunks, S, seg_chunks;
+  int p_parts;             // planes of the query matrix: 2, or 3 for fp32 outputs
+};
+
 // Rows of state in 8 bits.
 struct CacheParams {
   void* state;              // (rows, n)
@@ -200,6 +217,7 @@ hipError_t launch_conv1d_fwd(const ConvParams& p, Dt in, Dt out, bool vec, hipSt
 hipError_t launch_conv1d_update(const ConvParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_ssd(const SsdParams& p, Dt out, hipStream_t s);
 hipError_t launch_gdr_step(const GdrParams& p, Dt in, Dt out, hipStream_t s);
+hipError_t launch_gdr_chunk(const GdrChunkParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_state_cache(const CacheParams& p, Dt dt, bool write, hipStream_t s);
 
 }  // namespace mamba

@@ -59,6 +59,7 @@ SHARED = [
 @pytest.mark.parametrize("kw,code", SHARED + [
     (dict(L=0), SHAPE), (dict(L=1 << 40, B=1 << 10), SHAPE),
     (dict(init=P + 2), ALIGN), (dict(lengths=P + 2), ALIGN), (dict(fs=P + 1), ALIGN),
+    (dict(ws=None), WS), (dict(wsb=1000), WS), (dict(ws=P + 16), ALIGN),
 ])
 def test_fwd_rejects_bad_arguments(kw, code):
     assert fwd(**kw) == code
@@ -116,6 +117,28 @@ def test_workspace_size_of_invalid_shapes():
     assert ws(2, 4, 2, 64, 128, 256, BF16) < bad
     with pytest.raises(_lib.MambaError):
         _lib.gdr_workspace_size(2, 3, 2, 64, 128, 256)
+
+
+def test_workspace_size_plan():
+    """6 operand planes of 2 KB and 512 bytes of factors per head and chunk of 32 tokens; few heads over a
+    long L add segments: a transition and an end state for each but the last, a start for each."""
+    ws = _lib.gdr_workspace_size
+    a = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    assert ws(4, 40, 20, 128, 128, 1) == 0
+    blocks = 4 * 40 * 64
+    assert ws(4, 40, 20, 128, 128, 2048) == a(blocks * 6 * 2048) + a(blocks * 512)
+    with _lib.gdr_test_knobs(kernel="chunk", segments=3):
+        S, blocks = 3, 2 * 4
+        assert ws(1, 2, 2, 40, 96, 100) == (a(blocks * 6 * 2048) + a(blocks * 512) + a(2 * 1 * 96 * 96 * 4)
+                                            + a(2 * 1 * 40 * 96 * 4) + a(2 * 2 * 40 * 96 * 4))   # 4 chunks: 2 + 2
+    with _lib.gdr_test_knobs(kernel="token"):
+        assert ws(4, 40, 20, 128, 128, 2048) == 0
+
+
+def test_knob_errors():
+    f = _lib.lib().mamba_gdr_set_test_knobs
+    assert f(3, 0) == SHAPE and f(-1, 0) == SHAPE and f(0, -1) == SHAPE
+    assert f(0, 0) == 0
 
 
 def test_python_binding_rejects_before_calling():

@@ -56,8 +56,18 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("kernel", ["planner", "token", "chunk", "segments3"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "B%dH%dG%dP%dN%dL%d_%s_%s" % (c[:7] + ("-".join(sorted(c[7])) or "plain",)))
-def test_fwd_cases(case, dev):
+def test_fwd_cases(case, kernel, dev):
+    """Every case on the planner's kernel, token by token, in chunks, and in chunks over
+    three segments of L with carries between them."""
+    import selective_state_space_75_amd as m
+    seg = 3 if kernel == "segments3" else 0
+    with m.gdr_test_knobs(kernel="chunk" if seg else kernel, segments=seg):
+        _fwd_case(case, dev)
+
+
+def _fwd_case(case, dev):
     import torch
     import selective_state_space_75_amd as m
     B, H, G, P, N, L, dtype, o = case
