@@ -66,7 +66,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct GdrPlan {
   bool chunk = false;
   int64_t n_chunks = 0, S = 1, seg_chunks = 0;
-  size_t off_planes = 0, off_vec = 0, off_M = 0, off_h = 0, off_start = 0, bytes = 0;
+  size_t off_planes = 0, off_vec = 0, off_tk = 0, off_tq = 0, off_tv = 0, off_M = 0, off_h = 0, off_start = 0, bytes = 0;
 };
 
 // Sizes-only plan of the forward pass.  Up to 24 tokens go token by token (one
@@ -74,7 +74,7 @@ struct GdrPlan {
 // heads would leave SIMDs idle (there are 1024): the summary launch then adds
 // the N transition rows to the P value rows of every head, so fewer than three
 // segments do not pay.
-GdrPlan make_gdr_plan(int64_t B, int64_t H, int64_t P, int64_t N, int64_t L) {
+GdrPlan make_gdr_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L, size_t e) {
   GdrPlan q;
   const int kernel = g_kernel.load();
   q.chunk = kernel == 2 || (kernel == 0 && L > 24);
@@ -93,6 +93,9 @@ GdrPlan make_gdr_plan(int64_t B, int64_t H, int64_t P, int64_t N, int64_t L) {
   size_t o = 0;
   q.off_planes = o; o += align256(blocks * 6 * mamba::kGdrPlane * sizeof(uint16_t));
   q.off_vec = o; o += align256(blocks * mamba::kGdrVec * sizeof(float));
+  q.off_tk = o; o += align256(size_t(B) * G * N * mamba::kGdrChunk * e);
+  q.off_tq = o; o += align256(size_t(B) * G * N * mamba::kGdrChunk * e);
+  q.off_tv = o; o += align256(size_t(B) * H * P * mamba::kGdrChunk * e);
   if (q.S > 1) {
     const size_t heads = size_t(B) * H;
     q.off_M = o; o += align256(heads * (q.S - 1) * N * N * sizeof(float));
@@ -138,7 +141,7 @@ extern "C" {
 size_t mamba_gdr_workspace_size(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
                                 mamba_dtype_t in_dtype) {
   if (!dtype_ok(in_dtype) || !gdr_sizes_ok(B, H, G, P, N, L) || N > 128) return (size_t)-1;
-  return make_gdr_plan(B, H, P, N, L).bytes;
+  return make_gdr_plan(B, H, G, P, N, L, width(in_dtype)).bytes;
 }
 
 int mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* delta, const void* beta, const float* A,
@@ -156,7 +159,7 @@ int mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* delta
   for (const void* ptr : {(const void*)A, (const void*)delta_bias, (const void*)initial_state, (const void*)lengths,
                           (const void*)final_state})
     if (ptr && !aligned(ptr, 4)) return MAMBA_ERR_ALIGN;
-  const GdrPlan plan = make_gdr_plan(B, H, P, N, L);
+  const GdrPlan plan = make_gdr_plan(B, H, G, P, N, L, width(in_dtype));
   if (!gdr_grid_ok(plan, B, H, G, P, N)) return MAMBA_ERR_SHAPE;
   if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return MAMBA_ERR_WORKSPACE;
   if (plan.bytes && !aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
@@ -170,6 +173,7 @@ int mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* delta
     char* ws = static_cast<char*>(workspace);
     c.planes = reinterpret_cast<uint16_t*>(ws + plan.off_planes);
     c.vec = reinterpret_cast<float*>(ws + plan.off_vec);
+    c.tail_k = ws + plan.off_tk; c.tail_q = ws + plan.off_tq; c.tail_v = ws + plan.off_tv;
     c.n_chunks = plan.n_chunks; c.S = plan.S; c.seg_chunks = plan.seg_chunks;
     if (plan.S > 1) {
       c.seg_M = reinterpret_cast<float*>(ws + plan.off_M);

@@ -42,43 +42,10 @@ __device__ __forceinline__ uint16_t* planes_of(const GdrChunkParams& p, int64_t 
   return p.planes + blk * (int64_t)(3 + p.p_parts) * kGdrPlane;
 }
 
-// A tile of one chunk: kN rows (numbers of a key head) of 32 tokens, one plane per part.
-template <typename T, int kN>
-struct Tile {
-  static constexpr int kParts = GdrIn<T>::kParts;
-  static constexpr int kPlane = kN * kGdrRow;
-  static constexpr int kPieces = kN * 4 / 256;      // eight tokens each, per thread of a workgroup
-  using Raw = typename GdrIn<T>::Raw;
-  Raw raw[kPieces];
-  __device__ __forceinline__ void load(const T* rows, int64_t N, int64_t L, int64_t t0, int64_t end, int tid) {
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      const int id = tid + 256 * j;
-      const int64_t n = id >> 2;
-      if (n < N) raw[j].load(rows + n * L, t0 + 8 * (id & 3), end);
-      else raw[j].zero();
-    }
-  }
-  __device__ __forceinline__ void put(uint16_t* tile, int tid) const {
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      const int id = tid + 256 * j;
-      raw[j].template put<kPlane>(tile + (id >> 2) * kGdrRow + 8 * (id & 3));
-    }
-  }
-};
-
 // Orders a wave's LDS accesses across its lanes (no other wave is involved).
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-}
-
-template <typename T, int kN>
-__device__ __forceinline__ void frags_t(const uint16_t* tile, int row0, int col0, int lane,
-                                        bf16x8 (&f)[GdrIn<T>::kParts]) {
-#pragma unroll
-  for (int s = 0; s < GdrIn<T>::kParts; ++s) f[s] = gdr_frag_t<kGdrRow>(tile + s * kN * kGdrRow, row0, col0, lane);
 }
 
 // ----------------------------------------------------------------------------- preparation
@@ -109,9 +76,28 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
   uint16_t* Kt = reinterpret_cast<uint16_t*>(mem);
   uint16_t* Qt = Kt + kTile;
   {
-    Tile<T, kN> tk, tq;
-    tk.load(static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L, q.N, q.L, t0, len, tid);
-    tq.load(static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L, q.N, q.L, t0, len, tid);
+    GdrTile<T, kN> tk, tq;
+    tk.init(q.N, tid);
+    tq.init(q.N, tid);
+    const T* krows = static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L + t0;
+    const T* qrows = static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L + t0;
+    if (t0 + kC <= len) {
+      tk.load(krows, q.L, tid);
+      tq.load(qrows, q.L, tid);
+    } else {                     // the row ends here: leave padded copies for the chain
+      tk.load_part(krows, q.L, len - t0, tid);
+      tq.load_part(qrows, q.L, len - t0, tid);
+      tk.save(static_cast<T*>(p.tail_k) + bg * q.N * kC, tid);
+      tq.save(static_cast<T*>(p.tail_q) + bg * q.N * kC, tid);
+      const int64_t rows = q.H / q.G * q.P, first = (b * q.H + g * (q.H / q.G)) * q.P;
+      const T* v = static_cast<const T*>(q.v) + b * q.v_stride + g * rows * q.L + t0;
+      T* tv = static_cast<T*>(p.tail_v) + first * kC;
+      for (int64_t id = tid; id < rows * 4; id += 256) {
+        typename GdrIn<T>::Raw x;
+        x.part(v + (id >> 2) * q.L + 8 * (id & 3), len - t0 - 8 * (id & 3));
+        x.save(tv + 8 * id);
+      }
+    }
     tk.put(Kt, tid);
     tq.put(Qt, tid);
   }
@@ -123,10 +109,10 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
 #pragma unroll
     for (int kb = 0; kb < kN / 32; ++kb) {
       bf16x8 a[kParts], b0[kParts], b1[kParts];
-      frags_t<T, kN>(src, 32 * kb, 16 * rt, lane, a);
-      frags_t<T, kN>(Kt, 32 * kb, 0, lane, b0);
+      gdr_frags_t<T, kN>(src, 32 * kb, 16 * rt, lane, a);
+      gdr_frags_t<T, kN>(Kt, 32 * kb, 0, lane, b0);
       acc[0] = gdr_mma<3>(a, b0, acc[0]);
-      frags_t<T, kN>(Kt, 32 * kb, 16, lane, b1);
+      gdr_frags_t<T, kN>(Kt, 32 * kb, 16, lane, b1);
       acc[1] = gdr_mma<3>(a, b1, acc[1]);
     }
 #pragma unroll
@@ -298,14 +284,18 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   const bool ident = kMode == kSummary && slice >= vslices;  // rows of the transition
   const int64_t ch0 = (ident ? slice - vslices : slice) * 64 + 16 * w, ch = ch0 + i16;
   const int64_t channels = ident ? q.N : q.P;
-  const bool active = ch0 < channels, mine = ch < channels;
+  const bool mine = ch < channels;   // waves past the last channel run along on a channel that is there
   const int64_t len = gdr_length(q, b);
   const int64_t c0 = seg * p.seg_chunks, c1 = c0 + p.seg_chunks < p.n_chunks ? c0 + p.seg_chunks : p.n_chunks;
   const int64_t live = (len + kC - 1) / kC, ce = live < c1 ? live : c1;
 
   const T* krows = static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L;
   const T* qrows = static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L;
-  const T* vrow = static_cast<const T*>(q.v) + b * q.v_stride + (h * q.P + (mine && !ident ? ch : 0)) * q.L;
+  const T* tail_k = static_cast<const T*>(p.tail_k) + (b * q.G + g) * q.N * kC;
+  const T* tail_q = static_cast<const T*>(p.tail_q) + (b * q.G + g) * q.N * kC;
+  const int64_t vch = mine && !ident ? ch : 0;               // lanes without a channel read one that is there
+  const T* vrow = static_cast<const T*>(q.v) + b * q.v_stride + (h * q.P + vch) * q.L + 4 * g4;
+  const T* tail_v = static_cast<const T*>(p.tail_v) + (bh * q.P + vch) * kC + 4 * g4;
   O* yrow = static_cast<O*>(q.y) + (bh * q.P + (mine && !ident ? ch : 0)) * q.L;
   const bool values = mine && !ident;
 
@@ -327,36 +317,51 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
     }
   }
 
-  // what a wave needs of one chunk besides the shared tiles, loaded a chunk ahead
-  struct Ahead {
-    bf16x8 tf[2][3], pf[2][kOut];
-    f32x4 v[2], fk[2], fq[2], fu[2];
-    float dec;
-  } nx;
-  Tile<T, kN> tk, tq;
-  auto fetch = [&](int64_t c) {
-    const int64_t t0 = c * kC;
-    tk.load(krows, q.N, q.L, t0, len, tid);
-    if constexpr (kMode == kFull) tq.load(qrows, q.N, q.L, t0, len, tid);
-    if (!active) return;
-    const int64_t blk = block_of(p, b, h, c);
-    const uint16_t* planes = planes_of(p, blk) + lane * 8;
-    const float* vec = p.vec + blk * kGdrVec;
+  // What a wave needs of a chunk besides the shared tiles.  Each is reloaded for the
+  // next chunk right after its last use, so that it has a whole chunk to arrive
+  // without a second set of registers.
+  bf16x8 tf[2][3], pf[2][kOut];
+  typename GdrIn<T>::Four v[2];
+  f32x4 fk[2], fq[2], fu[2];
+  float dec = 0.0f;
+  const int64_t blk0 = block_of(p, b, h, 0);
+  const uint16_t* planes = planes_of(p, blk0) + lane * 8;
+  const int64_t pstride = (int64_t)(3 + p.p_parts) * kGdrPlane;
+  const float* vec = p.vec + blk0 * kGdrVec;
+  auto load_v = [&](int64_t c) {
+    const T* src = (c + 1) * kC <= len ? vrow + c * kC : tail_v;
+    v[0].load(src);
+    v[1].load(src + 16);
+  };
+  auto load_vec = [&](int64_t c, int which, f32x4 (&f)[2]) {
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt) {
+    for (int rt = 0; rt < 2; ++rt)
+      f[rt] = *reinterpret_cast<const f32x4*>(vec + c * kGdrVec + 32 * which + 16 * rt + 4 * g4);
+  };
+  auto load_t = [&](int64_t c) {
 #pragma unroll
-      for (int s = 0; s < 3; ++s) nx.tf[rt][s] = *reinterpret_cast<const bf16x8*>(planes + s * kGdrPlane + rt * 512);
-      nx.v[rt] = values ? gdr_load4(vrow, t0 + 16 * rt + 4 * g4, len) : f32x4{0.f, 0.f, 0.f, 0.f};
-      nx.fk[rt] = *reinterpret_cast<const f32x4*>(vec + 16 * rt + 4 * g4);
-      nx.fu[rt] = *reinterpret_cast<const f32x4*>(vec + 64 + 16 * rt + 4 * g4);
-      if constexpr (kMode == kFull) {
+    for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-        for (int s = 0; s < kOut; ++s)
-          nx.pf[rt][s] = *reinterpret_cast<const bf16x8*>(planes + (3 + s) * kGdrPlane + rt * 512);
-        nx.fq[rt] = *reinterpret_cast<const f32x4*>(vec + 32 + 16 * rt + 4 * g4);
-      }
+      for (int s = 0; s < 3; ++s)
+        tf[rt][s] = *reinterpret_cast<const bf16x8*>(planes + c * pstride + s * kGdrPlane + rt * 512);
+  };
+  auto load_p = [&](int64_t c) {
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int s = 0; s < kOut; ++s)
+        pf[rt][s] = *reinterpret_cast<const bf16x8*>(planes + c * pstride + (3 + s) * kGdrPlane + rt * 512);
+  };
+  GdrTile<T, kN> tk, tq;
+  tk.init(q.N, tid);
+  tq.init(q.N, tid);
+  auto load_tiles = [&](int64_t c) {
+    const GdrChunkSrc<T> sk(krows, q.L, tail_k, c, len);
+    tk.load(sk.at, sk.stride, tid);
+    if constexpr (kMode == kFull) {
+      const GdrChunkSrc<T> sq(qrows, q.L, tail_q, c, len);
+      tq.load(sq.at, sq.stride, tid);
     }
-    nx.dec = vec[96];
   };
   auto put = [&](int buf) {
     tk.put(Kt[buf], tid);
@@ -364,62 +369,94 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   };
 
   if (c0 < ce) {
-    fetch(c0);
+    load_tiles(c0);
+    load_v(c0);
+    load_vec(c0, 0, fk);
+    load_t(c0);
+    load_vec(c0, 2, fu);
+    dec = vec[c0 * kGdrVec + 96];
+    if constexpr (kMode == kFull) {
+      load_vec(c0, 1, fq);
+      load_p(c0);
+    }
     put(0);
     __syncthreads();
   }
   for (int64_t c = c0; c < ce; ++c) {
     const int buf = kBuf == 2 ? (int)((c - c0) & 1) : 0;
     const uint16_t* K = Kt[buf];
-    const Ahead cur = nx;
-    if (c + 1 < ce) fetch(c + 1);
-    if (active) {
-      f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}, Y[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
-#pragma unroll
-      for (int kb = 0; kb < kNB; ++kb) {
-        bf16x8 sb[3];
-        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
+    const uint16_t* Qb = Qt[kMode == kFull ? buf : 0];
+    const int64_t cn = c + 1 < ce ? c + 1 : c;             // the last chunk loads itself again
+    load_tiles(cn);
+    {
+      // operands of one block of 32 state rows are read while the one before is used
+      bf16x8 ka[2][2][kParts], qa[2][2][kParts];
+      auto load_a = [&](int kb) {
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
-          bf16x8 a[kParts];
-          frags_t<T, kN>(K, 32 * kb, 16 * rt, lane, a);
-          R[rt] = gdr_mma<3>(a, sb, R[rt]);
-          if constexpr (kMode == kFull) {
-            bf16x8 aq[kParts];
-            frags_t<T, kN>(Qt[buf], 32 * kb, 16 * rt, lane, aq);
-            Y[rt] = gdr_mma<kOut>(aq, sb, Y[rt]);
-          }
+          gdr_frags_t<T, kN>(K, 32 * kb, 16 * rt, lane, ka[kb & 1][rt]);
+          if constexpr (kMode == kFull) gdr_frags_t<T, kN>(Qb, 32 * kb, 16 * rt, lane, qa[kb & 1][rt]);
         }
+      };
+      f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}, Y[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+      load_a(0);
+#pragma unroll
+      for (int kb = 0; kb < kNB; ++kb) {
+        if (kb + 1 < kNB) load_a(kb + 1);
+        bf16x8 sb[3];
+        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
+        gdr_mma_rows<3>(ka[kb & 1], sb, R);
+        if constexpr (kMode == kFull) gdr_mma_rows<kOut>(qa[kb & 1], sb, Y);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      bf16x8 kt[kParts == 1 ? kNT : 1][kParts];            // bf16: all tiles of the update's operand at once
+      if constexpr (kParts == 1) {
+#pragma unroll
+        for (int tn = 0; tn < kNT; ++tn) gdr_frags<T, kN>(K, 16 * tn, 0, lane, kt[tn]);
       }
       bf16x8 rb[3];
-      gdr_split<3>(cur.v[0] - cur.fk[0] * R[0], cur.v[1] - cur.fk[1] * R[1], rb);
-      f32x4 U[2];
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) U[rt] = gdr_mma<3>(cur.tf[rt], rb, f32x4{0.f, 0.f, 0.f, 0.f});
+      if (ident) gdr_split<3>(-fk[0] * R[0], -fk[1] * R[1], rb);
+      else gdr_split<3>(v[0].get() - fk[0] * R[0], v[1].get() - fk[1] * R[1], rb);
+      load_v(cn);
+      load_vec(cn, 0, fk);
+      f32x4 U[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+      gdr_mma_rows<3>(tf, rb, U);
+      load_t(cn);
       bf16x8 wb[3];
-      gdr_split<3>(cur.fu[0] * U[0], cur.fu[1] * U[1], wb);
+      gdr_split<3>(fu[0] * U[0], fu[1] * U[1], wb);
+      load_vec(cn, 2, fu);
 #pragma unroll
-      for (int tn = 0; tn < kNT; ++tn) {
-        bf16x8 a[kParts];
+      for (int tn = 0; tn < kNT; ++tn) S[tn] *= dec;
+      if constexpr (kParts == 1) {
+        gdr_mma_rows<3>(kt, wb, S);
+      } else {
 #pragma unroll
-        for (int s = 0; s < kParts; ++s) a[s] = gdr_frag<kGdrRow>(K + s * kN * kGdrRow, 16 * tn, 0, lane);
-        S[tn] = gdr_mma<3>(a, wb, S[tn] * cur.dec);
+        for (int tn = 0; tn < kNT; ++tn) {
+          gdr_frags<T, kN>(K, 16 * tn, 0, lane, kt[0]);
+          S[tn] = gdr_mma<3>(kt[0], wb, S[tn]);
+        }
       }
+      dec = vec[cn * kGdrVec + 96];
       if constexpr (kMode == kFull) {
         bf16x8 ub[kOut];
         gdr_split<kOut>(U[0], U[1], ub);
+        Y[0] *= fq[0];
+        Y[1] *= fq[1];
+        gdr_mma_rows<kOut>(pf, ub, Y);
+        load_vec(cn, 1, fq);
+        load_p(cn);
+        if (values) {
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-          const f32x4 y = gdr_mma<kOut>(cur.pf[rt], ub, Y[rt] * cur.fq[rt]);
-          if (values) gdr_store4(yrow, c * kC + 16 * rt + 4 * g4, q.L, y);
+          for (int rt = 0; rt < 2; ++rt) {
+            if ((c + 1) * kC <= q.L) gdr_store_whole4(yrow + c * kC + 16 * rt + 4 * g4, Y[rt]);
+            else gdr_store4(yrow, c * kC + 16 * rt + 4 * g4, q.L, Y[rt]);
+          }
         }
       }
     }
-    if (c + 1 < ce) {
-      if constexpr (kBuf == 1) __syncthreads();
-      put(kBuf == 2 ? buf ^ 1 : 0);
-      __syncthreads();
-    }
+    if constexpr (kBuf == 1) __syncthreads();
+    put(kBuf == 2 ? buf ^ 1 : 0);
+    __syncthreads();
   }
 
   if constexpr (kMode == kFull) {

@@ -43,6 +43,20 @@ __device__ __forceinline__ f32x4 gdr_mma(const bf16x8 (&a)[kA], const bf16x8 (&b
   return c;
 }
 
+// The same for several results at once: the products of one result follow each other
+// at a distance, so that none waits for the accumulator of the one before.
+template <int kOrd, int kA, int kB, int kR>
+__device__ __forceinline__ void gdr_mma_rows(const bf16x8 (&a)[kR][kA], const bf16x8 (&b)[kB], f32x4 (&c)[kR]) {
+#pragma unroll
+  for (int o = kOrd - 1; o >= 0; --o)
+#pragma unroll
+    for (int i = 0; i < kA; ++i)
+      if (o - i >= 0 && o - i < kB) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r) c[r] = gdr_mfma(a[r][i], b[o - i], c[r]);
+      }
+}
+
 // Eight fp32 numbers (the rows of two stacked results) -> kParts bf16 operands.
 template <int kParts>
 __device__ __forceinline__ void gdr_split(f32x4 x, f32x4 y, bf16x8 (&out)[kParts]) {
@@ -102,72 +116,80 @@ typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 
-// Eight consecutive numbers of a row from token t, zeros from token `end` on.
+// Eight consecutive numbers of a row from token t: all of them (whole), or zeros from
+// token `end` on.  The two are separate calls so that whole chunks load without
+// branches: a load in a divergent branch is waited for where the branch ends.
 struct GdrRaw16 {
   uint4 v;
-  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void load(const uint16_t* row, int64_t t, int64_t end) {
-    if (t + 8 <= end) {
-      const u32x4_u x = *reinterpret_cast<const u32x4_u*>(row + t);
-      v = make_uint4(x[0], x[1], x[2], x[3]);
-    } else {
-      uint32_t h[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = t + j < end ? (uint32_t)row[t + j] : 0u;
-      v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    }
+  __device__ __forceinline__ void whole(const uint16_t* p) {
+    const u32x4_u x = *reinterpret_cast<const u32x4_u*>(p);
+    v = make_uint4(x[0], x[1], x[2], x[3]);
   }
-  // into the plane(s) of a tile
+  __device__ __forceinline__ void part(const uint16_t* p, int64_t valid) {
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = j < valid ? (uint32_t)p[j] : 0u;
+    v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  }
+  __device__ __forceinline__ void save(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  // into the plane(s) of a tile; zeros where mask is 0 (all ones otherwise)
   template <int kPlaneStride>
-  __device__ __forceinline__ void put(uint16_t* dst) const { *reinterpret_cast<uint4*>(dst) = v; }
+  __device__ __forceinline__ void put(uint16_t* dst, uint32_t mask) const {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(v.x & mask, v.y & mask, v.z & mask, v.w & mask);
+  }
 };
 
 struct GdrRaw32 {
   f32x4 a, b;
-  __device__ __forceinline__ void zero() { a = b = f32x4{0.f, 0.f, 0.f, 0.f}; }
-  __device__ __forceinline__ void load(const float* row, int64_t t, int64_t end) {
-    if (t + 8 <= end) {
-      a = *reinterpret_cast<const f32x4_u*>(row + t);
-      b = *reinterpret_cast<const f32x4_u*>(row + t + 4);
-    } else {
+  __device__ __forceinline__ void whole(const float* p) {
+    a = *reinterpret_cast<const f32x4_u*>(p);
+    b = *reinterpret_cast<const f32x4_u*>(p + 4);
+  }
+  __device__ __forceinline__ void part(const float* p, int64_t valid) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a[j] = t + j < end ? row[t + j] : 0.0f;
-        b[j] = t + 4 + j < end ? row[t + 4 + j] : 0.0f;
-      }
+    for (int j = 0; j < 4; ++j) {
+      a[j] = j < valid ? p[j] : 0.0f;
+      b[j] = 4 + j < valid ? p[4 + j] : 0.0f;
     }
   }
+  __device__ __forceinline__ void save(float* p) const {
+    *reinterpret_cast<f32x4*>(p) = a;
+    *reinterpret_cast<f32x4*>(p + 4) = b;
+  }
   template <int kPlaneStride>
-  __device__ __forceinline__ void put(uint16_t* dst) const {
+  __device__ __forceinline__ void put(uint16_t* dst, uint32_t mask) const {
     bf16x8 part[3];
     gdr_split<3>(a, b, part);
 #pragma unroll
-    for (int s = 0; s < 3; ++s) *reinterpret_cast<uint4*>(dst + s * kPlaneStride) = __builtin_bit_cast(uint4, part[s]);
+    for (int s = 0; s < 3; ++s) {
+      const uint4 w = __builtin_bit_cast(uint4, part[s]);
+      *reinterpret_cast<uint4*>(dst + s * kPlaneStride) = make_uint4(w.x & mask, w.y & mask, w.z & mask, w.w & mask);
+    }
   }
 };
 
-template <typename T> struct GdrIn;
-template <> struct GdrIn<uint16_t> { using Raw = GdrRaw16; static constexpr int kParts = 1; };
-template <> struct GdrIn<float> { using Raw = GdrRaw32; static constexpr int kParts = 3; };
 
-// Four consecutive numbers of a row from token t as fp32, zeros from `end` on.
-__device__ __forceinline__ f32x4 gdr_load4(const uint16_t* row, int64_t t, int64_t end) {
-  if (t + 4 <= end) {
-    const u32x2_u x = *reinterpret_cast<const u32x2_u*>(row + t);
-    return f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
-  }
-  f32x4 r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = t + j < end ? bf16_to_f32(row[t + j]) : 0.0f;
-  return r;
+// Four consecutive numbers of a row, kept as they are stored until they are used (a
+// conversion would be waited for at the load).
+struct GdrFour16 {
+  u32x2_u x;
+  __device__ __forceinline__ void load(const uint16_t* p) { x = *reinterpret_cast<const u32x2_u*>(p); }
+  __device__ __forceinline__ f32x4 get() const { return f32x4{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])}; }
+};
+struct GdrFour32 {
+  f32x4 x;
+  __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const f32x4_u*>(p); }
+  __device__ __forceinline__ f32x4 get() const { return x; }
+};
+
+template <typename T> struct GdrIn;
+template <> struct GdrIn<uint16_t> { using Raw = GdrRaw16; using Four = GdrFour16; static constexpr int kParts = 1; };
+template <> struct GdrIn<float> { using Raw = GdrRaw32; using Four = GdrFour32; static constexpr int kParts = 3; };
+
+__device__ __forceinline__ void gdr_store_whole4(uint16_t* p, f32x4 x) {
+  *reinterpret_cast<u32x2_u*>(p) = u32x2_u{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
 }
-__device__ __forceinline__ f32x4 gdr_load4(const float* row, int64_t t, int64_t end) {
-  if (t + 4 <= end) return *reinterpret_cast<const f32x4_u*>(row + t);
-  f32x4 r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = t + j < end ? row[t + j] : 0.0f;
-  return r;
-}
+__device__ __forceinline__ void gdr_store_whole4(float* p, f32x4 x) { *reinterpret_cast<f32x4_u*>(p) = x; }
 __device__ __forceinline__ void gdr_store4(uint16_t* row, int64_t t, int64_t end, f32x4 x) {
   if (t + 4 <= end) {
     *reinterpret_cast<u32x2_u*>(row + t) = u32x2_u{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
@@ -203,6 +225,76 @@ __device__ __forceinline__ void gdr_store_state(float* row, int64_t n, int64_t N
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (n + j < N) row[n + j] = x[j];
+}
+
+// The chunk of 32 tokens of a key head, staged by a 256-thread workgroup: kN rows
+// (numbers of the head, zeros past N) of 32 tokens in LDS, one plane per part.  Piece
+// j of thread t is eight tokens of row t / 4 + 64 j.
+template <typename T, int kN>
+struct GdrTile {
+  static constexpr int kParts = GdrIn<T>::kParts;
+  static constexpr int kPlane = kN * kGdrRow;
+  static constexpr int kSize = kPlane * kParts;
+  static constexpr int kPieces = kN / 64;
+  using Raw = typename GdrIn<T>::Raw;
+  int64_t row[kPieces];
+  Raw raw[kPieces];
+  uint32_t mask[kPieces];      // zero for rows past N
+  __device__ __forceinline__ void init(int64_t N, int tid) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int64_t n = (tid >> 2) + 64 * j;
+      mask[j] = n < N ? ~0u : 0u;
+      row[j] = n < N ? n : N - 1;
+    }
+  }
+  // all 32 tokens from `rows`, whose rows are `stride` apart
+  __device__ __forceinline__ void load(const T* rows, int64_t stride, int tid) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) raw[j].whole(rows + row[j] * stride + 8 * (tid & 3));
+  }
+  // the first `valid` of them, zeros behind
+  __device__ __forceinline__ void load_part(const T* rows, int64_t stride, int64_t valid, int tid) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) raw[j].part(rows + row[j] * stride + 8 * (tid & 3), valid - 8 * (tid & 3));
+  }
+  __device__ __forceinline__ void put(uint16_t* tile, int tid) const {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+      raw[j].template put<kPlane>(tile + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3), mask[j]);
+  }
+  // as they were loaded, into dense rows of 32
+  __device__ __forceinline__ void save(T* rows, int tid) const {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+      if (mask[j]) raw[j].save(rows + row[j] * kGdrChunk + 8 * (tid & 3));
+  }
+};
+
+// Where chunk c of the rows at `rows` (stride L) is read: in place, or, when the row
+// ends inside it, from its zero-padded copy (stride 32) that the preparation left.
+template <typename T>
+struct GdrChunkSrc {
+  const T* at;
+  int64_t stride;
+  __device__ __forceinline__ GdrChunkSrc(const T* rows, int64_t L, const T* tail, int64_t c, int64_t len) {
+    const bool whole = (c + 1) * kGdrChunk <= len;
+    at = whole ? rows + c * kGdrChunk : tail;
+    stride = whole ? L : kGdrChunk;
+  }
+};
+
+template <typename T, int kN>
+__device__ __forceinline__ void gdr_frags_t(const uint16_t* tile, int row0, int col0, int lane,
+                                            bf16x8 (&f)[GdrIn<T>::kParts]) {
+#pragma unroll
+  for (int s = 0; s < GdrIn<T>::kParts; ++s) f[s] = gdr_frag_t<kGdrRow>(tile + s * kN * kGdrRow, row0, col0, lane);
+}
+template <typename T, int kN>
+__device__ __forceinline__ void gdr_frags(const uint16_t* tile, int row0, int col0, int lane,
+                                          bf16x8 (&f)[GdrIn<T>::kParts]) {
+#pragma unroll
+  for (int s = 0; s < GdrIn<T>::kParts; ++s) f[s] = gdr_frag<kGdrRow>(tile + s * kN * kGdrRow, row0, col0, lane);
 }
 
 // Work item of workgroup `id` of `n` so that each of the 8 XCDs (workgroups go

@@ -185,6 +185,8 @@ struct GdrChunkParams {
   GdrParams g;
   uint16_t* planes;        // per block: 3 planes of T, then p_parts of the query matrix
   float* vec;              // per block: factors of k (32), of q (32), of u (32), the chunk's decay
+  void *tail_k, *tail_q;   // in dtype: (B, G, N, 32) a row's last, partial chunk, zeros behind its end
+  void* tail_v;            // (B, H, P, 32)
   float* seg_M;            // (B, S - 1, H, N, N) transition of each segment but the last (S > 1)
   float* seg_h;            // (B, S - 1, H, P, N) its end state from a zero start
   float* seg_start;        // (B, S, H, P, N) state entering each segment

@@ -120,16 +120,19 @@ def test_workspace_size_of_invalid_shapes():
 
 
 def test_workspace_size_plan():
-    """6 operand planes of 2 KB and 512 bytes of factors per head and chunk of 32 tokens; few heads over a
-    long L add segments: a transition and an end state for each but the last, a start for each."""
+    """6 operand planes of 2 KB and 512 bytes of factors per head and chunk of 32 tokens; a partial last chunk
+    of k, q and v per row; few heads over a long L add segments: a transition and an end state for each but
+    the last, a start for each."""
     ws = _lib.gdr_workspace_size
     a = lambda x: (x + 255) // 256 * 256  # noqa: E731
     assert ws(4, 40, 20, 128, 128, 1) == 0
     blocks = 4 * 40 * 64
-    assert ws(4, 40, 20, 128, 128, 2048) == a(blocks * 6 * 2048) + a(blocks * 512)
+    assert ws(4, 40, 20, 128, 128, 2048) == (a(blocks * 6 * 2048) + a(blocks * 512) + 2 * a(80 * 128 * 64)
+                                             + a(160 * 128 * 64))
     with _lib.gdr_test_knobs(kernel="chunk", segments=3):
-        S, blocks = 3, 2 * 4
-        assert ws(1, 2, 2, 40, 96, 100) == (a(blocks * 6 * 2048) + a(blocks * 512) + a(2 * 1 * 96 * 96 * 4)
+        blocks = 2 * 4
+        assert ws(1, 2, 2, 40, 96, 100) == (a(blocks * 6 * 2048) + a(blocks * 512) + 2 * a(2 * 96 * 64)
+                                            + a(2 * 40 * 64) + a(2 * 1 * 96 * 96 * 4)
                                             + a(2 * 1 * 40 * 96 * 4) + a(2 * 2 * 40 * 96 * 4))   # 4 chunks: 2 + 2
     with _lib.gdr_test_knobs(kernel="token"):
         assert ws(4, 40, 20, 128, 128, 2048) == 0
