@@ -89,6 +89,38 @@ int mamba_gdr_update(float* state, const int32_t* slots, const void* q, const vo
                      mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags, hipStream_t stream);
 
 /*
+ * Bytes of workspace mamba_gdr_bwd needs (sizes only; callable without a GPU),
+ * (size_t)-1 for an invalid or unsupported shape.  Per token and value head it holds
+ * the updates and the gradient of v in fp32 (8 P bytes), and per 128 tokens two states.
+ */
+size_t mamba_gdr_bwd_workspace_size(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
+                                    mamba_dtype_t in_dtype, mamba_dtype_t grad_dtype);
+
+/*
+ * Gradients of mamba_gdr_fwd for a gradient dy of y and, optionally, dfinal_state of
+ * the final state.  Nothing of the forward pass is kept: the states are recomputed.
+ *   dy             : (B, H*P, L) grad_dtype.
+ *   dfinal_state   : (B, H*P, N) fp32 or NULL (zeros).
+ *   dq, dk         : (B, G*N, L) grad_dtype, written (summed over the value heads of a key
+ *                    head, and through the normalisation with MAMBA_FLAG_QK_NORM).
+ *   dv             : (B, H*P, L) grad_dtype, written.
+ *   ddelta, dbeta  : (B, H, L) grad_dtype, written: gradients of the raw values.
+ *   dA, ddelta_bias : (H) fp32, written (summed over batch rows and tokens), also when
+ *                    delta_bias is NULL.
+ *   dinitial_state : (B, H*P, N) fp32, written, or NULL.
+ * All outputs are overwritten, dense, and zero for tokens behind a row's end.
+ */
+int mamba_gdr_bwd(const void* q, const void* k, const void* v, const void* delta, const void* beta,
+                  const float* A, const float* delta_bias, const float* initial_state,
+                  const int32_t* lengths, const void* dy, const float* dfinal_state,
+                  void* dq, void* dk, void* dv, void* ddelta, void* dbeta, float* dA, float* ddelta_bias,
+                  float* dinitial_state,
+                  int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
+                  int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                  mamba_dtype_t in_dtype, mamba_dtype_t grad_dtype, unsigned flags,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Test and diagnostic knobs, process-wide like mamba_set_test_knobs: how a call is
  * carried out, never what it computes (to fp32 rounding).  A workspace size asked
  * for before a change does not fit a call after it.

@@ -79,6 +79,10 @@ def lib() -> ctypes.CDLL:
             L.mamba_gdr_workspace_size.restype = sz
             L.mamba_gdr_fwd.argtypes = [vp] * 11 + [i64] * 9 + [f32, c_int, c_int, u32, vp, sz, vp]
             L.mamba_gdr_fwd.restype = c_int
+            L.mamba_gdr_bwd_workspace_size.argtypes = [i64] * 6 + [c_int, c_int]
+            L.mamba_gdr_bwd_workspace_size.restype = sz
+            L.mamba_gdr_bwd.argtypes = [vp] * 19 + [i64] * 9 + [f32, c_int, c_int, u32, vp, sz, vp]
+            L.mamba_gdr_bwd.restype = c_int
             L.mamba_gdr_update.argtypes = [vp] * 10 + [i64] * 9 + [f32, c_int, c_int, u32, vp]
             L.mamba_gdr_update.restype = c_int
             L.mamba_gdr_set_test_knobs.argtypes = [c_int, i64]
@@ -606,6 +610,61 @@ def gdr_fwd(q, k, v, delta, beta, A, delta_bias=None, *, groups=None, initial_st
     if st != 0:
         raise MambaError(st, "mamba_gdr_fwd")
     return (y, final_state) if return_final_state else y
+
+
+def gdr_bwd_workspace_size(B: int, H: int, G: int, P: int, N: int, L: int, dtype=None, grad_dtype=None) -> int:
+    """Bytes gdr_bwd needs for these sizes and dtypes (bfloat16 by default; gradients like the inputs)."""
+    f32 = _torch().float32
+    code = MAMBA_F32 if dtype == f32 else MAMBA_BF16
+    gcode = code if grad_dtype is None else MAMBA_F32 if grad_dtype == f32 else MAMBA_BF16
+    n = lib().mamba_gdr_bwd_workspace_size(B, H, G, P, N, L, code, gcode)
+    if n == ctypes.c_size_t(-1).value:
+        raise MambaError(-2, "mamba_gdr_bwd_workspace_size")
+    return n
+
+
+def gdr_bwd(q, k, v, delta, beta, A, delta_bias, dy, *, groups=None, initial_state=None, dfinal_state=None,
+            lengths=None, qk_norm=False, scale=None, workspace=None, stream=None):
+    """Gradients of gdr_fwd for the output gradient dy (B, H*P, L) and, optionally, the
+    final state's dfinal_state (B, H*P, N) fp32; the other arguments as for gdr_fwd.
+
+    Returns a dict: dq, dk (B, G*N, L), dv (B, H*P, L), ddelta, dbeta (B, H, L) in dy's
+    dtype; dA, ddelta_bias (H) fp32; dinitial_state (B, H*P, N) fp32 (None without
+    initial_state).
+    """
+    torch = _torch()
+    B, H, G, P, N = _gdr_sizes(q, v, delta, groups, 3)
+    L, dev, in_dt = q.shape[2], q.device, q.dtype
+    qs = _check_rows(q, "q", (B, G * N, L), in_dt, dev)
+    ks = _check_rows(k, "k", (B, G * N, L), in_dt, dev)
+    vs = _check_rows(v, "v", (B, H * P, L), in_dt, dev)
+    _check(delta, "delta", (B, H, L), in_dt, dev)
+    _check(beta, "beta", (B, H, L), in_dt, dev)
+    _check(A, "A", (H,), torch.float32, dev)
+    _check(delta_bias, "delta_bias", (H,), torch.float32, dev)
+    _check(initial_state, "initial_state", (B, H * P, N), torch.float32, dev)
+    _check(dfinal_state, "dfinal_state", (B, H * P, N), torch.float32, dev)
+    _check(lengths, "lengths", (B,), torch.int32, dev)
+    _dtype_code(dy)
+    _check(dy, "dy", (B, H * P, L), None, dev)
+    gdt = dy.dtype
+    with torch.cuda.device(dev):
+        def new(*shape, dtype=gdt):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        out = {"dq": new(B, G * N, L), "dk": new(B, G * N, L), "dv": new(B, H * P, L), "ddelta": new(B, H, L),
+               "dbeta": new(B, H, L), "dA": new(H, dtype=torch.float32), "ddelta_bias": new(H, dtype=torch.float32),
+               "dinitial_state": None if initial_state is None else new(B, H * P, N, dtype=torch.float32)}
+        workspace = _workspace(workspace, gdr_bwd_workspace_size(B, H, G, P, N, L, in_dt, gdt), dev)
+        st = lib().mamba_gdr_bwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(beta), _ptr(A), _ptr(delta_bias), _ptr(initial_state),
+            _ptr(lengths), _ptr(dy), _ptr(dfinal_state), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+            _ptr(out["ddelta"]), _ptr(out["dbeta"]), _ptr(out["dA"]), _ptr(out["ddelta_bias"]),
+            _ptr(out["dinitial_state"]), B, H, G, P, N, L, qs, ks, vs, _gdr_scale(scale, N), _dtype_code(q),
+            _dtype_code(dy), FLAG_QK_NORM if qk_norm else 0, _ptr(workspace), _nbytes(workspace), _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_gdr_bwd")
+    return out
 
 
 def gdr_update(state, q, k, v, delta, beta, A, delta_bias=None, *, groups=None, slots=None, qk_norm=False,

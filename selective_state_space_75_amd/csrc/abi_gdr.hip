@@ -106,6 +106,34 @@ GdrPlan make_gdr_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int
   return q;
 }
 
+struct GdrBwdPlan {
+  int64_t n_chunks = 0, n_blks = 0;
+  size_t off_planes = 0, off_vec = 0, off_tk = 0, off_tq = 0, off_tv = 0, off_tdy = 0, off_u = 0, off_dv = 0, off_S = 0,
+         off_dS = 0, off_part = 0, bytes = 0;
+};
+
+GdrBwdPlan make_gdr_bwd_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L, size_t e, size_t eg) {
+  GdrBwdPlan q;
+  q.n_chunks = (L + mamba::kGdrChunk - 1) / mamba::kGdrChunk;
+  q.n_blks = (q.n_chunks + mamba::kGdrBlk - 1) / mamba::kGdrBlk;
+  const size_t heads = size_t(B) * H, blocks = heads * q.n_chunks, C = mamba::kGdrChunk;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o += align256(bytes); return at; };
+  q.off_planes = take(blocks * 9 * mamba::kGdrPlane * sizeof(uint16_t));
+  q.off_vec = take(blocks * mamba::kGdrVecBwd * sizeof(float));
+  q.off_tk = take(size_t(B) * G * N * C * e);
+  q.off_tq = take(size_t(B) * G * N * C * e);
+  q.off_tv = take(heads * P * C * e);
+  q.off_tdy = take(heads * P * C * eg);
+  q.off_u = take(blocks * P * C * sizeof(float));
+  q.off_dv = take(blocks * P * C * sizeof(float));
+  q.off_S = take(heads * q.n_blks * P * N * sizeof(float));
+  q.off_dS = take(heads * q.n_blks * P * N * sizeof(float));
+  q.off_part = take(heads * q.n_blks * 2 * sizeof(float));
+  q.bytes = o;
+  return q;
+}
+
 // Workgroups of the largest launch of a plan.
 bool gdr_grid_ok(const GdrPlan& q, int64_t B, int64_t H, int64_t G, int64_t P, int64_t N) {
   if (!q.chunk) return B * H * ((P + 3) / 4) / 4 + 1 < kMaxGrid;
@@ -181,10 +209,65 @@ int mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* delta
       c.seg_start = reinterpret_cast<float*>(ws + plan.off_start);
     }
     c.p_parts = out_dtype == MAMBA_BF16 ? 2 : 3;
+    c.vec_stride = mamba::kGdrVec;
     return mamba::launch_gdr_chunk(c, dt_of(in_dtype), dt_of(out_dtype), stream) == hipSuccess ? MAMBA_OK
                                                                                               : MAMBA_ERR_HIP;
   }
   return mamba::launch_gdr_step(p, dt_of(in_dtype), dt_of(out_dtype), stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+}
+
+size_t mamba_gdr_bwd_workspace_size(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
+                                    mamba_dtype_t in_dtype, mamba_dtype_t grad_dtype) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(grad_dtype) || !gdr_sizes_ok(B, H, G, P, N, L) || N > 128) return (size_t)-1;
+  return make_gdr_bwd_plan(B, H, G, P, N, L, width(in_dtype), width(grad_dtype)).bytes;
+}
+
+int mamba_gdr_bwd(const void* q, const void* k, const void* v, const void* delta, const void* beta, const float* A,
+                  const float* delta_bias, const float* initial_state, const int32_t* lengths, const void* dy,
+                  const float* dfinal_state, void* dq, void* dk, void* dv, void* ddelta, void* dbeta, float* dA,
+                  float* ddelta_bias, float* dinitial_state, int64_t B, int64_t H, int64_t G, int64_t P, int64_t N,
+                  int64_t L, int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, mamba_dtype_t in_dtype,
+                  mamba_dtype_t grad_dtype, unsigned flags, void* workspace, size_t workspace_bytes,
+                  hipStream_t stream) {
+  const int st = check_gdr(B, H, G, P, N, L, q_stride, k_stride, v_stride, in_dtype, grad_dtype, flags);
+  if (st != MAMBA_OK) return st;
+  if (!q || !k || !v || !delta || !beta || !A || !dy || !dq || !dk || !dv || !ddelta || !dbeta || !dA || !ddelta_bias)
+    return MAMBA_ERR_NULL;
+  for (const void* ptr : {q, k, v, delta, beta})
+    if (!aligned(ptr, width(in_dtype))) return MAMBA_ERR_ALIGN;
+  for (const void* ptr : {dy, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)ddelta, (const void*)dbeta})
+    if (!aligned(ptr, width(grad_dtype))) return MAMBA_ERR_ALIGN;
+  for (const void* ptr : {(const void*)A, (const void*)delta_bias, (const void*)initial_state, (const void*)lengths,
+                          (const void*)dfinal_state, (const void*)dA, (const void*)ddelta_bias,
+                          (const void*)dinitial_state})
+    if (ptr && !aligned(ptr, 4)) return MAMBA_ERR_ALIGN;
+  const GdrBwdPlan plan = make_gdr_bwd_plan(B, H, G, P, N, L, width(in_dtype), width(grad_dtype));
+  if (B * G >= kMaxGrid / plan.n_chunks || B * H >= kMaxGrid / ((P + 63) / 64) || H >= kMaxGrid) return MAMBA_ERR_SHAPE;
+  if (!workspace || workspace_bytes < plan.bytes) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
+  mamba::GdrChunkParams c{};
+  c.g = gdr_params(q, k, v, delta, beta, A, delta_bias, B, H, G, P, N, L, q_stride, k_stride, v_stride, scale, flags);
+  c.g.init = initial_state; c.g.lengths = lengths;
+  c.g.state_vec = N % 4 == 0;
+  for (const void* ptr : {(const void*)initial_state, (const void*)dfinal_state, (const void*)dinitial_state})
+    if (ptr && !aligned(ptr, 16)) c.g.state_vec = 0;
+  char* ws = static_cast<char*>(workspace);
+  c.planes = reinterpret_cast<uint16_t*>(ws + plan.off_planes);
+  c.vec = reinterpret_cast<float*>(ws + plan.off_vec);
+  c.tail_k = ws + plan.off_tk; c.tail_q = ws + plan.off_tq; c.tail_v = ws + plan.off_tv; c.tail_dy = ws + plan.off_tdy;
+  c.n_chunks = plan.n_chunks; c.S = 1; c.seg_chunks = plan.n_chunks;
+  c.p_parts = 3;
+  c.vec_stride = mamba::kGdrVecBwd;
+  c.dy = dy; c.dfinal = dfinal_state;
+  c.u = reinterpret_cast<float*>(ws + plan.off_u);
+  c.dvw = reinterpret_cast<float*>(ws + plan.off_dv);
+  c.blk_S = reinterpret_cast<float*>(ws + plan.off_S);
+  c.blk_dS = reinterpret_cast<float*>(ws + plan.off_dS);
+  c.n_blks = plan.n_blks;
+  c.dq = dq; c.dk = dk; c.dv = dv; c.ddelta = ddelta; c.dbeta = dbeta;
+  c.dA = dA; c.dbias = ddelta_bias; c.dinit = dinitial_state;
+  c.part = reinterpret_cast<float*>(ws + plan.off_part);
+  return mamba::launch_gdr_bwd(c, dt_of(in_dtype), dt_of(grad_dtype), stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 
 int mamba_gdr_update(float* state, const int32_t* slots, const void* q, const void* k, const void* v,

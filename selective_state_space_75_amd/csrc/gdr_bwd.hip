@@ -1,0 +1,698 @@
+// gdr_bwd.hip -- gradients of the gated delta rule over sequences (gfx950).
+//
+// Notation of gdr_chunk.hip, for one chunk with entering state S0 and the gradient
+// dS of the state that leaves it (unit keys and queries when they are normalised):
+//   updates  u = T (V - exp(G) K S0^T)
+//   dV  = T^T (E K dS^T + Pm^T dY),  E = diag exp(G_C - G), Pm the scaled query matrix
+//   dS0 = exp(G_C) dS + (s exp(G) dY)^T Q - (exp(G) dV)^T K
+//   M1 = s tril(D o dY U^T),  M2 = stril(D o dV U^T)
+//   dQ  = s exp(G) dY S0 + M1 K
+//   dK  = E U dS + M1^T Q - (M2 + M2^T) K - exp(G) dV S0
+//   dbeta_raw_t = (dV_t . U_t) (1 - b_t) / b_t         (u = b (v - p), dV = b du)
+// The gradient of token t's log decay is everything that passes from before t to t
+// or after it:
+//   dg_t = sum_(i >= t > j) [M1_ij q_i.k_j - M2_ij k_i.k_j] + sum_(i >= t) X_i
+//          + sum_(j < t) Y_j + exp(G_C) <dS, S0>,
+//   X_i = q_i . (s exp(G) dY S0)_i - k_i . (exp(G) dV S0)_i,  Y_j = k_j . (E U dS)_j.
+// (The shorter identity dg_t = <dS, S> + sum_(i >= t) (q_i . dQ_i - v_i . dV_i) subtracts
+// the tokens' own terms again, which are larger than what is left: it loses an order
+// of magnitude in fp32 and the sums over tokens lose more.)
+//
+// Four launches after the preparation (gdr_chunk.hip, which leaves T, T^T, Pm^T):
+//   states  forward along L: U of every chunk, S at every block of 4 chunks;
+//   adjoint backward along L: dV of every chunk, dS at the end of every block;
+//   grads   all blocks at once: the states inside a block are rebuilt forward from S,
+//           the adjoints backward from dS, and everything else is products;
+//   sums    dA and ddelta_bias from the blocks' partial sums, in a fixed order.
+// The chains are cut over value channels (16 per wave, gdr_chunk.hip); the grads
+// launch is cut over the N numbers of the keys (16 per wave), where dQ and dK are
+// sums over value channels that stay inside a wave.  One workgroup takes all value
+// heads of a key head, so dQ and dK need no reduction between workgroups.
+#include "gdr_mfma.hpp"
+
+namespace mamba {
+namespace {
+
+// Sum over the 16 lanes of a lane group.
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+  for (int m = 1; m < 16; m *= 2) x += __shfl_xor(x, m);
+  return x;
+}
+
+// ----------------------------------------------------------------------------- adjoint chain
+template <typename T, typename O, int kN>
+__global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
+  constexpr int kParts = GdrIn<T>::kParts;
+  constexpr int kGParts = GdrIn<O>::kParts;
+  constexpr int kTile = kN * kGdrRow * kParts;
+  constexpr int kNT = kN / 16, kNB = kN / 32;
+  constexpr int kBuf = kParts == 1 ? 2 : 1;
+  __shared__ __align__(16) uint16_t Kt[kBuf][kTile];
+  __shared__ __align__(16) uint16_t Qt[kBuf][kTile];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const GdrParams& q = p.g;
+  const int64_t slices = (q.P + 63) / 64;
+  const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
+  const int64_t slice = it % slices, h = (it / slices) % q.H, b = it / (slices * q.H);
+  const int64_t bh = b * q.H + h, g = h / (q.H / q.G);
+  const int64_t ch = slice * 64 + 16 * w + i16;
+  const bool mine = ch < q.P;                    // lanes without a channel run along on channel 0
+  const int64_t vch = mine ? ch : 0;
+  const int64_t len = gdr_length(q, b), ce = (len + kC - 1) / kC;
+
+  const T* krows = static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L;
+  const T* qrows = static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L;
+  const T* tail_k = static_cast<const T*>(p.tail_k) + (b * q.G + g) * q.N * kC;
+  const T* tail_q = static_cast<const T*>(p.tail_q) + (b * q.G + g) * q.N * kC;
+  const O* dyrow = static_cast<const O*>(p.dy) + (bh * q.P + vch) * q.L + 4 * g4;
+  const O* tail_dy = static_cast<const O*>(p.tail_dy) + (bh * q.P + vch) * kC + 4 * g4;
+  O* dvrow = static_cast<O*>(p.dv) + (bh * q.P + vch) * q.L;
+  const int64_t blk0 = block_of(p, b, h, 0);
+  const uint16_t* planes = p.planes + blk0 * 9 * kGdrPlane + lane * 8;
+  const float* vec = p.vec + blk0 * p.vec_stride;
+
+  f32x4 S[kNT];                                  // dS: column ch, rows of the key numbers
+#pragma unroll
+  for (int tn = 0; tn < kNT; ++tn) {
+    S[tn] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (mine && p.dfinal) S[tn] = gdr_load_state(p.dfinal + (bh * q.P + ch) * q.N, 16 * tn + 4 * g4, q.N, q.state_vec);
+  }
+  // tokens behind the row's end
+  if (mine) {
+    for (int64_t t = ce * kC + 4 * g4; t < q.L; t += 16) gdr_store4(dvrow, t, q.L, f32x4{0.f, 0.f, 0.f, 0.f});
+  }
+
+  bf16x8 tf[2][3], pf[2][3];
+  typename GdrIn<O>::Four dy[2];
+  f32x4 fk[2], fq[2], fu[2];
+  float dec = 0.0f;
+  GdrTile<T, kN> tk, tq;
+  tk.init(q.N, tid);
+  tq.init(q.N, tid);
+  auto load_tiles = [&](int64_t c) {
+    const GdrChunkSrc<T> sk(krows, q.L, tail_k, c, len), sq(qrows, q.L, tail_q, c, len);
+    tk.load(sk.at, sk.stride, tid);
+    tq.load(sq.at, sq.stride, tid);
+  };
+  auto load_rest = [&](int64_t c) {
+    const O* src = (c + 1) * kC <= len ? dyrow + c * kC : tail_dy;
+    dy[0].load(src);
+    dy[1].load(src + 16);
+    const uint16_t* pl = planes + c * 9 * kGdrPlane;
+    const float* vc = vec + c * p.vec_stride + 4 * g4;
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+#pragma unroll
+      for (int s = 0; s < 3; ++s) {
+        tf[rt][s] = *reinterpret_cast<const bf16x8*>(pl + (3 + s) * kGdrPlane + rt * 512);
+        pf[rt][s] = *reinterpret_cast<const bf16x8*>(pl + (6 + s) * kGdrPlane + rt * 512);
+      }
+      fk[rt] = *reinterpret_cast<const f32x4*>(vc + 16 * rt);
+      fq[rt] = *reinterpret_cast<const f32x4*>(vc + 32 + 16 * rt);
+      fu[rt] = *reinterpret_cast<const f32x4*>(vc + 64 + 16 * rt);
+    }
+    dec = vec[c * p.vec_stride + 96];
+  };
+  if (ce > 0) {
+    load_tiles(ce - 1);
+    tk.put(Kt[0], tid);
+    tq.put(Qt[0], tid);
+#pragma unroll
+    for (int buf = 0; buf < kBuf; ++buf) {
+      tk.clear(Kt[buf], tid);
+      tq.clear(Qt[buf], tid);
+    }
+    load_rest(ce - 1);
+    __syncthreads();
+  }
+  for (int64_t c = ce - 1; c >= 0; --c) {
+    const int buf = kBuf == 2 ? (int)((ce - 1 - c) & 1) : 0;
+    const uint16_t *K = Kt[buf], *Q = Qt[buf];
+    const int64_t cn = c > 0 ? c - 1 : 0;                  // the first chunk loads itself again
+    load_tiles(cn);
+    if (mine && (c % kGdrBlk == kGdrBlk - 1 || c == ce - 1)) {
+      float* dst = p.blk_dS + ((bh * p.n_blks + c / kGdrBlk) * q.P + ch) * q.N;
+#pragma unroll
+      for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+    }
+    // right-hand side E K dS^T + Pm^T dY
+    f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+    bf16x8 ka[2][2][kParts];
+    auto load_a = [&](int kb) {
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) gdr_frags_t<T, kN>(K, 32 * kb, 16 * rt, lane, ka[kb & 1][rt]);
+    };
+    load_a(0);
+#pragma unroll
+    for (int kb = 0; kb < kNB; ++kb) {
+      if (kb + 1 < kNB) load_a(kb + 1);
+      bf16x8 sb[3];
+      gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
+      gdr_mma_rows<3>(ka[kb & 1], sb, R);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const f32x4 d0 = dy[0].get(), d1 = dy[1].get();
+    bf16x8 db[kGParts];
+    gdr_split<kGParts>(d0, d1, db);
+    R[0] *= fu[0];
+    R[1] *= fu[1];
+    gdr_mma_rows<3>(pf, db, R);
+    bf16x8 rb[3];
+    gdr_split<3>(R[0], R[1], rb);
+    f32x4 W[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};     // dV
+    gdr_mma_rows<3>(tf, rb, W);
+    bf16x8 wk[3], wq[3];
+    gdr_split<3>(-fk[0] * W[0], -fk[1] * W[1], wk);
+    gdr_split<3>(fq[0] * d0, fq[1] * d1, wq);
+    const float dc = dec;
+    load_rest(cn);
+#pragma unroll
+    for (int tn = 0; tn < kNT; ++tn) {
+      bf16x8 a[kParts], aq[kParts];
+      gdr_frags<T, kN>(K, 16 * tn, 0, lane, a);
+      gdr_frags<T, kN>(Q, 16 * tn, 0, lane, aq);
+      S[tn] = gdr_mma<3>(aq, wq, S[tn] * dc);
+      S[tn] = gdr_mma<3>(a, wk, S[tn]);
+    }
+    if (mine) {
+      float* dst = p.dvw + ((blk0 + c) * q.P + ch) * kC + 4 * g4;
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        *reinterpret_cast<f32x4*>(dst + 16 * rt) = W[rt];
+        gdr_store4(dvrow, c * kC + 16 * rt + 4 * g4, q.L, W[rt]);
+      }
+    }
+    if constexpr (kBuf == 1) __syncthreads();
+    tk.put(Kt[kBuf == 2 ? buf ^ 1 : 0], tid);
+    tq.put(Qt[kBuf == 2 ? buf ^ 1 : 0], tid);
+    __syncthreads();
+  }
+  if (mine && p.dinit) {
+    float* dst = p.dinit + (bh * q.P + ch) * q.N;
+#pragma unroll
+    for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+  }
+}
+
+// ----------------------------------------------------------------------------- the rest, block by block
+// Rows [0, rows) of 32 tokens into operand planes of kRows rows, zeros from row `rows` on.
+template <typename T, int kRows, int kThreads>
+__device__ __forceinline__ void stage_rows(uint16_t* tile, const T* src, int64_t stride, int64_t rows, int tid) {
+  constexpr int kParts = GdrIn<T>::kParts;
+#pragma unroll
+  for (int j = 0; j < (kRows * 4 + kThreads - 1) / kThreads; ++j) {
+    const int id = tid + kThreads * j;
+    if (kRows * 4 % kThreads != 0 && id >= kRows * 4) break;
+    const int64_t n = id >> 2;
+    uint16_t* dst = tile + n * kGdrRow + 8 * (id & 3);
+    if (n < rows) {
+      typename GdrIn<T>::Raw x;
+      x.whole(src + n * stride + 8 * (id & 3));
+      x.template put<kRows * kGdrRow>(dst);
+    } else {
+#pragma unroll
+      for (int s = 0; s < kParts; ++s) *reinterpret_cast<uint4*>(dst + s * kRows * kGdrRow) = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+template <int kParts, int kRows>
+__device__ __forceinline__ void plane_frags_t(const uint16_t* tile, int row0, int col0, int lane, bf16x8 (&f)[kParts]) {
+#pragma unroll
+  for (int s = 0; s < kParts; ++s) f[s] = gdr_frag_t<kGdrRow>(tile + s * kRows * kGdrRow, row0, col0, lane);
+}
+template <int kParts, int kRows>
+__device__ __forceinline__ void plane_frags(const uint16_t* tile, int row0, int col0, int lane, bf16x8 (&f)[kParts]) {
+#pragma unroll
+  for (int s = 0; s < kParts; ++s) f[s] = gdr_frag<kGdrRow>(tile + s * kRows * kGdrRow, row0, col0, lane);
+}
+
+// Four tokens 16 rt + 4 g .. of row n of a tile as fp32 (the parts added up).
+template <int kParts, int kRows>
+__device__ __forceinline__ f32x4 tile_four(const uint16_t* tile, int n, int t) {
+  f32x4 r = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = kParts - 1; s >= 0; --s) {
+    const uint2 x = *reinterpret_cast<const uint2*>(tile + s * kRows * kGdrRow + n * kGdrRow + t);
+    r += f32x4{bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+  }
+  return r;
+}
+
+// kPS: value channels taken at a time (a slab); every sum over value channels is
+// linear, so slabs and value heads are one loop.
+template <typename T, typename O, int kN, int kPS>
+__global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
+  constexpr int kParts = GdrIn<T>::kParts, kGParts = GdrIn<O>::kParts;
+  constexpr int kW = kN / 16, kThreads = 64 * kW;
+  constexpr int kPT = kPS / 16, kPB = kPS / 32;
+  __shared__ __align__(16) uint16_t dOt[kGParts * kPS * kGdrRow];
+  __shared__ __align__(16) uint16_t dVt[3 * kPS * kGdrRow];
+  __shared__ __align__(16) uint16_t Ut[3 * kPS * kGdrRow];
+  __shared__ __align__(16) uint16_t Kt[kParts * kN * kGdrRow];
+  __shared__ __align__(16) uint16_t Qt[kParts * kN * kGdrRow];
+  __shared__ __align__(16) uint16_t mf[3][3][2][512];     // operands made of M1, M1^T and M2 + M2^T
+  __shared__ float m[4][32 * 33];                          // M2, M1, Q K^T, K K^T
+  __shared__ double cum[32];
+  __shared__ __align__(16) float gam[32], en[32], rk[32], rq[32];
+  __shared__ __align__(16) float red[2][kW][32];
+  __shared__ float X[kGdrBlk][32], Y[kGdrBlk][32], pr[kGdrBlk][32], dvu[kGdrBlk][32], flow[kW];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const GdrParams& q = p.g;
+  const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
+  const int64_t blk = it % p.n_blks, bg = it / p.n_blks, g = bg % q.G, b = bg / q.G;
+  const int64_t len = gdr_length(q, b), nl = (len + kC - 1) / kC;
+  const int64_t cb = blk * kGdrBlk, rep = q.H / q.G;
+  const int nc = (int)(nl - cb < 0 ? 0 : nl - cb < kGdrBlk ? nl - cb : kGdrBlk);      // live chunks
+  const int64_t tb = cb * kC, te = tb + kGdrBlk * kC < q.L ? tb + kGdrBlk * kC : q.L;
+  const int n = 16 * w + i16;                              // this lane's key number
+
+  const T* krows = static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L;
+  const T* qrows = static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L;
+  const T* tail_k = static_cast<const T*>(p.tail_k) + bg * q.N * kC;
+  const T* tail_q = static_cast<const T*>(p.tail_q) + bg * q.N * kC;
+
+  f32x4 dq[kGdrBlk][2], dk[kGdrBlk][2];                    // column n, tokens 16 rt + 4 g4 ..
+#pragma unroll
+  for (int c = 0; c < kGdrBlk; ++c)
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) dq[c][rt] = dk[c][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int64_t slabs = (q.P + kPS - 1) / kPS;
+  for (int64_t hs = 0; hs < (nc > 0 ? rep * slabs : 0); ++hs) {
+    const int64_t h = g * rep + hs / slabs, bh = b * q.H + h, p0 = (hs % slabs) * kPS;
+    const bool first = hs % slabs == 0, last = hs % slabs == slabs - 1;
+    const int64_t prow = q.P - p0 < kPS ? q.P - p0 : kPS;  // channels of this slab
+    auto stage = [&](int c) {                              // everything of chunk cb + c
+      const int64_t cc = cb + c, bl = block_of(p, b, h, cc);
+      const GdrChunkSrc<T> sk(krows, q.L, tail_k, cc, len), sq(qrows, q.L, tail_q, cc, len);
+      const GdrChunkSrc<O> sy(static_cast<const O*>(p.dy) + (bh * q.P + p0) * q.L, q.L,
+                              static_cast<const O*>(p.tail_dy) + (bh * q.P + p0) * kC, cc, len);
+      stage_rows<T, kN, kThreads>(Kt, sk.at, sk.stride, q.N, tid);
+      stage_rows<T, kN, kThreads>(Qt, sq.at, sq.stride, q.N, tid);
+      stage_rows<O, kPS, kThreads>(dOt, sy.at, sy.stride, prow, tid);
+      stage_rows<float, kPS, kThreads>(dVt, p.dvw + (bl * q.P + p0) * kC, kC, prow, tid);
+      stage_rows<float, kPS, kThreads>(Ut, p.u + (bl * q.P + p0) * kC, kC, prow, tid);
+      if (tid < 32) {
+        const float* vec = p.vec + bl * p.vec_stride;
+        const double* cu = reinterpret_cast<const double*>(vec + 192);
+        const double x = cu[tid];
+        cum[tid] = x;
+        gam[tid] = hw_exp2((float)x);
+        en[tid] = hw_exp2((float)(cu[31] - x));
+        rk[tid] = vec[128 + tid];
+        rq[tid] = vec[160 + tid];
+      }
+    };
+    auto four = [&](const float* v, int rt) { return *reinterpret_cast<const f32x4*>(v + 16 * rt + 4 * g4); };
+    // sums over a chunk's key numbers: this wave's 16, then all waves by the first 32 threads
+    auto partial = [&](int which, f32x4 a, int rt) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float s = sum16(a[r]);
+        if (i16 == 0) red[which][w][16 * rt + 4 * g4 + r] = s;
+      }
+    };
+    auto collect = [&](int which, float (&to)[32]) {
+      if (tid < 32) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kW; ++k) s += red[which][k][tid];
+        to[tid] = first ? s : to[tid] + s;
+      }
+    };
+
+    // ---- forward through the block: S
+    f32x4 S[kPT];                                          // column n, rows of the value channels
+    {
+      const float* src = p.blk_S + (bh * p.n_blks + blk) * q.P * q.N;
+#pragma unroll
+      for (int tp = 0; tp < kPT; ++tp)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t row = p0 + 16 * tp + 4 * g4 + r;
+          S[tp][r] = (row < q.P && n < q.N) ? src[row * q.N + n] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kGdrBlk; ++c) {
+      if (c >= nc) break;
+      __syncthreads();
+      stage(c);
+      __syncthreads();
+      // 32 x 32 products, lower tiles only: dV U^T, dY U^T, Q K^T, K K^T
+      for (int task = w; task < 12; task += kW) {
+        const int kind = task / 3, rt = task % 3 > 0, ct = task % 3 > 1;
+        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (kind == 0) {
+#pragma unroll
+          for (int kb = 0; kb < kPB; ++kb) {
+            bf16x8 a[3], u[3];
+            plane_frags_t<3, kPS>(dVt, 32 * kb, 16 * rt, lane, a);
+            plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * ct, lane, u);
+            acc = gdr_mma<3>(a, u, acc);
+          }
+        } else if (kind == 1) {
+#pragma unroll
+          for (int kb = 0; kb < kPB; ++kb) {
+            bf16x8 a[kGParts], u[3];
+            plane_frags_t<kGParts, kPS>(dOt, 32 * kb, 16 * rt, lane, a);
+            plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * ct, lane, u);
+            acc = gdr_mma<3>(a, u, acc);
+          }
+        } else {
+          const uint16_t* rows = kind == 2 ? Qt : Kt;
+#pragma unroll
+          for (int kb = 0; kb < kN / 32; ++kb) {
+            bf16x8 a[kParts], k[kParts];
+            gdr_frags_t<T, kN>(rows, 32 * kb, 16 * rt, lane, a);
+            gdr_frags_t<T, kN>(Kt, 32 * kb, 16 * ct, lane, k);
+            acc = gdr_mma<3>(a, k, acc);
+          }
+        }
+        const int j = 16 * ct + i16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = 16 * rt + 4 * g4 + r;
+          float x = acc[r];
+          if (kind == 0 && i == j) {                       // dV_t . U_t
+            dvu[c][i] = first ? x : dvu[c][i] + x;
+          }
+          if (kind == 0) x = i > j ? x * hw_exp2((float)(cum[i] - cum[j])) : 0.0f;
+          if (kind == 1) x = i >= j ? x * q.scale * hw_exp2((float)(cum[i] - cum[j])) : 0.0f;
+          m[kind][i * 33 + j] = x;
+        }
+      }
+      // through the entering state
+      f32x4 Rq[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}, Rk[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+      for (int kb = 0; kb < kPB; ++kb) {
+        bf16x8 sb[3], ao[2][kGParts], av[2][3];
+        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+          plane_frags_t<kGParts, kPS>(dOt, 32 * kb, 16 * rt, lane, ao[rt]);
+          plane_frags_t<3, kPS>(dVt, 32 * kb, 16 * rt, lane, av[rt]);
+        }
+        gdr_mma_rows<3>(ao, sb, Rq);
+        gdr_mma_rows<3>(av, sb, Rk);
+      }
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        const f32x4 ga = four(gam, rt);
+        Rq[rt] *= ga * q.scale;
+        Rk[rt] *= ga;
+        partial(0, four(rq, rt) * tile_four<kParts, kN>(Qt, n, 16 * rt + 4 * g4) * Rq[rt] -
+                       four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4) * Rk[rt], rt);
+        dq[c][rt] += Rq[rt];
+        dk[c][rt] -= Rk[rt];
+      }
+      __syncthreads();
+      collect(0, X[c]);
+      // operands of the products with K and Q, the lengths of the contracted rows folded in;
+      // dK takes M2 + M2^T with a minus
+      for (int task = w; task < 6; task += kW) {
+        const int kind = task >> 1, rt = task & 1, row = 16 * rt + i16;
+        f32x4 x[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int col = (e < 4 ? 0 : 16) + 4 * g4 + (e & 3);
+          const int hi = row > col ? row : col, lo = row > col ? col : row;
+          float v;
+          if (kind == 0) v = row >= col ? m[1][row * 33 + col] * rk[col] : 0.0f;
+          else if (kind == 1) v = col >= row ? m[1][col * 33 + row] * rq[col] : 0.0f;
+          else v = hi > lo ? -m[0][hi * 33 + lo] * rk[col] : 0.0f;
+          x[e >> 2][e & 3] = v;
+        }
+        bf16x8 f[3];
+        gdr_split<3>(x[0], x[1], f);
+#pragma unroll
+        for (int s = 0; s < 3; ++s) *reinterpret_cast<bf16x8*>(&mf[kind][s][rt][lane * 8]) = f[s];
+      }
+      // pairs across each token: lane j walks its column from the last row up
+      if (w == kW - 1) {
+        const int j = lane & 31;
+        float acc = 0.0f;
+        const float kj = rk[j];
+        for (int t = 31; t >= 0; --t) {
+          if (t > j)
+            acc += kj * (m[1][t * 33 + j] * rq[t] * m[2][t * 33 + j] - m[0][t * 33 + j] * rk[t] * m[3][t * 33 + j]);
+          float s = (lane < 32 && j < t) ? acc : 0.0f;
+#pragma unroll
+          for (int d = 1; d < 32; d *= 2) s += __shfl_xor(s, d);
+          if (lane == 0) pr[c][t] = first ? s : pr[c][t] + s;
+        }
+      }
+      __syncthreads();
+      // within the chunk
+      {
+        bf16x8 kb_[kParts], qb[kParts];
+        plane_frags<kParts, kN>(Kt, 16 * w, 0, lane, kb_);
+        plane_frags<kParts, kN>(Qt, 16 * w, 0, lane, qb);
+        bf16x8 a[3][2][3];
+#pragma unroll
+        for (int kind = 0; kind < 3; ++kind)
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+            for (int s = 0; s < 3; ++s) a[kind][rt][s] = *reinterpret_cast<const bf16x8*>(&mf[kind][s][rt][lane * 8]);
+        gdr_mma_rows<3>(a[0], kb_, dq[c]);
+        gdr_mma_rows<3>(a[1], qb, dk[c]);
+        gdr_mma_rows<3>(a[2], kb_, dk[c]);
+      }
+      // the state after the chunk
+      {
+        const float dec = hw_exp2((float)cum[31]);
+        bf16x8 kb3[3];
+        gdr_split<3>(four(en, 0) * four(rk, 0) * tile_four<kParts, kN>(Kt, n, 4 * g4),
+                     four(en, 1) * four(rk, 1) * tile_four<kParts, kN>(Kt, n, 16 + 4 * g4), kb3);
+#pragma unroll
+        for (int tp = 0; tp < kPT; ++tp) {
+          bf16x8 a[3];
+          plane_frags<3, kPS>(Ut, 16 * tp, 0, lane, a);
+          S[tp] = gdr_mma<3>(a, kb3, S[tp] * dec);
+        }
+      }
+    }
+
+    // ---- backward through the block: dS; first what passes its end, <dS, S>
+    {
+      const float* src = p.blk_dS + (bh * p.n_blks + blk) * q.P * q.N;
+      float f = 0.0f;
+#pragma unroll
+      for (int tp = 0; tp < kPT; ++tp)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t row = p0 + 16 * tp + 4 * g4 + r;
+          const float x = (row < q.P && n < q.N) ? src[row * q.N + n] : 0.0f;
+          f = __builtin_fmaf(x, S[tp][r], f);
+          S[tp][r] = x;
+        }
+      f = sum16(f);
+      f += __shfl_xor(f, 16);
+      f += __shfl_xor(f, 32);
+      if (lane == 0) flow[w] = first ? f : flow[w] + f;
+    }
+#pragma unroll
+    for (int c = kGdrBlk - 1; c >= 0; --c) {
+      if (c >= nc) continue;
+      __syncthreads();
+      stage(c);
+      __syncthreads();
+      f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+      for (int kb = 0; kb < kPB; ++kb) {
+        bf16x8 sb[3], au[2][3];
+        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * rt, lane, au[rt]);
+        gdr_mma_rows<3>(au, sb, R);
+      }
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        R[rt] *= four(en, rt);
+        partial(1, four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4) * R[rt], rt);
+        dk[c][rt] += R[rt];
+      }
+      {
+        const float dec = hw_exp2((float)cum[31]);
+        bf16x8 kb3[3], qb3[3];
+        gdr_split<3>(-(four(gam, 0) * four(rk, 0)) * tile_four<kParts, kN>(Kt, n, 4 * g4),
+                     -(four(gam, 1) * four(rk, 1)) * tile_four<kParts, kN>(Kt, n, 16 + 4 * g4), kb3);
+        gdr_split<3>(four(gam, 0) * four(rq, 0) * q.scale * tile_four<kParts, kN>(Qt, n, 4 * g4),
+                     four(gam, 1) * four(rq, 1) * q.scale * tile_four<kParts, kN>(Qt, n, 16 + 4 * g4), qb3);
+#pragma unroll
+        for (int tp = 0; tp < kPT; ++tp) {
+          bf16x8 a[3], ao[kGParts];
+          plane_frags<3, kPS>(dVt, 16 * tp, 0, lane, a);
+          plane_frags<kGParts, kPS>(dOt, 16 * tp, 0, lane, ao);
+          S[tp] = gdr_mma<3>(a, kb3, S[tp] * dec);
+          S[tp] = gdr_mma<3>(ao, qb3, S[tp]);
+        }
+      }
+      __syncthreads();
+      collect(1, Y[c]);
+    }
+    __syncthreads();
+
+    // ---- gates of this head
+    if (last && w == 0) {
+      const int t = lane & 31;
+      float F = 0.0f, sA = 0.0f, sb = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kW; ++k) F += flow[k];
+      const float A = q.A[h], bias = q.bias ? q.bias[h] : 0.0f;
+      for (int c = nc - 1; c >= 0; --c) {
+        const float x = X[c][t], y = Y[c][t];
+        float xs = x, ys = y;                              // sums over i >= t and over j <= t
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const float o = __shfl_down(xs, d, 32), u = __shfl_up(ys, d, 32);
+          if (t + d < 32) xs += o;
+          if (t >= d) ys += u;
+        }
+        const float Z = F - __shfl(ys, 31, 32);            // what passes the whole chunk
+        const float dg = pr[c][t] + xs + (ys - y) + Z;
+        F = Z + __shfl(xs, 0, 32);                         // what passes the chunk's start
+        const int64_t tok = (cb + c) * kC + t;
+        if (lane < 32 && tok < len) {
+          const float xr = gdr_load(static_cast<const T*>(q.delta) + bh * q.L + tok) + bias;
+          const float br = gdr_load(static_cast<const T*>(q.beta) + bh * q.L + tok);
+          const float dd = dg * A * gdr_sigmoid(xr), bt = gdr_sigmoid(br);
+          gdr_store(static_cast<O*>(p.ddelta) + bh * q.L + tok, dd);
+          gdr_store(static_cast<O*>(p.dbeta) + bh * q.L + tok, bt > 0.0f ? dvu[c][t] / bt * gdr_sigmoid(-br) : 0.0f);
+          sA += dg * softplus(xr);
+          sb += dd;
+        }
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        sA += __shfl_xor(sA, d);
+        sb += __shfl_xor(sb, d);
+      }
+      if (lane == 0) {
+        float* dst = p.part + ((b * p.n_blks + blk) * q.H + h) * 2;
+        dst[0] = sA;
+        dst[1] = sb;
+      }
+    }
+  }
+
+  // gates behind the row's end, and heads of a dead block
+  for (int64_t hh = 0; hh < rep; ++hh) {
+    const int64_t bh = b * q.H + g * rep + hh;
+    for (int64_t t = (len > tb ? len : tb) + tid; t < te; t += kThreads) {
+      gdr_store(static_cast<O*>(p.ddelta) + bh * q.L + t, 0.0f);
+      gdr_store(static_cast<O*>(p.dbeta) + bh * q.L + t, 0.0f);
+    }
+    if (nc == 0 && tid < 2) p.part[((b * p.n_blks + blk) * q.H + g * rep + hh) * 2 + tid] = 0.0f;
+  }
+
+  // ---- dQ, dK: through the normalisation, rows behind the end as zeros
+  O* dqrow = static_cast<O*>(p.dq) + (bg * q.N + (n < q.N ? n : 0)) * q.L;
+  O* dkrow = static_cast<O*>(p.dk) + (bg * q.N + (n < q.N ? n : 0)) * q.L;
+#pragma unroll
+  for (int c = 0; c < kGdrBlk; ++c) {
+    const int64_t t0 = tb + c * kC;
+    if (t0 >= q.L) break;
+    if (c < nc && q.norm) {
+      const GdrChunkSrc<T> sk(krows, q.L, tail_k, cb + c, len), sq(qrows, q.L, tail_q, cb + c, len);
+      const int64_t row = n < q.N ? n : q.N - 1;
+      const float* vec = p.vec + block_of(p, b, g * rep, cb + c) * p.vec_stride + 4 * g4;
+      f32x4 kh[2], qh[2], fk[2], fq[2];
+      __syncthreads();
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        typename GdrIn<T>::Four x, y;
+        x.load(sk.at + row * sk.stride + 16 * rt + 4 * g4);
+        y.load(sq.at + row * sq.stride + 16 * rt + 4 * g4);
+        fk[rt] = *reinterpret_cast<const f32x4*>(vec + 128 + 16 * rt);
+        fq[rt] = *reinterpret_cast<const f32x4*>(vec + 160 + 16 * rt);
+        kh[rt] = x.get() * fk[rt];
+        qh[rt] = y.get() * fq[rt];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {                      // lanes past N hold zero gradients
+          const float a = sum16(qh[rt][r] * dq[c][rt][r]), e = sum16(kh[rt][r] * dk[c][rt][r]);
+          if (i16 == 0) {
+            red[0][w][16 * rt + 4 * g4 + r] = a;
+            red[1][w][16 * rt + 4 * g4 + r] = e;
+          }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        f32x4 sq4 = f32x4{0.f, 0.f, 0.f, 0.f}, sk4 = sq4;
+#pragma unroll
+        for (int k = 0; k < kW; ++k) {
+          sq4 += *reinterpret_cast<const f32x4*>(&red[0][k][16 * rt + 4 * g4]);
+          sk4 += *reinterpret_cast<const f32x4*>(&red[1][k][16 * rt + 4 * g4]);
+        }
+        dq[c][rt] = fq[rt] * (dq[c][rt] - qh[rt] * sq4);
+        dk[c][rt] = fk[rt] * (dk[c][rt] - kh[rt] * sk4);
+      }
+    }
+    if (n < q.N) {
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        gdr_store4(dqrow, t0 + 16 * rt + 4 * g4, q.L, dq[c][rt]);
+        gdr_store4(dkrow, t0 + 16 * rt + 4 * g4, q.L, dk[c][rt]);
+      }
+    }
+  }
+}
+
+// dA and ddelta_bias of one head per workgroup: the blocks' sums in a fixed order, in fp64.
+__global__ __launch_bounds__(64) void gdr_gate_sum_kernel(GdrChunkParams p) {
+  const int64_t h = blockIdx.x, rows = p.g.B * p.n_blks;
+  double a = 0.0, s = 0.0;
+  for (int64_t r = threadIdx.x; r < rows; r += 64) {
+    a += p.part[(r * p.g.H + h) * 2];
+    s += p.part[(r * p.g.H + h) * 2 + 1];
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    a += __shfl_xor(a, d);
+    s += __shfl_xor(s, d);
+  }
+  if (threadIdx.x == 0) {
+    p.dA[h] = (float)a;
+    p.dbias[h] = (float)s;
+  }
+}
+
+template <typename T, typename O, int kN>
+hipError_t bwd_n(const GdrChunkParams& p, hipStream_t s) {
+  const GdrParams& q = p.g;
+  hipLaunchKernelGGL((gdr_adjoint_kernel<T, O, kN>), dim3((unsigned)(q.B * q.H * ((q.P + 63) / 64))), dim3(256), 0, s, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)(q.B * q.G * p.n_blks));
+  // 128 channels at a time where the operands have one plane each (LDS)
+  constexpr bool kOne = GdrIn<T>::kParts == 1 && GdrIn<O>::kParts == 1;
+  if (kOne && q.P > 64)
+    hipLaunchKernelGGL((gdr_grad_kernel<T, O, kN, kOne ? 128 : 64>), grid, dim3(kN * 4), 0, s, p);
+  else
+    hipLaunchKernelGGL((gdr_grad_kernel<T, O, kN, 64>), grid, dim3(kN * 4), 0, s, p);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(gdr_gate_sum_kernel, dim3((unsigned)q.H), dim3(64), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t bwd_t(const GdrChunkParams& p, hipStream_t s) {
+  return p.g.N > 64 ? bwd_n<T, O, 128>(p, s) : bwd_n<T, O, 64>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_gdr_bwd(const GdrChunkParams& p, Dt in, Dt grad, hipStream_t s) {
+  hipError_t e = launch_gdr_prep(p, in, grad, true, s);
+  if (e != hipSuccess) return e;
+  if ((e = launch_gdr_states(p, in, s)) != hipSuccess) return e;
+  if (in == Dt::BF16) return grad == Dt::BF16 ? bwd_t<uint16_t, uint16_t>(p, s) : bwd_t<uint16_t, float>(p, s);
+  return grad == Dt::BF16 ? bwd_t<float, uint16_t>(p, s) : bwd_t<float, float>(p, s);
+}
+
+}  // namespace mamba

@@ -33,21 +33,6 @@
 namespace mamba {
 namespace {
 
-constexpr int kC = kGdrChunk;
-
-__device__ __forceinline__ int64_t block_of(const GdrChunkParams& p, int64_t b, int64_t h, int64_t c) {
-  return (b * p.g.H + h) * p.n_chunks + c;
-}
-__device__ __forceinline__ uint16_t* planes_of(const GdrChunkParams& p, int64_t blk) {
-  return p.planes + blk * (int64_t)(3 + p.p_parts) * kGdrPlane;
-}
-
-// Orders a wave's LDS accesses across its lanes (no other wave is involved).
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // ----------------------------------------------------------------------------- preparation
 // One workgroup per (batch row, key head, chunk).  K K^T and Q K^T once for all value
 // heads of the key head (wave w: rows 16 (w & 1) of K or Q), then a wave per value
@@ -55,7 +40,7 @@ __device__ __forceinline__ void wave_sync() {
 // column in registers: lane 32 half + c holds rows i = 2 m + half of column c of the
 // inverse; once row j is final, every later row takes its multiple of it, 15 fused
 // multiply-adds at most per lane and step with no dependence among them.
-template <typename T, int kN>
+template <typename T, typename O, int kN, bool kBwd>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
   constexpr int kParts = GdrIn<T>::kParts;
   constexpr int kTile = kN * kGdrRow * kParts;
@@ -97,9 +82,20 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
         x.part(v + (id >> 2) * q.L + 8 * (id & 3), len - t0 - 8 * (id & 3));
         x.save(tv + 8 * id);
       }
+      if constexpr (kBwd) {
+        const O* dy = static_cast<const O*>(p.dy) + first * q.L + t0;
+        O* td = static_cast<O*>(p.tail_dy) + first * kC;
+        for (int64_t id = tid; id < rows * 4; id += 256) {
+          typename GdrIn<O>::Raw x;
+          x.part(dy + (id >> 2) * q.L + 8 * (id & 3), len - t0 - 8 * (id & 3));
+          x.save(td + 8 * id);
+        }
+      }
     }
     tk.put(Kt, tid);
     tq.put(Qt, tid);
+    tk.clear(Kt, tid);
+    tq.clear(Qt, tid);
   }
   __syncthreads();
   {
@@ -155,8 +151,8 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
   for (int64_t hh = w; hh < rep; hh += 4) {
     const int64_t h = g * rep + hh, bh = b * q.H + h;
     const int64_t blk = block_of(p, b, h, c);
-    uint16_t* planes = planes_of(p, blk);
-    float* vec = p.vec + blk * kGdrVec;
+    uint16_t* planes = p.planes + blk * (int64_t)(kBwd ? 9 : 3 + p.p_parts) * kGdrPlane;
+    float* vec = p.vec + blk * p.vec_stride;
     // gates: base-2 log decay, held at 2^-1000 per token (zero in fp32) so that a
     // reset by an infinite step leaves differences finite
     const int64_t t = t0 + c32;
@@ -182,6 +178,11 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
       vec[32 + c32] = dec * rq;
       vec[64 + c32] = hw_exp2((float)(last - cum)) * rk;
       if (c32 == 0) vec[96] = hw_exp2((float)last);
+      if constexpr (kBwd) {
+        vec[128 + c32] = rk;
+        vec[160 + c32] = rlen[1][c32];
+        reinterpret_cast<double*>(vec + 192)[c32] = cum;
+      }
     }
     wave_sync();
     // M[j][i]: column j of the strictly lower-triangular A, its rows i with even i first
@@ -205,10 +206,21 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int col = (e < 4 ? 0 : 16) + 4 * g4 + (e & 3);
-        const float d = hw_exp2((float)(cr - cums[w][col]));
-        x[e >> 2][e & 3] = col <= row ? fr * rlen[0][col] * prod[1][row * 33 + col] * d : 0.0f;
+        if constexpr (kBwd) {             // transposed: this lane's row is a key, its columns queries
+          const float d = hw_exp2((float)(cums[w][col] - cr));
+          x[e >> 2][e & 3] = col >= row ? q.scale * rlen[1][col] * rlen[0][row] * prod[1][col * 33 + row] * d : 0.0f;
+        } else {
+          const float d = hw_exp2((float)(cr - cums[w][col]));
+          x[e >> 2][e & 3] = col <= row ? fr * rlen[0][col] * prod[1][row * 33 + col] * d : 0.0f;
+        }
       }
-      if (p.p_parts == 2) {
+      if constexpr (kBwd) {
+        bf16x8 f[3];
+        gdr_split<3>(x[0], x[1], f);
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+          *reinterpret_cast<bf16x8*>(planes + (6 + s) * kGdrPlane + rt * 512 + lane * 8) = f[s];
+      } else if (p.p_parts == 2) {
         bf16x8 f[2];
         gdr_split<2>(x[0], x[1], f);
 #pragma unroll
@@ -256,13 +268,23 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
       gdr_split<3>(y[0], y[1], f);
 #pragma unroll
       for (int s = 0; s < 3; ++s) *reinterpret_cast<bf16x8*>(planes + s * kGdrPlane + rt * 512 + lane * 8) = f[s];
+      if constexpr (kBwd) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = M[((e < 4 ? 0 : 16) + 4 * g4 + (e & 3)) * 33 + 16 * rt + i16];
+        gdr_split<3>(y[0], y[1], f);
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+          *reinterpret_cast<bf16x8*>(planes + (3 + s) * kGdrPlane + rt * 512 + lane * 8) = f[s];
+      }
     }
     wave_sync();
   }
 }
 
 // ----------------------------------------------------------------------------- the chain of chunks
-enum ChainMode { kFull = 0, kSummary = 1 };
+// kStates (for the backward pass): no queries; keeps every chunk's U and the state
+// entering every block of kGdrBlk chunks.
+enum ChainMode { kFull = 0, kSummary = 1, kStates = 2 };
 
 template <typename T, typename O, int kN, int kMode>
 __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
@@ -276,8 +298,8 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t vslices = (q.P + 63) / 64;
-  const int64_t slices = kMode == kFull ? vslices : vslices + (q.N + 63) / 64;
-  const int64_t segs = kMode == kFull ? p.S : p.S - 1;
+  const int64_t slices = kMode != kSummary ? vslices : vslices + (q.N + 63) / 64;
+  const int64_t segs = kMode != kSummary ? p.S : p.S - 1;
   const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
   const int64_t slice = it % slices, h = (it / slices) % q.H, bs = it / (slices * q.H);
   const int64_t seg = bs % segs, b = bs / segs, bh = b * q.H + h, g = h / (q.H / q.G);
@@ -303,8 +325,8 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   {
     const float* src = nullptr;
     if (mine) {
-      if (kMode == kFull && p.S > 1) src = p.seg_start + ((bs * q.H + h) * q.P + ch) * q.N;
-      else if (kMode == kFull && q.init) src = q.init + (bh * q.P + ch) * q.N;
+      if (kMode != kSummary && p.S > 1) src = p.seg_start + ((bs * q.H + h) * q.P + ch) * q.N;
+      else if (kMode != kSummary && q.init) src = q.init + (bh * q.P + ch) * q.N;
     }
 #pragma unroll
     for (int tn = 0; tn < kNT; ++tn) {
@@ -325,9 +347,9 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   f32x4 fk[2], fq[2], fu[2];
   float dec = 0.0f;
   const int64_t blk0 = block_of(p, b, h, 0);
-  const uint16_t* planes = planes_of(p, blk0) + lane * 8;
-  const int64_t pstride = (int64_t)(3 + p.p_parts) * kGdrPlane;
-  const float* vec = p.vec + blk0 * kGdrVec;
+  const int64_t pstride = (int64_t)(kMode == kStates ? 9 : 3 + p.p_parts) * kGdrPlane, vstride = p.vec_stride;
+  const uint16_t* planes = p.planes + blk0 * pstride + lane * 8;
+  const float* vec = p.vec + blk0 * vstride;
   auto load_v = [&](int64_t c) {
     const T* src = (c + 1) * kC <= len ? vrow + c * kC : tail_v;
     v[0].load(src);
@@ -336,7 +358,7 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   auto load_vec = [&](int64_t c, int which, f32x4 (&f)[2]) {
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
-      f[rt] = *reinterpret_cast<const f32x4*>(vec + c * kGdrVec + 32 * which + 16 * rt + 4 * g4);
+      f[rt] = *reinterpret_cast<const f32x4*>(vec + c * vstride + 32 * which + 16 * rt + 4 * g4);
   };
   auto load_t = [&](int64_t c) {
 #pragma unroll
@@ -374,12 +396,17 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
     load_vec(c0, 0, fk);
     load_t(c0);
     load_vec(c0, 2, fu);
-    dec = vec[c0 * kGdrVec + 96];
+    dec = vec[c0 * vstride + 96];
     if constexpr (kMode == kFull) {
       load_vec(c0, 1, fq);
       load_p(c0);
     }
     put(0);
+#pragma unroll
+    for (int buf = 0; buf < kBuf; ++buf) {
+      tk.clear(Kt[buf], tid);
+      if constexpr (kMode == kFull) tq.clear(Qt[buf], tid);
+    }
     __syncthreads();
   }
   for (int64_t c = c0; c < ce; ++c) {
@@ -388,6 +415,13 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
     const uint16_t* Qb = Qt[kMode == kFull ? buf : 0];
     const int64_t cn = c + 1 < ce ? c + 1 : c;             // the last chunk loads itself again
     load_tiles(cn);
+    if constexpr (kMode == kStates) {
+      if (c % kGdrBlk == 0 && mine) {
+        float* dst = p.blk_S + ((bh * p.n_blks + c / kGdrBlk) * q.P + ch) * q.N;
+#pragma unroll
+        for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+      }
+    }
     {
       // operands of one block of 32 state rows are read while the one before is used
       bf16x8 ka[2][2][kParts], qa[2][2][kParts];
@@ -422,6 +456,13 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
       f32x4 U[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
       gdr_mma_rows<3>(tf, rb, U);
       load_t(cn);
+      if constexpr (kMode == kStates) {
+        if (mine) {
+          float* dst = p.u + (((blk0 + c) * q.P) + ch) * kC + 4 * g4;
+          *reinterpret_cast<f32x4*>(dst) = U[0];
+          *reinterpret_cast<f32x4*>(dst + 16) = U[1];
+        }
+      }
       bf16x8 wb[3];
       gdr_split<3>(fu[0] * U[0], fu[1] * U[1], wb);
       load_vec(cn, 2, fu);
@@ -436,7 +477,7 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
           S[tn] = gdr_mma<3>(kt[0], wb, S[tn]);
         }
       }
-      dec = vec[cn * kGdrVec + 96];
+      dec = vec[cn * vstride + 96];
       if constexpr (kMode == kFull) {
         bf16x8 ub[kOut];
         gdr_split<kOut>(U[0], U[1], ub);
@@ -470,7 +511,7 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
 #pragma unroll
       for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
     }
-  } else if (mine) {
+  } else if (kMode == kSummary && mine) {
     float* dst = ident ? p.seg_M + ((bs * q.H + h) * q.N + ch) * q.N : p.seg_h + ((bs * q.H + h) * q.P + ch) * q.N;
 #pragma unroll
     for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
@@ -537,12 +578,23 @@ __global__ __launch_bounds__(256) void gdr_carry_kernel(GdrChunkParams p) {
   }
 }
 
+template <typename T, typename O, int kN, bool kBwd>
+hipError_t prep_n(const GdrChunkParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((gdr_prep_kernel<T, O, kN, kBwd>), dim3((unsigned)(p.g.B * p.g.G * p.n_chunks)), dim3(256), 0, s,
+                     p);
+  return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t prep_t(const GdrChunkParams& p, bool bwd, hipStream_t s) {
+  if (bwd) return p.g.N > 64 ? prep_n<T, O, 128, true>(p, s) : prep_n<T, O, 64, true>(p, s);
+  return p.g.N > 64 ? prep_n<T, O, 128, false>(p, s) : prep_n<T, O, 64, false>(p, s);
+}
+
 template <typename T, typename O, int kN>
 hipError_t chunk_n(const GdrChunkParams& p, hipStream_t s) {
   const GdrParams& q = p.g;
-  hipLaunchKernelGGL((gdr_prep_kernel<T, kN>), dim3((unsigned)(q.B * q.G * p.n_chunks)), dim3(256), 0, s, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e;
   const int64_t vslices = (q.P + 63) / 64, islices = (q.N + 63) / 64;
   if (p.S > 1) {
     hipLaunchKernelGGL((gdr_chain_kernel<T, O, kN, kSummary>),
@@ -561,9 +613,30 @@ hipError_t chunk_t(const GdrChunkParams& p, hipStream_t s) {
   return p.g.N > 64 ? chunk_n<T, O, 128>(p, s) : chunk_n<T, O, 64>(p, s);
 }
 
+template <typename T>
+hipError_t states_t(const GdrChunkParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.g.B * p.S * p.g.H * ((p.g.P + 63) / 64)));
+  if (p.g.N > 64)
+    hipLaunchKernelGGL((gdr_chain_kernel<T, float, 128, kStates>), grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((gdr_chain_kernel<T, float, 64, kStates>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
+hipError_t launch_gdr_prep(const GdrChunkParams& p, Dt in, Dt grad, bool bwd, hipStream_t s) {
+  if (!bwd || in == grad) return in == Dt::BF16 ? prep_t<uint16_t, uint16_t>(p, bwd, s) : prep_t<float, float>(p, bwd, s);
+  return in == Dt::BF16 ? prep_t<uint16_t, float>(p, bwd, s) : prep_t<float, uint16_t>(p, bwd, s);
+}
+
+hipError_t launch_gdr_states(const GdrChunkParams& p, Dt in, hipStream_t s) {
+  return in == Dt::BF16 ? states_t<uint16_t>(p, s) : states_t<float>(p, s);
+}
+
 hipError_t launch_gdr_chunk(const GdrChunkParams& p, Dt in, Dt out, hipStream_t s) {
+  const hipError_t e = launch_gdr_prep(p, in, in, false, s);
+  if (e != hipSuccess) return e;
   if (in == Dt::BF16) return out == Dt::BF16 ? chunk_t<uint16_t, uint16_t>(p, s) : chunk_t<uint16_t, float>(p, s);
   return out == Dt::BF16 ? chunk_t<float, uint16_t>(p, s) : chunk_t<float, float>(p, s);
 }

@@ -57,6 +57,13 @@ __device__ __forceinline__ void gdr_mma_rows(const bf16x8 (&a)[kR][kA], const bf
       }
 }
 
+// Two fp32 numbers rounded to bf16, as one v_cvt_pk_bf16_f32.
+__device__ __forceinline__ uint32_t gdr_pack(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 // Eight fp32 numbers (the rows of two stacked results) -> kParts bf16 operands.
 template <int kParts>
 __device__ __forceinline__ void gdr_split(f32x4 x, f32x4 y, bf16x8 (&out)[kParts]) {
@@ -64,9 +71,14 @@ __device__ __forceinline__ void gdr_split(f32x4 x, f32x4 y, bf16x8 (&out)[kParts
 #pragma unroll
   for (int s = 0; s < kParts; ++s) {
     uint32_t w[4];
-    if (s == kParts - 1) {           // the last part is rounded (exact for the third)
+    if (s == 2) {                    // what is left has eight bits: the upper halves hold it
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < 4; ++j)
+        w[j] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, v[2 * j + 1]), __builtin_bit_cast(uint32_t, v[2 * j]),
+                                     0x07060302u);
+    } else if (s == kParts - 1) {    // the last of one or two parts is rounded
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = gdr_pack(v[2 * j], v[2 * j + 1]);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -132,10 +144,10 @@ struct GdrRaw16 {
     v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   }
   __device__ __forceinline__ void save(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
-  // into the plane(s) of a tile; zeros where mask is 0 (all ones otherwise)
+  // into the plane(s) of a tile
   template <int kPlaneStride>
-  __device__ __forceinline__ void put(uint16_t* dst, uint32_t mask) const {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(v.x & mask, v.y & mask, v.z & mask, v.w & mask);
+  __device__ __forceinline__ void put(uint16_t* dst) const {
+    *reinterpret_cast<uint4*>(dst) = v;
   }
 };
 
@@ -157,14 +169,11 @@ struct GdrRaw32 {
     *reinterpret_cast<f32x4*>(p + 4) = b;
   }
   template <int kPlaneStride>
-  __device__ __forceinline__ void put(uint16_t* dst, uint32_t mask) const {
+  __device__ __forceinline__ void put(uint16_t* dst) const {
     bf16x8 part[3];
     gdr_split<3>(a, b, part);
 #pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      const uint4 w = __builtin_bit_cast(uint4, part[s]);
-      *reinterpret_cast<uint4*>(dst + s * kPlaneStride) = make_uint4(w.x & mask, w.y & mask, w.z & mask, w.w & mask);
-    }
+    for (int s = 0; s < 3; ++s) *reinterpret_cast<bf16x8*>(dst + s * kPlaneStride) = part[s];
   }
 };
 
@@ -187,12 +196,12 @@ template <> struct GdrIn<uint16_t> { using Raw = GdrRaw16; using Four = GdrFour1
 template <> struct GdrIn<float> { using Raw = GdrRaw32; using Four = GdrFour32; static constexpr int kParts = 3; };
 
 __device__ __forceinline__ void gdr_store_whole4(uint16_t* p, f32x4 x) {
-  *reinterpret_cast<u32x2_u*>(p) = u32x2_u{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+  *reinterpret_cast<u32x2_u*>(p) = u32x2_u{gdr_pack(x[0], x[1]), gdr_pack(x[2], x[3])};
 }
 __device__ __forceinline__ void gdr_store_whole4(float* p, f32x4 x) { *reinterpret_cast<f32x4_u*>(p) = x; }
 __device__ __forceinline__ void gdr_store4(uint16_t* row, int64_t t, int64_t end, f32x4 x) {
   if (t + 4 <= end) {
-    *reinterpret_cast<u32x2_u*>(row + t) = u32x2_u{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    *reinterpret_cast<u32x2_u*>(row + t) = u32x2_u{gdr_pack(x[0], x[1]), gdr_pack(x[2], x[3])};
     return;
   }
 #pragma unroll
@@ -239,12 +248,12 @@ struct GdrTile {
   using Raw = typename GdrIn<T>::Raw;
   int64_t row[kPieces];
   Raw raw[kPieces];
-  uint32_t mask[kPieces];      // zero for rows past N
+  bool ok[kPieces];            // false for rows past N: those are zeroed once (clear) and left alone
   __device__ __forceinline__ void init(int64_t N, int tid) {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
       const int64_t n = (tid >> 2) + 64 * j;
-      mask[j] = n < N ? ~0u : 0u;
+      ok[j] = n < N;
       row[j] = n < N ? n : N - 1;
     }
   }
@@ -261,13 +270,22 @@ struct GdrTile {
   __device__ __forceinline__ void put(uint16_t* tile, int tid) const {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j)
-      raw[j].template put<kPlane>(tile + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3), mask[j]);
+      if (ok[j]) raw[j].template put<kPlane>(tile + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3));
+  }
+  __device__ __forceinline__ void clear(uint16_t* tile, int tid) const {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+      if (!ok[j])
+#pragma unroll
+        for (int s = 0; s < kParts; ++s)
+          *reinterpret_cast<uint4*>(tile + s * kPlane + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3)) =
+              make_uint4(0, 0, 0, 0);
   }
   // as they were loaded, into dense rows of 32
   __device__ __forceinline__ void save(T* rows, int tid) const {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j)
-      if (mask[j]) raw[j].save(rows + row[j] * kGdrChunk + 8 * (tid & 3));
+      if (ok[j]) raw[j].save(rows + row[j] * kGdrChunk + 8 * (tid & 3));
   }
 };
 
@@ -295,6 +313,19 @@ __device__ __forceinline__ void gdr_frags(const uint16_t* tile, int row0, int co
                                           bf16x8 (&f)[GdrIn<T>::kParts]) {
 #pragma unroll
   for (int s = 0; s < GdrIn<T>::kParts; ++s) f[s] = gdr_frag<kGdrRow>(tile + s * kN * kGdrRow, row0, col0, lane);
+}
+
+constexpr int kC = kGdrChunk;
+
+// Block (b, h, c) of the preparation's outputs; kBwd: nine planes, else 3 + p_parts.
+__device__ __forceinline__ int64_t block_of(const GdrChunkParams& p, int64_t b, int64_t h, int64_t c) {
+  return (b * p.g.H + h) * p.n_chunks + c;
+}
+
+// Orders a wave's LDS accesses across its lanes (no other wave is involved).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // Work item of workgroup `id` of `n` so that each of the 8 XCDs (workgroups go

@@ -179,7 +179,9 @@ struct GdrParams {
 // leaves, per (batch row, head, chunk), what does not depend on the state.
 constexpr int kGdrChunk = 32;
 constexpr int kGdrPlane = 1024;                 // bf16 numbers of one 32 x 32 operand plane
-constexpr int kGdrVec = 128;                    // floats of per-token factors per block
+constexpr int kGdrVec = 128;                    // floats of per-token factors per block (forward)
+constexpr int kGdrVecBwd = 256;                 // backward: also 1/|k|, 1/|q| and the cumulated log decays (fp64)
+constexpr int kGdrBlk = 4;                      // chunks between the states that the backward pass keeps
 
 struct GdrChunkParams {
   GdrParams g;
@@ -192,6 +194,19 @@ struct GdrChunkParams {
   float* seg_start;        // (B, S, H, P, N) state entering each segment
   int64_t n_chunks, S, seg_chunks;
   int p_parts;             // planes of the query matrix: 2, or 3 for fp32 outputs
+  // backward pass: planes are 3 of T, 3 of T^T, 3 of the query matrix transposed
+  int vec_stride;          // kGdrVec or kGdrVecBwd
+  const void* dy;          // (B, H P, L) grad dtype
+  const float* dfinal;     // (B, H P, N) or null
+  void* tail_dy;           // (B, H, P, 32) grad dtype
+  float *u, *dvw;          // (B, H, n_chunks, P, 32): updates, gradients of v
+  float *blk_S, *blk_dS;   // (B, H, n_blks, P, N): state entering, gradient leaving each block of kGdrBlk chunks
+  int64_t n_blks;
+  void *dq, *dk, *dv;      // grad dtype, like q, k, v (dense)
+  void *ddelta, *dbeta;    // grad dtype (B, H, L)
+  float *dA, *dbias;       // (H)
+  float* dinit;            // (B, H P, N) or null
+  float* part;             // (B, n_blks, H, 2): sums of dA and dbias over a block
 };
 
 // Rows of state in 8 bits.
@@ -220,6 +235,9 @@ hipError_t launch_conv1d_update(const ConvParams& p, Dt in, Dt out, hipStream_t 
 hipError_t launch_ssd(const SsdParams& p, Dt out, hipStream_t s);
 hipError_t launch_gdr_step(const GdrParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_gdr_chunk(const GdrChunkParams& p, Dt in, Dt out, hipStream_t s);
+hipError_t launch_gdr_prep(const GdrChunkParams& p, Dt in, Dt grad, bool bwd, hipStream_t s);
+hipError_t launch_gdr_states(const GdrChunkParams& p, Dt in, hipStream_t s);
+hipError_t launch_gdr_bwd(const GdrChunkParams& p, Dt in, Dt grad, hipStream_t s);
 hipError_t launch_state_cache(const CacheParams& p, Dt dt, bool write, hipStream_t s);
 
 }  // namespace mamba

@@ -85,6 +85,34 @@ def test_update_rejects_bad_arguments(kw, code):
     assert update(**kw) == code
 
 
+def bwd(**kw):
+    names = ("q", "k", "v", "delta", "beta", "A", "bias", "init", "lengths", "dy", "dfs", "dq", "dk", "dv", "ddelta",
+             "dbeta", "dA", "dbias", "dinit")
+    a = dict.fromkeys(names, P)
+    a.update(bias=None, init=None, lengths=None, dfs=None, dinit=None, B=2, H=4, G=2, Pd=64, N=128, L=256, qs=None,
+             ks=None, vs=None, ind=BF16, outd=BF16, flags=0, ws=P, wsb=1 << 40)
+    a.update(kw)
+    if "y" in kw:                                     # the shared refusals speak of y: here its gradient
+        a["dy"] = kw["y"]
+    qs, vs = a["G"] * a["N"] * a["L"], a["H"] * a["Pd"] * a["L"]
+    return _lib.lib().mamba_gdr_bwd(*[_vp(a[n]) for n in names], a["B"], a["H"], a["G"], a["Pd"], a["N"], a["L"],
+                                    qs if a["qs"] is None else a["qs"], qs if a["ks"] is None else a["ks"],
+                                    vs if a["vs"] is None else a["vs"], 0.5, a["ind"], a["outd"], a["flags"],
+                                    _vp(a["ws"]), a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,code", SHARED + [
+    (dict(L=0), SHAPE), (dict(L=1 << 40, B=1 << 10), SHAPE),
+    (dict(dq=None), NULL), (dict(dk=None), NULL), (dict(dv=None), NULL), (dict(ddelta=None), NULL),
+    (dict(dbeta=None), NULL), (dict(dA=None), NULL), (dict(dbias=None), NULL),
+    (dict(dq=P + 1), ALIGN), (dict(outd=F32, dbeta=P + 2), ALIGN), (dict(dA=P + 2), ALIGN), (dict(dinit=P + 2), ALIGN),
+    (dict(dfs=P + 2), ALIGN), (dict(init=P + 1), ALIGN),
+    (dict(ws=None), WS), (dict(wsb=1 << 20), WS), (dict(ws=P + 16), ALIGN),
+])
+def test_bwd_rejects_bad_arguments(kw, code):
+    assert bwd(**kw) == code
+
+
 def cache(write, **kw):
     a = dict(state=P, slots=None, codes=P, exps=P, rows=2, n=64, S=4, dt=F32)
     a.update(kw)
@@ -136,6 +164,11 @@ def test_workspace_size_plan():
                                             + a(2 * 1 * 40 * 96 * 4) + a(2 * 2 * 40 * 96 * 4))   # 4 chunks: 2 + 2
     with _lib.gdr_test_knobs(kernel="token"):
         assert ws(4, 40, 20, 128, 128, 2048) == 0
+    # backward: 9 planes and 1 KB of factors per chunk, updates and gradients of v (fp32), two states per
+    # block of 4 chunks, two sums per block; one row of 2 heads, one key head, 5 chunks in 2 blocks
+    bw = _lib.lib().mamba_gdr_bwd_workspace_size(1, 2, 1, 40, 96, 130, BF16, F32)
+    assert bw == (a(10 * 9 * 2048) + a(10 * 1024) + 2 * a(96 * 64) + a(2 * 40 * 64) + a(2 * 40 * 128)
+                  + 2 * a(10 * 40 * 128) + 2 * a(4 * 40 * 96 * 4) + a(4 * 8))
 
 
 def test_knob_errors():
