@@ -91,7 +91,8 @@ int mamba_gdr_update(float* state, const int32_t* slots, const void* q, const vo
 /*
  * Bytes of workspace mamba_gdr_bwd needs (sizes only; callable without a GPU),
  * (size_t)-1 for an invalid or unsupported shape.  Per token and value head it holds
- * the updates and the gradient of v in fp32 (8 P bytes), and per 128 tokens two states.
+ * the updates and the gradient of v in fp32 (8 P bytes), and per 32 tokens about one
+ * and a quarter states (5 P N bytes).
  */
 size_t mamba_gdr_bwd_workspace_size(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
                                     mamba_dtype_t in_dtype, mamba_dtype_t grad_dtype);

@@ -109,7 +109,7 @@ GdrPlan make_gdr_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int
 struct GdrBwdPlan {
   int64_t n_chunks = 0, n_blks = 0;
   size_t off_planes = 0, off_vec = 0, off_tk = 0, off_tq = 0, off_tv = 0, off_tdy = 0, off_u = 0, off_dv = 0, off_S = 0,
-         off_dS = 0, off_part = 0, bytes = 0;
+         off_dS = 0, off_aq = 0, off_ak = 0, off_part = 0, bytes = 0;
 };
 
 GdrBwdPlan make_gdr_bwd_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L, size_t e, size_t eg) {
@@ -128,7 +128,11 @@ GdrBwdPlan make_gdr_bwd_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t
   q.off_u = take(blocks * P * C * sizeof(float));
   q.off_dv = take(blocks * P * C * sizeof(float));
   q.off_S = take(heads * q.n_blks * P * N * sizeof(float));
-  q.off_dS = take(heads * q.n_blks * P * N * sizeof(float));
+  q.off_dS = take(blocks * P * N * sizeof(float));
+  if (H > G || P > 64) {     // more than one turn of a key head's sums
+    q.off_aq = take(size_t(B) * G * q.n_chunks * N * C * sizeof(float));
+    q.off_ak = take(size_t(B) * G * q.n_chunks * N * C * sizeof(float));
+  }
   q.off_part = take(heads * q.n_blks * 2 * sizeof(float));
   q.bytes = o;
   return q;
@@ -262,7 +266,9 @@ int mamba_gdr_bwd(const void* q, const void* k, const void* v, const void* delta
   c.u = reinterpret_cast<float*>(ws + plan.off_u);
   c.dvw = reinterpret_cast<float*>(ws + plan.off_dv);
   c.blk_S = reinterpret_cast<float*>(ws + plan.off_S);
-  c.blk_dS = reinterpret_cast<float*>(ws + plan.off_dS);
+  c.chunk_dS = reinterpret_cast<float*>(ws + plan.off_dS);
+  c.acc_dq = reinterpret_cast<float*>(ws + plan.off_aq);
+  c.acc_dk = reinterpret_cast<float*>(ws + plan.off_ak);
   c.n_blks = plan.n_blks;
   c.dq = dq; c.dk = dk; c.dv = dv; c.ddelta = ddelta; c.dbeta = dbeta;
   c.dA = dA; c.dbias = ddelta_bias; c.dinit = dinitial_state;

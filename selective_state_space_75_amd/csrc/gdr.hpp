@@ -11,6 +11,19 @@ __device__ __forceinline__ float gdr_load(const uint16_t* p) { return bf16_to_f3
 __device__ __forceinline__ void gdr_store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void gdr_store(uint16_t* p, float x) { *p = f32_to_bf16(x); }
 
+// Sum over the 16 lanes of a lane group, in every lane (rotations inside the group:
+// four vector adds, no LDS).
+__device__ __forceinline__ float gdr_sum16(float x) {
+#define GDR_ROR(n) \
+  x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + n, 0xf, 0xf, true))
+  GDR_ROR(8);
+  GDR_ROR(4);
+  GDR_ROR(2);
+  GDR_ROR(1);
+#undef GDR_ROR
+  return x;
+}
+
 // Tokens of batch row b that count: all L, or lengths[b] held to 0 .. L.
 __device__ __forceinline__ int64_t gdr_length(const GdrParams& p, int64_t b) {
   if (!p.lengths) return p.L;

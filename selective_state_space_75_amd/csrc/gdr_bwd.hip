@@ -20,9 +20,9 @@
 //
 // Four launches after the preparation (gdr_chunk.hip, which leaves T, T^T, Pm^T):
 //   states  forward along L: U of every chunk, S at every block of 4 chunks;
-//   adjoint backward along L: dV of every chunk, dS at the end of every block;
+//   adjoint backward along L: dV and dS of every chunk;
 //   grads   all blocks at once: the states inside a block are rebuilt forward from S,
-//           the adjoints backward from dS, and everything else is products;
+//           everything else is products;
 //   sums    dA and ddelta_bias from the blocks' partial sums, in a fixed order.
 // The chains are cut over value channels (16 per wave, gdr_chunk.hip); the grads
 // launch is cut over the N numbers of the keys (16 per wave), where dQ and dK are
@@ -32,13 +32,6 @@
 
 namespace mamba {
 namespace {
-
-// Sum over the 16 lanes of a lane group.
-__device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-  for (int m = 1; m < 16; m *= 2) x += __shfl_xor(x, m);
-  return x;
-}
 
 // ----------------------------------------------------------------------------- adjoint chain
 template <typename T, typename O, int kN>
@@ -50,7 +43,7 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
   constexpr int kBuf = kParts == 1 ? 2 : 1;
   __shared__ __align__(16) uint16_t Kt[kBuf][kTile];
   __shared__ __align__(16) uint16_t Qt[kBuf][kTile];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t slices = (q.P + 63) / 64;
   const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
@@ -131,8 +124,8 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
     const uint16_t *K = Kt[buf], *Q = Qt[buf];
     const int64_t cn = c > 0 ? c - 1 : 0;                  // the first chunk loads itself again
     load_tiles(cn);
-    if (mine && (c % kGdrBlk == kGdrBlk - 1 || c == ce - 1)) {
-      float* dst = p.blk_dS + ((bh * p.n_blks + c / kGdrBlk) * q.P + ch) * q.N;
+    if (mine) {
+      float* dst = p.chunk_dS + ((blk0 + c) * q.P + ch) * q.N;
 #pragma unroll
       for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
     }
@@ -196,26 +189,36 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
 }
 
 // ----------------------------------------------------------------------------- the rest, block by block
-// Rows [0, rows) of 32 tokens into operand planes of kRows rows, zeros from row `rows` on.
+// kRows rows of 32 tokens, loaded by the workgroup into registers and put into operand
+// planes later; rows past the last one are zeros.
 template <typename T, int kRows, int kThreads>
-__device__ __forceinline__ void stage_rows(uint16_t* tile, const T* src, int64_t stride, int64_t rows, int tid) {
-  constexpr int kParts = GdrIn<T>::kParts;
+struct Rows {
+  static constexpr int kCount = (kRows * 4 + kThreads - 1) / kThreads;
+  static constexpr bool kSome = kRows * 4 % kThreads != 0;     // fewer pieces than threads
+  typename GdrIn<T>::Raw raw[kCount];
+  __device__ __forceinline__ void load(const T* src, int64_t stride, int64_t rows, int tid) {
 #pragma unroll
-  for (int j = 0; j < (kRows * 4 + kThreads - 1) / kThreads; ++j) {
-    const int id = tid + kThreads * j;
-    if (kRows * 4 % kThreads != 0 && id >= kRows * 4) break;
-    const int64_t n = id >> 2;
-    uint16_t* dst = tile + n * kGdrRow + 8 * (id & 3);
-    if (n < rows) {
-      typename GdrIn<T>::Raw x;
-      x.whole(src + n * stride + 8 * (id & 3));
-      x.template put<kRows * kGdrRow>(dst);
-    } else {
-#pragma unroll
-      for (int s = 0; s < kParts; ++s) *reinterpret_cast<uint4*>(dst + s * kRows * kGdrRow) = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < kCount; ++j) {
+      const int64_t n = (tid + kThreads * j) >> 2;
+      raw[j].whole(src + (n < rows ? n : rows - 1) * stride + 8 * (tid & 3));
     }
   }
-}
+  __device__ __forceinline__ void put(uint16_t* tile, int64_t rows, int tid) const {
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) {
+      const int n = (tid + kThreads * j) >> 2;
+      if (kSome && n >= kRows) continue;
+      uint16_t* dst = tile + n * kGdrRow + 8 * (tid & 3);
+      if (n < rows) {
+        raw[j].template put<kRows * kGdrRow>(dst);
+      } else {
+#pragma unroll
+        for (int s = 0; s < GdrIn<T>::kParts; ++s)
+          *reinterpret_cast<uint4*>(dst + s * kRows * kGdrRow) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+};
 
 template <int kParts, int kRows>
 __device__ __forceinline__ void plane_frags_t(const uint16_t* tile, int row0, int col0, int lane, bf16x8 (&f)[kParts]) {
@@ -241,7 +244,9 @@ __device__ __forceinline__ f32x4 tile_four(const uint16_t* tile, int n, int t) {
 }
 
 // kPS: value channels taken at a time (a slab); every sum over value channels is
-// linear, so slabs and value heads are one loop.
+// linear, so slabs and value heads are one loop of turns.  A turn walks the block's
+// chunks with the state in accumulators (column n of the keys, all value channels of
+// the slab); the next chunk's operands are loaded into registers meanwhile.
 template <typename T, typename O, int kN, int kPS>
 __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   constexpr int kParts = GdrIn<T>::kParts, kGParts = GdrIn<O>::kParts;
@@ -257,8 +262,8 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   __shared__ double cum[32];
   __shared__ __align__(16) float gam[32], en[32], rk[32], rq[32];
   __shared__ __align__(16) float red[2][kW][32];
-  __shared__ float X[kGdrBlk][32], Y[kGdrBlk][32], pr[kGdrBlk][32], dvu[kGdrBlk][32], flow[kW];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  __shared__ float X[kGdrBlk][32], Y[kGdrBlk][32], pr[kGdrBlk][32], dvu[kGdrBlk][32], Z[kGdrBlk], zw[kW];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
   const int64_t blk = it % p.n_blks, bg = it / p.n_blks, g = bg % q.G, b = bg / q.G;
@@ -267,35 +272,71 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   const int nc = (int)(nl - cb < 0 ? 0 : nl - cb < kGdrBlk ? nl - cb : kGdrBlk);      // live chunks
   const int64_t tb = cb * kC, te = tb + kGdrBlk * kC < q.L ? tb + kGdrBlk * kC : q.L;
   const int n = 16 * w + i16;                              // this lane's key number
+  const int64_t nn = n < q.N ? n : q.N - 1;                // one that is there
 
   const T* krows = static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L;
   const T* qrows = static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L;
   const T* tail_k = static_cast<const T*>(p.tail_k) + bg * q.N * kC;
   const T* tail_q = static_cast<const T*>(p.tail_q) + bg * q.N * kC;
+  O* dqrow = static_cast<O*>(p.dq) + (bg * q.N + nn) * q.L;
+  O* dkrow = static_cast<O*>(p.dk) + (bg * q.N + nn) * q.L;
 
-  f32x4 dq[kGdrBlk][2], dk[kGdrBlk][2];                    // column n, tokens 16 rt + 4 g4 ..
-#pragma unroll
-  for (int c = 0; c < kGdrBlk; ++c)
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt) dq[c][rt] = dk[c][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t slabs = (q.P + kPS - 1) / kPS, turns = nc > 0 ? rep * slabs : 0;
+  Rows<T, kN, kThreads> ldk, ldq;
+  Rows<O, kPS, kThreads> ldo;
+  Rows<float, kPS, kThreads> ldv, ldu;
+  f32x4 S[kPT], D[kPT];                                    // S and dS: column n, rows of the value channels
+  auto four = [&](const float* v, int rt) { return *reinterpret_cast<const f32x4*>(v + 16 * rt + 4 * g4); };
 
-  const int64_t slabs = (q.P + kPS - 1) / kPS;
-  for (int64_t hs = 0; hs < (nc > 0 ? rep * slabs : 0); ++hs) {
-    const int64_t h = g * rep + hs / slabs, bh = b * q.H + h, p0 = (hs % slabs) * kPS;
-    const bool first = hs % slabs == 0, last = hs % slabs == slabs - 1;
+  for (int64_t turn = 0; turn < turns; ++turn) {
+    const int64_t h = g * rep + turn / slabs, bh = b * q.H + h, p0 = (turn % slabs) * kPS;
+    const bool first = turn % slabs == 0, last = turn % slabs == slabs - 1;
     const int64_t prow = q.P - p0 < kPS ? q.P - p0 : kPS;  // channels of this slab
-    auto stage = [&](int c) {                              // everything of chunk cb + c
-      const int64_t cc = cb + c, bl = block_of(p, b, h, cc);
+    const int64_t bl0 = block_of(p, b, h, cb);
+    auto load_rows = [&](int c) {
+      const int64_t cc = cb + c, bl = bl0 + c;
       const GdrChunkSrc<T> sk(krows, q.L, tail_k, cc, len), sq(qrows, q.L, tail_q, cc, len);
       const GdrChunkSrc<O> sy(static_cast<const O*>(p.dy) + (bh * q.P + p0) * q.L, q.L,
                               static_cast<const O*>(p.tail_dy) + (bh * q.P + p0) * kC, cc, len);
-      stage_rows<T, kN, kThreads>(Kt, sk.at, sk.stride, q.N, tid);
-      stage_rows<T, kN, kThreads>(Qt, sq.at, sq.stride, q.N, tid);
-      stage_rows<O, kPS, kThreads>(dOt, sy.at, sy.stride, prow, tid);
-      stage_rows<float, kPS, kThreads>(dVt, p.dvw + (bl * q.P + p0) * kC, kC, prow, tid);
-      stage_rows<float, kPS, kThreads>(Ut, p.u + (bl * q.P + p0) * kC, kC, prow, tid);
+      ldk.load(sk.at, sk.stride, q.N, tid);
+      ldq.load(sq.at, sq.stride, q.N, tid);
+      ldo.load(sy.at, sy.stride, prow, tid);
+      ldv.load(p.dvw + (bl * q.P + p0) * kC, kC, prow, tid);
+      ldu.load(p.u + (bl * q.P + p0) * kC, kC, prow, tid);
+    };
+    auto load_state = [&](const float* src, f32x4 (&x)[kPT]) {
+      src += p0 * q.N + nn;
+      const int64_t N = q.N;
+      if (prow == kPS && N == kN) {
+#pragma unroll
+        for (int tp = 0; tp < kPT; ++tp)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[tp][r] = src[(16 * tp + 4 * g4 + r) * kN];
+      } else {
+#pragma unroll
+        for (int tp = 0; tp < kPT; ++tp)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int64_t row = 16 * tp + 4 * g4 + r;
+            const float v = src[(row < prow ? row : 0) * N];
+            x[tp][r] = (row < prow && n < N) ? v : 0.0f;
+          }
+      }
+    };
+    load_rows(0);
+    load_state(p.blk_S + (bh * p.n_blks + blk) * q.P * q.N, S);
+    load_state(p.chunk_dS + bl0 * q.P * q.N, D);
+    for (int c = 0; c < nc; ++c) {
+      const int64_t cc = cb + c;
+      const int cn = c + 1 < nc ? c + 1 : c;
+      __syncthreads();                                     // the chunk before is done with LDS
+      ldk.put(Kt, q.N, tid);
+      ldq.put(Qt, q.N, tid);
+      ldo.put(dOt, prow, tid);
+      ldv.put(dVt, prow, tid);
+      ldu.put(Ut, prow, tid);
       if (tid < 32) {
-        const float* vec = p.vec + bl * p.vec_stride;
+        const float* vec = p.vec + (bl0 + c) * p.vec_stride;
         const double* cu = reinterpret_cast<const double*>(vec + 192);
         const double x = cu[tid];
         cum[tid] = x;
@@ -304,49 +345,16 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         rk[tid] = vec[128 + tid];
         rq[tid] = vec[160 + tid];
       }
-    };
-    auto four = [&](const float* v, int rt) { return *reinterpret_cast<const f32x4*>(v + 16 * rt + 4 * g4); };
-    // sums over a chunk's key numbers: this wave's 16, then all waves by the first 32 threads
-    auto partial = [&](int which, f32x4 a, int rt) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float s = sum16(a[r]);
-        if (i16 == 0) red[which][w][16 * rt + 4 * g4 + r] = s;
-      }
-    };
-    auto collect = [&](int which, float (&to)[32]) {
-      if (tid < 32) {
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kW; ++k) s += red[which][k][tid];
-        to[tid] = first ? s : to[tid] + s;
-      }
-    };
+      load_rows(cn);
+      __syncthreads();
+      const float dec = hw_exp2((float)cum[31]);
 
-    // ---- forward through the block: S
-    f32x4 S[kPT];                                          // column n, rows of the value channels
-    {
-      const float* src = p.blk_S + (bh * p.n_blks + blk) * q.P * q.N;
-#pragma unroll
-      for (int tp = 0; tp < kPT; ++tp)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t row = p0 + 16 * tp + 4 * g4 + r;
-          S[tp][r] = (row < q.P && n < q.N) ? src[row * q.N + n] : 0.0f;
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < kGdrBlk; ++c) {
-      if (c >= nc) break;
-      __syncthreads();
-      stage(c);
-      __syncthreads();
       // 32 x 32 products, lower tiles only: dV U^T, dY U^T, Q K^T, K K^T
       for (int task = w; task < 12; task += kW) {
         const int kind = task / 3, rt = task % 3 > 0, ct = task % 3 > 1;
         f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
         if (kind == 0) {
-#pragma unroll
+#pragma unroll 1
           for (int kb = 0; kb < kPB; ++kb) {
             bf16x8 a[3], u[3];
             plane_frags_t<3, kPS>(dVt, 32 * kb, 16 * rt, lane, a);
@@ -354,7 +362,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
             acc = gdr_mma<3>(a, u, acc);
           }
         } else if (kind == 1) {
-#pragma unroll
+#pragma unroll 1
           for (int kb = 0; kb < kPB; ++kb) {
             bf16x8 a[kGParts], u[3];
             plane_frags_t<kGParts, kPS>(dOt, 32 * kb, 16 * rt, lane, a);
@@ -363,7 +371,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
           }
         } else {
           const uint16_t* rows = kind == 2 ? Qt : Kt;
-#pragma unroll
+#pragma unroll 1
           for (int kb = 0; kb < kN / 32; ++kb) {
             bf16x8 a[kParts], k[kParts];
             gdr_frags_t<T, kN>(rows, 32 * kb, 16 * rt, lane, a);
@@ -376,19 +384,19 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * rt + 4 * g4 + r;
           float x = acc[r];
-          if (kind == 0 && i == j) {                       // dV_t . U_t
-            dvu[c][i] = first ? x : dvu[c][i] + x;
-          }
+          if (kind == 0 && i == j) dvu[c][i] = first ? x : dvu[c][i] + x;     // dV_t . U_t
           if (kind == 0) x = i > j ? x * hw_exp2((float)(cum[i] - cum[j])) : 0.0f;
           if (kind == 1) x = i >= j ? x * q.scale * hw_exp2((float)(cum[i] - cum[j])) : 0.0f;
           m[kind][i * 33 + j] = x;
         }
       }
-      // through the entering state
+      // through the states that enter and leave
       f32x4 Rq[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}, Rk[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+      f32x4 Ru[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+      float z = 0.0f;
 #pragma unroll
       for (int kb = 0; kb < kPB; ++kb) {
-        bf16x8 sb[3], ao[2][kGParts], av[2][3];
+        bf16x8 sb[3], db[3], ao[2][kGParts], av[2][3];
         gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
@@ -397,19 +405,53 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         }
         gdr_mma_rows<3>(ao, sb, Rq);
         gdr_mma_rows<3>(av, sb, Rk);
+        gdr_split<3>(D[2 * kb], D[2 * kb + 1], db);
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * rt, lane, av[rt]);
+        gdr_mma_rows<3>(av, db, Ru);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          z = __builtin_fmaf(S[2 * kb][r], D[2 * kb][r], z);
+          z = __builtin_fmaf(S[2 * kb + 1][r], D[2 * kb + 1][r], z);
+        }
+        __builtin_amdgcn_sched_barrier(0);                 // one block's operands in registers at a time
       }
+      load_state(p.chunk_dS + (bl0 + cn) * q.P * q.N, D);
+      f32x4 aq[2], ak[2];                                  // what the turns before left
+      const int64_t acc_at = ((bg * p.n_chunks + cc) * q.N + nn) * kC + 4 * g4;
+      if (turn > 0) {
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+          aq[rt] = *reinterpret_cast<const f32x4*>(p.acc_dq + acc_at + 16 * rt);
+          ak[rt] = *reinterpret_cast<const f32x4*>(p.acc_dk + acc_at + 16 * rt);
+        }
+      } else {
+        aq[0] = aq[1] = ak[0] = ak[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      z = gdr_sum16(z);
+      z += __shfl_xor(z, 16);
+      z += __shfl_xor(z, 32);
+      if (lane == 0) zw[w] = z;
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) {
-        const f32x4 ga = four(gam, rt);
+        const f32x4 ga = four(gam, rt), kt4 = four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4);
+        const f32x4 qt4 = four(rq, rt) * tile_four<kParts, kN>(Qt, n, 16 * rt + 4 * g4);
         Rq[rt] *= ga * q.scale;
         Rk[rt] *= ga;
-        partial(0, four(rq, rt) * tile_four<kParts, kN>(Qt, n, 16 * rt + 4 * g4) * Rq[rt] -
-                       four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4) * Rk[rt], rt);
-        dq[c][rt] += Rq[rt];
-        dk[c][rt] -= Rk[rt];
+        Ru[rt] *= four(en, rt);
+        const f32x4 xs = qt4 * Rq[rt] - kt4 * Rk[rt], ys = kt4 * Ru[rt];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float a = gdr_sum16(xs[r]), e = gdr_sum16(ys[r]);
+          if (i16 == 0) {
+            red[0][w][16 * rt + 4 * g4 + r] = a;
+            red[1][w][16 * rt + 4 * g4 + r] = e;
+          }
+        }
+        Ru[rt] -= Rk[rt];
       }
       __syncthreads();
-      collect(0, X[c]);
+
       // operands of the products with K and Q, the lengths of the contracted rows folded in;
       // dK takes M2 + M2^T with a minus
       for (int task = w; task < 6; task += kW) {
@@ -430,120 +472,142 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
 #pragma unroll
         for (int s = 0; s < 3; ++s) *reinterpret_cast<bf16x8*>(&mf[kind][s][rt][lane * 8]) = f[s];
       }
-      // pairs across each token: lane j walks its column from the last row up
+      // sums over a chunk's key numbers, and the pairs across each token: lane (half, j) has
+      // rows 16 half .. + 15 of column j and walks them from the last up
       if (w == kW - 1) {
-        const int j = lane & 31;
-        float acc = 0.0f;
-        const float kj = rk[j];
-        for (int t = 31; t >= 0; --t) {
-          if (t > j)
-            acc += kj * (m[1][t * 33 + j] * rq[t] * m[2][t * 33 + j] - m[0][t * 33 + j] * rk[t] * m[3][t * 33 + j]);
-          float s = (lane < 32 && j < t) ? acc : 0.0f;
+        const int j = lane & 31, half = lane >> 5;
+        float s0 = 0.0f;
 #pragma unroll
-          for (int d = 1; d < 32; d *= 2) s += __shfl_xor(s, d);
-          if (lane == 0) pr[c][t] = first ? s : pr[c][t] + s;
+        for (int k = 0; k < kW; ++k) s0 += red[half][k][j];
+        float(&to)[32] = half ? Y[c] : X[c];
+        to[j] = first ? s0 : to[j] + s0;
+        if (lane == 0) {
+          float f = 0.0f;
+#pragma unroll
+          for (int k = 0; k < kW; ++k) f += zw[k];
+          Z[c] = dec * f + (first ? 0.0f : Z[c]);
         }
-      }
-      __syncthreads();
-      // within the chunk
-      {
-        bf16x8 kb_[kParts], qb[kParts];
-        plane_frags<kParts, kN>(Kt, 16 * w, 0, lane, kb_);
-        plane_frags<kParts, kN>(Qt, 16 * w, 0, lane, qb);
-        bf16x8 a[3][2][3];
+        float wv[16], all = 0.0f;
+        const float kj = rk[j];
 #pragma unroll
-        for (int kind = 0; kind < 3; ++kind)
+        for (int t16 = 0; t16 < 16; ++t16) {
+          const int t = 16 * half + t16, at = t * 33 + j;
+          const float v = m[1][at] * rq[t] * m[2][at] - m[0][at] * rk[t] * m[3][at];
+          wv[t16] = t > j ? kj * v : 0.0f;                 // (the upper tile holds nothing)
+          all += wv[t16];
+        }
+        const float above = __shfl_xor(all, 32);
+        float acc = half ? 0.0f : above;
+        wave_sync();                                       // column j of m[3] is this lane pair's from here on
 #pragma unroll
-          for (int rt = 0; rt < 2; ++rt)
+        for (int t16 = 15; t16 >= 0; --t16) {
+          const int t = 16 * half + t16;
+          acc += wv[t16];
+          m[3][t * 33 + j] = j < t ? acc : 0.0f;
+        }
+        wave_sync();
+        float s1 = 0.0f;
 #pragma unroll
-            for (int s = 0; s < 3; ++s) a[kind][rt][s] = *reinterpret_cast<const bf16x8*>(&mf[kind][s][rt][lane * 8]);
-        gdr_mma_rows<3>(a[0], kb_, dq[c]);
-        gdr_mma_rows<3>(a[1], qb, dk[c]);
-        gdr_mma_rows<3>(a[2], kb_, dk[c]);
+        for (int k = 0; k < 16; ++k) s1 += m[3][j * 33 + 16 * half + k];
+        s1 += __shfl_xor(s1, 32);
+        if (half == 0) pr[c][j] = first ? s1 : pr[c][j] + s1;
       }
       // the state after the chunk
       {
-        const float dec = hw_exp2((float)cum[31]);
         bf16x8 kb3[3];
         gdr_split<3>(four(en, 0) * four(rk, 0) * tile_four<kParts, kN>(Kt, n, 4 * g4),
                      four(en, 1) * four(rk, 1) * tile_four<kParts, kN>(Kt, n, 16 + 4 * g4), kb3);
 #pragma unroll
-        for (int tp = 0; tp < kPT; ++tp) {
-          bf16x8 a[3];
-          plane_frags<3, kPS>(Ut, 16 * tp, 0, lane, a);
-          S[tp] = gdr_mma<3>(a, kb3, S[tp] * dec);
+        for (int tp = 0; tp < kPT; tp += 2) {
+          bf16x8 a[2][3];
+          plane_frags<3, kPS>(Ut, 16 * tp, 0, lane, a[0]);
+          plane_frags<3, kPS>(Ut, 16 * tp + 16, 0, lane, a[1]);
+          f32x4 s2[2] = {S[tp] * dec, S[tp + 1] * dec};
+          gdr_mma_rows<3>(a, kb3, s2);
+          S[tp] = s2[0];
+          S[tp + 1] = s2[1];
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-    }
+      __syncthreads();
 
-    // ---- backward through the block: dS; first what passes its end, <dS, S>
-    {
-      const float* src = p.blk_dS + (bh * p.n_blks + blk) * q.P * q.N;
-      float f = 0.0f;
+      // within the chunk
+      {
+        bf16x8 kb_[kParts], qb[kParts], a[2][3];
+        plane_frags<kParts, kN>(Kt, 16 * w, 0, lane, kb_);
+        plane_frags<kParts, kN>(Qt, 16 * w, 0, lane, qb);
+        auto get = [&](int kind) {
 #pragma unroll
-      for (int tp = 0; tp < kPT; ++tp)
+          for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t row = p0 + 16 * tp + 4 * g4 + r;
-          const float x = (row < q.P && n < q.N) ? src[row * q.N + n] : 0.0f;
-          f = __builtin_fmaf(x, S[tp][r], f);
-          S[tp][r] = x;
-        }
-      f = sum16(f);
-      f += __shfl_xor(f, 16);
-      f += __shfl_xor(f, 32);
-      if (lane == 0) flow[w] = first ? f : flow[w] + f;
-    }
-#pragma unroll
-    for (int c = kGdrBlk - 1; c >= 0; --c) {
-      if (c >= nc) continue;
-      __syncthreads();
-      stage(c);
-      __syncthreads();
-      f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
-#pragma unroll
-      for (int kb = 0; kb < kPB; ++kb) {
-        bf16x8 sb[3], au[2][3];
-        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * rt, lane, au[rt]);
-        gdr_mma_rows<3>(au, sb, R);
+            for (int s = 0; s < 3; ++s) a[rt][s] = *reinterpret_cast<const bf16x8*>(&mf[kind][s][rt][lane * 8]);
+        };
+        get(0);
+        gdr_mma_rows<3>(a, kb_, Rq);
+        get(1);
+        gdr_mma_rows<3>(a, qb, Ru);
+        get(2);
+        gdr_mma_rows<3>(a, kb_, Ru);
       }
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) {
-        R[rt] *= four(en, rt);
-        partial(1, four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4) * R[rt], rt);
-        dk[c][rt] += R[rt];
+        aq[rt] += Rq[rt];
+        ak[rt] += Ru[rt];
       }
-      {
-        const float dec = hw_exp2((float)cum[31]);
-        bf16x8 kb3[3], qb3[3];
-        gdr_split<3>(-(four(gam, 0) * four(rk, 0)) * tile_four<kParts, kN>(Kt, n, 4 * g4),
-                     -(four(gam, 1) * four(rk, 1)) * tile_four<kParts, kN>(Kt, n, 16 + 4 * g4), kb3);
-        gdr_split<3>(four(gam, 0) * four(rq, 0) * q.scale * tile_four<kParts, kN>(Qt, n, 4 * g4),
-                     four(gam, 1) * four(rq, 1) * q.scale * tile_four<kParts, kN>(Qt, n, 16 + 4 * g4), qb3);
+      if (turn + 1 < turns) {
+        if (n < q.N) {
 #pragma unroll
-        for (int tp = 0; tp < kPT; ++tp) {
-          bf16x8 a[3], ao[kGParts];
-          plane_frags<3, kPS>(dVt, 16 * tp, 0, lane, a);
-          plane_frags<kGParts, kPS>(dOt, 16 * tp, 0, lane, ao);
-          S[tp] = gdr_mma<3>(a, kb3, S[tp] * dec);
-          S[tp] = gdr_mma<3>(ao, qb3, S[tp]);
+          for (int rt = 0; rt < 2; ++rt) {
+            *reinterpret_cast<f32x4*>(p.acc_dq + acc_at + 16 * rt) = aq[rt];
+            *reinterpret_cast<f32x4*>(p.acc_dk + acc_at + 16 * rt) = ak[rt];
+          }
+        }
+      } else {                                             // all of dQ and dK: through the normalisation, out
+        if (q.norm) {
+          f32x4 kh[2], qh[2];
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt) {
+            kh[rt] = four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4);
+            qh[rt] = four(rq, rt) * tile_four<kParts, kN>(Qt, n, 16 * rt + 4 * g4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float a = gdr_sum16(qh[rt][r] * aq[rt][r]), e = gdr_sum16(kh[rt][r] * ak[rt][r]);
+              if (i16 == 0) {
+                red[0][w][16 * rt + 4 * g4 + r] = a;
+                red[1][w][16 * rt + 4 * g4 + r] = e;
+              }
+            }
+          }
+          __syncthreads();
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt) {
+            f32x4 sq4 = f32x4{0.f, 0.f, 0.f, 0.f}, sk4 = sq4;
+#pragma unroll
+            for (int k = 0; k < kW; ++k) {
+              sq4 += *reinterpret_cast<const f32x4*>(&red[0][k][16 * rt + 4 * g4]);
+              sk4 += *reinterpret_cast<const f32x4*>(&red[1][k][16 * rt + 4 * g4]);
+            }
+            aq[rt] = four(rq, rt) * (aq[rt] - qh[rt] * sq4);
+            ak[rt] = four(rk, rt) * (ak[rt] - kh[rt] * sk4);
+          }
+        }
+        if (n < q.N) {
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt) {
+            gdr_store4(dqrow, cc * kC + 16 * rt + 4 * g4, q.L, aq[rt]);
+            gdr_store4(dkrow, cc * kC + 16 * rt + 4 * g4, q.L, ak[rt]);
+          }
         }
       }
-      __syncthreads();
-      collect(1, Y[c]);
     }
     __syncthreads();
 
     // ---- gates of this head
     if (last && w == 0) {
       const int t = lane & 31;
-      float F = 0.0f, sA = 0.0f, sb = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kW; ++k) F += flow[k];
+      float sA = 0.0f, sb = 0.0f;
       const float A = q.A[h], bias = q.bias ? q.bias[h] : 0.0f;
-      for (int c = nc - 1; c >= 0; --c) {
+      for (int c = 0; c < nc; ++c) {
         const float x = X[c][t], y = Y[c][t];
         float xs = x, ys = y;                              // sums over i >= t and over j <= t
 #pragma unroll
@@ -552,9 +616,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
           if (t + d < 32) xs += o;
           if (t >= d) ys += u;
         }
-        const float Z = F - __shfl(ys, 31, 32);            // what passes the whole chunk
-        const float dg = pr[c][t] + xs + (ys - y) + Z;
-        F = Z + __shfl(xs, 0, 32);                         // what passes the chunk's start
+        const float dg = pr[c][t] + xs + (ys - y) + Z[c];
         const int64_t tok = (cb + c) * kC + t;
         if (lane < 32 && tok < len) {
           const float xr = gdr_load(static_cast<const T*>(q.delta) + bh * q.L + tok) + bias;
@@ -579,7 +641,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
     }
   }
 
-  // gates behind the row's end, and heads of a dead block
+  // tokens behind the row's end: gates and whole chunks of dQ and dK
   for (int64_t hh = 0; hh < rep; ++hh) {
     const int64_t bh = b * q.H + g * rep + hh;
     for (int64_t t = (len > tb ? len : tb) + tid; t < te; t += kThreads) {
@@ -588,57 +650,10 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
     }
     if (nc == 0 && tid < 2) p.part[((b * p.n_blks + blk) * q.H + g * rep + hh) * 2 + tid] = 0.0f;
   }
-
-  // ---- dQ, dK: through the normalisation, rows behind the end as zeros
-  O* dqrow = static_cast<O*>(p.dq) + (bg * q.N + (n < q.N ? n : 0)) * q.L;
-  O* dkrow = static_cast<O*>(p.dk) + (bg * q.N + (n < q.N ? n : 0)) * q.L;
-#pragma unroll
-  for (int c = 0; c < kGdrBlk; ++c) {
-    const int64_t t0 = tb + c * kC;
-    if (t0 >= q.L) break;
-    if (c < nc && q.norm) {
-      const GdrChunkSrc<T> sk(krows, q.L, tail_k, cb + c, len), sq(qrows, q.L, tail_q, cb + c, len);
-      const int64_t row = n < q.N ? n : q.N - 1;
-      const float* vec = p.vec + block_of(p, b, g * rep, cb + c) * p.vec_stride + 4 * g4;
-      f32x4 kh[2], qh[2], fk[2], fq[2];
-      __syncthreads();
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        typename GdrIn<T>::Four x, y;
-        x.load(sk.at + row * sk.stride + 16 * rt + 4 * g4);
-        y.load(sq.at + row * sq.stride + 16 * rt + 4 * g4);
-        fk[rt] = *reinterpret_cast<const f32x4*>(vec + 128 + 16 * rt);
-        fq[rt] = *reinterpret_cast<const f32x4*>(vec + 160 + 16 * rt);
-        kh[rt] = x.get() * fk[rt];
-        qh[rt] = y.get() * fq[rt];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {                      // lanes past N hold zero gradients
-          const float a = sum16(qh[rt][r] * dq[c][rt][r]), e = sum16(kh[rt][r] * dk[c][rt][r]);
-          if (i16 == 0) {
-            red[0][w][16 * rt + 4 * g4 + r] = a;
-            red[1][w][16 * rt + 4 * g4 + r] = e;
-          }
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        f32x4 sq4 = f32x4{0.f, 0.f, 0.f, 0.f}, sk4 = sq4;
-#pragma unroll
-        for (int k = 0; k < kW; ++k) {
-          sq4 += *reinterpret_cast<const f32x4*>(&red[0][k][16 * rt + 4 * g4]);
-          sk4 += *reinterpret_cast<const f32x4*>(&red[1][k][16 * rt + 4 * g4]);
-        }
-        dq[c][rt] = fq[rt] * (dq[c][rt] - qh[rt] * sq4);
-        dk[c][rt] = fk[rt] * (dk[c][rt] - kh[rt] * sk4);
-      }
-    }
-    if (n < q.N) {
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        gdr_store4(dqrow, t0 + 16 * rt + 4 * g4, q.L, dq[c][rt]);
-        gdr_store4(dkrow, t0 + 16 * rt + 4 * g4, q.L, dk[c][rt]);
-      }
+  if (n < q.N) {
+    for (int64_t t = tb + nc * kC + 4 * g4; t < te; t += 16) {
+      gdr_store4(dqrow, t, q.L, f32x4{0.f, 0.f, 0.f, 0.f});
+      gdr_store4(dkrow, t, q.L, f32x4{0.f, 0.f, 0.f, 0.f});
     }
   }
 }

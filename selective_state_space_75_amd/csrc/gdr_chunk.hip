@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
   __shared__ float red[2][8][32];
   __shared__ float rlen[2][32];                            // 1 / |k|, 1 / |q| (1 without normalisation)
   __shared__ double cums[4][32];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
   const int64_t c = it % p.n_chunks, bg = it / p.n_chunks, g = bg % q.G, b = bg / q.G;
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   constexpr int kBuf = kParts == 1 ? 2 : 1;               // fp32 tiles take three planes: one buffer
   __shared__ __align__(16) uint16_t Kt[kBuf][kTile];
   __shared__ __align__(16) uint16_t Qt[kMode == kFull ? kBuf : 1][kMode == kFull ? kTile : 8];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t vslices = (q.P + 63) / 64;
   const int64_t slices = kMode != kSummary ? vslices : vslices + (q.N + 63) / 64;
@@ -526,7 +526,7 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
 __global__ __launch_bounds__(256) void gdr_carry_kernel(GdrChunkParams p) {
   constexpr int kRow = 132;
   __shared__ float A[2][16 * kRow];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t tiles = (q.P + 15) / 16;
   const int64_t bh = blockIdx.x / tiles, b = bh / q.H, h = bh % q.H, p0 = (blockIdx.x % tiles) * 16;

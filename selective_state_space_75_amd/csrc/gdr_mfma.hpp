@@ -13,11 +13,13 @@
 // state -> residual -> update -> state of a chunk never moves between lanes.
 //
 // fp32 operands are split into bf16 parts that are multiplied separately.  Three
-// parts by truncation hold an fp32 number exactly (8 + 8 + 8 bits), so products of
-// parts i and j with i + j < 3 leave out only terms below 2^-24 of the largest:
-// fp32 accuracy at three products for a bf16 operand (exact in one part) times an
-// fp32 one and six for two fp32 ones, on units 16 times as fast as the fp32 MFMA.
-// Results that are rounded to bf16 at once take two parts (2^-16).
+// parts hold an fp32 number exactly (8 bits each), so products of parts i and j with
+// i + j < 3 leave out only terms below 2^-25 of the largest: fp32 accuracy at three
+// products for a bf16 operand (exact in one part) times an fp32 one and six for two
+// fp32 ones, on units 16 times as fast as the fp32 MFMA.  Each part is rounded to
+// nearest, so that the left-out terms have either sign (truncated parts all have
+// the number's sign: every product came out 2^-24 too small, and sums over tokens
+// kept that).  Results that are rounded to bf16 at once take two parts (2^-17).
 #pragma once
 
 #include "gdr.hpp"
@@ -71,21 +73,12 @@ __device__ __forceinline__ void gdr_split(f32x4 x, f32x4 y, bf16x8 (&out)[kParts
 #pragma unroll
   for (int s = 0; s < kParts; ++s) {
     uint32_t w[4];
-    if (s == 2) {                    // what is left has eight bits: the upper halves hold it
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, v[2 * j + 1]), __builtin_bit_cast(uint32_t, v[2 * j]),
-                                     0x07060302u);
-    } else if (s == kParts - 1) {    // the last of one or two parts is rounded
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = gdr_pack(v[2 * j], v[2 * j + 1]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a = __builtin_bit_cast(uint32_t, v[2 * j]), b = __builtin_bit_cast(uint32_t, v[2 * j + 1]);
-        w[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);          // both upper halves
-        v[2 * j] -= __builtin_bit_cast(float, a & 0xffff0000u);
-        v[2 * j + 1] -= __builtin_bit_cast(float, b & 0xffff0000u);
+    for (int j = 0; j < 4; ++j) {
+      w[j] = gdr_pack(v[2 * j], v[2 * j + 1]);
+      if (s + 1 < kParts) {
+        v[2 * j] -= bf16_lo(w[j]);
+        v[2 * j + 1] -= bf16_hi(w[j]);
       }
     }
     out[s] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));

@@ -19,13 +19,6 @@
 namespace mamba {
 namespace {
 
-// Sum over the 16 lanes that share a row; every lane gets the sum.
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-  for (int m = 1; m < 16; m *= 2) x += __shfl_xor(x, m);
-  return x;
-}
-
 // kVec: N % 4 == 0 and the states 16-byte aligned.
 template <typename T, typename O, int kE, bool kVec, int kSets>
 __global__ __launch_bounds__(256) void gdr_step_kernel(GdrParams p) {
@@ -88,10 +81,10 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrParams p) {
     }
     float rk = 1.0f, rq = p.scale;
     if (p.norm) {
-      rk = gdr_rnorm(row_sum(kk));
-      rq *= gdr_rnorm(row_sum(qq));
+      rk = gdr_rnorm(gdr_sum16(kk));
+      rq *= gdr_rnorm(gdr_sum16(qq));
     }
-    kq = row_sum(kq) * rk * rq;
+    kq = gdr_sum16(kq) * rk * rq;
 #pragma unroll
     for (int s = 0; s < kSets; ++s) {
       float sk = 0.0f, sq = 0.0f;
@@ -100,8 +93,8 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrParams p) {
         sk = __builtin_fmaf(S[s][e], kv[e], sk);
         sq = __builtin_fmaf(S[s][e], qv[e], sq);
       }
-      sk = row_sum(sk);
-      sq = row_sum(sq);
+      sk = gdr_sum16(sk);
+      sq = gdr_sum16(sq);
       const float u = bt * (vv[s] - a * rk * sk);
       const float w = u * rk;
 #pragma unroll
