@@ -125,13 +125,14 @@ GdrBwdPlan make_gdr_bwd_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t
   q.off_tq = take(size_t(B) * G * N * C * e);
   q.off_tv = take(heads * P * C * e);
   q.off_tdy = take(heads * P * C * eg);
-  q.off_u = take(blocks * P * C * sizeof(float));
-  q.off_dv = take(blocks * P * C * sizeof(float));
-  q.off_S = take(heads * q.n_blks * P * N * sizeof(float));
-  q.off_dS = take(blocks * P * N * sizeof(float));
+  const size_t Pp = (P + 63) / 64 * 64, Np = (N + 63) / 64 * 64;
+  q.off_u = take(blocks * Pp * C * sizeof(float));
+  q.off_dv = take(blocks * Pp * C * sizeof(float));
+  q.off_S = take(heads * q.n_blks * Pp * Np * sizeof(float));
+  q.off_dS = take(blocks * Pp * Np * sizeof(float));
   if (H > G || P > 64) {     // more than one turn of a key head's sums
-    q.off_aq = take(size_t(B) * G * q.n_chunks * N * C * sizeof(float));
-    q.off_ak = take(size_t(B) * G * q.n_chunks * N * C * sizeof(float));
+    q.off_aq = take(size_t(B) * G * q.n_chunks * Np * C * sizeof(float));
+    q.off_ak = take(size_t(B) * G * q.n_chunks * Np * C * sizeof(float));
   }
   q.off_part = take(heads * q.n_blks * 2 * sizeof(float));
   q.bytes = o;

@@ -61,8 +61,8 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
   const O* dyrow = static_cast<const O*>(p.dy) + (bh * q.P + vch) * q.L + 4 * g4;
   const O* tail_dy = static_cast<const O*>(p.tail_dy) + (bh * q.P + vch) * kC + 4 * g4;
   O* dvrow = static_cast<O*>(p.dv) + (bh * q.P + vch) * q.L;
-  const int64_t blk0 = block_of(p, b, h, 0);
-  const uint16_t* planes = p.planes + blk0 * 9 * kGdrPlane + lane * 8;
+  const int64_t blk0 = block_of(p, b, h, 0), Pp = slices * 64;
+  const uint16_t* planes = p.planes + blk0 * 9 * kGdrPlane;
   const float* vec = p.vec + blk0 * p.vec_stride;
 
   f32x4 S[kNT];                                  // dS: column ch, rows of the key numbers
@@ -93,17 +93,17 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
     dy[0].load(src);
     dy[1].load(src + 16);
     const uint16_t* pl = planes + c * 9 * kGdrPlane;
-    const float* vc = vec + c * p.vec_stride + 4 * g4;
+    const float* vc = vec + c * p.vec_stride;
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
 #pragma unroll
       for (int s = 0; s < 3; ++s) {
-        tf[rt][s] = *reinterpret_cast<const bf16x8*>(pl + (3 + s) * kGdrPlane + rt * 512);
-        pf[rt][s] = *reinterpret_cast<const bf16x8*>(pl + (6 + s) * kGdrPlane + rt * 512);
+        tf[rt][s] = lane_load<bf16x8>(pl + (3 + s) * kGdrPlane + rt * 512, lane * 16);
+        pf[rt][s] = lane_load<bf16x8>(pl + (6 + s) * kGdrPlane + rt * 512, lane * 16);
       }
-      fk[rt] = *reinterpret_cast<const f32x4*>(vc + 16 * rt);
-      fq[rt] = *reinterpret_cast<const f32x4*>(vc + 32 + 16 * rt);
-      fu[rt] = *reinterpret_cast<const f32x4*>(vc + 64 + 16 * rt);
+      fk[rt] = lane_load<f32x4>(vc + 16 * rt, g4 * 16);
+      fq[rt] = lane_load<f32x4>(vc + 32 + 16 * rt, g4 * 16);
+      fu[rt] = lane_load<f32x4>(vc + 64 + 16 * rt, g4 * 16);
     }
     dec = vec[c * p.vec_stride + 96];
   };
@@ -124,10 +124,11 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
     const uint16_t *K = Kt[buf], *Q = Qt[buf];
     const int64_t cn = c > 0 ? c - 1 : 0;                  // the first chunk loads itself again
     load_tiles(cn);
-    if (mine) {
-      float* dst = p.chunk_dS + ((blk0 + c) * q.P + ch) * q.N;
+    {
+      float* dst = p.chunk_dS + ((blk0 + c) * Pp + ch) * kN;
 #pragma unroll
-      for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+      for (int tn = 0; tn < kNT; ++tn)
+        *reinterpret_cast<f32x4*>(dst + 16 * tn + 4 * g4) = mine ? S[tn] : f32x4{0.f, 0.f, 0.f, 0.f};
     }
     // right-hand side E K dS^T + Pm^T dY
     f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
@@ -168,13 +169,11 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
       S[tn] = gdr_mma<3>(aq, wq, S[tn] * dc);
       S[tn] = gdr_mma<3>(a, wk, S[tn]);
     }
-    if (mine) {
-      float* dst = p.dvw + ((blk0 + c) * q.P + ch) * kC + 4 * g4;
+    float* wdst = p.dvw + ((blk0 + c) * Pp + ch) * kC + 4 * g4;
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        *reinterpret_cast<f32x4*>(dst + 16 * rt) = W[rt];
-        gdr_store4(dvrow, c * kC + 16 * rt + 4 * g4, q.L, W[rt]);
-      }
+    for (int rt = 0; rt < 2; ++rt) {
+      *reinterpret_cast<f32x4*>(wdst + 16 * rt) = mine ? W[rt] : f32x4{0.f, 0.f, 0.f, 0.f};
+      if (mine) gdr_store4(dvrow, c * kC + 16 * rt + 4 * g4, q.L, W[rt]);
     }
     if constexpr (kBuf == 1) __syncthreads();
     tk.put(Kt[kBuf == 2 ? buf ^ 1 : 0], tid);
@@ -203,19 +202,22 @@ struct Rows {
       raw[j].whole(src + (n < rows ? n : rows - 1) * stride + 8 * (tid & 3));
     }
   }
-  __device__ __forceinline__ void put(uint16_t* tile, int64_t rows, int tid) const {
+  // all kRows rows, one after the other
+  __device__ __forceinline__ void load_dense(const T* src, int tid) {
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) {
+      const int id = tid + kThreads * j;
+      raw[j].whole(reinterpret_cast<const T*>(reinterpret_cast<const char*>(src) +
+                                              (uint32_t)(kSome && id >= kRows * 4 ? 0 : id) * 8u * sizeof(T)));
+    }
+  }
+  __device__ __forceinline__ void put(uint16_t* tile, int rows, int tid) const {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
       const int n = (tid + kThreads * j) >> 2;
       if (kSome && n >= kRows) continue;
       uint16_t* dst = tile + n * kGdrRow + 8 * (tid & 3);
-      if (n < rows) {
-        raw[j].template put<kRows * kGdrRow>(dst);
-      } else {
-#pragma unroll
-        for (int s = 0; s < GdrIn<T>::kParts; ++s)
-          *reinterpret_cast<uint4*>(dst + s * kRows * kGdrRow) = make_uint4(0, 0, 0, 0);
-      }
+      raw[j].template put<kRows * kGdrRow>(dst, rows == kRows || n < rows ? ~0u : 0u);
     }
   }
 };
@@ -243,6 +245,11 @@ __device__ __forceinline__ f32x4 tile_four(const uint16_t* tile, int n, int t) {
   return r;
 }
 
+// No branch that only some lanes of a wave take inside the loop: every lane writes (the
+// same value where one would do), addresses are clamped.  At such a branch's end the
+// compiler may save registers before it re-enables the other lanes when it runs
+// out of them.
+//
 // kPS: value channels taken at a time (a slab); every sum over value channels is
 // linear, so slabs and value heads are one loop of turns.  A turn walks the block's
 // chunks with the state in accumulators (column n of the keys, all value channels of
@@ -262,7 +269,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   __shared__ double cum[32];
   __shared__ __align__(16) float gam[32], en[32], rk[32], rq[32];
   __shared__ __align__(16) float red[2][kW][32];
-  __shared__ float X[kGdrBlk][32], Y[kGdrBlk][32], pr[kGdrBlk][32], dvu[kGdrBlk][32], Z[kGdrBlk], zw[kW];
+  __shared__ float X[kGdrBlk][32], Y[kGdrBlk][32], pr[kGdrBlk][32], dvu[kGdrBlk + 1][32], Z[kGdrBlk], zw[kW];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
@@ -281,6 +288,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   O* dqrow = static_cast<O*>(p.dq) + (bg * q.N + nn) * q.L;
   O* dkrow = static_cast<O*>(p.dk) + (bg * q.N + nn) * q.L;
 
+  const int64_t Pp = (q.P + 63) / 64 * 64;
   const int64_t slabs = (q.P + kPS - 1) / kPS, turns = nc > 0 ? rep * slabs : 0;
   Rows<T, kN, kThreads> ldk, ldq;
   Rows<O, kPS, kThreads> ldo;
@@ -291,7 +299,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   for (int64_t turn = 0; turn < turns; ++turn) {
     const int64_t h = g * rep + turn / slabs, bh = b * q.H + h, p0 = (turn % slabs) * kPS;
     const bool first = turn % slabs == 0, last = turn % slabs == slabs - 1;
-    const int64_t prow = q.P - p0 < kPS ? q.P - p0 : kPS;  // channels of this slab
+    const int prow = (int)(q.P - p0 < kPS ? q.P - p0 : kPS);  // channels of this slab
     const int64_t bl0 = block_of(p, b, h, cb);
     auto load_rows = [&](int c) {
       const int64_t cc = cb + c, bl = bl0 + c;
@@ -301,51 +309,39 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       ldk.load(sk.at, sk.stride, q.N, tid);
       ldq.load(sq.at, sq.stride, q.N, tid);
       ldo.load(sy.at, sy.stride, prow, tid);
-      ldv.load(p.dvw + (bl * q.P + p0) * kC, kC, prow, tid);
-      ldu.load(p.u + (bl * q.P + p0) * kC, kC, prow, tid);
+      ldv.load_dense(p.dvw + (bl * Pp + p0) * kC, tid);
+      ldu.load_dense(p.u + (bl * Pp + p0) * kC, tid);
     };
+    const uint32_t soff = (uint32_t)(4 * g4 * kN + n) * 4u;
     auto load_state = [&](const float* src, f32x4 (&x)[kPT]) {
-      src += p0 * q.N + nn;
-      const int64_t N = q.N;
-      if (prow == kPS && N == kN) {
 #pragma unroll
-        for (int tp = 0; tp < kPT; ++tp)
+      for (int tp = 0; tp < kPT; ++tp)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) x[tp][r] = src[(16 * tp + 4 * g4 + r) * kN];
-      } else {
-#pragma unroll
-        for (int tp = 0; tp < kPT; ++tp)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int64_t row = 16 * tp + 4 * g4 + r;
-            const float v = src[(row < prow ? row : 0) * N];
-            x[tp][r] = (row < prow && n < N) ? v : 0.0f;
-          }
-      }
+        for (int r = 0; r < 4; ++r) x[tp][r] = lane_load<float>(src + (16 * tp + r) * kN, soff);
     };
     load_rows(0);
-    load_state(p.blk_S + (bh * p.n_blks + blk) * q.P * q.N, S);
-    load_state(p.chunk_dS + bl0 * q.P * q.N, D);
+    load_state(p.blk_S + ((bh * p.n_blks + blk) * Pp + p0) * kN, S);
+    load_state(p.chunk_dS + (bl0 * Pp + p0) * kN, D);
     for (int c = 0; c < nc; ++c) {
       const int64_t cc = cb + c;
       const int cn = c + 1 < nc ? c + 1 : c;
       __syncthreads();                                     // the chunk before is done with LDS
-      ldk.put(Kt, q.N, tid);
-      ldq.put(Qt, q.N, tid);
+      ldk.put(Kt, (int)q.N, tid);
+      ldq.put(Qt, (int)q.N, tid);
       ldo.put(dOt, prow, tid);
-      ldv.put(dVt, prow, tid);
-      ldu.put(Ut, prow, tid);
-      if (tid < 32) {
+      ldv.put(dVt, kPS, tid);
+      ldu.put(Ut, kPS, tid);
+      if (w == 0) {
         const float* vec = p.vec + (bl0 + c) * p.vec_stride;
         const double* cu = reinterpret_cast<const double*>(vec + 192);
-        const double x = cu[tid];
-        cum[tid] = x;
-        gam[tid] = hw_exp2((float)x);
-        en[tid] = hw_exp2((float)(cu[31] - x));
-        rk[tid] = vec[128 + tid];
-        rq[tid] = vec[160 + tid];
+        const int t = lane & 31;
+        const double x = cu[t];
+        cum[t] = x;
+        gam[t] = hw_exp2((float)x);
+        en[t] = hw_exp2((float)(cu[31] - x));
+        rk[t] = vec[128 + t];
+        rq[t] = vec[160 + t];
       }
-      load_rows(cn);
       __syncthreads();
       const float dec = hw_exp2((float)cum[31]);
 
@@ -384,9 +380,12 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * rt + 4 * g4 + r;
           float x = acc[r];
-          if (kind == 0 && i == j) dvu[c][i] = first ? x : dvu[c][i] + x;     // dV_t . U_t
-          if (kind == 0) x = i > j ? x * hw_exp2((float)(cum[i] - cum[j])) : 0.0f;
-          if (kind == 1) x = i >= j ? x * q.scale * hw_exp2((float)(cum[i] - cum[j])) : 0.0f;
+          // diagonal of the first: dV_t . U_t (the other lanes write to a row of their own)
+          float* diag = &dvu[kind == 0 && i == j ? c : kGdrBlk][kind == 0 && i == j ? i : lane & 31];
+          *diag = first ? x : *diag + x;
+          const float dij = kind < 2 ? hw_exp2((float)(cum[i] - cum[j])) : 1.0f;
+          if (kind == 0) x = i > j ? x * dij : 0.0f;
+          if (kind == 1) x = i >= j ? x * q.scale * dij : 0.0f;
           m[kind][i * 33 + j] = x;
         }
       }
@@ -416,22 +415,10 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         }
         __builtin_amdgcn_sched_barrier(0);                 // one block's operands in registers at a time
       }
-      load_state(p.chunk_dS + (bl0 + cn) * q.P * q.N, D);
-      f32x4 aq[2], ak[2];                                  // what the turns before left
-      const int64_t acc_at = ((bg * p.n_chunks + cc) * q.N + nn) * kC + 4 * g4;
-      if (turn > 0) {
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-          aq[rt] = *reinterpret_cast<const f32x4*>(p.acc_dq + acc_at + 16 * rt);
-          ak[rt] = *reinterpret_cast<const f32x4*>(p.acc_dk + acc_at + 16 * rt);
-        }
-      } else {
-        aq[0] = aq[1] = ak[0] = ak[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
       z = gdr_sum16(z);
       z += __shfl_xor(z, 16);
       z += __shfl_xor(z, 32);
-      if (lane == 0) zw[w] = z;
+      zw[w] = z;
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) {
         const f32x4 ga = four(gam, rt), kt4 = four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4);
@@ -442,15 +429,26 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         const f32x4 xs = qt4 * Rq[rt] - kt4 * Rk[rt], ys = kt4 * Ru[rt];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float a = gdr_sum16(xs[r]), e = gdr_sum16(ys[r]);
-          if (i16 == 0) {
-            red[0][w][16 * rt + 4 * g4 + r] = a;
-            red[1][w][16 * rt + 4 * g4 + r] = e;
-          }
+          red[0][w][16 * rt + 4 * g4 + r] = gdr_sum16(xs[r]);
+          red[1][w][16 * rt + 4 * g4 + r] = gdr_sum16(ys[r]);
         }
         Ru[rt] -= Rk[rt];
       }
       __syncthreads();
+      // for the next chunk, and what the turns before left of this one
+      load_rows(cn);
+      load_state(p.chunk_dS + ((bl0 + cn) * Pp + p0) * kN, D);
+      f32x4 aq[2], ak[2];
+      const int64_t acc_at = ((bg * p.n_chunks + cc) * kN + n) * kC + 4 * g4;
+      if (turn > 0) {
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+          aq[rt] = *reinterpret_cast<const f32x4*>(p.acc_dq + acc_at + 16 * rt);
+          ak[rt] = *reinterpret_cast<const f32x4*>(p.acc_dk + acc_at + 16 * rt);
+        }
+      } else {
+        aq[0] = aq[1] = ak[0] = ak[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
 
       // operands of the products with K and Q, the lengths of the contracted rows folded in;
       // dK takes M2 + M2^T with a minus
@@ -481,12 +479,10 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         for (int k = 0; k < kW; ++k) s0 += red[half][k][j];
         float(&to)[32] = half ? Y[c] : X[c];
         to[j] = first ? s0 : to[j] + s0;
-        if (lane == 0) {
-          float f = 0.0f;
+        float f = 0.0f;
 #pragma unroll
-          for (int k = 0; k < kW; ++k) f += zw[k];
-          Z[c] = dec * f + (first ? 0.0f : Z[c]);
-        }
+        for (int k = 0; k < kW; ++k) f += zw[k];
+        Z[c] = dec * f + (first ? 0.0f : Z[c]);
         float wv[16], all = 0.0f;
         const float kj = rk[j];
 #pragma unroll
@@ -510,7 +506,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) s1 += m[3][j * 33 + 16 * half + k];
         s1 += __shfl_xor(s1, 32);
-        if (half == 0) pr[c][j] = first ? s1 : pr[c][j] + s1;
+        pr[c][j] = first ? s1 : pr[c][j] + s1;
       }
       // the state after the chunk
       {
@@ -555,7 +551,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         ak[rt] += Ru[rt];
       }
       if (turn + 1 < turns) {
-        if (n < q.N) {
+        {
 #pragma unroll
           for (int rt = 0; rt < 2; ++rt) {
             *reinterpret_cast<f32x4*>(p.acc_dq + acc_at + 16 * rt) = aq[rt];
@@ -571,11 +567,8 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
             qh[rt] = four(rq, rt) * tile_four<kParts, kN>(Qt, n, 16 * rt + 4 * g4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float a = gdr_sum16(qh[rt][r] * aq[rt][r]), e = gdr_sum16(kh[rt][r] * ak[rt][r]);
-              if (i16 == 0) {
-                red[0][w][16 * rt + 4 * g4 + r] = a;
-                red[1][w][16 * rt + 4 * g4 + r] = e;
-              }
+              red[0][w][16 * rt + 4 * g4 + r] = gdr_sum16(qh[rt][r] * aq[rt][r]);
+              red[1][w][16 * rt + 4 * g4 + r] = gdr_sum16(kh[rt][r] * ak[rt][r]);
             }
           }
           __syncthreads();
@@ -684,9 +677,10 @@ hipError_t bwd_n(const GdrChunkParams& p, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)(q.B * q.G * p.n_blks));
-  // 128 channels at a time where the operands have one plane each (LDS)
+  // 128 channels at a time where the operands have one plane each (LDS) and the padded
+  // channels come in pairs of 64
   constexpr bool kOne = GdrIn<T>::kParts == 1 && GdrIn<O>::kParts == 1;
-  if (kOne && q.P > 64)
+  if (kOne && (q.P + 63) / 64 % 2 == 0)
     hipLaunchKernelGGL((gdr_grad_kernel<T, O, kN, kOne ? 128 : 64>), grid, dim3(kN * 4), 0, s, p);
   else
     hipLaunchKernelGGL((gdr_grad_kernel<T, O, kN, 64>), grid, dim3(kN * 4), 0, s, p);

@@ -320,6 +320,8 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   const T* tail_v = static_cast<const T*>(p.tail_v) + (bh * q.P + vch) * kC + 4 * g4;
   O* yrow = static_cast<O*>(q.y) + (bh * q.P + (mine && !ident ? ch : 0)) * q.L;
   const bool values = mine && !ident;
+  const int64_t Pp = vslices * 64;
+  (void)Pp;
 
   f32x4 S[kNT];
   {
@@ -348,7 +350,7 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   float dec = 0.0f;
   const int64_t blk0 = block_of(p, b, h, 0);
   const int64_t pstride = (int64_t)(kMode == kStates ? 9 : 3 + p.p_parts) * kGdrPlane, vstride = p.vec_stride;
-  const uint16_t* planes = p.planes + blk0 * pstride + lane * 8;
+  const uint16_t* planes = p.planes + blk0 * pstride;
   const float* vec = p.vec + blk0 * vstride;
   auto load_v = [&](int64_t c) {
     const T* src = (c + 1) * kC <= len ? vrow + c * kC : tail_v;
@@ -358,21 +360,21 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   auto load_vec = [&](int64_t c, int which, f32x4 (&f)[2]) {
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
-      f[rt] = *reinterpret_cast<const f32x4*>(vec + c * vstride + 32 * which + 16 * rt + 4 * g4);
+      f[rt] = lane_load<f32x4>(vec + c * vstride + 32 * which + 16 * rt, g4 * 16);
   };
   auto load_t = [&](int64_t c) {
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
       for (int s = 0; s < 3; ++s)
-        tf[rt][s] = *reinterpret_cast<const bf16x8*>(planes + c * pstride + s * kGdrPlane + rt * 512);
+        tf[rt][s] = lane_load<bf16x8>(planes + c * pstride + s * kGdrPlane + rt * 512, lane * 16);
   };
   auto load_p = [&](int64_t c) {
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
       for (int s = 0; s < kOut; ++s)
-        pf[rt][s] = *reinterpret_cast<const bf16x8*>(planes + c * pstride + (3 + s) * kGdrPlane + rt * 512);
+        pf[rt][s] = lane_load<bf16x8>(planes + c * pstride + (3 + s) * kGdrPlane + rt * 512, lane * 16);
   };
   GdrTile<T, kN> tk, tq;
   tk.init(q.N, tid);
@@ -409,6 +411,9 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
     }
     __syncthreads();
   }
+  bf16x8 sb[kNB][3];                                       // the state's operand parts
+#pragma unroll
+  for (int kb = 0; kb < kNB; ++kb) gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb[kb]);
   for (int64_t c = c0; c < ce; ++c) {
     const int buf = kBuf == 2 ? (int)((c - c0) & 1) : 0;
     const uint16_t* K = Kt[buf];
@@ -416,74 +421,116 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
     const int64_t cn = c + 1 < ce ? c + 1 : c;             // the last chunk loads itself again
     load_tiles(cn);
     if constexpr (kMode == kStates) {
-      if (c % kGdrBlk == 0 && mine) {
-        float* dst = p.blk_S + ((bh * p.n_blks + c / kGdrBlk) * q.P + ch) * q.N;
+      if (c % kGdrBlk == 0) {
+        float* dst = p.blk_S + ((bh * p.n_blks + c / kGdrBlk) * Pp + ch) * kN;
 #pragma unroll
-        for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+        for (int tn = 0; tn < kNT; ++tn)
+          *reinterpret_cast<f32x4*>(dst + 16 * tn + 4 * g4) = mine ? S[tn] : f32x4{0.f, 0.f, 0.f, 0.f};
       }
     }
     {
-      // operands of one block of 32 state rows are read while the one before is used
-      bf16x8 ka[2][2][kParts], qa[2][2][kParts];
-      auto load_a = [&](int kb) {
+      // K S0 (and Q S0), the state already split: operands of one block of 32 state rows are
+      // read while the one before is used
+      constexpr int kA = kParts == 1 ? kNB : 1;              // bf16: all blocks' operands at once
+      bf16x8 ka[kA][2][kParts], qa[kMode == kFull ? kA : 1][2][kParts];
+      auto load_k = [&](int kb) {
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-          gdr_frags_t<T, kN>(K, 32 * kb, 16 * rt, lane, ka[kb & 1][rt]);
-          if constexpr (kMode == kFull) gdr_frags_t<T, kN>(Qb, 32 * kb, 16 * rt, lane, qa[kb & 1][rt]);
-        }
+        for (int rt = 0; rt < 2; ++rt) gdr_frags_t<T, kN>(K, 32 * kb, 16 * rt, lane, ka[kb % kA][rt]);
+      };
+      auto load_q = [&](int kb) {
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) gdr_frags_t<T, kN>(Qb, 32 * kb, 16 * rt, lane, qa[kb % kA][rt]);
       };
       f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}, Y[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
-      load_a(0);
+#pragma unroll
+      for (int kb = 0; kb < kA; ++kb) load_k(kb);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int kb = 0; kb < kNB; ++kb) {
-        if (kb + 1 < kNB) load_a(kb + 1);
-        bf16x8 sb[3];
-        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
-        gdr_mma_rows<3>(ka[kb & 1], sb, R);
-        if constexpr (kMode == kFull) gdr_mma_rows<kOut>(qa[kb & 1], sb, Y);
+        gdr_mma_rows<3>(ka[kb % kA], sb[kb], R);
+        if (kb + kA < kNB) load_k(kb + kA);
+        if constexpr (kMode == kFull) {
+          if (kb + kA >= kNB) load_q(kb + kA - kNB);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
-      bf16x8 kt[kParts == 1 ? kNT : 1][kParts];            // bf16: all tiles of the update's operand at once
-      if constexpr (kParts == 1) {
-#pragma unroll
-        for (int tn = 0; tn < kNT; ++tn) gdr_frags<T, kN>(K, 16 * tn, 0, lane, kt[tn]);
-      }
       bf16x8 rb[3];
-      if (ident) gdr_split<3>(-fk[0] * R[0], -fk[1] * R[1], rb);
-      else gdr_split<3>(v[0].get() - fk[0] * R[0], v[1].get() - fk[1] * R[1], rb);
+      const f32x4 v0 = ident ? f32x4{0.f, 0.f, 0.f, 0.f} : v[0].get(), v1 = ident ? f32x4{0.f, 0.f, 0.f, 0.f} : v[1].get();
+      gdr_split<3>(v0 - fk[0] * R[0], v1 - fk[1] * R[1], rb);
+      if constexpr (kMode == kFull) {
+#pragma unroll
+        for (int kb = 0; kb < kNB; ++kb) {
+          gdr_mma_rows<kOut>(qa[kb % kA], sb[kb], Y);
+          if (kb + kA < kNB) load_q(kb + kA);
+        }
+        // one product, then what the vector unit can do of the residual meanwhile
+#pragma unroll
+        for (int i = 0; i < 4 * kNB; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+        }
+        pin(rb);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       load_v(cn);
       load_vec(cn, 0, fk);
       f32x4 U[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
       gdr_mma_rows<3>(tf, rb, U);
+#pragma unroll
+      for (int tn = 0; tn < kNT; ++tn) S[tn] *= dec;
+#pragma unroll
+      for (int i = 0; i < 12; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
       load_t(cn);
       if constexpr (kMode == kStates) {
-        if (mine) {
-          float* dst = p.u + (((blk0 + c) * q.P) + ch) * kC + 4 * g4;
-          *reinterpret_cast<f32x4*>(dst) = U[0];
-          *reinterpret_cast<f32x4*>(dst + 16) = U[1];
-        }
+        float* dst = p.u + ((blk0 + c) * Pp + ch) * kC + 4 * g4;
+        *reinterpret_cast<f32x4*>(dst) = mine ? U[0] : f32x4{0.f, 0.f, 0.f, 0.f};
+        *reinterpret_cast<f32x4*>(dst + 16) = mine ? U[1] : f32x4{0.f, 0.f, 0.f, 0.f};
       }
+      constexpr int kT = kParts == 1 ? kNB : 1;
+      bf16x8 kt[kT][2][kParts];
+      auto load_kt = [&](int t2) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) gdr_frags<T, kN>(K, 16 * (2 * t2 + j), 0, lane, kt[t2 % kT][j]);
+      };
+#pragma unroll
+      for (int t2 = 0; t2 < kT; ++t2) load_kt(t2);
+      __builtin_amdgcn_sched_barrier(0);
       bf16x8 wb[3];
       gdr_split<3>(fu[0] * U[0], fu[1] * U[1], wb);
       load_vec(cn, 2, fu);
-#pragma unroll
-      for (int tn = 0; tn < kNT; ++tn) S[tn] *= dec;
-      if constexpr (kParts == 1) {
-        gdr_mma_rows<3>(kt, wb, S);
-      } else {
-#pragma unroll
-        for (int tn = 0; tn < kNT; ++tn) {
-          gdr_frags<T, kN>(K, 16 * tn, 0, lane, kt[0]);
-          S[tn] = gdr_mma<3>(kt[0], wb, S[tn]);
-        }
-      }
       dec = vec[cn * vstride + 96];
+      __builtin_amdgcn_sched_barrier(0);
+      // the state two tiles at a time; the tiles before are split meanwhile
+#pragma unroll
+      for (int t2 = 0; t2 < kNB; ++t2) {
+        f32x4 s2[2] = {S[2 * t2], S[2 * t2 + 1]};
+        gdr_mma_rows<3>(kt[t2 % kT], wb, s2);
+        if (t2 + kT < kNB) load_kt(t2 + kT);
+        S[2 * t2] = s2[0];
+        S[2 * t2 + 1] = s2[1];
+        if (t2 > 0) gdr_split<3>(S[2 * t2 - 2], S[2 * t2 - 1], sb[t2 - 1]);
+      }
       if constexpr (kMode == kFull) {
         bf16x8 ub[kOut];
         gdr_split<kOut>(U[0], U[1], ub);
         Y[0] *= fq[0];
         Y[1] *= fq[1];
         gdr_mma_rows<kOut>(pf, ub, Y);
+      }
+      gdr_split<3>(S[kNT - 2], S[kNT - 1], sb[kNB - 1]);
+#pragma unroll
+      for (int i = 0; i < 6 * kNB + (kMode == kFull ? 6 : 0); ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 7, 0);
+      }
+#pragma unroll
+      for (int kb = 0; kb < kNB; ++kb) pin(sb[kb]);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (kMode == kFull) {
         load_vec(cn, 1, fq);
         load_p(cn);
         if (values) {
@@ -551,16 +598,22 @@ __global__ __launch_bounds__(256) void gdr_carry_kernel(GdrChunkParams p) {
       const int n = 16 * (w + 4 * t2) + i16;
       if (16 * (w + 4 * t2) >= N) continue;
       f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-      f32x4 hs = acc;
+      // no branches around live registers: clamped addresses and selects
+      f32x4 hs;
+      const int nc = n < N ? n : N - 1;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (n < N && p0 + 4 * g4 + r < q.P) hs[r] = p.seg_h[(sm * q.P + p0 + 4 * g4 + r) * N + n];
+      for (int r = 0; r < 4; ++r) {
+        const int64_t row = p0 + 4 * g4 + r;
+        const float x = p.seg_h[(sm * q.P + (row < q.P ? row : q.P - 1)) * N + nc];
+        hs[r] = n < N && row < q.P ? x : 0.0f;
+      }
       for (int k0 = 0; k0 < N; k0 += 32) {
         float m[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int k = k0 + 4 * j + g4;
-          m[j] = (k < N && n < N) ? M[(int64_t)k * N + n] : 0.0f;
+          const float x = M[(int64_t)(k < N ? k : N - 1) * N + nc];
+          m[j] = k < N && n < N ? x : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)

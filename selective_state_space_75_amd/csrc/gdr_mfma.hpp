@@ -85,10 +85,18 @@ __device__ __forceinline__ void gdr_split(f32x4 x, f32x4 y, bf16x8 (&out)[kParts
   }
 }
 
-// Operand tiles in LDS: rows of 32 tokens (or of other bf16 numbers), 40 apart.
-// 80 bytes put the 16 rows that a ds_read_b64 pair of one lane group touches on
-// different banks.
-constexpr int kGdrRow = 40;
+// Keeps the computation of operands where it stands (the compiler moves it past the
+// products it should overlap with otherwise).
+template <int kParts>
+__device__ __forceinline__ void pin(bf16x8 (&x)[kParts]) {
+#pragma unroll
+  for (int s = 0; s < kParts; ++s) asm volatile("" : "+v"(x[s]));
+}
+
+// Operand tiles in LDS: rows of 32 tokens, 36 apart.  72 bytes (18 banks) spread
+// both reads of a lane group over the banks: 16 rows at one token (gdr_frag), and
+// 4 rows at 16 tokens (gdr_frag_t).
+constexpr int kGdrRow = 36;
 
 // A or B operand whose row (column) index runs along the stored row: lane i takes
 // column col0 + i of rows row0 + 4 g .. + 3 and row0 + 16 + 4 g .. + 3.  The
@@ -121,6 +129,12 @@ typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 
+// 16 bytes into a tile row (8-byte aligned)
+__device__ __forceinline__ void gdr_put16(uint16_t* dst, uint4 v) {
+  reinterpret_cast<uint2*>(dst)[0] = make_uint2(v.x, v.y);
+  reinterpret_cast<uint2*>(dst)[1] = make_uint2(v.z, v.w);
+}
+
 // Eight consecutive numbers of a row from token t: all of them (whole), or zeros from
 // token `end` on.  The two are separate calls so that whole chunks load without
 // branches: a load in a divergent branch is waited for where the branch ends.
@@ -137,10 +151,10 @@ struct GdrRaw16 {
     v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   }
   __device__ __forceinline__ void save(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
-  // into the plane(s) of a tile
+  // into the plane(s) of a tile, as zeros where mask is 0 (else all ones)
   template <int kPlaneStride>
-  __device__ __forceinline__ void put(uint16_t* dst) const {
-    *reinterpret_cast<uint4*>(dst) = v;
+  __device__ __forceinline__ void put(uint16_t* dst, uint32_t mask = ~0u) const {
+    gdr_put16(dst, make_uint4(v.x & mask, v.y & mask, v.z & mask, v.w & mask));
   }
 };
 
@@ -162,14 +176,24 @@ struct GdrRaw32 {
     *reinterpret_cast<f32x4*>(p + 4) = b;
   }
   template <int kPlaneStride>
-  __device__ __forceinline__ void put(uint16_t* dst) const {
+  __device__ __forceinline__ void put(uint16_t* dst, uint32_t mask = ~0u) const {
     bf16x8 part[3];
     gdr_split<3>(a, b, part);
 #pragma unroll
-    for (int s = 0; s < 3; ++s) *reinterpret_cast<bf16x8*>(dst + s * kPlaneStride) = part[s];
+    for (int s = 0; s < 3; ++s) {
+      const uint4 w = __builtin_bit_cast(uint4, part[s]);
+      gdr_put16(dst + s * kPlaneStride, make_uint4(w.x & mask, w.y & mask, w.z & mask, w.w & mask));
+    }
   }
 };
 
+
+// A vector at a byte offset of this lane from a base that all lanes share (scalar base
+// plus 32-bit offset: no 64-bit address arithmetic per lane).
+template <typename V, typename T>
+__device__ __forceinline__ V lane_load(const T* base, uint32_t off) {
+  return *reinterpret_cast<const V*>(reinterpret_cast<const char*>(base) + off);
+}
 
 // Four consecutive numbers of a row, kept as they are stored until they are used (a
 // conversion would be waited for at the load).
@@ -271,8 +295,7 @@ struct GdrTile {
       if (!ok[j])
 #pragma unroll
         for (int s = 0; s < kParts; ++s)
-          *reinterpret_cast<uint4*>(tile + s * kPlane + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3)) =
-              make_uint4(0, 0, 0, 0);
+          gdr_put16(tile + s * kPlane + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3), make_uint4(0, 0, 0, 0));
   }
   // as they were loaded, into dense rows of 32
   __device__ __forceinline__ void save(T* rows, int tid) const {

@@ -199,10 +199,11 @@ struct GdrChunkParams {
   const void* dy;          // (B, H P, L) grad dtype
   const float* dfinal;     // (B, H P, N) or null
   void* tail_dy;           // (B, H, P, 32) grad dtype
-  float *u, *dvw;          // (B, H, n_chunks, P, 32): updates, gradients of v
-  float* blk_S;            // (B, H, n_blks, P, N): state entering each block of kGdrBlk chunks
-  float* chunk_dS;         // (B, H, n_chunks, P, N): gradient of the state leaving each chunk
-  float *acc_dq, *acc_dk;  // (B, G, n_chunks, N, 32): sums over value heads (more than one, or P > a slab)
+  // with Pp = P and Np = N rounded up to 64 (Np: 64 or 128), zeros in between
+  float *u, *dvw;          // (B, H, n_chunks, Pp, 32): updates, gradients of v
+  float* blk_S;            // (B, H, n_blks, Pp, Np): state entering each block of kGdrBlk chunks
+  float* chunk_dS;         // (B, H, n_chunks, Pp, Np): gradient of the state leaving each chunk
+  float *acc_dq, *acc_dk;  // (B, G, n_chunks, Np, 32): sums over value heads (more than one, or P > a slab)
   int64_t n_blks;
   void *dq, *dk, *dv;      // grad dtype, like q, k, v (dense)
   void *ddelta, *dbeta;    // grad dtype (B, H, L)

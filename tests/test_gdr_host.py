@@ -165,11 +165,11 @@ def test_workspace_size_plan():
     with _lib.gdr_test_knobs(kernel="token"):
         assert ws(4, 40, 20, 128, 128, 2048) == 0
     # backward: 9 planes and 1 KB of factors per chunk, updates and gradients of v (fp32), a state per block
-    # of 4 chunks and per chunk, sums of dq and dk over value heads, two sums per block; one row of 2 heads,
-    # one key head, 5 chunks in 2 blocks
+    # of 4 chunks and per chunk, sums of dq and dk over value heads (P and N rounded up to 64), two sums per
+    # block; one row of 2 heads, one key head, 5 chunks in 2 blocks
     bw = _lib.lib().mamba_gdr_bwd_workspace_size(1, 2, 1, 40, 96, 130, BF16, F32)
     assert bw == (a(10 * 9 * 2048) + a(10 * 1024) + 2 * a(96 * 64) + a(2 * 40 * 64) + a(2 * 40 * 128)
-                  + 2 * a(10 * 40 * 128) + a(4 * 40 * 96 * 4) + a(10 * 40 * 96 * 4) + 2 * a(5 * 96 * 128) + a(4 * 8))
+                  + 2 * a(10 * 64 * 128) + a(4 * 64 * 128 * 4) + a(10 * 64 * 128 * 4) + 2 * a(5 * 128 * 128) + a(4 * 8))
 
 
 def test_knob_errors():
