@@ -293,6 +293,8 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   Rows<T, kN, kThreads> ldk, ldq;
   Rows<O, kPS, kThreads> ldo;
   Rows<float, kPS, kThreads> ldv, ldu;
+  double lcum, llast;                                      // the next chunk's cumulated decay and lengths
+  float lrk, lrq;
   f32x4 S[kPT], D[kPT];                                    // S and dS: column n, rows of the value channels
   auto four = [&](const float* v, int rt) { return *reinterpret_cast<const f32x4*>(v + 16 * rt + 4 * g4); };
 
@@ -306,6 +308,11 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       const GdrChunkSrc<T> sk(krows, q.L, tail_k, cc, len), sq(qrows, q.L, tail_q, cc, len);
       const GdrChunkSrc<O> sy(static_cast<const O*>(p.dy) + (bh * q.P + p0) * q.L, q.L,
                               static_cast<const O*>(p.tail_dy) + (bh * q.P + p0) * kC, cc, len);
+      const float* vec = p.vec + bl * p.vec_stride;
+      lrk = lane_load<float>(vec + 128, (lane & 31) * 4);
+      lrq = lane_load<float>(vec + 160, (lane & 31) * 4);
+      lcum = lane_load<double>(vec + 192, (lane & 31) * 8);
+      llast = *reinterpret_cast<const double*>(vec + 192 + 62);
       ldk.load(sk.at, sk.stride, q.N, tid);
       ldq.load(sq.at, sq.stride, q.N, tid);
       ldo.load(sy.at, sy.stride, prow, tid);
@@ -332,15 +339,12 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       ldv.put(dVt, kPS, tid);
       ldu.put(Ut, kPS, tid);
       if (w == 0) {
-        const float* vec = p.vec + (bl0 + c) * p.vec_stride;
-        const double* cu = reinterpret_cast<const double*>(vec + 192);
         const int t = lane & 31;
-        const double x = cu[t];
-        cum[t] = x;
-        gam[t] = hw_exp2((float)x);
-        en[t] = hw_exp2((float)(cu[31] - x));
-        rk[t] = vec[128 + t];
-        rq[t] = vec[160 + t];
+        cum[t] = lcum;
+        gam[t] = hw_exp2((float)lcum);
+        en[t] = hw_exp2((float)(llast - lcum));
+        rk[t] = lrk;
+        rq[t] = lrq;
       }
       __syncthreads();
       const float dec = hw_exp2((float)cum[31]);
@@ -435,9 +439,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         Ru[rt] -= Rk[rt];
       }
       __syncthreads();
-      // for the next chunk, and what the turns before left of this one
-      load_rows(cn);
-      load_state(p.chunk_dS + ((bl0 + cn) * Pp + p0) * kN, D);
+      // what the turns before left of this chunk, and the next one
       f32x4 aq[2], ak[2];
       const int64_t acc_at = ((bg * p.n_chunks + cc) * kN + n) * kC + 4 * g4;
       if (turn > 0) {
@@ -450,20 +452,29 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         aq[0] = aq[1] = ak[0] = ak[1] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
 
+      load_rows(cn);
+      load_state(p.chunk_dS + ((bl0 + cn) * Pp + p0) * kN, D);
       // operands of the products with K and Q, the lengths of the contracted rows folded in;
       // dK takes M2 + M2^T with a minus
       for (int task = w; task < 6; task += kW) {
         const int kind = task >> 1, rt = task & 1, row = 16 * rt + i16;
+        // (read first, chosen afterwards: what the upper tile holds is dropped)
+        const float* mk = m[kind == 2 ? 0 : 1];
+        const f32x4* lens = reinterpret_cast<const f32x4*>(kind == 1 ? rq : rk);
+        const f32x4 l0 = lens[g4], l1 = lens[4 + g4];
         f32x4 x[2];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int col = (e < 4 ? 0 : 16) + 4 * g4 + (e & 3);
           const int hi = row > col ? row : col, lo = row > col ? col : row;
-          float v;
-          if (kind == 0) v = row >= col ? m[1][row * 33 + col] * rk[col] : 0.0f;
-          else if (kind == 1) v = col >= row ? m[1][col * 33 + row] * rq[col] : 0.0f;
-          else v = hi > lo ? -m[0][hi * 33 + lo] * rk[col] : 0.0f;
-          x[e >> 2][e & 3] = v;
+          x[e >> 2][e & 3] = mk[hi * 33 + lo] * (e < 4 ? l0 : l1)[e & 3];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int col = (e < 4 ? 0 : 16) + 4 * g4 + (e & 3);
+          const bool in = kind == 0 ? row >= col : kind == 1 ? col >= row : row != col;
+          const float v = x[e >> 2][e & 3];
+          x[e >> 2][e & 3] = in ? (kind == 2 ? -v : v) : 0.0f;
         }
         bf16x8 f[3];
         gdr_split<3>(x[0], x[1], f);
