@@ -247,7 +247,7 @@ int mamba_gdr_bwd(const void* q, const void* k, const void* v, const void* delta
                           (const void*)dinitial_state})
     if (ptr && !aligned(ptr, 4)) return MAMBA_ERR_ALIGN;
   const GdrBwdPlan plan = make_gdr_bwd_plan(B, H, G, P, N, L, width(in_dtype), width(grad_dtype));
-  if (B * G >= kMaxGrid / plan.n_chunks || B * H >= kMaxGrid / ((P + 63) / 64) || H >= kMaxGrid) return MAMBA_ERR_SHAPE;
+  if (B * H >= kMaxGrid / plan.n_chunks || B * H >= kMaxGrid / ((P + 63) / 64)) return MAMBA_ERR_SHAPE;
   if (!workspace || workspace_bytes < plan.bytes) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
   mamba::GdrChunkParams c{};

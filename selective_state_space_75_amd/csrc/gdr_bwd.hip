@@ -18,9 +18,11 @@
 // the tokens' own terms again, which are larger than what is left: it loses an order
 // of magnitude in fp32 and the sums over tokens lose more.)
 //
-// Four launches after the preparation (gdr_chunk.hip, which leaves T, T^T, Pm^T):
+// Five launches after the preparation (gdr_chunk.hip, which leaves T, T^T, Pm^T):
 //   states  forward along L: U of every chunk, S at every block of 4 chunks;
 //   adjoint backward along L: dV and dS of every chunk;
+//   pairs   all chunks at once: M1 and M2 as operands (over T's planes, which are not
+//           needed any more), and what of dg and dbeta follows from them alone;
 //   grads   all blocks at once: the states inside a block are rebuilt forward from S,
 //           everything else is products;
 //   sums    dA and ddelta_bias from the blocks' partial sums, in a fixed order.
@@ -245,11 +247,189 @@ __device__ __forceinline__ f32x4 tile_four(const uint16_t* tile, int n, int t) {
   return r;
 }
 
-// No branch that only some lanes of a wave take inside the loop: every lane writes (the
-// same value where one would do), addresses are clamped.  At such a branch's end the
-// compiler may save registers before it re-enables the other lanes when it runs
-// out of them.
-//
+// In both kernels below no branch that only some lanes of a wave take encloses or follows
+// live registers: every lane writes (the same value where one would do), addresses are
+// clamped.  At such a branch's end the compiler may save registers before it
+// re-enables the other lanes when it runs out of them.
+
+// One workgroup per (batch row, value head, chunk): the 32 x 32 products dV U^T, dY U^T
+// (64 value channels at a time), K K^T and Q K^T, lower tiles only.  Leaves M1 (columns
+// times 1/|k|), M1^T (times 1/|q|) and -(M2 + M2^T) (times 1/|k|) as operand planes of
+// the products with K and Q, and per token the pairs' part of dg and dV_t . U_t.
+template <typename T, typename O, int kN>
+__global__ __launch_bounds__(256) void gdr_pair_kernel(GdrChunkParams p) {
+  constexpr int kParts = GdrIn<T>::kParts, kGParts = GdrIn<O>::kParts, kPS = 64;
+  __shared__ __align__(16) uint16_t dOt[kGParts * kPS * kGdrRow];
+  __shared__ __align__(16) uint16_t dVt[3 * kPS * kGdrRow];
+  __shared__ __align__(16) uint16_t Ut[3 * kPS * kGdrRow];
+  __shared__ __align__(16) uint16_t Kt[kParts * kN * kGdrRow];
+  __shared__ __align__(16) uint16_t Qt[kParts * kN * kGdrRow];
+  __shared__ float m[4][32 * 33];                          // M2, M1, Q K^T, K K^T
+  __shared__ double cum[32];
+  __shared__ __align__(16) float rk[32], rq[32], dvu[33];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15,
+            g4 = lane >> 4;
+  const GdrParams& q = p.g;
+  const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
+  const int64_t c = it % p.n_chunks, bh = it / p.n_chunks, b = bh / q.H, h = bh % q.H, g = h / (q.H / q.G);
+  const int64_t len = gdr_length(q, b), bg = b * q.G + g;
+  if (c * kC >= len) return;
+  const int64_t bl = block_of(p, b, h, c), Pp = (q.P + 63) / 64 * 64;
+  float* vec = p.vec + bl * p.vec_stride;
+  const GdrChunkSrc<T> sk(static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L, q.L,
+                          static_cast<const T*>(p.tail_k) + bg * q.N * kC, c, len);
+  const GdrChunkSrc<T> sq(static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L, q.L,
+                          static_cast<const T*>(p.tail_q) + bg * q.N * kC, c, len);
+  const GdrChunkSrc<O> sy(static_cast<const O*>(p.dy) + bh * q.P * q.L, q.L,
+                          static_cast<const O*>(p.tail_dy) + bh * q.P * kC, c, len);
+  Rows<O, kPS, 256> ldo;
+  Rows<float, kPS, 256> ldv, ldu;
+  auto load = [&](int64_t p0) {
+    ldo.load(sy.at + p0 * sy.stride, sy.stride, q.P - p0 < kPS ? q.P - p0 : kPS, tid);
+    ldv.load_dense(p.dvw + (bl * Pp + p0) * kC, tid);
+    ldu.load_dense(p.u + (bl * Pp + p0) * kC, tid);
+  };
+  {
+    Rows<T, kN, 256> ldk, ldq;
+    ldk.load(sk.at, sk.stride, q.N, tid);
+    ldq.load(sq.at, sq.stride, q.N, tid);
+    const double lcum = lane_load<double>(vec + 192, (lane & 31) * 8);
+    const float lrk = lane_load<float>(vec + 128, (lane & 31) * 4), lrq = lane_load<float>(vec + 160, (lane & 31) * 4);
+    load(0);
+    ldk.put(Kt, (int)q.N, tid);
+    ldq.put(Qt, (int)q.N, tid);
+    if (w == 0) {
+      cum[lane & 31] = lcum;
+      rk[lane & 31] = lrk;
+      rq[lane & 31] = lrq;
+    }
+  }
+  // tile t of the lower triangle: rows 16 (t > 0), columns 16 (t > 1)
+  f32x4 acc[3];                                            // waves 0 to 2: tile w of dV U^T; wave 3: dY U^T
+#pragma unroll
+  for (int t = 0; t < 3; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int64_t p0 = 0; p0 < q.P; p0 += kPS) {
+    const int rows = (int)(q.P - p0 < kPS ? q.P - p0 : kPS);
+    if (p0 > 0) __syncthreads();
+    ldo.put(dOt, rows, tid);
+    ldv.put(dVt, kPS, tid);
+    ldu.put(Ut, kPS, tid);
+    if (p0 + kPS < q.P) load(p0 + kPS);
+    __syncthreads();
+    if (w < 3) {
+      const int rt = w > 0, ct = w > 1;
+#pragma unroll
+      for (int kb = 0; kb < kPS / 32; ++kb) {
+        bf16x8 a[3], u[3];
+        plane_frags_t<3, kPS>(dVt, 32 * kb, 16 * rt, lane, a);
+        plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * ct, lane, u);
+        acc[0] = gdr_mma<3>(a, u, acc[0]);
+      }
+    } else {
+#pragma unroll
+      for (int kb = 0; kb < kPS / 32; ++kb) {
+        bf16x8 a[2][kGParts], u[2][3];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          plane_frags_t<kGParts, kPS>(dOt, 32 * kb, 16 * t, lane, a[t]);
+          plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * t, lane, u[t]);
+        }
+        acc[0] = gdr_mma<3>(a[0], u[0], acc[0]);
+        acc[1] = gdr_mma<3>(a[1], u[0], acc[1]);
+        acc[2] = gdr_mma<3>(a[1], u[1], acc[2]);
+      }
+    }
+  }
+  auto put = [&](int kind, int t, f32x4 v) {
+    const int j = (t > 1 ? 16 : 0) + i16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = (t > 0 ? 16 : 0) + 4 * g4 + r;
+      float x = v[r];
+      if (kind == 0) dvu[i == j ? i : 32] = x;             // dV_t . U_t (32: dropped)
+      if (kind < 2) {
+        const float d = hw_exp2((float)(cum[i] - cum[j]));
+        x = (kind == 0 ? i > j : i >= j) ? x * d * (kind == 0 ? 1.0f : q.scale) : 0.0f;
+      }
+      m[kind][i * 33 + j] = x;
+    }
+  };
+  if (w < 3) {
+    put(0, w, acc[0]);
+#pragma unroll
+    for (int kind = 2; kind < 4; ++kind) {
+      const uint16_t* rows = kind == 2 ? Qt : Kt;
+      const int rt = w > 0, ct = w > 1;
+      f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < kN / 32; ++kb) {
+        bf16x8 a[kParts], k[kParts];
+        gdr_frags_t<T, kN>(rows, 32 * kb, 16 * rt, lane, a);
+        gdr_frags_t<T, kN>(Kt, 32 * kb, 16 * ct, lane, k);
+        x = gdr_mma<3>(a, k, x);
+      }
+      put(kind, w, x);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 3; ++t) put(1, t, acc[t]);
+  }
+  __syncthreads();
+  if (w < 3) {
+    // operands (kind w), the lengths of the contracted rows folded in; read first, chosen
+    // afterwards (what the upper tile holds is dropped)
+    const float* mk = m[w == 2 ? 0 : 1];
+    const f32x4* lens = reinterpret_cast<const f32x4*>(w == 1 ? rq : rk);
+    const f32x4 l0 = lens[g4], l1 = lens[4 + g4];
+    uint16_t* planes = p.planes + (bl * 9 + 3 * w) * kGdrPlane;
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+      const int row = 16 * rt + i16;
+      f32x4 x[2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int col = (e < 4 ? 0 : 16) + 4 * g4 + (e & 3);
+        const int hi = row > col ? row : col, lo = row > col ? col : row;
+        const float v = mk[hi * 33 + lo] * (e < 4 ? l0 : l1)[e & 3];
+        const bool in = w == 0 ? row >= col : w == 1 ? col >= row : row != col;
+        x[e >> 2][e & 3] = in ? (w == 2 ? -v : v) : 0.0f;
+      }
+      bf16x8 f[3];
+      gdr_split<3>(x[0], x[1], f);
+#pragma unroll
+      for (int s = 0; s < 3; ++s) *reinterpret_cast<bf16x8*>(planes + s * kGdrPlane + rt * 512 + lane * 8) = f[s];
+    }
+  } else {
+    // the pairs across each token: lane (half, j) has rows 16 half .. + 15 of column j and
+    // walks them from the last up
+    const int j = lane & 31, half = lane >> 5;
+    float wv[16], all = 0.0f;
+    const float kj = rk[j];
+#pragma unroll
+    for (int t16 = 0; t16 < 16; ++t16) {
+      const int t = 16 * half + t16, at = t * 33 + j;
+      const float v = m[1][at] * rq[t] * m[2][at] - m[0][at] * rk[t] * m[3][at];
+      wv[t16] = t > j ? kj * v : 0.0f;                     // (the upper tile holds nothing)
+      all += wv[t16];
+    }
+    const float above = __shfl_xor(all, 32);
+    float s0 = half ? 0.0f : above;
+    wave_sync();                                           // m[3] is this wave's from here on
+#pragma unroll
+    for (int t16 = 15; t16 >= 0; --t16) {
+      const int t = 16 * half + t16;
+      s0 += wv[t16];
+      m[3][t * 33 + j] = j < t ? s0 : 0.0f;
+    }
+    wave_sync();
+    float s1 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s1 += m[3][j * 33 + 16 * half + k];
+    s1 += __shfl_xor(s1, 32);
+    vec[lane] = half ? dvu[j] : s1;                        // over the factors of k and q
+  }
+}
+
 // kPS: value channels taken at a time (a slab); every sum over value channels is
 // linear, so slabs and value heads are one loop of turns.  A turn walks the block's
 // chunks with the state in accumulators (column n of the keys, all value channels of
@@ -259,18 +439,19 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   constexpr int kParts = GdrIn<T>::kParts, kGParts = GdrIn<O>::kParts;
   constexpr int kW = kN / 16, kThreads = 64 * kW;
   constexpr int kPT = kPS / 16, kPB = kPS / 32;
+  constexpr int kMf = (9 * kGdrPlane / 8 + kThreads - 1) / kThreads;      // 16-byte pieces of the planes per thread
   __shared__ __align__(16) uint16_t dOt[kGParts * kPS * kGdrRow];
   __shared__ __align__(16) uint16_t dVt[3 * kPS * kGdrRow];
   __shared__ __align__(16) uint16_t Ut[3 * kPS * kGdrRow];
   __shared__ __align__(16) uint16_t Kt[kParts * kN * kGdrRow];
   __shared__ __align__(16) uint16_t Qt[kParts * kN * kGdrRow];
-  __shared__ __align__(16) uint16_t mf[3][3][2][512];     // operands made of M1, M1^T and M2 + M2^T
-  __shared__ float m[4][32 * 33];                          // M2, M1, Q K^T, K K^T
+  __shared__ __align__(16) uint16_t mf[kMf * kThreads * 8];               // operands made of M1, M1^T and M2 + M2^T
   __shared__ double cum[32];
   __shared__ __align__(16) float gam[32], en[32], rk[32], rq[32];
   __shared__ __align__(16) float red[2][kW][32];
-  __shared__ float X[kGdrBlk][32], Y[kGdrBlk][32], pr[kGdrBlk][32], dvu[kGdrBlk + 1][32], Z[kGdrBlk], zw[kW];
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g4 = lane >> 4;
+  __shared__ float X[kGdrBlk][kW][32], Y[kGdrBlk][kW][32], Z[kGdrBlk][kW], decs[kGdrBlk];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15,
+            g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);
   const int64_t blk = it % p.n_blks, bg = it / p.n_blks, g = bg % q.G, b = bg / q.G;
@@ -293,6 +474,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   Rows<T, kN, kThreads> ldk, ldq;
   Rows<O, kPS, kThreads> ldo;
   Rows<float, kPS, kThreads> ldv, ldu;
+  uint4 ldm[kMf];
   double lcum, llast;                                      // the next chunk's cumulated decay and lengths
   float lrk, lrq;
   f32x4 S[kPT], D[kPT];                                    // S and dS: column n, rows of the value channels
@@ -318,6 +500,12 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       ldo.load(sy.at, sy.stride, prow, tid);
       ldv.load_dense(p.dvw + (bl * Pp + p0) * kC, tid);
       ldu.load_dense(p.u + (bl * Pp + p0) * kC, tid);
+      const uint16_t* planes = p.planes + bl * 9 * kGdrPlane;
+#pragma unroll
+      for (int j = 0; j < kMf; ++j) {
+        const uint32_t at = (tid + kThreads * j) * 16;
+        ldm[j] = lane_load<uint4>(planes, at < 9 * kGdrPlane * 2 ? at : 0);
+      }
     };
     const uint32_t soff = (uint32_t)(4 * g4 * kN + n) * 4u;
     auto load_state = [&](const float* src, f32x4 (&x)[kPT]) {
@@ -338,6 +526,8 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       ldo.put(dOt, prow, tid);
       ldv.put(dVt, kPS, tid);
       ldu.put(Ut, kPS, tid);
+#pragma unroll
+      for (int j = 0; j < kMf; ++j) *reinterpret_cast<uint4*>(&mf[(tid + kThreads * j) * 8]) = ldm[j];
       if (w == 0) {
         const int t = lane & 31;
         cum[t] = lcum;
@@ -345,73 +535,30 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         en[t] = hw_exp2((float)(llast - lcum));
         rk[t] = lrk;
         rq[t] = lrq;
+        decs[c] = hw_exp2((float)llast);
       }
       __syncthreads();
-      const float dec = hw_exp2((float)cum[31]);
+      const float dec = decs[c];
 
-      // 32 x 32 products, lower tiles only: dV U^T, dY U^T, Q K^T, K K^T
-      for (int task = w; task < 12; task += kW) {
-        const int kind = task / 3, rt = task % 3 > 0, ct = task % 3 > 1;
-        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (kind == 0) {
-#pragma unroll 1
-          for (int kb = 0; kb < kPB; ++kb) {
-            bf16x8 a[3], u[3];
-            plane_frags_t<3, kPS>(dVt, 32 * kb, 16 * rt, lane, a);
-            plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * ct, lane, u);
-            acc = gdr_mma<3>(a, u, acc);
-          }
-        } else if (kind == 1) {
-#pragma unroll 1
-          for (int kb = 0; kb < kPB; ++kb) {
-            bf16x8 a[kGParts], u[3];
-            plane_frags_t<kGParts, kPS>(dOt, 32 * kb, 16 * rt, lane, a);
-            plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * ct, lane, u);
-            acc = gdr_mma<3>(a, u, acc);
-          }
-        } else {
-          const uint16_t* rows = kind == 2 ? Qt : Kt;
-#pragma unroll 1
-          for (int kb = 0; kb < kN / 32; ++kb) {
-            bf16x8 a[kParts], k[kParts];
-            gdr_frags_t<T, kN>(rows, 32 * kb, 16 * rt, lane, a);
-            gdr_frags_t<T, kN>(Kt, 32 * kb, 16 * ct, lane, k);
-            acc = gdr_mma<3>(a, k, acc);
-          }
-        }
-        const int j = 16 * ct + i16;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * rt + 4 * g4 + r;
-          float x = acc[r];
-          // diagonal of the first: dV_t . U_t (the other lanes write to a row of their own)
-          float* diag = &dvu[kind == 0 && i == j ? c : kGdrBlk][kind == 0 && i == j ? i : lane & 31];
-          *diag = first ? x : *diag + x;
-          const float dij = kind < 2 ? hw_exp2((float)(cum[i] - cum[j])) : 1.0f;
-          if (kind == 0) x = i > j ? x * dij : 0.0f;
-          if (kind == 1) x = i >= j ? x * q.scale * dij : 0.0f;
-          m[kind][i * 33 + j] = x;
-        }
-      }
       // through the states that enter and leave
       f32x4 Rq[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}, Rk[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
       f32x4 Ru[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
       float z = 0.0f;
 #pragma unroll
       for (int kb = 0; kb < kPB; ++kb) {
-        bf16x8 sb[3], db[3], ao[2][kGParts], av[2][3];
-        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
+        bf16x8 sb[3], db[3], ao[2][kGParts], av[2][3], au[2][3];
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
           plane_frags_t<kGParts, kPS>(dOt, 32 * kb, 16 * rt, lane, ao[rt]);
           plane_frags_t<3, kPS>(dVt, 32 * kb, 16 * rt, lane, av[rt]);
         }
+        gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb);
         gdr_mma_rows<3>(ao, sb, Rq);
         gdr_mma_rows<3>(av, sb, Rk);
         gdr_split<3>(D[2 * kb], D[2 * kb + 1], db);
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt) plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * rt, lane, av[rt]);
-        gdr_mma_rows<3>(av, db, Ru);
+        for (int rt = 0; rt < 2; ++rt) plane_frags_t<3, kPS>(Ut, 32 * kb, 16 * rt, lane, au[rt]);
+        gdr_mma_rows<3>(au, db, Ru);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           z = __builtin_fmaf(S[2 * kb][r], D[2 * kb][r], z);
@@ -419,26 +566,6 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         }
         __builtin_amdgcn_sched_barrier(0);                 // one block's operands in registers at a time
       }
-      z = gdr_sum16(z);
-      z += __shfl_xor(z, 16);
-      z += __shfl_xor(z, 32);
-      zw[w] = z;
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        const f32x4 ga = four(gam, rt), kt4 = four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4);
-        const f32x4 qt4 = four(rq, rt) * tile_four<kParts, kN>(Qt, n, 16 * rt + 4 * g4);
-        Rq[rt] *= ga * q.scale;
-        Rk[rt] *= ga;
-        Ru[rt] *= four(en, rt);
-        const f32x4 xs = qt4 * Rq[rt] - kt4 * Rk[rt], ys = kt4 * Ru[rt];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          red[0][w][16 * rt + 4 * g4 + r] = gdr_sum16(xs[r]);
-          red[1][w][16 * rt + 4 * g4 + r] = gdr_sum16(ys[r]);
-        }
-        Ru[rt] -= Rk[rt];
-      }
-      __syncthreads();
       // what the turns before left of this chunk, and the next one
       f32x4 aq[2], ak[2];
       const int64_t acc_at = ((bg * p.n_chunks + cc) * kN + n) * kC + 4 * g4;
@@ -451,74 +578,49 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       } else {
         aq[0] = aq[1] = ak[0] = ak[1] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
-
-      load_rows(cn);
       load_state(p.chunk_dS + ((bl0 + cn) * Pp + p0) * kN, D);
-      // operands of the products with K and Q, the lengths of the contracted rows folded in;
-      // dK takes M2 + M2^T with a minus
-      for (int task = w; task < 6; task += kW) {
-        const int kind = task >> 1, rt = task & 1, row = 16 * rt + i16;
-        // (read first, chosen afterwards: what the upper tile holds is dropped)
-        const float* mk = m[kind == 2 ? 0 : 1];
-        const f32x4* lens = reinterpret_cast<const f32x4*>(kind == 1 ? rq : rk);
-        const f32x4 l0 = lens[g4], l1 = lens[4 + g4];
-        f32x4 x[2];
+      z = gdr_sum16(z);
+      z += __shfl_xor(z, 16);
+      z += __shfl_xor(z, 32);
+      Z[c][w] = first ? z : Z[c][w] + z;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int col = (e < 4 ? 0 : 16) + 4 * g4 + (e & 3);
-          const int hi = row > col ? row : col, lo = row > col ? col : row;
-          x[e >> 2][e & 3] = mk[hi * 33 + lo] * (e < 4 ? l0 : l1)[e & 3];
+      for (int rt = 0; rt < 2; ++rt) {
+        const f32x4 ga = four(gam, rt), kt4 = four(rk, rt) * tile_four<kParts, kN>(Kt, n, 16 * rt + 4 * g4);
+        const f32x4 qt4 = four(rq, rt) * tile_four<kParts, kN>(Qt, n, 16 * rt + 4 * g4);
+        Rq[rt] *= ga * q.scale;
+        Rk[rt] *= ga;
+        Ru[rt] *= four(en, rt);
+        const f32x4 xs = qt4 * Rq[rt] - kt4 * Rk[rt], ys = kt4 * Ru[rt];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float *x = &X[c][w][16 * rt + 4 * g4 + r], *y = &Y[c][w][16 * rt + 4 * g4 + r];
+          const float a = gdr_sum16(xs[r]), e = gdr_sum16(ys[r]);
+          *x = first ? a : *x + a;
+          *y = first ? e : *y + e;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int col = (e < 4 ? 0 : 16) + 4 * g4 + (e & 3);
-          const bool in = kind == 0 ? row >= col : kind == 1 ? col >= row : row != col;
-          const float v = x[e >> 2][e & 3];
-          x[e >> 2][e & 3] = in ? (kind == 2 ? -v : v) : 0.0f;
-        }
-        bf16x8 f[3];
-        gdr_split<3>(x[0], x[1], f);
-#pragma unroll
-        for (int s = 0; s < 3; ++s) *reinterpret_cast<bf16x8*>(&mf[kind][s][rt][lane * 8]) = f[s];
+        Ru[rt] -= Rk[rt];
       }
-      // sums over a chunk's key numbers, and the pairs across each token: lane (half, j) has
-      // rows 16 half .. + 15 of column j and walks them from the last up
-      if (w == kW - 1) {
-        const int j = lane & 31, half = lane >> 5;
-        float s0 = 0.0f;
+      // within the chunk: M1 and M2 are sums over all slabs, so a head's first one adds them
+      if (first) {
+        bf16x8 kb_[kParts], qb[kParts], a[2][3];
+        plane_frags<kParts, kN>(Kt, 16 * w, 0, lane, kb_);
+        plane_frags<kParts, kN>(Qt, 16 * w, 0, lane, qb);
+        auto get = [&](int kind) {
 #pragma unroll
-        for (int k = 0; k < kW; ++k) s0 += red[half][k][j];
-        float(&to)[32] = half ? Y[c] : X[c];
-        to[j] = first ? s0 : to[j] + s0;
-        float f = 0.0f;
+          for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-        for (int k = 0; k < kW; ++k) f += zw[k];
-        Z[c] = dec * f + (first ? 0.0f : Z[c]);
-        float wv[16], all = 0.0f;
-        const float kj = rk[j];
-#pragma unroll
-        for (int t16 = 0; t16 < 16; ++t16) {
-          const int t = 16 * half + t16, at = t * 33 + j;
-          const float v = m[1][at] * rq[t] * m[2][at] - m[0][at] * rk[t] * m[3][at];
-          wv[t16] = t > j ? kj * v : 0.0f;                 // (the upper tile holds nothing)
-          all += wv[t16];
-        }
-        const float above = __shfl_xor(all, 32);
-        float acc = half ? 0.0f : above;
-        wave_sync();                                       // column j of m[3] is this lane pair's from here on
-#pragma unroll
-        for (int t16 = 15; t16 >= 0; --t16) {
-          const int t = 16 * half + t16;
-          acc += wv[t16];
-          m[3][t * 33 + j] = j < t ? acc : 0.0f;
-        }
-        wave_sync();
-        float s1 = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) s1 += m[3][j * 33 + 16 * half + k];
-        s1 += __shfl_xor(s1, 32);
-        pr[c][j] = first ? s1 : pr[c][j] + s1;
+            for (int s = 0; s < 3; ++s)
+              a[rt][s] = *reinterpret_cast<const bf16x8*>(&mf[(3 * kind + s) * kGdrPlane + rt * 512 + lane * 8]);
+        };
+        get(0);
+        gdr_mma_rows<3>(a, kb_, Rq);
+        get(1);
+        gdr_mma_rows<3>(a, qb, Ru);
+        get(2);
+        gdr_mma_rows<3>(a, kb_, Ru);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      load_rows(cn);
       // the state after the chunk
       {
         bf16x8 kb3[3];
@@ -536,38 +638,16 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-      __syncthreads();
-
-      // within the chunk
-      {
-        bf16x8 kb_[kParts], qb[kParts], a[2][3];
-        plane_frags<kParts, kN>(Kt, 16 * w, 0, lane, kb_);
-        plane_frags<kParts, kN>(Qt, 16 * w, 0, lane, qb);
-        auto get = [&](int kind) {
-#pragma unroll
-          for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-            for (int s = 0; s < 3; ++s) a[rt][s] = *reinterpret_cast<const bf16x8*>(&mf[kind][s][rt][lane * 8]);
-        };
-        get(0);
-        gdr_mma_rows<3>(a, kb_, Rq);
-        get(1);
-        gdr_mma_rows<3>(a, qb, Ru);
-        get(2);
-        gdr_mma_rows<3>(a, kb_, Ru);
-      }
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) {
         aq[rt] += Rq[rt];
         ak[rt] += Ru[rt];
       }
       if (turn + 1 < turns) {
-        {
 #pragma unroll
-          for (int rt = 0; rt < 2; ++rt) {
-            *reinterpret_cast<f32x4*>(p.acc_dq + acc_at + 16 * rt) = aq[rt];
-            *reinterpret_cast<f32x4*>(p.acc_dk + acc_at + 16 * rt) = ak[rt];
-          }
+        for (int rt = 0; rt < 2; ++rt) {
+          *reinterpret_cast<f32x4*>(p.acc_dq + acc_at + 16 * rt) = aq[rt];
+          *reinterpret_cast<f32x4*>(p.acc_dk + acc_at + 16 * rt) = ak[rt];
         }
       } else {                                             // all of dQ and dK: through the normalisation, out
         if (q.norm) {
@@ -612,24 +692,32 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       float sA = 0.0f, sb = 0.0f;
       const float A = q.A[h], bias = q.bias ? q.bias[h] : 0.0f;
       for (int c = 0; c < nc; ++c) {
-        const float x = X[c][t], y = Y[c][t];
+        const float* vec = p.vec + (bl0 + c) * p.vec_stride;
+        float x = 0.0f, y = 0.0f, f = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kW; ++k) {
+          x += X[c][k][t];
+          y += Y[c][k][t];
+          f += Z[c][k];
+        }
         float xs = x, ys = y;                              // sums over i >= t and over j <= t
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
           const float o = __shfl_down(xs, d, 32), u = __shfl_up(ys, d, 32);
-          if (t + d < 32) xs += o;
-          if (t >= d) ys += u;
+          xs += t + d < 32 ? o : 0.0f;
+          ys += t >= d ? u : 0.0f;
         }
-        const float dg = pr[c][t] + xs + (ys - y) + Z[c];
-        const int64_t tok = (cb + c) * kC + t;
+        const float dg = vec[t] + xs + (ys - y) + decs[c] * f;
+        const int64_t tok = (cb + c) * kC + t, at = bh * q.L + (tok < len ? tok : len - 1);
+        const float xr = gdr_load(static_cast<const T*>(q.delta) + at) + bias;
+        const float br = gdr_load(static_cast<const T*>(q.beta) + at);
+        const float dd = dg * A * gdr_sigmoid(xr), bt = gdr_sigmoid(br), step = softplus(xr);
+        const float db = bt > 0.0f ? vec[32 + t] / bt * gdr_sigmoid(-br) : 0.0f;
+        sA += tok < len ? dg * step : 0.0f;
+        sb += tok < len ? dd : 0.0f;
         if (lane < 32 && tok < len) {
-          const float xr = gdr_load(static_cast<const T*>(q.delta) + bh * q.L + tok) + bias;
-          const float br = gdr_load(static_cast<const T*>(q.beta) + bh * q.L + tok);
-          const float dd = dg * A * gdr_sigmoid(xr), bt = gdr_sigmoid(br);
-          gdr_store(static_cast<O*>(p.ddelta) + bh * q.L + tok, dd);
-          gdr_store(static_cast<O*>(p.dbeta) + bh * q.L + tok, bt > 0.0f ? dvu[c][t] / bt * gdr_sigmoid(-br) : 0.0f);
-          sA += dg * softplus(xr);
-          sb += dd;
+          gdr_store(static_cast<O*>(p.ddelta) + at, dd);
+          gdr_store(static_cast<O*>(p.dbeta) + at, db);
         }
       }
 #pragma unroll
@@ -637,11 +725,9 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         sA += __shfl_xor(sA, d);
         sb += __shfl_xor(sb, d);
       }
-      if (lane == 0) {
-        float* dst = p.part + ((b * p.n_blks + blk) * q.H + h) * 2;
-        dst[0] = sA;
-        dst[1] = sb;
-      }
+      float* dst = p.part + ((b * p.n_blks + blk) * q.H + h) * 2;
+      dst[0] = sA;
+      dst[1] = sb;
     }
   }
 
@@ -687,6 +773,8 @@ hipError_t bwd_n(const GdrChunkParams& p, hipStream_t s) {
   hipLaunchKernelGGL((gdr_adjoint_kernel<T, O, kN>), dim3((unsigned)(q.B * q.H * ((q.P + 63) / 64))), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((gdr_pair_kernel<T, O, kN>), dim3((unsigned)(q.B * q.H * p.n_chunks)), dim3(256), 0, s, p);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   const dim3 grid((unsigned)(q.B * q.G * p.n_blks));
   // 128 channels at a time where the operands have one plane each (LDS) and the padded
   // channels come in pairs of 64
