@@ -567,65 +567,66 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
 
 // ----------------------------------------------------------------------------- carries
 // start[0] = initial state, start[s + 1] = start[s] M_s + h_s.  The rows of the state
-// are independent: one workgroup per 16 of them, wave w the 16-column tiles w, w + 4.
-// Exact fp32 products (v_mfma_f32_16x16x4_f32): the chain is short and its bytes
-// (one N x N matrix per segment) come from L2.
-__global__ __launch_bounds__(256) void gdr_carry_kernel(GdrChunkParams p) {
-  constexpr int kRow = 132;
+// are independent: one workgroup per 16 of them, one wave per 16 columns.  Exact fp32
+// products (v_mfma_f32_16x16x4_f32).  The chain of segments is latency: a wave keeps its
+// columns of the next segment's M in registers (a load per 32 keys where they are used
+// cost 338 us at 16 heads, 128 x 128, 32 segments; so it is 46).
+template <int kN>
+__global__ __launch_bounds__(kN * 4) void gdr_carry_kernel(GdrChunkParams p) {
+  constexpr int kRow = kN + 4, kThreads = kN * 4, kB = kN / 4;
   __shared__ float A[2][16 * kRow];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), i16 = lane & 15, g4 = lane >> 4;
   const GdrParams& q = p.g;
   const int64_t tiles = (q.P + 15) / 16;
-  const int64_t bh = blockIdx.x / tiles, b = bh / q.H, h = bh % q.H, p0 = (blockIdx.x % tiles) * 16;
+  const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);      // the tiles of a head share M in one L2
+  const int64_t bh = it / tiles, b = bh / q.H, h = bh % q.H, p0 = (it % tiles) * 16;
   const int N = (int)q.N;
-  for (int e = tid; e < 16 * 128; e += 256) {
-    const int row = e >> 7, n = e & 127;
+  for (int e = tid; e < 16 * kN; e += kThreads) {
+    const int row = e / kN, n = e % kN;
     float x = 0.0f;
     if (p0 + row < q.P && n < N) {
       if (q.init) x = q.init[(bh * q.P + p0 + row) * N + n];
       p.seg_start[(((b * p.S) * q.H + h) * q.P + p0 + row) * N + n] = x;
     }
     A[0][row * kRow + n] = x;
-    A[1][row * kRow + n] = 0.0f;       // columns past N meet zeros of M, so they must be finite
   }
-  __syncthreads();
-  for (int64_t s = 0; s + 1 < p.S; ++s) {
-    const float* a = A[s & 1];
+  const int n = 16 * w + i16, nc = n < N ? n : N - 1;
+  float m[kB], hs[4];
+  // no branches around live registers: clamped addresses, and selects where they are used
+  auto load = [&](int64_t s) {
     const int64_t sm = (b * (p.S - 1) + s) * q.H + h;
     const float* M = p.seg_M + sm * (int64_t)N * N;
 #pragma unroll
-    for (int t2 = 0; t2 < 2; ++t2) {
-      const int n = 16 * (w + 4 * t2) + i16;
-      if (16 * (w + 4 * t2) >= N) continue;
-      f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-      // no branches around live registers: clamped addresses and selects
-      f32x4 hs;
-      const int nc = n < N ? n : N - 1;
+    for (int j = 0; j < kB; ++j) {
+      const int k = 4 * j + g4;
+      m[j] = lane_load<float>(M, (uint32_t)((k < N ? k : N - 1) * N + nc) * 4u);
+    }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t row = p0 + 4 * g4 + r;
-        const float x = p.seg_h[(sm * q.P + (row < q.P ? row : q.P - 1)) * N + nc];
-        hs[r] = n < N && row < q.P ? x : 0.0f;
-      }
-      for (int k0 = 0; k0 < N; k0 += 32) {
-        float m[8];
+    for (int r = 0; r < 4; ++r) {
+      const int64_t row = p0 + 4 * g4 + r;
+      hs[r] = p.seg_h[(sm * q.P + (row < q.P ? row : q.P - 1)) * N + nc];
+    }
+  };
+  load(0);
+  __syncthreads();
+  for (int64_t s = 0; s + 1 < p.S; ++s) {
+    const float* a = A[s & 1];
+    float mc[kB], hc[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int k = k0 + 4 * j + g4;
-          const float x = M[(int64_t)(k < N ? k : N - 1) * N + nc];
-          m[j] = k < N && n < N ? x : 0.0f;
-        }
+    for (int j = 0; j < kB; ++j) mc[j] = 4 * j + g4 < N && n < N ? m[j] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i16 * kRow + k0 + 4 * j + g4], m[j], acc, 0, 0, 0);
-      }
+    for (int r = 0; r < 4; ++r) hc[r] = n < N && p0 + 4 * g4 + r < q.P ? hs[r] : 0.0f;
+    load(s + 2 < p.S ? s + 1 : s);                         // the last segment loads itself again
+    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 4 * g4 + r;
-        const float x = acc[r] + hs[r];
-        A[(s + 1) & 1][row * kRow + n] = x;
-        if (n < N && p0 + row < q.P) p.seg_start[(((b * p.S + s + 1) * q.H + h) * q.P + p0 + row) * N + n] = x;
-      }
+    for (int j = 0; j < kB; ++j)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i16 * kRow + 4 * j + g4], mc[j], acc, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * g4 + r;
+      const float x = acc[r] + hc[r];
+      A[(s + 1) & 1][row * kRow + n] = x;                  // zero where n >= N: both terms are
+      if (n < N && p0 + row < q.P) p.seg_start[(((b * p.S + s + 1) * q.H + h) * q.P + p0 + row) * N + n] = x;
     }
     __syncthreads();
   }
@@ -653,7 +654,7 @@ hipError_t chunk_n(const GdrChunkParams& p, hipStream_t s) {
     hipLaunchKernelGGL((gdr_chain_kernel<T, O, kN, kSummary>),
                        dim3((unsigned)(q.B * (p.S - 1) * q.H * (vslices + islices))), dim3(256), 0, s, p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(gdr_carry_kernel, dim3((unsigned)(q.B * q.H * ((q.P + 15) / 16))), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(gdr_carry_kernel<kN>, dim3((unsigned)(q.B * q.H * ((q.P + 15) / 16))), dim3(kN * 4), 0, s, p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   hipLaunchKernelGGL((gdr_chain_kernel<T, O, kN, kFull>), dim3((unsigned)(q.B * p.S * q.H * vslices)), dim3(256), 0,
