@@ -69,22 +69,33 @@ struct GdrPlan {
   size_t off_planes = 0, off_vec = 0, off_tk = 0, off_tq = 0, off_tv = 0, off_M = 0, off_h = 0, off_start = 0, bytes = 0;
 };
 
-// Sizes-only plan of the forward pass.  Up to 24 tokens go token by token (one
-// launch).  In chunks, L is cut into segments when the 16-channel waves of all
-// heads would leave SIMDs idle (there are 1024): the summary launch then adds
-// the N transition rows to the P value rows of every head, so fewer than three
-// segments do not pay.
+// Sizes-only plan of the forward pass.
+// Token by token (one launch) while the steps cost less than the chunks' launches: a
+// step takes 2.1 us at N = 128 and 1.3 us at N = 64 until about 5000 rows of state keep
+// every CU busy, and grows with the rows from there.  Measured, call to call, token
+// against chunks: 32 heads of 128 x 128, L = 11: 22.4 and 27.8 us, L = 12: 28.9 and 28.1;
+// 4 heads of 64 x 64, L = 19: 22.3 and 26.6, L = 20: 28.0 and 26.3; 160 heads of 128 x 128,
+// L = 2: 22.4 and 26.5, L = 4: 38.6 and 27.9.
+// In chunks, L is cut into segments when the 16-channel waves of all heads would leave
+// SIMDs idle (there are 1024).  The summary launch then adds the N transition rows to the
+// P value rows of every head, so fewer than three segments do not pay, and the two launches
+// cost what 16 chunks do.  One wave per SIMD is the aim, in segments of 8 chunks or more, 32
+// at most.  128 x 128, one segment, the
+// rule's and two or three times as many: 16 heads, L = 32768: 2112, 726 (8), 755 us (24);
+// 16 heads, L = 2048: 140, 85 (8), 108 (16); 64 heads, L = 4096: 295 (1), 306 (4).  60 heads
+// of 80 x 96, L = 1003: 99 (1), 116 (3).
 GdrPlan make_gdr_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L, size_t e) {
   GdrPlan q;
   const int kernel = g_kernel.load();
-  q.chunk = kernel == 2 || (kernel == 0 && L > 24);
+  const int64_t rows = B * H * P, steps = L * ((rows + 5119) / 5120);
+  q.chunk = kernel == 2 || (kernel == 0 && steps > (N > 64 ? 11 : 19));
   if (!q.chunk) return q;
   q.n_chunks = (L + mamba::kGdrChunk - 1) / mamba::kGdrChunk;
   const int64_t waves = B * H * ((P + 15) / 16);
-  int64_t S = waves <= 512 ? 2048 / waves : 1;
-  if (S > q.n_chunks / 16) S = q.n_chunks / 16;
+  int64_t S = (1024 + waves / 2) / waves;
+  if (S > q.n_chunks / 8) S = q.n_chunks / 8;
   if (S > 32) S = 32;
-  if (S < 3) S = 1;
+  if (S < 3 || q.n_chunks - 2 * ((q.n_chunks + S - 1) / S) < 16) S = 1;
   const int64_t forced = g_segments.load();
   if (forced > 0) S = forced < q.n_chunks ? forced : q.n_chunks;
   q.seg_chunks = (q.n_chunks + S - 1) / S;
