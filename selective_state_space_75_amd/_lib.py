@@ -9,6 +9,7 @@ fallback.  If the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -553,6 +554,17 @@ def gdr_workspace_size(B: int, H: int, G: int, P: int, N: int, L: int, dtype=Non
     return n
 
 
+def _on(dev, stream):
+    """The device of a call, and the stream whose pool its own tensors come from: memory of
+    another stream's pool could be handed out again while the call's kernels still use it."""
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError("stream is on %s, expected %s" % (stream.device, dev))
+    return torch.cuda.stream(stream)
+
+
 def _workspace(workspace, need, dev):
     torch = _torch()
     if workspace is None:
@@ -593,7 +605,7 @@ def gdr_fwd(q, k, v, delta, beta, A, delta_bias=None, *, groups=None, initial_st
     _check(initial_state, "initial_state", (B, H * P, N), torch.float32, dev)
     _check(lengths, "lengths", (B,), torch.int32, dev)
     out_dt = in_dt if out_dtype is None else out_dtype
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
         if y is None:
             y = torch.empty((B, H * P, L), dtype=out_dt, device=dev)
         _check(y, "y", (B, H * P, L), out_dt, dev)
@@ -648,7 +660,7 @@ def gdr_bwd(q, k, v, delta, beta, A, delta_bias, dy, *, groups=None, initial_sta
     _dtype_code(dy)
     _check(dy, "dy", (B, H * P, L), None, dev)
     gdt = dy.dtype
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
         def new(*shape, dtype=gdt):
             return torch.empty(shape, dtype=dtype, device=dev)
 
@@ -689,7 +701,7 @@ def gdr_update(state, q, k, v, delta, beta, A, delta_bias=None, *, groups=None, 
     _check(state, "state", (S, H * P, N), torch.float32, dev)
     _check(slots, "slots", (B,), torch.int32, dev)
     out_dt = in_dt if out_dtype is None else out_dtype
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
         if y is None:
             y = torch.empty((B, H * P), dtype=out_dt, device=dev)
         _check(y, "y", (B, H * P), out_dt, dev)
@@ -737,7 +749,7 @@ def state_cache_write(state, codes, exps, *, slots=None, stream=None):
     mamba_state_cache.h): row r in slot slots[r] (int32 (rows); None: slot r;
     negative: not kept) of codes (n_slots, n) int8 and exps (n_slots, ceil(n / 32)) uint8."""
     rows, n, S, dev = _cache_args(codes, exps, slots, state, "state")
-    with _torch().cuda.device(dev):
+    with _on(dev, stream):
         st = lib().mamba_state_cache_write(_ptr(state), _ptr(slots), _ptr(codes), _ptr(exps), rows, n, S,
                                            _dtype_code(state), _stream(dev, stream))
     if st != 0:
@@ -751,9 +763,10 @@ def state_cache_read(codes, exps, *, slots=None, out=None, dtype=None, stream=No
     torch = _torch()
     if out is None:
         rows = codes.shape[0] if slots is None else slots.shape[0]
-        out = torch.empty((rows, codes.shape[1]), dtype=dtype or torch.float32, device=codes.device)
+        with _on(codes.device, stream) if codes.is_cuda else contextlib.nullcontext():
+            out = torch.empty((rows, codes.shape[1]), dtype=dtype or torch.float32, device=codes.device)
     rows, n, S, dev = _cache_args(codes, exps, slots, out, "out")
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
         st = lib().mamba_state_cache_read(_ptr(codes), _ptr(exps), _ptr(slots), _ptr(out), rows, n, S,
                                           _dtype_code(out), _stream(dev, stream))
     if st != 0:

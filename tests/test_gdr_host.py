@@ -197,3 +197,10 @@ def test_python_binding_rejects_before_calling():
         m.state_cache_write(torch.zeros(2, 5), torch.zeros(2, 5, dtype=torch.int8), torch.zeros(2, 1, dtype=torch.uint8))
     with pytest.raises(ValueError, match="codes"):
         m.state_cache_read(torch.zeros(5, dtype=torch.int8), torch.zeros(2, 1, dtype=torch.uint8), out=torch.zeros(2, 5))
+
+
+def test_a_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+    import torch
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        _lib._on(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1)))

@@ -1,0 +1,158 @@
+"""The gated delta rule's calls as they are used together: a prompt through the convolution and
+the rule, its state parked in 8 bits and taken back, tokens one by one; training forward and
+backward; all of it captured into a graph; and on streams of its own.
+
+Bars are those of the single calls, because every step is compared with the fp64 oracle from
+the GPU's own inputs of that step: bf16 outputs relative L2 2e-3 and max-abs 1e-2 max|y|, fp32
+1e-5; parking is exact; graph replays and other streams give the same bits."""
+import numpy as np
+import pytest
+
+from helpers import F32_REL_L2, assert_close, f64, from_dev, log, rel_l2, to_dev
+from oracle import gdr as O
+from selective_state_space_75_amd import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(B, H, G, P, N, L, dtype, seed, dev):
+    return {n: to_dev(a, dev) for n, a in W.gdr_inputs(B, H, G, P, N, L, dtype, seed).items()}
+
+
+@pytest.mark.parametrize("B,H,G,P,N,L,K", [(3, 4, 2, 64, 128, 75, 4), (2, 6, 3, 40, 64, 12, 4)])
+def test_prompt_park_and_decode(B, H, G, P, N, L, K, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    T, D, S = 3, 2 * G * N + H * P, B + 2
+    rng = np.random.default_rng(B * L)
+    f32 = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dev)  # noqa: E731
+    x, w = f32(B, D, L + T).bfloat16(), f32(D, K) * 0.5
+    gates = f32(2, B, H, L + T).bfloat16()
+    A, bias = -f32(H).abs() - 0.1, f32(H)
+    kw = dict(groups=G, qk_norm=True)
+
+    def ranges(z):
+        return z[:, :G * N], z[:, G * N:2 * G * N], z[:, 2 * G * N:]
+
+    z, cs = m.conv1d_fwd(x[:, :, :L].contiguous(), w, return_final_state=True)
+    dl, be = (gates[i, :, :, :L].contiguous() for i in range(2))
+    y, last = m.gdr_fwd(*ranges(z), dl, be, A, bias, return_final_state=True, **kw)
+    ar = [f64(from_dev(t)) for t in (*ranges(z), dl, be, A, bias)]
+    yr, sr = O.gdr(*ar, groups=G, norm=True)
+    assert_close(from_dev(y), yr, True, "prompt y")
+    assert rel_l2(from_dev(last), sr) <= F32_REL_L2
+
+    slots = torch.from_numpy(rng.permutation(S)[:B].astype(np.int32)).to(dev)
+    codes, exps = m.state_cache(S, H * P * N, dev)
+    m.state_cache_write(last, codes, exps, slots=slots)
+    state = torch.full((B, H * P, N), 7.0, device=dev)
+    m.state_cache_read(codes, exps, slots=slots, out=state)
+    for b in range(B):
+        kept = O.cache_read(*O.cache_write(from_dev(last)[b].reshape(-1)))
+        assert np.array_equal(from_dev(state)[b].reshape(-1), kept)
+
+    for t in range(L, L + T):
+        zt = m.conv1d_update(cs, x[:, :, t].contiguous(), w)
+        dl, be = (gates[i, :, :, t].contiguous() for i in range(2))
+        before = f64(from_dev(state))
+        yt = m.gdr_update(state, *ranges(zt), dl, be, A, bias, **kw)
+        a = [f64(from_dev(v))[..., None] for v in (*ranges(zt), dl, be)] + [f64(from_dev(A)), f64(from_dev(bias))]
+        yr, sr = O.gdr(*a, groups=G, norm=True, initial_state=before)
+        assert_close(from_dev(yt), yr[..., 0], True, "token %d" % t)
+        assert rel_l2(from_dev(state), sr) <= F32_REL_L2
+    # the convolution's steps go on where its prompt ended
+    whole = m.conv1d_fwd(x, w)
+    assert_close(from_dev(zt), f64(from_dev(whole))[:, :, -1], True, "last convolution")
+
+
+@pytest.mark.parametrize("kernel,segments", [("planner", 0), ("chunk", 3)])
+def test_graph_replays_equal_eager(kernel, segments, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    B, H, G, P, N, L = 2, 4, 2, 64, 64, 200
+    sets = [_inputs(B, H, G, P, N, L, "bf16", 40 + k, dev) for k in range(3)]
+    bufs = {n: a.clone() for n, a in sets[0].items()}
+    names = ("q", "k", "v", "delta_raw", "beta_raw", "A", "delta_bias")
+    state = torch.empty((B, H * P, N), device=dev)
+    codes, exps = m.state_cache(B, H * P * N, dev)
+    wb = torch.empty(m.gdr_bwd_workspace_size(B, H, G, P, N, L), dtype=torch.uint8, device=dev)
+
+    def run(x, c, e, st):
+        args = [x[n] for n in names]
+        kw = dict(groups=G, qk_norm=True)
+        y, last = m.gdr_fwd(*args, return_final_state=True, initial_state=x["initial_state"], workspace=wf, **kw)
+        gr = m.gdr_bwd(*args, x["dy"], initial_state=x["initial_state"], dfinal_state=x["dfinal_state"], workspace=wb,
+                       **kw)
+        m.state_cache_write(last, c, e)
+        m.state_cache_read(c, e, out=st)
+        yt = m.gdr_update(st, *[x[n][:, :, 0].contiguous() for n in names[:5]], x["A"], x["delta_bias"], **kw)
+        return [y, last, yt] + [gr[n] for n in sorted(gr)]
+
+    with m.gdr_test_knobs(kernel=kernel, segments=segments):
+        need = m.gdr_workspace_size(B, H, G, P, N, L)
+        wf = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        side = torch.cuda.Stream(dev)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs = run(bufs, codes, exps, state)
+        for rep in range(5):
+            src = sets[rep % 3]
+            for n in bufs:
+                bufs[n].copy_(src[n])
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            got = [o.clone() for o in outs] + [state.clone(), codes.clone(), exps.clone()]
+            c2, e2 = m.state_cache(B, H * P * N, dev)
+            st2 = torch.empty_like(state)
+            ref = run(src, c2, e2, st2) + [st2, c2, e2]
+            torch.cuda.synchronize()
+            for i, (a, r) in enumerate(zip(got, ref)):
+                assert torch.equal(a, r), "replay %d, output %d" % (rep, i)
+
+
+def test_two_streams_at_once(dev):
+    """Calls on two streams at once, the wrapper's own workspaces: the bits of one call alone."""
+    import torch
+    import selective_state_space_75_amd as m
+    B, H, G, P, N, L = 2, 8, 4, 128, 128, 300
+    xs = [_inputs(B, H, G, P, N, L, "bf16", 60 + k, dev) for k in range(2)]
+    names = ("q", "k", "v", "delta_raw", "beta_raw", "A", "delta_bias")
+
+    def run(x, stream):
+        args = [x[n] for n in names]
+        y, st = m.gdr_fwd(*args, groups=G, qk_norm=True, return_final_state=True, stream=stream)
+        gr = m.gdr_bwd(*args, x["dy"], groups=G, qk_norm=True, stream=stream)
+        return [y, st] + [gr[n] for n in sorted(gr) if gr[n] is not None]
+
+    alone = [run(x, None) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in xs]
+    for _ in range(3):
+        got = [run(x, s) for x, s in zip(xs, streams)]
+        # the caller's stream allocates meanwhile: none of it may be a running call's workspace
+        junk = [torch.full((1 << 20,), float("nan"), device=dev) for _ in range(8)]
+        torch.cuda.synchronize()
+        del junk
+        for a, b in zip(alone, got):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_training_step_from_the_convolution(dev):
+    """fp32 gradients of the rule on the convolution's output ranges against the oracle."""
+    import torch
+    import selective_state_space_75_amd as m
+    B, H, G, P, N, L, K = 2, 4, 2, 48, 64, 70, 4
+    rng = np.random.default_rng(5)
+    f32 = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dev)  # noqa: E731
+    z = m.conv1d_fwd(f32(B, 2 * G * N + H * P, L), f32(2 * G * N + H * P, K) * 0.5)
+    q, k, v = z[:, :G * N], z[:, G * N:2 * G * N], z[:, 2 * G * N:]
+    dl, be, A, bias = f32(B, H, L), f32(B, H, L), -f32(H).abs() - 0.1, f32(H)
+    y = m.gdr_fwd(q, k, v, dl, be, A, bias, groups=G, qk_norm=True)
+    gr = m.gdr_bwd(q, k, v, dl, be, A, bias, y, groups=G, qk_norm=True)      # of sum(y^2) / 2
+    ref = O.gdr_bwd(*[f64(from_dev(t)) for t in (q, k, v, dl, be, A, bias, y)], groups=G, norm=True)
+    for n in ("dq", "dk", "dv", "ddelta", "dbeta", "dA", "ddelta_bias"):
+        e = rel_l2(from_dev(gr[n]), ref[n])
+        log("  %s: rel_l2=%.3e" % (n, e))
+        assert e <= F32_REL_L2, n
