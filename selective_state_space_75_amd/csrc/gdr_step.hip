@@ -11,7 +11,8 @@
 // rows (times kSets), and the two sums over a row are four lane exchanges.
 //
 // One token moves 8 bytes per number of the state (fp32 read and written in
-// place) and computes 7 flops on it: HBM-bound, like mamba_state_update.
+// place) and computes 7 flops on it: HBM-bound, like mamba_state_update.  128 rows of 32
+// heads of 128 x 128: 125 us, 4.2 TB/s (a large copy: 4.78).
 #include "device_math.hpp"
 #include "gdr.hpp"
 #include "kernels.hpp"
