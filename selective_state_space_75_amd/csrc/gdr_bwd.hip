@@ -256,7 +256,10 @@ __device__ __forceinline__ f32x4 tile_four(const uint16_t* tile, int n, int t) {
 // In both kernels below no branch that only some lanes of a wave take encloses or follows
 // live registers: every lane writes (the same value where one would do), addresses are
 // clamped.  At such a branch's end the compiler may save registers before it
-// re-enables the other lanes when it runs out of them.
+// re-enables the other lanes when it runs out of them.  (One remains: the stores of dQ and
+// dK where N is less than the tile, since a clamped row would be another lane's.  The
+// assembly of every variant has no copy between its end and the restored lanes; look
+// again after a change.)
 
 // One workgroup per (batch row, value head, chunk): the 32 x 32 products dV U^T, dY U^T
 // (64 value channels at a time), K K^T and Q K^T, lower tiles only.  Leaves M1 (columns

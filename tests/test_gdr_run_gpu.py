@@ -156,3 +156,43 @@ def test_training_step_from_the_convolution(dev):
         e = rel_l2(from_dev(gr[n]), ref[n])
         log("  %s: rel_l2=%.3e" % (n, e))
         assert e <= F32_REL_L2, n
+
+
+@pytest.mark.parametrize("B,H,G,P,N,L,dtype,gdt,lengths", [
+    (2, 4, 2, 200, 96, 70, "bf16", "bf16", [70, 33]),       # two slabs of 128, the last partly empty
+    (1, 6, 2, 130, 128, 161, "f32", "f32", None),           # three slabs of 64, three value heads each
+    (2, 2, 1, 72, 20, 40, "bf16", "f32", [0, 40]),          # a row without tokens
+    (1, 2, 2, 256, 64, 129, "f32", "bf16", None),           # a chunk of one token
+])
+def test_gradients_over_slabs_of_value_channels(B, H, G, P, N, L, dtype, gdt, lengths, dev):
+    """The products within a chunk are sums over all value channels and count once, however many
+    slabs the sweep takes; gates at both ends of their range among the tokens."""
+    import torch
+    import selective_state_space_75_amd as m
+    log("[gdr slabs] %s" % ((B, H, G, P, N, L, dtype, gdt),))
+    x = W.gdr_inputs(B, H, G, P, N, L, dtype, 70 + P)
+    names = ("q", "k", "v", "delta_raw", "beta_raw", "A", "delta_bias")
+    t = {n: to_dev(a, dev) for n, a in x.items()}
+    for i, b in enumerate((-60.0, 60.0, -25.0, 25.0)):
+        t["beta_raw"][:, :, i] = b
+    t["delta_raw"][:, :, 5] = 40.0
+    t["delta_raw"][:, :, 6] = -40.0
+    dy = t["dy"].to(torch.float32 if gdt == "f32" else torch.bfloat16)
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=dev)
+    g = m.gdr_bwd(*[t[n] for n in names], dy, groups=G, qk_norm=True, lengths=ln)
+    ref = O.gdr_bwd(*[f64(from_dev(t[n])) for n in names], f64(from_dev(dy)), groups=G, lengths=lengths, norm=True)
+    # A bf16 number is off by at most half a step, 2^-8 of it, so a tensor's relative L2 is at
+    # most 2^-8 (1 + e) + e with e = 1e-5 before the rounding.  (The 2e-3 of the other tests is
+    # what values spread over a binade give; the extreme gates leave ddelta's norm in a few
+    # numbers.)  That e itself is held to 1e-5 by the same gradients asked for in fp32.
+    e = F32_REL_L2
+    full = m.gdr_bwd(*[t[n] for n in names], dy.float(), groups=G, qk_norm=True, lengths=ln)
+    for n in ("dq", "dk", "dv", "ddelta", "dbeta", "dA", "ddelta_bias"):
+        got, got32 = rel_l2(from_dev(g[n]), ref[n]), rel_l2(from_dev(full[n]), ref[n])
+        log("  %s: rel_l2=%.3e, as fp32 %.3e" % (n, got, got32))
+        assert got32 <= e, n
+        assert got <= (2.0 ** -8 * (1 + e) + e if g[n].dtype == torch.bfloat16 else e), n
+    if lengths is not None:
+        for n in ("dq", "dk", "dv", "ddelta", "dbeta"):
+            for b in range(B):
+                assert not from_dev(g[n])[b, :, lengths[b]:].any(), n
