@@ -133,10 +133,11 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
     const int64_t cn = c > 0 ? c - 1 : 0;                  // the first chunk loads itself again
     load_tiles(cn);
     {
-      float* dst = p.chunk_dS + ((blk0 + c) * Pp + ch) * kN;
+      // in tiles of 16 channels x 16 keys: 1 KB a store, and what a wave of the grads reads
+      float* dst = p.chunk_dS + ((blk0 + c) * Pp + slice * 64 + 16 * w) * kN + 16 * i16 + 4 * g4;
 #pragma unroll
       for (int tn = 0; tn < kNT; ++tn)
-        *reinterpret_cast<f32x4*>(dst + 16 * tn + 4 * g4) = mine ? S[tn] : f32x4{0.f, 0.f, 0.f, 0.f};
+        *reinterpret_cast<f32x4*>(dst + 256 * tn) = mine ? S[tn] : f32x4{0.f, 0.f, 0.f, 0.f};
     }
     // right-hand side E K dS^T + Pm^T dY
     f32x4 R[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
@@ -533,9 +534,17 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[tp][r] = lane_load<float>(src + (16 * tp + r) * kN, soff);
     };
+    auto load_dstate = [&](int64_t bl) {
+      const float* src = p.chunk_dS + (bl * Pp + p0) * kN + w * 256;
+#pragma unroll
+      for (int tp = 0; tp < kPT; ++tp)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          D[tp][r] = lane_load<float>(src + tp * 16 * kN + 16 * r, (uint32_t)(64 * g4 + i16) * 4u);
+    };
     load_rows(0);
     load_state(p.blk_S + ((bh * p.n_blks + blk) * Pp + p0) * kN, S);
-    load_state(p.chunk_dS + (bl0 * Pp + p0) * kN, D);
+    load_dstate(bl0);
     for (int c = 0; c < nc; ++c) {
       const int64_t cc = cb + c;
       const int cn = c + 1 < nc ? c + 1 : c;
@@ -596,7 +605,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       } else {
         aq[0] = aq[1] = ak[0] = ak[1] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
-      load_state(p.chunk_dS + ((bl0 + cn) * Pp + p0) * kN, D);
+      load_dstate(bl0 + cn);
       z = gdr_sum16(z);
       z += __shfl_xor(z, 16);
       z += __shfl_xor(z, 32);

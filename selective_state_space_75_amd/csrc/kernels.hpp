@@ -203,7 +203,7 @@ struct GdrChunkParams {
   // with Pp = P and Np = N rounded up to 64 (Np: 64 or 128), zeros in between
   float *u, *dvw;          // (B, H, n_chunks, Pp, 32): updates, gradients of v
   float* blk_S;            // (B, H, n_blks, Pp, Np): state entering each block of kGdrBlk chunks
-  float* chunk_dS;         // (B, H, n_chunks, Pp, Np): gradient of the state leaving each chunk
+  float* chunk_dS;         // (B, H, n_chunks, Pp/16, Np/16, 16, 16): gradient of the state leaving each chunk
   float *acc_dq, *acc_dk;  // (B, G, n_chunks, Np, 32): sums over value heads (more than one, or P > a slab)
   int64_t n_blks;
   void *dq, *dk, *dv;      // grad dtype, like q, k, v (dense)
