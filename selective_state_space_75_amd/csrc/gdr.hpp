@@ -36,15 +36,6 @@ __device__ __forceinline__ float gdr_sigmoid(float x) { return hw_rcp(1.0f + hw_
 // a = exp(A softplus(x))
 __device__ __forceinline__ float gdr_decay(float x, float A) { return hw_exp2(softplus(x) * A * kLog2e); }
 
-// The same scalars for the backward pass, in 64 bits.  Each scales a whole row of 128
-// numbers, so its error does not average out over the row as the products' roundings do,
-// and the gates' gradients are sums over tokens that cancel to a few hundredths of their
-// terms.  There are 32 of each per chunk.  40 heads of 128 x 128, batch 4, L = 2048, errors
-// against fp64 with the hardware's forms and these: dA 7e-7 to 1.05e-6 and 6e-7; ddelta in
-// fp32 2.3e-7 and 2.0e-7; they cost 4% of the call.
-__device__ __forceinline__ double gdr_sigmoid_64(double x) { return 1.0 / (1.0 + exp(-x)); }
-__device__ __forceinline__ double gdr_softplus_64(double x) { return (x > 0.0 ? x : 0.0) + log1p(exp(-__builtin_fabs(x))); }
-
 // 1 / |x| of a key or query from its sum of squares.  One Newton step on the
 // hardware's reciprocal root (1 ulp) leaves about half an ulp: the factor goes
 // into every number of the row.

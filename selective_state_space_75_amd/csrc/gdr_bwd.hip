@@ -22,7 +22,7 @@
 //   states  forward along L: U of every chunk, S at every block of 4 chunks;
 //   adjoint backward along L: dV and dS of every chunk;
 //   pairs   all chunks at once: M1 and M2 as operands (over T's planes, which are not
-//           needed any more), dbeta, and what of dg follows from them alone;
+//           needed any more), and what of dg and dbeta follows from them alone;
 //   grads   all blocks at once: the states inside a block are rebuilt forward from S,
 //           everything else is products;
 //   sums    dA and ddelta_bias from the blocks' partial sums, in a fixed order.
@@ -265,9 +265,7 @@ __device__ __forceinline__ f32x4 tile_four(const uint16_t* tile, int n, int t) {
 // One workgroup per (batch row, value head, chunk): the 32 x 32 products dV U^T, dY U^T
 // (64 value channels at a time), K K^T and Q K^T, lower tiles only.  Leaves M1 (columns
 // times 1/|k|), M1^T (times 1/|q|) and -(M2 + M2^T) (times 1/|k|) as operand planes of
-// the products with K and Q, dbeta (from dV_t . U_t), and per token the pairs' part of
-// dg and the gates' factors (in 64 bits here: in the sweep they would spill registers,
-// 680 us against 568).
+// the products with K and Q, and per token the pairs' part of dg and dV_t . U_t.
 template <typename T, typename O, int kN>
 __global__ __launch_bounds__(256) void gdr_pair_kernel(GdrChunkParams p) {
   constexpr int kParts = GdrIn<T>::kParts, kGParts = GdrIn<O>::kParts, kPS = 64;
@@ -438,17 +436,7 @@ __global__ __launch_bounds__(256) void gdr_pair_kernel(GdrChunkParams p) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) s1 += m[3][j * 33 + 16 * half + k];
     s1 += __shfl_xor(s1, 32);
-    // over the chunk's factors, all that the gradients' sweep needs of the gates; dbeta
-    // needs nothing else
-    const int64_t tok = c * kC + j, at = bh * q.L + (tok < len ? tok : len - 1);
-    const double x = (double)gdr_load(static_cast<const T*>(q.delta) + at) + (q.bias ? q.bias[h] : 0.0f);
-    const float br = gdr_load(static_cast<const T*>(q.beta) + at), bt = (float)gdr_sigmoid_64(br);
-    const double G = cum[j], last = cum[31];
-    vec[lane] = half ? (float)gdr_softplus_64(x) : s1;
-    vec[64 + lane] = (float)exp2(half ? G : last - G);
-    vec[192 + j] = (float)(q.A[h] * gdr_sigmoid_64(x));
-    const float db = bt > 0.0f ? dvu[j] / bt * (float)gdr_sigmoid_64(-br) : 0.0f;
-    if (half == 0 && tok < len) gdr_store(static_cast<O*>(p.dbeta) + at, db);
+    vec[lane] = half ? dvu[j] : s1;                        // over the factors of k and q
   }
 }
 
@@ -468,6 +456,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   __shared__ __align__(16) uint16_t Kt[kParts * kN * kGdrRow];
   __shared__ __align__(16) uint16_t Qt[kParts * kN * kGdrRow];
   __shared__ __align__(16) uint16_t mf[kMf * kThreads * 8];               // operands made of M1, M1^T and M2 + M2^T
+  __shared__ double cum[32];
   __shared__ __align__(16) float gam[32], en[32], rk[32], rq[32];
   __shared__ __align__(16) float red[2][kW][32];
   __shared__ float X[kGdrBlk][kW][32], Y[kGdrBlk][kW][32], Z[kGdrBlk][kW], decs[kGdrBlk];
@@ -496,7 +485,8 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   Rows<O, kPS, kThreads> ldo;
   Rows<float, kPS, kThreads> ldv, ldu;
   uint4 ldm[kMf];
-  float lgam, lend, lrk, lrq;                              // the next chunk's decays and lengths
+  double lcum, llast;                                      // the next chunk's cumulated decay and lengths
+  float lrk, lrq;
   f32x4 S[kPT], D[kPT];                                    // S and dS: column n, rows of the value channels
   auto four = [&](const float* v, int rt) { return *reinterpret_cast<const f32x4*>(v + 16 * rt + 4 * g4); };
 
@@ -513,8 +503,8 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       const float* vec = p.vec + bl * p.vec_stride;
       lrk = lane_load<float>(vec + 128, (lane & 31) * 4);
       lrq = lane_load<float>(vec + 160, (lane & 31) * 4);
-      lgam = lane_load<float>(vec + 96, (lane & 31) * 4);
-      lend = lane_load<float>(vec + 64, (lane & 31) * 4);
+      lcum = lane_load<double>(vec + 192, (lane & 31) * 8);
+      llast = *reinterpret_cast<const double*>(vec + 192 + 62);
       ldk.load(sk.at, sk.stride, q.N, tid);
       ldq.load(sq.at, sq.stride, q.N, tid);
       ldo.load(sy.at, sy.stride, prow, tid);
@@ -558,11 +548,12 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
       for (int j = 0; j < kMf; ++j) *reinterpret_cast<uint4*>(&mf[(tid + kThreads * j) * 8]) = ldm[j];
       if (w == 0) {
         const int t = lane & 31;
-        gam[t] = lgam;
-        en[t] = lend;
+        cum[t] = lcum;
+        gam[t] = hw_exp2((float)lcum);
+        en[t] = hw_exp2((float)(llast - lcum));
         rk[t] = lrk;
         rq[t] = lrq;
-        decs[c] = __shfl(lgam, 31);
+        decs[c] = hw_exp2((float)llast);
       }
       __syncthreads();
       const float dec = decs[c];
@@ -717,6 +708,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
     if (last && w == 0) {
       const int t = lane & 31;
       float sA = 0.0f, sb = 0.0f;
+      const float A = q.A[h], bias = q.bias ? q.bias[h] : 0.0f;
       for (int c = 0; c < nc; ++c) {
         const float* vec = p.vec + (bl0 + c) * p.vec_stride;
         float x = 0.0f, y = 0.0f, f = 0.0f;
@@ -726,20 +718,25 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
           y += Y[c][k][t];
           f += Z[c][k];
         }
-        float xs = x, ys = y;                              // sums over i >= t and over j <= t (then j < t)
+        float xs = x, ys = y;                              // sums over i >= t and over j <= t
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
           const float o = __shfl_down(xs, d, 32), u = __shfl_up(ys, d, 32);
           xs += t + d < 32 ? o : 0.0f;
           ys += t >= d ? u : 0.0f;
         }
-        const float before = __shfl_up(ys, 1, 32);
-        const float dg = vec[t] + xs + (t > 0 ? before : 0.0f) + decs[c] * f;
+        const float dg = vec[t] + xs + (ys - y) + decs[c] * f;
         const int64_t tok = (cb + c) * kC + t, at = bh * q.L + (tok < len ? tok : len - 1);
-        const float dd = dg * vec[192 + t];
-        sA += tok < len ? dg * vec[32 + t] : 0.0f;
+        const float xr = gdr_load(static_cast<const T*>(q.delta) + at) + bias;
+        const float br = gdr_load(static_cast<const T*>(q.beta) + at);
+        const float dd = dg * A * gdr_sigmoid(xr), bt = gdr_sigmoid(br), step = softplus(xr);
+        const float db = bt > 0.0f ? vec[32 + t] / bt * gdr_sigmoid(-br) : 0.0f;
+        sA += tok < len ? dg * step : 0.0f;
         sb += tok < len ? dd : 0.0f;
-        if (lane < 32 && tok < len) gdr_store(static_cast<O*>(p.ddelta) + at, dd);
+        if (lane < 32 && tok < len) {
+          gdr_store(static_cast<O*>(p.ddelta) + at, dd);
+          gdr_store(static_cast<O*>(p.dbeta) + at, db);
+        }
       }
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {

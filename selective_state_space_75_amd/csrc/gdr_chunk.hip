@@ -166,12 +166,10 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
     double cum = 0.0;
     float beta = 0.0f;
     if (t < len) {
-      const float x = gdr_load(static_cast<const T*>(q.delta) + bh * q.L + t), bias = q.bias ? q.bias[h] : 0.0f;
-      const float bt = gdr_load(static_cast<const T*>(q.beta) + bh * q.L + t);
-      const double g2 = kBwd ? gdr_softplus_64((double)x + bias) * q.A[h] * 1.4426950408889634
-                             : (double)(softplus(x + bias) * q.A[h] * kLog2e);
-      cum = g2 < -1000.0 ? -1000.0 : g2;
-      beta = kBwd ? (float)gdr_sigmoid_64(bt) : gdr_sigmoid(bt);
+      const float x = gdr_load(static_cast<const T*>(q.delta) + bh * q.L + t) + (q.bias ? q.bias[h] : 0.0f);
+      const float g2 = softplus(x) * q.A[h] * kLog2e;
+      cum = g2 < -1000.0f ? -1000.0 : (double)g2;
+      beta = gdr_sigmoid(gdr_load(static_cast<const T*>(q.beta) + bh * q.L + t));
     }
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -181,13 +179,12 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
     if (half == 0) cums[w][c32] = cum;
     const double last = __shfl(cum, 31, 32);
     const float rk = rlen[0][c32], rq = rlen[1][c32] * q.scale;
-    const float dec = kBwd ? (float)exp2(cum) : hw_exp2((float)cum);
-    const float rest = kBwd ? (float)exp2(last - cum) : hw_exp2((float)(last - cum));
+    const float dec = hw_exp2((float)cum);
     if (half == 0) {
       vec[c32] = dec * rk;
       vec[32 + c32] = dec * rq;
-      vec[64 + c32] = rest * rk;
-      if (c32 == 31) vec[96] = dec;
+      vec[64 + c32] = hw_exp2((float)(last - cum)) * rk;
+      if (c32 == 0) vec[96] = hw_exp2((float)last);
       if constexpr (kBwd) {
         vec[128 + c32] = rk;
         vec[160 + c32] = rlen[1][c32];

@@ -180,7 +180,7 @@ struct GdrParams {
 constexpr int kGdrChunk = 32;
 constexpr int kGdrPlane = 1024;                 // bf16 numbers of one 32 x 32 operand plane
 constexpr int kGdrVec = 128;                    // floats of per-token factors per block (forward)
-constexpr int kGdrVecBwd = 256;                 // backward: also 1/|k|, 1/|q|, cumulated log decays (fp64); see gdr_pair_kernel
+constexpr int kGdrVecBwd = 256;                 // backward: also 1/|k|, 1/|q| and the cumulated log decays (fp64)
 constexpr int kGdrBlk = 4;                      // chunks between the states that the backward pass keeps
 
 struct GdrChunkParams {
@@ -194,8 +194,7 @@ struct GdrChunkParams {
   float* seg_start;        // (B, S, H, P, N) state entering each segment
   int64_t n_chunks, S, seg_chunks;
   int p_parts;             // planes of the query matrix: 2, or 3 for fp32 outputs
-  // backward pass: planes are 3 of T, 3 of T^T, 3 of the query matrix transposed, then
-  // (gdr_pair_kernel) 3 each of M1, M1^T and -(M2 + M2^T)
+  // backward pass: planes are 3 of T, 3 of T^T, 3 of the query matrix transposed
   int vec_stride;          // kGdrVec or kGdrVecBwd
   const void* dy;          // (B, H P, L) grad dtype
   const float* dfinal;     // (B, H P, N) or null
