@@ -31,8 +31,8 @@
 // sums over value channels that stay inside a wave.  One workgroup takes all value
 // heads of a key head, so dQ and dK need no reduction between workgroups.
 //
-// Measured, bf16, 40 heads of 128 x 128, batch 4, L = 2048 (422 MB): preparation 79 us,
-// states 230, adjoint 495, pairs 199, grads 585, sums 5; the call 1.57 ms.  The bytes at a large
+// Measured, bf16, 40 heads of 128 x 128, batch 4, L = 2048 (422 MB): preparation 73 us,
+// states 230, adjoint 462, pairs 175, grads 563, sums 5; the call 1.49 ms.  The bytes at a large
 // copy's rate are 88 us.  The chains are bound as the forward's; the adjoint also writes
 // dS of every chunk (671 MB) so that the grads need no second backward sweep.  The grads
 // hold S and dS in registers, which leaves one workgroup per CU.
