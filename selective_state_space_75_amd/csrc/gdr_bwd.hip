@@ -58,8 +58,8 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
   const int64_t slice = it % slices, h = (it / slices) % q.H, b = it / (slices * q.H);
   const int64_t bh = b * q.H + h, g = h / (q.H / q.G);
   const int64_t ch = slice * 64 + 16 * w + i16;
-  const bool mine = ch < q.P;                    // lanes without a channel run along on channel 0
-  const int64_t vch = mine ? ch : 0;
+  const bool mine = ch < q.P, some = slice * 64 + 16 * w < q.P;
+  const int64_t vch = mine ? ch : q.P - 1;       // lanes past the last channel run along on it
   const int64_t len = gdr_length(q, b), ce = (len + kC - 1) / kC;
 
   const T* krows = static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L;
@@ -77,11 +77,7 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
 #pragma unroll
   for (int tn = 0; tn < kNT; ++tn) {
     S[tn] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (mine && p.dfinal) S[tn] = gdr_load_state(p.dfinal + (bh * q.P + ch) * q.N, 16 * tn + 4 * g4, q.N, q.state_vec);
-  }
-  // tokens behind the row's end
-  if (mine) {
-    for (int64_t t = ce * kC + 4 * g4; t < q.L; t += 16) gdr_store4(dvrow, t, q.L, f32x4{0.f, 0.f, 0.f, 0.f});
+    if (p.dfinal) S[tn] = gdr_load_state(p.dfinal + (bh * q.P + vch) * q.N, 16 * tn + 4 * g4, q.N, q.state_vec);
   }
 
   bf16x8 tf[2][3], pf[2][3];
@@ -119,11 +115,6 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
     load_tiles(ce - 1);
     tk.put(Kt[0], tid);
     tq.put(Qt[0], tid);
-#pragma unroll
-    for (int buf = 0; buf < kBuf; ++buf) {
-      tk.clear(Kt[buf], tid);
-      tq.clear(Qt[buf], tid);
-    }
     load_rest(ce - 1);
     __syncthreads();
   }
@@ -180,19 +171,29 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
     }
     float* wdst = p.dvw + ((blk0 + c) * Pp + ch) * kC + 4 * g4;
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt) {
+    for (int rt = 0; rt < 2; ++rt)
       *reinterpret_cast<f32x4*>(wdst + 16 * rt) = mine ? W[rt] : f32x4{0.f, 0.f, 0.f, 0.f};
-      if (mine) gdr_store4(dvrow, c * kC + 16 * rt + 4 * g4, q.L, W[rt]);
+    if (some && (c + 1) * kC <= len) {                     // (the chunk of the row's end: after the loop)
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) gdr_store_whole4(dvrow + c * kC + 16 * rt + 4 * g4, W[rt]);
     }
     if constexpr (kBuf == 1) __syncthreads();
     tk.put(Kt[kBuf == 2 ? buf ^ 1 : 0], tid);
     tq.put(Qt[kBuf == 2 ? buf ^ 1 : 0], tid);
     __syncthreads();
   }
-  if (mine && p.dinit) {
-    float* dst = p.dinit + (bh * q.P + ch) * q.N;
-#pragma unroll
-    for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+  if (p.dinit) {
+    const int64_t ch0 = slice * 64 + 16 * w;
+    gdr_store_rows(p.dinit + (bh * q.P + ch0) * q.N, q.P - ch0, q.N, q.state_vec, S, lane);
+  }
+  if (mine) {
+    if (ce * kC > len) {
+      const float* wsrc = p.dvw + ((blk0 + ce - 1) * Pp + ch) * kC + 4 * g4;
+      const f32x4 W[2] = {*reinterpret_cast<const f32x4*>(wsrc), *reinterpret_cast<const f32x4*>(wsrc + 16)};
+      gdr_store_end(dvrow, (ce - 1) * kC, len, q.L, W, g4);
+    }
+    // tokens behind the row's end
+    for (int64_t t = ce * kC + 4 * g4; t < q.L; t += 16) gdr_store4(dvrow, t, q.L, f32x4{0.f, 0.f, 0.f, 0.f});
   }
 }
 
@@ -224,7 +225,8 @@ struct Rows {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
       const int n = (tid + kThreads * j) >> 2;
-      if (kSome && n >= kRows) continue;
+      static_assert(kRows % 16 == 0, "a wave has 16 rows or none");
+      if (kSome && __builtin_amdgcn_readfirstlane(n) >= kRows) continue;
       uint16_t* dst = tile + n * kGdrRow + 8 * (tid & 3);
       raw[j].template put<kRows * kGdrRow>(dst, rows == kRows || n < rows ? ~0u : 0u);
     }
@@ -253,14 +255,6 @@ __device__ __forceinline__ f32x4 tile_four(const uint16_t* tile, int n, int t) {
   }
   return r;
 }
-
-// In both kernels below no branch that only some lanes of a wave take encloses or follows
-// live registers: every lane writes (the same value where one would do), addresses are
-// clamped.  At such a branch's end the compiler may save registers before it
-// re-enables the other lanes when it runs out of them.  (One remains: the stores of dQ and
-// dK where N is less than the tile, since a clamped row would be another lane's.  The
-// assembly of every variant has no copy between its end and the restored lanes; look
-// again after a change.)
 
 // One workgroup per (batch row, value head, chunk): the 32 x 32 products dV U^T, dY U^T
 // (64 value channels at a time), K K^T and Q K^T, lower tiles only.  Leaves M1 (columns
@@ -470,14 +464,19 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   const int nc = (int)(nl - cb < 0 ? 0 : nl - cb < kGdrBlk ? nl - cb : kGdrBlk);      // live chunks
   const int64_t tb = cb * kC, te = tb + kGdrBlk * kC < q.L ? tb + kGdrBlk * kC : q.L;
   const int n = 16 * w + i16;                              // this lane's key number
-  const int64_t nn = n < q.N ? n : q.N - 1;                // one that is there
 
   const T* krows = static_cast<const T*>(q.k) + b * q.k_stride + g * q.N * q.L;
   const T* qrows = static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L;
   const T* tail_k = static_cast<const T*>(p.tail_k) + bg * q.N * kC;
   const T* tail_q = static_cast<const T*>(p.tail_q) + bg * q.N * kC;
-  O* dqrow = static_cast<O*>(p.dq) + (bg * q.N + nn) * q.L;
-  O* dkrow = static_cast<O*>(p.dk) + (bg * q.N + nn) * q.L;
+  // this lane's row of dQ and dK (n < N) and its tokens of chunk c, worked out where it is used
+  // (not before the loops: that would hold registers over them)
+  auto drow = [&](int c) {
+    int own = n;
+    asm volatile("" : "+v"(own), "+s"(c));
+    return (bg * q.N + own) * q.L + (cb + c) * kC + 4 * g4;
+  };
+  O *dq = static_cast<O*>(p.dq), *dk = static_cast<O*>(p.dk);
 
   const int64_t Pp = (q.P + 63) / 64 * 64;
   const int64_t slabs = (q.P + kPS - 1) / kPS, turns = nc > 0 ? rep * slabs : 0;
@@ -489,6 +488,12 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
   float lrk, lrq;
   f32x4 S[kPT], D[kPT];                                    // S and dS: column n, rows of the value channels
   auto four = [&](const float* v, int rt) { return *reinterpret_cast<const f32x4*>(v + 16 * rt + 4 * g4); };
+
+  // dQ and dK of a wave with lanes past the last key number, and of the chunk of the row's end,
+  // are stored after the last turn; until then they take the place of the four first tiles of
+  // dS (of the chunk, last head and last slab) that this wave alone reads.
+  const bool split = 16 * w + 16 > q.N;
+  auto kept = [&](int64_t bl, int64_t p0) { return p.chunk_dS + (bl * Pp + p0) * kN + w * 256; };
 
   for (int64_t turn = 0; turn < turns; ++turn) {
     const int64_t h = g * rep + turn / slabs, bh = b * q.H + h, p0 = (turn % slabs) * kPS;
@@ -693,11 +698,21 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
             ak[rt] = four(rk, rt) * (ak[rt] - kh[rt] * sk4);
           }
         }
-        if (n < q.N) {
+        if (split || (cc + 1) * kC > len) {                // kept where this wave's dS was, stored last
+          int here = c;
+          asm volatile("" : "+s"(here));
+          float* at = kept(bl0 + here, p0);
 #pragma unroll
           for (int rt = 0; rt < 2; ++rt) {
-            gdr_store4(dqrow, cc * kC + 16 * rt + 4 * g4, q.L, aq[rt]);
-            gdr_store4(dkrow, cc * kC + 16 * rt + 4 * g4, q.L, ak[rt]);
+            lane_store(at + rt * 16 * kN, lane * 16u, aq[rt]);
+            lane_store(at + (2 + rt) * 16 * kN, lane * 16u, ak[rt]);
+          }
+        } else {
+          const int64_t at = drow(c);
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt) {
+            gdr_store_whole4(dq + at + 16 * rt, aq[rt]);
+            gdr_store_whole4(dk + at + 16 * rt, ak[rt]);
           }
         }
       }
@@ -729,14 +744,14 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         const int64_t tok = (cb + c) * kC + t, at = bh * q.L + (tok < len ? tok : len - 1);
         const float xr = gdr_load(static_cast<const T*>(q.delta) + at) + bias;
         const float br = gdr_load(static_cast<const T*>(q.beta) + at);
-        const float dd = dg * A * gdr_sigmoid(xr), bt = gdr_sigmoid(br), step = softplus(xr);
-        const float db = bt > 0.0f ? vec[32 + t] / bt * gdr_sigmoid(-br) : 0.0f;
+        const float bt = gdr_sigmoid(br), step = softplus(xr);
+        const float dd = dg * A * gdr_sigmoid(xr);
+        const float db = vec[32 + t] / (bt > 0.0f ? bt : 1.0f) * gdr_sigmoid(-br);     // (b = 0: 0 / 1)
         sA += tok < len ? dg * step : 0.0f;
         sb += tok < len ? dd : 0.0f;
-        if (lane < 32 && tok < len) {
-          gdr_store(static_cast<O*>(p.ddelta) + at, dd);
-          gdr_store(static_cast<O*>(p.dbeta) + at, db);
-        }
+        const int64_t at0 = bh * q.L + (cb + c) * kC, left = len - (cb + c) * kC;
+        gdr_store_within(static_cast<O*>(p.ddelta) + at0, left, t, dd);
+        gdr_store_within(static_cast<O*>(p.dbeta) + at0, left, t, db);
       }
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -759,6 +774,16 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
     if (nc == 0 && tid < 2) p.part[((b * p.n_blks + blk) * q.H + g * rep + hh) * 2 + tid] = 0.0f;
   }
   if (n < q.N) {
+    O *dqrow = dq + (bg * q.N + n) * q.L, *dkrow = dk + (bg * q.N + n) * q.L;
+    for (int c = 0; c < nc; ++c) {
+      if (!split && (cb + c + 1) * kC <= len) continue;
+      const float* src = kept(block_of(p, b, g * rep + rep - 1, cb + c), (slabs - 1) * kPS);
+      f32x4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const f32x4*>(src + j * 16 * kN + lane * 4);
+      gdr_store_end(dqrow, (cb + c) * kC, len, q.L, {x[0], x[1]}, g4);
+      gdr_store_end(dkrow, (cb + c) * kC, len, q.L, {x[2], x[3]}, g4);
+    }
     for (int64_t t = tb + nc * kC + 4 * g4; t < te; t += 16) {
       gdr_store4(dqrow, t, q.L, f32x4{0.f, 0.f, 0.f, 0.f});
       gdr_store4(dkrow, t, q.L, f32x4{0.f, 0.f, 0.f, 0.f});

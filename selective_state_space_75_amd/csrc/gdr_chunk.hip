@@ -101,8 +101,6 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
     }
     tk.put(Kt, tid);
     tq.put(Qt, tid);
-    tk.clear(Kt, tid);
-    tq.clear(Qt, tid);
   }
   __syncthreads();
   {
@@ -313,7 +311,8 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   const bool ident = kMode == kSummary && slice >= vslices;  // rows of the transition
   const int64_t ch0 = (ident ? slice - vslices : slice) * 64 + 16 * w, ch = ch0 + i16;
   const int64_t channels = ident ? q.N : q.P;
-  const bool mine = ch < channels;   // waves past the last channel run along on a channel that is there
+  const bool mine = ch < channels, some = ch0 < channels;
+  const int64_t mch = mine ? ch : channels - 1;              // lanes past the last channel run along on it
   const int64_t len = gdr_length(q, b);
   const int64_t c0 = seg * p.seg_chunks, c1 = c0 + p.seg_chunks < p.n_chunks ? c0 + p.seg_chunks : p.n_chunks;
   const int64_t live = (len + kC - 1) / kC, ce = live < c1 ? live : c1;
@@ -322,28 +321,25 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
   const T* qrows = static_cast<const T*>(q.q) + b * q.q_stride + g * q.N * q.L;
   const T* tail_k = static_cast<const T*>(p.tail_k) + (b * q.G + g) * q.N * kC;
   const T* tail_q = static_cast<const T*>(p.tail_q) + (b * q.G + g) * q.N * kC;
-  const int64_t vch = mine && !ident ? ch : 0;               // lanes without a channel read one that is there
+  const int64_t vch = ident ? 0 : mch;                       // the transition's rows read a value and drop it
   const T* vrow = static_cast<const T*>(q.v) + b * q.v_stride + (h * q.P + vch) * q.L + 4 * g4;
   const T* tail_v = static_cast<const T*>(p.tail_v) + (bh * q.P + vch) * kC + 4 * g4;
-  O* yrow = static_cast<O*>(q.y) + (bh * q.P + (mine && !ident ? ch : 0)) * q.L;
-  const bool values = mine && !ident;
+  O* yrow = static_cast<O*>(q.y) + (bh * q.P + vch) * q.L;
   const int64_t Pp = vslices * 64;
   (void)Pp;
 
   f32x4 S[kNT];
   {
     const float* src = nullptr;
-    if (mine) {
-      if (kMode != kSummary && p.S > 1) src = p.seg_start + ((bs * q.H + h) * q.P + ch) * q.N;
-      else if (kMode != kSummary && q.init) src = q.init + (bh * q.P + ch) * q.N;
-    }
+    if (kMode != kSummary && p.S > 1) src = p.seg_start + ((bs * q.H + h) * q.P + mch) * q.N;
+    else if (kMode != kSummary && q.init) src = q.init + (bh * q.P + mch) * q.N;
 #pragma unroll
     for (int tn = 0; tn < kNT; ++tn) {
       S[tn] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (src) S[tn] = gdr_load_state(src, 16 * tn + 4 * g4, q.N, q.state_vec);
       if (ident) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[tn][r] = (mine && 16 * tn + 4 * g4 + r == ch) ? 1.0f : 0.0f;
+        for (int r = 0; r < 4; ++r) S[tn][r] = 16 * tn + 4 * g4 + r == mch ? 1.0f : 0.0f;
       }
     }
   }
@@ -411,16 +407,15 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
       load_p(c0);
     }
     put(0);
-#pragma unroll
-    for (int buf = 0; buf < kBuf; ++buf) {
-      tk.clear(Kt[buf], tid);
-      if constexpr (kMode == kFull) tq.clear(Qt[buf], tid);
-    }
     __syncthreads();
   }
   bf16x8 sb[kNB][3];                                       // the state's operand parts
 #pragma unroll
   for (int kb = 0; kb < kNB; ++kb) gdr_split<3>(S[2 * kb], S[2 * kb + 1], sb[kb]);
+  auto end_of = [&](int buf) {
+    const int free = kBuf == 2 ? buf ^ 1 : 0;
+    return reinterpret_cast<float*>(w & 2 ? &Qt[free][0] : &Kt[free][0]) + (w & 1) * 512 + lane * 8;
+  };
   for (int64_t c = c0; c < ce; ++c) {
     const int buf = kBuf == 2 ? (int)((c - c0) & 1) : 0;
     const uint16_t* K = Kt[buf];
@@ -540,35 +535,41 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
       if constexpr (kMode == kFull) {
         load_vec(cn, 1, fq);
         load_p(cn);
-        if (values) {
+        if (some && (c + 1) * kC <= len) {
 #pragma unroll
-          for (int rt = 0; rt < 2; ++rt) {
-            if ((c + 1) * kC <= q.L) gdr_store_whole4(yrow + c * kC + 16 * rt + 4 * g4, Y[rt]);
-            else gdr_store4(yrow, c * kC + 16 * rt + 4 * g4, q.L, Y[rt]);
-          }
+          for (int rt = 0; rt < 2; ++rt) gdr_store_whole4(yrow + c * kC + 16 * rt + 4 * g4, Y[rt]);
+        }
+      }
+      if constexpr (kBuf == 1) __syncthreads();
+      if constexpr (kMode == kFull) {
+        if ((c + 1) * kC > len) {                            // the row's end: kept in a free tile, stored last
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt) *reinterpret_cast<f32x4*>(end_of(buf) + 4 * rt) = Y[rt];
         }
       }
     }
-    if constexpr (kBuf == 1) __syncthreads();
-    put(kBuf == 2 ? buf ^ 1 : 0);
-    __syncthreads();
+    if (c + 1 < ce) {
+      put(kBuf == 2 ? buf ^ 1 : 0);
+      __syncthreads();
+    }
   }
 
   if constexpr (kMode == kFull) {
+    if (q.final_state && seg == p.S - 1)
+      gdr_store_rows(q.final_state + (bh * q.P + ch0) * q.N, q.P - ch0, q.N, q.state_vec, S, lane);
     // tokens of this segment behind the row's end
-    if (values) {
+    if (mine) {
+      if (ce > c0 && ce * kC > len) {
+        const float* kept = end_of(kBuf == 2 ? (int)((ce - 1 - c0) & 1) : 0);
+        gdr_store_end(yrow, (ce - 1) * kC, len, q.L,
+                      {*reinterpret_cast<const f32x4*>(kept), *reinterpret_cast<const f32x4*>(kept + 4)}, g4);
+      }
       const int64_t from = (ce > c0 ? ce : c0) * kC, to = c1 * kC < q.L ? c1 * kC : q.L;
       for (int64_t t = from + 4 * g4; t < to; t += 16) gdr_store4(yrow, t, to, f32x4{0.f, 0.f, 0.f, 0.f});
     }
-    if (q.final_state && seg == p.S - 1 && mine) {
-      float* dst = q.final_state + (bh * q.P + ch) * q.N;
-#pragma unroll
-      for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
-    }
-  } else if (kMode == kSummary && mine) {
-    float* dst = ident ? p.seg_M + ((bs * q.H + h) * q.N + ch) * q.N : p.seg_h + ((bs * q.H + h) * q.P + ch) * q.N;
-#pragma unroll
-    for (int tn = 0; tn < kNT; ++tn) gdr_store_state(dst, 16 * tn + 4 * g4, q.N, q.state_vec, S[tn]);
+  } else if (kMode == kSummary) {
+    float* dst = ident ? p.seg_M + ((bs * q.H + h) * q.N + ch0) * q.N : p.seg_h + ((bs * q.H + h) * q.P + ch0) * q.N;
+    gdr_store_rows(dst, channels - ch0, q.N, q.state_vec, S, lane);
   }
 }
 

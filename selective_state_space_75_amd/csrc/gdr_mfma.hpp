@@ -26,6 +26,8 @@
 
 namespace mamba {
 
+constexpr int kC = kGdrChunk;
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -195,6 +197,11 @@ __device__ __forceinline__ V lane_load(const T* base, uint32_t off) {
   return *reinterpret_cast<const V*>(reinterpret_cast<const char*>(base) + off);
 }
 
+template <typename V, typename T>
+__device__ __forceinline__ void lane_store(T* base, uint32_t off, V x) {
+  *reinterpret_cast<V*>(reinterpret_cast<char*>(base) + off) = x;
+}
+
 // Four consecutive numbers of a row, kept as they are stored until they are used (a
 // conversion would be waited for at the load).
 struct GdrFour16 {
@@ -235,22 +242,74 @@ __device__ __forceinline__ void gdr_store4(float* row, int64_t t, int64_t end, f
     if (t + j < end) row[t + j] = x[j];
 }
 
+// A chunk's results x (lane group g: tokens 16 rt + 4 g .. + 3) of the chunk from token t that
+// the row of `len` tokens ends in: zeros from `len` on, nothing from L on.
+template <typename O>
+__device__ __forceinline__ void gdr_store_end(O* row, int64_t t, int64_t len, int64_t L, const f32x4 (&x)[2], int g) {
+#pragma unroll
+  for (int rt = 0; rt < 2; ++rt) {
+    const int64_t at = t + 16 * rt + 4 * g;
+    f32x4 v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = at + r < len ? x[rt][r] : 0.0f;
+    gdr_store4(row, at, L, v);
+  }
+}
+
+// Between the first and the last product of the chain, adjoint, pair and grad kernels, which
+// use nearly all of their registers or more, no branch is taken by some lanes of a wave only:
+// at such a branch's end the compiler may copy registers before it re-enables the other
+// lanes.  Lanes with nothing of their own read clamped addresses and write what another
+// lane writes, or are dropped by the bounds of a buffer.  tests/test_gdr_codegen.py looks at
+// the compiled code.
+
 // Four numbers n .. n + 3 of a state row of N (zeros behind it).
 __device__ __forceinline__ f32x4 gdr_load_state(const float* row, int64_t n, int64_t N, bool vec) {
-  if (vec) return n < N ? *reinterpret_cast<const f32x4*>(row + n) : f32x4{0.f, 0.f, 0.f, 0.f};
   f32x4 r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = n + j < N ? row[n + j] : 0.0f;
-  return r;
-}
-__device__ __forceinline__ void gdr_store_state(float* row, int64_t n, int64_t N, bool vec, f32x4 x) {
   if (vec) {
-    if (n < N) *reinterpret_cast<f32x4*>(row + n) = x;
-    return;
+    r = *reinterpret_cast<const f32x4*>(row + (n < N ? n : 0));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = row[n + j < N ? n + j : N - 1];
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (n + j < N) row[n + j] = x[j];
+  for (int j = 0; j < 4; ++j) r[j] = n + j < N ? r[j] : 0.0f;
+  return r;
+}
+
+// Number i of `count` consecutive ones at `row`; i >= count is dropped.
+__device__ __forceinline__ void gdr_store_within(float* row, int64_t count, int i, float x) {
+  const auto buf = __builtin_amdgcn_make_buffer_rsrc(row, 0, (int)(count < kC ? count : kC) * 4, 0x00020000);
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), buf, 4 * i, 0, 0);
+}
+__device__ __forceinline__ void gdr_store_within(uint16_t* row, int64_t count, int i, float x) {
+  const auto buf = __builtin_amdgcn_make_buffer_rsrc(row, 0, (int)(count < kC ? count : kC) * 2, 0x00020000);
+  __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(x), buf, 2 * i, 0, 0);
+}
+
+// A wave's 16 rows of state (kNT tiles of 16 numbers), the first `count` of which are there
+// (0 or less: none), to consecutive rows of N at `rows`.
+template <int kNT>
+__device__ __forceinline__ void gdr_store_rows(float* rows, int64_t count, int64_t N, bool vec, const f32x4 (&S)[kNT],
+                                               int lane) {
+  constexpr uint32_t kDrop = 0x80000000u;                  // past the buffer's end: not written
+  const int bytes = (int)((count < 0 ? 0 : count < 16 ? count : 16) * N * 4);
+  const auto buf = __builtin_amdgcn_make_buffer_rsrc(rows, 0, bytes, 0x00020000);
+  const int i = lane & 15, g = lane >> 4, width = (int)N;
+#pragma unroll
+  for (int tn = 0; tn < kNT; ++tn) {
+    const int n = 16 * tn + 4 * g;
+    const uint32_t at = (uint32_t)(i * width + n) * 4u;
+    if (vec) {
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[tn]), buf, n < width ? at : kDrop, 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (float)S[tn][j]), buf,
+                                              n + j < width ? at + 4u * j : kDrop, 0, 0);
+    }
+  }
 }
 
 // The chunk of 32 tokens of a key head, staged by a 256-thread workgroup: kN rows
@@ -265,7 +324,7 @@ struct GdrTile {
   using Raw = typename GdrIn<T>::Raw;
   int64_t row[kPieces];
   Raw raw[kPieces];
-  bool ok[kPieces];            // false for rows past N: those are zeroed once (clear) and left alone
+  bool ok[kPieces];            // false for rows past N: put as zeros
   __device__ __forceinline__ void init(int64_t N, int tid) {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
@@ -287,21 +346,13 @@ struct GdrTile {
   __device__ __forceinline__ void put(uint16_t* tile, int tid) const {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j)
-      if (ok[j]) raw[j].template put<kPlane>(tile + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3));
+      raw[j].template put<kPlane>(tile + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3), ok[j] ? ~0u : 0u);
   }
-  __device__ __forceinline__ void clear(uint16_t* tile, int tid) const {
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j)
-      if (!ok[j])
-#pragma unroll
-        for (int s = 0; s < kParts; ++s)
-          gdr_put16(tile + s * kPlane + ((tid >> 2) + 64 * j) * kGdrRow + 8 * (tid & 3), make_uint4(0, 0, 0, 0));
-  }
-  // as they were loaded, into dense rows of 32
+  // as they were loaded, into dense rows of 32 (row N - 1 again for rows past it)
   __device__ __forceinline__ void save(T* rows, int tid) const {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j)
-      if (ok[j]) raw[j].save(rows + row[j] * kGdrChunk + 8 * (tid & 3));
+      raw[j].save(rows + row[j] * kGdrChunk + 8 * (tid & 3));
   }
 };
 
@@ -330,8 +381,6 @@ __device__ __forceinline__ void gdr_frags(const uint16_t* tile, int row0, int co
 #pragma unroll
   for (int s = 0; s < GdrIn<T>::kParts; ++s) f[s] = gdr_frag<kGdrRow>(tile + s * kN * kGdrRow, row0, col0, lane);
 }
-
-constexpr int kC = kGdrChunk;
 
 // Block (b, h, c) of the preparation's outputs; kBwd: nine planes, else 3 + p_parts.
 __device__ __forceinline__ int64_t block_of(const GdrChunkParams& p, int64_t b, int64_t h, int64_t c) {
