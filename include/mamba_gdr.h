@@ -36,6 +36,11 @@
  * B*G*N*L < 2^46.  in_dtype and the output dtypes may each be MAMBA_F32 or
  * MAMBA_BF16.  Alignment: every array to its element size (16 bytes, and sizes that
  * are multiples of a vector, select vector accesses); workspaces 256 bytes.
+ * A NaN or an infinity among the inputs of a token leaves the outputs of the tokens
+ * before it as they are; from that token on, every output and state that it reaches
+ * is NaN or infinite.  (An infinite delta or beta is a number: its softplus or sigmoid's
+ * limit.  Numbers beyond 3.38e38 count as infinite.)  In the backward pass any gradient
+ * of such a batch row may be NaN, dA and ddelta_bias with it.
  * State, gates and sums are fp32 or better; the results are deterministic
  * (sums in a fixed order, no atomics) and do not depend on the other rows of the batch.
  */

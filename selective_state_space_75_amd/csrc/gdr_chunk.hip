@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
     const float rk = rlen[0][c32], rq = rlen[1][c32] * q.scale;
     const float dec = hw_exp2((float)cum);
     if (half == 0) {
-      vec[c32] = dec * rk;
+      vec[c32] = beta == beta ? dec * rk : beta;           // a NaN shows in the token's residual
       vec[32 + c32] = dec * rq;
       vec[64 + c32] = hw_exp2((float)(last - cum)) * rk;
       if (c32 == 0) vec[96] = hw_exp2((float)last);
@@ -262,7 +262,8 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
     }
     wave_sync();
 #pragma unroll
-    for (int m = 0; m < 16; ++m) M[(2 * m + half) * 33 + c32] = x[m] * beta;
+    for (int m = 0; m < 16; ++m)     // (above the diagonal zero, also times a NaN)
+      M[(2 * m + half) * 33 + c32] = 2 * m + half >= c32 ? x[m] * beta : 0.0f;
     wave_sync();
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
@@ -290,6 +291,48 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(GdrChunkParams p) {
 // kStates (for the backward pass): no queries; keeps every chunk's U and the state
 // entering every block of kGdrBlk chunks.
 enum ChainMode { kFull = 0, kSummary = 1, kStates = 2 };
+
+// Takes a channel's residuals R (parts rb) that are not finite out of a chunk: U = T R again
+// with zeros from the first such token on, U itself zero from it on (so that the query matrix
+// gives the tokens before it what is theirs), the factors of its queries and its state NaN.
+template <int kNT>
+__device__ __forceinline__ void gdr_from_first(const bf16x8 (&tf)[2][3], const bf16x8 (&rb)[3], f32x4 (&U)[2],
+                                               f32x4 (&fq)[2], f32x4 (&S)[kNT], int g4) {
+  const float nan = __builtin_nanf("");
+  auto token = [&](int e) { return (e < 4 ? 0 : 16) + 4 * g4 + (e & 3); };
+  const uint4 top = __builtin_bit_cast(uint4, rb[0]);
+  const uint32_t tw[4] = {top.x, top.y, top.z, top.w};
+  int first = kC;
+#pragma unroll
+  for (int e = 7; e >= 0; --e)
+    if ((tw[e >> 1] >> (16 * (e & 1)) & 0x7f80u) == 0x7f80u) first = token(e);
+  first = min(first, __shfl_xor(first, 16));
+  first = min(first, __shfl_xor(first, 32));
+  bf16x8 part[3];
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const uint4 x = __builtin_bit_cast(uint4, rb[s]);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] &= (token(2 * j) < first ? 0xffffu : 0u) | (token(2 * j + 1) < first ? 0xffff0000u : 0u);
+    part[s] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  U[0] = U[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  gdr_mma_rows<3>(tf, part, U);
+#pragma unroll
+  for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool before = 16 * rt + 4 * g4 + r < first;
+      U[rt][r] = before ? U[rt][r] : 0.0f;
+      fq[rt][r] = before ? fq[rt][r] : nan;
+    }
+#pragma unroll
+  for (int tn = 0; tn < kNT; ++tn)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[tn][r] = first < kC ? nan : S[tn][r];
+}
 
 template <typename T, typename O, int kN, int kMode>
 __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
@@ -486,6 +529,12 @@ __global__ __launch_bounds__(256, 2) void gdr_chain_kernel(GdrChunkParams p) {
         __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (kMode == kFull) {
+        // A residual that is not finite makes every update of its channel NaN, the tokens
+        // before it included (T holds zeros for them, and 0 times it is NaN): rare, found in
+        // any one of the updates.
+        if (__builtin_expect(__ballot(U[0][0] != U[0][0]) != 0, 0)) gdr_from_first<kNT>(tf, rb, U, fq, S, g4);
+      }
       load_t(cn);
       if constexpr (kMode == kStates) {
         float* dst = p.u + ((blk0 + c) * Pp + ch) * kC + 4 * g4;
