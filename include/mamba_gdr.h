@@ -33,7 +33,9 @@
  *                 the one after lengths[b] tokens.
  *
  * Sizes: 1 <= N <= 128; B, H, G, P, L >= 1; H a multiple of G; B*H*P*L and
- * B*G*N*L < 2^46.  in_dtype and the output dtypes may each be MAMBA_F32 or
+ * B*G*N*L < 2^46; and no launch of 2^32 threads or more: B*H*ceil(P/4) < 2^26 for one token (four times
+ * that with vector accesses); B*H*ceil(P/64)*ceil(L/32) < 2^23 is enough for sequences.
+ * in_dtype and the output dtypes may each be MAMBA_F32 or
  * MAMBA_BF16.  Alignment: every array to its element size (16 bytes, and sizes that
  * are multiples of a vector, select vector accesses); workspaces 256 bytes.
  * A NaN or an infinity among the inputs of a token leaves the outputs of the tokens

@@ -22,7 +22,9 @@
  *            unspecified.
  *   codes  : (n_slots, n) int8.   exps : (n_slots, ceil(n / 32)) uint8.
  *
- * Sizes: rows, n, n_slots >= 1; rows * n < 2^46.  Alignment: element size
+ * Sizes: rows, n, n_slots >= 1; rows * n < 2^46, and fewer than 2^24 workgroups of 1024
+ * consecutive numbers of a row (4096 for vector accesses and rows * n of 2^23 or more), so that
+ * a launch has fewer than 2^32 threads.  Alignment: element size
  * (16 bytes and n % 4 == 0 select vector accesses).  No workspace.
  */
 #ifndef MAMBA_STATE_CACHE_H_

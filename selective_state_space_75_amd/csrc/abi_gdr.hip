@@ -12,7 +12,6 @@ namespace {
 using mamba::Dt;
 
 constexpr int64_t kMaxElems = int64_t(1) << 46;
-constexpr int64_t kMaxGrid = int64_t(1) << 31;
 
 bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 bool dtype_ok(int t) { return t == MAMBA_F32 || t == MAMBA_BF16; }
@@ -150,21 +149,27 @@ GdrBwdPlan make_gdr_bwd_plan(int64_t B, int64_t H, int64_t G, int64_t P, int64_t
   return q;
 }
 
-// Workgroups of the largest launch of a plan.
-bool gdr_grid_ok(const GdrPlan& q, int64_t B, int64_t H, int64_t G, int64_t P, int64_t N) {
-  if (!q.chunk) return B * H * ((P + 3) / 4) / 4 + 1 < kMaxGrid;
-  const int64_t slices = (P + 63) / 64 + (q.S > 1 ? (N + 63) / 64 : 0);
-  return B * G < kMaxGrid / q.n_chunks && B * H < kMaxGrid / (q.S * slices) && B * H < kMaxGrid / ((P + 15) / 16);
+// Whether every launch of a pass in chunks is one: preparation, summaries and full chain, carries.
+bool gdr_chunk_fits(const GdrPlan& q, int64_t B, int64_t H, int64_t G, int64_t P, int64_t N) {
+  const int64_t vs = (P + 63) / 64, is = (N + 63) / 64;
+  return mamba::launch_fits(B * G * q.n_chunks, 256) && mamba::launch_fits(B * q.S * H * vs, 256) &&
+         (q.S == 1 || (mamba::launch_fits(B * (q.S - 1) * H * (vs + is), 256) &&
+                       mamba::launch_fits(B * H * ((P + 15) / 16), N > 64 ? 512 : 256)));
+}
+// The same for the backward pass: preparation, chains, pairs, grads, sums.
+bool gdr_bwd_fits(const GdrBwdPlan& q, int64_t B, int64_t H, int64_t G, int64_t P, int64_t N) {
+  return mamba::launch_fits(B * G * q.n_chunks, 256) && mamba::launch_fits(B * H * ((P + 63) / 64), 256) &&
+         mamba::launch_fits(B * H * q.n_chunks, 256) && mamba::launch_fits(B * G * q.n_blks, N > 64 ? 512 : 256) &&
+         mamba::launch_fits(H, 64);
 }
 
-int check_cache(const void* state, const int32_t* slots, const void* codes, const void* exps, int64_t rows, int64_t n,
-                int64_t n_slots, int dtype) {
+int check_cache(const mamba::CacheParams& p, int dtype) {
   if (!dtype_ok(dtype)) return MAMBA_ERR_DTYPE;
-  if (!product_ok(rows, n, 1) || !product_ok(n_slots, n, 1)) return MAMBA_ERR_SHAPE;
-  if (!slots && n_slots < rows) return MAMBA_ERR_SHAPE;
-  if (!state || !codes || !exps) return MAMBA_ERR_NULL;
-  if (!aligned(state, width(dtype)) || (slots && !aligned(slots, 4))) return MAMBA_ERR_ALIGN;
-  if (n > (kMaxGrid - 1) / rows * 1024 - 1024) return MAMBA_ERR_SHAPE;
+  if (!product_ok(p.rows, p.n, 1) || !product_ok(p.n_slots, p.n, 1)) return MAMBA_ERR_SHAPE;
+  if (!p.slots && p.n_slots < p.rows) return MAMBA_ERR_SHAPE;
+  if (!p.state || !p.codes || !p.exps) return MAMBA_ERR_NULL;
+  if (!mamba::launch_fits(mamba::cache_workgroups(p), 256)) return MAMBA_ERR_SHAPE;
+  if (!aligned(p.state, width(dtype)) || (p.slots && !aligned(p.slots, 4))) return MAMBA_ERR_ALIGN;
   return MAMBA_OK;
 }
 
@@ -173,7 +178,7 @@ mamba::CacheParams cache_params(void* state, const int32_t* slots, int8_t* codes
   mamba::CacheParams p{};
   p.state = state; p.slots = slots; p.codes = codes; p.exps = exps;
   p.rows = rows; p.n = n; p.n_slots = n_slots;
-  p.groups = (n + 31) / 32;
+  p.groups = n / 32 + (n % 32 > 0);
   p.vec = n % 4 == 0 && aligned(state, dtype == MAMBA_BF16 ? 8 : 16) && aligned(codes, 4);
   return p;
 }
@@ -197,20 +202,21 @@ int mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* delta
   const int st = check_gdr(B, H, G, P, N, L, q_stride, k_stride, v_stride, in_dtype, out_dtype, flags);
   if (st != MAMBA_OK) return st;
   if (!q || !k || !v || !delta || !beta || !A || !y) return MAMBA_ERR_NULL;
+  const GdrPlan plan = make_gdr_plan(B, H, G, P, N, L, width(in_dtype));
+  mamba::GdrParams p = gdr_params(q, k, v, delta, beta, A, delta_bias, B, H, G, P, N, L, q_stride, k_stride, v_stride,
+                                  scale, flags);
+  p.init = initial_state; p.lengths = lengths; p.y = y; p.final_state = final_state;
+  p.state_vec = N % 4 == 0 && (!initial_state || aligned(initial_state, 16)) && (!final_state || aligned(final_state, 16));
+  if (plan.chunk ? !gdr_chunk_fits(plan, B, H, G, P, N) : !mamba::launch_fits(mamba::gdr_step_workgroups(p), 256))
+    return MAMBA_ERR_SHAPE;
   for (const void* ptr : {q, k, v, delta, beta})
     if (!aligned(ptr, width(in_dtype))) return MAMBA_ERR_ALIGN;
   if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
   for (const void* ptr : {(const void*)A, (const void*)delta_bias, (const void*)initial_state, (const void*)lengths,
                           (const void*)final_state})
     if (ptr && !aligned(ptr, 4)) return MAMBA_ERR_ALIGN;
-  const GdrPlan plan = make_gdr_plan(B, H, G, P, N, L, width(in_dtype));
-  if (!gdr_grid_ok(plan, B, H, G, P, N)) return MAMBA_ERR_SHAPE;
   if (plan.bytes && (!workspace || workspace_bytes < plan.bytes)) return MAMBA_ERR_WORKSPACE;
   if (plan.bytes && !aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
-  mamba::GdrParams p = gdr_params(q, k, v, delta, beta, A, delta_bias, B, H, G, P, N, L, q_stride, k_stride, v_stride,
-                                  scale, flags);
-  p.init = initial_state; p.lengths = lengths; p.y = y; p.final_state = final_state;
-  p.state_vec = N % 4 == 0 && (!initial_state || aligned(initial_state, 16)) && (!final_state || aligned(final_state, 16));
   if (plan.chunk) {
     mamba::GdrChunkParams c{};
     c.g = p;
@@ -258,7 +264,7 @@ int mamba_gdr_bwd(const void* q, const void* k, const void* v, const void* delta
                           (const void*)dinitial_state})
     if (ptr && !aligned(ptr, 4)) return MAMBA_ERR_ALIGN;
   const GdrBwdPlan plan = make_gdr_bwd_plan(B, H, G, P, N, L, width(in_dtype), width(grad_dtype));
-  if (B * H >= kMaxGrid / plan.n_chunks || B * H >= kMaxGrid / ((P + 63) / 64)) return MAMBA_ERR_SHAPE;
+  if (!gdr_bwd_fits(plan, B, H, G, P, N)) return MAMBA_ERR_SHAPE;
   if (!workspace || workspace_bytes < plan.bytes) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
   mamba::GdrChunkParams c{};
@@ -297,16 +303,16 @@ int mamba_gdr_update(float* state, const int32_t* slots, const void* q, const vo
   if (st != MAMBA_OK) return st;
   if (!product_ok(n_slots, H * P, N) || (!slots && n_slots < B)) return MAMBA_ERR_SHAPE;
   if (!state || !q || !k || !v || !delta || !beta || !A || !y) return MAMBA_ERR_NULL;
+  mamba::GdrParams p = gdr_params(q, k, v, delta, beta, A, delta_bias, B, H, G, P, N, 1, q_stride, k_stride, v_stride,
+                                  scale, flags);
+  p.init = state; p.final_state = state; p.slots = slots; p.n_slots = n_slots; p.y = y;
+  p.state_vec = N % 4 == 0 && aligned(state, 16);
+  if (!mamba::launch_fits(mamba::gdr_step_workgroups(p), 256)) return MAMBA_ERR_SHAPE;
   for (const void* ptr : {q, k, v, delta, beta})
     if (!aligned(ptr, width(in_dtype))) return MAMBA_ERR_ALIGN;
   if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
   for (const void* ptr : {(const void*)A, (const void*)delta_bias, (const void*)state, (const void*)slots})
     if (ptr && !aligned(ptr, 4)) return MAMBA_ERR_ALIGN;
-  if (B * H * ((P + 3) / 4) / 4 + 1 >= kMaxGrid) return MAMBA_ERR_SHAPE;
-  mamba::GdrParams p = gdr_params(q, k, v, delta, beta, A, delta_bias, B, H, G, P, N, 1, q_stride, k_stride, v_stride,
-                                  scale, flags);
-  p.init = state; p.final_state = state; p.slots = slots; p.n_slots = n_slots; p.y = y;
-  p.state_vec = N % 4 == 0 && aligned(state, 16);
   return mamba::launch_gdr_step(p, dt_of(in_dtype), dt_of(out_dtype), stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 
@@ -319,18 +325,18 @@ int mamba_gdr_set_test_knobs(int kernel, int64_t segments) {
 
 int mamba_state_cache_write(const void* state, const int32_t* slots, int8_t* codes, uint8_t* exps, int64_t rows,
                             int64_t n, int64_t n_slots, mamba_dtype_t dtype, hipStream_t stream) {
-  const int st = check_cache(state, slots, codes, exps, rows, n, n_slots, dtype);
-  if (st != MAMBA_OK) return st;
   const mamba::CacheParams p = cache_params(const_cast<void*>(state), slots, codes, exps, rows, n, n_slots, dtype);
+  const int st = check_cache(p, dtype);
+  if (st != MAMBA_OK) return st;
   return mamba::launch_state_cache(p, dt_of(dtype), true, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 
 int mamba_state_cache_read(const int8_t* codes, const uint8_t* exps, const int32_t* slots, void* state, int64_t rows,
                            int64_t n, int64_t n_slots, mamba_dtype_t dtype, hipStream_t stream) {
-  const int st = check_cache(state, slots, codes, exps, rows, n, n_slots, dtype);
-  if (st != MAMBA_OK) return st;
   const mamba::CacheParams p = cache_params(state, slots, const_cast<int8_t*>(codes), const_cast<uint8_t*>(exps), rows,
                                             n, n_slots, dtype);
+  const int st = check_cache(p, dtype);
+  if (st != MAMBA_OK) return st;
   return mamba::launch_state_cache(p, dt_of(dtype), false, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 

@@ -132,14 +132,13 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrParams p) {
 
 template <typename T, typename O, int kE, bool kVec, int kSets>
 hipError_t step_launch(const GdrParams& p, hipStream_t s) {
-  const int64_t waves = p.B * p.H * ((p.P + 4 * kSets - 1) / (4 * kSets));
-  hipLaunchKernelGGL((gdr_step_kernel<T, O, kE, kVec, kSets>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((gdr_step_kernel<T, O, kE, kVec, kSets>), dim3((unsigned)gdr_step_workgroups(p)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T, typename O>
 hipError_t step_t(const GdrParams& p, hipStream_t s) {
-  const bool wide = p.N > 64, many = p.B * p.H * p.P >= 16 * 4096;
+  const bool wide = p.N > 64, many = gdr_step_sets(p) == 4;
   if (!p.state_vec) return wide ? step_launch<T, O, 8, false, 1>(p, s) : step_launch<T, O, 4, false, 1>(p, s);
   if (wide) return many ? step_launch<T, O, 8, true, 4>(p, s) : step_launch<T, O, 8, true, 1>(p, s);
   return many ? step_launch<T, O, 4, true, 4>(p, s) : step_launch<T, O, 4, true, 1>(p, s);

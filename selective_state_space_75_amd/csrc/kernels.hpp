@@ -222,6 +222,24 @@ struct CacheParams {
   int vec;                  // n % 4 == 0 and aligned for four numbers at a time
 };
 
+// Whether a launch of this many workgroups is one: HIP takes fewer than 2^32 threads in all.
+inline bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups <= int64_t(0xffffffff) / threads; }
+
+// Token by token: sets of four state rows per wave, and workgroups of 256 threads.  Four sets
+// (more independent loads per wave) once there are rows enough for every wave slot.
+inline int gdr_step_sets(const GdrParams& p) { return p.state_vec && p.B * p.H * p.P >= 16 * 4096 ? 4 : 1; }
+inline int64_t gdr_step_workgroups(const GdrParams& p) {
+  const int64_t rows = 4 * gdr_step_sets(p);
+  return (p.B * p.H * ((p.P + rows - 1) / rows) + 3) / 4;
+}
+
+// State cache: pieces of four numbers per thread (csrc/state_cache.hip), and workgroups of 256.
+inline int cache_pieces(const CacheParams& p) { return p.vec && p.rows * (p.n / 4096) >= 2048 ? 4 : 1; }
+inline int64_t cache_workgroups(const CacheParams& p) {
+  const int64_t numbers = 1024 * cache_pieces(p);
+  return p.rows * ((p.n + numbers - 1) / numbers);
+}
+
 // Each returns hipSuccess or the launch error.
 hipError_t launch_scan_full(const ScanParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_scan_summary(const ScanParams& p, Dt in, hipStream_t s);

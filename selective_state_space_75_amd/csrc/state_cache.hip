@@ -163,7 +163,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(CacheParams p) {
 
 template <typename T, bool kVec, int kU>
 hipError_t launch_u(const CacheParams& p, bool write, hipStream_t s) {
-  const int64_t wgs = p.rows * ((p.n + 1024 * kU - 1) / (1024 * kU));
+  const int64_t wgs = cache_workgroups(p);
   if (write)
     hipLaunchKernelGGL((cache_write_kernel<T, kVec, kU>), dim3((unsigned)wgs), dim3(256), 0, s, p);
   else
@@ -173,8 +173,7 @@ hipError_t launch_u(const CacheParams& p, bool write, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_t(const CacheParams& p, bool write, hipStream_t s) {
-  const bool many = p.rows * (p.n / 4096) >= 2048;
-  if (p.vec) return many ? launch_u<T, true, 4>(p, write, s) : launch_u<T, true, 1>(p, write, s);
+  if (p.vec) return cache_pieces(p) == 4 ? launch_u<T, true, 4>(p, write, s) : launch_u<T, true, 1>(p, write, s);
   return launch_u<T, false, 1>(p, write, s);
 }
 
