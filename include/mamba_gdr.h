@@ -43,8 +43,12 @@
  * is NaN or infinite.  (An infinite delta or beta is a number: its softplus or sigmoid's
  * limit.  Numbers beyond 3.38e38 count as infinite.)  In the backward pass any gradient
  * of such a batch row may be NaN, dA and ddelta_bias with it.
- * State, gates and sums are fp32 or better; the results are deterministic
- * (sums in a fixed order, no atomics) and do not depend on the other rows of the batch.
+ * State, gates and sums are fp32 or better.  The results are deterministic (sums in a
+ * fixed order, no atomics): the same call gives the same bits, and what the other rows of
+ * the batch hold has no influence on a row.  How many rows there are has: in mamba_gdr_fwd
+ * B, like every other size, takes part in the choice between token by token and chunks
+ * and of the segments of L, and those agree to fp32 rounding only.  mamba_gdr_update and
+ * mamba_gdr_bwd give a row the same bits in a batch of any size.
  */
 #ifndef MAMBA_GDR_H_
 #define MAMBA_GDR_H_

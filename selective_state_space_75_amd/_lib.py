@@ -588,7 +588,8 @@ def gdr_fwd(q, k, v, delta, beta, A, delta_bias=None, *, groups=None, initial_st
     q, k: (B, G*N, L); v: (B, H*P, L); delta, beta: (B, H, L), raw; A, delta_bias: (H)
     fp32.  groups = G (default H) key heads serve the H heads of delta.  q, k and v may be
     channel ranges of a wider tensor.  initial_state: (B, H*P, N) fp32; lengths: (B)
-    int32, tokens per row; scale: default N**-0.5.
+    int32, tokens per row; scale: default N**-0.5.  The number of rows B takes part in the
+    choice of the kernel: a row alone and in a batch agrees to fp32 rounding.
 
     Returns y (B, H*P, L), or (y, final_state (B, H*P, N) fp32) when return_final_state.
     """
