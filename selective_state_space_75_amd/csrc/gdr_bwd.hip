@@ -8,7 +8,7 @@
 //   M1 = s tril(D o dY U^T),  M2 = stril(D o dV U^T)
 //   dQ  = s exp(G) dY S0 + M1 K
 //   dK  = E U dS + M1^T Q - (M2 + M2^T) K - exp(G) dV S0
-//   dbeta_raw_t = (dV_t . U_t) (1 - b_t) / b_t         (u = b (v - p), dV = b du)
+//   dbeta_raw_t = (dV_t . U_t) / b_t (1 - b_t)         (u = b (v - p), dV = b du)
 // The gradient of token t's log decay is everything that passes from before t to t
 // or after it:
 //   dg_t = sum_(i >= t > j) [M1_ij q_i.k_j - M2_ij k_i.k_j] + sum_(i >= t) X_i
@@ -259,7 +259,7 @@ __device__ __forceinline__ f32x4 tile_four(const uint16_t* tile, int n, int t) {
 // One workgroup per (batch row, value head, chunk): the 32 x 32 products dV U^T, dY U^T
 // (64 value channels at a time), K K^T and Q K^T, lower tiles only.  Leaves M1 (columns
 // times 1/|k|), M1^T (times 1/|q|) and -(M2 + M2^T) (times 1/|k|) as operand planes of
-// the products with K and Q, and per token the pairs' part of dg and dV_t . U_t.
+// the products with K and Q, and per token the pairs' part of dg and dV_t . U_t / b_t.
 template <typename T, typename O, int kN>
 __global__ __launch_bounds__(256) void gdr_pair_kernel(GdrChunkParams p) {
   constexpr int kParts = GdrIn<T>::kParts, kGParts = GdrIn<O>::kParts, kPS = 64;
@@ -293,12 +293,15 @@ __global__ __launch_bounds__(256) void gdr_pair_kernel(GdrChunkParams p) {
     ldv.load_dense(p.dvw + (bl * Pp + p0) * kC, tid);
     ldu.load_dense(p.u + (bl * Pp + p0) * kC, tid);
   };
+  float braw;
   {
     Rows<T, kN, 256> ldk, ldq;
     ldk.load(sk.at, sk.stride, q.N, tid);
     ldq.load(sq.at, sq.stride, q.N, tid);
     const double lcum = lane_load<double>(vec + 192, (lane & 31) * 8);
     const float lrk = lane_load<float>(vec + 128, (lane & 31) * 4), lrq = lane_load<float>(vec + 160, (lane & 31) * 4);
+    const int64_t tok = c * kC + (lane & 31);
+    braw = gdr_load(static_cast<const T*>(q.beta) + bh * q.L + (tok < len ? tok : len - 1));
     load(0);
     ldk.put(Kt, (int)q.N, tid);
     ldq.put(Qt, (int)q.N, tid);
@@ -430,7 +433,23 @@ __global__ __launch_bounds__(256) void gdr_pair_kernel(GdrChunkParams p) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) s1 += m[3][j * 33 + 16 * half + k];
     s1 += __shfl_xor(s1, 32);
-    vec[lane] = half ? dvu[j] : s1;                        // over the factors of k and q
+    const float bt = gdr_sigmoid(braw);
+    float ratio = dvu[j] / (bt > 0.0f ? bt : 1.0f);        // dV_t . U_t / b_t (b = 0: 0 / 1)
+    // dV and U each carry b, and the matrix cores drop what is below 2^-126: their product is
+    // gone below b = 2^-63, its third parts (2^-16) below 2^-55.  From 2^-40 on, which leaves 30
+    // bits for the sizes of dV / b and U / b, it is summed again with both times 2^-e, b = m 2^e.
+    if (__builtin_expect(__ballot(bt > 0.0f && bt < 0x1p-40f) != 0, 0)) {
+      const uint32_t e = __builtin_bit_cast(uint32_t, bt) >> 23;
+      const float up = __builtin_bit_cast(float, (254u - e) << 23), down = __builtin_bit_cast(float, e << 23);
+      float x = 0.0f;
+      for (int64_t ch = half; ch < q.P; ch += 2) {
+        const int64_t at = (bl * Pp + ch) * kC + j;
+        x = __builtin_fmaf(p.dvw[at] * up, p.u[at] * up, x);
+      }
+      x += __shfl_xor(x, 32);
+      ratio = bt > 0.0f && bt < 0x1p-40f ? x * down / (bt * up) : ratio;
+    }
+    vec[lane] = half ? ratio : s1;                         // over the factors of k and q
   }
 }
 
@@ -744,9 +763,9 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         const int64_t tok = (cb + c) * kC + t, at = bh * q.L + (tok < len ? tok : len - 1);
         const float xr = gdr_load(static_cast<const T*>(q.delta) + at) + bias;
         const float br = gdr_load(static_cast<const T*>(q.beta) + at);
-        const float bt = gdr_sigmoid(br), step = softplus(xr);
+        const float step = softplus(xr);
         const float dd = dg * A * gdr_sigmoid(xr);
-        const float db = vec[32 + t] / (bt > 0.0f ? bt : 1.0f) * gdr_sigmoid(-br);     // (b = 0: 0 / 1)
+        const float db = vec[32 + t] * gdr_sigmoid(-br);
         sA += tok < len ? dg * step : 0.0f;
         sb += tok < len ? dd : 0.0f;
         const int64_t at0 = bh * q.L + (cb + c) * kC, left = len - (cb + c) * kC;
