@@ -101,9 +101,11 @@ int mamba_gdr_update(float* state, const int32_t* slots, const void* q, const vo
 
 /*
  * Bytes of workspace mamba_gdr_bwd needs (sizes only; callable without a GPU),
- * (size_t)-1 for an invalid or unsupported shape.  Per token and value head it holds
- * the updates and the gradient of v in fp32 (8 P bytes), and per 32 tokens about one
- * and a quarter states (5 P N bytes).
+ * (size_t)-1 for an invalid or unsupported shape.  With Pp and Np, P and N rounded up to
+ * 64, it holds per value head and chunk of 32 tokens 19 KiB of operands and factors, 256 Pp
+ * bytes of updates and gradients of v and 5 Pp Np bytes of states; where a key head has
+ * more than one value head or P > 64, 256 Np bytes per key head and chunk; and a padded last
+ * chunk of q, k, v and dy per row.  160 heads of 128 x 128, two to a key head, L = 2048: 1.55 GB.
  */
 size_t mamba_gdr_bwd_workspace_size(int64_t B, int64_t H, int64_t G, int64_t P, int64_t N, int64_t L,
                                     mamba_dtype_t in_dtype, mamba_dtype_t grad_dtype);
