@@ -638,6 +638,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_carry_kernel(GdrChunkParams p) {
   const int64_t it = gdr_xcd_item(blockIdx.x, gridDim.x);      // the tiles of a head share M in one L2
   const int64_t bh = it / tiles, b = bh / q.H, h = bh % q.H, p0 = (it % tiles) * 16;
   const int N = (int)q.N;
+  const int64_t len = gdr_length(q, b);
   for (int e = tid; e < 16 * kN; e += kThreads) {
     const int row = e / kN, n = e % kN;
     float x = 0.0f;
@@ -681,7 +682,8 @@ __global__ __launch_bounds__(kN * 4) void gdr_carry_kernel(GdrChunkParams p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 4 * g4 + r;
-      const float x = acc[r] + hc[r];
+      // a segment without tokens hands the state on as it is (also what is not finite in it)
+      const float x = s * p.seg_chunks * kC < len ? acc[r] + hc[r] : a[row * kRow + n];
       A[(s + 1) & 1][row * kRow + n] = x;                  // zero where n >= N: both terms are
       if (n < N && p0 + row < q.P) p.seg_start[(((b * p.S + s + 1) * q.H + h) * q.P + p0 + row) * N + n] = x;
     }

@@ -87,6 +87,18 @@ def test_infinite_gates_are_resets(kernel, segments, dev):
     assert rel_l2(from_dev(y), yr) <= 20 * 2.0 ** -24 and rel_l2(from_dev(S), Sr) <= 20 * 2.0 ** -24
 
 
+@pytest.mark.parametrize("kernel,segments", [("token", 0), ("chunk", 0), ("chunk", 3)])
+def test_a_row_without_tokens_keeps_its_state(kernel, segments, dev):
+    import torch
+    N = 40
+    t = {n: to_dev(a, dev) for n, a in W.gdr_inputs(B, H, G, P, N, L, "f32", 8470).items()}
+    t["initial_state"][ROW, 7, 3] = float("inf")
+    t["initial_state"][ROW, 9, 38] = float("nan")
+    y, S = _run(t, kernel, segments, torch.float32, dev, [L, 0])
+    assert torch.equal(S[ROW].view(torch.int32), t["initial_state"][ROW].view(torch.int32))
+    assert not y[ROW].any() and torch.isfinite(y[0]).all() and torch.isfinite(S[0]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_gradients_behind_the_end_stay_zero(dtype, dev):
     import torch
