@@ -40,9 +40,10 @@
  * are multiples of a vector, select vector accesses); workspaces 256 bytes.
  * A NaN or an infinity among the inputs of a token leaves the outputs of the tokens
  * before it as they are; from that token on, every output and state that it reaches
- * is NaN or infinite.  (An infinite delta or beta is a number: its softplus or sigmoid's
- * limit.  Numbers beyond 3.38e38 count as infinite.)  In the backward pass any gradient
- * of such a batch row may be NaN, dA and ddelta_bias with it.
+ * is NaN or infinite.  (Numbers beyond 3.38e38 count as infinite.)  In the backward pass
+ * any gradient of such a batch row may be NaN, dA and ddelta_bias with it.  An infinite
+ * delta or beta is not meant: a step of infinite length forgets the state (A < 0), and the
+ * gates and all gradients take their limits.
  * State, gates and sums are fp32 or better.  The results are deterministic (sums in a
  * fixed order, no atomics): the same call gives the same bits, and what the other rows of
  * the batch hold has no influence on a row.  How many rows there are has: in mamba_gdr_fwd

@@ -766,7 +766,7 @@ __global__ __launch_bounds__(kN * 4) void gdr_grad_kernel(GdrChunkParams p) {
         const float step = softplus(xr);
         const float dd = dg * A * gdr_sigmoid(xr);
         const float db = vec[32 + t] * gdr_sigmoid(-br);
-        sA += tok < len ? dg * step : 0.0f;
+        sA += tok < len && dg != 0.0f ? dg * step : 0.0f;   // (an infinite step: a and dg are 0)
         sb += tok < len ? dd : 0.0f;
         const int64_t at0 = bh * q.L + (cb + c) * kC, left = len - (cb + c) * kC;
         gdr_store_within(static_cast<O*>(p.ddelta) + at0, left, t, dd);

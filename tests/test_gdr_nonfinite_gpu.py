@@ -87,6 +87,29 @@ def test_infinite_gates_are_resets(kernel, segments, dev):
     assert rel_l2(from_dev(y), yr) <= 20 * 2.0 ** -24 and rel_l2(from_dev(S), Sr) <= 20 * 2.0 ** -24
 
 
+def test_gradients_of_infinite_gates(dev):
+    """The gradients' limits: those of a step of 1e5 for delta = +inf (A < -1: exp(-1e5) is 0), of delta =
+    -1e5 for -inf, of |beta| = 800.  Bars of test_gdr_variants_gpu.py."""
+    import selective_state_space_75_amd as m
+    from helpers import f64, from_dev, rel_l2
+    N = 40
+    x = W.gdr_inputs(B, H, G, P, N, L, "f32", 8480)
+    ref = {n: f64(a) for n, a in x.items()}
+    for i, (n, v, far) in enumerate([("delta_raw", np.inf, 1e5), ("delta_raw", -np.inf, -1e5), ("beta_raw", np.inf, 800.0),
+                                     ("beta_raw", -np.inf, -800.0)]):
+        x[n][:, :, 9 + 14 * i], ref[n][:, :, 9 + 14 * i] = v, far
+    t = {n: to_dev(a, dev) for n, a in x.items()}
+    g = m.gdr_bwd(*[t[n] for n in NAMES], t["A"], t["delta_bias"], t["dy"], groups=G, initial_state=t["initial_state"],
+                  dfinal_state=t["dfinal_state"], qk_norm=True)
+    with np.errstate(over="ignore"):
+        want = O.gdr_bwd(*[ref[n] for n in NAMES], ref["A"], ref["delta_bias"], ref["dy"], groups=G, norm=True,
+                         initial_state=ref["initial_state"], dfinal_state=ref["dfinal_state"])
+    for n, a in g.items():
+        e = rel_l2(from_dev(a), want[n])
+        log("  %s: rel_l2=%.3e" % (n, e))
+        assert e <= (4e-5 if n in ("dA", "ddelta_bias") else 20 * 2.0 ** -24), n
+
+
 @pytest.mark.parametrize("kernel,segments", [("token", 0), ("chunk", 0), ("chunk", 3)])
 def test_a_row_without_tokens_keeps_its_state(kernel, segments, dev):
     import torch
