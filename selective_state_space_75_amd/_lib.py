@@ -727,10 +727,16 @@ def state_cache(n_slots: int, n: int, device):
             torch.zeros((n_slots, (n + CACHE_GROUP - 1) // CACHE_GROUP), dtype=torch.uint8, device=device))
 
 
-def _cache_args(codes, exps, slots, state, what):
-    torch = _torch()
+def _check_codes(codes):
+    if not isinstance(codes, _torch().Tensor):
+        raise TypeError("codes must be a torch.Tensor")
     if codes.dim() != 2:
         raise ValueError("codes must be (n_slots, n)")
+
+
+def _cache_args(codes, exps, slots, state, what):
+    torch = _torch()
+    _check_codes(codes)
     S, n = codes.shape
     dev = codes.device
     if dev.type != "cuda":
@@ -762,7 +768,10 @@ def state_cache_read(codes, exps, *, slots=None, out=None, dtype=None, stream=No
     (rows); None: every slot in order; negative: zeros).  `out` (rows, ...) fp32 or bf16
     is written when given, else a (rows, n) tensor of `dtype` (fp32) is made."""
     torch = _torch()
+    _check_codes(codes)
     if out is None:
+        if slots is not None and (not isinstance(slots, torch.Tensor) or slots.dim() != 1):
+            raise ValueError("slots must be an int32 tensor of one dimension")
         rows = codes.shape[0] if slots is None else slots.shape[0]
         with _on(codes.device, stream) if codes.is_cuda else contextlib.nullcontext():
             out = torch.empty((rows, codes.shape[1]), dtype=dtype or torch.float32, device=codes.device)
