@@ -166,8 +166,11 @@ __global__ __launch_bounds__(256, 2) void gdr_adjoint_kernel(GdrChunkParams p) {
       bf16x8 a[kParts], aq[kParts];
       gdr_frags<T, kN>(K, 16 * tn, 0, lane, a);
       gdr_frags<T, kN>(Q, 16 * tn, 0, lane, aq);
-      S[tn] = gdr_mma<3>(aq, wq, S[tn] * dc);
-      S[tn] = gdr_mma<3>(a, wk, S[tn]);
+      // Summed from zero and added once: on top of dS each of the six products would round at
+      // its size (dA, a sum over tokens that cancels, was 1.5 times as far off, and 10 us went
+      // into waiting for the accumulators).
+      const f32x4 x = gdr_mma<3>(aq, wq, f32x4{0.f, 0.f, 0.f, 0.f});
+      S[tn] = gdr_fma(S[tn], f32x4{dc, dc, dc, dc}, gdr_mma<3>(a, wk, x));
     }
     float* wdst = p.dvw + ((blk0 + c) * Pp + ch) * kC + 4 * g4;
 #pragma unroll

@@ -61,6 +61,14 @@ __device__ __forceinline__ void gdr_mma_rows(const bf16x8 (&a)[kR][kA], const bf
       }
 }
 
+// a b + c, rounded once.
+__device__ __forceinline__ f32x4 gdr_fma(f32x4 a, f32x4 b, f32x4 c) {
+  f32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = __builtin_fmaf(a[j], b[j], c[j]);
+  return r;
+}
+
 // Two fp32 numbers rounded to bf16, as one v_cvt_pk_bf16_f32.
 __device__ __forceinline__ uint32_t gdr_pack(float lo, float hi) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
