@@ -69,12 +69,15 @@ struct GdrPlan {
 };
 
 // Sizes-only plan of the forward pass.
-// Token by token (one launch) while the steps cost less than the chunks' launches: a
-// step takes 2.1 us at N = 128 and 1.3 us at N = 64 until about 5000 rows of state keep
-// every CU busy, and grows with the rows from there.  Measured, call to call, token
-// against chunks: 32 heads of 128 x 128, L = 11: 22.4 and 27.8 us, L = 12: 28.9 and 28.1;
-// 4 heads of 64 x 64, L = 19: 22.3 and 26.6, L = 20: 28.0 and 26.3; 160 heads of 128 x 128,
-// L = 2: 22.4 and 26.5, L = 4: 38.6 and 27.9.
+// Token by token (one launch) while the steps cost less than the chunks' launches, about 27 us
+// up to L = 32.  Steps cost more the more rows of state there are beyond about 5000, which
+// keep every CU busy, and 1.2 to 1.9 times their neighbours where L is a multiple of 4
+// (gdr_step.hip).  The rule ends in front of the first such L that loses.  Measured, call to
+// call, token against chunks, in us.  32 heads of 128 x 128: L = 11: 22.8, 27.3; 12: 29.1, 27.0;
+// 13: 24.0, 28.5; 15: 26.8, 28.9; 16: 37.9, 27.1; 17: 29.6, 27.3; 24: 55.1, 27.2; 31: 51.7, 27.2.
+// 4 heads of 64 x 64: L = 19: 22.8, 27.2; 20: 28.0, 27.2; 21: 23.6, 27.2; 23: 25.4, 27.3; 24: 33.0, 26.9;
+// 25: 27.4, 27.3; 31: 32.8, 27.1.  160 heads of 128 x 128: L = 2: 23.5, 28.2; 3: 23.5, 27.7; 4: 38.6, 28.0.
+// So it gives up 2 to 4 us at the odd lengths between 12 and 15, or 20 and 23.
 // In chunks, L is cut into segments when the 16-channel waves of all heads would leave
 // SIMDs idle (there are 1024).  The summary launch then adds the N transition rows to the
 // P value rows of every head, so fewer than three segments do not pay, and the two launches

@@ -31,11 +31,12 @@
 // sums over value channels that stay inside a wave.  One workgroup takes all value
 // heads of a key head, so dQ and dK need no reduction between workgroups.
 //
-// Measured, bf16, 40 heads of 128 x 128, batch 4, L = 2048 (422 MB): preparation 73 us,
-// states 230, adjoint 462, pairs 175, grads 563, sums 5; the call 1.49 ms.  The bytes at a large
-// copy's rate are 88 us.  The chains are bound as the forward's; the adjoint also writes
-// dS of every chunk (671 MB) so that the grads need no second backward sweep.  The grads
-// hold S and dS in registers, which leaves one workgroup per CU.
+// Measured after warm-up, bf16, 40 heads of 128 x 128, batch 4, L = 2048 (422 MB, 88 us at a large
+// copy's rate): preparation 72 us, states 225, adjoint 451, pairs 174, grads 588, sums 5; the call
+// 1.52 ms, 5.6 GB of HBM traffic.  The chains are bound as the forward's (320 workgroups on 256
+// CUs); the adjoint also writes dS of every chunk (671 MB) so that the grads need no second
+// backward sweep.  The grads hold S and dS in registers, which leaves one workgroup per CU,
+// and the variant with 128 channels a slab spills 11 vector and 136 scalar registers.
 #include "gdr_mfma.hpp"
 
 namespace mamba {

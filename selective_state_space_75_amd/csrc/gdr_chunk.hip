@@ -29,12 +29,14 @@
 // have no values; they end as M.  A carry kernel chains the segments, and the full
 // launch runs all of them at once.
 //
-// Measured, bf16, 128 x 128.  40 heads, batch 4, L = 2048 (263 MB): preparation 54 us,
-// chain 229 us, the call 261 us.  Its bytes at the rate of a large copy (4.78 TB/s) are 55 us:
-// the chain is bound by the issue of a single wave per SIMD (about 5300 cycles a chunk, of
-// which the 82 products take 1340; the rest is 433 vector instructions, operand reads
-// and waits).  16 heads, batch 1, L = 32768: preparation 138, summary 331, carry 21, full
-// launch 295 us.
+// Measured after warm-up, bf16, 128 x 128.  40 heads, batch 4, L = 2048 (263 MB, 55 us at the
+// 4.78 TB/s of a large copy): preparation 53 us, chain 216 us; a call is 268 us traced, 258 us not.
+// The chain's 320 workgroups meet 256 CUs, and the CUs with two of them set its time: 256
+// workgroups (32 heads) take 144 us, 512 (64 heads) 255 us.  With one per CU a chunk takes
+// 2.2 us, 5300 cycles: its 82 products 1312, the rest the issue of 420 vector instructions by
+// one wave per SIMD, operand reads and waits (0.28 of a wave's time it waits to issue, 0.23 for
+// memory or LDS).  16 heads, batch 1, L = 32768: preparation 132, summary 305, carry 21, full launch
+// 266 us.  Registers: at 256 the variants for N > 64 with fp32 inputs or outputs spill 8 to 24.
 #include "gdr_mfma.hpp"
 
 namespace mamba {

@@ -103,9 +103,11 @@ __device__ __forceinline__ void pin(bf16x8 (&x)[kParts]) {
   for (int s = 0; s < kParts; ++s) asm volatile("" : "+v"(x[s]));
 }
 
-// Operand tiles in LDS: rows of 32 tokens, 36 apart.  72 bytes (18 banks) spread
-// both reads of a lane group over the banks: 16 rows at one token (gdr_frag), and
-// 4 rows at 16 tokens (gdr_frag_t).
+// Operand tiles in LDS: rows of 32 tokens, 36 apart.  72 bytes (18 banks of 64) spread both
+// reads of a lane group, 16 rows at one token (gdr_frag) and 4 rows at 16 tokens (gdr_frag_t),
+// over most of the banks; rows 7 apart still meet in two.  Measured on the layer (40 heads, L =
+// 2048): bank conflicts are 0.38 of the LDS's access cycles in the forward chain, 0.25 in the
+// adjoint, 0.27 in the grads and 0.45 in the pairs, which is 0.06, 0.02, 0.07 and 0.13 of their time.
 constexpr int kGdrRow = 36;
 
 // A or B operand whose row (column) index runs along the stored row: lane i takes

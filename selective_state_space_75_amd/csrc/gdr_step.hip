@@ -12,7 +12,9 @@
 //
 // One token moves 8 bytes per number of the state (fp32 read and written in
 // place) and computes 7 flops on it: HBM-bound, like mamba_state_update.  128 rows of 32
-// heads of 128 x 128: 125 us, 4.2 TB/s (a large copy: 4.78).
+// heads of 128 x 128: 116 us, 4.6 TB/s (a large copy: 4.78).  Sequences are read one number
+// per lane at a stride of L, which is slow where L is a multiple of 4: 32 heads, L = 15, 16, 17: 27,
+// 38, 30 us.
 #include "device_math.hpp"
 #include "gdr.hpp"
 #include "kernels.hpp"
