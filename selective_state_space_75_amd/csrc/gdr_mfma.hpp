@@ -266,12 +266,11 @@ __device__ __forceinline__ void gdr_store_end(O* row, int64_t t, int64_t len, in
   }
 }
 
-// Between the first and the last product of the chain, adjoint, pair and grad kernels, which
-// use nearly all of their registers or more, no branch is taken by some lanes of a wave only:
-// at such a branch's end the compiler may copy registers before it re-enables the other
-// lanes.  Lanes with nothing of their own read clamped addresses and write what another
-// lane writes, or are dropped by the bounds of a buffer.  tests/test_gdr_codegen.py looks at
-// the compiled code.
+// Between the first and the last product of the chain, adjoint, pair and grad kernels no branch
+// is taken by some lanes of a wave only: at such a branch's end the compiler, out of registers
+// (only the pairs have some left), may copy some before it re-enables the other lanes.  Lanes
+// with nothing of their own read clamped addresses and write what another lane writes, or are
+// dropped by the bounds of a buffer.  tests/test_gdr_codegen.py looks at the compiled code.
 
 // Four numbers n .. n + 3 of a state row of N (zeros behind it).
 __device__ __forceinline__ f32x4 gdr_load_state(const float* row, int64_t n, int64_t N, bool vec) {

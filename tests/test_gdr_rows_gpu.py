@@ -57,7 +57,7 @@ def test_forward_over_batch_sizes(H, G, P, N, L, few, many, dev):
     assert torch.equal(y[0], y2[0]) and torch.equal(S[0], S2[0]) and not torch.equal(y[1], y2[1])
 
 
-@pytest.mark.parametrize("H,G,P,N,B", [(8, 4, 128, 128, 70), (3, 1, 40, 96, 5)])
+@pytest.mark.parametrize("H,G,P,N,B", [(8, 4, 128, 128, 70), (8, 8, 128, 64, 70), (3, 1, 40, 96, 5)])
 def test_update_over_batch_sizes(H, G, P, N, B, dev):
     import torch
     import selective_state_space_75_amd as m
