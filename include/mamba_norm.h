@@ -1,0 +1,60 @@
+/*
+ * mamba_norm.h -- C ABI of the layer norm over channels: the norm in front of a
+ * block, and the norm per head of a layer's output with the output gate that
+ * mamba_gdr_fwd and mamba_ssd_fwd leave to what follows them.  The conventions of
+ * mamba_scan.h hold.
+ *
+ * For every token (b, t) and group of Dg = D / groups consecutive channels:
+ *     xh = (x - mean) / sqrt(var + eps)          (var: the mean of (x - mean)^2)
+ *     y  = (xh weight[d] + bias[d]) z sigmoid(z)  (without the gate where z is NULL)
+ * With MAMBA_FLAG_RMS, xh = x / sqrt(mean of x^2 + eps).
+ *
+ *   x      : (B, D, L) in_dtype.  z : (B, D, L) in_dtype or NULL.  L = 1 is the
+ *            token-major form: (rows, D), channels consecutive.
+ *   x_stride, z_stride : elements from one batch row to the next (at least D*L).
+ *   weight : (D) fp32 or NULL (ones).  bias : (D) fp32 or NULL (zeros).
+ *
+ * Sizes: B, D, L >= 1; D a multiple of groups; B*D*L < 2^46, strides < 2^46 / B; B*groups*ceil(L/8) < 2^22.
+ * in_dtype and the output dtypes may each be MAMBA_F32 or MAMBA_BF16.  Alignment: every array to
+ * its element size; workspaces 256 bytes.  Statistics and sums are fp32; the variance is taken
+ * around the mean, not as a difference of squares.  A NaN or an infinity stays in its own token
+ * and group (dweight and dbias aside).  Deterministic: sums in a fixed order, no atomics; a token's
+ * bits do not depend on B.
+ */
+#ifndef MAMBA_NORM_H_
+#define MAMBA_NORM_H_
+
+#include "mamba_scan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MAMBA_FLAG_RMS 0x10u             /* no mean taken off */
+
+int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, const float* bias, void* y,
+                         int64_t B, int64_t D, int64_t L, int64_t groups, int64_t x_stride,
+                         int64_t z_stride, float eps, mamba_dtype_t in_dtype, mamba_dtype_t out_dtype,
+                         unsigned flags, hipStream_t stream);
+
+/* Bytes of workspace mamba_layer_norm_bwd needs, (size_t)-1 for an invalid shape. */
+size_t mamba_layer_norm_bwd_workspace_size(int64_t B, int64_t D, int64_t L, int64_t groups);
+
+/*
+ * Gradients for a gradient dy of y; the statistics are recomputed.
+ *   dy            : (B, D, L) grad_dtype, dense.
+ *   dx, dz        : (B, D, L) grad_dtype, written, dense; dz NULL where z is (required otherwise).
+ *   dweight, dbias : (D) fp32, written (summed over batch rows and tokens), also where weight or
+ *                   bias is NULL.
+ */
+int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, const float* bias,
+                         const void* dy, void* dx, void* dz, float* dweight, float* dbias, int64_t B,
+                         int64_t D, int64_t L, int64_t groups, int64_t x_stride, int64_t z_stride,
+                         float eps, mamba_dtype_t in_dtype, mamba_dtype_t grad_dtype, unsigned flags,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MAMBA_NORM_H_ */

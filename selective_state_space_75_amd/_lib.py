@@ -1,5 +1,6 @@
 """ctypes binding of libmamba_scan.so (the C ABI of include/mamba_scan.h,
-include/mamba_gdr.h and include/mamba_state_cache.h).
+include/mamba_gdr.h, include/mamba_state_cache.h, include/mamba_glr.h and
+include/mamba_norm.h).
 
 Argument marshalling only: tensors are checked (device, dtype, shape,
 contiguity), outputs and the workspace are allocated with torch, and raw
@@ -21,6 +22,8 @@ MAMBA_F32, MAMBA_BF16 = 0, 1
 FLAG_DELTA_B = 0x1
 FLAG_ACCURATE_EXPM1 = 0x2
 FLAG_QK_NORM = 0x4
+FLAG_BLEND = 0x8
+FLAG_RMS = 0x10
 
 STATUS = {
     0: "MAMBA_OK", -1: "MAMBA_ERR_NULL", -2: "MAMBA_ERR_SHAPE", -3: "MAMBA_ERR_DTYPE",
@@ -92,6 +95,24 @@ def lib() -> ctypes.CDLL:
             L.mamba_state_cache_write.restype = c_int
             L.mamba_state_cache_read.argtypes = [vp] * 4 + [i64] * 3 + [c_int, vp]
             L.mamba_state_cache_read.restype = c_int
+            L.mamba_glr_workspace_size.argtypes = [i64] * 3
+            L.mamba_glr_workspace_size.restype = sz
+            L.mamba_glr_fwd.argtypes = [vp] * 11 + [i64] * 7 + [c_int, c_int, u32, vp, sz, vp]
+            L.mamba_glr_fwd.restype = c_int
+            L.mamba_glr_update.argtypes = [vp] * 10 + [i64] * 7 + [c_int, c_int, u32, vp]
+            L.mamba_glr_update.restype = c_int
+            L.mamba_glr_bwd_workspace_size.argtypes = [i64] * 3
+            L.mamba_glr_bwd_workspace_size.restype = sz
+            L.mamba_glr_bwd.argtypes = [vp] * 19 + [i64] * 7 + [c_int, c_int, u32, vp, sz, vp]
+            L.mamba_glr_bwd.restype = c_int
+            L.mamba_glr_set_test_knobs.argtypes = [c_int, i64]
+            L.mamba_glr_set_test_knobs.restype = c_int
+            L.mamba_layer_norm_fwd.argtypes = [vp] * 5 + [i64] * 6 + [f32, c_int, c_int, u32, vp]
+            L.mamba_layer_norm_fwd.restype = c_int
+            L.mamba_layer_norm_bwd_workspace_size.argtypes = [i64] * 4
+            L.mamba_layer_norm_bwd_workspace_size.restype = sz
+            L.mamba_layer_norm_bwd.argtypes = [vp] * 9 + [i64] * 6 + [f32, c_int, c_int, u32, vp, sz, vp]
+            L.mamba_layer_norm_bwd.restype = c_int
             L.mamba_scan_kernel.argtypes = [i64, i64, i64, i64]
             L.mamba_scan_kernel.restype = c_int
             L.mamba_set_test_knobs.argtypes = [ctypes.POINTER(TestKnobs)]
@@ -781,4 +802,254 @@ def state_cache_read(codes, exps, *, slots=None, out=None, dtype=None, stream=No
                                           _dtype_code(out), _stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_state_cache_read")
+    return out
+
+
+# ----------------------------------------------------------------------------- gated linear recurrence
+class glr_test_knobs:  # noqa: N801 (used as a context manager)
+    """``with glr_test_knobs(waves=2, segments=3): ...`` sets the gated linear recurrence's
+    test knobs (mamba_glr_set_test_knobs) for the block and restores the planner's choices
+    after it."""
+    __test__ = False   # not a pytest test class
+
+    def __init__(self, waves: int = 0, segments: int = 0):
+        self.args = (waves, segments)
+
+    def __enter__(self):
+        st = lib().mamba_glr_set_test_knobs(*self.args)
+        if st != 0:
+            raise MambaError(st, "mamba_glr_set_test_knobs")
+        return self
+
+    def __exit__(self, *exc):
+        lib().mamba_glr_set_test_knobs(0, 0)
+        return False
+
+
+def _rows_of(t, name, shape, dtype, device):
+    """(tensor, row stride) of a (B, ...) input that may be a channel range, or (None, 0)."""
+    return (None, 0) if t is None else (t, _check_rows(t, name, shape, dtype, device))
+
+
+def _first(x, dims, what):
+    """Checks the input that the others are held to, and returns its device and dtype."""
+    if not isinstance(x, _torch().Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() not in dims:
+        raise ValueError("x must be %s" % what)
+    if x.device.type != "cuda":
+        raise ValueError("inputs must be on a GPU device")
+    _dtype_code(x)
+    return x.device, x.dtype
+
+
+def _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend):
+    """Checks of the inputs that every call of the recurrence has; returns the batch strides."""
+    torch = _torch()
+    shape, dev, dt, D = tuple(x.shape), x.device, x.dtype, x.shape[1]
+    if r is None:
+        raise TypeError("r must be a torch.Tensor")
+    strides = [_rows_of(t, n, shape, dt, dev)[1] for t, n in ((x, "x"), (r, "r"), (i, "i"), (z, "z"))]
+    if blend:
+        if A is not None:
+            raise ValueError("A is not used with blend=True and must be None")
+    elif A is None:
+        raise ValueError("A is needed unless blend=True")
+    if i is None and i_bias is not None:
+        raise ValueError("i_bias without i")
+    for t, n in ((A, "A"), (r_bias, "r_bias"), (i_bias, "i_bias")):
+        _check(t, n, (D,), torch.float32, dev)
+    return strides
+
+
+def glr_workspace_size(B: int, D: int, L: int) -> int:
+    """Bytes glr_fwd needs for these sizes."""
+    n = lib().mamba_glr_workspace_size(B, D, L)
+    if n == ctypes.c_size_t(-1).value:
+        raise MambaError(-2, "mamba_glr_workspace_size")
+    return n
+
+
+def glr_fwd(x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *, blend=False, initial_state=None, lengths=None,
+            return_final_state=False, out_dtype=None, y=None, final_state=None, workspace=None, stream=None):
+    """Gated linear recurrence over whole sequences (include/mamba_glr.h), per channel
+
+        h_t = a_t h_(t-1) + n_t sigmoid(i_t + i_bias) x_t,   y_t = h_t silu(z_t)
+
+    with s = sigmoid(r + r_bias), a = exp(A s) and n = sqrt(1 - a^2), or a = 1 - s and n = s with
+    blend=True (then A is None).  x, r, i, z: (B, D, L), i and z optional; they may be channel ranges
+    of a wider tensor.  A (below zero), r_bias, i_bias: (D) fp32.  initial_state: (B, D) fp32;
+    lengths: (B) int32, tokens per row.
+
+    Returns y (B, D, L), or (y, final_state (B, D) fp32) when return_final_state.
+    """
+    torch = _torch()
+    dev, in_dt = _first(x, (3,), "(B, D, L)")
+    B, D, L = x.shape
+    strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
+    _check(initial_state, "initial_state", (B, D), torch.float32, dev)
+    _check(lengths, "lengths", (B,), torch.int32, dev)
+    out_dt = in_dt if out_dtype is None else out_dtype
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((B, D, L), dtype=out_dt, device=dev)
+        _check(y, "y", (B, D, L), out_dt, dev)
+        if return_final_state:
+            if final_state is None:
+                final_state = torch.empty((B, D), dtype=torch.float32, device=dev)
+            _check(final_state, "final_state", (B, D), torch.float32, dev)
+        workspace = _workspace(workspace, glr_workspace_size(B, D, L), dev)
+        st = lib().mamba_glr_fwd(
+            _ptr(x), _ptr(r), _ptr(i), _ptr(z), _ptr(A), _ptr(r_bias), _ptr(i_bias), _ptr(initial_state), _ptr(lengths),
+            _ptr(y), _ptr(final_state if return_final_state else None), B, D, L, *strides, _dtype_code(x),
+            _dtype_code(y), FLAG_BLEND if blend else 0, _ptr(workspace), _nbytes(workspace), _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_glr_fwd")
+    return (y, final_state) if return_final_state else y
+
+
+def glr_bwd_workspace_size(B: int, D: int, L: int) -> int:
+    """Bytes glr_bwd needs for these sizes."""
+    n = lib().mamba_glr_bwd_workspace_size(B, D, L)
+    if n == ctypes.c_size_t(-1).value:
+        raise MambaError(-2, "mamba_glr_bwd_workspace_size")
+    return n
+
+
+def glr_bwd(x, r, i, A, r_bias, i_bias, z, dy, *, blend=False, initial_state=None, dfinal_state=None, lengths=None,
+            workspace=None, stream=None):
+    """Gradients of glr_fwd for the output gradient dy (B, D, L) and, optionally, the final
+    state's dfinal_state (B, D) fp32; the other arguments as for glr_fwd.
+
+    Returns a dict: dx, dr, di, dz (B, D, L) in dy's dtype (di and dz None without i and z); dA
+    (None with blend), dr_bias, di_bias (None without i) (D) fp32; dinitial_state (B, D) fp32
+    (None without initial_state).
+    """
+    torch = _torch()
+    dev, _ = _first(x, (3,), "(B, D, L)")
+    B, D, L = x.shape
+    strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
+    _check(initial_state, "initial_state", (B, D), torch.float32, dev)
+    _check(dfinal_state, "dfinal_state", (B, D), torch.float32, dev)
+    _check(lengths, "lengths", (B,), torch.int32, dev)
+    if dy is None:
+        raise TypeError("dy must be a torch.Tensor")
+    _check(dy, "dy", (B, D, L), None, dev)
+    gcode = _dtype_code(dy)
+    with _on(dev, stream):
+        def new(*shape, dtype=dy.dtype, wanted=True):
+            return torch.empty(shape, dtype=dtype, device=dev) if wanted else None
+
+        f32 = torch.float32
+        out = {"dx": new(B, D, L), "dr": new(B, D, L), "di": new(B, D, L, wanted=i is not None),
+               "dz": new(B, D, L, wanted=z is not None), "dA": new(D, dtype=f32, wanted=not blend),
+               "dr_bias": new(D, dtype=f32), "di_bias": new(D, dtype=f32, wanted=i is not None),
+               "dinitial_state": new(B, D, dtype=f32, wanted=initial_state is not None)}
+        workspace = _workspace(workspace, glr_bwd_workspace_size(B, D, L), dev)
+        st = lib().mamba_glr_bwd(
+            _ptr(x), _ptr(r), _ptr(i), _ptr(z), _ptr(A), _ptr(r_bias), _ptr(i_bias), _ptr(initial_state), _ptr(lengths),
+            _ptr(dy), _ptr(dfinal_state), _ptr(out["dx"]), _ptr(out["dr"]), _ptr(out["di"]), _ptr(out["dz"]),
+            _ptr(out["dA"]), _ptr(out["dr_bias"]), _ptr(out["di_bias"]), _ptr(out["dinitial_state"]), B, D, L, *strides,
+            _dtype_code(x), gcode, FLAG_BLEND if blend else 0, _ptr(workspace), _nbytes(workspace),
+            _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_glr_bwd")
+    return out
+
+
+def glr_update(state, x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *, blend=False, slots=None,
+               out_dtype=None, y=None, stream=None):
+    """One token of the gated linear recurrence for every row; `state` (S, D) fp32 is updated in
+    place at the rows' slots (int32 (B); None: row b has state b; negative: an empty row, y = 0).
+    x, r, i, z: (B, D).  Returns y (B, D)."""
+    torch = _torch()
+    dev, in_dt = _first(x, (2,), "(B, D)")
+    B, D = x.shape
+    if state is None or state.dim() != 2:
+        raise ValueError("state must be (S, D)")
+    strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
+    _check(state, "state", (state.shape[0], D), torch.float32, dev)
+    _check(slots, "slots", (B,), torch.int32, dev)
+    out_dt = in_dt if out_dtype is None else out_dtype
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((B, D), dtype=out_dt, device=dev)
+        _check(y, "y", (B, D), out_dt, dev)
+        st = lib().mamba_glr_update(
+            _ptr(state), _ptr(slots), _ptr(x), _ptr(r), _ptr(i), _ptr(z), _ptr(A), _ptr(r_bias), _ptr(i_bias), _ptr(y),
+            B, D, state.shape[0], *strides, _dtype_code(x), _dtype_code(y), FLAG_BLEND if blend else 0,
+            _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_glr_update")
+    return y
+
+
+# ----------------------------------------------------------------------------- layer norm over channels
+def _norm_inputs(x, weight, bias, z, groups):
+    """Checks of the norm's inputs; returns (B, D, L, batch strides of x and z)."""
+    torch = _torch()
+    dev, dt = _first(x, (2, 3), "(B, D, L) or (rows, D)")
+    B, D = x.shape[:2]
+    L = x.shape[2] if x.dim() == 3 else 1
+    if int(groups) < 1 or D % int(groups):
+        raise ValueError("%d channels do not divide into %s groups" % (D, groups))
+    strides = [_rows_of(t, n, tuple(x.shape), dt, dev)[1] for t, n in ((x, "x"), (z, "z"))]
+    _check(weight, "weight", (D,), torch.float32, dev)
+    _check(bias, "bias", (D,), torch.float32, dev)
+    return B, D, L, strides
+
+
+def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms=False, out_dtype=None, y=None,
+                   stream=None):
+    """Layer norm of every token over its channels, or over each of `groups` equal ranges of them,
+    with the output gate (include/mamba_norm.h): (xh weight + bias) silu(z), xh = (x - mean) /
+    sqrt(var + eps), or x / sqrt(mean x^2 + eps) with rms=True.  x, z: (B, D, L), or (rows, D) for
+    token-major rows; both may be channel ranges of a wider tensor.  weight, bias: (D) fp32 or None.
+    Returns y like x, in out_dtype."""
+    torch = _torch()
+    B, D, L, strides = _norm_inputs(x, weight, bias, z, groups)
+    dev = x.device
+    out_dt = x.dtype if out_dtype is None else out_dtype
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=out_dt, device=dev)
+        _check(y, "y", tuple(x.shape), out_dt, dev)
+        st = lib().mamba_layer_norm_fwd(
+            _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(y), B, D, L, int(groups), *strides, float(eps),
+            _dtype_code(x), _dtype_code(y), FLAG_RMS if rms else 0, _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_layer_norm_fwd")
+    return y
+
+
+def layer_norm_bwd_workspace_size(B: int, D: int, L: int, groups: int = 1) -> int:
+    """Bytes layer_norm_bwd needs for these sizes (L = 1 for token-major rows)."""
+    n = lib().mamba_layer_norm_bwd_workspace_size(B, D, L, groups)
+    if n == ctypes.c_size_t(-1).value:
+        raise MambaError(-2, "mamba_layer_norm_bwd_workspace_size")
+    return n
+
+
+def layer_norm_bwd(x, weight, bias, z, dy, *, groups=1, eps=1e-5, rms=False, workspace=None, stream=None):
+    """Gradients of layer_norm_fwd for the output gradient dy (like x).  Returns a dict: dx, dz like x
+    in dy's dtype (dz None without z); dweight, dbias (D) fp32, also where weight or bias is None."""
+    torch = _torch()
+    B, D, L, strides = _norm_inputs(x, weight, bias, z, groups)
+    dev = x.device
+    if dy is None:
+        raise TypeError("dy must be a torch.Tensor")
+    _check(dy, "dy", tuple(x.shape), None, dev)
+    gcode = _dtype_code(dy)
+    with _on(dev, stream):
+        out = {"dx": torch.empty(x.shape, dtype=dy.dtype, device=dev),
+               "dz": None if z is None else torch.empty(x.shape, dtype=dy.dtype, device=dev),
+               "dweight": torch.empty((D,), dtype=torch.float32, device=dev),
+               "dbias": torch.empty((D,), dtype=torch.float32, device=dev)}
+        workspace = _workspace(workspace, layer_norm_bwd_workspace_size(B, D, L, int(groups)), dev)
+        st = lib().mamba_layer_norm_bwd(
+            _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(out["dx"]), _ptr(out["dz"]), _ptr(out["dweight"]),
+            _ptr(out["dbias"]), B, D, L, int(groups), *strides, float(eps), _dtype_code(x), gcode,
+            FLAG_RMS if rms else 0, _ptr(workspace), _nbytes(workspace), _stream(dev, stream))
+    if st != 0:
+        raise MambaError(st, "mamba_layer_norm_bwd")
     return out

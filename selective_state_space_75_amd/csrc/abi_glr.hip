@@ -1,0 +1,290 @@
+// abi_glr.hip -- the C ABI declared in include/mamba_glr.h and include/mamba_norm.h:
+// argument checks, plans and launches.  Every check runs before any HIP call.
+#include <atomic>
+
+#include "kernels.hpp"
+#include "mamba_glr.h"
+#include "mamba_norm.h"
+
+namespace {
+
+using mamba::Dt;
+
+constexpr int64_t kMaxElems = int64_t(1) << 46;
+
+bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
+bool dtype_ok(int t) { return t == MAMBA_F32 || t == MAMBA_BF16; }
+size_t width(int t) { return t == MAMBA_BF16 ? 2 : 4; }
+Dt dt_of(int t) { return t == MAMBA_BF16 ? Dt::BF16 : Dt::F32; }
+
+// a * b * c with every factor >= 1 and the product below kMaxElems
+bool product_ok(int64_t a, int64_t b, int64_t c) {
+  if (a < 1 || b < 1 || c < 1) return false;
+  if (a > kMaxElems / b) return false;
+  return a * b <= (kMaxElems - 1) / c;
+}
+
+bool stride_ok(int64_t s, int64_t B, int64_t row) { return s >= row && s <= kMaxElems / B; }
+bool all_aligned(std::initializer_list<const void*> ptrs, size_t a) {
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned(ptr, a)) return false;
+  return true;
+}
+
+// Test knobs (mamba_glr_set_test_knobs), read once per call.
+std::atomic<int> g_waves{0};
+std::atomic<int64_t> g_segments{0};
+
+struct GlrPlan {
+  int64_t S = 1, seg_len = 0;
+  int waves = 1;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// L in S segments of a multiple of 8 tokens each, as even as that allows.
+void cut(GlrPlan& q, int64_t L, int64_t S) {
+  q.seg_len = ceil_div(ceil_div(L, S), mamba::kGlrLane) * mamba::kGlrLane;
+  q.S = ceil_div(L, q.seg_len);
+}
+
+// Sizes-only plan of the forward pass: waves per row, and segments of L.
+GlrPlan make_glr_plan(int64_t B, int64_t D, int64_t L) {
+  GlrPlan q;
+  const int64_t rows = B * D, tiles = ceil_div(L, mamba::kGlrWave);
+  int64_t waves = ceil_div(8192, rows);
+  if (waves > 16) waves = 16;
+  const int forced = g_waves.load();
+  if (forced > 0) waves = forced;
+  if (waves > tiles) waves = tiles;
+  int64_t S = 1024 / (rows * waves);
+  if (S > tiles / (2 * waves)) S = tiles / (2 * waves);
+  const int64_t forced_s = g_segments.load();
+  if (forced_s > 0) S = forced_s;
+  cut(q, L, S < 1 ? 1 : S);
+  q.waves = (int)waves;
+  return q;
+}
+
+// The backward pass: a workgroup holds its segment on the chip.
+GlrPlan make_glr_bwd_plan(int64_t L) {
+  GlrPlan q;
+  const int forced = g_waves.load();
+  const int64_t most = (forced > 0 ? forced : 16) * int64_t(mamba::kGlrWave);
+  int64_t S = ceil_div(L, most);
+  const int64_t forced_s = g_segments.load();
+  if (forced_s > S) S = forced_s;
+  cut(q, L, S);
+  q.waves = (int)ceil_div(q.seg_len, mamba::kGlrWave);
+  return q;
+}
+
+bool glr_sizes_ok(int64_t B, int64_t D, int64_t L) { return product_ok(B, D, L); }
+
+int check_glr(const mamba::GlrParams& p, int in_dtype, int out_dtype, unsigned flags) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return MAMBA_ERR_DTYPE;
+  if (flags & ~MAMBA_FLAG_BLEND) return MAMBA_ERR_UNSUPPORTED;
+  if (!glr_sizes_ok(p.B, p.D, p.L)) return MAMBA_ERR_SHAPE;
+  const int64_t row = p.D * p.L;
+  if (!stride_ok(p.x_stride, p.B, row) || !stride_ok(p.r_stride, p.B, row)) return MAMBA_ERR_SHAPE;
+  if ((p.i && !stride_ok(p.i_stride, p.B, row)) || (p.z && !stride_ok(p.z_stride, p.B, row))) return MAMBA_ERR_SHAPE;
+  if (!p.x || !p.r || (!p.blend && !p.A)) return MAMBA_ERR_NULL;
+  if (!all_aligned({p.x, p.r, p.i, p.z}, width(in_dtype))) return MAMBA_ERR_ALIGN;
+  if (!all_aligned({p.A, p.r_bias, p.i_bias, p.init, p.lengths, p.slots, p.final_state}, 4)) return MAMBA_ERR_ALIGN;
+  return MAMBA_OK;
+}
+
+mamba::GlrParams glr_params(const void* x, const void* r, const void* i, const void* z, const float* A,
+                            const float* r_bias, const float* i_bias, int64_t B, int64_t D, int64_t L, int64_t xs,
+                            int64_t rs, int64_t is, int64_t zs, unsigned flags) {
+  mamba::GlrParams p{};
+  p.x = x; p.r = r; p.i = i; p.z = z;
+  p.A = A; p.r_bias = r_bias; p.i_bias = i ? i_bias : nullptr;
+  p.B = B; p.D = D; p.L = L; p.n_slots = B;
+  p.x_stride = xs; p.r_stride = rs; p.i_stride = is; p.z_stride = zs;
+  p.blend = (flags & MAMBA_FLAG_BLEND) ? 1 : 0;
+  p.S = 1;
+  return p;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+size_t glr_bytes(const GlrPlan& q, int64_t B, int64_t D) {
+  return q.S > 1 ? align256(size_t(B) * D * q.S * 2 * sizeof(float)) : 0;
+}
+size_t glr_bwd_sum_bytes(const GlrPlan& q, int64_t B, int64_t D) {
+  return q.S > 1 ? align256(size_t(B) * D * q.S * 3 * sizeof(float)) : 0;
+}
+size_t glr_bwd_bytes(const GlrPlan& q, int64_t B, int64_t D) {
+  return glr_bwd_sum_bytes(q, B, D) + align256(size_t(B) * q.S * 3 * D * sizeof(float));
+}
+
+bool norm_sizes_ok(int64_t B, int64_t D, int64_t L, int64_t G) {
+  return product_ok(B, D, L) && G >= 1 && D % G == 0;
+}
+
+// Parts of dweight and dbias: workgroups per group of channels.
+int64_t norm_parts(int64_t B, int64_t L, int64_t G) {
+  const int64_t tiles = L == 1 ? B : B * ceil_div(L, 64);
+  int64_t parts = ceil_div(1024, G);
+  if (parts < 8) parts = 8;
+  return parts < tiles ? parts : tiles;
+}
+
+int check_norm(const mamba::NormParams& p, int in_dtype, int out_dtype, unsigned flags) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return MAMBA_ERR_DTYPE;
+  if (flags & ~MAMBA_FLAG_RMS) return MAMBA_ERR_UNSUPPORTED;
+  if (!norm_sizes_ok(p.B, p.D, p.L, p.G)) return MAMBA_ERR_SHAPE;
+  if (!stride_ok(p.x_stride, p.B, p.D * p.L) || (p.z && !stride_ok(p.z_stride, p.B, p.D * p.L))) return MAMBA_ERR_SHAPE;
+  if (!(p.eps >= 0.0f)) return MAMBA_ERR_UNSUPPORTED;
+  if (!p.x) return MAMBA_ERR_NULL;
+  if (!all_aligned({p.x, p.z}, width(in_dtype)) || !all_aligned({p.weight, p.bias}, 4)) return MAMBA_ERR_ALIGN;
+  return MAMBA_OK;
+}
+
+mamba::NormParams norm_params(const void* x, const void* z, const float* weight, const float* bias, int64_t B, int64_t D,
+                              int64_t L, int64_t G, int64_t xs, int64_t zs, float eps, unsigned flags) {
+  mamba::NormParams p{};
+  p.x = x; p.z = z; p.weight = weight; p.bias = bias;
+  p.B = B; p.D = D; p.L = L; p.G = G;
+  p.x_stride = xs; p.z_stride = zs;
+  p.eps = eps;
+  p.rms = (flags & MAMBA_FLAG_RMS) ? 1 : 0;
+  return p;
+}
+
+// After the checks: G >= 1.
+void norm_group(mamba::NormParams& p) {
+  p.Dg = p.D / p.G;
+  p.inv_dg = (float)(1.0 / (double)p.Dg);
+}
+
+int status_of(hipError_t e) { return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP; }
+
+}  // namespace
+
+extern "C" {
+
+size_t mamba_glr_workspace_size(int64_t B, int64_t D, int64_t L) {
+  if (!glr_sizes_ok(B, D, L)) return (size_t)-1;
+  return glr_bytes(make_glr_plan(B, D, L), B, D);
+}
+
+int mamba_glr_fwd(const void* x, const void* r, const void* i, const void* z, const float* A, const float* r_bias,
+                  const float* i_bias, const float* initial_state, const int32_t* lengths, void* y, float* final_state,
+                  int64_t B, int64_t D, int64_t L, int64_t x_stride, int64_t r_stride, int64_t i_stride,
+                  int64_t z_stride, mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream) {
+  mamba::GlrParams p = glr_params(x, r, i, z, A, r_bias, i_bias, B, D, L, x_stride, r_stride, i_stride, z_stride, flags);
+  p.init = initial_state; p.lengths = lengths; p.y = y; p.final_state = final_state;
+  const int st = check_glr(p, in_dtype, out_dtype, flags);
+  if (st != MAMBA_OK) return st;
+  if (!y) return MAMBA_ERR_NULL;
+  if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
+  const GlrPlan q = make_glr_plan(B, D, L);
+  if (!mamba::launch_fits(B * D * q.S, 64 * q.waves)) return MAMBA_ERR_SHAPE;
+  const size_t need = glr_bytes(q, B, D);
+  if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
+  p.S = q.S; p.seg_len = q.seg_len; p.waves = q.waves;
+  p.sum = static_cast<float*>(workspace);
+  return status_of(mamba::launch_glr_fwd(p, dt_of(in_dtype), dt_of(out_dtype), stream));
+}
+
+int mamba_glr_update(float* state, const int32_t* slots, const void* x, const void* r, const void* i, const void* z,
+                     const float* A, const float* r_bias, const float* i_bias, void* y, int64_t B, int64_t D,
+                     int64_t n_slots, int64_t x_stride, int64_t r_stride, int64_t i_stride, int64_t z_stride,
+                     mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags, hipStream_t stream) {
+  mamba::GlrParams p = glr_params(x, r, i, z, A, r_bias, i_bias, B, D, 1, x_stride, r_stride, i_stride, z_stride, flags);
+  p.final_state = state; p.slots = slots; p.n_slots = n_slots; p.y = y;
+  const int st = check_glr(p, in_dtype, out_dtype, flags);
+  if (st != MAMBA_OK) return st;
+  if (!product_ok(n_slots, D, 1) || (!slots && n_slots < B)) return MAMBA_ERR_SHAPE;
+  if (!state || !y) return MAMBA_ERR_NULL;
+  if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
+  if (!mamba::launch_fits(B * ceil_div(D, 256), 256)) return MAMBA_ERR_SHAPE;
+  return status_of(mamba::launch_glr_update(p, dt_of(in_dtype), dt_of(out_dtype), stream));
+}
+
+size_t mamba_glr_bwd_workspace_size(int64_t B, int64_t D, int64_t L) {
+  if (!glr_sizes_ok(B, D, L)) return (size_t)-1;
+  return glr_bwd_bytes(make_glr_bwd_plan(L), B, D);
+}
+
+int mamba_glr_bwd(const void* x, const void* r, const void* i, const void* z, const float* A, const float* r_bias,
+                  const float* i_bias, const float* initial_state, const int32_t* lengths, const void* dy,
+                  const float* dfinal_state, void* dx, void* dr, void* di, void* dz, float* dA, float* dr_bias,
+                  float* di_bias, float* dinitial_state, int64_t B, int64_t D, int64_t L, int64_t x_stride,
+                  int64_t r_stride, int64_t i_stride, int64_t z_stride, mamba_dtype_t in_dtype,
+                  mamba_dtype_t grad_dtype, unsigned flags, void* workspace, size_t workspace_bytes,
+                  hipStream_t stream) {
+  mamba::GlrParams p = glr_params(x, r, i, z, A, r_bias, i_bias, B, D, L, x_stride, r_stride, i_stride, z_stride, flags);
+  p.init = initial_state; p.lengths = lengths;
+  const int st = check_glr(p, in_dtype, grad_dtype, flags);
+  if (st != MAMBA_OK) return st;
+  if (!dy || !dx || !dr || (i && !di) || (z && !dz) || (!p.blend && !dA) || !dr_bias || (i && !di_bias))
+    return MAMBA_ERR_NULL;
+  if (!all_aligned({dy, dx, dr, di, dz}, width(grad_dtype))) return MAMBA_ERR_ALIGN;
+  if (!all_aligned({dfinal_state, dA, dr_bias, di_bias, dinitial_state}, 4)) return MAMBA_ERR_ALIGN;
+  const GlrPlan q = make_glr_bwd_plan(L);
+  if (B * D > kMaxElems / q.S || !mamba::launch_fits(B * D * q.S, 64 * q.waves)) return MAMBA_ERR_SHAPE;
+  const size_t need = glr_bwd_bytes(q, B, D);
+  if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
+  p.S = q.S; p.seg_len = q.seg_len; p.waves = q.waves;
+  p.sum = static_cast<float*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + glr_bwd_sum_bytes(q, B, D));
+  p.dy = dy; p.dfinal = dfinal_state;
+  p.dx = dx; p.dr = dr; p.di = i ? di : nullptr; p.dz = z ? dz : nullptr;
+  p.dA = p.blend ? nullptr : dA; p.dr_bias = dr_bias; p.di_bias = i ? di_bias : nullptr;
+  p.dinit = dinitial_state;
+  return status_of(mamba::launch_glr_bwd(p, dt_of(in_dtype), dt_of(grad_dtype), stream));
+}
+
+int mamba_glr_set_test_knobs(int waves, int64_t segments) {
+  if (waves < 0 || waves > 16 || segments < 0) return MAMBA_ERR_SHAPE;
+  g_waves.store(waves);
+  g_segments.store(segments);
+  return MAMBA_OK;
+}
+
+int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, const float* bias, void* y, int64_t B,
+                         int64_t D, int64_t L, int64_t groups, int64_t x_stride, int64_t z_stride, float eps,
+                         mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags, hipStream_t stream) {
+  mamba::NormParams p = norm_params(x, z, weight, bias, B, D, L, groups, x_stride, z_stride, eps, flags);
+  p.y = y;
+  const int st = check_norm(p, in_dtype, out_dtype, flags);
+  if (st != MAMBA_OK) return st;
+  if (!y) return MAMBA_ERR_NULL;
+  if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
+  norm_group(p);
+  if (!mamba::launch_fits(B * groups * ceil_div(L, 64), 256)) return MAMBA_ERR_SHAPE;
+  return status_of(mamba::launch_norm_fwd(p, dt_of(in_dtype), dt_of(out_dtype), stream));
+}
+
+size_t mamba_layer_norm_bwd_workspace_size(int64_t B, int64_t D, int64_t L, int64_t groups) {
+  if (!norm_sizes_ok(B, D, L, groups)) return (size_t)-1;
+  return size_t(norm_parts(B, L, groups)) * 2 * D * sizeof(float);
+}
+
+int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, const float* bias, const void* dy, void* dx,
+                         void* dz, float* dweight, float* dbias, int64_t B, int64_t D, int64_t L, int64_t groups,
+                         int64_t x_stride, int64_t z_stride, float eps, mamba_dtype_t in_dtype,
+                         mamba_dtype_t grad_dtype, unsigned flags, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream) {
+  mamba::NormParams p = norm_params(x, z, weight, bias, B, D, L, groups, x_stride, z_stride, eps, flags);
+  const int st = check_norm(p, in_dtype, grad_dtype, flags);
+  if (st != MAMBA_OK) return st;
+  if (!dy || !dx || (z && !dz) || !dweight || !dbias) return MAMBA_ERR_NULL;
+  if (!all_aligned({dy, dx, dz}, width(grad_dtype)) || !all_aligned({dweight, dbias}, 4)) return MAMBA_ERR_ALIGN;
+  norm_group(p);
+  p.parts = norm_parts(B, L, groups);
+  if (!mamba::launch_fits(p.parts * groups, 256) || !mamba::launch_fits(ceil_div(2 * D, 32), 256)) return MAMBA_ERR_SHAPE;
+  const size_t need = size_t(p.parts) * 2 * D * sizeof(float);
+  if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
+  p.dy = dy; p.dx = dx; p.dz = z ? dz : nullptr; p.dweight = dweight; p.dbias = dbias;
+  p.part = static_cast<float*>(workspace);
+  return status_of(mamba::launch_norm_bwd(p, dt_of(in_dtype), dt_of(grad_dtype), stream));
+}
+
+}  // extern "C"

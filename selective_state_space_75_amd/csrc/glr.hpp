@@ -1,0 +1,235 @@
+// glr.hpp -- device helpers shared by the gated linear recurrence's and the layer norm's kernels (gfx950).
+#pragma once
+
+#include "device_math.hpp"
+#include "kernels.hpp"
+
+namespace mamba {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// The same at any element's alignment: the target takes unaligned global accesses.
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight consecutive numbers of a row as they lie in memory.
+template <typename T>
+struct Raw8 {
+  u32x4 w[sizeof(T) / 2];
+};
+
+// n < 8: only the first n are there, the others read as zero.
+template <typename T, bool kNT = false>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* p, int n) {
+  Raw8<T> o;
+  if (n >= 8) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+      const u32x4_u* q = reinterpret_cast<const u32x4_u*>(p) + k;
+      if constexpr (kNT) o.w[k] = __builtin_nontemporal_load(q);
+      else o.w[k] = *q;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) o.w[k] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < n) {
+        if constexpr (sizeof(T) == 2) o.w[0][j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+        else o.w[j / 4][j & 3] = __builtin_bit_cast(uint32_t, p[j]);
+      }
+    }
+  }
+  return o;
+}
+
+__device__ __forceinline__ float get8(const Raw8<uint16_t>& r, int j) {
+  return (j & 1) ? bf16_hi(r.w[0][j / 2]) : bf16_lo(r.w[0][j / 2]);
+}
+__device__ __forceinline__ float get8(const Raw8<float>& r, int j) {
+  const uint32_t w = r.w[j / 4][j & 3];      // a copy: a bit cast of a vector's element itself reads element 0
+  return __builtin_bit_cast(float, w);
+}
+
+__device__ __forceinline__ void put1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put1(uint16_t* p, float x) { *p = f32_to_bf16(x); }
+__device__ __forceinline__ float get1(const float* p) { return *p; }
+__device__ __forceinline__ float get1(const uint16_t* p) { return bf16_to_f32(*p); }
+
+// Eight consecutive numbers written: the first `live` as they are, up to `n` as zeros.
+template <typename O, bool kNT = true>
+__device__ __forceinline__ void store8(O* p, const float (&v)[8], int live, int n) {
+  if (live >= 8) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(O) / 2; ++k) {
+      u32x4 w;
+      if constexpr (sizeof(O) == 2) {
+        w = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      } else {
+        w = u32x4{__builtin_bit_cast(uint32_t, v[4 * k]), __builtin_bit_cast(uint32_t, v[4 * k + 1]),
+                  __builtin_bit_cast(uint32_t, v[4 * k + 2]), __builtin_bit_cast(uint32_t, v[4 * k + 3])};
+      }
+      u32x4_u* q = reinterpret_cast<u32x4_u*>(p) + k;
+      if constexpr (kNT) __builtin_nontemporal_store((u32x4_u)w, q);
+      else *q = w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) put1(p + j, j < live ? v[j] : 0.0f);
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return hw_rcp(1.0f + hw_exp2(-x * kLog2e)); }
+
+// One lane exchange of the scans: `old` where the control reaches no lane or the row mask leaves one out.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float dpp(float old, float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, x),
+                                                               kCtrl, kRows, 0xf, false));
+}
+__device__ __forceinline__ float lane_of(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
+// A stretch of the recurrence: it takes the state h in front of it to P h + H behind it.
+struct Affine {
+  float P = 1.0f, H = 0.0f;
+};
+
+// The stretch v, then the stretch `by`.
+__device__ __forceinline__ Affine glr_through(Affine v, Affine by) {
+  v.H = __builtin_fmaf(by.P, v.H, by.H);
+  v.P *= by.P;
+  return v;
+}
+
+// (P, H) of lanes 0 .. this one, in order, in every lane.  Four shifts inside the rows of 16
+// lanes, then the rows' last lanes handed on.
+__device__ __forceinline__ Affine scan_up(Affine v) {
+#define GLR_STEP(ctrl, rows)                                   \
+  {                                                            \
+    const float p = dpp<ctrl, rows>(1.0f, v.P);                \
+    const float h = dpp<ctrl, rows>(0.0f, v.H);                \
+    v.H = __builtin_fmaf(v.P, h, v.H);                         \
+    v.P *= p;                                                  \
+  }
+  GLR_STEP(0x111, 0xf)
+  GLR_STEP(0x112, 0xf)
+  GLR_STEP(0x114, 0xf)
+  GLR_STEP(0x118, 0xf)
+  GLR_STEP(0x142, 0xa)
+  GLR_STEP(0x143, 0xc)
+#undef GLR_STEP
+  return v;
+}
+// The lane below's; nothing for lane 0.
+__device__ __forceinline__ Affine shift_up(const Affine& v) {
+  Affine o;
+  o.P = dpp<0x138, 0xf>(1.0f, v.P);
+  o.H = dpp<0x138, 0xf>(0.0f, v.H);
+  return o;
+}
+
+// The same from lane 63 down to this one.  There is no broadcast from a row to the row below
+// it, so the rows' totals travel through scalar registers.
+__device__ __forceinline__ Affine scan_down(Affine v, int lane) {
+#define GLR_STEP(ctrl)                                         \
+  {                                                            \
+    const float p = dpp<ctrl, 0xf>(1.0f, v.P);                 \
+    const float h = dpp<ctrl, 0xf>(0.0f, v.H);                 \
+    v.H = __builtin_fmaf(v.P, h, v.H);                         \
+    v.P *= p;                                                  \
+  }
+  GLR_STEP(0x101)
+  GLR_STEP(0x102)
+  GLR_STEP(0x104)
+  GLR_STEP(0x108)
+#undef GLR_STEP
+  const float p1 = lane_of(v.P, 16), h1 = lane_of(v.H, 16);
+  const float p3 = lane_of(v.P, 48), h3 = lane_of(v.H, 48);
+  const int row = lane >> 4;
+  const float pa = row == 0 ? p1 : row == 2 ? p3 : 1.0f, ha = row == 0 ? h1 : row == 2 ? h3 : 0.0f;
+  v.H = __builtin_fmaf(v.P, ha, v.H);
+  v.P *= pa;
+  const float p2 = lane_of(v.P, 32), h2 = lane_of(v.H, 32);
+  const float pb = row < 2 ? p2 : 1.0f, hb = row < 2 ? h2 : 0.0f;
+  v.H = __builtin_fmaf(v.P, hb, v.H);
+  v.P *= pb;
+  return v;
+}
+__device__ __forceinline__ Affine shift_down(const Affine& v) {
+  Affine o;
+  o.P = dpp<0x130, 0xf>(1.0f, v.P);
+  o.H = dpp<0x130, 0xf>(0.0f, v.H);
+  return o;
+}
+
+// Sum over the wave in lane 63 (fixed order).
+__device__ __forceinline__ float wave_sum63(float x) {
+  x += dpp<0x111, 0xf>(0.0f, x);
+  x += dpp<0x112, 0xf>(0.0f, x);
+  x += dpp<0x114, 0xf>(0.0f, x);
+  x += dpp<0x118, 0xf>(0.0f, x);
+  x += dpp<0x142, 0xa>(0.0f, x);
+  x += dpp<0x143, 0xc>(0.0f, x);
+  return x;
+}
+
+// 1 - e^(2 l) for l = x2 ln2 <= 0, a = 2^x2 given.  For |2 l| < 1/8 the Taylor series to
+// (2 l)^5 (truncation below (1/8)^5 / 720 = 4.3e-8 relative); otherwise 1 - a^2 in one rounding,
+// where the error of a (about one unit of 2^-24) is at most 1e-6 of the result, 5e-7 of its root.
+__device__ __forceinline__ float glr_rest(float x2, float a) {
+  const float y = x2 * (2.0f * kLn2);
+  float p = __builtin_fmaf(y, 1.0f / 120.0f, 1.0f / 24.0f);
+  p = __builtin_fmaf(y, p, 1.0f / 6.0f);
+  p = __builtin_fmaf(y, p, 0.5f);
+  p = __builtin_fmaf(y, p, 1.0f);
+  return y > -0.125f ? -y * p : __builtin_fmaf(-a, a, 1.0f);
+}
+
+// The gates of a token.
+struct GlrGate {
+  float a, n, s;      // decay, input factor, sigmoid of r
+  float ra;           // a^2 / n: minus the derivative of n with respect to log a (decay rule)
+};
+
+// nb: -bias log2(e); A2: A log2(e).  r = -inf stands for a token that is not there: s = 0, a = 1.
+// n is held to 3e-19 or more, so that its reciprocal stays finite where s underflows.
+template <bool kBlend>
+__device__ __forceinline__ GlrGate glr_gate(float r, float nb, float A2) {
+  GlrGate o;
+  float e = hw_exp2(__builtin_fmaf(r, -kLog2e, nb));
+  if constexpr (kBlend) {
+    e = __builtin_fminf(e, 0x1p126f);
+    o.s = hw_rcp(1.0f + e);
+    o.a = e * o.s;
+    o.n = o.s;
+    o.ra = 0.0f;
+  } else {
+    o.s = hw_rcp(1.0f + e);
+    const float x2 = A2 * o.s;
+    o.a = hw_exp2(x2);
+    float q = glr_rest(x2, o.a);
+    q = q < 1e-37f ? 1e-37f : q;               // a comparison, so that a NaN stays one
+    const float rs = __builtin_amdgcn_rsqf(q);
+    o.n = q * rs;
+    o.ra = o.a * o.a * rs;
+  }
+  return o;
+}
+
+// Tokens of batch row b that count: all L, or lengths[b] held to 0 .. L.
+__device__ __forceinline__ int64_t glr_length(const GlrParams& p, int64_t b) {
+  if (!p.lengths) return p.L;
+  const int64_t n = p.lengths[b];
+  return n < 0 ? 0 : n > p.L ? p.L : n;
+}
+
+__device__ __forceinline__ int clamp8(int64_t n) { return n < 0 ? 0 : n > 8 ? 8 : (int)n; }
+
+// r of a token that is not there.
+template <typename T>
+__device__ __forceinline__ float glr_r(const Raw8<T>& r, int j, int live) {
+  return j < live ? get8(r, j) : -__builtin_inff();
+}
+
+}  // namespace mamba

@@ -222,6 +222,49 @@ struct CacheParams {
   int vec;                  // n % 4 == 0 and aligned for four numbers at a time
 };
 
+// Gated linear recurrence: one state per channel (rows = B * D).
+struct GlrParams {
+  const void *x, *r, *i, *z;                    // (B, D, L) in dtype; i, z may be null
+  const float *A, *r_bias, *i_bias;             // (D); biases may be null, A null with blend
+  const float* init;                            // (B, D) or null; update: the pool (n_slots, D)
+  const int32_t* lengths;                       // (B) or null
+  const int32_t* slots;                         // (B) or null (update)
+  void* y;                                      // (B, D, L) out dtype
+  float* final_state;                           // (B, D) or null; update: the pool
+  int64_t B, D, L, n_slots;
+  int64_t x_stride, r_stride, i_stride, z_stride;   // elements from one batch row to the next
+  int64_t S, seg_len;                           // segments of L, a multiple of 8 tokens each
+  int waves;                                    // waves of a workgroup: 512 tokens of a row each at a time
+  int blend;
+  float* sum;                                   // S > 1: (rows, S, 2) P and H of each segment (backward: (rows, S, 3), and C)
+  // backward pass
+  const void* dy;                               // (B, D, L) grad dtype
+  const float* dfinal;                          // (B, D) or null
+  void *dx, *dr, *di, *dz;                      // grad dtype, dense
+  float *dA, *dr_bias, *di_bias;                // (D)
+  float* dinit;                                 // (B, D) or null
+  float* part;                                  // (B * S, 3, D): sums over a segment
+};
+constexpr int kGlrLane = 8;                     // consecutive tokens of a lane
+constexpr int kGlrWave = 64 * kGlrLane;         // and of a wave
+
+// Layer norm over groups of Dg channels.
+struct NormParams {
+  const void *x, *z;                            // (B, D, L) in dtype; z may be null
+  const float *weight, *bias;                   // (D) or null
+  void* y;                                      // (B, D, L) out dtype
+  int64_t B, D, L, G, Dg;
+  int64_t x_stride, z_stride;
+  float eps, inv_dg;
+  int rms;
+  // backward pass
+  const void* dy;                               // (B, D, L) grad dtype
+  void *dx, *dz;
+  float *dweight, *dbias;                       // (D)
+  float* part;                                  // (parts, 2, D) sums of dweight and dbias
+  int64_t parts;
+};
+
 // Whether a launch of this many workgroups is one: HIP takes fewer than 2^32 threads in all.
 inline bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups <= int64_t(0xffffffff) / threads; }
 
@@ -259,6 +302,11 @@ hipError_t launch_gdr_chunk(const GdrChunkParams& p, Dt in, Dt out, hipStream_t 
 hipError_t launch_gdr_prep(const GdrChunkParams& p, Dt in, Dt grad, bool bwd, hipStream_t s);
 hipError_t launch_gdr_states(const GdrChunkParams& p, Dt in, hipStream_t s);
 hipError_t launch_gdr_bwd(const GdrChunkParams& p, Dt in, Dt grad, hipStream_t s);
+hipError_t launch_glr_fwd(const GlrParams& p, Dt in, Dt out, hipStream_t s);
+hipError_t launch_glr_update(const GlrParams& p, Dt in, Dt out, hipStream_t s);
+hipError_t launch_glr_bwd(const GlrParams& p, Dt in, Dt grad, hipStream_t s);
+hipError_t launch_norm_fwd(const NormParams& p, Dt in, Dt out, hipStream_t s);
+hipError_t launch_norm_bwd(const NormParams& p, Dt in, Dt grad, hipStream_t s);
 hipError_t launch_state_cache(const CacheParams& p, Dt dt, bool write, hipStream_t s);
 
 }  // namespace mamba

@@ -38,6 +38,7 @@ _ID_PARAMS, _ID_DELTA, _ID_U, _ID_Z, _ID_B, _ID_C, _ID_STATE = range(7)
 _ID_CONV_X, _ID_CONV_PARAMS, _ID_CONV_STATE = range(7, 10)
 _ID_SSD_PARAMS, _ID_SSD_X, _ID_SSD_DT, _ID_SSD_Z, _ID_SSD_B, _ID_SSD_C = range(10, 16)
 _ID_GDR_PARAMS, _ID_GDR_Q, _ID_GDR_K, _ID_GDR_V, _ID_GDR_DT, _ID_GDR_BETA, _ID_GDR_S, _ID_GDR_DY = range(16, 24)
+_ID_GLR_PARAMS, _ID_GLR_X, _ID_GLR_R, _ID_GLR_I, _ID_GLR_Z, _ID_GLR_DY, _ID_GLR_S, _ID_NORM_PARAMS, _ID_NORM_X = range(24, 33)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -366,3 +367,33 @@ def gdr_inputs(B: int, H: int, G: int, P: int, N: int, L: int, dtype: str, seed:
     st = _normal_f32([seed, _ID_GDR_S], 2 * B * H * P * N).reshape(2, B, H * P, N) * np.float32(0.1)
     out["initial_state"], out["dfinal_state"] = st[0].copy(), st[1].copy()
     return out
+
+
+# ----------------------------------------------------------------------------- gated linear recurrence, layer norm
+def glr_inputs(B: int, D: int, L: int, dtype: str, seed: int) -> dict:
+    """x, r, i, z, dy (B, D, L) ~ N(0, 1) in `dtype` (bf16 as uint16 bit patterns); A = 8 log u with
+    u ~ U[0.9, 0.999] per channel (a wholly open gate keeps u^8 of the state per token); r_bias,
+    i_bias ~ N(0, 0.5); initial_state, dfinal_state (B, D) ~ N(0, 0.5); all fp32."""
+    g = np.random.Generator(np.random.PCG64(np.random.SeedSequence([seed, _ID_GLR_PARAMS])))
+    out = {"A": (8.0 * np.log(g.uniform(0.9, 0.999, size=D))).astype(np.float32),
+           "r_bias": (0.5 * g.standard_normal(D)).astype(np.float32),
+           "i_bias": (0.5 * g.standard_normal(D)).astype(np.float32)}
+    for name, k in (("x", _ID_GLR_X), ("r", _ID_GLR_R), ("i", _ID_GLR_I), ("z", _ID_GLR_Z), ("dy", _ID_GLR_DY)):
+        out[name] = _store(_normal_f32([seed, k], B * D * L).reshape(B, D, L), dtype)
+    st = _normal_f32([seed, _ID_GLR_S], 2 * B * D).reshape(2, B, D) * np.float32(0.5)
+    out["initial_state"], out["dfinal_state"] = st[0].copy(), st[1].copy()
+    return out
+
+
+def norm_inputs(shape, dtype: str, seed: int, offset: float = 0.5) -> dict:
+    """x, z, dy of `shape` (B, D, L) or (rows, D) in `dtype`: x with a scale and an offset per
+    channel, exp(0.5 N) and offset * N; weight 1 + 0.2 N, bias 0.1 N (D) fp32."""
+    D = shape[1]
+    g = np.random.Generator(np.random.PCG64(np.random.SeedSequence([seed, _ID_NORM_PARAMS])))
+    per = (1, D) + (1,) * (len(shape) - 2)
+    n = int(np.prod(shape))
+    draw = _normal_f32([seed, _ID_NORM_X], 3 * n).reshape((3,) + tuple(shape))
+    x = draw[0] * np.exp(0.5 * g.standard_normal(per)) + offset * g.standard_normal(per)
+    return {"x": _store(x.astype(np.float32), dtype), "z": _store(draw[1], dtype), "dy": _store(draw[2], dtype),
+            "weight": (1.0 + 0.2 * g.standard_normal(D)).astype(np.float32),
+            "bias": (0.1 * g.standard_normal(D)).astype(np.float32)}

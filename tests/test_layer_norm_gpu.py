@@ -1,0 +1,202 @@
+"""The layer norm over channels on the GPU against the fp64 oracle: both layouts, groups, gates, types,
+sizes around every boundary, offsets and alignments.
+
+Bars.  x - mean is off by the mean's rounding (2^-24 of its size; inputs here are offset by half their
+scale) and one rounding, the root by about one unit: 1e-6 relative L2 leaves a factor of five.  Gradients
+of x relative to the size of the terms that they are differences of (the oracle's "scale"), weight sums
+relative to the sums of magnitudes, summed in fp32 over fixed trees, 2e-6.  bf16 results add one rounding."""
+import numpy as np
+import pytest
+
+from helpers import f64, from_dev, log, to_dev
+from oracle import glr as O
+from selective_state_space_75_amd import workloads as W
+from test_glr_gpu import near
+
+pytestmark = pytest.mark.gpu
+
+E = 1e-6
+
+#        shape            groups dtype  out    gated  rms   affine ranges
+CASES = [((1, 1, 1), 1, "f32", "f32", False, False, True, False),
+         ((2, 7, 3), 1, "f32", "f32", True, False, True, False),
+         ((2, 16, 9), 4, "bf16", "f32", False, True, True, True),
+         ((3, 60, 65), 3, "f32", "bf16", True, True, False, False),
+         ((1, 96, 64), 1, "bf16", "bf16", False, False, True, False),
+         ((2, 80, 63), 1, "bf16", "f32", True, False, True, True),
+         ((2, 384, 129), 3, "f32", "f32", True, True, True, True),
+         ((1, 1000, 130), 1, "bf16", "f32", False, False, True, False),
+         ((1, 2047, 40), 1, "f32", "f32", False, False, True, False),
+         ((1, 2500, 17), 1, "bf16", "f32", True, False, True, False),
+         ((1, 5120, 72), 1, "bf16", "f32", False, False, True, False),
+         ((1, 5000, 33), 1, "f32", "f32", True, False, True, True),
+         ((1, 10007, 10), 1, "bf16", "f32", False, False, True, False),
+         ((1, 9000, 21), 1, "f32", "f32", True, True, True, False),
+         ((70, 24, 5), 2, "bf16", "f32", False, False, True, False),
+         ((1, 1), 1, "f32", "f32", False, False, True, False),
+         ((5, 7), 7, "f32", "f32", True, True, True, False),
+         ((3, 8), 1, "bf16", "f32", False, False, True, False),
+         ((4, 100), 4, "bf16", "bf16", True, False, True, True),
+         ((130, 768), 6, "f32", "f32", True, True, True, True),
+         ((9, 513), 1, "bf16", "f32", False, False, False, False),
+         ((600, 1000), 1, "bf16", "f32", True, False, True, False),
+         ((33, 5120), 1, "bf16", "f32", False, False, True, True),
+         ((5, 4097), 1, "f32", "f32", True, False, True, False),
+         ((3, 20001), 1, "bf16", "f32", False, False, True, False),
+         ((2, 70001), 1, "f32", "f32", True, True, True, False)]
+
+
+def tensors(shape, dtype, seed, gated, affine, ranges, dev, offset=0.5):
+    import torch
+    x = W.norm_inputs(shape, dtype, seed, offset)
+    t = {n: to_dev(x[n], dev) for n in x}
+    if not gated:
+        x["z"] = t["z"] = None
+    if not affine:
+        x["weight"] = x["bias"] = t["weight"] = t["bias"] = None
+    if ranges:                                         # channel ranges of a wider tensor
+        D = shape[1]
+        wide = torch.cat([t["x"], t["dy"] if t["z"] is None else t["z"], t["x"][:, :1]], 1)
+        t["x"] = wide[:, :D]
+        if gated:
+            t["z"] = wide[:, D:2 * D]
+    return x, t
+
+
+def opt(x):
+    return None if x is None else f64(x)
+
+
+@pytest.mark.parametrize("shape,groups,dtype,out,gated,rms,affine,ranges", CASES)
+def test_forward_and_backward(shape, groups, dtype, out, gated, rms, affine, ranges, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    log("[norm] %s" % ((shape, groups, dtype, out, gated, rms, affine, ranges),))
+    x, t = tensors(shape, dtype, 400 + shape[1], gated, affine, ranges, dev)
+    kw = dict(groups=groups, rms=rms)
+    odt = torch.float32 if out == "f32" else torch.bfloat16
+    y = m.layer_norm_fwd(t["x"], t["weight"], t["bias"], t["z"], out_dtype=odt, **kw)
+    ins = (f64(x["x"]), opt(x["weight"]), opt(x["bias"]), opt(x["z"]))
+    yr = O.layer_norm(*ins, **kw)
+    near(y, yr, E, "y", np.maximum(np.abs(yr), 1e-3 if shape[1] // groups == 1 else 0.0))
+    dy = t["dy"].to(odt)
+    g = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], dy, **kw)
+    torch.cuda.synchronize()
+    ref = O.layer_norm_bwd(*ins, f64(from_dev(dy)), **kw)
+    near(g["dx"], ref["dx"], E, "dx", ref["scale"]["dx"])
+    if gated:
+        near(g["dz"], ref["dz"], E, "dz")
+    else:
+        assert g["dz"] is None
+    for n in ("dweight", "dbias"):
+        near(g[n], ref[n], 2 * E, n, np.maximum(ref["scale"][n], 1e-30))
+
+
+@pytest.mark.parametrize("shape", [(2, 300, 50), (20, 1500), (1, 6000, 20), (2, 40000)])
+def test_a_large_mean_is_taken_off(shape, dev):
+    """Offsets a thousand times the spread: x - mean loses 2^-24 of the offset, 1e3 * 6e-8 = 6e-5 of the
+    spread per number, to the inputs' own rounding none (they are given); the variance around the mean is
+    unhurt, where a difference of squares would lose all of it."""
+    import selective_state_space_75_amd as m
+    x, t = tensors(shape, "f32", 77, False, True, False, dev)
+    t["x"] = t["x"] * 0.5 + 1000.0
+    xs = from_dev(t["x"])
+    y = m.layer_norm_fwd(t["x"], t["weight"], t["bias"])
+    near(y, O.layer_norm(xs, x["weight"], x["bias"]), 1.2e-4, "y")
+    g = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], None, t["dy"])
+    ref = O.layer_norm_bwd(xs, x["weight"], x["bias"], None, f64(x["dy"]))
+    near(g["dx"], ref["dx"], 2.4e-4, "dx", ref["scale"]["dx"])
+
+
+@pytest.mark.parametrize("shape,groups", [((2, 24, 70), 2), ((1, 3000, 30), 1), ((9, 640), 4), ((3, 30000), 1)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_stays_in_its_token_and_group(shape, groups, bad, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    x, t = tensors(shape, "f32", 78, True, True, False, dev)
+    kw = dict(groups=groups)
+    at = (shape[0] - 1, 5) + ((17,) if len(shape) == 3 else ())
+    a = m.layer_norm_fwd(t["x"], t["weight"], t["bias"], t["z"], **kw)
+    ga = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"], **kw)
+    q = t["x"].clone()
+    q[at] = bad
+    b = m.layer_norm_fwd(q, t["weight"], t["bias"], t["z"], **kw)
+    gb = m.layer_norm_bwd(q, t["weight"], t["bias"], t["z"], t["dy"], **kw)
+    torch.cuda.synchronize()
+    own = torch.zeros(shape, dtype=torch.bool, device=dev)
+    own[(at[0], slice(0, shape[1] // groups)) + at[2:]] = True
+    for u, v in ((a, b), (ga["dx"], gb["dx"]), (ga["dz"], gb["dz"])):
+        assert torch.equal(u[~own], v[~own])
+    assert torch.isnan(b[own]).all()
+
+
+@pytest.mark.parametrize("shape,groups", [((2, 30, 67), 3), ((1, 2100, 19), 1), ((7, 1030), 2), ((3, 9), 3)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_alignment_and_neighbours(shape, groups, dtype, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    x, t = tensors(shape, dtype, 79, True, True, False, dev)
+    n = t["x"].numel()
+    kw = dict(groups=groups)
+    ref = m.layer_norm_fwd(t["x"], t["weight"], t["bias"], t["z"], **kw)
+    gref = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"], **kw)
+    for off in (1, 5):
+        q = {k: torch.empty(n + 16, dtype=t[k].dtype, device=dev)[off:off + n].view(shape).copy_(t[k]) for k in ("x", "z", "dy")}
+        out = torch.full((n + 32,), 5.0, dtype=ref.dtype, device=dev)
+        m.layer_norm_fwd(q["x"], t["weight"], t["bias"], q["z"], y=out[8 + off:8 + off + n].view(shape), **kw)
+        g = m.layer_norm_bwd(q["x"], t["weight"], t["bias"], q["z"], q["dy"], **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(out[8 + off:8 + off + n].view(shape), ref)
+        assert (out[:8 + off] == 5.0).all() and (out[8 + off + n:] == 5.0).all()
+        for k in gref:
+            assert torch.equal(g[k], gref[k]), k
+
+
+def test_a_tokens_bits_do_not_depend_on_the_batch(dev):
+    import torch
+    import selective_state_space_75_amd as m
+    for shape in ((6, 700, 40), (900, 700)):
+        x, t = tensors(shape, "bf16", 80, True, True, False, dev)
+        y = m.layer_norm_fwd(t["x"], t["weight"], t["bias"], t["z"])
+        g = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"])
+        one = slice(3, 4)
+        z1 = t["z"][one]
+        assert torch.equal(m.layer_norm_fwd(t["x"][one], t["weight"], t["bias"], z1), y[one])
+        g1 = m.layer_norm_bwd(t["x"][one], t["weight"], t["bias"], z1, t["dy"][one])
+        assert torch.equal(g1["dx"], g["dx"][one]) and torch.equal(g1["dz"], g["dz"][one])
+        again = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"])
+        assert all(torch.equal(again[n], g[n]) for n in g)
+
+
+def test_zero_variance_and_eps(dev):
+    import torch
+    import selective_state_space_75_amd as m
+    for shape in ((1, 64, 16), (4, 64)):
+        x = torch.full(shape, 3.0, device=dev)
+        assert not from_dev(m.layer_norm_fwd(x)).any()                            # x - mean = 0
+        y = m.layer_norm_fwd(x, rms=True, eps=7.0)
+        assert np.allclose(from_dev(y), 3.0 / 4.0, rtol=1e-6)
+
+
+def test_refusals_on_the_gpu(dev):
+    import torch
+    import selective_state_space_75_amd as m
+    x = torch.zeros(2, 6, 8, device=dev)
+    with pytest.raises(ValueError, match="do not divide"):
+        m.layer_norm_fwd(x, groups=4)
+    with pytest.raises(ValueError, match="do not divide"):
+        m.layer_norm_fwd(x, groups=0)
+    with pytest.raises(TypeError, match="weight has dtype"):
+        m.layer_norm_fwd(x, torch.ones(6, device=dev).bfloat16())
+    with pytest.raises(ValueError, match="z has shape"):
+        m.layer_norm_fwd(x, None, None, x[:, :3])
+    with pytest.raises(ValueError, match="dense within"):
+        m.layer_norm_fwd(x.transpose(1, 2))
+    with pytest.raises(m.MambaError):
+        m.layer_norm_fwd(x, eps=-1.0)
+    with pytest.raises(TypeError, match="dy must be"):
+        m.layer_norm_bwd(x, None, None, None, None)
+    with pytest.raises(m.MambaError):
+        m.layer_norm_bwd(x, None, None, None, x, workspace=torch.empty(8, dtype=torch.uint8, device=dev))
+    with pytest.raises(ValueError, match="y has shape"):
+        m.layer_norm_fwd(x, y=torch.zeros(2, 6, 9, device=dev))
