@@ -826,30 +826,72 @@ class glr_test_knobs:  # noqa: N801 (used as a context manager)
         return False
 
 
-def _rows_of(t, name, shape, dtype, device):
-    """(tensor, row stride) of a (B, ...) input that may be a channel range, or (None, 0)."""
-    return (None, 0) if t is None else (t, _check_rows(t, name, shape, dtype, device))
+def _row_stride(t, name, shape, dtype, device):
+    """_check_rows without the view it makes: for a call of one token the checks are most of the
+    call.  (B, D, L) or (B, D); an absent tensor has stride 0.  What is not plainly right is left to
+    _check_rows, which names it."""
+    if t is None:
+        return 0
+    if isinstance(t, _torch().Tensor) and t.dtype == dtype and t.shape == shape and t.device == device:
+        row = 1
+        for n in shape[1:]:
+            row *= n
+        if t.is_contiguous():
+            return row
+        s = t.stride()
+        if shape[0] > 1 and s[0] >= row and s[-1] == 1 and (len(s) == 2 or s[1] == shape[2]):
+            return s[0]
+    return _check_rows(t, name, shape, dtype, device)
+
+
+def _plain(t, name, shape, dtype, device):
+    """_check for a tensor or None, the address in its place."""
+    if t is None:
+        return None
+    if not (isinstance(t, _torch().Tensor) and t.dtype == dtype and t.shape == shape and t.is_contiguous()
+            and t.device == device):
+        _check(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _there(dev, stream):
+    """_on, which is entered only where the call's device is not the current one or a stream is given."""
+    if stream is None and _torch().cuda.current_device() == dev.index:
+        return _HERE
+    return _on(dev, stream)
+
+
+def _raw_stream(dev, stream):
+    return _torch()._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
 def _first(x, dims, what):
-    """Checks the input that the others are held to, and returns its device and dtype."""
-    if not isinstance(x, _torch().Tensor):
+    """Checks the input that the others are held to, and returns its device, dtype and dtype code."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() not in dims:
         raise ValueError("x must be %s" % what)
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("inputs must be on a GPU device")
-    _dtype_code(x)
-    return x.device, x.dtype
+    return x.device, x.dtype, _dtype_code(x)
 
 
 def _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend):
-    """Checks of the inputs that every call of the recurrence has; returns the batch strides."""
-    torch = _torch()
-    shape, dev, dt, D = tuple(x.shape), x.device, x.dtype, x.shape[1]
+    """Checks of the inputs that every call of the recurrence has; returns the addresses of x, r, i, z, A
+    and the biases, and the batch strides."""
+    shape, dev, dt = x.shape, x.device, x.dtype
     if r is None:
         raise TypeError("r must be a torch.Tensor")
-    strides = [_rows_of(t, n, shape, dt, dev)[1] for t, n in ((x, "x"), (r, "r"), (i, "i"), (z, "z"))]
+    strides = (_row_stride(x, "x", shape, dt, dev), _row_stride(r, "r", shape, dt, dev),
+               _row_stride(i, "i", shape, dt, dev), _row_stride(z, "z", shape, dt, dev))
     if blend:
         if A is not None:
             raise ValueError("A is not used with blend=True and must be None")
@@ -857,9 +899,9 @@ def _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend):
         raise ValueError("A is needed unless blend=True")
     if i is None and i_bias is not None:
         raise ValueError("i_bias without i")
-    for t, n in ((A, "A"), (r_bias, "r_bias"), (i_bias, "i_bias")):
-        _check(t, n, (D,), torch.float32, dev)
-    return strides
+    per, f32 = (shape[1],), _torch().float32
+    return (x.data_ptr(), r.data_ptr(), _addr(i), _addr(z), _plain(A, "A", per, f32, dev),
+            _plain(r_bias, "r_bias", per, f32, dev), _plain(i_bias, "i_bias", per, f32, dev)), strides
 
 
 def glr_workspace_size(B: int, D: int, L: int) -> int:
@@ -884,25 +926,24 @@ def glr_fwd(x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *, blend=Fal
     Returns y (B, D, L), or (y, final_state (B, D) fp32) when return_final_state.
     """
     torch = _torch()
-    dev, in_dt = _first(x, (3,), "(B, D, L)")
-    B, D, L = x.shape
-    strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
-    _check(initial_state, "initial_state", (B, D), torch.float32, dev)
-    _check(lengths, "lengths", (B,), torch.int32, dev)
+    dev, in_dt, code = _first(x, (3,), "(B, D, L)")
+    B, D, L = shape = x.shape
+    ins, strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
+    init = _plain(initial_state, "initial_state", (B, D), torch.float32, dev)
+    ends = _plain(lengths, "lengths", (B,), torch.int32, dev)
     out_dt = in_dt if out_dtype is None else out_dtype
-    with _on(dev, stream):
+    with _there(dev, stream):
         if y is None:
-            y = torch.empty((B, D, L), dtype=out_dt, device=dev)
-        _check(y, "y", (B, D, L), out_dt, dev)
+            y = torch.empty(shape, dtype=out_dt, device=dev)
+        yp, last = _plain(y, "y", shape, out_dt, dev), None
         if return_final_state:
             if final_state is None:
                 final_state = torch.empty((B, D), dtype=torch.float32, device=dev)
-            _check(final_state, "final_state", (B, D), torch.float32, dev)
+            last = _plain(final_state, "final_state", (B, D), torch.float32, dev)
         workspace = _workspace(workspace, glr_workspace_size(B, D, L), dev)
-        st = lib().mamba_glr_fwd(
-            _ptr(x), _ptr(r), _ptr(i), _ptr(z), _ptr(A), _ptr(r_bias), _ptr(i_bias), _ptr(initial_state), _ptr(lengths),
-            _ptr(y), _ptr(final_state if return_final_state else None), B, D, L, *strides, _dtype_code(x),
-            _dtype_code(y), FLAG_BLEND if blend else 0, _ptr(workspace), _nbytes(workspace), _stream(dev, stream))
+        st = lib().mamba_glr_fwd(*ins, init, ends, yp, last, B, D, L, *strides, code, _dtype_code(y),
+                                 FLAG_BLEND if blend else 0, _addr(workspace), _nbytes(workspace),
+                                 _raw_stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_glr_fwd")
     return (y, final_state) if return_final_state else y
@@ -926,32 +967,28 @@ def glr_bwd(x, r, i, A, r_bias, i_bias, z, dy, *, blend=False, initial_state=Non
     (None without initial_state).
     """
     torch = _torch()
-    dev, _ = _first(x, (3,), "(B, D, L)")
-    B, D, L = x.shape
-    strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
-    _check(initial_state, "initial_state", (B, D), torch.float32, dev)
-    _check(dfinal_state, "dfinal_state", (B, D), torch.float32, dev)
-    _check(lengths, "lengths", (B,), torch.int32, dev)
-    if dy is None:
+    dev, _, code = _first(x, (3,), "(B, D, L)")
+    B, D, L = shape = x.shape
+    ins, strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
+    init = _plain(initial_state, "initial_state", (B, D), torch.float32, dev)
+    dfinal = _plain(dfinal_state, "dfinal_state", (B, D), torch.float32, dev)
+    ends = _plain(lengths, "lengths", (B,), torch.int32, dev)
+    if not isinstance(dy, torch.Tensor):
         raise TypeError("dy must be a torch.Tensor")
-    _check(dy, "dy", (B, D, L), None, dev)
-    gcode = _dtype_code(dy)
-    with _on(dev, stream):
-        def new(*shape, dtype=dy.dtype, wanted=True):
+    gdt, gcode = dy.dtype, _dtype_code(dy)
+    dyp = _plain(dy, "dy", shape, gdt, dev)
+    with _there(dev, stream):
+        def new(shape, dtype, wanted=True):
             return torch.empty(shape, dtype=dtype, device=dev) if wanted else None
 
         f32 = torch.float32
-        out = {"dx": new(B, D, L), "dr": new(B, D, L), "di": new(B, D, L, wanted=i is not None),
-               "dz": new(B, D, L, wanted=z is not None), "dA": new(D, dtype=f32, wanted=not blend),
-               "dr_bias": new(D, dtype=f32), "di_bias": new(D, dtype=f32, wanted=i is not None),
-               "dinitial_state": new(B, D, dtype=f32, wanted=initial_state is not None)}
+        out = {"dx": new(shape, gdt), "dr": new(shape, gdt), "di": new(shape, gdt, i is not None),
+               "dz": new(shape, gdt, z is not None), "dA": new((D,), f32, not blend), "dr_bias": new((D,), f32),
+               "di_bias": new((D,), f32, i is not None), "dinitial_state": new((B, D), f32, init is not None)}
         workspace = _workspace(workspace, glr_bwd_workspace_size(B, D, L), dev)
-        st = lib().mamba_glr_bwd(
-            _ptr(x), _ptr(r), _ptr(i), _ptr(z), _ptr(A), _ptr(r_bias), _ptr(i_bias), _ptr(initial_state), _ptr(lengths),
-            _ptr(dy), _ptr(dfinal_state), _ptr(out["dx"]), _ptr(out["dr"]), _ptr(out["di"]), _ptr(out["dz"]),
-            _ptr(out["dA"]), _ptr(out["dr_bias"]), _ptr(out["di_bias"]), _ptr(out["dinitial_state"]), B, D, L, *strides,
-            _dtype_code(x), gcode, FLAG_BLEND if blend else 0, _ptr(workspace), _nbytes(workspace),
-            _stream(dev, stream))
+        st = lib().mamba_glr_bwd(*ins, init, ends, dyp, dfinal, *[_addr(t) for t in out.values()], B, D, L, *strides,
+                                 code, gcode, FLAG_BLEND if blend else 0, _addr(workspace), _nbytes(workspace),
+                                 _raw_stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_glr_bwd")
     return out
@@ -963,22 +1000,20 @@ def glr_update(state, x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *,
     place at the rows' slots (int32 (B); None: row b has state b; negative: an empty row, y = 0).
     x, r, i, z: (B, D).  Returns y (B, D)."""
     torch = _torch()
-    dev, in_dt = _first(x, (2,), "(B, D)")
-    B, D = x.shape
-    if state is None or state.dim() != 2:
+    dev, in_dt, code = _first(x, (2,), "(B, D)")
+    B, D = shape = x.shape
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
         raise ValueError("state must be (S, D)")
-    strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
-    _check(state, "state", (state.shape[0], D), torch.float32, dev)
-    _check(slots, "slots", (B,), torch.int32, dev)
+    ins, strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
+    S = state.shape[0]
+    pool = _plain(state, "state", (S, D), torch.float32, dev)
+    rows = _plain(slots, "slots", (B,), torch.int32, dev)
     out_dt = in_dt if out_dtype is None else out_dtype
-    with _on(dev, stream):
+    with _there(dev, stream):
         if y is None:
-            y = torch.empty((B, D), dtype=out_dt, device=dev)
-        _check(y, "y", (B, D), out_dt, dev)
-        st = lib().mamba_glr_update(
-            _ptr(state), _ptr(slots), _ptr(x), _ptr(r), _ptr(i), _ptr(z), _ptr(A), _ptr(r_bias), _ptr(i_bias), _ptr(y),
-            B, D, state.shape[0], *strides, _dtype_code(x), _dtype_code(y), FLAG_BLEND if blend else 0,
-            _stream(dev, stream))
+            y = torch.empty(shape, dtype=out_dt, device=dev)
+        st = lib().mamba_glr_update(pool, rows, *ins, _plain(y, "y", shape, out_dt, dev), B, D, S, *strides, code,
+                                    _dtype_code(y), FLAG_BLEND if blend else 0, _raw_stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_glr_update")
     return y
@@ -986,17 +1021,17 @@ def glr_update(state, x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *,
 
 # ----------------------------------------------------------------------------- layer norm over channels
 def _norm_inputs(x, weight, bias, z, groups):
-    """Checks of the norm's inputs; returns (B, D, L, batch strides of x and z)."""
-    torch = _torch()
-    dev, dt = _first(x, (2, 3), "(B, D, L) or (rows, D)")
-    B, D = x.shape[:2]
-    L = x.shape[2] if x.dim() == 3 else 1
-    if int(groups) < 1 or D % int(groups):
-        raise ValueError("%d channels do not divide into %s groups" % (D, groups))
-    strides = [_rows_of(t, n, tuple(x.shape), dt, dev)[1] for t, n in ((x, "x"), (z, "z"))]
-    _check(weight, "weight", (D,), torch.float32, dev)
-    _check(bias, "bias", (D,), torch.float32, dev)
-    return B, D, L, strides
+    """Checks of the norm's inputs; returns the device, x's dtype code, the addresses of x, z, weight and
+    bias, and (B, D, L, groups, batch strides of x and z)."""
+    f32 = _torch().float32
+    dev, dt, code = _first(x, (2, 3), "(B, D, L) or (rows, D)")
+    shape, groups = x.shape, int(groups)
+    D = shape[1]
+    if groups < 1 or D % groups:
+        raise ValueError("%d channels do not divide into %d groups" % (D, groups))
+    strides = _row_stride(x, "x", shape, dt, dev), _row_stride(z, "z", shape, dt, dev)
+    ins = (x.data_ptr(), _addr(z), _plain(weight, "weight", (D,), f32, dev), _plain(bias, "bias", (D,), f32, dev))
+    return dev, code, ins, (shape[0], D, shape[2] if len(shape) == 3 else 1, groups) + strides
 
 
 def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms=False, out_dtype=None, y=None,
@@ -1007,16 +1042,13 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms
     token-major rows; both may be channel ranges of a wider tensor.  weight, bias: (D) fp32 or None.
     Returns y like x, in out_dtype."""
     torch = _torch()
-    B, D, L, strides = _norm_inputs(x, weight, bias, z, groups)
-    dev = x.device
+    dev, code, ins, sizes = _norm_inputs(x, weight, bias, z, groups)
     out_dt = x.dtype if out_dtype is None else out_dtype
-    with _on(dev, stream):
+    with _there(dev, stream):
         if y is None:
             y = torch.empty(x.shape, dtype=out_dt, device=dev)
-        _check(y, "y", tuple(x.shape), out_dt, dev)
-        st = lib().mamba_layer_norm_fwd(
-            _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(y), B, D, L, int(groups), *strides, float(eps),
-            _dtype_code(x), _dtype_code(y), FLAG_RMS if rms else 0, _stream(dev, stream))
+        st = lib().mamba_layer_norm_fwd(*ins, _plain(y, "y", x.shape, out_dt, dev), *sizes, eps, code, _dtype_code(y),
+                                        FLAG_RMS if rms else 0, _raw_stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_layer_norm_fwd")
     return y
@@ -1034,22 +1066,20 @@ def layer_norm_bwd(x, weight, bias, z, dy, *, groups=1, eps=1e-5, rms=False, wor
     """Gradients of layer_norm_fwd for the output gradient dy (like x).  Returns a dict: dx, dz like x
     in dy's dtype (dz None without z); dweight, dbias (D) fp32, also where weight or bias is None."""
     torch = _torch()
-    B, D, L, strides = _norm_inputs(x, weight, bias, z, groups)
-    dev = x.device
-    if dy is None:
+    dev, code, ins, sizes = _norm_inputs(x, weight, bias, z, groups)
+    if not isinstance(dy, torch.Tensor):
         raise TypeError("dy must be a torch.Tensor")
-    _check(dy, "dy", tuple(x.shape), None, dev)
-    gcode = _dtype_code(dy)
-    with _on(dev, stream):
-        out = {"dx": torch.empty(x.shape, dtype=dy.dtype, device=dev),
-               "dz": None if z is None else torch.empty(x.shape, dtype=dy.dtype, device=dev),
-               "dweight": torch.empty((D,), dtype=torch.float32, device=dev),
-               "dbias": torch.empty((D,), dtype=torch.float32, device=dev)}
-        workspace = _workspace(workspace, layer_norm_bwd_workspace_size(B, D, L, int(groups)), dev)
-        st = lib().mamba_layer_norm_bwd(
-            _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(out["dx"]), _ptr(out["dz"]), _ptr(out["dweight"]),
-            _ptr(out["dbias"]), B, D, L, int(groups), *strides, float(eps), _dtype_code(x), gcode,
-            FLAG_RMS if rms else 0, _ptr(workspace), _nbytes(workspace), _stream(dev, stream))
+    shape, gdt, gcode = x.shape, dy.dtype, _dtype_code(dy)
+    dyp = _plain(dy, "dy", shape, gdt, dev)
+    with _there(dev, stream):
+        out = {"dx": torch.empty(shape, dtype=gdt, device=dev),
+               "dz": None if z is None else torch.empty(shape, dtype=gdt, device=dev),
+               "dweight": torch.empty(shape[1], dtype=torch.float32, device=dev),
+               "dbias": torch.empty(shape[1], dtype=torch.float32, device=dev)}
+        workspace = _workspace(workspace, layer_norm_bwd_workspace_size(*sizes[:4]), dev)
+        st = lib().mamba_layer_norm_bwd(*ins, dyp, *[_addr(t) for t in out.values()], *sizes, eps, code, gcode,
+                                        FLAG_RMS if rms else 0, _addr(workspace), _nbytes(workspace),
+                                        _raw_stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_layer_norm_bwd")
     return out

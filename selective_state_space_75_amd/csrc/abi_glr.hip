@@ -122,12 +122,21 @@ bool norm_sizes_ok(int64_t B, int64_t D, int64_t L, int64_t G) {
   return product_ok(B, D, L) && G >= 1 && D % G == 0;
 }
 
-// Parts of dweight and dbias: workgroups per group of channels.
-int64_t norm_parts(int64_t B, int64_t L, int64_t G) {
-  const int64_t tiles = L == 1 ? B : B * ceil_div(L, 64);
-  int64_t parts = ceil_div(1024, G);
-  if (parts < 8) parts = 8;
-  return parts < tiles ? parts : tiles;
+// The plan depends on the element widths and the gate; the workspace is enough for all of them.
+size_t norm_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
+  int64_t parts = 0;
+  for (int in : {2, 4})
+    for (int grad : {2, 4})
+      for (bool gate : {false, true}) {
+        const int64_t n = mamba::norm_plan(B, D, L, G, in, grad, gate).parts;
+        if (n > parts) parts = n;
+      }
+  return size_t(parts) * 2 * D * sizeof(float);
+}
+
+// Workgroups of a launch by its plan.
+bool norm_fits(const mamba::NormPlan& q, int64_t items) {
+  return mamba::launch_fits(q.kind == mamba::kNormRowTeam ? ceil_div(items, 256 / q.lanes) : items, q.threads);
 }
 
 int check_norm(const mamba::NormParams& p, int in_dtype, int out_dtype, unsigned flags) {
@@ -153,9 +162,12 @@ mamba::NormParams norm_params(const void* x, const void* z, const float* weight,
 }
 
 // After the checks: G >= 1.
-void norm_group(mamba::NormParams& p) {
+void norm_set(mamba::NormParams& p, const mamba::NormPlan& q) {
   p.Dg = p.D / p.G;
   p.inv_dg = (float)(1.0 / (double)p.Dg);
+  p.tiles = q.tiles;
+  p.team = q.lanes;
+  p.parts = q.parts;
 }
 
 int status_of(hipError_t e) { return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP; }
@@ -256,14 +268,15 @@ int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, cons
   if (st != MAMBA_OK) return st;
   if (!y) return MAMBA_ERR_NULL;
   if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
-  norm_group(p);
-  if (!mamba::launch_fits(B * groups * ceil_div(L, 64), 256)) return MAMBA_ERR_SHAPE;
-  return status_of(mamba::launch_norm_fwd(p, dt_of(in_dtype), dt_of(out_dtype), stream));
+  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), 0, z != nullptr);
+  if (!norm_fits(q, B * groups * q.tiles)) return MAMBA_ERR_SHAPE;
+  norm_set(p, q);
+  return status_of(mamba::launch_norm_fwd(p, q, dt_of(in_dtype), dt_of(out_dtype), stream));
 }
 
 size_t mamba_layer_norm_bwd_workspace_size(int64_t B, int64_t D, int64_t L, int64_t groups) {
   if (!norm_sizes_ok(B, D, L, groups)) return (size_t)-1;
-  return size_t(norm_parts(B, L, groups)) * 2 * D * sizeof(float);
+  return norm_bytes(B, D, L, groups);
 }
 
 int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, const float* bias, const void* dy, void* dx,
@@ -276,15 +289,16 @@ int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, cons
   if (st != MAMBA_OK) return st;
   if (!dy || !dx || (z && !dz) || !dweight || !dbias) return MAMBA_ERR_NULL;
   if (!all_aligned({dy, dx, dz}, width(grad_dtype)) || !all_aligned({dweight, dbias}, 4)) return MAMBA_ERR_ALIGN;
-  norm_group(p);
-  p.parts = norm_parts(B, L, groups);
-  if (!mamba::launch_fits(p.parts * groups, 256) || !mamba::launch_fits(ceil_div(2 * D, 32), 256)) return MAMBA_ERR_SHAPE;
-  const size_t need = size_t(p.parts) * 2 * D * sizeof(float);
+  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), (int)width(grad_dtype),
+                                              z != nullptr);
+  if (!norm_fits(q, q.parts * groups) || !mamba::launch_fits(ceil_div(2 * D, 32), 256)) return MAMBA_ERR_SHAPE;
+  norm_set(p, q);
+  const size_t need = norm_bytes(B, D, L, groups);
   if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
   p.dy = dy; p.dx = dx; p.dz = z ? dz : nullptr; p.dweight = dweight; p.dbias = dbias;
   p.part = static_cast<float*>(workspace);
-  return status_of(mamba::launch_norm_bwd(p, dt_of(in_dtype), dt_of(grad_dtype), stream));
+  return status_of(mamba::launch_norm_bwd(p, q, dt_of(in_dtype), dt_of(grad_dtype), stream));
 }
 
 }  // extern "C"

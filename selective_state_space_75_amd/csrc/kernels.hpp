@@ -257,6 +257,8 @@ struct NormParams {
   int64_t x_stride, z_stride;
   float eps, inv_dg;
   int rms;
+  int64_t tiles;                                // tiles of a row's tokens (channel-major)
+  int team;                                     // threads of a token (token-major)
   // backward pass
   const void* dy;                               // (B, D, L) grad dtype
   void *dx, *dz;
@@ -264,6 +266,34 @@ struct NormParams {
   float* part;                                  // (parts, 2, D) sums of dweight and dbias
   int64_t parts;
 };
+
+// How the norm is carried out (sizes and element widths only).
+//   0 .. 5        channel-major, at least 8 tokens: a workgroup's tile of 8 * lanes tokens is held in
+//                 registers, in the smallest of the shapes below that holds the group
+//   kNormColLong  channel-major, any group and any length: the tile is read again for every sweep
+//   kNormRowTeam  token-major, 8 to 512 channels: teams of 2^k <= 64 lanes, 8 channels each
+//   kNormRowBlock token-major, up to 8192 channels: a workgroup, 8 channels a thread
+//   kNormRowLong  token-major, any group
+enum NormKind : int { kNormShapes = 6, kNormColLong = 6, kNormRowTeam, kNormRowBlock, kNormRowLong };
+
+struct NormShape {
+  int threads, lanes, chans;                    // workgroup, token lanes of 8 tokens, channels of a thread
+};
+// Registers of a channel's 8 tokens: 4 in the forward pass of 2-byte inputs; 8 of 4-byte inputs, and in
+// the backward pass of two 2-byte arrays (which has no room for 20 channels next to a gate); 12 or 16 in that
+// with a 4-byte array.
+constexpr NormShape kNorm4[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {1024, 8, 16}, {1024, 4, 20}, {1024, 2, 16}};
+constexpr NormShape kNorm8[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {512, 4, 20}, {512, 2, 20}, {512, 1, 16}};
+constexpr NormShape kNorm8Gate[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {512, 4, 16}, {512, 2, 16}, {512, 1, 16}};
+constexpr NormShape kNorm16[kNormShapes] = {{256, 8, 4}, {256, 8, 8}, {512, 8, 8}, {512, 4, 8}, {512, 2, 8}, {512, 1, 8}};
+constexpr int64_t kNormMostLds = 7680;          // channels whose numbers in LDS, 16 bytes each, leave room for the sums
+
+struct NormPlan {
+  int kind, threads, lanes;
+  int64_t tiles, parts;                         // tiles of a row's tokens; parts of the weight's sums (backward)
+};
+NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width,
+                   bool gate);                  // grad_width 0: forward
 
 // Whether a launch of this many workgroups is one: HIP takes fewer than 2^32 threads in all.
 inline bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups <= int64_t(0xffffffff) / threads; }
@@ -305,8 +335,8 @@ hipError_t launch_gdr_bwd(const GdrChunkParams& p, Dt in, Dt grad, hipStream_t s
 hipError_t launch_glr_fwd(const GlrParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_glr_update(const GlrParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrParams& p, Dt in, Dt grad, hipStream_t s);
-hipError_t launch_norm_fwd(const NormParams& p, Dt in, Dt out, hipStream_t s);
-hipError_t launch_norm_bwd(const NormParams& p, Dt in, Dt grad, hipStream_t s);
+hipError_t launch_norm_fwd(const NormParams& p, const NormPlan& q, Dt in, Dt out, hipStream_t s);
+hipError_t launch_norm_bwd(const NormParams& p, const NormPlan& q, Dt in, Dt grad, hipStream_t s);
 hipError_t launch_state_cache(const CacheParams& p, Dt dt, bool write, hipStream_t s);
 
 }  // namespace mamba

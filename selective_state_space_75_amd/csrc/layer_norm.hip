@@ -1,316 +1,276 @@
-// layer_norm.hip -- the layer norm over channels and its gradients (gfx950).
+// layer_norm.hip -- the layer norm over channels, forward (gfx950), and the plan of both passes.
 //
 // Per token and group of Dg channels: xh = (x - mean) k, k = 1 / sqrt(var + eps) (rms: mean = 0 and the
-// mean of x^2), m = xh w + b, y = m silu(z).  With dm = dy silu(z) and g = dm w:
-//     dx = k (g - mean(g) - xh mean(g xh))  (rms: without mean(g)),  dz = dy m sigma (1 + z (1 - sigma)),
-//     dw = sum over tokens of dm xh,  db = sum of dm.
+// mean of x^2), y = (xh w + b) silu(z).  One read of x (and z) and one write of y is what HBM has to
+// carry, so the tile stays on the chip between the sweeps for the mean, the variance and the result.
 //
-// Two forms.  Channel-major (L > 1): channels are L apart, so a thread takes 8 consecutive tokens
-// of a channel (one load) and neighbouring lanes the tokens after them; the sums run over the channel
-// lanes of a workgroup.  Token-major (L = 1): a row's channels lie together, and a thread takes 8 of
-// them.  One read of each input and one write of each output is what HBM has to carry.
-#include "glr.hpp"
+// Channel-major (L > 1): channels are L apart, so a thread takes 8 consecutive tokens (one load) of every
+// CL-th channel, neighbouring lanes the tokens after them, and the sums run over a workgroup's CL channel
+// lanes.  Token-major (L = 1): a row's channels lie together; a thread takes 8 of them.
+#include "layer_norm.hpp"
 
 namespace mamba {
 namespace {
 
-// Sums of kN numbers over the lanes of a workgroup that share threadIdx.x % kT, in every lane.
-// lds: waves * kT * kN floats.
-template <int kT, int kN>
-__device__ __forceinline__ void group_sum(float (&v)[kN], float* lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-#pragma unroll
-  for (int m = kT; m < 64; m *= 2) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] += __shfl_xor(v[j], m);
-  }
-  if (waves == 1) return;
-  __syncthreads();                       // an earlier sum may still be read
-  if (lane < kT) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j) lds[(wave * kT + lane) * kN + j] = v[j];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kN; ++j) v[j] = 0.0f;
-  for (int w = 0; w < waves; ++w) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] += lds[(w * kT + lane % kT) * kN + j];
-  }
-}
+template <typename T, typename O, int kThreads, int kT, int kC>
+__global__ __launch_bounds__(kThreads) void norm_col_fwd_kernel(NormParams p) {
+  constexpr int kCL = kThreads / kT;
+  __shared__ float lds[(kThreads / 64 + 1) * kT * 8];
+  extern __shared__ float affine[];                      // weight, bias of the group
+  const int64_t id = by_xcd(blockIdx.x, gridDim.x);
+  const int64_t bg = id / p.tiles, tile = id - bg * p.tiles;
+  const int64_t b = bg / p.G, ch = (bg - b * p.G) * p.Dg;
+  const int Dg = (int)p.Dg, c0 = threadIdx.x / kT;
+  // The last lane of a row takes its last 8 tokens whole: those that the lane before it has too come out
+  // of the same sums, with the same bits.
+  const int64_t t0 = tile * (8 * kT) + (threadIdx.x % kT) * 8;
+  const bool on = t0 < p.L;
+  const int64_t t = t0 < p.L - 8 ? t0 : p.L - 8;
+  const uint32_t at = (uint32_t)(c0 * p.L + t);
+  const int64_t step = kCL * p.L;
+  const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch * p.L;
+  const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch * p.L : nullptr;
+  O* y = static_cast<O*>(p.y) + (b * p.D + ch) * p.L;
 
-// 1 / sqrt(v), the hardware's root with one Newton step (about half an ulp): it goes into every
-// number of the token.
-__device__ __forceinline__ float norm_root(float v) {
-  const float r = __builtin_amdgcn_rsqf(v);
-  const float h = __builtin_fmaf(-0.5f * v * r, r, 1.5f);
-  return r * (v < 1e37f && v > 1e-37f ? h : 1.0f);
-}
-
-constexpr int kLanes = 8;                // token lanes: 64 tokens, 128 bytes of bf16
-
-// Statistics of 8 tokens over the group's channels, in two sweeps.
-template <typename T>
-__device__ __forceinline__ void col_stats(const NormParams& p, const T* x, int live, float (&mu)[8], float (&k)[8],
-                                          float* lds) {
-  const int64_t c0 = threadIdx.x / kLanes, step = blockDim.x / kLanes;
+  Raw8<T> r[kC];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) mu[j] = k[j] = 0.0f;
+  for (int k = 0; k < kC; ++k) {
+    if (c0 + k * kCL < Dg) r[k] = load_all8(lane_at(x + k * step, at));
+  }
+  for (int c = threadIdx.x; c < Dg; c += kThreads) {
+    affine[c] = p.weight ? p.weight[ch + c] : 1.0f;
+    affine[Dg + c] = p.bias ? p.bias[ch + c] : 0.0f;
+  }
+  float mu[8], v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) mu[j] = v[j] = 0.0f;
   if (!p.rms) {
-    for (int64_t c = c0; c < p.Dg; c += step) {
-      const Raw8<T> r = load_raw8(x + c * p.L, live);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mu[j] += get8(r, j);
+    for (int k = 0; k < kC; ++k) {
+      if (c0 + k * kCL < Dg) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mu[j] += get8(r[k], j);
+      }
     }
-    group_sum<kLanes, 8>(mu, lds);
+    group_sum<kT, 8, kThreads>(mu, lds);
 #pragma unroll
     for (int j = 0; j < 8; ++j) mu[j] *= p.inv_dg;
   }
-  for (int64_t c = c0; c < p.Dg; c += step) {
-    const Raw8<T> r = load_raw8(x + c * p.L, live);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = get8(r, j) - mu[j];
-      k[j] = __builtin_fmaf(v, v, k[j]);
+  for (int k = 0; k < kC; ++k)
+    if (k * kCL < Dg) keep(r[k]);
+#pragma unroll
+  for (int k = 0; k < kC; ++k) {
+    if (c0 + k * kCL < Dg) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = get8(r[k], j) - mu[j];
+        v[j] = __builtin_fmaf(d, d, v[j]);
+      }
     }
   }
-  group_sum<kLanes, 8>(k, lds);
+  group_sum<kT, 8, kThreads>(v, lds);                    // its barriers also publish `affine`
 #pragma unroll
-  for (int j = 0; j < 8; ++j) k[j] = norm_root(__builtin_fmaf(k[j], p.inv_dg, p.eps));
+  for (int j = 0; j < 8; ++j) v[j] = norm_root(__builtin_fmaf(v[j], p.inv_dg, p.eps));
+#pragma unroll
+  for (int k = 0; k < kC; ++k)
+    if (k * kCL < Dg) keep(r[k]);
+#pragma unroll
+  for (int kk = 0; kk < kC; kk += 4) {
+    if (kk * kCL >= Dg) continue;
+    Raw8<T> zr[4];
+    if (z) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (c0 + (kk + i) * kCL < Dg) zr[i] = load_all8(lane_at(z + (kk + i) * step, at));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + (kk + i) * kCL;
+      if (c < Dg && on) {
+        const float w = affine[c], bias = affine[Dg + c];
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf((get8(r[kk + i], j) - mu[j]) * v[j], w, bias);
+        if (z) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr[i], j));
+        }
+        store8(lane_at(y + (kk + i) * step, at), o, 8, 8);
+      }
+    }
+  }
 }
 
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void norm_col_fwd_kernel(NormParams p) {
-  __shared__ float lds[4 * kLanes * 8];
-  const int64_t tiles = (p.L + 8 * kLanes - 1) / (8 * kLanes);
-  const int64_t bg = blockIdx.x / tiles, tile = blockIdx.x - bg * tiles;
+// Any group, any length: kTok (8 or 1) tokens a lane, 8 lanes of them, three sweeps over the tile.
+template <typename T, typename O, int kTok>
+__global__ __launch_bounds__(256) void norm_col_long_fwd_kernel(NormParams p) {
+  __shared__ float lds[5 * 8 * 8];
+  const int64_t bg = blockIdx.x / p.tiles, tile = blockIdx.x - bg * p.tiles;
   const int64_t b = bg / p.G, ch = (bg - b * p.G) * p.Dg;
-  const int64_t t = tile * (8 * kLanes) + (threadIdx.x % kLanes) * 8;
-  const int live = clamp8(p.L - t);
+  const int64_t t = (tile * 8 + threadIdx.x % 8) * kTok;
+  const int live = kTok == 8 ? clamp8(p.L - t) : t < p.L ? 1 : 0;
   const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch * p.L + t;
   const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch * p.L + t : nullptr;
   O* y = static_cast<O*>(p.y) + (b * p.D + ch) * p.L + t;
   float mu[8], k[8];
-  col_stats(p, x, live, mu, k, lds);
-  for (int64_t c = threadIdx.x / kLanes; c < p.Dg; c += blockDim.x / kLanes) {
-    const Raw8<T> r = load_raw8(x + c * p.L, live);
+  norm_col_stats<T, kTok>(p, x, live, mu, k, lds);
+  for (int64_t c = threadIdx.x / 8; c < p.Dg; c += 32) {
+    float v[kTok], o[8];
+    load_tok<T, kTok>(x + c * p.L, live, v);
     const float w = p.weight ? p.weight[ch + c] : 1.0f, bias = p.bias ? p.bias[ch + c] : 0.0f;
-    float o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf((get8(r, j) - mu[j]) * k[j], w, bias);
+    for (int j = 0; j < kTok; ++j) o[j] = __builtin_fmaf((v[j] - mu[j]) * k[j], w, bias);
     if (z) {
-      const Raw8<T> zr = load_raw8(z + c * p.L, live);
+      load_tok<T, kTok>(z + c * p.L, live, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr, j));
+      for (int j = 0; j < kTok; ++j) o[j] *= silu(v[j]);
     }
-    store8(y + c * p.L, o, live, live);
+    store_tok<O, kTok>(y + c * p.L, live, o);
   }
 }
 
-// A workgroup takes every parts-th tile and keeps its sums of dweight and dbias in its part of p.part.
-template <typename T, typename Gr>
-__global__ __launch_bounds__(256) void norm_col_bwd_kernel(NormParams p) {
-  __shared__ float lds[4 * kLanes * 16];
-  const int64_t tiles = (p.L + 8 * kLanes - 1) / (8 * kLanes);
-  const int64_t part = blockIdx.x / p.G, ch = (blockIdx.x - part * p.G) * p.Dg;
-  float* sums = p.part + part * 2 * p.D + ch;
-  bool first = true;
-  for (int64_t i = part; i < p.B * tiles; i += p.parts, first = false) {
-    const int64_t b = i / tiles, t = (i - b * tiles) * (8 * kLanes) + (threadIdx.x % kLanes) * 8;
-    const int live = clamp8(p.L - t);
-    const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch * p.L + t;
-    const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch * p.L + t : nullptr;
-    const int64_t at = (b * p.D + ch) * p.L + t;
-    const Gr* dy = static_cast<const Gr*>(p.dy) + at;
-    float mu[8], k[8], sg[16];
-    col_stats(p, x, live, mu, k, lds);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) sg[j] = 0.0f;
-    for (int64_t c = threadIdx.x / kLanes; c < p.Dg; c += blockDim.x / kLanes) {
-      const Raw8<T> r = load_raw8(x + c * p.L, live);
-      const Raw8<Gr> dr = load_raw8(dy + c * p.L, live);
-      const float w = p.weight ? p.weight[ch + c] : 1.0f;
-      float g[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = get8(dr, j) * w;
-      if (z) {
-        const Raw8<T> zr = load_raw8(z + c * p.L, live);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] *= silu(get8(zr, j));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sg[j] += g[j];
-        sg[8 + j] = __builtin_fmaf(g[j], (get8(r, j) - mu[j]) * k[j], sg[8 + j]);
-      }
-    }
-    group_sum<kLanes, 16>(sg, lds);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sg[j] = p.rms ? 0.0f : sg[j] * p.inv_dg;
-      sg[8 + j] *= p.inv_dg;
-    }
-    for (int64_t c = threadIdx.x / kLanes; c < p.Dg; c += blockDim.x / kLanes) {
-      const Raw8<T> r = load_raw8(x + c * p.L, live);
-      const Raw8<Gr> dr = load_raw8(dy + c * p.L, live);
-      const float w = p.weight ? p.weight[ch + c] : 1.0f, bias = p.bias ? p.bias[ch + c] : 0.0f;
-      float dm[8], o[8], sw = 0.0f, sb = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dm[j] = get8(dr, j);
-      if (z) {
-        const Raw8<T> zr = load_raw8(z + c * p.L, live);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float zj = get8(zr, j), s = sigmoid(zj);
-          o[j] = dm[j] * __builtin_fmaf((get8(r, j) - mu[j]) * k[j], w, bias) * s * __builtin_fmaf(zj, 1.0f - s, 1.0f);
-          dm[j] *= zj * s;
-        }
-        store8(static_cast<Gr*>(p.dz) + at + c * p.L, o, live, live);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xh = (get8(r, j) - mu[j]) * k[j];
-        o[j] = k[j] * (dm[j] * w - sg[j] - xh * sg[8 + j]);
-        if (j < live) {
-          sw = __builtin_fmaf(dm[j], xh, sw);
-          sb += dm[j];
-        }
-      }
-      store8(static_cast<Gr*>(p.dx) + at + c * p.L, o, live, live);
-#pragma unroll
-      for (int m = 1; m < kLanes; m *= 2) {
-        sw += __shfl_xor(sw, m);
-        sb += __shfl_xor(sb, m);
-      }
-      if (threadIdx.x % kLanes == 0) {
-        sums[c] = first ? sw : sums[c] + sw;
-        sums[p.D + c] = first ? sb : sums[p.D + c] + sb;
-      }
-    }
-  }
-}
-
-// Token-major: a workgroup per row and group.
-template <typename T>
-__device__ __forceinline__ void row_stats(const NormParams& p, const T* x, float& mu, float& k, float* lds) {
-  float v[1] = {0.0f};
+// Token-major: a team of lanes, or a workgroup, per token and group; 8 channels a thread.  The last
+// thread takes the group's last 8 channels whole; those that the one before it has too (the first
+// `dup` of them) are left out of the sums.
+template <typename T, typename O, bool kBlock>
+__global__ __launch_bounds__(kBlock ? 1024 : 256) void norm_row_fwd_kernel(NormParams p) {
+  __shared__ float lds[16];
+  const int team = p.team;
+  const int64_t id = kBlock ? blockIdx.x : (int64_t)blockIdx.x * (256 / team) + threadIdx.x / team;
+  const int at = (kBlock ? threadIdx.x : threadIdx.x % team) * 8, Dg = (int)p.Dg;
+  const bool on = at < Dg && id < p.B * p.G;
+  const int64_t bg = id < p.B * p.G ? id : 0;
+  const int64_t b = bg / p.G, ch = (bg - b * p.G) * p.Dg;
+  const int c = at < Dg - 8 ? at : Dg - 8, dup = on ? at - c : 8;
+  const Raw8<T> r = load_all8(static_cast<const T*>(p.x) + b * p.x_stride + ch + c);
+  Raw8<T> zr;
+  Raw8<float> w, bias;
+  if (p.z) zr = load_all8(static_cast<const T*>(p.z) + b * p.z_stride + ch + c);
+  if (p.weight) w = load_all8(p.weight + ch + c);
+  if (p.bias) bias = load_all8(p.bias + ch + c);
+  float mu[1] = {0.0f}, k[1] = {0.0f};
   if (!p.rms) {
-    for (int64_t c = threadIdx.x; c < p.Dg; c += blockDim.x) v[0] += get1(x + c);
-    group_sum<1, 1>(v, lds);
-    v[0] *= p.inv_dg;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mu[0] += j < dup ? 0.0f : get8(r, j);
+    team_sum<1, kBlock>(mu, team, lds);
+    mu[0] *= p.inv_dg;
   }
-  mu = v[0];
-  v[0] = 0.0f;
-  for (int64_t c = threadIdx.x; c < p.Dg; c += blockDim.x) {
-    const float d = get1(x + c) - mu;
-    v[0] = __builtin_fmaf(d, d, v[0]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float d = j < dup ? 0.0f : get8(r, j) - mu[0];
+    k[0] = __builtin_fmaf(d, d, k[0]);
   }
-  group_sum<1, 1>(v, lds);
-  k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
+  team_sum<1, kBlock>(k, team, lds);
+  k[0] = norm_root(__builtin_fmaf(k[0], p.inv_dg, p.eps));
+  if (!on) return;
+  float o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    o[j] = __builtin_fmaf((get8(r, j) - mu[0]) * k[0], p.weight ? get8(w, j) : 1.0f, p.bias ? get8(bias, j) : 0.0f);
+  if (p.z) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr, j));
+  }
+  store8(static_cast<O*>(p.y) + b * p.D + ch + c, o, 8, 8);
 }
 
+// Token-major, any group: a workgroup per token and group, three sweeps.
 template <typename T, typename O>
-__global__ __launch_bounds__(256) void norm_row_fwd_kernel(NormParams p) {
+__global__ __launch_bounds__(256) void norm_row_long_fwd_kernel(NormParams p) {
   __shared__ float lds[4];
   const int64_t b = blockIdx.x / p.G, ch = (blockIdx.x - b * p.G) * p.Dg;
   const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch;
   const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch : nullptr;
   O* y = static_cast<O*>(p.y) + b * p.D + ch;
   float mu, k;
-  row_stats(p, x, mu, k, lds);
-  for (int64_t c = threadIdx.x; c < p.Dg; c += blockDim.x) {
+  norm_row_stats(p, x, mu, k, lds);
+  for (int64_t c = threadIdx.x; c < p.Dg; c += 256) {
     float o = __builtin_fmaf((get1(x + c) - mu) * k, p.weight ? p.weight[ch + c] : 1.0f, p.bias ? p.bias[ch + c] : 0.0f);
     if (z) o *= silu(get1(z + c));
     put1(y + c, o);
   }
 }
 
-template <typename T, typename Gr>
-__global__ __launch_bounds__(256) void norm_row_bwd_kernel(NormParams p) {
-  __shared__ float lds[8];
-  const int64_t part = blockIdx.x / p.G, ch = (blockIdx.x - part * p.G) * p.Dg;
-  float* sums = p.part + part * 2 * p.D + ch;
-  bool first = true;
-  for (int64_t b = part; b < p.B; b += p.parts, first = false) {
-    const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch;
-    const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch : nullptr;
-    const int64_t at = b * p.D + ch;
-    const Gr* dy = static_cast<const Gr*>(p.dy) + at;
-    float mu, k, sg[2] = {0.0f, 0.0f};
-    row_stats(p, x, mu, k, lds);
-    for (int64_t c = threadIdx.x; c < p.Dg; c += blockDim.x) {
-      float g = get1(dy + c) * (p.weight ? p.weight[ch + c] : 1.0f);
-      if (z) g *= silu(get1(z + c));
-      sg[0] += g;
-      sg[1] = __builtin_fmaf(g, (get1(x + c) - mu) * k, sg[1]);
-    }
-    group_sum<1, 2>(sg, lds);
-    sg[0] = p.rms ? 0.0f : sg[0] * p.inv_dg;
-    sg[1] *= p.inv_dg;
-    for (int64_t c = threadIdx.x; c < p.Dg; c += blockDim.x) {
-      const float w = p.weight ? p.weight[ch + c] : 1.0f, xh = (get1(x + c) - mu) * k;
-      float dm = get1(dy + c);
-      if (z) {
-        const float zj = get1(z + c), s = sigmoid(zj);
-        put1(static_cast<Gr*>(p.dz) + at + c, dm * __builtin_fmaf(xh, w, p.bias ? p.bias[ch + c] : 0.0f) * s *
-                                                   __builtin_fmaf(zj, 1.0f - s, 1.0f));
-        dm *= zj * s;
-      }
-      put1(static_cast<Gr*>(p.dx) + at + c, k * (dm * w - sg[0] - xh * sg[1]));
-      sums[c] = first ? dm * xh : __builtin_fmaf(dm, xh, sums[c]);
-      sums[p.D + c] = first ? dm : sums[p.D + c] + dm;
-    }
-  }
-}
-
-// dweight and dbias from their parts: 32 channels x 8 parts at a time per workgroup.
-__global__ __launch_bounds__(256) void norm_sum_kernel(NormParams p) {
-  __shared__ float half[8][32];
-  const int64_t n = 2 * p.D, c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-  const int y = threadIdx.x >> 5;
-  float o = 0.0f;
-  if (c < n)
-    for (int64_t i = y; i < p.parts; i += 8) o += p.part[i * n + c];
-  half[y][threadIdx.x & 31] = o;
-  __syncthreads();
-  if (y || c >= n) return;
-  for (int w = 1; w < 8; ++w) o += half[w][threadIdx.x];
-  if (c < p.D) p.dweight[c] = o;
-  else p.dbias[c - p.D] = o;
-}
-
-template <typename T, typename O>
-hipError_t fwd_t(const NormParams& p, hipStream_t s) {
-  if (p.L == 1) {
-    hipLaunchKernelGGL((norm_row_fwd_kernel<T, O>), dim3((unsigned)(p.B * p.G)), dim3(256), 0, s, p);
-  } else {
-    const int64_t tiles = (p.L + 8 * kLanes - 1) / (8 * kLanes);
-    hipLaunchKernelGGL((norm_col_fwd_kernel<T, O>), dim3((unsigned)(p.B * p.G * tiles)), dim3(256), 0, s, p);
-  }
+template <typename T, typename O, int kI>
+hipError_t col_t(const NormParams& p, unsigned grid, hipStream_t s) {
+  constexpr NormShape q = sizeof(T) == 2 ? kNorm4[kI] : kNorm8[kI];
+  hipLaunchKernelGGL((norm_col_fwd_kernel<T, O, q.threads, q.lanes, q.chans>), dim3(grid), dim3(q.threads),
+                     (unsigned)(2 * p.Dg * sizeof(float)), s, p);
   return hipGetLastError();
 }
 
-template <typename T, typename Gr>
-hipError_t bwd_t(const NormParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.parts * p.G));
-  if (p.L == 1) hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((norm_col_bwd_kernel<T, Gr>), grid, dim3(256), 0, s, p);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((2 * p.D + 31) / 32)), dim3(256), 0, s, p);
+template <typename T, typename O>
+hipError_t fwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
+  const unsigned items = (unsigned)(p.B * p.G), grid = (unsigned)(p.B * p.G * q.tiles);
+  switch (q.kind) {
+    case 0: return col_t<T, O, 0>(p, grid, s);
+    case 1: return col_t<T, O, 1>(p, grid, s);
+    case 2: return col_t<T, O, 2>(p, grid, s);
+    case 3: return col_t<T, O, 3>(p, grid, s);
+    case 4: return col_t<T, O, 4>(p, grid, s);
+    case 5: return col_t<T, O, 5>(p, grid, s);
+    case kNormColLong:
+      if (p.L < 8) hipLaunchKernelGGL((norm_col_long_fwd_kernel<T, O, 1>), dim3(grid), dim3(256), 0, s, p);
+      else hipLaunchKernelGGL((norm_col_long_fwd_kernel<T, O, 8>), dim3(grid), dim3(256), 0, s, p);
+      break;
+    case kNormRowTeam:
+      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, false>), dim3((items + 256 / p.team - 1) / (256 / p.team)), dim3(256),
+                         0, s, p);
+      break;
+    case kNormRowBlock:
+      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, true>), dim3(items), dim3(q.threads), 0, s, p);
+      break;
+    default:
+      hipLaunchKernelGGL((norm_row_long_fwd_kernel<T, O>), dim3(items), dim3(256), 0, s, p);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_norm_fwd(const NormParams& p, Dt in, Dt out, hipStream_t s) {
-  if (in == Dt::BF16) return out == Dt::BF16 ? fwd_t<uint16_t, uint16_t>(p, s) : fwd_t<uint16_t, float>(p, s);
-  return out == Dt::BF16 ? fwd_t<float, uint16_t>(p, s) : fwd_t<float, float>(p, s);
+NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width, bool gate) {
+  const int64_t Dg = D / G;
+  NormPlan q{};
+  q.tiles = 1;
+  q.threads = 256;
+  if (L == 1) {
+    q.kind = Dg < 8 || Dg > 8192 ? kNormRowLong : Dg > 512 ? kNormRowBlock : kNormRowTeam;
+    q.lanes = 1;                                       // threads of a token
+    while (q.kind == kNormRowTeam && q.lanes * 8 < Dg) q.lanes *= 2;
+    if (q.kind == kNormRowBlock) q.threads = q.lanes = (int)((Dg + 511) / 512) * 64;
+  } else {
+    const NormShape* shapes = in_width == 2 ? kNorm4 : kNorm8;
+    if (grad_width) shapes = in_width + grad_width > 4 ? kNorm16 : gate ? kNorm8Gate : kNorm8;
+    q.kind = kNormColLong;
+    q.lanes = 8;
+    for (int i = 0; i < kNormShapes && L >= 8 && Dg <= kNormMostLds; ++i) {
+      const int64_t lanes = shapes[i].threads / shapes[i].lanes;      // channel lanes
+      if (Dg > lanes * shapes[i].chans || L >= (int64_t(1) << 30) / (lanes + 1)) continue;   // 32-bit byte offsets
+      q.kind = i;
+      q.threads = shapes[i].threads;
+      q.lanes = shapes[i].lanes;
+      break;
+    }
+    const int64_t tokens = 8 * q.lanes / (L < 8 ? 8 : 1);
+    q.tiles = (L + tokens - 1) / tokens;
+  }
+  if (grad_width) {
+    // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.
+    int64_t most = (q.threads >= 512 ? 512 : 1024) / G;
+    if (q.kind == kNormRowTeam) most = 262144 / (q.lanes * G);
+    const int64_t work = B * q.tiles;
+    if (most < 1) most = 1;
+    if (most > work) most = work;
+    q.parts = (work + (work + most - 1) / most - 1) / ((work + most - 1) / most);
+  }
+  return q;
 }
 
-hipError_t launch_norm_bwd(const NormParams& p, Dt in, Dt grad, hipStream_t s) {
-  if (in == Dt::BF16) return grad == Dt::BF16 ? bwd_t<uint16_t, uint16_t>(p, s) : bwd_t<uint16_t, float>(p, s);
-  return grad == Dt::BF16 ? bwd_t<float, uint16_t>(p, s) : bwd_t<float, float>(p, s);
+hipError_t launch_norm_fwd(const NormParams& p, const NormPlan& q, Dt in, Dt out, hipStream_t s) {
+  if (in == Dt::BF16) return out == Dt::BF16 ? fwd_t<uint16_t, uint16_t>(p, q, s) : fwd_t<uint16_t, float>(p, q, s);
+  return out == Dt::BF16 ? fwd_t<float, uint16_t>(p, q, s) : fwd_t<float, float>(p, q, s);
 }
 
 }  // namespace mamba

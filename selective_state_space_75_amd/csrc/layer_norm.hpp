@@ -1,0 +1,200 @@
+// layer_norm.hpp -- device helpers shared by the layer norm's kernels (gfx950).
+#pragma once
+
+#include "glr.hpp"
+
+namespace mamba {
+
+// 1 / sqrt(v), the hardware's root with one Newton step (about half an ulp): it goes into every
+// number of the token.
+__device__ __forceinline__ float norm_root(float v) {
+  const float r = __builtin_amdgcn_rsqf(v);
+  const float h = __builtin_fmaf(-0.5f * v * r, r, 1.5f);
+  return r * (v < 1e37f && v > 1e-37f ? h : 1.0f);
+}
+
+// Halves a wave's numbers over its halves: a becomes the sum over lane ^ 32 of a in the lower 32
+// lanes, and of b in the upper.
+__device__ __forceinline__ float fold32(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false,
+                                                  false);
+  const uint32_t x = r[0], y = r[1];
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+// The same over lane ^ 16: a in even rows of 16 lanes, b in odd ones.
+__device__ __forceinline__ float fold16(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false,
+                                                  false);
+  const uint32_t x = r[0], y = r[1];
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Sum over the lanes of a row of 16 that share lane % kT, in all of them.
+template <int kT>
+__device__ __forceinline__ float row_sum(float x) {
+  if constexpr (kT <= 8) x += dpp<0x128, 0xf>(0.0f, x);
+  if constexpr (kT <= 4) x += dpp<0x124, 0xf>(0.0f, x);
+  if constexpr (kT <= 2) x += dpp<0x122, 0xf>(0.0f, x);
+  if constexpr (kT <= 1) x += dpp<0x121, 0xf>(0.0f, x);
+  return x;
+}
+
+// Sums of kN numbers (a multiple of 4) over the lanes of a workgroup that share threadIdx.x % kT
+// (kT <= 8), in every lane.  Inside a wave the numbers are folded over its halves and rows, so that each
+// exchange halves how many there are; a quarter of them per row of 16 lanes is then left in LDS,
+// summed over the waves by one lane per sum, and read back.
+// lds: (waves + 1) * kT * kN floats.
+template <int kT, int kN, int kThreads>
+__device__ __forceinline__ void group_sum(float (&v)[kN], float* lds) {
+  static_assert(kN % 4 == 0 && kT <= 8, "four quarters");
+  constexpr int kWaves = kThreads / 64, kQ = kN / 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float h[kN / 2], q[kQ];
+#pragma unroll
+  for (int j = 0; j < kN / 2; ++j) h[j] = fold32(v[j], v[j + kN / 2]);
+#pragma unroll
+  for (int j = 0; j < kQ; ++j) q[j] = row_sum<kT>(fold16(h[j], h[j + kQ]));
+  // row 0 holds numbers 0 .., row 1 those from kQ, row 2 from 2 kQ, row 3 from 3 kQ
+  float* total = lds + kWaves * kT * kN;
+  __syncthreads();                       // an earlier sum may still be read
+  if ((lane & 15) < kT) {
+    float* at = (kWaves > 1 ? lds + wave * kT * kN : total) + (lane & 15) * kN + (lane >> 4) * kQ;
+#pragma unroll
+    for (int j = 0; j < kQ; ++j) at[j] = q[j];
+  }
+  __syncthreads();
+  if constexpr (kWaves > 1) {
+    if (threadIdx.x < kT * kN) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) s += lds[w * kT * kN + threadIdx.x];
+      total[threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < kN; ++j) v[j] = total[(lane % kT) * kN + j];
+}
+
+// Sum of kN numbers over a team of 2^k <= 64 neighbouring lanes, or over the workgroup (lds: waves * kN
+// floats), in every lane of it.
+template <int kN, bool kBlock>
+__device__ __forceinline__ void team_sum(float (&v)[kN], int team, float* lds) {
+  if constexpr (!kBlock) {
+    for (int m = 1; m < team; m *= 2) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) v[j] += __shfl_xor(v[j], m);
+    }
+  } else {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = wave_sum63(v[j]);
+    __syncthreads();                     // an earlier sum may still be read
+    if (lane == 63) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) lds[wave * kN + j] = v[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = 0.0f;
+    for (int w = 0; w < waves; ++w) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) v[j] += lds[w * kN + j];
+    }
+  }
+}
+
+// Workgroups go to the eight XCDs in turn.  Work is renumbered so that each XCD has a contiguous
+// range of it: neighbouring tiles share cache lines, and those then meet in one L2.
+__device__ __forceinline__ int64_t by_xcd(int64_t i, int64_t n) {
+  const int64_t xcd = i & 7, q = n >> 3, r = n & 7;
+  return xcd * q + (xcd < r ? xcd : r) + (i >> 3);
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_all8(const T* p) {
+  Raw8<T> o;
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k) o.w[k] = *(reinterpret_cast<const u32x4_u*>(p) + k);
+  return o;
+}
+// base[v]: a base that the workgroup shares and a lane's 32-bit offset (v * sizeof(T) < 2^32), one register for
+// all the channels of a lane.
+template <typename T>
+__device__ __forceinline__ T* lane_at(T* base, uint32_t v) {
+  return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(base) + (uint32_t)(v * sizeof(T)));
+}
+
+// The numbers as they lie in memory are what stays in registers between two sweeps: without this the
+// compiler keeps the widened and centred ones of the first for the second, twice the registers and more.
+template <typename T>
+__device__ __forceinline__ void keep(Raw8<T>& o) {
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k) asm("" : "+v"(o.w[k]));
+}
+
+// kTok (8 or 1) tokens of a channel, `live` of them there.
+template <typename T, int kTok>
+__device__ __forceinline__ void load_tok(const T* p, int live, float (&v)[kTok]) {
+  if constexpr (kTok == 8) {
+    const Raw8<T> r = load_raw8(p, live);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = get8(r, j);
+  } else {
+    v[0] = live ? get1(p) : 0.0f;
+  }
+}
+template <typename O, int kTok>
+__device__ __forceinline__ void store_tok(O* p, int live, const float (&o)[8]) {
+  if constexpr (kTok == 8) store8(p, o, live, live);
+  else if (live) put1(p, o[0]);
+}
+
+// Statistics of kTok tokens over the group's channels, a workgroup of 256: 32 channel lanes of 8 token
+// lanes, in two sweeps.  (Arrays of 8 whatever kTok is; the rest is not used.)
+template <typename T, int kTok>
+__device__ __forceinline__ void norm_col_stats(const NormParams& p, const T* x, int live, float (&mu)[8], float (&k)[8],
+                                               float* lds) {
+  float v[kTok];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) mu[j] = k[j] = 0.0f;
+  if (!p.rms) {
+    for (int64_t c = threadIdx.x / 8; c < p.Dg; c += 32) {
+      load_tok<T, kTok>(x + c * p.L, live, v);
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) mu[j] += v[j];
+    }
+    group_sum<8, 8, 256>(mu, lds);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mu[j] *= p.inv_dg;
+  }
+  for (int64_t c = threadIdx.x / 8; c < p.Dg; c += 32) {
+    load_tok<T, kTok>(x + c * p.L, live, v);
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) k[j] = __builtin_fmaf(v[j] - mu[j], v[j] - mu[j], k[j]);
+  }
+  group_sum<8, 8, 256>(k, lds);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) k[j] = norm_root(__builtin_fmaf(k[j], p.inv_dg, p.eps));
+}
+
+// Statistics of one token-major row, a workgroup of 256.
+template <typename T>
+__device__ __forceinline__ void norm_row_stats(const NormParams& p, const T* x, float& mu, float& k, float* lds) {
+  float v[1] = {0.0f};
+  if (!p.rms) {
+    for (int64_t c = threadIdx.x; c < p.Dg; c += 256) v[0] += get1(x + c);
+    team_sum<1, true>(v, 256, lds);
+    v[0] *= p.inv_dg;
+  }
+  mu = v[0];
+  v[0] = 0.0f;
+  for (int64_t c = threadIdx.x; c < p.Dg; c += 256) {
+    const float d = get1(x + c) - mu;
+    v[0] = __builtin_fmaf(d, d, v[0]);
+  }
+  team_sum<1, true>(v, 256, lds);
+  k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
+}
+
+}  // namespace mamba
