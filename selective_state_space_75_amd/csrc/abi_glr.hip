@@ -31,6 +31,8 @@ bool all_aligned(std::initializer_list<const void*> ptrs, size_t a) {
   return true;
 }
 
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
 // Test knobs (mamba_glr_set_test_knobs), read once per call.
 std::atomic<int> g_waves{0};
 std::atomic<int64_t> g_segments{0};
@@ -107,7 +109,6 @@ mamba::GlrParams glr_params(const void* x, const void* r, const void* i, const v
   return p;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t glr_bytes(const GlrPlan& q, int64_t B, int64_t D) {
   return q.S > 1 ? align256(size_t(B) * D * q.S * 2 * sizeof(float)) : 0;
 }
@@ -122,21 +123,27 @@ bool norm_sizes_ok(int64_t B, int64_t D, int64_t L, int64_t G) {
   return product_ok(B, D, L) && G >= 1 && D % G == 0;
 }
 
-// The plan depends on the element widths and the gate; the workspace is enough for all of them.
-size_t norm_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
-  int64_t parts = 0;
-  for (int in : {2, 4})
-    for (int grad : {2, 4})
-      for (bool gate : {false, true}) {
-        const int64_t n = mamba::norm_plan(B, D, L, G, in, grad, gate).parts;
-        if (n > parts) parts = n;
-      }
-  return size_t(parts) * 2 * D * sizeof(float);
+size_t norm_part_bytes(const mamba::NormPlan& q, int64_t D) { return align256(size_t(q.parts) * 2 * D * sizeof(float)); }
+size_t norm_stat_bytes(const mamba::NormPlan& q, int64_t B, int64_t L, int64_t G) {
+  return q.kind == mamba::kNormColTwo ? size_t(B) * G * q.chunks * 4 * L * sizeof(float) : 0;
 }
 
-// Workgroups of a launch by its plan.
+// The plan of the backward pass does not depend on the element widths.
+mamba::NormPlan norm_bwd_plan(int64_t B, int64_t D, int64_t L, int64_t G) { return mamba::norm_plan(B, D, L, G, 4, 4); }
+size_t norm_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
+  const mamba::NormPlan q = norm_bwd_plan(B, D, L, G);
+  return norm_part_bytes(q, D) + norm_stat_bytes(q, B, L, G);
+}
+
+// Whether every launch is one.
 bool norm_fits(const mamba::NormPlan& q, int64_t items) {
   return mamba::launch_fits(q.kind == mamba::kNormRowTeam ? ceil_div(items, 256 / q.lanes) : items, q.threads);
+}
+bool norm_bwd_fits(const mamba::NormPlan& q, int64_t B, int64_t D, int64_t G) {
+  if (!mamba::launch_fits(ceil_div(2 * D, 32), 256)) return false;
+  if (q.kind != mamba::kNormColTwo) return norm_fits(q, q.parts * G);
+  return mamba::launch_fits(B * G * q.chunks * q.tiles, q.threads) &&
+         mamba::launch_fits(q.parts * G * ceil_div(D / G, q.apply_chans), mamba::kNormApplyThreads);
 }
 
 int check_norm(const mamba::NormParams& p, int in_dtype, int out_dtype, unsigned flags) {
@@ -168,6 +175,7 @@ void norm_set(mamba::NormParams& p, const mamba::NormPlan& q) {
   p.tiles = q.tiles;
   p.team = q.lanes;
   p.parts = q.parts;
+  p.chunks = q.chunks; p.chunk = q.chunk; p.apply_chans = q.apply_chans;
 }
 
 int status_of(hipError_t e) { return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP; }
@@ -268,7 +276,7 @@ int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, cons
   if (st != MAMBA_OK) return st;
   if (!y) return MAMBA_ERR_NULL;
   if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
-  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), 0, z != nullptr);
+  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), 0);
   if (!norm_fits(q, B * groups * q.tiles)) return MAMBA_ERR_SHAPE;
   norm_set(p, q);
   return status_of(mamba::launch_norm_fwd(p, q, dt_of(in_dtype), dt_of(out_dtype), stream));
@@ -289,15 +297,15 @@ int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, cons
   if (st != MAMBA_OK) return st;
   if (!dy || !dx || (z && !dz) || !dweight || !dbias) return MAMBA_ERR_NULL;
   if (!all_aligned({dy, dx, dz}, width(grad_dtype)) || !all_aligned({dweight, dbias}, 4)) return MAMBA_ERR_ALIGN;
-  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), (int)width(grad_dtype),
-                                              z != nullptr);
-  if (!norm_fits(q, q.parts * groups) || !mamba::launch_fits(ceil_div(2 * D, 32), 256)) return MAMBA_ERR_SHAPE;
+  const mamba::NormPlan q = norm_bwd_plan(B, D, L, groups);
+  if (!norm_bwd_fits(q, B, D, groups)) return MAMBA_ERR_SHAPE;
   norm_set(p, q);
   const size_t need = norm_bytes(B, D, L, groups);
   if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
   p.dy = dy; p.dx = dx; p.dz = z ? dz : nullptr; p.dweight = dweight; p.dbias = dbias;
   p.part = static_cast<float*>(workspace);
+  p.stat = reinterpret_cast<float*>(static_cast<char*>(workspace) + norm_part_bytes(q, D));
   return status_of(mamba::launch_norm_bwd(p, q, dt_of(in_dtype), dt_of(grad_dtype), stream));
 }
 

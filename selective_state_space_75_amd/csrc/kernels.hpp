@@ -265,35 +265,41 @@ struct NormParams {
   float *dweight, *dbias;                       // (D)
   float* part;                                  // (parts, 2, D) sums of dweight and dbias
   int64_t parts;
+  float* stat;                                  // (B G, chunks, 4, L): mean, sum of squares around it, sums of g and g (x - mean)
+  int64_t chunks, chunk, apply_chans;
 };
 
 // How the norm is carried out (sizes and element widths only).
 //   0 .. 5        channel-major, at least 8 tokens: a workgroup's tile of 8 * lanes tokens is held in
-//                 registers, in the smallest of the shapes below that holds the group
+//                 registers, in the smallest of the shapes below that holds the group (backward: 0 and 1)
 //   kNormColLong  channel-major, any group and any length: the tile is read again for every sweep
+//   kNormColTwo   channel-major, backward, at least 8 tokens: statistics in one launch, results in the next
 //   kNormRowTeam  token-major, 8 to 512 channels: teams of 2^k <= 64 lanes, 8 channels each
 //   kNormRowBlock token-major, up to 8192 channels: a workgroup, 8 channels a thread
 //   kNormRowLong  token-major, any group
-enum NormKind : int { kNormShapes = 6, kNormColLong = 6, kNormRowTeam, kNormRowBlock, kNormRowLong };
+enum NormKind : int { kNormShapes = 6, kNormColLong = 6, kNormColTwo, kNormRowTeam, kNormRowBlock, kNormRowLong };
 
 struct NormShape {
   int threads, lanes, chans;                    // workgroup, token lanes of 8 tokens, channels of a thread
 };
 // Registers of a channel's 8 tokens: 4 in the forward pass of 2-byte inputs; 8 of 4-byte inputs, and in
-// the backward pass of two 2-byte arrays (which has no room for 20 channels next to a gate); 12 or 16 in that
-// with a 4-byte array.
+// the backward pass of two 2-byte arrays; 12 or 16 in that with a 4-byte array.
 constexpr NormShape kNorm4[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {1024, 8, 16}, {1024, 4, 20}, {1024, 2, 16}};
 constexpr NormShape kNorm8[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {512, 4, 20}, {512, 2, 20}, {512, 1, 16}};
-constexpr NormShape kNorm8Gate[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {512, 4, 16}, {512, 2, 16}, {512, 1, 16}};
-constexpr NormShape kNorm16[kNormShapes] = {{256, 8, 4}, {256, 8, 8}, {512, 8, 8}, {512, 4, 8}, {512, 2, 8}, {512, 1, 8}};
-constexpr int64_t kNormMostLds = 7680;          // channels whose numbers in LDS, 16 bytes each, leave room for the sums
+constexpr NormShape kNormBwd[2] = {{256, 8, 4}, {256, 8, 8}};
+constexpr int64_t kNormMostLds = 7680;          // channels whose weight and bias fit in 60 KB of LDS
+
+// The two launches of kNormColTwo.
+constexpr int kNormStatThreads = 512, kNormStatLanes = 8;    // 64 tokens, 64 channel lanes
+constexpr int kNormApplyThreads = 512;                       // 64 or 8 token lanes
 
 struct NormPlan {
   int kind, threads, lanes;
   int64_t tiles, parts;                         // tiles of a row's tokens; parts of the weight's sums (backward)
+  int64_t chunks, chunk;                        // kNormColTwo: pieces of the group, and their channels
+  int64_t apply_lanes, apply_chans;             // token lanes, and channels of a workgroup
 };
-NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width,
-                   bool gate);                  // grad_width 0: forward
+NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width);   // grad_width 0: forward
 
 // Whether a launch of this many workgroups is one: HIP takes fewer than 2^32 threads in all.
 inline bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups <= int64_t(0xffffffff) / threads; }

@@ -230,7 +230,7 @@ hipError_t fwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
 
 }  // namespace
 
-NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width, bool gate) {
+NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width) {
   const int64_t Dg = D / G;
   NormPlan q{};
   q.tiles = 1;
@@ -241,11 +241,10 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     while (q.kind == kNormRowTeam && q.lanes * 8 < Dg) q.lanes *= 2;
     if (q.kind == kNormRowBlock) q.threads = q.lanes = (int)((Dg + 511) / 512) * 64;
   } else {
-    const NormShape* shapes = in_width == 2 ? kNorm4 : kNorm8;
-    if (grad_width) shapes = in_width + grad_width > 4 ? kNorm16 : gate ? kNorm8Gate : kNorm8;
+    const NormShape* shapes = grad_width ? kNormBwd : in_width == 2 ? kNorm4 : kNorm8;
     q.kind = kNormColLong;
     q.lanes = 8;
-    for (int i = 0; i < kNormShapes && L >= 8 && Dg <= kNormMostLds; ++i) {
+    for (int i = 0; i < (grad_width ? 2 : (int)kNormShapes) && L >= 8 && Dg <= kNormMostLds; ++i) {
       const int64_t lanes = shapes[i].threads / shapes[i].lanes;      // channel lanes
       if (Dg > lanes * shapes[i].chans || L >= (int64_t(1) << 30) / (lanes + 1)) continue;   // 32-bit byte offsets
       q.kind = i;
@@ -256,15 +255,29 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     const int64_t tokens = 8 * q.lanes / (L < 8 ? 8 : 1);
     q.tiles = (L + tokens - 1) / tokens;
   }
-  if (grad_width) {
-    // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.
-    int64_t most = (q.threads >= 512 ? 512 : 1024) / G;
-    if (q.kind == kNormRowTeam) most = 262144 / (q.lanes * G);
-    const int64_t work = B * q.tiles;
-    if (most < 1) most = 1;
-    if (most > work) most = work;
-    q.parts = (work + (work + most - 1) / most - 1) / ((work + most - 1) / most);
+  if (!grad_width) return q;
+  if (q.kind == kNormColLong && L >= 8) {
+    q.kind = kNormColTwo;
+    q.threads = kNormStatThreads;
+    // Statistics: 4 to 32 channels a thread, in as few pieces as fill the chip.
+    const int64_t lanes = kNormStatThreads / kNormStatLanes, blocks = B * G * q.tiles;
+    q.chunks = (Dg + 32 * lanes - 1) / (32 * lanes);
+    while (q.chunks * blocks < 512 && Dg / (q.chunks * 2) >= 4 * lanes) q.chunks *= 2;
+    q.chunk = (Dg + q.chunks - 1) / q.chunks;
+    q.chunks = (Dg + q.chunk - 1) / q.chunk;
+    q.apply_lanes = L > 256 ? 64 : 8;
+    q.apply_chans = kNormApplyThreads / q.apply_lanes * 8;
+    q.parts = B * ((L + 8 * q.apply_lanes - 1) / (8 * q.apply_lanes));
+    return q;
   }
+  // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.
+  int64_t most = 1024 / G;
+  if (q.kind == kNormRowBlock) most = 512 / G;
+  if (q.kind == kNormRowTeam) most = 262144 / (q.lanes * G);
+  const int64_t work = B * q.tiles;
+  if (most < 1) most = 1;
+  if (most > work) most = work;
+  q.parts = (work + (work + most - 1) / most - 1) / ((work + most - 1) / most);
   return q;
 }
 
