@@ -32,10 +32,17 @@ extern "C" {
 
 #define MAMBA_FLAG_RMS 0x10u             /* no mean taken off */
 
+/*
+ * Bytes of workspace mamba_layer_norm_fwd needs (sizes only; callable without a GPU); 0 when it
+ * needs none, (size_t)-1 for an invalid shape.
+ */
+size_t mamba_layer_norm_workspace_size(int64_t B, int64_t D, int64_t L, int64_t groups);
+
+/* y : (B, D, L) out_dtype, written, dense. */
 int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, const float* bias, void* y,
                          int64_t B, int64_t D, int64_t L, int64_t groups, int64_t x_stride,
                          int64_t z_stride, float eps, mamba_dtype_t in_dtype, mamba_dtype_t out_dtype,
-                         unsigned flags, hipStream_t stream);
+                         unsigned flags, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace mamba_layer_norm_bwd needs, (size_t)-1 for an invalid shape. */
 size_t mamba_layer_norm_bwd_workspace_size(int64_t B, int64_t D, int64_t L, int64_t groups);

@@ -15,7 +15,7 @@ The computation runs in hand-written HIP kernels inside ``libmamba_scan.so``
 from ._lib import (FLAG_ACCURATE_EXPM1, FLAG_BLEND, FLAG_DELTA_B, FLAG_QK_NORM, FLAG_RMS, MambaError, conv1d_fwd, conv1d_update,  # noqa: F401
                    gdr_bwd, gdr_bwd_workspace_size, gdr_fwd, gdr_test_knobs, gdr_update, gdr_workspace_size, state_cache, state_cache_read, state_cache_write,
                    glr_bwd, glr_bwd_workspace_size, glr_fwd, glr_test_knobs, glr_update, glr_workspace_size,
-                   layer_norm_bwd, layer_norm_bwd_workspace_size, layer_norm_fwd,
+                   layer_norm_bwd, layer_norm_bwd_workspace_size, layer_norm_fwd, layer_norm_workspace_size,
                    lib, scan_bwd, scan_bwd_workspace_size, scan_fwd, scan_fwd_noalloc, scan_kernel, set_test_knobs, ssd_fwd, ssd_workspace_size,
                    state_update, status_string, test_knobs, workspace_size)
 
@@ -24,4 +24,4 @@ __all__ = ["scan_fwd", "scan_bwd", "scan_bwd_workspace_size", "state_update", "c
            "FLAG_ACCURATE_EXPM1", "set_test_knobs", "test_knobs", "scan_fwd_noalloc", "scan_kernel",
            "gdr_bwd", "gdr_bwd_workspace_size", "gdr_fwd", "gdr_test_knobs", "gdr_update", "gdr_workspace_size", "state_cache", "state_cache_read", "state_cache_write",
            "FLAG_QK_NORM", "glr_bwd", "glr_bwd_workspace_size", "glr_fwd", "glr_test_knobs", "glr_update",
-           "glr_workspace_size", "layer_norm_bwd", "layer_norm_bwd_workspace_size", "layer_norm_fwd", "FLAG_BLEND", "FLAG_RMS"]
+           "glr_workspace_size", "layer_norm_bwd", "layer_norm_bwd_workspace_size", "layer_norm_fwd", "layer_norm_workspace_size", "FLAG_BLEND", "FLAG_RMS"]

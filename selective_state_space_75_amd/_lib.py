@@ -107,7 +107,9 @@ def lib() -> ctypes.CDLL:
             L.mamba_glr_bwd.restype = c_int
             L.mamba_glr_set_test_knobs.argtypes = [c_int, i64]
             L.mamba_glr_set_test_knobs.restype = c_int
-            L.mamba_layer_norm_fwd.argtypes = [vp] * 5 + [i64] * 6 + [f32, c_int, c_int, u32, vp]
+            L.mamba_layer_norm_workspace_size.argtypes = [i64] * 4
+            L.mamba_layer_norm_workspace_size.restype = sz
+            L.mamba_layer_norm_fwd.argtypes = [vp] * 5 + [i64] * 6 + [f32, c_int, c_int, u32, vp, sz, vp]
             L.mamba_layer_norm_fwd.restype = c_int
             L.mamba_layer_norm_bwd_workspace_size.argtypes = [i64] * 4
             L.mamba_layer_norm_bwd_workspace_size.restype = sz
@@ -1034,8 +1036,16 @@ def _norm_inputs(x, weight, bias, z, groups):
     return dev, code, ins, (shape[0], D, shape[2] if len(shape) == 3 else 1, groups) + strides
 
 
+def layer_norm_workspace_size(B: int, D: int, L: int, groups: int = 1) -> int:
+    """Bytes layer_norm_fwd needs for these sizes (L = 1 for token-major rows)."""
+    n = lib().mamba_layer_norm_workspace_size(B, D, L, groups)
+    if n == ctypes.c_size_t(-1).value:
+        raise MambaError(-2, "mamba_layer_norm_workspace_size")
+    return n
+
+
 def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms=False, out_dtype=None, y=None,
-                   stream=None):
+                   workspace=None, stream=None):
     """Layer norm of every token over its channels, or over each of `groups` equal ranges of them,
     with the output gate (include/mamba_norm.h): (xh weight + bias) silu(z), xh = (x - mean) /
     sqrt(var + eps), or x / sqrt(mean x^2 + eps) with rms=True.  x, z: (B, D, L), or (rows, D) for
@@ -1047,8 +1057,10 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms
     with _there(dev, stream):
         if y is None:
             y = torch.empty(x.shape, dtype=out_dt, device=dev)
+        workspace = _workspace(workspace, layer_norm_workspace_size(*sizes[:4]), dev)
         st = lib().mamba_layer_norm_fwd(*ins, _plain(y, "y", x.shape, out_dt, dev), *sizes, eps, code, _dtype_code(y),
-                                        FLAG_RMS if rms else 0, _raw_stream(dev, stream))
+                                        FLAG_RMS if rms else 0, _addr(workspace), _nbytes(workspace),
+                                        _raw_stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_layer_norm_fwd")
     return y

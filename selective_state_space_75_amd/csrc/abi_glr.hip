@@ -124,26 +124,35 @@ bool norm_sizes_ok(int64_t B, int64_t D, int64_t L, int64_t G) {
 }
 
 size_t norm_part_bytes(const mamba::NormPlan& q, int64_t D) { return align256(size_t(q.parts) * 2 * D * sizeof(float)); }
-size_t norm_stat_bytes(const mamba::NormPlan& q, int64_t B, int64_t L, int64_t G) {
-  return q.kind == mamba::kNormColTwo ? size_t(B) * G * q.chunks * 4 * L * sizeof(float) : 0;
+size_t norm_stat_bytes(const mamba::NormPlan& q, int64_t B, int64_t L, int64_t G, int numbers) {
+  return q.kind == mamba::kNormColTwo ? size_t(B) * G * q.chunks * numbers * L * sizeof(float) : 0;
 }
 
-// The plan of the backward pass does not depend on the element widths.
-mamba::NormPlan norm_bwd_plan(int64_t B, int64_t D, int64_t L, int64_t G) { return mamba::norm_plan(B, D, L, G, 4, 4); }
-size_t norm_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
-  const mamba::NormPlan q = norm_bwd_plan(B, D, L, G);
-  return norm_part_bytes(q, D) + norm_stat_bytes(q, B, L, G);
+// The plan depends on the element widths; the workspace is enough for all of them.
+size_t norm_fwd_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
+  size_t most = 0;
+  for (int in : {2, 4}) {
+    const size_t n = norm_stat_bytes(mamba::norm_plan(B, D, L, G, in, 0), B, L, G, 2);
+    if (n > most) most = n;
+  }
+  return most;
+}
+size_t norm_bwd_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
+  size_t most = 0;
+  for (int grad : {2, 4}) {
+    const mamba::NormPlan q = mamba::norm_plan(B, D, L, G, 2, grad);
+    const size_t n = norm_part_bytes(q, D) + norm_stat_bytes(q, B, L, G, 4);
+    if (n > most) most = n;
+  }
+  return most;
 }
 
-// Whether every launch is one.
-bool norm_fits(const mamba::NormPlan& q, int64_t items) {
+// Whether every launch is one; items: workgroups of a plan of one launch.
+bool norm_fits(const mamba::NormPlan& q, int64_t B, int64_t D, int64_t L, int64_t G, int64_t items) {
+  if (q.kind == mamba::kNormColTwo)
+    return mamba::launch_fits(B * G * q.chunks * q.tiles, q.threads) &&
+           mamba::launch_fits(B * ceil_div(L, 8 * q.apply_lanes) * G * ceil_div(D / G, q.apply_chans), mamba::kNormApplyThreads);
   return mamba::launch_fits(q.kind == mamba::kNormRowTeam ? ceil_div(items, 256 / q.lanes) : items, q.threads);
-}
-bool norm_bwd_fits(const mamba::NormPlan& q, int64_t B, int64_t D, int64_t G) {
-  if (!mamba::launch_fits(ceil_div(2 * D, 32), 256)) return false;
-  if (q.kind != mamba::kNormColTwo) return norm_fits(q, q.parts * G);
-  return mamba::launch_fits(B * G * q.chunks * q.tiles, q.threads) &&
-         mamba::launch_fits(q.parts * G * ceil_div(D / G, q.apply_chans), mamba::kNormApplyThreads);
 }
 
 int check_norm(const mamba::NormParams& p, int in_dtype, int out_dtype, unsigned flags) {
@@ -267,9 +276,15 @@ int mamba_glr_set_test_knobs(int waves, int64_t segments) {
   return MAMBA_OK;
 }
 
+size_t mamba_layer_norm_workspace_size(int64_t B, int64_t D, int64_t L, int64_t groups) {
+  if (!norm_sizes_ok(B, D, L, groups)) return (size_t)-1;
+  return norm_fwd_bytes(B, D, L, groups);
+}
+
 int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, const float* bias, void* y, int64_t B,
                          int64_t D, int64_t L, int64_t groups, int64_t x_stride, int64_t z_stride, float eps,
-                         mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags, hipStream_t stream) {
+                         mamba_dtype_t in_dtype, mamba_dtype_t out_dtype, unsigned flags, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream) {
   mamba::NormParams p = norm_params(x, z, weight, bias, B, D, L, groups, x_stride, z_stride, eps, flags);
   p.y = y;
   const int st = check_norm(p, in_dtype, out_dtype, flags);
@@ -277,14 +292,18 @@ int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, cons
   if (!y) return MAMBA_ERR_NULL;
   if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
   const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), 0);
-  if (!norm_fits(q, B * groups * q.tiles)) return MAMBA_ERR_SHAPE;
+  if (!norm_fits(q, B, D, L, groups, B * groups * q.tiles)) return MAMBA_ERR_SHAPE;
+  const size_t need = norm_fwd_bytes(B, D, L, groups);
+  if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
   norm_set(p, q);
+  p.stat = static_cast<float*>(workspace);
   return status_of(mamba::launch_norm_fwd(p, q, dt_of(in_dtype), dt_of(out_dtype), stream));
 }
 
 size_t mamba_layer_norm_bwd_workspace_size(int64_t B, int64_t D, int64_t L, int64_t groups) {
   if (!norm_sizes_ok(B, D, L, groups)) return (size_t)-1;
-  return norm_bytes(B, D, L, groups);
+  return norm_bwd_bytes(B, D, L, groups);
 }
 
 int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, const float* bias, const void* dy, void* dx,
@@ -297,10 +316,11 @@ int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, cons
   if (st != MAMBA_OK) return st;
   if (!dy || !dx || (z && !dz) || !dweight || !dbias) return MAMBA_ERR_NULL;
   if (!all_aligned({dy, dx, dz}, width(grad_dtype)) || !all_aligned({dweight, dbias}, 4)) return MAMBA_ERR_ALIGN;
-  const mamba::NormPlan q = norm_bwd_plan(B, D, L, groups);
-  if (!norm_bwd_fits(q, B, D, groups)) return MAMBA_ERR_SHAPE;
+  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), (int)width(grad_dtype));
+  if (!norm_fits(q, B, D, L, groups, q.parts * groups) || !mamba::launch_fits(ceil_div(2 * D, 32), 256))
+    return MAMBA_ERR_SHAPE;
   norm_set(p, q);
-  const size_t need = norm_bytes(B, D, L, groups);
+  const size_t need = norm_bwd_bytes(B, D, L, groups);
   if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
   p.dy = dy; p.dx = dx; p.dz = z ? dz : nullptr; p.dweight = dweight; p.dbias = dbias;

@@ -265,29 +265,29 @@ struct NormParams {
   float *dweight, *dbias;                       // (D)
   float* part;                                  // (parts, 2, D) sums of dweight and dbias
   int64_t parts;
-  float* stat;                                  // (B G, chunks, 4, L): mean, sum of squares around it, sums of g and g (x - mean)
+  float* stat;                                  // (B G, chunks, 4 or 2, L): mean, sum of squares around it; backward: sums of g and g (x - mean)
   int64_t chunks, chunk, apply_chans;
 };
 
 // How the norm is carried out (sizes and element widths only).
-//   0 .. 5        channel-major, at least 8 tokens: a workgroup's tile of 8 * lanes tokens is held in
-//                 registers, in the smallest of the shapes below that holds the group (backward: 0 and 1)
-//   kNormColLong  channel-major, any group and any length: the tile is read again for every sweep
-//   kNormColTwo   channel-major, backward, at least 8 tokens: statistics in one launch, results in the next
+//   0 .. 3        channel-major, at least 8 tokens: a workgroup's tile of 8 * lanes tokens is held in
+//                 registers, in the smallest of the shapes below that holds the group (backward: 0 to 2)
+//   kNormColTwo   channel-major, at least 8 tokens: statistics in one launch, results in the next
+//   kNormColLong  channel-major, fewer than 8 tokens
 //   kNormRowTeam  token-major, 8 to 512 channels: teams of 2^k <= 64 lanes, 8 channels each
 //   kNormRowBlock token-major, up to 8192 channels: a workgroup, 8 channels a thread
 //   kNormRowLong  token-major, any group
-enum NormKind : int { kNormShapes = 6, kNormColLong = 6, kNormColTwo, kNormRowTeam, kNormRowBlock, kNormRowLong };
+enum NormKind : int { kNormShapes = 4, kNormBwdShapes = 3, kNormColTwo = 4, kNormColLong, kNormRowTeam, kNormRowBlock, kNormRowLong };
 
 struct NormShape {
   int threads, lanes, chans;                    // workgroup, token lanes of 8 tokens, channels of a thread
 };
-// Registers of a channel's 8 tokens: 4 in the forward pass of 2-byte inputs; 8 of 4-byte inputs, and in
-// the backward pass of two 2-byte arrays; 12 or 16 in that with a 4-byte array.
-constexpr NormShape kNorm4[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {1024, 8, 16}, {1024, 4, 20}, {1024, 2, 16}};
-constexpr NormShape kNorm8[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {512, 4, 20}, {512, 2, 20}, {512, 1, 16}};
-constexpr NormShape kNormBwd[2] = {{256, 8, 4}, {256, 8, 8}};
-constexpr int64_t kNormMostLds = 7680;          // channels whose weight and bias fit in 60 KB of LDS
+// Token lanes make whole cache lines of 128 bytes.  For 2-byte and 4-byte inputs (backward: with a 4-byte
+// array among them).
+constexpr NormShape kNormFwd2[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {1024, 8, 16}};
+constexpr NormShape kNormFwd4[kNormShapes] = {{256, 4, 4}, {256, 4, 8}, {512, 4, 8}, {512, 4, 20}};
+constexpr NormShape kNormBwd2[kNormBwdShapes] = {{256, 8, 4}, {256, 8, 8}, {512, 8, 8}};
+constexpr NormShape kNormBwd4[kNormBwdShapes] = {{256, 4, 2}, {256, 4, 4}, {512, 4, 4}};
 
 // The two launches of kNormColTwo.
 constexpr int kNormStatThreads = 512, kNormStatLanes = 8;    // 64 tokens, 64 channel lanes

@@ -7,7 +7,7 @@
 // Channel-major (L > 1): channels are L apart, so a thread takes 8 consecutive tokens (one load) of every
 // CL-th channel, neighbouring lanes the tokens after them, and the sums run over a workgroup's CL channel
 // lanes.  Token-major (L = 1): a row's channels lie together; a thread takes 8 of them.
-#include "layer_norm.hpp"
+#include "layer_norm_two.hpp"
 
 namespace mamba {
 namespace {
@@ -103,31 +103,22 @@ __global__ __launch_bounds__(kThreads) void norm_col_fwd_kernel(NormParams p) {
   }
 }
 
-// Any group, any length: kTok (8 or 1) tokens a lane, 8 lanes of them, three sweeps over the tile.
-template <typename T, typename O, int kTok>
+// Fewer than 8 tokens: a token a lane, 8 token lanes, three sweeps over the group.
+template <typename T, typename O>
 __global__ __launch_bounds__(256) void norm_col_long_fwd_kernel(NormParams p) {
-  __shared__ float lds[5 * 8 * 8];
-  const int64_t bg = blockIdx.x / p.tiles, tile = blockIdx.x - bg * p.tiles;
-  const int64_t b = bg / p.G, ch = (bg - b * p.G) * p.Dg;
-  const int64_t t = (tile * 8 + threadIdx.x % 8) * kTok;
-  const int live = kTok == 8 ? clamp8(p.L - t) : t < p.L ? 1 : 0;
+  __shared__ float lds[5 * 8 * 4];
+  const int64_t b = blockIdx.x / p.G, ch = (blockIdx.x - b * p.G) * p.Dg;
+  const int t = threadIdx.x % 8;
+  const bool on = t < p.L;
   const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch * p.L + t;
   const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch * p.L + t : nullptr;
   O* y = static_cast<O*>(p.y) + (b * p.D + ch) * p.L + t;
-  float mu[8], k[8];
-  norm_col_stats<T, kTok>(p, x, live, mu, k, lds);
-  for (int64_t c = threadIdx.x / 8; c < p.Dg; c += 32) {
-    float v[kTok], o[8];
-    load_tok<T, kTok>(x + c * p.L, live, v);
-    const float w = p.weight ? p.weight[ch + c] : 1.0f, bias = p.bias ? p.bias[ch + c] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) o[j] = __builtin_fmaf((v[j] - mu[j]) * k[j], w, bias);
-    if (z) {
-      load_tok<T, kTok>(z + c * p.L, live, v);
-#pragma unroll
-      for (int j = 0; j < kTok; ++j) o[j] *= silu(v[j]);
-    }
-    store_tok<O, kTok>(y + c * p.L, live, o);
+  float mu, k;
+  norm_short_stats(p, x, on, mu, k, lds);
+  for (int64_t c = threadIdx.x / 8; c < p.Dg && on; c += 32) {
+    float o = __builtin_fmaf((get1(x + c * p.L) - mu) * k, p.weight ? p.weight[ch + c] : 1.0f, p.bias ? p.bias[ch + c] : 0.0f);
+    if (z) o *= silu(get1(z + c * p.L));
+    put1(y + c * p.L, o);
   }
 }
 
@@ -195,7 +186,7 @@ __global__ __launch_bounds__(256) void norm_row_long_fwd_kernel(NormParams p) {
 
 template <typename T, typename O, int kI>
 hipError_t col_t(const NormParams& p, unsigned grid, hipStream_t s) {
-  constexpr NormShape q = sizeof(T) == 2 ? kNorm4[kI] : kNorm8[kI];
+  constexpr NormShape q = sizeof(T) == 2 ? kNormFwd2[kI] : kNormFwd4[kI];
   hipLaunchKernelGGL((norm_col_fwd_kernel<T, O, q.threads, q.lanes, q.chans>), dim3(grid), dim3(q.threads),
                      (unsigned)(2 * p.Dg * sizeof(float)), s, p);
   return hipGetLastError();
@@ -209,11 +200,9 @@ hipError_t fwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
     case 1: return col_t<T, O, 1>(p, grid, s);
     case 2: return col_t<T, O, 2>(p, grid, s);
     case 3: return col_t<T, O, 3>(p, grid, s);
-    case 4: return col_t<T, O, 4>(p, grid, s);
-    case 5: return col_t<T, O, 5>(p, grid, s);
+    case kNormColTwo: return p.z ? norm_two<T, O, false, true>(p, q, s) : norm_two<T, O, false, false>(p, q, s);
     case kNormColLong:
-      if (p.L < 8) hipLaunchKernelGGL((norm_col_long_fwd_kernel<T, O, 1>), dim3(grid), dim3(256), 0, s, p);
-      else hipLaunchKernelGGL((norm_col_long_fwd_kernel<T, O, 8>), dim3(grid), dim3(256), 0, s, p);
+      hipLaunchKernelGGL((norm_col_long_fwd_kernel<T, O>), dim3(grid), dim3(256), 0, s, p);
       break;
     case kNormRowTeam:
       hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, false>), dim3((items + 256 / p.team - 1) / (256 / p.team)), dim3(256),
@@ -228,10 +217,13 @@ hipError_t fwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
   return hipGetLastError();
 }
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 }  // namespace
 
 NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width) {
   const int64_t Dg = D / G;
+  const bool bwd = grad_width != 0;
   NormPlan q{};
   q.tiles = 1;
   q.threads = 256;
@@ -240,11 +232,13 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     q.lanes = 1;                                       // threads of a token
     while (q.kind == kNormRowTeam && q.lanes * 8 < Dg) q.lanes *= 2;
     if (q.kind == kNormRowBlock) q.threads = q.lanes = (int)((Dg + 511) / 512) * 64;
-  } else {
-    const NormShape* shapes = grad_width ? kNormBwd : in_width == 2 ? kNorm4 : kNorm8;
+  } else if (L < 8) {
     q.kind = kNormColLong;
     q.lanes = 8;
-    for (int i = 0; i < (grad_width ? 2 : (int)kNormShapes) && L >= 8 && Dg <= kNormMostLds; ++i) {
+  } else {
+    const NormShape* shapes = bwd ? (in_width + grad_width == 4 ? kNormBwd2 : kNormBwd4) : in_width == 2 ? kNormFwd2 : kNormFwd4;
+    q.kind = kNormColTwo;
+    for (int i = 0; i < (bwd ? (int)kNormBwdShapes : (int)kNormShapes); ++i) {
       const int64_t lanes = shapes[i].threads / shapes[i].lanes;      // channel lanes
       if (Dg > lanes * shapes[i].chans || L >= (int64_t(1) << 30) / (lanes + 1)) continue;   // 32-bit byte offsets
       q.kind = i;
@@ -252,32 +246,34 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
       q.lanes = shapes[i].lanes;
       break;
     }
-    const int64_t tokens = 8 * q.lanes / (L < 8 ? 8 : 1);
-    q.tiles = (L + tokens - 1) / tokens;
+    if (q.kind == kNormColTwo) {
+      q.threads = kNormStatThreads;
+      q.lanes = kNormStatLanes;
+    }
+    q.tiles = ceil_div(L, 8 * q.lanes);
   }
-  if (!grad_width) return q;
-  if (q.kind == kNormColLong && L >= 8) {
-    q.kind = kNormColTwo;
-    q.threads = kNormStatThreads;
-    // Statistics: 4 to 32 channels a thread, in as few pieces as fill the chip.
+  if (q.kind == kNormColTwo) {
+    // Statistics: 4 to 40 channels a thread, in as few pieces as give every CU a workgroup.
     const int64_t lanes = kNormStatThreads / kNormStatLanes, blocks = B * G * q.tiles;
-    q.chunks = (Dg + 32 * lanes - 1) / (32 * lanes);
-    while (q.chunks * blocks < 512 && Dg / (q.chunks * 2) >= 4 * lanes) q.chunks *= 2;
-    q.chunk = (Dg + q.chunks - 1) / q.chunks;
-    q.chunks = (Dg + q.chunk - 1) / q.chunk;
+    const int64_t least = ceil_div(Dg, 40 * lanes), most = Dg / (4 * lanes) + 1;
+    q.chunks = ceil_div(256, blocks);
+    if (q.chunks > most) q.chunks = most;
+    if (q.chunks < least) q.chunks = least;
+    q.chunk = ceil_div(Dg, q.chunks);
+    q.chunks = ceil_div(Dg, q.chunk);
     q.apply_lanes = L > 256 ? 64 : 8;
-    q.apply_chans = kNormApplyThreads / q.apply_lanes * 8;
-    q.parts = B * ((L + 8 * q.apply_lanes - 1) / (8 * q.apply_lanes));
+    q.apply_chans = kNormApplyThreads / q.apply_lanes * (bwd ? 8 : 4);
+    q.parts = B * ceil_div(L, 8 * q.apply_lanes);
     return q;
   }
   // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.
-  int64_t most = 1024 / G;
-  if (q.kind == kNormRowBlock) most = 512 / G;
+  int64_t most = 2048 / G;
+  if (q.kind == kNormRowBlock || q.threads == 512) most = 512 / G;
   if (q.kind == kNormRowTeam) most = 262144 / (q.lanes * G);
   const int64_t work = B * q.tiles;
   if (most < 1) most = 1;
   if (most > work) most = work;
-  q.parts = (work + (work + most - 1) / most - 1) / ((work + most - 1) / most);
+  q.parts = ceil_div(work, ceil_div(work, most));
   return q;
 }
 

@@ -133,49 +133,25 @@ __device__ __forceinline__ void keep(Raw8<T>& o) {
   for (int k = 0; k < (int)sizeof(T) / 2; ++k) asm("" : "+v"(o.w[k]));
 }
 
-// kTok (8 or 1) tokens of a channel, `live` of them there.
-template <typename T, int kTok>
-__device__ __forceinline__ void load_tok(const T* p, int live, float (&v)[kTok]) {
-  if constexpr (kTok == 8) {
-    const Raw8<T> r = load_raw8(p, live);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = get8(r, j);
-  } else {
-    v[0] = live ? get1(p) : 0.0f;
-  }
-}
-template <typename O, int kTok>
-__device__ __forceinline__ void store_tok(O* p, int live, const float (&o)[8]) {
-  if constexpr (kTok == 8) store8(p, o, live, live);
-  else if (live) put1(p, o[0]);
-}
-
-// Statistics of kTok tokens over the group's channels, a workgroup of 256: 32 channel lanes of 8 token
-// lanes, in two sweeps.  (Arrays of 8 whatever kTok is; the rest is not used.)
-template <typename T, int kTok>
-__device__ __forceinline__ void norm_col_stats(const NormParams& p, const T* x, int live, float (&mu)[8], float (&k)[8],
-                                               float* lds) {
-  float v[kTok];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) mu[j] = k[j] = 0.0f;
+// Statistics of one token per lane over the group's channels, fewer than 8 tokens, a workgroup of 256: 32
+// channel lanes of 8 token lanes, in two sweeps.  lds: 5 * 8 * 4 floats.
+template <typename T>
+__device__ __forceinline__ void norm_short_stats(const NormParams& p, const T* x, bool on, float& mu, float& k, float* lds) {
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (!p.rms) {
-    for (int64_t c = threadIdx.x / 8; c < p.Dg; c += 32) {
-      load_tok<T, kTok>(x + c * p.L, live, v);
-#pragma unroll
-      for (int j = 0; j < kTok; ++j) mu[j] += v[j];
-    }
-    group_sum<8, 8, 256>(mu, lds);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) mu[j] *= p.inv_dg;
+    for (int64_t c = threadIdx.x / 8; c < p.Dg && on; c += 32) v[0] += get1(x + c * p.L);
+    group_sum<8, 4, 256>(v, lds);
+    v[0] *= p.inv_dg;
   }
-  for (int64_t c = threadIdx.x / 8; c < p.Dg; c += 32) {
-    load_tok<T, kTok>(x + c * p.L, live, v);
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) k[j] = __builtin_fmaf(v[j] - mu[j], v[j] - mu[j], k[j]);
+  mu = v[0];
+  v[0] = 0.0f;
+  for (int64_t c = threadIdx.x / 8; c < p.Dg && on; c += 32) {
+    const float d = get1(x + c * p.L) - mu;
+    v[0] = __builtin_fmaf(d, d, v[0]);
   }
-  group_sum<8, 8, 256>(k, lds);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) k[j] = norm_root(__builtin_fmaf(k[j], p.inv_dg, p.eps));
+  v[1] = v[2] = v[3] = 0.0f;
+  group_sum<8, 4, 256>(v, lds);
+  k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
 }
 
 // Statistics of one token-major row, a workgroup of 256.

@@ -114,7 +114,7 @@ def norm_fwd(**kw):
     a = {**NORM, **kw}
     return _lib.lib().mamba_layer_norm_fwd(*[_vp(a[n]) for n in ("x", "z", "w", "b", "y")], a["B"], a["D"], a["L"], a["G"],
                                            *_strides(a, ("xs", "zs"), a["D"] * a["L"]), a["eps"], a["ind"], a["outd"],
-                                           a["flags"], None)
+                                           a["flags"], _vp(a["ws"]), a["wsb"], None)
 
 
 def norm_bwd(**kw):
@@ -136,7 +136,8 @@ NORM_SHARED = [
 ]
 
 
-@pytest.mark.parametrize("kw,code", NORM_SHARED + [(dict(B=1 << 27, D=1, G=1, L=1), SHAPE), (dict(B=1 << 14, D=1 << 12, G=1 << 12, L=64), SHAPE)])
+@pytest.mark.parametrize("kw,code", NORM_SHARED + [(dict(D=10000, G=1, ws=None), WS), (dict(D=10000, G=1, wsb=3), WS), (dict(D=10000, G=1, ws=P + 16), ALIGN),
+                                               (dict(B=1 << 27, D=1, G=1, L=1), SHAPE), (dict(B=1 << 14, D=1 << 12, G=1 << 12, L=64), SHAPE)])
 def test_norm_fwd_rejects_bad_arguments(kw, code):
     assert norm_fwd(**kw) == code
 
@@ -157,8 +158,10 @@ def test_workspace_sizes():
     assert L.mamba_glr_workspace_size(4, 5120, 2048) == 0             # rows enough: one launch
     assert 0 < L.mamba_glr_workspace_size(1, 2, 1 << 20) < 1 << 20
     assert L.mamba_glr_bwd_workspace_size(4, 5120, 2048) >= 3 * 4 * 5120 * 4
-    assert L.mamba_layer_norm_bwd_workspace_size(2, 12, 40, 5) == bad
-    assert L.mamba_layer_norm_bwd_workspace_size(2, 12, 40, 0) == bad
+    for f in (L.mamba_layer_norm_workspace_size, L.mamba_layer_norm_bwd_workspace_size):
+        assert f(2, 12, 40, 5) == bad and f(2, 12, 40, 0) == bad and f(0, 12, 40, 3) == bad
+    assert L.mamba_layer_norm_workspace_size(2, 12, 40, 3) == 0 and L.mamba_layer_norm_workspace_size(128, 5120, 1, 1) == 0
+    assert L.mamba_layer_norm_workspace_size(1, 10000, 64, 1) >= 2 * 64 * 4
     assert L.mamba_layer_norm_bwd_workspace_size(2, 12, 40, 3) >= 2 * 12 * 4
 
 
