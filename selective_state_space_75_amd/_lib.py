@@ -828,16 +828,13 @@ class glr_test_knobs:  # noqa: N801 (used as a context manager)
         return False
 
 
-def _row_stride(t, name, shape, dtype, device):
+def _row_stride(t, name, shape, dtype, device, row):
     """_check_rows without the view it makes: for a call of one token the checks are most of the
-    call.  (B, D, L) or (B, D); an absent tensor has stride 0.  What is not plainly right is left to
-    _check_rows, which names it."""
+    call.  (B, D, L) or (B, D) of `row` numbers a batch row; an absent tensor has stride 0.  What is not
+    plainly right is left to _check_rows, which names it."""
     if t is None:
         return 0
     if isinstance(t, _torch().Tensor) and t.dtype == dtype and t.shape == shape and t.device == device:
-        row = 1
-        for n in shape[1:]:
-            row *= n
         if t.is_contiguous():
             return row
         s = t.stride()
@@ -858,6 +855,14 @@ def _plain(t, name, shape, dtype, device):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _like(x, dtype):
+    """A dense tensor of x's shape (empty_like is the shorter call)."""
+    torch = _torch()
+    if x.dtype == dtype and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=dtype, device=x.device)
 
 
 _HERE = contextlib.nullcontext()
@@ -892,8 +897,9 @@ def _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend):
     shape, dev, dt = x.shape, x.device, x.dtype
     if r is None:
         raise TypeError("r must be a torch.Tensor")
-    strides = (_row_stride(x, "x", shape, dt, dev), _row_stride(r, "r", shape, dt, dev),
-               _row_stride(i, "i", shape, dt, dev), _row_stride(z, "z", shape, dt, dev))
+    row = shape[1] * shape[2] if len(shape) == 3 else shape[1]
+    strides = (_row_stride(x, "x", shape, dt, dev, row), _row_stride(r, "r", shape, dt, dev, row),
+               _row_stride(i, "i", shape, dt, dev, row), _row_stride(z, "z", shape, dt, dev, row))
     if blend:
         if A is not None:
             raise ValueError("A is not used with blend=True and must be None")
@@ -936,7 +942,7 @@ def glr_fwd(x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *, blend=Fal
     out_dt = in_dt if out_dtype is None else out_dtype
     with _there(dev, stream):
         if y is None:
-            y = torch.empty(shape, dtype=out_dt, device=dev)
+            y = _like(x, out_dt)
         yp, last = _plain(y, "y", shape, out_dt, dev), None
         if return_final_state:
             if final_state is None:
@@ -980,13 +986,13 @@ def glr_bwd(x, r, i, A, r_bias, i_bias, z, dy, *, blend=False, initial_state=Non
     gdt, gcode = dy.dtype, _dtype_code(dy)
     dyp = _plain(dy, "dy", shape, gdt, dev)
     with _there(dev, stream):
-        def new(shape, dtype, wanted=True):
-            return torch.empty(shape, dtype=dtype, device=dev) if wanted else None
+        def param(wanted=True):
+            return torch.empty(D, dtype=torch.float32, device=dev) if wanted else None
 
-        f32 = torch.float32
-        out = {"dx": new(shape, gdt), "dr": new(shape, gdt), "di": new(shape, gdt, i is not None),
-               "dz": new(shape, gdt, z is not None), "dA": new((D,), f32, not blend), "dr_bias": new((D,), f32),
-               "di_bias": new((D,), f32, i is not None), "dinitial_state": new((B, D), f32, init is not None)}
+        out = {"dx": torch.empty_like(dy), "dr": torch.empty_like(dy), "di": None if i is None else torch.empty_like(dy),
+               "dz": None if z is None else torch.empty_like(dy), "dA": param(not blend), "dr_bias": param(),
+               "di_bias": param(i is not None),
+               "dinitial_state": None if init is None else torch.empty_like(initial_state)}
         workspace = _workspace(workspace, glr_bwd_workspace_size(B, D, L), dev)
         st = lib().mamba_glr_bwd(*ins, init, ends, dyp, dfinal, *[_addr(t) for t in out.values()], B, D, L, *strides,
                                  code, gcode, FLAG_BLEND if blend else 0, _addr(workspace), _nbytes(workspace),
@@ -1013,7 +1019,7 @@ def glr_update(state, x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *,
     out_dt = in_dt if out_dtype is None else out_dtype
     with _there(dev, stream):
         if y is None:
-            y = torch.empty(shape, dtype=out_dt, device=dev)
+            y = _like(x, out_dt)
         st = lib().mamba_glr_update(pool, rows, *ins, _plain(y, "y", shape, out_dt, dev), B, D, S, *strides, code,
                                     _dtype_code(y), FLAG_BLEND if blend else 0, _raw_stream(dev, stream))
     if st != 0:
@@ -1031,9 +1037,10 @@ def _norm_inputs(x, weight, bias, z, groups):
     D = shape[1]
     if groups < 1 or D % groups:
         raise ValueError("%d channels do not divide into %d groups" % (D, groups))
-    strides = _row_stride(x, "x", shape, dt, dev), _row_stride(z, "z", shape, dt, dev)
+    L = shape[2] if len(shape) == 3 else 1
+    strides = _row_stride(x, "x", shape, dt, dev, D * L), _row_stride(z, "z", shape, dt, dev, D * L)
     ins = (x.data_ptr(), _addr(z), _plain(weight, "weight", (D,), f32, dev), _plain(bias, "bias", (D,), f32, dev))
-    return dev, code, ins, (shape[0], D, shape[2] if len(shape) == 3 else 1, groups) + strides
+    return dev, code, ins, (shape[0], D, L, groups) + strides
 
 
 def layer_norm_workspace_size(B: int, D: int, L: int, groups: int = 1) -> int:
@@ -1056,7 +1063,7 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms
     out_dt = x.dtype if out_dtype is None else out_dtype
     with _there(dev, stream):
         if y is None:
-            y = torch.empty(x.shape, dtype=out_dt, device=dev)
+            y = _like(x, out_dt)
         workspace = _workspace(workspace, layer_norm_workspace_size(*sizes[:4]), dev)
         st = lib().mamba_layer_norm_fwd(*ins, _plain(y, "y", x.shape, out_dt, dev), *sizes, eps, code, _dtype_code(y),
                                         FLAG_RMS if rms else 0, _addr(workspace), _nbytes(workspace),
@@ -1084,8 +1091,7 @@ def layer_norm_bwd(x, weight, bias, z, dy, *, groups=1, eps=1e-5, rms=False, wor
     shape, gdt, gcode = x.shape, dy.dtype, _dtype_code(dy)
     dyp = _plain(dy, "dy", shape, gdt, dev)
     with _there(dev, stream):
-        out = {"dx": torch.empty(shape, dtype=gdt, device=dev),
-               "dz": None if z is None else torch.empty(shape, dtype=gdt, device=dev),
+        out = {"dx": torch.empty_like(dy), "dz": None if z is None else torch.empty_like(dy),
                "dweight": torch.empty(shape[1], dtype=torch.float32, device=dev),
                "dbias": torch.empty(shape[1], dtype=torch.float32, device=dev)}
         workspace = _workspace(workspace, layer_norm_bwd_workspace_size(*sizes[:4]), dev)

@@ -51,20 +51,29 @@ void cut(GlrPlan& q, int64_t L, int64_t S) {
 }
 
 // Sizes-only plan of the forward pass: waves per row, and segments of L.
+// A workgroup's waves lie one after the other on the row, so more of them read longer stretches at a time, and
+// a row of up to 16 waves' tokens is one tile.  1, 2, 4, 8, 16 waves, in us: 20480 rows, L = 2048: 82.2, 80.3,
+// 78.7; 4096 rows, L = 32768: 280, 280, 275, 267, 250; 1536 rows, L = 8192: 39.4, 35.4, 28.7, 28.4, 29.4; 16
+// rows, L = 4096: 14.6, 10.5, 8.0, 7.0.  Rows of two tiles are the exception where there are rows enough for
+// every wave slot: 7680 rows, L = 1000: 20.1, 21.2 (2000 rows, L = 2000: 15.6, 14.2).
+// Few rows are cut into segments of a tile of 4 waves, in two launches, as many as make 1024 workgroups.
+// One segment of 16 waves against that: 16 rows, L = 32768: 18.6, 10.6 (16 segments); 64 rows: 18.8, 15.1 (16);
+// 512 rows: 38.3, 54.8 (4).
 GlrPlan make_glr_plan(int64_t B, int64_t D, int64_t L) {
   GlrPlan q;
   const int64_t rows = B * D, tiles = ceil_div(L, mamba::kGlrWave);
-  int64_t waves = ceil_div(8192, rows);
-  if (waves > 16) waves = 16;
+  int64_t waves = tiles <= 2 && rows >= 4096 ? 1 : 16, S = 1;
+  if (rows <= 128 && tiles >= 16) {
+    S = tiles / 4 < 1024 / rows ? tiles / 4 : 1024 / rows;
+    waves = 4;
+  }
   const int forced = g_waves.load();
   if (forced > 0) waves = forced;
-  if (waves > tiles) waves = tiles;
-  int64_t S = 1024 / (rows * waves);
-  if (S > tiles / (2 * waves)) S = tiles / (2 * waves);
   const int64_t forced_s = g_segments.load();
   if (forced_s > 0) S = forced_s;
-  cut(q, L, S < 1 ? 1 : S);
-  q.waves = (int)waves;
+  cut(q, L, S);
+  const int64_t own = ceil_div(q.seg_len, mamba::kGlrWave);
+  q.waves = (int)(waves < own ? waves : own);
   return q;
 }
 

@@ -113,7 +113,9 @@ __global__ __launch_bounds__(1024) void glr_fwd_kernel(GlrParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr, j));
       }
-      store8(y + t, o, live, clamp8(t1 - t));
+      // Past the caches where whole lines are written at once; 4-byte outputs take two stores a line.  20480 rows,
+      // L = 2048, fp32 out: 94.8 us past the caches, 89.6 through them; 4096 rows, L = 32768, bf16: 250, 260.
+      store8<O, sizeof(O) == 2>(y + t, o, live, clamp8(t1 - t));
       carry = __builtin_fmaf(tile_total.P, carry, tile_total.H);
     }
   }

@@ -267,7 +267,7 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     return q;
   }
   // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.
-  int64_t most = 2048 / G;
+  int64_t most = 1024 / G;
   if (q.kind == kNormRowBlock || q.threads == 512) most = 512 / G;
   if (q.kind == kNormRowTeam) most = 262144 / (q.lanes * G);
   const int64_t work = B * q.tiles;

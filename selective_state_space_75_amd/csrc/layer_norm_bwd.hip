@@ -41,13 +41,15 @@ __global__ __launch_bounds__(kThreads) void norm_col_bwd_kernel(NormParams p) {
     const Gr* dy = static_cast<const Gr*>(p.dy) + row;
     Gr* dx = static_cast<Gr*>(p.dx) + row;
     Gr* dz = kGate ? static_cast<Gr*>(p.dz) + row : nullptr;
-    Raw8<T> r[kC];
+    constexpr bool kHold = kGate && kC <= 4;             // z stays too
+    Raw8<T> r[kC], zh[kHold ? kC : 1];
     Raw8<Gr> dr[kC];
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
       if (c0 + k * kCL < Dg) {
         r[k] = load_all8(lane_at(x + k * step, at));
         dr[k] = load_all8(lane_at(dy + k * step, at));
+        if constexpr (kHold) zh[k] = load_all8(lane_at(z + k * step, at));
       }
     }
     float mu[8], v[24];
@@ -78,8 +80,10 @@ __global__ __launch_bounds__(kThreads) void norm_col_bwd_kernel(NormParams p) {
       Raw8<T> zr[kBatch];
       if constexpr (kGate) {
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-          if (c0 + (kk + q) * kCL < Dg) zr[q] = load_all8(lane_at(z + (kk + q) * step, at));
+        for (int q = 0; q < kBatch; ++q) {
+          if constexpr (kHold) zr[q] = zh[kk + q];
+          else if (c0 + (kk + q) * kCL < Dg) zr[q] = load_all8(lane_at(z + (kk + q) * step, at));
+        }
       }
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
@@ -110,6 +114,7 @@ __global__ __launch_bounds__(kThreads) void norm_col_bwd_kernel(NormParams p) {
       if (k * kCL < Dg) {
         keep(r[k]);
         keep(dr[k]);
+        if constexpr (kHold) keep(zh[k]);
       }
     }
     asm("" : "+s"(step));
@@ -119,8 +124,10 @@ __global__ __launch_bounds__(kThreads) void norm_col_bwd_kernel(NormParams p) {
       Raw8<T> zr[kBatch];
       if constexpr (kGate) {
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-          if (c0 + (kk + q) * kCL < Dg) zr[q] = load_all8(lane_at(z + (kk + q) * step, at));
+        for (int q = 0; q < kBatch; ++q) {
+          if constexpr (kHold) zr[q] = zh[kk + q];
+          else if (c0 + (kk + q) * kCL < Dg) zr[q] = load_all8(lane_at(z + (kk + q) * step, at));
+        }
       }
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
