@@ -986,12 +986,10 @@ def glr_bwd(x, r, i, A, r_bias, i_bias, z, dy, *, blend=False, initial_state=Non
     gdt, gcode = dy.dtype, _dtype_code(dy)
     dyp = _plain(dy, "dy", shape, gdt, dev)
     with _there(dev, stream):
-        def param(wanted=True):
-            return torch.empty(D, dtype=torch.float32, device=dev) if wanted else None
-
+        sums = torch.empty((3, D), dtype=torch.float32, device=dev).unbind()
         out = {"dx": torch.empty_like(dy), "dr": torch.empty_like(dy), "di": None if i is None else torch.empty_like(dy),
-               "dz": None if z is None else torch.empty_like(dy), "dA": param(not blend), "dr_bias": param(),
-               "di_bias": param(i is not None),
+               "dz": None if z is None else torch.empty_like(dy), "dA": None if blend else sums[0], "dr_bias": sums[1],
+               "di_bias": None if i is None else sums[2],
                "dinitial_state": None if init is None else torch.empty_like(initial_state)}
         workspace = _workspace(workspace, glr_bwd_workspace_size(B, D, L), dev)
         st = lib().mamba_glr_bwd(*ins, init, ends, dyp, dfinal, *[_addr(t) for t in out.values()], B, D, L, *strides,
@@ -1091,9 +1089,9 @@ def layer_norm_bwd(x, weight, bias, z, dy, *, groups=1, eps=1e-5, rms=False, wor
     shape, gdt, gcode = x.shape, dy.dtype, _dtype_code(dy)
     dyp = _plain(dy, "dy", shape, gdt, dev)
     with _there(dev, stream):
+        sums = torch.empty((2, shape[1]), dtype=torch.float32, device=dev).unbind()
         out = {"dx": torch.empty_like(dy), "dz": None if z is None else torch.empty_like(dy),
-               "dweight": torch.empty(shape[1], dtype=torch.float32, device=dev),
-               "dbias": torch.empty(shape[1], dtype=torch.float32, device=dev)}
+               "dweight": sums[0], "dbias": sums[1]}
         workspace = _workspace(workspace, layer_norm_bwd_workspace_size(*sizes[:4]), dev)
         st = lib().mamba_layer_norm_bwd(*ins, dyp, *[_addr(t) for t in out.values()], *sizes, eps, code, gcode,
                                         FLAG_RMS if rms else 0, _addr(workspace), _nbytes(workspace),

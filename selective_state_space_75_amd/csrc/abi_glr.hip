@@ -156,12 +156,12 @@ size_t norm_bwd_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
   return most;
 }
 
-// Whether every launch is one; items: workgroups of a plan of one launch.
+// Whether every launch is one; items: tokens and groups (forward) or parts and groups (backward).
 bool norm_fits(const mamba::NormPlan& q, int64_t B, int64_t D, int64_t L, int64_t G, int64_t items) {
   if (q.kind == mamba::kNormColTwo)
     return mamba::launch_fits(B * G * q.chunks * q.tiles, q.threads) &&
            mamba::launch_fits(B * ceil_div(L, 8 * q.apply_lanes) * G * ceil_div(D / G, q.apply_chans), mamba::kNormApplyThreads);
-  return mamba::launch_fits(q.kind == mamba::kNormRowTeam ? ceil_div(items, 256 / q.lanes) : items, q.threads);
+  return mamba::launch_fits(items, q.threads);
 }
 
 int check_norm(const mamba::NormParams& p, int in_dtype, int out_dtype, unsigned flags) {
@@ -326,7 +326,7 @@ int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, cons
   if (!dy || !dx || (z && !dz) || !dweight || !dbias) return MAMBA_ERR_NULL;
   if (!all_aligned({dy, dx, dz}, width(grad_dtype)) || !all_aligned({dweight, dbias}, 4)) return MAMBA_ERR_ALIGN;
   const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), (int)width(grad_dtype));
-  if (!norm_fits(q, B, D, L, groups, q.parts * groups) || !mamba::launch_fits(ceil_div(2 * D, 32), 256))
+  if (!norm_fits(q, B, D, L, groups, q.parts * groups) || !mamba::launch_fits(ceil_div(2 * D, 16), 256))
     return MAMBA_ERR_SHAPE;
   norm_set(p, q);
   const size_t need = norm_bwd_bytes(B, D, L, groups);

@@ -174,6 +174,21 @@ __device__ __forceinline__ float wave_sum63(float x) {
   return x;
 }
 
+// Sum of a[i * stride] over i = y, y + 16, ... below n, four loads under way at a time.
+__device__ __forceinline__ float strided_sum(const float* a, int64_t stride, int64_t y, int64_t n) {
+  float o = 0.0f;
+  int64_t i = y;
+  for (; i + 48 < n; i += 64) {
+    const float v0 = a[i * stride], v1 = a[(i + 16) * stride], v2 = a[(i + 32) * stride], v3 = a[(i + 48) * stride];
+    o += v0;
+    o += v1;
+    o += v2;
+    o += v3;
+  }
+  for (; i < n; i += 16) o += a[i * stride];
+  return o;
+}
+
 // 1 - e^(2 l) for l = x2 ln2 <= 0, a = 2^x2 given.  For |2 l| < 1/8 the Taylor series to
 // (2 l)^5 (truncation below (1/8)^5 / 720 = 4.3e-8 relative); otherwise 1 - a^2 in one rounding,
 // where the error of a (about one unit of 2^-24) is at most 1e-6 of the result, 5e-7 of its root.

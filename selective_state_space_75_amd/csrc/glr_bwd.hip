@@ -176,24 +176,28 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
   if (threadIdx.x < 3) {
     float o = 0.0f;
     for (int w = 0; w < waves; ++w) o += sums[threadIdx.x][w];
-    p.part[((b * p.S + seg) * 3 + threadIdx.x) * p.D + d] = o;
+    if (rows * p.S == p.D) {                     // nothing to add up
+      float* dst = threadIdx.x == 0 ? p.dA : threadIdx.x == 1 ? p.dr_bias : p.di_bias;
+      if (dst) dst[d] = o;
+    } else {
+      p.part[((b * p.S + seg) * 3 + threadIdx.x) * p.D + d] = o;
+    }
   }
 }
 
-// Sums over batch rows and segments: 32 channels x 8 parts of them per workgroup.
+// Sums over batch rows and segments: 16 channels x 16 shares of them per workgroup.
 __global__ __launch_bounds__(256) void glr_sum_kernel(GlrParams p) {
-  __shared__ float part[8][32];
-  const int64_t blocks = (p.D + 31) / 32;
+  __shared__ float share[16][16];
+  const int64_t blocks = (p.D + 15) / 16;
   const int k = (int)(blockIdx.x / blocks);
-  const int64_t d = (blockIdx.x - k * blocks) * 32 + (threadIdx.x & 31);
-  const int y = threadIdx.x >> 5;
+  const int64_t d = (blockIdx.x - k * blocks) * 16 + (threadIdx.x & 15);
+  const int y = threadIdx.x >> 4;
   float o = 0.0f;
-  if (d < p.D)
-    for (int64_t e = y; e < p.B * p.S; e += 8) o += p.part[(e * 3 + k) * p.D + d];
-  part[y][threadIdx.x & 31] = o;
+  if (d < p.D) o = strided_sum(p.part + k * p.D + d, 3 * p.D, y, p.B * p.S);
+  share[y][threadIdx.x & 15] = o;
   __syncthreads();
   if (y || d >= p.D) return;
-  for (int w = 1; w < 8; ++w) o += part[w][threadIdx.x];
+  for (int w = 1; w < 16; ++w) o += share[w][threadIdx.x];
   float* dst = k == 0 ? p.dA : k == 1 ? p.dr_bias : p.di_bias;
   if (dst) dst[d] = o;
 }
@@ -209,7 +213,8 @@ hipError_t bwd_n(const GlrParams& p, hipStream_t s) {
   hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, kThreads>), grid, block, 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(glr_sum_kernel, dim3((unsigned)(3 * ((p.D + 31) / 32))), dim3(256), 0, s, p);
+  if (p.B * p.S == 1) return hipSuccess;
+  hipLaunchKernelGGL(glr_sum_kernel, dim3((unsigned)(3 * ((p.D + 15) / 16))), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

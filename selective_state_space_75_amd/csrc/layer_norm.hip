@@ -256,7 +256,7 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     // Statistics: 4 to 40 channels a thread, in as few pieces as give every CU a workgroup.
     const int64_t lanes = kNormStatThreads / kNormStatLanes, blocks = B * G * q.tiles;
     const int64_t least = ceil_div(Dg, 40 * lanes), most = Dg / (4 * lanes) + 1;
-    q.chunks = ceil_div(256, blocks);
+    q.chunks = blocks < 256 ? 256 / blocks : 1;
     if (q.chunks > most) q.chunks = most;
     if (q.chunks < least) q.chunks = least;
     q.chunk = ceil_div(Dg, q.chunks);
@@ -267,10 +267,8 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     return q;
   }
   // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.
-  int64_t most = 1024 / G;
-  if (q.kind == kNormRowBlock || q.threads == 512) most = 512 / G;
-  if (q.kind == kNormRowTeam) most = 262144 / (q.lanes * G);
-  const int64_t work = B * q.tiles;
+  int64_t most = (q.threads > 256 ? 512 : 1024) / G;
+  const int64_t work = q.kind == kNormRowTeam ? ceil_div(B, 256 / q.lanes) : B * q.tiles;
   if (most < 1) most = 1;
   if (most > work) most = work;
   q.parts = ceil_div(work, ceil_div(work, most));

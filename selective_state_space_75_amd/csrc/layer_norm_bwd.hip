@@ -225,16 +225,16 @@ __global__ __launch_bounds__(256) void norm_col_long_bwd_kernel(NormParams p) {
   }
 }
 
-// Token-major: a team of lanes, or a workgroup, takes every parts-th token of a group; 8 channels a thread,
-// the last thread the group's last 8 whole (see norm_row_fwd_kernel).
+// Token-major: a workgroup takes a group of channels and every parts-th share of the tokens, one a team of lanes
+// (or one at a time) at once; 8 channels a thread, the last thread the group's last 8 whole (see
+// norm_row_fwd_kernel).  Its teams' sums of dw and db are added up at the end.
 template <typename T, typename Gr, bool kBlock>
 __global__ __launch_bounds__(kBlock ? 1024 : 256) void norm_row_bwd_kernel(NormParams p) {
-  __shared__ float lds[3 * 16];
-  const int team = p.team;
-  const int64_t id = kBlock ? blockIdx.x : (int64_t)blockIdx.x * (256 / team) + threadIdx.x / team;
+  __shared__ float lds[kBlock ? 3 * 16 : 4 * 64 * 16];
+  const int team = p.team, teams = kBlock ? 1 : 256 / team, own = kBlock ? 0 : threadIdx.x / team;
   const int at = (kBlock ? threadIdx.x : threadIdx.x % team) * 8, Dg = (int)p.Dg;
-  const int64_t part = id / p.G, ch = (id - part * p.G) * p.Dg;
-  const bool on = at < Dg && part < p.parts;
+  const int64_t part = blockIdx.x / p.G, ch = (blockIdx.x - part * p.G) * p.Dg;
+  const bool on = at < Dg;
   const int c = at < Dg - 8 ? at : Dg - 8, dup = on ? at - c : 8;
   Raw8<float> wr, br;
   if (p.weight) wr = load_all8(p.weight + ch + c);
@@ -242,7 +242,10 @@ __global__ __launch_bounds__(kBlock ? 1024 : 256) void norm_row_bwd_kernel(NormP
   float sw[8], sb[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sw[j] = sb[j] = 0.0f;
-  for (int64_t b = part; b < p.B; b += p.parts) {
+  // A wave's lanes stay together: a team past the last token goes through that one again and leaves it out.
+  for (int64_t first = part * teams; first < p.B; first += p.parts * teams) {
+    const bool mine = first + own < p.B;
+    const int64_t b = mine ? first + own : p.B - 1;
     const Raw8<T> r = load_all8(static_cast<const T*>(p.x) + b * p.x_stride + ch + c);
     const Raw8<Gr> dr = load_all8(static_cast<const Gr*>(p.dy) + b * p.D + ch + c);
     Raw8<T> zr;
@@ -283,15 +286,42 @@ __global__ __launch_bounds__(kBlock ? 1024 : 256) void norm_row_bwd_kernel(NormP
                __builtin_fmaf(zj, 1.0f - s, 1.0f);
         dm[j] *= zj * s;
       }
-      if (on) store8(static_cast<Gr*>(p.dz) + out, o, 8, 8);
+      if (on && mine) store8(static_cast<Gr*>(p.dz) + out, o, 8, 8);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       o[j] = k * (__builtin_fmaf(dm[j], p.weight ? get8(wr, j) : 1.0f, -mg) - xh[j] * mx);
-      sw[j] = __builtin_fmaf(dm[j], xh[j], sw[j]);
-      sb[j] += dm[j];
+      if (mine) {
+        sw[j] = __builtin_fmaf(dm[j], xh[j], sw[j]);
+        sb[j] += dm[j];
+      }
     }
-    if (on) store8(static_cast<Gr*>(p.dx) + out, o, 8, 8);
+    if (on && mine) store8(static_cast<Gr*>(p.dx) + out, o, 8, 8);
+  }
+  if constexpr (!kBlock) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int m = team; m < 64; m *= 2) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sw[j] += __shfl_xor(sw[j], m);
+        sb[j] += __shfl_xor(sb[j], m);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      lds[(wave * 64 + lane) * 16 + j] = sw[j];
+      lds[(wave * 64 + lane) * 16 + 8 + j] = sb[j];
+    }
+    __syncthreads();
+    if (own) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sw[j] = sb[j] = 0.0f;
+      for (int w = 0; w < 4; ++w) {
+        sw[j] += lds[(w * 64 + lane) * 16 + j];
+        sb[j] += lds[(w * 64 + lane) * 16 + 8 + j];
+      }
+    }
   }
   if (!on) return;
   // channels that two threads have: both hold the same sums
@@ -339,18 +369,17 @@ __global__ __launch_bounds__(256) void norm_row_long_bwd_kernel(NormParams p) {
   }
 }
 
-// dweight and dbias from their parts: 32 channels x 8 parts at a time per workgroup.
+// dweight and dbias from their parts: 16 channels x 16 shares of them per workgroup, four loads under way.
 __global__ __launch_bounds__(256) void norm_sum_kernel(NormParams p) {
-  __shared__ float half[8][32];
-  const int64_t n = 2 * p.D, c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-  const int y = threadIdx.x >> 5;
+  __shared__ float share[16][16];
+  const int64_t n = 2 * p.D, c = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
+  const int y = threadIdx.x >> 4;
   float o = 0.0f;
-  if (c < n)
-    for (int64_t i = y; i < p.parts; i += 8) o += p.part[i * n + c];
-  half[y][threadIdx.x & 31] = o;
+  if (c < n) o = strided_sum(p.part + c, n, y, p.parts);
+  share[y][threadIdx.x & 15] = o;
   __syncthreads();
   if (y || c >= n) return;
-  for (int w = 1; w < 8; ++w) o += half[w][threadIdx.x];
+  for (int w = 1; w < 16; ++w) o += share[w][threadIdx.x];
   if (c < p.D) p.dweight[c] = o;
   else p.dbias[c - p.D] = o;
 }
@@ -378,8 +407,7 @@ hipError_t main_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
       hipLaunchKernelGGL((norm_col_long_bwd_kernel<T, Gr>), dim3(grid), dim3(256), 0, s, p);
       break;
     case kNormRowTeam:
-      hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, false>), dim3((grid + 256 / p.team - 1) / (256 / p.team)), dim3(256),
-                         0, s, p);
+      hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, false>), dim3(grid), dim3(256), 0, s, p);
       break;
     case kNormRowBlock:
       hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, true>), dim3(grid), dim3(q.threads), 0, s, p);
@@ -394,7 +422,7 @@ template <typename T, typename Gr>
 hipError_t bwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
   const hipError_t e = main_t<T, Gr>(p, q, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((2 * p.D + 31) / 32)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((2 * p.D + 15) / 16)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
