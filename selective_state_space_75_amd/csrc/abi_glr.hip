@@ -39,6 +39,7 @@ std::atomic<int64_t> g_segments{0};
 
 struct GlrPlan {
   int64_t S = 1, seg_len = 0;
+  int64_t group = 1, groups = 1;                // backward: segments of a workgroup, workgroups of a row
   int waves = 1;
 };
 
@@ -77,16 +78,24 @@ GlrPlan make_glr_plan(int64_t B, int64_t D, int64_t L) {
   return q;
 }
 
-// The backward pass: a workgroup holds its segment on the chip.
-GlrPlan make_glr_bwd_plan(int64_t L) {
+// The backward pass: a workgroup holds a segment on the chip, a row of up to 16 waves in one.  Longer rows are
+// cut.  With 512 rows or more a workgroup takes all segments of a row, of 4 waves each (three such workgroups
+// share a CU, of 8 waves one: 2560 rows, L = 16384, bf16: 213 us, 263), and the first launch reads three arrays
+// instead of five; below that, a workgroup takes one segment of 8 waves.  One segment against all, bf16,
+// L = 32768, in us: 128 rows: 45, 68; 256: 63, 73; 512: 116, 110; 900: 194, 183; 1300: 270, 241; L = 12000, 512 rows:
+// 50, 49.
+GlrPlan make_glr_bwd_plan(int64_t B, int64_t D, int64_t L) {
   GlrPlan q;
   const int forced = g_waves.load();
-  const int64_t most = (forced > 0 ? forced : 16) * int64_t(mamba::kGlrWave);
-  int64_t S = ceil_div(L, most);
+  const bool many = B * D >= 512;
+  const int64_t waves = forced > 0 ? forced : L <= 16 * mamba::kGlrWave ? 16 : many ? 4 : 8;
+  int64_t S = ceil_div(L, waves * mamba::kGlrWave);
   const int64_t forced_s = g_segments.load();
   if (forced_s > S) S = forced_s;
   cut(q, L, S);
   q.waves = (int)ceil_div(q.seg_len, mamba::kGlrWave);
+  if (many && q.waves <= 8) q.group = q.S;
+  q.groups = ceil_div(q.S, q.group);
   return q;
 }
 
@@ -122,10 +131,10 @@ size_t glr_bytes(const GlrPlan& q, int64_t B, int64_t D) {
   return q.S > 1 ? align256(size_t(B) * D * q.S * 2 * sizeof(float)) : 0;
 }
 size_t glr_bwd_sum_bytes(const GlrPlan& q, int64_t B, int64_t D) {
-  return q.S > 1 ? align256(size_t(B) * D * q.S * 3 * sizeof(float)) : 0;
+  return q.S > 1 ? align256(size_t(B) * D * q.S * (q.groups > 1 ? 3 : 2) * sizeof(float)) : 0;
 }
 size_t glr_bwd_bytes(const GlrPlan& q, int64_t B, int64_t D) {
-  return glr_bwd_sum_bytes(q, B, D) + align256(size_t(B) * q.S * 3 * D * sizeof(float));
+  return glr_bwd_sum_bytes(q, B, D) + align256(size_t(B) * q.groups * 3 * D * sizeof(float));
 }
 
 bool norm_sizes_ok(int64_t B, int64_t D, int64_t L, int64_t G) {
@@ -245,7 +254,7 @@ int mamba_glr_update(float* state, const int32_t* slots, const void* x, const vo
 
 size_t mamba_glr_bwd_workspace_size(int64_t B, int64_t D, int64_t L) {
   if (!glr_sizes_ok(B, D, L)) return (size_t)-1;
-  return glr_bwd_bytes(make_glr_bwd_plan(L), B, D);
+  return glr_bwd_bytes(make_glr_bwd_plan(B, D, L), B, D);
 }
 
 int mamba_glr_bwd(const void* x, const void* r, const void* i, const void* z, const float* A, const float* r_bias,
@@ -263,12 +272,12 @@ int mamba_glr_bwd(const void* x, const void* r, const void* i, const void* z, co
     return MAMBA_ERR_NULL;
   if (!all_aligned({dy, dx, dr, di, dz}, width(grad_dtype))) return MAMBA_ERR_ALIGN;
   if (!all_aligned({dfinal_state, dA, dr_bias, di_bias, dinitial_state}, 4)) return MAMBA_ERR_ALIGN;
-  const GlrPlan q = make_glr_bwd_plan(L);
+  const GlrPlan q = make_glr_bwd_plan(B, D, L);
   if (B * D > kMaxElems / q.S || !mamba::launch_fits(B * D * q.S, 64 * q.waves)) return MAMBA_ERR_SHAPE;
   const size_t need = glr_bwd_bytes(q, B, D);
   if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
-  p.S = q.S; p.seg_len = q.seg_len; p.waves = q.waves;
+  p.S = q.S; p.seg_len = q.seg_len; p.waves = q.waves; p.group = q.group; p.groups = q.groups;
   p.sum = static_cast<float*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + glr_bwd_sum_bytes(q, B, D));
   p.dy = dy; p.dfinal = dfinal_state;

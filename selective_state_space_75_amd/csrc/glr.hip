@@ -14,21 +14,6 @@
 namespace mamba {
 namespace {
 
-// State in front of segment `seg`: the initial state through the segments before it, 64 at a
-// time.  sum: this row's (P, H) pairs, `stride` floats from one segment to the next.
-__device__ __forceinline__ float glr_enter(const float* sum, int stride, int64_t seg, float h, int lane) {
-  for (int64_t base = 0; base < seg; base += 64) {
-    Affine v;
-    if (base + lane < seg) {
-      v.P = sum[(base + lane) * stride];
-      v.H = sum[(base + lane) * stride + 1];
-    }
-    v = scan_up(v);
-    h = __builtin_fmaf(lane_of(v.P, 63), h, lane_of(v.H, 63));
-  }
-  return h;
-}
-
 // kSummary: only the (P, H) of each segment but the last.
 template <typename T, typename O, bool kBlend, bool kSummary>
 __global__ __launch_bounds__(1024) void glr_fwd_kernel(GlrParams p) {
@@ -162,12 +147,19 @@ __global__ __launch_bounds__(256) void glr_update_kernel(GlrParams p) {
   }
 }
 
+template <typename T>
+hipError_t summary_t(const GlrParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.B * p.D * (p.S - 1))), block(64u * p.waves);
+  if (p.blend) hipLaunchKernelGGL((glr_fwd_kernel<T, T, true, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((glr_fwd_kernel<T, T, false, true>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
 template <typename T, typename O, bool kBlend>
 hipError_t fwd_b(const GlrParams& p, hipStream_t s) {
   const unsigned rows = (unsigned)(p.B * p.D), threads = 64u * p.waves;
   if (p.S > 1) {
-    hipLaunchKernelGGL((glr_fwd_kernel<T, T, kBlend, true>), dim3(rows * (unsigned)(p.S - 1)), dim3(threads), 0, s, p);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = summary_t<T>(p, s);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((glr_fwd_kernel<T, O, kBlend, false>), dim3(rows * (unsigned)p.S), dim3(threads), 0, s, p);
@@ -192,6 +184,11 @@ hipError_t upd_t(const GlrParams& p, hipStream_t s) {
 hipError_t launch_glr_fwd(const GlrParams& p, Dt in, Dt out, hipStream_t s) {
   if (in == Dt::BF16) return out == Dt::BF16 ? fwd_t<uint16_t, uint16_t>(p, s) : fwd_t<uint16_t, float>(p, s);
   return out == Dt::BF16 ? fwd_t<float, uint16_t>(p, s) : fwd_t<float, float>(p, s);
+}
+
+// (P, H) of every segment but a row's last.
+hipError_t launch_glr_summary(const GlrParams& p, Dt in, hipStream_t s) {
+  return in == Dt::BF16 ? summary_t<uint16_t>(p, s) : summary_t<float>(p, s);
 }
 
 hipError_t launch_glr_update(const GlrParams& p, Dt in, Dt out, hipStream_t s) {

@@ -49,6 +49,14 @@ __device__ __forceinline__ float get8(const Raw8<float>& r, int j) {
   return __builtin_bit_cast(float, w);
 }
 
+// The numbers as they lie in memory are what stays in registers between two sweeps: without this the
+// compiler keeps the widened and centred ones of the first for the second, twice the registers and more.
+template <typename T>
+__device__ __forceinline__ void keep(Raw8<T>& o) {
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k) asm("" : "+v"(o.w[k]));
+}
+
 __device__ __forceinline__ void put1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put1(uint16_t* p, float x) { *p = f32_to_bf16(x); }
 __device__ __forceinline__ float get1(const float* p) { return *p; }
@@ -161,6 +169,21 @@ __device__ __forceinline__ Affine shift_down(const Affine& v) {
   o.P = dpp<0x130, 0xf>(1.0f, v.P);
   o.H = dpp<0x130, 0xf>(0.0f, v.H);
   return o;
+}
+
+// State in front of segment `seg`: the initial state through the segments before it, 64 at a
+// time.  sum: this row's (P, H) pairs, `stride` floats from one segment to the next.
+__device__ __forceinline__ float glr_enter(const float* sum, int stride, int64_t seg, float h, int lane) {
+  for (int64_t base = 0; base < seg; base += 64) {
+    Affine v;
+    if (base + lane < seg) {
+      v.P = sum[(base + lane) * stride];
+      v.H = sum[(base + lane) * stride + 1];
+    }
+    v = scan_up(v);
+    h = __builtin_fmaf(lane_of(v.P, 63), h, lane_of(v.H, 63));
+  }
+  return h;
 }
 
 // Sum over the wave in lane 63 (fixed order).

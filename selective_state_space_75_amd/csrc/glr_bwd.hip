@@ -7,163 +7,178 @@
 //     dx = q n g,  di = dx x (1 - g),  dz = dy h sigma (1 + z (1 - sigma)), sigma = sigmoid(z)
 //     dl = q (a h_prev - g x a^2 / n),  dr = dl A s (1 - s),  dA = sum dl s   (decay rule, l = A s)
 //     dr = q (g x - h_prev) s a                                                (blend)
-// A workgroup has a row of up to 8192 tokens (16 waves of 512) on the chip: its five inputs stay
-// in registers, both scans run at once and the gradients are written from there.  Longer rows
-// are cut into segments; a first launch leaves every segment's (P, H, C), and each workgroup
-// takes its entering states through those of the others.
-// dA and the biases' gradients: a sum per segment, then one small launch over batch rows and segments.
+// A workgroup has a tile of up to 8192 tokens (16 waves of 512) on the chip: its five inputs stay in
+// registers, both scans run at once and the gradients are written from there.  A longer row is cut into
+// tiles, whose entering states come from the (P, H) of the tiles before them, left by a first launch that reads
+// x, r and i (mamba::launch_glr_summary).  Where there are rows enough, a workgroup takes all tiles of its row
+// from the last to the first and c stays with it; few rows have a workgroup per tile, and the first launch
+// (kSummary below, all five inputs) leaves C too.
+// dA and the biases' gradients: a sum per workgroup, then one small launch over batch rows and workgroups of a row.
 #include "glr.hpp"
 
 namespace mamba {
 namespace {
 
-// kSummary: only the (P, H, C) of each segment.
-template <typename T, typename Gr, bool kBlend, bool kSummary, int kThreads>
+// kSummary: only the (P, H, C) of each tile.  kLoop: more than one tile a workgroup.
+template <typename T, typename Gr, bool kBlend, bool kSummary, bool kLoop, int kThreads>
 __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
-  __shared__ float totals[3][16];
+  __shared__ float totals[2][3][16];
   __shared__ float sums[3][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int64_t rows = p.B * p.D;
-  const int64_t seg = blockIdx.x / rows, row = blockIdx.x - seg * rows;
+  const int64_t own = blockIdx.x / rows, row = blockIdx.x - own * rows;     // of the row's workgroups
   const int64_t b = row / p.D, d = row - b * p.D;
-  const int64_t t0 = seg * p.seg_len;
-  const int64_t t1 = p.L - t0 < p.seg_len ? p.L : t0 + p.seg_len;
   const int64_t len = glr_length(p, b);
-  const int64_t t = t0 + (int64_t)threadIdx.x * kGlrLane;
-  const int live = clamp8((len < t1 ? len : t1) - t);
-  const Raw8<T> xr = load_raw8(static_cast<const T*>(p.x) + b * p.x_stride + d * p.L + t, live);
-  const Raw8<T> rr = load_raw8(static_cast<const T*>(p.r) + b * p.r_stride + d * p.L + t, live);
-  const Raw8<Gr> yr = load_raw8(static_cast<const Gr*>(p.dy) + row * p.L + t, live);
-  Raw8<T> ir, zr;
-  if (p.i) ir = load_raw8(static_cast<const T*>(p.i) + b * p.i_stride + d * p.L + t, live);
-  if (p.z) zr = load_raw8(static_cast<const T*>(p.z) + b * p.z_stride + d * p.L + t, live);
+  const T* x = static_cast<const T*>(p.x) + b * p.x_stride + d * p.L;
+  const T* r = static_cast<const T*>(p.r) + b * p.r_stride + d * p.L;
+  const T* ig = p.i ? static_cast<const T*>(p.i) + b * p.i_stride + d * p.L : nullptr;
+  const T* zg = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + d * p.L : nullptr;
+  const Gr* dy = static_cast<const Gr*>(p.dy) + row * p.L;
   const float A = kBlend ? 0.0f : p.A[d], A2 = A * kLog2e;
   const float rb = p.r_bias ? -p.r_bias[d] * kLog2e : 0.0f;
   const float ib = p.i_bias ? -p.i_bias[d] * kLog2e : 0.0f;
+  const int width = p.groups > 1 ? 3 : 2;                                   // numbers of a tile's summary
+  const float* sum = p.S > 1 ? p.sum + row * p.S * width : nullptr;
+  const int64_t lo = own * p.group, hi = p.S < lo + p.group ? p.S : lo + p.group;
 
-  float a[8], n[8], s[8], ra[8], g[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const GlrGate k = glr_gate<kBlend>(glr_r(rr, j, live), rb, A2);
-    a[j] = k.a; n[j] = k.n; s[j] = k.s; ra[j] = k.ra;
+  float c_in = 0.0f;                           // what the tiles behind hand to this one
+  if constexpr (!kSummary) {
+    c_in = p.dfinal ? p.dfinal[row] : 0.0f;
+    for (int64_t base = p.S - 1; base >= hi; base -= 64) {
+      Affine v;
+      if (base - lane >= hi) v = Affine{sum[(base - lane) * 3], sum[(base - lane) * 3 + 2]};
+      v = scan_up(v);
+      c_in = __builtin_fmaf(lane_of(v.P, 63), c_in, lane_of(v.H, 63));
+    }
   }
-  if (p.i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = hw_rcp(1.0f + hw_exp2(__builtin_fmaf(get8(ir, j), -kLog2e, ib)));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = 1.0f;
-  }
-  float e[8], sz[8];
-  if (p.z) {
+  float sA = 0.0f, sr = 0.0f, si = 0.0f;
+  int turn = 0;
+  for (int64_t seg = hi - 1; seg >= (kLoop ? lo : hi - 1); --seg, turn ^= 1) {
+    const int64_t t0 = seg * p.seg_len;
+    const int64_t t1 = p.L - t0 < p.seg_len ? p.L : t0 + p.seg_len;
+    const int64_t t = t0 + (int64_t)threadIdx.x * kGlrLane;
+    const int live = clamp8((len < t1 ? len : t1) - t);
+    Raw8<T> xr = load_raw8(x + t, live), rr = load_raw8(r + t, live);
+    Raw8<Gr> yr = load_raw8(dy + t, live);
+    Raw8<T> ir, zr;
+    if (ig) ir = load_raw8(ig + t, live);
+    if (zg) zr = load_raw8(zg + t, live);
+
+    float a[8], n[8], s[8], ra[8], g[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      sz[j] = sigmoid(get8(zr, j));
-      e[j] = get8(yr, j) * get8(zr, j) * sz[j];
+      const GlrGate k = glr_gate<kBlend>(glr_r(rr, j, live), rb, A2);
+      a[j] = k.a; n[j] = k.n; s[j] = k.s; ra[j] = k.ra;
     }
-  } else {
+    if (ig) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = get8(yr, j);
-  }
-  Affine f, k;                                 // forwards and backwards over the lane's tokens
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    f.P *= a[j];
-    f.H = __builtin_fmaf(a[j], f.H, n[j] * g[j] * get8(xr, j));
-  }
-#pragma unroll
-  for (int j = 7; j >= 0; --j) k.H = a[j] * (k.H + e[j]);
-  k.P = f.P;
-  f = scan_up(f);
-  k = scan_down(k, lane);
-  if (lane == 63) {
-    totals[0][wave] = f.P;
-    totals[1][wave] = f.H;
-  }
-  if (lane == 0) totals[2][wave] = k.H;
-  __syncthreads();
-  Affine front, behind, all, back;             // waves in front of this one, behind it, and all of them
-  for (int w = 0; w < waves; ++w) {
-    if (w == wave) front = all;
-    all = glr_through(all, Affine{totals[0][w], totals[1][w]});
-  }
-  for (int w = waves - 1; w >= 0; --w) {
-    if (w == wave) behind = back;
-    back = glr_through(back, Affine{totals[0][w], totals[2][w]});
-  }
-  if constexpr (kSummary) {
-    if (threadIdx.x == 0) {
-      float* o = p.sum + (row * p.S + seg) * 3;
-      o[0] = all.P; o[1] = all.H; o[2] = back.H;
-    }
-    return;
-  }
-  float h = p.init ? p.init[row] : 0.0f, c = p.dfinal ? p.dfinal[row] : 0.0f;
-  if (p.S > 1) {
-    const float* sum = p.sum + row * p.S * 3;
-    for (int64_t base = 0; base < seg; base += 64) {
-      Affine v;
-      if (base + lane < seg) v = Affine{sum[(base + lane) * 3], sum[(base + lane) * 3 + 1]};
-      v = scan_up(v);
-      h = __builtin_fmaf(lane_of(v.P, 63), h, lane_of(v.H, 63));
-    }
-    for (int64_t base = p.S - 1; base > seg; base -= 64) {
-      Affine v;
-      if (base - lane > seg) v = Affine{sum[(base - lane) * 3], sum[(base - lane) * 3 + 2]};
-      v = scan_up(v);
-      c = __builtin_fmaf(lane_of(v.P, 63), c, lane_of(v.H, 63));
-    }
-  }
-  if (p.dinit && seg == 0 && threadIdx.x == 0) p.dinit[row] = __builtin_fmaf(back.P, c, back.H);
-  h = __builtin_fmaf(front.P, h, front.H);
-  c = __builtin_fmaf(behind.P, c, behind.H);
-  const Affine fe = shift_up(f), ke = shift_down(k);
-  h = __builtin_fmaf(fe.P, h, fe.H);
-  c = __builtin_fmaf(ke.P, c, ke.H);
-
-  const int there = clamp8(t1 - t);
-  const int64_t at = row * p.L + t;
-  float hp[8];                                 // state in front of each token
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    hp[j] = h;
-    h = __builtin_fmaf(a[j], h, n[j] * g[j] * get8(xr, j));
-  }
-  if (p.z) {
-    float o[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float hj = j < 7 ? hp[j < 7 ? j + 1 : 7] : h;
-      o[j] = get8(yr, j) * hj * sz[j] * __builtin_fmaf(get8(zr, j), 1.0f - sz[j], 1.0f);
-    }
-    store8(static_cast<Gr*>(p.dz) + at, o, live, there);
-  }
-  float dx[8], dr[8], sA = 0.0f, sr = 0.0f, si = 0.0f;
-#pragma unroll
-  for (int j = 7; j >= 0; --j) {
-    const float q = e[j] + c;
-    c = a[j] * q;
-    dx[j] = q * n[j] * g[j];
-    const float gx = g[j] * get8(xr, j);
-    if constexpr (kBlend) {
-      dr[j] = q * (gx - hp[j]) * s[j] * a[j];
+      for (int j = 0; j < 8; ++j) g[j] = hw_rcp(1.0f + hw_exp2(__builtin_fmaf(get8(ir, j), -kLog2e, ib)));
     } else {
-      const float ds = q * __builtin_fmaf(a[j], hp[j], -gx * ra[j]) * s[j];
-      sA += ds;
-      dr[j] = ds * A * (1.0f - s[j]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = 1.0f;
     }
-    sr += dr[j];
-  }
-  store8(static_cast<Gr*>(p.dx) + at, dx, live, there);
-  store8(static_cast<Gr*>(p.dr) + at, dr, live, there);
-  if (p.i) {
+    float e[8], sz[8];
+    if (zg) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sz[j] = sigmoid(get8(zr, j));
+        e[j] = get8(yr, j) * get8(zr, j) * sz[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = get8(yr, j);
+    }
+    Affine f, k;                               // forwards and backwards over the lane's tokens
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      dx[j] *= get8(xr, j) * (1.0f - g[j]);
-      si += dx[j];
+      f.P *= a[j];
+      f.H = __builtin_fmaf(a[j], f.H, n[j] * g[j] * get8(xr, j));
     }
-    store8(static_cast<Gr*>(p.di) + at, dx, live, there);
+#pragma unroll
+    for (int j = 7; j >= 0; --j) k.H = a[j] * (k.H + e[j]);
+    k.P = f.P;
+    f = scan_up(f);
+    k = scan_down(k, lane);
+    if (lane == 63) {
+      totals[turn][0][wave] = f.P;
+      totals[turn][1][wave] = f.H;
+    }
+    if (lane == 0) totals[turn][2][wave] = k.H;
+    __syncthreads();                           // the other half of `totals` may still be read: the next tile writes that one
+    Affine front, behind, all, back;           // waves in front of this one, behind it, and all of them
+    for (int w = 0; w < waves; ++w) {
+      if (w == wave) front = all;
+      all = glr_through(all, Affine{totals[turn][0][w], totals[turn][1][w]});
+    }
+    for (int w = waves - 1; w >= 0; --w) {
+      if (w == wave) behind = back;
+      back = glr_through(back, Affine{totals[turn][0][w], totals[turn][2][w]});
+    }
+    if constexpr (kSummary) {
+      if (threadIdx.x == 0) {
+        float* o = p.sum + (row * p.S + seg) * 3;
+        o[0] = all.P; o[1] = all.H; o[2] = back.H;
+      }
+      continue;
+    }
+    keep(xr);
+    keep(yr);
+    if (zg) keep(zr);
+    float h = p.init ? p.init[row] : 0.0f, c = c_in;
+    if (seg) h = glr_enter(sum, width, seg, h, lane);
+    c_in = __builtin_fmaf(back.P, c_in, back.H);
+    h = __builtin_fmaf(front.P, h, front.H);
+    c = __builtin_fmaf(behind.P, c, behind.H);
+    const Affine fe = shift_up(f), ke = shift_down(k);
+    h = __builtin_fmaf(fe.P, h, fe.H);
+    c = __builtin_fmaf(ke.P, c, ke.H);
+
+    const int there = clamp8(t1 - t);
+    const int64_t at = row * p.L + t;
+    float hp[8];                               // state in front of each token
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      hp[j] = h;
+      h = __builtin_fmaf(a[j], h, n[j] * g[j] * get8(xr, j));
+    }
+    if (zg) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float hj = j < 7 ? hp[j < 7 ? j + 1 : 7] : h;
+        o[j] = get8(yr, j) * hj * sz[j] * __builtin_fmaf(get8(zr, j), 1.0f - sz[j], 1.0f);
+      }
+      store8(static_cast<Gr*>(p.dz) + at, o, live, there);
+    }
+    float dx[8], dr[8];
+#pragma unroll
+    for (int j = 7; j >= 0; --j) {
+      const float q = e[j] + c;
+      c = a[j] * q;
+      dx[j] = q * n[j] * g[j];
+      const float gx = g[j] * get8(xr, j);
+      if constexpr (kBlend) {
+        dr[j] = q * (gx - hp[j]) * s[j] * a[j];
+      } else {
+        const float ds = q * __builtin_fmaf(a[j], hp[j], -gx * ra[j]) * s[j];
+        sA += ds;
+        dr[j] = ds * A * (1.0f - s[j]);
+      }
+      sr += dr[j];
+    }
+    store8(static_cast<Gr*>(p.dx) + at, dx, live, there);
+    store8(static_cast<Gr*>(p.dr) + at, dr, live, there);
+    if (ig) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dx[j] *= get8(xr, j) * (1.0f - g[j]);
+        si += dx[j];
+      }
+      store8(static_cast<Gr*>(p.di) + at, dx, live, there);
+    }
   }
+  if constexpr (kSummary) return;
+  if (p.dinit && lo == 0 && threadIdx.x == 0) p.dinit[row] = c_in;
   sA = wave_sum63(sA);
   sr = wave_sum63(sr);
   si = wave_sum63(si);
@@ -176,16 +191,16 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
   if (threadIdx.x < 3) {
     float o = 0.0f;
     for (int w = 0; w < waves; ++w) o += sums[threadIdx.x][w];
-    if (rows * p.S == p.D) {                     // nothing to add up
+    if (p.B * p.groups == 1) {                 // nothing to add up
       float* dst = threadIdx.x == 0 ? p.dA : threadIdx.x == 1 ? p.dr_bias : p.di_bias;
       if (dst) dst[d] = o;
     } else {
-      p.part[((b * p.S + seg) * 3 + threadIdx.x) * p.D + d] = o;
+      p.part[((b * p.groups + own) * 3 + threadIdx.x) * p.D + d] = o;
     }
   }
 }
 
-// Sums over batch rows and segments: 16 channels x 16 shares of them per workgroup.
+// Sums over batch rows and workgroups of a row: 16 channels x 16 shares of them per workgroup.
 __global__ __launch_bounds__(256) void glr_sum_kernel(GlrParams p) {
   __shared__ float share[16][16];
   const int64_t blocks = (p.D + 15) / 16;
@@ -193,7 +208,7 @@ __global__ __launch_bounds__(256) void glr_sum_kernel(GlrParams p) {
   const int64_t d = (blockIdx.x - k * blocks) * 16 + (threadIdx.x & 15);
   const int y = threadIdx.x >> 4;
   float o = 0.0f;
-  if (d < p.D) o = strided_sum(p.part + k * p.D + d, 3 * p.D, y, p.B * p.S);
+  if (d < p.D) o = strided_sum(p.part + k * p.D + d, 3 * p.D, y, p.B * p.groups);
   share[y][threadIdx.x & 15] = o;
   __syncthreads();
   if (y || d >= p.D) return;
@@ -204,22 +219,33 @@ __global__ __launch_bounds__(256) void glr_sum_kernel(GlrParams p) {
 
 template <typename T, typename Gr, bool kBlend, int kThreads>
 hipError_t bwd_n(const GlrParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.B * p.D * p.S)), block(64u * p.waves);
-  if (p.S > 1) {
-    hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, true, kThreads>), grid, block, 0, s, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  const unsigned rows = (unsigned)(p.B * p.D);
+  const dim3 block(64u * p.waves), grid(rows * (unsigned)p.groups);
+  hipError_t e = hipSuccess;
+  if (p.groups > 1) {
+    GlrParams one = p;
+    one.group = 1;
+    hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, true, false, kThreads>), dim3(rows * (unsigned)p.S), block, 0, s, one);
+    e = hipGetLastError();
+  } else if (p.S > 1) {
+    e = launch_glr_summary(p, sizeof(T) == 2 ? Dt::BF16 : Dt::F32, s);
   }
-  hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, kThreads>), grid, block, 0, s, p);
-  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (p.B * p.S == 1) return hipSuccess;
+  if constexpr (kThreads == 512) {             // more waves are only taken for one tile
+    if (p.group > 1) hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, true, 512>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, false, 512>), grid, block, 0, s, p);
+  } else {
+    hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, false, kThreads>), grid, block, 0, s, p);
+  }
+  e = hipGetLastError();
+  if (e != hipSuccess || p.B * p.groups == 1) return e;
   hipLaunchKernelGGL(glr_sum_kernel, dim3((unsigned)(3 * ((p.D + 15) / 16))), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T, typename Gr>
 hipError_t bwd_t(const GlrParams& p, hipStream_t s) {
+  if (p.waves <= 8) return p.blend ? bwd_n<T, Gr, true, 512>(p, s) : bwd_n<T, Gr, false, 512>(p, s);
   return p.blend ? bwd_n<T, Gr, true, 1024>(p, s) : bwd_n<T, Gr, false, 1024>(p, s);
 }
 

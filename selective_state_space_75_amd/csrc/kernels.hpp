@@ -236,14 +236,15 @@ struct GlrParams {
   int64_t S, seg_len;                           // segments of L, a multiple of 8 tokens each
   int waves;                                    // waves of a workgroup: 512 tokens of a row each at a time
   int blend;
-  float* sum;                                   // S > 1: (rows, S, 2) P and H of each segment (backward: (rows, S, 3), and C)
+  float* sum;                                   // S > 1: (rows, S, 2) P and H of each segment (backward, groups > 1: (rows, S, 3), and C)
   // backward pass
   const void* dy;                               // (B, D, L) grad dtype
   const float* dfinal;                          // (B, D) or null
   void *dx, *dr, *di, *dz;                      // grad dtype, dense
   float *dA, *dr_bias, *di_bias;                // (D)
   float* dinit;                                 // (B, D) or null
-  float* part;                                  // (B * S, 3, D): sums over a segment
+  int64_t group, groups;                        // segments of a workgroup, and workgroups of a row
+  float* part;                                  // (B * groups, 3, D): sums over a workgroup's segments
 };
 constexpr int kGlrLane = 8;                     // consecutive tokens of a lane
 constexpr int kGlrWave = 64 * kGlrLane;         // and of a wave
@@ -339,6 +340,7 @@ hipError_t launch_gdr_prep(const GdrChunkParams& p, Dt in, Dt grad, bool bwd, hi
 hipError_t launch_gdr_states(const GdrChunkParams& p, Dt in, hipStream_t s);
 hipError_t launch_gdr_bwd(const GdrChunkParams& p, Dt in, Dt grad, hipStream_t s);
 hipError_t launch_glr_fwd(const GlrParams& p, Dt in, Dt out, hipStream_t s);
+hipError_t launch_glr_summary(const GlrParams& p, Dt in, hipStream_t s);
 hipError_t launch_glr_update(const GlrParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrParams& p, Dt in, Dt grad, hipStream_t s);
 hipError_t launch_norm_fwd(const NormParams& p, const NormPlan& q, Dt in, Dt out, hipStream_t s);

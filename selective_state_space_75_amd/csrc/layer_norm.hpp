@@ -125,14 +125,6 @@ __device__ __forceinline__ T* lane_at(T* base, uint32_t v) {
   return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(base) + (uint32_t)(v * sizeof(T)));
 }
 
-// The numbers as they lie in memory are what stays in registers between two sweeps: without this the
-// compiler keeps the widened and centred ones of the first for the second, twice the registers and more.
-template <typename T>
-__device__ __forceinline__ void keep(Raw8<T>& o) {
-#pragma unroll
-  for (int k = 0; k < (int)sizeof(T) / 2; ++k) asm("" : "+v"(o.w[k]));
-}
-
 // Statistics of one token per lane over the group's channels, fewer than 8 tokens, a workgroup of 256: 32
 // channel lanes of 8 token lanes, in two sweeps.  lds: 5 * 8 * 4 floats.
 template <typename T>
