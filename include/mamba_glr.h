@@ -33,8 +33,8 @@
  *              its outputs and gradients there are zero, and its final state is
  *              the one after lengths[b] tokens.
  *
- * Sizes: B, D, L >= 1; B*D*L < 2^46, strides < 2^46 / B; B*D < 2^22, so that every launch has
- * fewer than 2^32 threads, and for mamba_glr_bwd B*D*ceil(L/8192) < 2^22.  in_dtype and the
+ * Sizes: B, D, L >= 1; B*D*L < 2^46, strides < 2^46 / B; and no launch of 2^32 threads or more:
+ * B*D*(ceil(L/512) + ceil(L/2048)) < 2^26 is enough (mamba_glr_update: B*ceil(D/256) < 2^24).  in_dtype and the
  * output dtypes may each be MAMBA_F32 or MAMBA_BF16.  Alignment: every array to its element
  * size; workspaces 256 bytes.
  * A NaN or an infinity among the inputs of a token leaves the outputs of the tokens before it
@@ -43,7 +43,7 @@
  * that holds it, and that channel's sums.
  * State, gates and sums are fp32.  The results are deterministic (sums in a fixed order, no
  * atomics): the same call gives the same bits.  B, like every other size, takes part in
- * mamba_glr_fwd's choice of how a row is cut over waves, and those agree to fp32 rounding only.
+ * the choice of how a row is cut over waves and segments, and those agree to fp32 rounding only.
  */
 #ifndef MAMBA_GLR_H_
 #define MAMBA_GLR_H_
@@ -117,9 +117,10 @@ int mamba_glr_bwd(const void* x, const void* r, const void* i, const void* z, co
  * Test and diagnostic knobs, process-wide like mamba_set_test_knobs: how a call is
  * carried out, never what it computes (to fp32 rounding).  A workspace size asked
  * for before a change does not fit a call after it.
- *   waves    : > 0: waves per row and pass, 1 .. 16 (a wave takes 512 tokens at a time); 0: the planner decides.
+ *   waves    : > 0: at most this many waves of a workgroup on a row, 1 .. 16 (a wave takes 512 tokens at a
+ *              time); 0: the planner decides.
  *   segments : > 0: L is cut into this many segments (at most one per 8 tokens; in mamba_glr_bwd
- *              at least ceil(L / 8192)); 0: the planner decides.
+ *              at least as many as its waves need); 0: the planner decides.
  * Returns MAMBA_ERR_SHAPE for other values.
  */
 int mamba_glr_set_test_knobs(int waves, int64_t segments);

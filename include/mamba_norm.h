@@ -14,12 +14,15 @@
  *   x_stride, z_stride : elements from one batch row to the next (at least D*L).
  *   weight : (D) fp32 or NULL (ones).  bias : (D) fp32 or NULL (zeros).
  *
- * Sizes: B, D, L >= 1; D a multiple of groups; B*D*L < 2^46, strides < 2^46 / B; B*groups*ceil(L/8) < 2^22.
- * in_dtype and the output dtypes may each be MAMBA_F32 or MAMBA_BF16.  Alignment: every array to
+ * Sizes: B, D, L >= 1; D a multiple of groups; B*D*L < 2^46, strides < 2^46 / B; and no launch of 2^32
+ * threads or more: D < 2^27, B*groups*ceil(L/32) < 2^22 and B*D*ceil(L/64) < 2^29 are enough.
+ * in_dtype and the output dtypes may each be MAMBA_F32 or MAMBA_BF16.  eps >= 0.  Alignment: every array to
  * its element size; workspaces 256 bytes.  Statistics and sums are fp32; the variance is taken
- * around the mean, not as a difference of squares.  A NaN or an infinity stays in its own token
- * and group (dweight and dbias aside).  Deterministic: sums in a fixed order, no atomics; a token's
- * bits do not depend on B.
+ * around the mean, or around one of the numbers for a few of them, never as a difference of large squares.  A NaN
+ * or an infinity stays in its own token and group (dweight and dbias aside).  Deterministic: sums in a
+ * fixed order, no atomics: the same call gives the same bits.  B takes part in how channel-major groups of more
+ * than 256 channels are cut, which agrees to fp32 rounding; token-major rows and smaller groups have the
+ * same bits in a batch of any size (dweight and dbias aside).
  */
 #ifndef MAMBA_NORM_H_
 #define MAMBA_NORM_H_

@@ -95,7 +95,11 @@ CASES = [(1, 1, 1, "f32", "f32", False, True, True, True, None, False, 0, 0),
          (2, 2, 8192, "bf16", "f32", False, False, True, True, None, False, 0, 0),
          (1, 3, 8193, "bf16", "f32", False, True, True, True, [8192], True, 0, 0),
          (1, 2, 17001, "f32", "f32", False, True, True, True, None, False, 0, 0),
-         (2, 1, 40000, "bf16", "f32", False, True, True, False, [40000, 12345], False, 0, 0)]
+         (2, 1, 40000, "bf16", "f32", False, True, True, False, [40000, 12345], False, 0, 0),
+         (2, 300, 1100, "bf16", "f32", False, True, True, True, [1100, 801], True, 0, 3),     # rows enough to walk a row's tiles
+         (1, 600, 700, "f32", "f32", True, True, False, True, None, False, 1, 0),
+         (1, 515, 9000, "bf16", "f32", False, True, True, True, [8500], False, 0, 0),
+         (8, 520, 600, "bf16", "f32", False, False, True, False, None, False, 0, 0)]
 
 
 @pytest.mark.parametrize("B,D,L,dtype,out,blend,with_i,with_z,init,lengths,ranges,waves,segments", CASES)
@@ -151,6 +155,22 @@ def test_backward(B, D, L, dtype, out, blend, with_i, with_z, init, lengths, ran
         for n in ("dx", "dr", "di", "dz"):
             for b in range(B):
                 assert g[n] is None or not from_dev(g[n])[b, :, max(0, lengths[b]):].any(), n
+
+
+@pytest.mark.parametrize("with_init,with_final", [(True, False), (False, True)])
+@pytest.mark.parametrize("waves,segments", [(0, 0), (1, 3)])
+def test_one_of_the_two_states(with_init, with_final, waves, segments, dev):
+    """A given state without a gradient of the last one, and the other way round."""
+    import selective_state_space_75_amd as m
+    x = make(2, 7, 900, "f32", 14, False, True, True, True)
+    x["initial_state"] = x["initial_state"] if with_init else None
+    x["dfinal_state"] = x["dfinal_state"] if with_final else None
+    t = put(x, dev, NAMES)
+    with m.glr_test_knobs(waves=waves, segments=segments):
+        g = gradients(t, t["dy"], False, None)
+    ref = O.glr_bwd(*oracle_args(x), f64(x["dy"]), initial_state=x["initial_state"], dfinal_state=x["dfinal_state"])
+    assert (g["dinitial_state"] is None) == (not with_init)
+    check_gradients(g, ref, x)
 
 
 def test_gradients_are_differences_of_the_forward(dev):

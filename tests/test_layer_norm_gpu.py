@@ -33,6 +33,17 @@ CASES = [((1, 1, 1), 1, "f32", "f32", False, False, True, False),
          ((1, 10007, 10), 1, "bf16", "f32", False, False, True, False),
          ((1, 9000, 21), 1, "f32", "f32", True, True, True, False),
          ((70, 24, 5), 2, "bf16", "f32", False, False, True, False),
+         ((3, 20, 8), 1, "bf16", "f32", True, False, True, False),
+         ((1, 3000, 8), 1, "f32", "f32", True, True, True, False),
+         ((2, 200, 70), 1, "bf16", "f32", True, False, True, True),
+         ((2, 400, 50), 2, "f32", "bf16", True, False, True, False),
+         ((1, 400, 50), 1, "bf16", "bf16", True, True, True, False),
+         ((1, 512, 33), 1, "f32", "f32", False, False, True, False),
+         ((1, 1500, 70), 1, "bf16", "f32", True, False, False, True),
+         ((1, 600, 300), 1, "bf16", "f32", True, False, True, True),
+         ((2, 2600, 515), 1, "f32", "f32", False, False, True, False),
+         ((1, 5200, 1030), 2, "bf16", "f32", True, True, True, False),
+         ((9, 24, 2), 1, "f32", "f32", True, True, True, False),
          ((1, 1), 1, "f32", "f32", False, False, True, False),
          ((5, 7), 7, "f32", "f32", True, True, True, False),
          ((3, 8), 1, "bf16", "f32", False, False, True, False),
@@ -155,17 +166,52 @@ def test_alignment_and_neighbours(shape, groups, dtype, dev):
 def test_a_tokens_bits_do_not_depend_on_the_batch(dev):
     import torch
     import selective_state_space_75_amd as m
-    for shape in ((6, 700, 40), (900, 700)):
+    for shape, groups in (((6, 700, 40), 4), ((6, 250, 300), 1), ((900, 700), 1), ((40, 96), 3)):
         x, t = tensors(shape, "bf16", 80, True, True, False, dev)
-        y = m.layer_norm_fwd(t["x"], t["weight"], t["bias"], t["z"])
-        g = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"])
+        kw = dict(groups=groups)
+        y = m.layer_norm_fwd(t["x"], t["weight"], t["bias"], t["z"], **kw)
+        g = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"], **kw)
         one = slice(3, 4)
         z1 = t["z"][one]
-        assert torch.equal(m.layer_norm_fwd(t["x"][one], t["weight"], t["bias"], z1), y[one])
-        g1 = m.layer_norm_bwd(t["x"][one], t["weight"], t["bias"], z1, t["dy"][one])
+        assert torch.equal(m.layer_norm_fwd(t["x"][one], t["weight"], t["bias"], z1, **kw), y[one])
+        g1 = m.layer_norm_bwd(t["x"][one], t["weight"], t["bias"], z1, t["dy"][one], **kw)
         assert torch.equal(g1["dx"], g["dx"][one]) and torch.equal(g1["dz"], g["dz"][one])
-        again = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"])
-        assert all(torch.equal(again[n], g[n]) for n in g)
+
+
+@pytest.mark.parametrize("shape,groups", [((3, 700, 333), 1), ((2, 240, 700), 3), ((700, 900), 1), ((3000, 96), 3),
+                                          ((5, 60, 6), 2)])
+def test_the_same_call_gives_the_same_bits(shape, groups, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    x, t = tensors(shape, "bf16", 81, True, True, False, dev)
+    call = lambda: m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"], groups=groups)  # noqa: E731
+    a = call()
+    for _ in range(3):
+        b = call()
+        assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_gradients_are_differences_of_the_forward(dev):
+    """Along random directions over a step of 2^-6 both ways: sums of fp32 outputs off by 1e-6 of their
+    numbers with either sign, over 2^-5, leave 3e-5 sqrt(n), three times that at most; the third derivatives add the
+    step squared over six, 4e-5, times themselves, held to 120 times the gradient's size."""
+    import torch
+    import selective_state_space_75_amd as m
+    for shape, groups, rms in (((2, 24, 40), 2, False), ((1, 700, 20), 1, True), ((6, 640), 1, False)):
+        x, t = tensors(shape, "f32", 82, True, True, False, dev)
+        kw = dict(groups=groups, rms=rms)
+        g = m.layer_norm_bwd(t["x"], t["weight"], t["bias"], t["z"], t["dy"], **kw)
+        rng = np.random.default_rng(1)
+        for n, gn in (("x", "dx"), ("z", "dz"), ("weight", "dweight"), ("bias", "dbias")):
+            v = torch.from_numpy(rng.standard_normal(tuple(t[n].shape)).astype(np.float32)).to(dev)
+            vals = []
+            for s in (2.0 ** -6, -2.0 ** -6):
+                q = {**t, n: t[n] + s * v}
+                vals.append(float((m.layer_norm_fwd(q["x"], q["weight"], q["bias"], q["z"], **kw).double() * t["dy"].double()).sum()))
+            num, want = (vals[0] - vals[1]) * 32, float((g[gn].double() * v.double()).sum())
+            size, count = float((g[gn].double() * v.double()).norm()), t["x"].numel() ** 0.5
+            log("  %s: %.6e against %.6e" % (n, num, want))
+            assert abs(num - want) <= 4.8e-3 * size + 9e-5 * count, n
 
 
 def test_zero_variance_and_eps(dev):
