@@ -335,7 +335,7 @@ int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, cons
   if (!dy || !dx || (z && !dz) || !dweight || !dbias) return MAMBA_ERR_NULL;
   if (!all_aligned({dy, dx, dz}, width(grad_dtype)) || !all_aligned({dweight, dbias}, 4)) return MAMBA_ERR_ALIGN;
   const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), (int)width(grad_dtype));
-  if (!norm_fits(q, B, D, L, groups, q.parts * groups) || !mamba::launch_fits(ceil_div(2 * D, 16), 256))
+  if (!norm_fits(q, B, D, L, groups, q.parts * groups) || !mamba::launch_fits(ceil_div(2 * D, 64), 1024))
     return MAMBA_ERR_SHAPE;
   norm_set(p, q);
   const size_t need = norm_bwd_bytes(B, D, L, groups);

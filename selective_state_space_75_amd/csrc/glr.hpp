@@ -197,16 +197,16 @@ __device__ __forceinline__ float wave_sum63(float x) {
   return x;
 }
 
-// Sum of a[i * stride] over i = y, y + 16, ... below n, four loads under way at a time.
+// Sum of a[i * stride] over i = y, y + 16, ... below n, eight loads under way at a time.
 __device__ __forceinline__ float strided_sum(const float* a, int64_t stride, int64_t y, int64_t n) {
   float o = 0.0f;
   int64_t i = y;
-  for (; i + 48 < n; i += 64) {
-    const float v0 = a[i * stride], v1 = a[(i + 16) * stride], v2 = a[(i + 32) * stride], v3 = a[(i + 48) * stride];
-    o += v0;
-    o += v1;
-    o += v2;
-    o += v3;
+  for (; i + 112 < n; i += 128) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = a[(i + 16 * k) * stride];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o += v[k];
   }
   for (; i < n; i += 16) o += a[i * stride];
   return o;

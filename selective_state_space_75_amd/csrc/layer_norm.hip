@@ -232,6 +232,7 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     q.lanes = 1;                                       // threads of a token
     while (q.kind == kNormRowTeam && q.lanes * 8 < Dg) q.lanes *= 2;
     if (q.kind == kNormRowBlock) q.threads = q.lanes = (int)((Dg + 511) / 512) * 64;
+    if (bwd && q.kind != kNormRowLong) q.threads = 1024 / q.lanes * q.lanes;     // as many teams as that holds
   } else if (L < 8) {
     q.kind = kNormColLong;
     q.lanes = 8;
@@ -255,7 +256,7 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
   if (q.kind == kNormColTwo) {
     // Statistics: 4 to 40 channels a thread, in as few pieces as give every CU a workgroup.
     const int64_t lanes = kNormStatThreads / kNormStatLanes, blocks = B * G * q.tiles;
-    const int64_t least = ceil_div(Dg, 40 * lanes), most = Dg / (4 * lanes) + 1;
+    const int64_t least = ceil_div(Dg, 40 * lanes), most = Dg / (4 * lanes) < 16 ? Dg / (4 * lanes) + 1 : 16;
     q.chunks = blocks < 256 ? 256 / blocks : 1;
     if (q.chunks > most) q.chunks = most;
     if (q.chunks < least) q.chunks = least;
@@ -266,9 +267,12 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     q.parts = B * ceil_div(L, 8 * q.apply_lanes);
     return q;
   }
-  // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.
-  int64_t most = (q.threads > 256 ? 512 : 1024) / G;
-  const int64_t work = q.kind == kNormRowTeam ? ceil_div(B, 256 / q.lanes) : B * q.tiles;
+  // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.  Token-major
+  // that is one a CU, or two where two of them fit (a group's one team of up to 640 threads: 8192 tokens of 5120
+  // channels, bf16, 68 us, with one 93; of 512 channels, where one workgroup holds 1024 threads, 18 us with two and 14 with one).
+  const bool rows = q.kind == kNormRowTeam || q.kind == kNormRowBlock;
+  int64_t most = (rows ? 256 * (1280 / q.threads) : q.threads > 256 ? 512 : 1024) / G;
+  const int64_t work = rows ? ceil_div(B, q.threads / q.lanes) : B * q.tiles;
   if (most < 1) most = 1;
   if (most > work) most = work;
   q.parts = ceil_div(work, ceil_div(work, most));

@@ -3,10 +3,11 @@
 // With xh = (x - mean) k, m = xh w + b, y = m silu(z), dm = dy silu(z) and g = dm w, per token:
 //     dx = k (g - mean(g) - xh mean(g xh))   (rms: without mean(g)),   dz = dy m sigma (1 + z (1 - sigma))
 // and over tokens dw = sum dm xh, db = sum dm.  The sums of g, g (x - mean) and (x - mean)^2 are taken in one
-// sweep once the mean is known.  The tile of x and dy stays in registers (z is read again from the caches);
-// the layouts are those of layer_norm.hip.  A workgroup takes every parts-th tile and keeps its channels' sums
-// of dw and db on the chip, so that one partial sum per workgroup and channel is written, and one
-// small launch adds those up in a fixed order.
+// sweep once the mean is known.  What HBM has to carry is one read of x, dy (z) and one write of dx (dz); the
+// tile of x and dy stays in registers between the sweeps, z with it where a thread has at most four channels,
+// and is read again from the caches otherwise.  The layouts are those of layer_norm.hip.  A workgroup takes every
+// parts-th tile and keeps its channels' sums of dw and db on the chip, so that one partial sum per workgroup and
+// channel is written; one small launch (norm_sum_kernel, 4 us) adds those up in a fixed order.
 #include "layer_norm_two.hpp"
 
 namespace mamba {
@@ -225,109 +226,167 @@ __global__ __launch_bounds__(256) void norm_col_long_bwd_kernel(NormParams p) {
   }
 }
 
-// Token-major: a workgroup takes a group of channels and every parts-th share of the tokens, one a team of lanes
-// (or one at a time) at once; 8 channels a thread, the last thread the group's last 8 whole (see
-// norm_row_fwd_kernel).  Its teams' sums of dw and db are added up at the end.
-template <typename T, typename Gr, bool kBlock>
-__global__ __launch_bounds__(kBlock ? 1024 : 256) void norm_row_bwd_kernel(NormParams p) {
-  __shared__ float lds[kBlock ? 3 * 16 : 4 * 64 * 16];
-  const int team = p.team, teams = kBlock ? 1 : 256 / team, own = kBlock ? 0 : threadIdx.x / team;
-  const int at = (kBlock ? threadIdx.x : threadIdx.x % team) * 8, Dg = (int)p.Dg;
+// Sum of kN numbers over a team of 2^k <= 64 neighbouring lanes, or of whole waves (lds: waves * kN floats), in every
+// lane of it.
+template <int kN, bool kWaves>
+__device__ __forceinline__ void teams_sum(float (&v)[kN], int team, float* lds) {
+  if constexpr (!kWaves) {
+    team_sum<kN, false>(v, team, lds);
+  } else {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, of = team >> 6, first = wave - wave % of;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = wave_sum63(v[j]);
+    __syncthreads();                     // an earlier sum may still be read
+    if (lane == 63) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) lds[wave * kN + j] = v[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = 0.0f;
+    for (int w = first; w < first + of; ++w) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) v[j] += lds[w * kN + j];
+    }
+  }
+}
+
+// Token-major: a workgroup takes a group of channels and every parts-th share of the tokens, one a team at once: of
+// lanes, or (kWaves) of as many waves as the group needs.  8 channels a thread, the last thread the group's last 8
+// whole (see norm_row_fwd_kernel); kRagged: Dg is no multiple of 8.  A token waits for its loads and then for two sums
+// over the team, so the next token's inputs are loaded while one is worked on, where the registers allow (128 of them:
+// not z beside 4-byte inputs, none of the gate's four 4-byte streams).  The teams' sums of dw and db are added up
+// at the end.  8192 tokens of 5120 channels, bf16: 68 us (90 without the loads ahead; HBM 49), gated 128 us (82);
+// 8192 of 512: 14 us, of which the sum over parts is 4.
+template <typename T, typename Gr, bool kWaves, bool kRagged, bool kGate>
+__global__ __launch_bounds__(1024) void norm_row_bwd_kernel(NormParams p) {
+  __shared__ float lds[3 * 16];
+  __shared__ float fold[16 * 64 * 8];
+  const int team = p.team, teams = blockDim.x / team, own = threadIdx.x / team, lane = threadIdx.x % team;
+  const int Dg = (int)p.Dg;
   const int64_t part = blockIdx.x / p.G, ch = (blockIdx.x - part * p.G) * p.Dg;
-  const bool on = at < Dg;
-  const int c = at < Dg - 8 ? at : Dg - 8, dup = on ? at - c : 8;
+  const bool on = lane * 8 < Dg;
+  const int c = lane * 8 < Dg - 8 ? lane * 8 : Dg - 8, dup = on ? lane * 8 - c : 8;
+  float w[8];
   Raw8<float> wr, br;
   if (p.weight) wr = load_all8(p.weight + ch + c);
-  if (p.bias) br = load_all8(p.bias + ch + c);
+  if (kGate && p.bias) br = load_all8(p.bias + ch + c);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = p.weight ? get8(wr, j) : 1.0f;
   float sw[8], sb[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sw[j] = sb[j] = 0.0f;
-  // A wave's lanes stay together: a team past the last token goes through that one again and leaves it out.
-  for (int64_t first = part * teams; first < p.B; first += p.parts * teams) {
+  const T* x = static_cast<const T*>(p.x) + ch + c;
+  const Gr* dy = static_cast<const Gr*>(p.dy) + ch + c;
+  // The teams stay together: one past the last token goes through that one again and leaves it out.
+  auto token = [&](int64_t first) { return first + own < p.B ? first + own : p.B - 1; };
+  const int64_t stride = p.parts * teams;
+  const T* z = kGate ? static_cast<const T*>(p.z) + ch + c : nullptr;
+  constexpr bool kAhead = kGate && sizeof(T) == 2;       // z too, where there are registers for it
+  Raw8<T> zn;
+  if constexpr (kAhead) zn = load_all8(z + token(part * teams) * p.z_stride);
+  constexpr bool kNext = !kGate || sizeof(T) + sizeof(Gr) < 8;
+  Raw8<T> rn;
+  Raw8<Gr> dn;
+  if constexpr (kNext) {
+    rn = load_all8(x + token(part * teams) * p.x_stride);
+    dn = load_all8(dy + token(part * teams) * p.D);
+  }
+  for (int64_t first = part * teams; first < p.B; first += stride) {
     const bool mine = first + own < p.B;
-    const int64_t b = mine ? first + own : p.B - 1;
-    const Raw8<T> r = load_all8(static_cast<const T*>(p.x) + b * p.x_stride + ch + c);
-    const Raw8<Gr> dr = load_all8(static_cast<const Gr*>(p.dy) + b * p.D + ch + c);
-    Raw8<T> zr;
-    if (p.z) zr = load_all8(static_cast<const T*>(p.z) + b * p.z_stride + ch + c);
-    float mu[1] = {0.0f}, v[3] = {0.0f, 0.0f, 0.0f};
+    const int64_t b = token(first);
+    Raw8<T> r = rn, zr;
+    Raw8<Gr> dr = dn;
+    if constexpr (kAhead) zr = zn;
+    else if constexpr (kGate) zr = load_all8(z + b * p.z_stride);
+    if constexpr (!kNext) {
+      r = load_all8(x + b * p.x_stride);
+      dr = load_all8(dy + b * p.D);
+    } else if (first + stride < p.B) {
+      if constexpr (kAhead) zn = load_all8(z + token(first + stride) * p.z_stride);
+      rn = load_all8(x + token(first + stride) * p.x_stride);
+      dn = load_all8(dy + token(first + stride) * p.D);
+    }
+    float mu[1] = {0.0f}, v[3] = {0.0f, 0.0f, 0.0f}, d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = get8(r, j);
     if (!p.rms) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mu[0] += j < dup ? 0.0f : get8(r, j);
-      team_sum<1, kBlock>(mu, team, lds);
+      for (int j = 0; j < 8; ++j) mu[0] += !on || (kRagged && j < dup) ? 0.0f : d[j];
+      teams_sum<1, kWaves>(mu, team, lds);
       mu[0] *= p.inv_dg;
-    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float d = get8(r, j) - mu[0];
-      float g = get8(dr, j) * (p.weight ? get8(wr, j) : 1.0f);
-      if (p.z) g *= silu(get8(zr, j));
-      if (j >= dup) {
-        v[0] = __builtin_fmaf(d, d, v[0]);
-        v[1] += g;
-        v[2] = __builtin_fmaf(g, d, v[2]);
-      }
+      for (int j = 0; j < 8; ++j) d[j] -= mu[0];
     }
-    team_sum<3, kBlock>(v, team, lds);
-    const float k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
-    const float mg = p.rms ? 0.0f : v[1] * p.inv_dg, mx = v[2] * k * p.inv_dg;
-    float o[8], dm[8], xh[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      dm[j] = get8(dr, j);
-      xh[j] = (get8(r, j) - mu[0]) * k;
-    }
-    const int64_t out = b * p.D + ch + c;
-    if (p.z) {
+    if (on) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float zj = get8(zr, j), s = sigmoid(zj);
-        o[j] = dm[j] * __builtin_fmaf(xh[j], p.weight ? get8(wr, j) : 1.0f, p.bias ? get8(br, j) : 0.0f) * s *
-               __builtin_fmaf(zj, 1.0f - s, 1.0f);
-        dm[j] *= zj * s;
+        float gj = get8(dr, j) * w[j];
+        if constexpr (kGate) gj *= silu(get8(zr, j));
+        const float dj = kRagged && j < dup ? 0.0f : d[j];
+        if (kRagged && j < dup) gj = 0.0f;
+        v[0] = __builtin_fmaf(dj, dj, v[0]);
+        v[1] += gj;
+        v[2] = __builtin_fmaf(gj, dj, v[2]);
       }
-      if (on && mine) store8(static_cast<Gr*>(p.dz) + out, o, 8, 8);
     }
+    teams_sum<3, kWaves>(v, team, lds);
+    // dx = k (g - mean(g) - xh mean(g xh)) with xh = k d
+    const float k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
+    const float mg = p.rms ? 0.0f : -k * v[1] * p.inv_dg, mx = -k * k * (v[2] * k * p.inv_dg);
+    float o[8];
+    const int64_t out = b * p.D + ch + c;
+    if (on && mine) {
+      float dm[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      o[j] = k * (__builtin_fmaf(dm[j], p.weight ? get8(wr, j) : 1.0f, -mg) - xh[j] * mx);
-      if (mine) {
-        sw[j] = __builtin_fmaf(dm[j], xh[j], sw[j]);
+      for (int j = 0; j < 8; ++j) dm[j] = get8(dr, j);
+      if constexpr (kGate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float zj = get8(zr, j), s = sigmoid(zj);
+          o[j] = dm[j] * __builtin_fmaf(d[j] * k, w[j], p.bias ? get8(br, j) : 0.0f) * s * __builtin_fmaf(zj, 1.0f - s, 1.0f);
+          dm[j] *= zj * s;
+        }
+        store8(static_cast<Gr*>(p.dz) + out, o, 8, 8);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[j] = __builtin_fmaf(d[j], mx, __builtin_fmaf(k, dm[j] * w[j], mg));
+        sw[j] = __builtin_fmaf(dm[j], d[j] * k, sw[j]);
         sb[j] += dm[j];
       }
+      store8(static_cast<Gr*>(p.dx) + out, o, 8, 8);
     }
-    if (on && mine) store8(static_cast<Gr*>(p.dx) + out, o, 8, 8);
   }
-  if constexpr (!kBlock) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int m = team; m < 64; m *= 2) {
+  // Teams of a wave first, then a thread of the first team takes the same channels of the others, once for sw and
+  // once for sb.
+  const int of = kWaves ? team >> 6 : 1, waves = blockDim.x >> 6, at = threadIdx.x & 63;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sw[j] += __shfl_xor(sw[j], m);
-        sb[j] += __shfl_xor(sb[j], m);
+  for (int turn = 0; turn < 2; ++turn) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = turn ? sb[j] : sw[j];
+    if constexpr (!kWaves) {
+      for (int m = team; m < 64; m *= 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += __shfl_xor(v[j], m);
       }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lds[(wave * 64 + lane) * 16 + j] = sw[j];
-      lds[(wave * 64 + lane) * 16 + 8 + j] = sb[j];
     }
     __syncthreads();
-    if (own) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sw[j] = sb[j] = 0.0f;
-      for (int w = 0; w < 4; ++w) {
-        sw[j] += lds[(w * 64 + lane) * 16 + j];
-        sb[j] += lds[(w * 64 + lane) * 16 + 8 + j];
+    for (int j = 0; j < 8; ++j) fold[((threadIdx.x >> 6) * 64 + at) * 8 + j] = v[j];
+    __syncthreads();
+    if (own == 0 && on) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      for (int w = threadIdx.x >> 6; w < waves; w += of) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += fold[(w * 64 + at) * 8 + j];
       }
+      // channels that two threads have: both hold the same sums
+      store8<float, false>(p.part + (part * 2 + turn) * p.D + ch + c, v, 8, 8);
     }
   }
-  if (!on) return;
-  // channels that two threads have: both hold the same sums
-  float* sums = p.part + part * 2 * p.D + ch + c;
-  store8<float, false>(sums, sw, 8, 8);
-  store8<float, false>(sums + p.D, sb, 8, 8);
 }
 
 // Token-major, any group.
@@ -369,16 +428,17 @@ __global__ __launch_bounds__(256) void norm_row_long_bwd_kernel(NormParams p) {
   }
 }
 
-// dweight and dbias from their parts: 16 channels x 16 shares of them per workgroup, four loads under way.
-__global__ __launch_bounds__(256) void norm_sum_kernel(NormParams p) {
-  __shared__ float share[16][16];
-  const int64_t n = 2 * p.D, c = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
-  const int y = threadIdx.x >> 4;
+// dweight and dbias from their parts: 64 channels x 16 shares of the parts per workgroup.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormParams p) {
+  __shared__ float share[16][64];
+  const int64_t n = 2 * p.D, c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  const int y = threadIdx.x >> 6;
   float o = 0.0f;
   if (c < n) o = strided_sum(p.part + c, n, y, p.parts);
-  share[y][threadIdx.x & 15] = o;
+  share[y][threadIdx.x & 63] = o;
   __syncthreads();
   if (y || c >= n) return;
+#pragma unroll
   for (int w = 1; w < 16; ++w) o += share[w][threadIdx.x];
   if (c < p.D) p.dweight[c] = o;
   else p.dbias[c - p.D] = o;
@@ -395,6 +455,19 @@ hipError_t col_t(const NormParams& p, unsigned grid, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, typename Gr, bool kWaves>
+hipError_t row_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
+  const dim3 grid((unsigned)(p.parts * p.G)), block(q.threads);
+  if (p.Dg % 8) {
+    if (p.z) hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, kWaves, true, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, kWaves, true, false>), grid, block, 0, s, p);
+  } else {
+    if (p.z) hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, kWaves, false, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, kWaves, false, false>), grid, block, 0, s, p);
+  }
+  return hipGetLastError();
+}
+
 template <typename T, typename Gr>
 hipError_t main_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
   const unsigned grid = (unsigned)(p.parts * p.G);
@@ -406,12 +479,8 @@ hipError_t main_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
     case kNormColLong:
       hipLaunchKernelGGL((norm_col_long_bwd_kernel<T, Gr>), dim3(grid), dim3(256), 0, s, p);
       break;
-    case kNormRowTeam:
-      hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, false>), dim3(grid), dim3(256), 0, s, p);
-      break;
-    case kNormRowBlock:
-      hipLaunchKernelGGL((norm_row_bwd_kernel<T, Gr, true>), dim3(grid), dim3(q.threads), 0, s, p);
-      break;
+    case kNormRowTeam: return row_t<T, Gr, false>(p, q, s);
+    case kNormRowBlock: return row_t<T, Gr, true>(p, q, s);
     default:
       hipLaunchKernelGGL((norm_row_long_bwd_kernel<T, Gr>), dim3(grid), dim3(256), 0, s, p);
   }
@@ -422,7 +491,7 @@ template <typename T, typename Gr>
 hipError_t bwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
   const hipError_t e = main_t<T, Gr>(p, q, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((2 * p.D + 15) / 16)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((2 * p.D + 63) / 64)), dim3(1024), 0, s, p);
   return hipGetLastError();
 }
 
