@@ -278,7 +278,8 @@ struct NormParams {
 //   kNormRowTeam  token-major, 8 to 512 channels: teams of 2^k <= 64 lanes, 8 channels each
 //   kNormRowBlock token-major, up to 8192 channels: a workgroup, 8 channels a thread
 //   kNormRowLong  token-major, any group
-enum NormKind : int { kNormShapes = 4, kNormBwdShapes = 3, kNormColTwo = 4, kNormColLong, kNormRowTeam, kNormRowBlock, kNormRowLong };
+enum NormKind : int { kNormShapes = 4, kNormBwdShapes = 3, kNormColTwo = 4, kNormColLong, kNormRowTeam, kNormRowBlock,
+                      kNormRowWide, kNormRowLong };
 
 struct NormShape {
   int threads, lanes, chans;                    // workgroup, token lanes of 8 tokens, channels of a thread

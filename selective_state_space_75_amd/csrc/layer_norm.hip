@@ -122,49 +122,66 @@ __global__ __launch_bounds__(256) void norm_col_long_fwd_kernel(NormParams p) {
   }
 }
 
-// Token-major: a team of lanes, or a workgroup, per token and group; 8 channels a thread.  The last
-// thread takes the group's last 8 channels whole; those that the one before it has too (the first
-// `dup` of them) are left out of the sums.
-template <typename T, typename O, bool kBlock>
+// Token-major: a team of lanes, or a workgroup, per token and group; kC times 8 channels a thread.  The thread at the
+// group's end takes its last 8 channels whole; those that the one before it has too (the first `dup` of them)
+// are left out of the sums.
+template <typename T, typename O, bool kBlock, int kC>
 __global__ __launch_bounds__(kBlock ? 1024 : 256) void norm_row_fwd_kernel(NormParams p) {
   __shared__ float lds[16];
   const int team = p.team;
   const int64_t id = kBlock ? blockIdx.x : (int64_t)blockIdx.x * (256 / team) + threadIdx.x / team;
   const int at = (kBlock ? threadIdx.x : threadIdx.x % team) * 8, Dg = (int)p.Dg;
-  const bool on = at < Dg && id < p.B * p.G;
   const int64_t bg = id < p.B * p.G ? id : 0;
   const int64_t b = bg / p.G, ch = (bg - b * p.G) * p.Dg;
-  const int c = at < Dg - 8 ? at : Dg - 8, dup = on ? at - c : 8;
-  const Raw8<T> r = load_all8(static_cast<const T*>(p.x) + b * p.x_stride + ch + c);
-  Raw8<T> zr;
-  Raw8<float> w, bias;
-  if (p.z) zr = load_all8(static_cast<const T*>(p.z) + b * p.z_stride + ch + c);
-  if (p.weight) w = load_all8(p.weight + ch + c);
-  if (p.bias) bias = load_all8(p.bias + ch + c);
+  const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch;
+  const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch : nullptr;
+  bool on[kC];
+  int c[kC], dup[kC];
+  Raw8<T> r[kC], zr[kC];
+  Raw8<float> w[kC], bias[kC];
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    const int own = at + i * 8 * team;
+    on[i] = own < Dg && id < p.B * p.G;
+    c[i] = own < Dg - 8 ? own : Dg - 8;
+    dup[i] = on[i] ? own - c[i] : 8;
+    r[i] = load_all8(x + c[i]);
+    if (p.z) zr[i] = load_all8(z + c[i]);
+    if (p.weight) w[i] = load_all8(p.weight + ch + c[i]);
+    if (p.bias) bias[i] = load_all8(p.bias + ch + c[i]);
+  }
   float mu[1] = {0.0f}, k[1] = {0.0f};
   if (!p.rms) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mu[0] += j < dup ? 0.0f : get8(r, j);
+    for (int i = 0; i < kC; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mu[0] += j < dup[i] ? 0.0f : get8(r[i], j);
     team_sum<1, kBlock>(mu, team, lds);
     mu[0] *= p.inv_dg;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float d = j < dup ? 0.0f : get8(r, j) - mu[0];
-    k[0] = __builtin_fmaf(d, d, k[0]);
+  for (int i = 0; i < kC; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = j < dup[i] ? 0.0f : get8(r[i], j) - mu[0];
+      k[0] = __builtin_fmaf(d, d, k[0]);
+    }
   }
   team_sum<1, kBlock>(k, team, lds);
   k[0] = norm_root(__builtin_fmaf(k[0], p.inv_dg, p.eps));
-  if (!on) return;
-  float o[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    o[j] = __builtin_fmaf((get8(r, j) - mu[0]) * k[0], p.weight ? get8(w, j) : 1.0f, p.bias ? get8(bias, j) : 0.0f);
-  if (p.z) {
+  for (int i = 0; i < kC; ++i) {
+    if (!on[i]) continue;
+    float o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr, j));
+    for (int j = 0; j < 8; ++j)
+      o[j] = __builtin_fmaf((get8(r[i], j) - mu[0]) * k[0], p.weight ? get8(w[i], j) : 1.0f, p.bias ? get8(bias[i], j) : 0.0f);
+    if (p.z) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr[i], j));
+    }
+    store8(static_cast<O*>(p.y) + b * p.D + ch + c[i], o, 8, 8);
   }
-  store8(static_cast<O*>(p.y) + b * p.D + ch + c, o, 8, 8);
 }
 
 // Token-major, any group: a workgroup per token and group, three sweeps.
@@ -205,11 +222,14 @@ hipError_t fwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
       hipLaunchKernelGGL((norm_col_long_fwd_kernel<T, O>), dim3(grid), dim3(256), 0, s, p);
       break;
     case kNormRowTeam:
-      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, false>), dim3((items + 256 / p.team - 1) / (256 / p.team)), dim3(256),
+      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, false, 1>), dim3((items + 256 / p.team - 1) / (256 / p.team)), dim3(256),
                          0, s, p);
       break;
     case kNormRowBlock:
-      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, true>), dim3(items), dim3(q.threads), 0, s, p);
+      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, true, 1>), dim3(items), dim3(q.threads), 0, s, p);
+      break;
+    case kNormRowWide:
+      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, true, 2>), dim3(items), dim3(q.threads), 0, s, p);
       break;
     default:
       hipLaunchKernelGGL((norm_row_long_fwd_kernel<T, O>), dim3(items), dim3(256), 0, s, p);
@@ -228,10 +248,11 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
   q.tiles = 1;
   q.threads = 256;
   if (L == 1) {
-    q.kind = Dg < 8 || Dg > 8192 ? kNormRowLong : Dg > 512 ? kNormRowBlock : kNormRowTeam;
+    q.kind = Dg < 8 || Dg > 16384 ? kNormRowLong : Dg > 8192 ? kNormRowWide : Dg > 512 ? kNormRowBlock : kNormRowTeam;
     q.lanes = 1;                                       // threads of a token
     while (q.kind == kNormRowTeam && q.lanes * 8 < Dg) q.lanes *= 2;
     if (q.kind == kNormRowBlock) q.threads = q.lanes = (int)((Dg + 511) / 512) * 64;
+    if (q.kind == kNormRowWide) q.threads = q.lanes = (int)((Dg + 1023) / 1024) * 64;
     if (bwd && q.kind != kNormRowLong) q.threads = 1024 / q.lanes * q.lanes;     // as many teams as that holds
   } else if (L < 8) {
     q.kind = kNormColLong;
@@ -270,8 +291,8 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
   // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.  Token-major
   // that is one a CU, or two where two of them fit (a group's one team of up to 640 threads: 8192 tokens of 5120
   // channels, bf16, 68 us, with one 93; of 512 channels, where one workgroup holds 1024 threads, 18 us with two and 14 with one).
-  const bool rows = q.kind == kNormRowTeam || q.kind == kNormRowBlock;
-  int64_t most = (rows ? 256 * (1280 / q.threads) : q.threads > 256 ? 512 : 1024) / G;
+  const bool rows = q.kind == kNormRowTeam || q.kind == kNormRowBlock || q.kind == kNormRowWide;
+  int64_t most = (rows ? 256 * (q.kind == kNormRowWide ? 1 : 1280 / q.threads) : q.threads > 256 ? 512 : 1024) / G;
   const int64_t work = rows ? ceil_div(B, q.threads / q.lanes) : B * q.tiles;
   if (most < 1) most = 1;
   if (most > work) most = work;

@@ -389,6 +389,149 @@ __global__ __launch_bounds__(1024) void norm_row_bwd_kernel(NormParams p) {
   }
 }
 
+// Token-major, groups of 8193 to 16384 channels: a workgroup per token, 2 x 8 channels a thread.  Weights, bias and z
+// come from the caches again for each token: the sums of dw and db, x and dy fill the 128 registers, and with the
+// gate's work beside them the sums live in LDS, a thread's own 32 numbers.
+template <typename T, typename Gr, bool kGate>
+__global__ __launch_bounds__(1024) void norm_row_wide_bwd_kernel(NormParams p) {
+  __shared__ float lds[3 * 16];
+  const int Dg = (int)p.Dg;
+  const int64_t part = blockIdx.x / p.G, ch = (blockIdx.x - part * p.G) * p.Dg;
+  bool on[2];
+  int c[2], dup[2];
+  float sw[kGate ? 1 : 2][8], sb[kGate ? 1 : 2][8];
+  __shared__ float4 own_sums[kGate ? 8 : 1][kGate ? 1024 : 1];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int own = (threadIdx.x + i * blockDim.x) * 8;
+    on[i] = own < Dg;
+    c[i] = own < Dg - 8 ? own : Dg - 8;
+    dup[i] = on[i] ? own - c[i] : 8;
+    if constexpr (kGate) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) own_sums[i * 4 + q][threadIdx.x] = float4{0.0f, 0.0f, 0.0f, 0.0f};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sw[i][j] = sb[i][j] = 0.0f;
+    }
+  }
+  for (int64_t b = part; b < p.B; b += p.parts) {
+    const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch;
+    const T* z = kGate ? static_cast<const T*>(p.z) + b * p.z_stride + ch : nullptr;
+    const int64_t row = b * p.D + ch;
+    const float* weight = p.weight ? p.weight + ch : nullptr;
+    const float* shift = p.bias ? p.bias + ch : nullptr;
+    const Gr* dy = static_cast<const Gr*>(p.dy) + row;
+    Raw8<T> r[2];
+    Raw8<Gr> dr[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r[i] = load_all8(lane_at(x, c[i]));
+      dr[i] = load_all8(lane_at(dy, c[i]));
+    }
+    float mu[1] = {0.0f}, v[3] = {0.0f, 0.0f, 0.0f};
+    if (!p.rms) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mu[0] += j < dup[i] ? 0.0f : get8(r[i], j);
+      team_sum<1, true>(mu, 0, lds);
+      mu[0] *= p.inv_dg;
+    }
+    keep(r[0]);
+    keep(r[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      asm("" : "+s"(weight), "+s"(z), "+v"(v[0]));       // loaded piece by piece: not worth registers for longer
+      Raw8<float> w;
+      Raw8<T> zr;
+      if (weight) w = load_all8(lane_at(weight, c[i]));
+      if constexpr (kGate) zr = load_all8(lane_at(z, c[i]));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = j < dup[i] ? 0.0f : get8(r[i], j) - mu[0];
+        float g = get8(dr[i], j) * (weight ? get8(w, j) : 1.0f);
+        if constexpr (kGate) g *= silu(get8(zr, j));
+        g = j < dup[i] ? 0.0f : g;
+        v[0] = __builtin_fmaf(d, d, v[0]);
+        v[1] += g;
+        v[2] = __builtin_fmaf(g, d, v[2]);
+      }
+    }
+    team_sum<3, true>(v, 0, lds);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      keep(r[i]);
+      keep(dr[i]);
+    }
+    const float k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
+    const float mg = p.rms ? 0.0f : -k * v[1] * p.inv_dg, mx = -k * k * (v[2] * k * p.inv_dg);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      asm("" : "+s"(weight), "+s"(shift), "+s"(z), "+v"(v[1]));
+      if (!on[i]) continue;
+      Raw8<float> w;
+      if (weight) w = load_all8(lane_at(weight, c[i]));
+      float o[8], dm[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dm[j] = get8(dr[i], j);
+      if constexpr (kGate) {
+        const Raw8<T> zr = load_all8(lane_at(z, c[i]));
+        Raw8<float> bias;
+        if (shift) bias = load_all8(lane_at(shift, c[i]));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float zj = get8(zr, j), s = sigmoid(zj), xh = (get8(r[i], j) - mu[0]) * k;
+          o[j] = dm[j] * __builtin_fmaf(xh, weight ? get8(w, j) : 1.0f, shift ? get8(bias, j) : 0.0f) * s *
+                 __builtin_fmaf(zj, 1.0f - s, 1.0f);
+          dm[j] *= zj * s;
+        }
+        store8(lane_at(static_cast<Gr*>(p.dz) + row, c[i]), o, 8, 8);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = get8(r[i], j) - mu[0];
+        o[j] = __builtin_fmaf(d, mx, __builtin_fmaf(k, dm[j] * (weight ? get8(w, j) : 1.0f), mg));
+        if constexpr (!kGate) {
+          sw[i][j] = __builtin_fmaf(dm[j], d * k, sw[i][j]);
+          sb[i][j] += dm[j];
+        }
+      }
+      store8(lane_at(static_cast<Gr*>(p.dx) + row, c[i]), o, 8, 8);
+      if constexpr (kGate) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float4 t = own_sums[i * 4 + q][threadIdx.x];
+          float* a = &t.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = (q & 1) * 4 + e;
+            a[e] = q < 2 ? __builtin_fmaf(dm[j], (get8(r[i], j) - mu[0]) * k, a[e]) : a[e] + dm[j];
+          }
+          own_sums[i * 4 + q][threadIdx.x] = t;
+        }
+      }
+    }
+  }
+  float* sums = p.part + part * 2 * p.D + ch;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!on[i]) continue;                                // channels that two threads have: both hold the same sums
+    if constexpr (kGate) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 t = own_sums[i * 4 + q][threadIdx.x];
+        (q < 2 ? sw : sb)[0][(q & 1) * 4] = t.x;
+        (q < 2 ? sw : sb)[0][(q & 1) * 4 + 1] = t.y;
+        (q < 2 ? sw : sb)[0][(q & 1) * 4 + 2] = t.z;
+        (q < 2 ? sw : sb)[0][(q & 1) * 4 + 3] = t.w;
+      }
+    }
+    store8<float, false>(sums + c[i], sw[kGate ? 0 : i], 8, 8);
+    store8<float, false>(sums + p.D + c[i], sb[kGate ? 0 : i], 8, 8);
+  }
+}
+
 // Token-major, any group.
 template <typename T, typename Gr>
 __global__ __launch_bounds__(256) void norm_row_long_bwd_kernel(NormParams p) {
@@ -481,6 +624,10 @@ hipError_t main_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
       break;
     case kNormRowTeam: return row_t<T, Gr, false>(p, q, s);
     case kNormRowBlock: return row_t<T, Gr, true>(p, q, s);
+    case kNormRowWide:
+      if (p.z) hipLaunchKernelGGL((norm_row_wide_bwd_kernel<T, Gr, true>), dim3(grid), dim3(q.threads), 0, s, p);
+      else hipLaunchKernelGGL((norm_row_wide_bwd_kernel<T, Gr, false>), dim3(grid), dim3(q.threads), 0, s, p);
+      break;
     default:
       hipLaunchKernelGGL((norm_row_long_bwd_kernel<T, Gr>), dim3(grid), dim3(256), 0, s, p);
   }

@@ -53,6 +53,13 @@ CASES = [((1, 1, 1), 1, "f32", "f32", False, False, True, False),
          ((600, 1000), 1, "bf16", "f32", True, False, True, False),
          ((33, 5120), 1, "bf16", "f32", False, False, True, True),
          ((5, 4097), 1, "f32", "f32", True, False, True, False),
+         ((3, 8193), 1, "bf16", "f32", False, False, True, False),
+         ((300, 8200), 1, "f32", "f32", True, False, True, True),
+         ((5, 9003), 1, "f32", "bf16", False, True, False, False),
+         ((4, 20480), 2, "bf16", "bf16", True, False, True, True),
+         ((3, 16383), 1, "bf16", "f32", True, True, False, False),
+         ((2, 16384), 1, "f32", "f32", True, False, True, False),
+         ((3, 16385), 1, "f32", "f32", True, False, True, False),
          ((3, 20001), 1, "bf16", "f32", False, False, True, False),
          ((2, 70001), 1, "f32", "f32", True, True, True, False)]
 
@@ -103,7 +110,7 @@ def test_forward_and_backward(shape, groups, dtype, out, gated, rms, affine, ran
         near(g[n], ref[n], 2 * E, n, np.maximum(ref["scale"][n], 1e-30))
 
 
-@pytest.mark.parametrize("shape", [(2, 300, 50), (20, 1500), (1, 6000, 20), (2, 40000)])
+@pytest.mark.parametrize("shape", [(2, 300, 50), (20, 1500), (1, 6000, 20), (3, 12000), (2, 40000)])
 def test_a_large_mean_is_taken_off(shape, dev):
     """Offsets a thousand times the spread: x - mean loses 2^-24 of the offset, 1e3 * 6e-8 = 6e-5 of the
     spread per number, to the inputs' own rounding none (they are given); the variance around the mean is
@@ -119,7 +126,7 @@ def test_a_large_mean_is_taken_off(shape, dev):
     near(g["dx"], ref["dx"], 2.4e-4, "dx", ref["scale"]["dx"])
 
 
-@pytest.mark.parametrize("shape,groups", [((2, 24, 70), 2), ((1, 3000, 30), 1), ((9, 640), 4), ((3, 30000), 1)])
+@pytest.mark.parametrize("shape,groups", [((2, 24, 70), 2), ((1, 3000, 30), 1), ((9, 640), 4), ((3, 9001), 1), ((3, 30000), 1)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_what_is_not_finite_stays_in_its_token_and_group(shape, groups, bad, dev):
     import torch
@@ -141,7 +148,7 @@ def test_what_is_not_finite_stays_in_its_token_and_group(shape, groups, bad, dev
     assert torch.isnan(b[own]).all()
 
 
-@pytest.mark.parametrize("shape,groups", [((2, 30, 67), 3), ((1, 2100, 19), 1), ((7, 1030), 2), ((3, 9), 3)])
+@pytest.mark.parametrize("shape,groups", [((2, 30, 67), 3), ((1, 2100, 19), 1), ((7, 1030), 2), ((3, 10007), 1), ((3, 9), 3)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_alignment_and_neighbours(shape, groups, dtype, dev):
     import torch
@@ -166,7 +173,7 @@ def test_alignment_and_neighbours(shape, groups, dtype, dev):
 def test_a_tokens_bits_do_not_depend_on_the_batch(dev):
     import torch
     import selective_state_space_75_amd as m
-    for shape, groups in (((6, 700, 40), 4), ((6, 250, 300), 1), ((900, 700), 1), ((40, 96), 3)):
+    for shape, groups in (((6, 700, 40), 4), ((6, 250, 300), 1), ((900, 700), 1), ((300, 9000), 1), ((40, 96), 3)):
         x, t = tensors(shape, "bf16", 80, True, True, False, dev)
         kw = dict(groups=groups)
         y = m.layer_norm_fwd(t["x"], t["weight"], t["bias"], t["z"], **kw)
@@ -178,7 +185,7 @@ def test_a_tokens_bits_do_not_depend_on_the_batch(dev):
         assert torch.equal(g1["dx"], g["dx"][one]) and torch.equal(g1["dz"], g["dz"][one])
 
 
-@pytest.mark.parametrize("shape,groups", [((3, 700, 333), 1), ((2, 240, 700), 3), ((700, 900), 1), ((3000, 96), 3),
+@pytest.mark.parametrize("shape,groups", [((3, 700, 333), 1), ((2, 240, 700), 3), ((700, 900), 1), ((3000, 96), 3), ((600, 9000), 1),
                                           ((5, 60, 6), 2)])
 def test_the_same_call_gives_the_same_bits(shape, groups, dev):
     import torch
