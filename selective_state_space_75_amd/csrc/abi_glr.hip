@@ -310,7 +310,8 @@ int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, cons
   if (!y) return MAMBA_ERR_NULL;
   if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
   const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), 0);
-  if (!norm_fits(q, B, D, L, groups, B * groups * q.tiles)) return MAMBA_ERR_SHAPE;
+  const bool by_part = q.kind == mamba::kNormRowBlock || q.kind == mamba::kNormRowWide;
+  if (!norm_fits(q, B, D, L, groups, by_part ? q.parts * groups : B * groups * q.tiles)) return MAMBA_ERR_SHAPE;
   const size_t need = norm_fwd_bytes(B, D, L, groups);
   if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
   if (need && !aligned(workspace, 256)) return MAMBA_ERR_ALIGN;

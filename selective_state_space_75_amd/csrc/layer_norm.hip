@@ -122,65 +122,131 @@ __global__ __launch_bounds__(256) void norm_col_long_fwd_kernel(NormParams p) {
   }
 }
 
-// Token-major: a team of lanes, or a workgroup, per token and group; kC times 8 channels a thread.  The thread at the
-// group's end takes its last 8 channels whole; those that the one before it has too (the first `dup` of them)
-// are left out of the sums.
-template <typename T, typename O, bool kBlock, int kC>
-__global__ __launch_bounds__(kBlock ? 1024 : 256) void norm_row_fwd_kernel(NormParams p) {
-  __shared__ float lds[16];
+// Token-major, groups of up to 512 channels: a team of lanes per token and group, 8 channels a lane.  The last lane
+// takes the group's last 8 channels whole; those that the one before it has too (the first `dup` of them) are
+// left out of the sums.
+template <typename T, typename O>
+__global__ __launch_bounds__(256) void norm_row_fwd_kernel(NormParams p) {
   const int team = p.team;
-  const int64_t id = kBlock ? blockIdx.x : (int64_t)blockIdx.x * (256 / team) + threadIdx.x / team;
-  const int at = (kBlock ? threadIdx.x : threadIdx.x % team) * 8, Dg = (int)p.Dg;
+  const int64_t id = (int64_t)blockIdx.x * (256 / team) + threadIdx.x / team;
+  const int at = (threadIdx.x % team) * 8, Dg = (int)p.Dg;
+  const bool on = at < Dg && id < p.B * p.G;
   const int64_t bg = id < p.B * p.G ? id : 0;
   const int64_t b = bg / p.G, ch = (bg - b * p.G) * p.Dg;
-  const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch;
-  const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch : nullptr;
-  bool on[kC];
-  int c[kC], dup[kC];
-  Raw8<T> r[kC], zr[kC];
-  Raw8<float> w[kC], bias[kC];
-#pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    const int own = at + i * 8 * team;
-    on[i] = own < Dg && id < p.B * p.G;
-    c[i] = own < Dg - 8 ? own : Dg - 8;
-    dup[i] = on[i] ? own - c[i] : 8;
-    r[i] = load_all8(x + c[i]);
-    if (p.z) zr[i] = load_all8(z + c[i]);
-    if (p.weight) w[i] = load_all8(p.weight + ch + c[i]);
-    if (p.bias) bias[i] = load_all8(p.bias + ch + c[i]);
-  }
+  const int c = at < Dg - 8 ? at : Dg - 8, dup = on ? at - c : 8;
+  const Raw8<T> r = load_all8(static_cast<const T*>(p.x) + b * p.x_stride + ch + c);
+  Raw8<T> zr;
+  Raw8<float> w, bias;
+  if (p.z) zr = load_all8(static_cast<const T*>(p.z) + b * p.z_stride + ch + c);
+  if (p.weight) w = load_all8(p.weight + ch + c);
+  if (p.bias) bias = load_all8(p.bias + ch + c);
   float mu[1] = {0.0f}, k[1] = {0.0f};
   if (!p.rms) {
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mu[0] += j < dup[i] ? 0.0f : get8(r[i], j);
-    team_sum<1, kBlock>(mu, team, lds);
+    for (int j = 0; j < 8; ++j) mu[0] += j < dup ? 0.0f : get8(r, j);
+    team_sum<1, false>(mu, team, nullptr);
     mu[0] *= p.inv_dg;
   }
 #pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float d = j < dup ? 0.0f : get8(r, j) - mu[0];
+    k[0] = __builtin_fmaf(d, d, k[0]);
+  }
+  team_sum<1, false>(k, team, nullptr);
+  k[0] = norm_root(__builtin_fmaf(k[0], p.inv_dg, p.eps));
+  if (!on) return;
+  float o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    o[j] = __builtin_fmaf((get8(r, j) - mu[0]) * k[0], p.weight ? get8(w, j) : 1.0f, p.bias ? get8(bias, j) : 0.0f);
+  if (p.z) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr, j));
+  }
+  store8(static_cast<O*>(p.y) + b * p.D + ch + c, o, 8, 8);
+}
+
+// Token-major, a workgroup of the group's width, kC times 8 channels a thread: it takes every parts-th token, keeps
+// the weights (8 bytes a channel, twice what a token's bf16 x and y are), and has the next token's x and z loaded
+// while one is worked on.
+template <typename T, typename O, bool kGate, int kC>
+__global__ __launch_bounds__(1024) void norm_row_block_fwd_kernel(NormParams p) {
+  __shared__ float lds[16];
+  const int Dg = (int)p.Dg;
+  const int64_t part = blockIdx.x / p.G, ch = (blockIdx.x - part * p.G) * p.Dg;
+  const T* x = static_cast<const T*>(p.x) + ch;
+  const T* z = kGate ? static_cast<const T*>(p.z) + ch : nullptr;
+  O* y = static_cast<O*>(p.y) + ch;
+  bool on[kC];
+  int c[kC], dup[kC];
+  float w[kC][8], bias[kC][8];
+  Raw8<T> rn[kC], zn[kC];
+#pragma unroll
   for (int i = 0; i < kC; ++i) {
+    const int at = (threadIdx.x + i * blockDim.x) * 8;
+    on[i] = at < Dg;
+    c[i] = at < Dg - 8 ? at : Dg - 8;
+    dup[i] = on[i] ? at - c[i] : 8;
+    rn[i] = load_all8(x + part * p.x_stride + c[i]);
+    if constexpr (kGate) zn[i] = load_all8(z + part * p.z_stride + c[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    Raw8<float> wr, br;
+    if (p.weight) wr = load_all8(p.weight + ch + c[i]);
+    if (p.bias) br = load_all8(p.bias + ch + c[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float d = j < dup[i] ? 0.0f : get8(r[i], j) - mu[0];
-      k[0] = __builtin_fmaf(d, d, k[0]);
+      w[i][j] = p.weight ? get8(wr, j) : 1.0f;
+      bias[i][j] = p.bias ? get8(br, j) : 0.0f;
     }
   }
-  team_sum<1, kBlock>(k, team, lds);
-  k[0] = norm_root(__builtin_fmaf(k[0], p.inv_dg, p.eps));
+  for (int64_t b = part; b < p.B; b += p.parts) {
+    Raw8<T> r[kC], zr[kC];
 #pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    if (!on[i]) continue;
-    float o[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      o[j] = __builtin_fmaf((get8(r[i], j) - mu[0]) * k[0], p.weight ? get8(w[i], j) : 1.0f, p.bias ? get8(bias[i], j) : 0.0f);
-    if (p.z) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr[i], j));
+    for (int i = 0; i < kC; ++i) {
+      r[i] = rn[i];
+      if constexpr (kGate) zr[i] = zn[i];
     }
-    store8(static_cast<O*>(p.y) + b * p.D + ch + c[i], o, 8, 8);
+    if (b + p.parts < p.B) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        rn[i] = load_all8(x + (b + p.parts) * p.x_stride + c[i]);
+        if constexpr (kGate) zn[i] = load_all8(z + (b + p.parts) * p.z_stride + c[i]);
+      }
+    }
+    float mu[1] = {0.0f}, k[1] = {0.0f};
+    if (!p.rms) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mu[0] += j < dup[i] ? 0.0f : get8(r[i], j);
+      }
+      team_sum<1, true>(mu, 0, lds);
+      mu[0] *= p.inv_dg;
+    }
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = j < dup[i] ? 0.0f : get8(r[i], j) - mu[0];
+        k[0] = __builtin_fmaf(d, d, k[0]);
+      }
+    }
+    team_sum<1, true>(k, 0, lds);
+    k[0] = norm_root(__builtin_fmaf(k[0], p.inv_dg, p.eps));
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      if (!on[i]) continue;
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = __builtin_fmaf((get8(r[i], j) - mu[0]) * k[0], w[i][j], bias[i][j]);
+      if constexpr (kGate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr[i], j));
+      }
+      store8(y + b * p.D + c[i], o, 8, 8);
+    }
   }
 }
 
@@ -209,6 +275,14 @@ hipError_t col_t(const NormParams& p, unsigned grid, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, typename O, int kC>
+hipError_t block_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
+  const dim3 grid((unsigned)(p.parts * p.G)), block(q.threads);
+  if (p.z) hipLaunchKernelGGL((norm_row_block_fwd_kernel<T, O, true, kC>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((norm_row_block_fwd_kernel<T, O, false, kC>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
 template <typename T, typename O>
 hipError_t fwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
   const unsigned items = (unsigned)(p.B * p.G), grid = (unsigned)(p.B * p.G * q.tiles);
@@ -222,15 +296,10 @@ hipError_t fwd_t(const NormParams& p, const NormPlan& q, hipStream_t s) {
       hipLaunchKernelGGL((norm_col_long_fwd_kernel<T, O>), dim3(grid), dim3(256), 0, s, p);
       break;
     case kNormRowTeam:
-      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, false, 1>), dim3((items + 256 / p.team - 1) / (256 / p.team)), dim3(256),
-                         0, s, p);
+      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O>), dim3((items + 256 / p.team - 1) / (256 / p.team)), dim3(256), 0, s, p);
       break;
-    case kNormRowBlock:
-      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, true, 1>), dim3(items), dim3(q.threads), 0, s, p);
-      break;
-    case kNormRowWide:
-      hipLaunchKernelGGL((norm_row_fwd_kernel<T, O, true, 2>), dim3(items), dim3(q.threads), 0, s, p);
-      break;
+    case kNormRowBlock: return block_t<T, O, 1>(p, q, s);
+    case kNormRowWide: return block_t<T, O, 2>(p, q, s);
     default:
       hipLaunchKernelGGL((norm_row_long_fwd_kernel<T, O>), dim3(items), dim3(256), 0, s, p);
   }
@@ -288,12 +357,16 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     q.parts = B * ceil_div(L, 8 * q.apply_lanes);
     return q;
   }
-  // Workgroups that fill the chip and no more: every part of the weight's sums is written and read.  Token-major
-  // that is one a CU, or two where two of them fit (a group's one team of up to 640 threads: 8192 tokens of 5120
-  // channels, bf16, 68 us, with one 93; of 512 channels, where one workgroup holds 1024 threads, 18 us with two and 14 with one).
+  // Backward, workgroups that fill the chip and no more: every part of the weight's sums is written and read.
+  // Token-major that is one a CU, or two where two of them fit (a group's one team of up to 640 threads: 8192 tokens of
+  // 5120 channels, bf16, 68 us, with one 93; of 512 channels, where one workgroup holds 1024 threads, 18 us with two
+  // and 14 with one).  Forward (kNormRowBlock, kNormRowWide) a CU gets the power of two that makes up to 2048
+  // threads: two workgroups of 640 for 5120 channels 33 us, three 38; two of 896 for 7168 channels 51 us, one 68.
   const bool rows = q.kind == kNormRowTeam || q.kind == kNormRowBlock || q.kind == kNormRowWide;
-  int64_t most = (rows ? 256 * (q.kind == kNormRowWide ? 1 : 1280 / q.threads) : q.threads > 256 ? 512 : 1024) / G;
-  const int64_t work = rows ? ceil_div(B, q.threads / q.lanes) : B * q.tiles;
+  int64_t fit = bwd && q.kind != kNormRowWide && q.threads <= 640 ? 2 : 1;
+  while (!bwd && 2 * fit * q.threads <= 2048) fit *= 2;
+  int64_t most = (rows ? 256 * fit : q.threads > 256 ? 512 : 1024) / G;
+  const int64_t work = rows ? ceil_div(B, bwd ? q.threads / q.lanes : 1) : B * q.tiles;
   if (most < 1) most = 1;
   if (most > work) most = work;
   q.parts = ceil_div(work, ceil_div(work, most));
