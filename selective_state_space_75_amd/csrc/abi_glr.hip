@@ -146,11 +146,11 @@ size_t norm_stat_bytes(const mamba::NormPlan& q, int64_t B, int64_t L, int64_t G
   return q.kind == mamba::kNormColTwo ? size_t(B) * G * q.chunks * numbers * L * sizeof(float) : 0;
 }
 
-// The plan depends on the element widths; the workspace is enough for all of them.
+// The plan depends on the element widths and on z; the workspace is enough for all of them.
 size_t norm_fwd_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
   size_t most = 0;
   for (int in : {2, 4}) {
-    const size_t n = norm_stat_bytes(mamba::norm_plan(B, D, L, G, in, 0), B, L, G, 2);
+    const size_t n = norm_stat_bytes(mamba::norm_plan(B, D, L, G, in, 0, false), B, L, G, 2);
     if (n > most) most = n;
   }
   return most;
@@ -158,9 +158,11 @@ size_t norm_fwd_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
 size_t norm_bwd_bytes(int64_t B, int64_t D, int64_t L, int64_t G) {
   size_t most = 0;
   for (int grad : {2, 4}) {
-    const mamba::NormPlan q = mamba::norm_plan(B, D, L, G, 2, grad);
-    const size_t n = norm_part_bytes(q, D) + norm_stat_bytes(q, B, L, G, 4);
-    if (n > most) most = n;
+    for (bool gate : {false, true}) {
+      const mamba::NormPlan q = mamba::norm_plan(B, D, L, G, 2, grad, gate);
+      const size_t n = norm_part_bytes(q, D) + norm_stat_bytes(q, B, L, G, 4);
+      if (n > most) most = n;
+    }
   }
   return most;
 }
@@ -309,7 +311,7 @@ int mamba_layer_norm_fwd(const void* x, const void* z, const float* weight, cons
   if (st != MAMBA_OK) return st;
   if (!y) return MAMBA_ERR_NULL;
   if (!aligned(y, width(out_dtype))) return MAMBA_ERR_ALIGN;
-  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), 0);
+  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), 0, z != nullptr);
   const bool by_part = q.kind == mamba::kNormRowBlock || q.kind == mamba::kNormRowWide;
   if (!norm_fits(q, B, D, L, groups, by_part ? q.parts * groups : B * groups * q.tiles)) return MAMBA_ERR_SHAPE;
   const size_t need = norm_fwd_bytes(B, D, L, groups);
@@ -335,7 +337,7 @@ int mamba_layer_norm_bwd(const void* x, const void* z, const float* weight, cons
   if (st != MAMBA_OK) return st;
   if (!dy || !dx || (z && !dz) || !dweight || !dbias) return MAMBA_ERR_NULL;
   if (!all_aligned({dy, dx, dz}, width(grad_dtype)) || !all_aligned({dweight, dbias}, 4)) return MAMBA_ERR_ALIGN;
-  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), (int)width(grad_dtype));
+  const mamba::NormPlan q = mamba::norm_plan(B, D, L, groups, (int)width(in_dtype), (int)width(grad_dtype), z != nullptr);
   if (!norm_fits(q, B, D, L, groups, q.parts * groups) || !mamba::launch_fits(ceil_div(2 * D, 64), 1024))
     return MAMBA_ERR_SHAPE;
   norm_set(p, q);

@@ -283,13 +283,14 @@ enum NormKind : int { kNormShapes = 4, kNormBwdShapes = 3, kNormColTwo = 4, kNor
 
 struct NormShape {
   int threads, lanes, chans;                    // workgroup, token lanes of 8 tokens, channels of a thread
+  int cu, cu_gate;                              // backward: workgroups that a CU's registers hold, without and with z
 };
 // Token lanes make whole cache lines of 128 bytes.  For 2-byte and 4-byte inputs (backward: with a 4-byte
 // array among them).
 constexpr NormShape kNormFwd2[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {1024, 8, 16}};
 constexpr NormShape kNormFwd4[kNormShapes] = {{256, 4, 4}, {256, 4, 8}, {512, 4, 8}, {512, 4, 20}};
-constexpr NormShape kNormBwd2[kNormBwdShapes] = {{256, 8, 4}, {256, 8, 8}, {512, 8, 8}};
-constexpr NormShape kNormBwd4[kNormBwdShapes] = {{256, 4, 2}, {256, 4, 4}, {512, 4, 4}};
+constexpr NormShape kNormBwd2[kNormBwdShapes] = {{256, 8, 4, 4, 3}, {256, 8, 8, 3, 2}, {512, 8, 8, 1, 1}};
+constexpr NormShape kNormBwd4[kNormBwdShapes] = {{256, 4, 2, 4, 4}, {256, 4, 4, 3, 2}, {512, 4, 4, 1, 1}};
 
 // The two launches of kNormColTwo.
 constexpr int kNormStatThreads = 512, kNormStatLanes = 8;    // 64 tokens, 64 channel lanes
@@ -301,7 +302,8 @@ struct NormPlan {
   int64_t chunks, chunk;                        // kNormColTwo: pieces of the group, and their channels
   int64_t apply_lanes, apply_chans;             // token lanes, and channels of a workgroup
 };
-NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width);   // grad_width 0: forward
+// grad_width 0: forward.  gate (backward): there is a z.
+NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width, bool gate);
 
 // Whether a launch of this many workgroups is one: HIP takes fewer than 2^32 threads in all.
 inline bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups <= int64_t(0xffffffff) / threads; }

@@ -310,10 +310,11 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width) {
+NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int grad_width, bool gate) {
   const int64_t Dg = D / G;
   const bool bwd = grad_width != 0;
   NormPlan q{};
+  int64_t cu = 4;                                      // workgroups that a CU holds at once
   q.tiles = 1;
   q.threads = 256;
   if (L == 1) {
@@ -333,6 +334,7 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
       const int64_t lanes = shapes[i].threads / shapes[i].lanes;      // channel lanes
       if (Dg > lanes * shapes[i].chans || L >= (int64_t(1) << 30) / (lanes + 1)) continue;   // 32-bit byte offsets
       q.kind = i;
+      cu = gate ? shapes[i].cu_gate : shapes[i].cu;
       q.threads = shapes[i].threads;
       q.lanes = shapes[i].lanes;
       break;
@@ -357,16 +359,32 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     q.parts = B * ceil_div(L, 8 * q.apply_lanes);
     return q;
   }
+  const bool rows = q.kind == kNormRowTeam || q.kind == kNormRowBlock || q.kind == kNormRowWide;
+  const int64_t work = rows ? ceil_div(B, bwd ? q.threads / q.lanes : 1) : B * q.tiles;
+  if (bwd && q.kind < kNormColTwo) {
+    // Every workgroup takes `each` tiles, in rounds of what the chip holds at once: the fewest tiles one after
+    // the other, and among equals the fewest parts of the weight's sums (4 x 5120 channels, 40 groups, L = 2048, bf16,
+    // gated: 5120 tiles, 768 workgroups at once, seven tiles each 108 us; five each, a second round of a third, 131).
+    const int64_t all = work * G, once = 256 * cu, last = ceil_div(all, once);
+    int64_t each = last < work ? last : work, least = ceil_div(ceil_div(work, each) * G, once) * each;
+    for (int64_t n = each - 1; n > 0 && n >= last - 64; --n) {
+      const int64_t rounds = ceil_div(ceil_div(work, n) * G, once) * n;
+      if (rounds < least) {
+        least = rounds;
+        each = n;
+      }
+    }
+    q.parts = ceil_div(work, each);
+    return q;
+  }
   // Backward, workgroups that fill the chip and no more: every part of the weight's sums is written and read.
   // Token-major that is one a CU, or two where two of them fit (a group's one team of up to 640 threads: 8192 tokens of
   // 5120 channels, bf16, 68 us, with one 93; of 512 channels, where one workgroup holds 1024 threads, 18 us with two
   // and 14 with one).  Forward (kNormRowBlock, kNormRowWide) a CU gets the power of two that makes up to 2048
   // threads: two workgroups of 640 for 5120 channels 33 us, three 38; two of 896 for 7168 channels 51 us, one 68.
-  const bool rows = q.kind == kNormRowTeam || q.kind == kNormRowBlock || q.kind == kNormRowWide;
-  int64_t fit = bwd && q.kind != kNormRowWide && q.threads <= 640 ? 2 : 1;
-  while (!bwd && 2 * fit * q.threads <= 2048) fit *= 2;
-  int64_t most = (rows ? 256 * fit : q.threads > 256 ? 512 : 1024) / G;
-  const int64_t work = rows ? ceil_div(B, bwd ? q.threads / q.lanes : 1) : B * q.tiles;
+  int64_t fit = !rows ? 4 : bwd && q.kind != kNormRowWide && q.threads <= 640 ? 2 : 1;
+  while (!bwd && rows && 2 * fit * q.threads <= 2048) fit *= 2;
+  int64_t most = 256 * fit / G;
   if (most < 1) most = 1;
   if (most > work) most = work;
   q.parts = ceil_div(work, ceil_div(work, most));
