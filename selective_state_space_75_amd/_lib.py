@@ -865,6 +865,17 @@ def _like(x, dtype):
     return torch.empty(x.shape, dtype=dtype, device=x.device)
 
 
+def _apart(y, name, ins, strides):
+    """The caller's y, which must not lie over an input: tiles are read more than once."""
+    lo = y.data_ptr()
+    hi = lo + y.numel() * y.element_size()
+    for t, s in zip(ins, strides):
+        if t is not None and t.numel():
+            at, B = t.data_ptr(), t.shape[0]
+            if at < hi and lo < at + ((B - 1) * s + t.numel() // B) * t.element_size():
+                raise ValueError("%s must not overlap the inputs" % name)
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -943,7 +954,11 @@ def glr_fwd(x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *, blend=Fal
     with _there(dev, stream):
         if y is None:
             y = _like(x, out_dt)
-        yp, last = _plain(y, "y", shape, out_dt, dev), None
+            yp = y.data_ptr()
+        else:
+            yp = _plain(y, "y", shape, out_dt, dev)
+            _apart(y, "y", (x, r, i, z), strides)
+        last = None
         if return_final_state:
             if final_state is None:
                 final_state = torch.empty((B, D), dtype=torch.float32, device=dev)
@@ -1018,7 +1033,11 @@ def glr_update(state, x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *,
     with _there(dev, stream):
         if y is None:
             y = _like(x, out_dt)
-        st = lib().mamba_glr_update(pool, rows, *ins, _plain(y, "y", shape, out_dt, dev), B, D, S, *strides, code,
+            yp = y.data_ptr()
+        else:
+            yp = _plain(y, "y", shape, out_dt, dev)
+            _apart(y, "y", (x, r, i, z), strides)
+        st = lib().mamba_glr_update(pool, rows, *ins, yp, B, D, S, *strides, code,
                                     _dtype_code(y), FLAG_BLEND if blend else 0, _raw_stream(dev, stream))
     if st != 0:
         raise MambaError(st, "mamba_glr_update")
@@ -1062,8 +1081,12 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms
     with _there(dev, stream):
         if y is None:
             y = _like(x, out_dt)
+            yp = y.data_ptr()
+        else:
+            yp = _plain(y, "y", x.shape, out_dt, dev)
+            _apart(y, "y", (x, z), sizes[4:])
         workspace = _workspace(workspace, layer_norm_workspace_size(*sizes[:4]), dev)
-        st = lib().mamba_layer_norm_fwd(*ins, _plain(y, "y", x.shape, out_dt, dev), *sizes, eps, code, _dtype_code(y),
+        st = lib().mamba_layer_norm_fwd(*ins, yp, *sizes, eps, code, _dtype_code(y),
                                         FLAG_RMS if rms else 0, _addr(workspace), _nbytes(workspace),
                                         _raw_stream(dev, stream))
     if st != 0:

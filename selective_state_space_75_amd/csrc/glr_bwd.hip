@@ -14,6 +14,8 @@
 // from the last to the first and c stays with it; few rows have a workgroup per tile, and the first launch
 // (kSummary below, all five inputs) leaves C too.
 // dA and the biases' gradients: a sum per workgroup, then one small launch over batch rows and workgroups of a row.
+// HBM bounds it: 20480 rows, L = 2048, bf16 with both gates, 150 us for 755 MB, 5.0 TB/s; vector instructions take
+// 0.8 of the issue cycles beside that.
 #include "glr.hpp"
 
 namespace mamba {

@@ -410,3 +410,8 @@ def test_refusals_on_the_gpu(dev):
         m.glr_update(torch.zeros(1, 4, device=dev), x[:, :, 0].contiguous(), x[:, :, 0].contiguous(), None, A)
     with pytest.raises(ValueError, match="must be contiguous|dense"):
         m.glr_update(torch.zeros(2, 4, device=dev), x[:, :, 0], x[:, :, 0], None, A)
+    with pytest.raises(ValueError, match="overlap"):
+        m.glr_fwd(x, x.clone(), None, A, y=x)
+    with pytest.raises(ValueError, match="overlap"):
+        q = torch.zeros(2, 4, device=dev)
+        m.glr_update(torch.zeros(2, 4, device=dev), q.clone(), q, None, A, y=q)

@@ -77,3 +77,22 @@ def test_update_in_a_pool_past_32_bit_offsets(dev):
     yr, hr = O.glr(from_dev(x)[..., None], from_dev(r)[..., None], None, from_dev(A), initial_state=h0)
     near(y, yr[..., 0], E, "y")
     near(pool[slots.long()], hr, E, "state")
+
+
+@pytest.mark.parametrize("rows,D,gated", [(1800000, 1300, False), (260000, 9000, True)])
+def test_token_major_norm_past_32_bit_offsets(rows, D, gated, dev):
+    """The last tokens have the bits that they have alone."""
+    import torch
+    import selective_state_space_75_amd as m
+    torch.manual_seed(2)
+    x, dy = (torch.randn(3000, D, device=dev).bfloat16().repeat((rows + 2999) // 3000, 1)[:rows] for _ in range(2))
+    w = torch.randn(D, device=dev)
+    z = dy if gated else None
+    cut = lambda t: None if t is None else t[rows - 3:].contiguous()  # noqa: E731
+    y = m.layer_norm_fwd(x, w, w, z)
+    assert torch.equal(y[rows - 3:], m.layer_norm_fwd(cut(x), w, w, cut(z)))
+    del y
+    g = m.layer_norm_bwd(x, w, w, z, dy)
+    g1 = m.layer_norm_bwd(cut(x), w, w, cut(z), cut(dy))
+    for n in ("dx", "dz"):
+        assert g[n] is None or torch.equal(g[n][rows - 3:], g1[n]), n

@@ -253,3 +253,10 @@ def test_refusals_on_the_gpu(dev):
         m.layer_norm_bwd(x, None, None, None, x, workspace=torch.empty(8, dtype=torch.uint8, device=dev))
     with pytest.raises(ValueError, match="y has shape"):
         m.layer_norm_fwd(x, y=torch.zeros(2, 6, 9, device=dev))
+    with pytest.raises(ValueError, match="overlap"):
+        m.layer_norm_fwd(x, y=x)
+    with pytest.raises(ValueError, match="overlap"):
+        wide = torch.zeros(2, 12, 8, device=dev)
+        m.layer_norm_fwd(wide[:, :6], y=wide.view(-1)[96:].view(2, 6, 8))
+    wide = torch.zeros(1, 12, 8, device=dev)
+    m.layer_norm_fwd(wide[:, :6], y=wide[:, 6:])                # one row: beside it
