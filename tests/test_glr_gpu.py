@@ -157,6 +157,16 @@ def test_backward(B, D, L, dtype, out, blend, with_i, with_z, init, lengths, ran
                 assert g[n] is None or not from_dev(g[n])[b, :, max(0, lengths[b]):].any(), n
 
 
+@pytest.mark.parametrize("with_i,with_z", [(True, True), (False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("blend", [False, True])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+def test_every_split_of_every_type(dtype, out, blend, with_i, with_z, dev):
+    """A wave, 16 waves, segments of few rows, and segments that one workgroup goes through."""
+    for B, D, L, waves in ((2, 3, 301, 0), (1, 2, 8192, 0), (2, 2, 9001, 0), (1, 516, 1203, 1)):
+        for test in (test_forward, test_backward):
+            test(B, D, L, dtype, out, blend, with_i, with_z, True, [L - 5 * b for b in range(B)], False, waves, 0, dev)
+
+
 @pytest.mark.parametrize("with_init,with_final", [(True, False), (False, True)])
 @pytest.mark.parametrize("waves,segments", [(0, 0), (1, 3)])
 def test_one_of_the_two_states(with_init, with_final, waves, segments, dev):

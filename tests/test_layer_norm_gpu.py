@@ -110,6 +110,18 @@ def test_forward_and_backward(shape, groups, dtype, out, gated, rms, affine, ran
         near(g[n], ref[n], 2 * E, n, np.maximum(ref["scale"][n], 1e-30))
 
 
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+def test_every_layout_of_every_type(dtype, out, gated, rms, dev):
+    """One shape for each way that a group is laid out over lanes, waves and launches, the last lanes' tokens and channels
+    their neighbours' too."""
+    for shape in ((2, 100, 41), (1, 200, 70), (1, 400, 37), (1, 900, 33), (1, 1800, 40), (1, 2600, 45), (1, 2600, 300),
+                  (1, 2601, 523), (4, 50, 5), (70, 96), (70, 99), (20, 520), (20, 515), (9, 5000), (5, 7001), (7, 9000),
+                  (5, 9003), (3, 16500), (5, 6)):
+        test_forward_and_backward(shape, 1, dtype, out, gated, rms, True, False, dev)
+
+
 @pytest.mark.parametrize("shape", [(2, 300, 50), (20, 1500), (1, 6000, 20), (3, 12000), (2, 40000)])
 def test_a_large_mean_is_taken_off(shape, dev):
     """Offsets a thousand times the spread: x - mean loses 2^-24 of the offset, 1e3 * 6e-8 = 6e-5 of the
