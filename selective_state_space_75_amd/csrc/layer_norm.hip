@@ -31,6 +31,7 @@ __global__ __launch_bounds__(kThreads) void norm_col_fwd_kernel(NormParams p) {
   const T* x = static_cast<const T*>(p.x) + b * p.x_stride + ch * p.L;
   const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + ch * p.L : nullptr;
   O* y = static_cast<O*>(p.y) + (b * p.D + ch) * p.L;
+  const bool past = past_caches(p.y, p.L * sizeof(O), p.B * p.D * p.L * sizeof(O), sizeof(O) == 2);
 
   Raw8<T> r[kC];
 #pragma unroll
@@ -97,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void norm_col_fwd_kernel(NormParams p) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr[i], j));
         }
-        store8(lane_at(y + (kk + i) * step, at), o, 8, 8);
+        store_all8(lane_at(y + (kk + i) * step, at), o, past);
       }
     }
   }

@@ -1,6 +1,8 @@
 // layer_norm.hpp -- device helpers shared by the layer norm's kernels (gfx950).
 #pragma once
 
+#include <type_traits>
+
 #include "glr.hpp"
 
 namespace mamba {
@@ -122,7 +124,28 @@ __device__ __forceinline__ Raw8<T> load_all8(const T* p) {
 // all the channels of a lane.
 template <typename T>
 __device__ __forceinline__ T* lane_at(T* base, uint32_t v) {
-  return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(base) + (uint32_t)(v * sizeof(T)));
+  using Byte = std::conditional_t<std::is_const_v<T>, const char, char>;
+  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(base) + (uint32_t)(v * sizeof(T)));
+}
+
+// Whether a tile's results go past the caches.  They do where they are whole cache lines, rows being `row` bytes apart.
+// Parts of a line are left to meet the neighbouring tile's in L2 (4 x 5120 channels in 40 groups, L = 1003, fp32: forward
+// 81 us past the caches, 43 through them, backward 92, 64, gated 182, 105), unless a call's results, `all` bytes
+// of them, fit into the 32 MB of the L2s and `few` says that this is faster: 2-byte numbers (8 x 500 channels,
+// L = 2045, gated: 20.0, 24.4, backward 33.0, 35.5) and the gated backward pass (12 heads of 80, 3 x 1003 tokens, fp32:
+// 22.9, 24.8), not ungated fp32 (8 x 200 channels, L = 2045: 12.6, 10.6, backward 20.0, 17.4).
+__device__ __forceinline__ bool past_caches(const void* base, int64_t row, int64_t all, bool few) {
+  return (reinterpret_cast<uintptr_t>(base) | (uint64_t)row) % 128 == 0 || (few && all < (int64_t(32) << 20));
+}
+template <typename O>
+__device__ __forceinline__ void store_all8(O* p, const float (&v)[8], bool past) {
+  if (past) {
+    asm volatile("");                    // without these the compiler makes one plain store of the two
+    store8<O, true>(p, v, 8, 8);
+    asm volatile("");
+  } else {
+    store8<O, false>(p, v, 8, 8);
+  }
 }
 
 // Statistics of one token per lane over the group's channels, fewer than 8 tokens, a workgroup of 256: 32

@@ -21,6 +21,8 @@ __global__ __launch_bounds__(kThreads) void norm_col_bwd_kernel(NormParams p) {
   const int64_t id = by_xcd(blockIdx.x, gridDim.x);
   const int64_t g = id / p.parts, part = id - g * p.parts, ch = g * p.Dg;
   const int Dg = (int)p.Dg, c0 = threadIdx.x / kT;
+  const bool past = past_caches(p.dx, p.L * sizeof(Gr), (kGate ? 2 : 1) * p.B * p.D * p.L * sizeof(Gr),
+                                kGate || sizeof(Gr) == 2);
   for (int c = threadIdx.x; c < Dg; c += kThreads) {
     channel[c] = p.weight ? p.weight[ch + c] : 1.0f;
     channel[Dg + c] = channel[2 * Dg + c] = 0.0f;
@@ -146,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void norm_col_bwd_kernel(NormParams p) {
               o[j] = dm[j] * __builtin_fmaf(xh, w, bias) * s * __builtin_fmaf(zj, 1.0f - s, 1.0f);
               dm[j] *= zj * s;
             }
-            if (on) store8(lane_at(dz + (kk + q) * step, at), o, 8, 8);
+            if (on) store_all8(lane_at(dz + (kk + q) * step, at), o, past);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -156,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void norm_col_bwd_kernel(NormParams p) {
             sw = __builtin_fmaf(one, j < dup ? 0.0f : xh, sw);
             sb += one;
           }
-          if (on) store8(lane_at(dx + (kk + q) * step, at), o, 8, 8);
+          if (on) store_all8(lane_at(dx + (kk + q) * step, at), o, past);
           sw = lane_sum<kT>(sw);
           sb = lane_sum<kT>(sb);
           if (threadIdx.x % kT == 0) {                   // this lane's alone
