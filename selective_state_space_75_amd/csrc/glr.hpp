@@ -62,6 +62,13 @@ __device__ __forceinline__ void put1(uint16_t* p, float x) { *p = f32_to_bf16(x)
 __device__ __forceinline__ float get1(const float* p) { return *p; }
 __device__ __forceinline__ float get1(const uint16_t* p) { return bf16_to_f32(*p); }
 
+// Two numbers rounded by one instruction (halves rounded by themselves take four to put together).
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef float F2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 B2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((F2{lo, hi}), B2));
+}
+
 // Eight consecutive numbers written: the first `live` as they are, up to `n` as zeros.
 template <typename O, bool kNT = true>
 __device__ __forceinline__ void store8(O* p, const float (&v)[8], int live, int n) {
@@ -70,7 +77,7 @@ __device__ __forceinline__ void store8(O* p, const float (&v)[8], int live, int 
     for (int k = 0; k < (int)sizeof(O) / 2; ++k) {
       u32x4 w;
       if constexpr (sizeof(O) == 2) {
-        w = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+        w = u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
       } else {
         w = u32x4{__builtin_bit_cast(uint32_t, v[4 * k]), __builtin_bit_cast(uint32_t, v[4 * k + 1]),
                   __builtin_bit_cast(uint32_t, v[4 * k + 2]), __builtin_bit_cast(uint32_t, v[4 * k + 3])};

@@ -78,17 +78,20 @@ __device__ __forceinline__ void group_sum(float (&v)[kN], float* lds) {
   for (int j = 0; j < kN; ++j) v[j] = total[(lane % kT) * kN + j];
 }
 
-// Sum of kN numbers over a team of 2^k <= 64 neighbouring lanes, or over the workgroup (lds: waves * kN
-// floats), in every lane of it.
-template <int kN, bool kBlock>
+// Sum of kN numbers over a team of 2^k <= 64 neighbouring lanes, or (kWaves) of team / 64 <= 16 whole waves, in every lane
+// of it.  Lane l of a row of 16 reads wave l's sum, so that all waves' come in one round trip to LDS (read one after
+// the other they took a tenth of a token's time with ten waves, and a fifth with 14; for two waves it is the other
+// way round, 1000 channels 18.9 us, 19.8.  kMany: there are more than two).  lds: waves * kN floats.
+template <int kN, bool kWaves, bool kMany = false>
 __device__ __forceinline__ void team_sum(float (&v)[kN], int team, float* lds) {
-  if constexpr (!kBlock) {
+  if constexpr (!kWaves) {
     for (int m = 1; m < team; m *= 2) {
 #pragma unroll
       for (int j = 0; j < kN; ++j) v[j] += __shfl_xor(v[j], m);
     }
   } else {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, w = lane & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int of = team >> 6, first = wave - wave % of;
 #pragma unroll
     for (int j = 0; j < kN; ++j) v[j] = wave_sum63(v[j]);
     __syncthreads();                     // an earlier sum may still be read
@@ -97,11 +100,13 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], int team, float* lds) {
       for (int j = 0; j < kN; ++j) lds[wave * kN + j] = v[j];
     }
     __syncthreads();
+    if (!kMany && of <= 2) {
 #pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] = 0.0f;
-    for (int w = 0; w < waves; ++w) {
+      for (int j = 0; j < kN; ++j) v[j] = lds[first * kN + j] + (of == 2 ? lds[(first + of - 1) * kN + j] : 0.0f);
+    } else {
+      const float* at = lds + (first + (w < of ? w : 0)) * kN;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) v[j] += lds[w * kN + j];
+      for (int j = 0; j < kN; ++j) v[j] = lane_of(row_sum<1>(w < of ? at[j] : 0.0f), 0);
     }
   }
 }
@@ -175,7 +180,7 @@ __device__ __forceinline__ void norm_row_stats(const NormParams& p, const T* x, 
   float v[1] = {0.0f};
   if (!p.rms) {
     for (int64_t c = threadIdx.x; c < p.Dg; c += 256) v[0] += get1(x + c);
-    team_sum<1, true>(v, 256, lds);
+    team_sum<1, true, true>(v, 256, lds);
     v[0] *= p.inv_dg;
   }
   mu = v[0];
@@ -184,7 +189,7 @@ __device__ __forceinline__ void norm_row_stats(const NormParams& p, const T* x, 
     const float d = get1(x + c) - mu;
     v[0] = __builtin_fmaf(d, d, v[0]);
   }
-  team_sum<1, true>(v, 256, lds);
+  team_sum<1, true, true>(v, 256, lds);
   k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
 }
 

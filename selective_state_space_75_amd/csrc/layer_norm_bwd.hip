@@ -228,31 +228,6 @@ __global__ __launch_bounds__(256) void norm_col_long_bwd_kernel(NormParams p) {
   }
 }
 
-// Sum of kN numbers over a team of 2^k <= 64 neighbouring lanes, or of whole waves (lds: waves * kN floats), in every
-// lane of it.
-template <int kN, bool kWaves>
-__device__ __forceinline__ void teams_sum(float (&v)[kN], int team, float* lds) {
-  if constexpr (!kWaves) {
-    team_sum<kN, false>(v, team, lds);
-  } else {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, of = team >> 6, first = wave - wave % of;
-#pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] = wave_sum63(v[j]);
-    __syncthreads();                     // an earlier sum may still be read
-    if (lane == 63) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) lds[wave * kN + j] = v[j];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] = 0.0f;
-    for (int w = first; w < first + of; ++w) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) v[j] += lds[w * kN + j];
-    }
-  }
-}
-
 // Token-major: a workgroup takes a group of channels and every parts-th share of the tokens, one a team at once: of
 // lanes, or (kWaves) of as many waves as the group needs.  8 channels a thread, the last thread the group's last 8
 // whole (see norm_row_fwd_kernel); kRagged: Dg is no multiple of 8.  A token waits for its loads and then for two sums
@@ -315,7 +290,7 @@ __global__ __launch_bounds__(1024) void norm_row_bwd_kernel(NormParams p) {
     if (!p.rms) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) mu[0] += !on || (kRagged && j < dup) ? 0.0f : d[j];
-      teams_sum<1, kWaves>(mu, team, lds);
+      team_sum<1, kWaves>(mu, team, lds);
       mu[0] *= p.inv_dg;
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] -= mu[0];
@@ -332,7 +307,7 @@ __global__ __launch_bounds__(1024) void norm_row_bwd_kernel(NormParams p) {
         v[2] = __builtin_fmaf(gj, dj, v[2]);
       }
     }
-    teams_sum<3, kWaves>(v, team, lds);
+    team_sum<3, kWaves>(v, team, lds);
     // dx = k (g - mean(g) - xh mean(g xh)) with xh = k d
     const float k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
     const float mg = p.rms ? 0.0f : -k * v[1] * p.inv_dg, mx = -k * k * (v[2] * k * p.inv_dg);
@@ -393,7 +368,7 @@ __global__ __launch_bounds__(1024) void norm_row_bwd_kernel(NormParams p) {
 
 // Token-major, groups of 8193 to 16384 channels: a workgroup per token, 2 x 8 channels a thread.  Weights, bias and z
 // come from the caches again for each token: the sums of dw and db, x and dy fill the 128 registers, and with the
-// gate's work beside them the sums live in LDS, a thread's own 32 numbers.
+// gate's work beside them the sums live in LDS, a thread's own 32 numbers (with 4-byte x and z, x comes again too).
 template <typename T, typename Gr, bool kGate>
 __global__ __launch_bounds__(1024) void norm_row_wide_bwd_kernel(NormParams p) {
   __shared__ float lds[3 * 16];
@@ -437,11 +412,14 @@ __global__ __launch_bounds__(1024) void norm_row_wide_bwd_kernel(NormParams p) {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) mu[0] += j < dup[i] ? 0.0f : get8(r[i], j);
-      team_sum<1, true>(mu, 0, lds);
+      team_sum<1, true, true>(mu, blockDim.x, lds);
       mu[0] *= p.inv_dg;
     }
-    keep(r[0]);
-    keep(r[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      keep(r[i]);
+      keep(dr[i]);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       asm("" : "+s"(weight), "+s"(z), "+v"(v[0]));       // loaded piece by piece: not worth registers for longer
@@ -460,18 +438,20 @@ __global__ __launch_bounds__(1024) void norm_row_wide_bwd_kernel(NormParams p) {
         v[2] = __builtin_fmaf(g, d, v[2]);
       }
     }
-    team_sum<3, true>(v, 0, lds);
+    team_sum<3, true, true>(v, blockDim.x, lds);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      keep(r[i]);
+      if constexpr (!kGate || sizeof(T) == 2) keep(r[i]);
       keep(dr[i]);
     }
     const float k = norm_root(__builtin_fmaf(v[0], p.inv_dg, p.eps));
     const float mg = p.rms ? 0.0f : -k * v[1] * p.inv_dg, mx = -k * k * (v[2] * k * p.inv_dg);
+    float last = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      asm("" : "+s"(weight), "+s"(shift), "+s"(z), "+v"(v[1]));
+      asm("" : "+s"(weight), "+s"(shift), "+s"(z), "+s"(x), "+v"(last));
       if (!on[i]) continue;
+      if constexpr (kGate && sizeof(T) == 4) r[i] = load_all8(lane_at(x, c[i]));
       Raw8<float> w;
       if (weight) w = load_all8(lane_at(weight, c[i]));
       float o[8], dm[8];
@@ -499,6 +479,7 @@ __global__ __launch_bounds__(1024) void norm_row_wide_bwd_kernel(NormParams p) {
           sb[i][j] += dm[j];
         }
       }
+      last = o[7];
       store8(lane_at(static_cast<Gr*>(p.dx) + row, c[i]), o, 8, 8);
       if constexpr (kGate) {
 #pragma unroll
@@ -554,7 +535,7 @@ __global__ __launch_bounds__(256) void norm_row_long_bwd_kernel(NormParams p) {
       sg[0] += g;
       sg[1] = __builtin_fmaf(g, (get1(x + c) - mu) * k, sg[1]);
     }
-    team_sum<2, true>(sg, 256, lds);
+    team_sum<2, true, true>(sg, 256, lds);
     sg[0] = p.rms ? 0.0f : sg[0] * p.inv_dg;
     sg[1] *= p.inv_dg;
     for (int64_t c = threadIdx.x; c < p.Dg; c += 256) {
