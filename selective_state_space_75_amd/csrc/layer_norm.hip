@@ -223,7 +223,7 @@ __global__ __launch_bounds__(1024) void norm_row_block_fwd_kernel(NormParams p) 
 #pragma unroll
         for (int j = 0; j < 8; ++j) mu[0] += j < dup[i] ? 0.0f : get8(r[i], j);
       }
-      team_sum<1, true, (kC > 1)>(mu, blockDim.x, lds);
+      team_sum<1, true>(mu, blockDim.x, lds);
       mu[0] *= p.inv_dg;
     }
 #pragma unroll
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(1024) void norm_row_block_fwd_kernel(NormParams p) 
         k[0] = __builtin_fmaf(d, d, k[0]);
       }
     }
-    team_sum<1, true, (kC > 1)>(k, blockDim.x, lds);
+    team_sum<1, true>(k, blockDim.x, lds);
     k[0] = norm_root(__builtin_fmaf(k[0], p.inv_dg, p.eps));
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
