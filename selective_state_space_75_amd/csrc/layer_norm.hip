@@ -6,7 +6,10 @@
 //
 // Channel-major (L > 1): channels are L apart, so a thread takes 8 consecutive tokens (one load) of every
 // CL-th channel, neighbouring lanes the tokens after them, and the sums run over a workgroup's CL channel
-// lanes.  Token-major (L = 1): a row's channels lie together; a thread takes 8 of them.
+// lanes.  Groups too large for that go through layer_norm_two.hpp.  Token-major (L = 1): a row's channels lie
+// together; a thread takes 8 of them.
+// bf16: 4 x 5120 channels in 40 groups, L = 2048: 30 us, 8192 token-major rows of 5120: 33 us (HBM: 33); in one
+// group, channel-major: 43 us in two launches.  128 rows of 5120 channels: 4 us on the GPU, one token's latency.
 #include "layer_norm_two.hpp"
 
 namespace mamba {
@@ -169,7 +172,9 @@ __global__ __launch_bounds__(256) void norm_row_fwd_kernel(NormParams p) {
 
 // Token-major, a workgroup of the group's width, kC times 8 channels a thread: it takes every parts-th token, keeps
 // the weights (8 bytes a channel, twice what a token's bf16 x and y are), and has the next token's x and z loaded
-// while one is worked on.
+// while one is worked on (8192 rows of 5120 channels, bf16: 33 us, a workgroup per token 43; of 10240 channels: 65).
+// The sums keep team_sum's branch for two waves where there are never so few: it ends the scheduler's block in front
+// of the sum, and the loads ahead stay early (79 without it).
 template <typename T, typename O, bool kGate, int kC>
 __global__ __launch_bounds__(1024) void norm_row_block_fwd_kernel(NormParams p) {
   __shared__ float lds[16];
@@ -379,11 +384,13 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     return q;
   }
   // Backward, workgroups that fill the chip and no more: every part of the weight's sums is written and read.
-  // Token-major that is one a CU, or two where two of them fit (a group's one team of up to 640 threads: 8192 tokens of
-  // 5120 channels, bf16, 68 us, with one 93; of 512 channels, where one workgroup holds 1024 threads, 18 us with two
-  // and 14 with one).  Forward (kNormRowBlock, kNormRowWide) a CU gets the power of two that makes up to 2048
-  // threads: two workgroups of 640 for 5120 channels 33 us, three 38; two of 896 for 7168 channels 51 us, one 68.
-  int64_t fit = !rows ? 4 : bwd && q.kind != kNormRowWide && q.threads <= 640 ? 2 : 1;
+  // Token-major that is one a CU, or two where the registers hold two (a group's one team of up to 640 threads, no gate,
+  // 2-byte numbers: 8192 tokens of 5120 channels, bf16, 66 us, with one 76; fp32 110, 105; gated 109, 108; of 512
+  // channels, where one workgroup holds 1024 threads, 17.5, 13.6; of 7168, 99, 92).  Forward (kNormRowBlock,
+  // kNormRowWide) a CU gets the power of two that makes up to 2048 threads: two workgroups of 640 for 5120 channels
+  // 33 us, three 38; two of 896 for 7168 channels 51 us, one 68.
+  const bool two = q.kind == kNormRowBlock && q.threads <= 640 && !gate && in_width + grad_width == 4;
+  int64_t fit = !rows ? 4 : bwd && two ? 2 : 1;
   while (!bwd && rows && 2 * fit * q.threads <= 2048) fit *= 2;
   int64_t most = 256 * fit / G;
   if (most < 1) most = 1;
