@@ -41,6 +41,7 @@ struct GlrPlan {
   int64_t S = 1, seg_len = 0;
   int64_t group = 1, groups = 1;                // backward: segments of a workgroup, workgroups of a row
   int waves = 1;
+  int lanes = 0;                                // short rows: lanes of a row, several rows a wave
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -49,6 +50,16 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 void cut(GlrPlan& q, int64_t L, int64_t S) {
   q.seg_len = ceil_div(ceil_div(L, S), mamba::kGlrLane) * mamba::kGlrLane;
   q.S = ceil_div(L, q.seg_len);
+}
+
+// Short rows go several to a wave (unless a test asks for waves or segments).  Forward and backward, us, against a
+// wave a row: SHORTFIGS
+constexpr int64_t kShort = 256;
+bool short_rows(GlrPlan& q, int64_t L) {
+  if (L > kShort || g_waves.load() > 0 || g_segments.load() > 0) return false;
+  cut(q, L, 1);
+  for (q.lanes = 1; q.lanes * mamba::kGlrLane < L;) q.lanes *= 2;
+  return true;
 }
 
 // Sizes-only plan of the forward pass: waves per row, and segments of L.
@@ -62,6 +73,7 @@ void cut(GlrPlan& q, int64_t L, int64_t S) {
 // 512 rows: 38.3, 54.8 (4).
 GlrPlan make_glr_plan(int64_t B, int64_t D, int64_t L) {
   GlrPlan q;
+  if (short_rows(q, L)) return q;
   const int64_t rows = B * D, tiles = ceil_div(L, mamba::kGlrWave);
   int64_t waves = tiles <= 2 && rows >= 4096 ? 1 : 16, S = 1;
   if (rows <= 128 && tiles >= 16) {
@@ -86,6 +98,7 @@ GlrPlan make_glr_plan(int64_t B, int64_t D, int64_t L) {
 // 50, 49.
 GlrPlan make_glr_bwd_plan(int64_t B, int64_t D, int64_t L) {
   GlrPlan q;
+  if (short_rows(q, L)) return q;
   const int forced = g_waves.load();
   const bool many = B * D >= 512;
   const int64_t waves = forced > 0 ? forced : L <= 16 * mamba::kGlrWave ? 16 : many ? 4 : 8;
@@ -234,7 +247,7 @@ int mamba_glr_fwd(const void* x, const void* r, const void* i, const void* z, co
   const size_t need = glr_bytes(q, B, D);
   if (need && (!workspace || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
   if (need && !aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
-  p.S = q.S; p.seg_len = q.seg_len; p.waves = q.waves;
+  p.S = q.S; p.seg_len = q.seg_len; p.waves = q.waves; p.lanes = q.lanes;
   p.sum = static_cast<float*>(workspace);
   return status_of(mamba::launch_glr_fwd(p, dt_of(in_dtype), dt_of(out_dtype), stream));
 }
@@ -279,7 +292,7 @@ int mamba_glr_bwd(const void* x, const void* r, const void* i, const void* z, co
   const size_t need = glr_bwd_bytes(q, B, D);
   if (!workspace || workspace_bytes < need) return MAMBA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MAMBA_ERR_ALIGN;
-  p.S = q.S; p.seg_len = q.seg_len; p.waves = q.waves; p.group = q.group; p.groups = q.groups;
+  p.S = q.S; p.seg_len = q.seg_len; p.waves = q.waves; p.lanes = q.lanes; p.group = q.group; p.groups = q.groups;
   p.sum = static_cast<float*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + glr_bwd_sum_bytes(q, B, D));
   p.dy = dy; p.dfinal = dfinal_state;

@@ -186,6 +186,7 @@ hipError_t upd_t(const GlrParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_glr_fwd(const GlrParams& p, Dt in, Dt out, hipStream_t s) {
+  if (p.lanes) return launch_glr_short_fwd(p, in, out, s);
   if (in == Dt::BF16) return out == Dt::BF16 ? fwd_t<uint16_t, uint16_t>(p, s) : fwd_t<uint16_t, float>(p, s);
   return out == Dt::BF16 ? fwd_t<float, uint16_t>(p, s) : fwd_t<float, float>(p, s);
 }

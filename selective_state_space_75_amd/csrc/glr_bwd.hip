@@ -239,9 +239,6 @@ hipError_t bwd_n(const GlrParams& p, hipStream_t s) {
   } else {
     hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, false, kThreads>), grid, block, 0, s, p);
   }
-  e = hipGetLastError();
-  if (e != hipSuccess || p.B * p.groups == 1) return e;
-  hipLaunchKernelGGL(glr_sum_kernel, dim3((unsigned)(3 * ((p.D + 15) / 16))), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -254,8 +251,13 @@ hipError_t bwd_t(const GlrParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_glr_bwd(const GlrParams& p, Dt in, Dt grad, hipStream_t s) {
-  if (in == Dt::BF16) return grad == Dt::BF16 ? bwd_t<uint16_t, uint16_t>(p, s) : bwd_t<uint16_t, float>(p, s);
-  return grad == Dt::BF16 ? bwd_t<float, uint16_t>(p, s) : bwd_t<float, float>(p, s);
+  hipError_t e;
+  if (p.lanes) e = launch_glr_short_bwd(p, in, grad, s);
+  else if (in == Dt::BF16) e = grad == Dt::BF16 ? bwd_t<uint16_t, uint16_t>(p, s) : bwd_t<uint16_t, float>(p, s);
+  else e = grad == Dt::BF16 ? bwd_t<float, uint16_t>(p, s) : bwd_t<float, float>(p, s);
+  if (e != hipSuccess || p.B * p.groups == 1) return e;
+  hipLaunchKernelGGL(glr_sum_kernel, dim3((unsigned)(3 * ((p.D + 15) / 16))), dim3(256), 0, s, p);
+  return hipGetLastError();
 }
 
 }  // namespace mamba

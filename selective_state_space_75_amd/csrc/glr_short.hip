@@ -1,0 +1,268 @@
+// glr_short.hip -- the gated linear recurrence over short rows, forward and backward (gfx950).
+//
+// The mathematics of glr.hip and glr_bwd.hip, with several rows in a wave: a row has `p.lanes` neighbouring lanes (a power
+// of two, 8 tokens each), scans and sums run over those, and a workgroup of four waves takes 256 / lanes rows.
+// A wave per row would leave most lanes without a token, and the chip waiting for workgroups that do next to nothing.
+// The last lane of a row of 8 tokens or more takes its last 8 with one load; those that the lane before it has too (the
+// first `lo`) are left out there like tokens behind the row's end: s = 0, a = 1, and zeros in the other inputs.
+#include "glr.hpp"
+
+namespace mamba {
+namespace {
+
+// A lane's share of a row.
+struct Share {
+  int64_t b, d, row, t;         // its 8 tokens begin at t
+  int sub, lo, there, live;     // lane of the row; its own tokens are lo .. lo + there, the first `live` of them count
+  uint32_t on;                  // a bit for each token that counts
+  bool mine;                    // there is such a row
+};
+
+__device__ __forceinline__ Share glr_share(const GlrParams& p) {
+  Share o;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = p.B * p.D;
+  o.row = id / p.lanes;
+  o.sub = threadIdx.x & (p.lanes - 1);
+  o.mine = o.row < rows;
+  if (!o.mine) o.row = rows - 1;
+  o.b = o.row / p.D;
+  o.d = o.row - o.b * p.D;
+  const int64_t first = o.sub * kGlrLane, last = p.L - kGlrLane, len = glr_length(p, o.b);
+  o.t = last < 0 ? 0 : first < last ? first : last;
+  o.there = o.mine ? clamp8(p.L - first) : 0;
+  o.lo = o.there ? (int)(first - o.t) : 0;
+  o.live = o.there < clamp8(len - first) ? o.there : clamp8(len - first);
+  o.on = ((1u << o.live) - 1) << o.lo;
+  return o;
+}
+
+// The lane's 8 tokens of a row of n, `dead` (its bits) in the place of those that do not count.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_share(const T* row, int64_t n, const Share& q, uint32_t dead) {
+  Raw8<T> o;
+  if (n >= 8) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) o.w[k] = *(reinterpret_cast<const u32x4_u*>(row + q.t) + k);
+  } else {
+    o = load_raw8(row, (int)n);
+  }
+  if (q.on != 0xff) {
+#pragma unroll
+    for (int j = 0; j < 4 * (int)sizeof(T); j += 2) {
+      const int e = sizeof(T) == 2 ? j : j / 2;          // the word's first (or only) token
+      uint32_t w = o.w[j / 8][j / 2 & 3];
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t m = (q.on >> e & 1 ? 0xffffu : 0u) | (q.on >> (e + 1) & 1 ? 0xffff0000u : 0u);
+        w = (w & m) | (dead & ~m);
+      } else {
+        w = q.on >> e & 1 ? w : dead;
+      }
+      o.w[j / 8][j / 2 & 3] = w;
+    }
+  }
+  return o;
+}
+template <typename T>
+constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+
+// The lane's own tokens, zeros for those that do not count.
+template <typename O>
+__device__ __forceinline__ void store_share(O* row, const float (&v)[8], const Share& q) {
+  if (q.lo == 0) {
+    store8<O, false>(row + q.t, v, q.live, q.there);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j >= q.lo) put1(row + q.t + j, j < q.lo + q.live ? v[j] : 0.0f);
+  }
+}
+
+// (P, H) of the row's lanes up to this one, and from this one on (composed from the last to the first).
+__device__ __forceinline__ Affine share_up(Affine v, int sub, int lanes) {
+  for (int m = 1; m < lanes; m *= 2) {
+    const float P = __shfl_up(v.P, m), H = __shfl_up(v.H, m);
+    if (sub >= m) {
+      v.H = __builtin_fmaf(v.P, H, v.H);
+      v.P *= P;
+    }
+  }
+  return v;
+}
+__device__ __forceinline__ Affine share_down(Affine v, int sub, int lanes) {
+  for (int m = 1; m < lanes; m *= 2) {
+    const float P = __shfl_down(v.P, m), H = __shfl_down(v.H, m);
+    if (sub + m < lanes) {
+      v.H = __builtin_fmaf(v.P, H, v.H);
+      v.P *= P;
+    }
+  }
+  return v;
+}
+
+template <typename T, typename O, bool kBlend>
+__global__ __launch_bounds__(256) void glr_short_fwd_kernel(GlrParams p) {
+  const Share q = glr_share(p);
+  const int64_t at = q.d * p.L;
+  const Raw8<T> xr = load_share(static_cast<const T*>(p.x) + q.b * p.x_stride + at, p.L, q, 0);
+  const Raw8<T> rr = load_share(static_cast<const T*>(p.r) + q.b * p.r_stride + at, p.L, q, kMinusInf<T>);
+  Raw8<T> ir, zr;
+  if (p.i) ir = load_share(static_cast<const T*>(p.i) + q.b * p.i_stride + at, p.L, q, 0);
+  if (p.z) zr = load_share(static_cast<const T*>(p.z) + q.b * p.z_stride + at, p.L, q, 0);
+  const float A2 = kBlend ? 0.0f : p.A[q.d] * kLog2e;
+  const float rb = p.r_bias ? -p.r_bias[q.d] * kLog2e : 0.0f, ib = p.i_bias ? -p.i_bias[q.d] * kLog2e : 0.0f;
+  const float before = p.init ? p.init[q.row] : 0.0f;
+  float a[8], u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const GlrGate g = glr_gate<kBlend>(get8(rr, j), rb, A2);
+    a[j] = g.a;
+    u[j] = g.n * get8(xr, j);
+  }
+  if (p.i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] *= hw_rcp(1.0f + hw_exp2(__builtin_fmaf(get8(ir, j), -kLog2e, ib)));
+  }
+  Affine v;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v.P *= a[j];
+    v.H = __builtin_fmaf(a[j], v.H, u[j]);
+  }
+  v = share_up(v, q.sub, p.lanes);
+  Affine front{__shfl_up(v.P, 1), __shfl_up(v.H, 1)};
+  if (q.sub == 0) front = Affine{};
+  float h = __builtin_fmaf(front.P, before, front.H), o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    h = __builtin_fmaf(a[j], h, u[j]);
+    o[j] = h;
+  }
+  if (p.z) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr, j));
+  }
+  store_share(static_cast<O*>(p.y) + q.row * p.L, o, q);
+  if (p.final_state && q.mine && q.sub == p.lanes - 1) p.final_state[q.row] = __builtin_fmaf(v.P, before, v.H);
+}
+
+template <typename T, typename Gr, bool kBlend>
+__global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
+  const Share q = glr_share(p);
+  const int64_t at = q.d * p.L, out = q.row * p.L;
+  Raw8<T> xr = load_share(static_cast<const T*>(p.x) + q.b * p.x_stride + at, p.L, q, 0);
+  const Raw8<T> rr = load_share(static_cast<const T*>(p.r) + q.b * p.r_stride + at, p.L, q, kMinusInf<T>);
+  Raw8<Gr> yr = load_share(static_cast<const Gr*>(p.dy) + out, p.L, q, 0);
+  Raw8<T> ir, zr;
+  if (p.i) ir = load_share(static_cast<const T*>(p.i) + q.b * p.i_stride + at, p.L, q, 0);
+  if (p.z) zr = load_share(static_cast<const T*>(p.z) + q.b * p.z_stride + at, p.L, q, 0);
+  const float A = kBlend ? 0.0f : p.A[q.d], A2 = A * kLog2e;
+  const float rb = p.r_bias ? -p.r_bias[q.d] * kLog2e : 0.0f, ib = p.i_bias ? -p.i_bias[q.d] * kLog2e : 0.0f;
+  const float before = p.init ? p.init[q.row] : 0.0f, after = p.dfinal ? p.dfinal[q.row] : 0.0f;
+  float a[8], n[8], s[8], ra[8], g[8], e[8], sz[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const GlrGate k = glr_gate<kBlend>(get8(rr, j), rb, A2);
+    a[j] = k.a; n[j] = k.n; s[j] = k.s; ra[j] = k.ra;
+    g[j] = p.i ? hw_rcp(1.0f + hw_exp2(__builtin_fmaf(get8(ir, j), -kLog2e, ib))) : 1.0f;
+    sz[j] = p.z ? sigmoid(get8(zr, j)) : 1.0f;
+    e[j] = get8(yr, j);
+    if (p.z) e[j] *= get8(zr, j) * sz[j];
+  }
+  Affine f, k;                                 // forwards and backwards over the lane's tokens
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    f.P *= a[j];
+    f.H = __builtin_fmaf(a[j], f.H, n[j] * g[j] * get8(xr, j));
+  }
+#pragma unroll
+  for (int j = 7; j >= 0; --j) k.H = a[j] * (k.H + e[j]);
+  k.P = f.P;
+  f = share_up(f, q.sub, p.lanes);
+  k = share_down(k, q.sub, p.lanes);
+  Affine front{__shfl_up(f.P, 1), __shfl_up(f.H, 1)}, behind{__shfl_down(k.P, 1), __shfl_down(k.H, 1)};
+  if (q.sub == 0) front = Affine{};
+  if (q.sub == p.lanes - 1) behind = Affine{};
+  float h = __builtin_fmaf(front.P, before, front.H), c = __builtin_fmaf(behind.P, after, behind.H);
+  if (p.dinit && q.mine && q.sub == 0) p.dinit[q.row] = __builtin_fmaf(k.P, after, k.H);
+  float hp[8], o[8];                           // hp: state in front of each token
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    hp[j] = h;
+    h = __builtin_fmaf(a[j], h, n[j] * g[j] * get8(xr, j));
+  }
+  if (p.z) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float hj = j < 7 ? hp[j < 7 ? j + 1 : 7] : h;
+      o[j] = get8(yr, j) * hj * sz[j] * __builtin_fmaf(get8(zr, j), 1.0f - sz[j], 1.0f);
+    }
+    store_share(static_cast<Gr*>(p.dz) + out, o, q);
+  }
+  float dr[8], sums[3] = {0.0f, 0.0f, 0.0f};   // of A, r_bias, i_bias
+#pragma unroll
+  for (int j = 7; j >= 0; --j) {
+    const float y = e[j] + c, gx = g[j] * get8(xr, j);
+    c = a[j] * y;
+    o[j] = y * n[j] * g[j];
+    if constexpr (kBlend) {
+      dr[j] = y * (gx - hp[j]) * s[j] * a[j];
+    } else {
+      const float ds = y * __builtin_fmaf(a[j], hp[j], -gx * ra[j]) * s[j];
+      sums[0] += ds;
+      dr[j] = ds * A * (1.0f - s[j]);
+    }
+    sums[1] += dr[j];
+  }
+  store_share(static_cast<Gr*>(p.dx) + out, o, q);
+  store_share(static_cast<Gr*>(p.dr) + out, dr, q);
+  if (p.i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      o[j] *= get8(xr, j) * (1.0f - g[j]);
+      sums[2] += o[j];
+    }
+    store_share(static_cast<Gr*>(p.di) + out, o, q);
+  }
+  for (int m = 1; m < p.lanes; m *= 2) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) sums[j] += __shfl_xor(sums[j], m);
+  }
+  if (q.sub || !q.mine) return;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    float* dst = p.B > 1 ? p.part + (q.b * 3 + j) * p.D : j == 0 ? p.dA : j == 1 ? p.dr_bias : p.di_bias;
+    if (dst) dst[q.d] = sums[j];
+  }
+}
+
+template <typename T, typename O, bool kBlend>
+hipError_t fwd_b(const GlrParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((glr_short_fwd_kernel<T, O, kBlend>), dim3((unsigned)((p.B * p.D * p.lanes + 255) / 256)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+template <typename T, typename O>
+hipError_t fwd_t(const GlrParams& p, hipStream_t s) {
+  return p.blend ? fwd_b<T, O, true>(p, s) : fwd_b<T, O, false>(p, s);
+}
+template <typename T, typename Gr, bool kBlend>
+hipError_t bwd_b(const GlrParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((glr_short_bwd_kernel<T, Gr, kBlend>), dim3((unsigned)((p.B * p.D * p.lanes + 255) / 256)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+template <typename T, typename Gr>
+hipError_t bwd_t(const GlrParams& p, hipStream_t s) {
+  return p.blend ? bwd_b<T, Gr, true>(p, s) : bwd_b<T, Gr, false>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_glr_short_fwd(const GlrParams& p, Dt in, Dt out, hipStream_t s) {
+  if (in == Dt::BF16) return out == Dt::BF16 ? fwd_t<uint16_t, uint16_t>(p, s) : fwd_t<uint16_t, float>(p, s);
+  return out == Dt::BF16 ? fwd_t<float, uint16_t>(p, s) : fwd_t<float, float>(p, s);
+}
+hipError_t launch_glr_short_bwd(const GlrParams& p, Dt in, Dt grad, hipStream_t s) {
+  if (in == Dt::BF16) return grad == Dt::BF16 ? bwd_t<uint16_t, uint16_t>(p, s) : bwd_t<uint16_t, float>(p, s);
+  return grad == Dt::BF16 ? bwd_t<float, uint16_t>(p, s) : bwd_t<float, float>(p, s);
+}
+
+}  // namespace mamba

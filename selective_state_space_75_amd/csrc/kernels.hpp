@@ -235,6 +235,7 @@ struct GlrParams {
   int64_t x_stride, r_stride, i_stride, z_stride;   // elements from one batch row to the next
   int64_t S, seg_len;                           // segments of L, a multiple of 8 tokens each
   int waves;                                    // waves of a workgroup: 512 tokens of a row each at a time
+  int lanes;                                    // > 0: a short row's lanes, several rows a wave
   int blend;
   float* sum;                                   // S > 1: (rows, S, 2) P and H of each segment (backward, groups > 1: (rows, S, 3), and C)
   // backward pass
@@ -343,6 +344,8 @@ hipError_t launch_gdr_prep(const GdrChunkParams& p, Dt in, Dt grad, bool bwd, hi
 hipError_t launch_gdr_states(const GdrChunkParams& p, Dt in, hipStream_t s);
 hipError_t launch_gdr_bwd(const GdrChunkParams& p, Dt in, Dt grad, hipStream_t s);
 hipError_t launch_glr_fwd(const GlrParams& p, Dt in, Dt out, hipStream_t s);
+hipError_t launch_glr_short_fwd(const GlrParams& p, Dt in, Dt out, hipStream_t s);    // p.lanes > 0
+hipError_t launch_glr_short_bwd(const GlrParams& p, Dt in, Dt grad, hipStream_t s);
 hipError_t launch_glr_summary(const GlrParams& p, Dt in, hipStream_t s);
 hipError_t launch_glr_update(const GlrParams& p, Dt in, Dt out, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrParams& p, Dt in, Dt grad, hipStream_t s);
