@@ -18,8 +18,11 @@
 namespace mamba {
 namespace {
 
-// kSummary: only the (P, H) of each segment but the last.
-template <typename T, typename O, bool kBlend, bool kSummary>
+// kSummary: only the (P, H) of each segment but the last.  kEdge: rows whose last lane has four to seven tokens, through
+// Share (32768 rows of 333 tokens, bf16: 60 us without, 41 with it).  With fewer tokens there the lane's own loads cost
+// no more (7680 rows of 1003 tokens: 22.3, 23.4), nor do 4-byte ones (333 tokens: 47, 54), and past 8 waves Share's
+// registers cost two workgroups of 16 waves their place on a CU (16381 tokens: 118, 131).
+template <typename T, typename O, bool kBlend, bool kSummary, bool kEdge>
 __global__ __launch_bounds__(1024) void glr_fwd_kernel(GlrParams p) {
   __shared__ float totals[2][2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -47,17 +50,23 @@ __global__ __launch_bounds__(1024) void glr_fwd_kernel(GlrParams p) {
   int turn = 0;
   for (int64_t tile = t0; tile < t1; tile += (int64_t)waves * kGlrWave, turn ^= 1) {
     const int64_t t = tile + (int64_t)threadIdx.x * kGlrLane;
+    Share q;
     const int live = clamp8((len < t1 ? len : t1) - t);
-    const Raw8<T> xr = load_raw8(x + t, live), rr = load_raw8(r + t, live);
+    if constexpr (kEdge) q = glr_share(p.L, t1, len, t);
+    auto load = [&](const T* from, uint32_t dead) {
+      if constexpr (kEdge) return load_share(from, p.L, q, dead);
+      else return load_raw8(from + t, live);
+    };
+    const Raw8<T> xr = load(x, 0), rr = load(r, kMinusInf<T>);
     Raw8<T> ir, zr;
-    if (ig) ir = load_raw8(ig + t, live);
+    if (ig) ir = load(ig, 0);
     if constexpr (!kSummary)
-      if (z) zr = load_raw8(z + t, live);
+      if (z) zr = load(z, 0);
     float a[8], u[8];
     Affine v;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const GlrGate g = glr_gate<kBlend>(glr_r(rr, j, live), rb, A2);
+      const GlrGate g = glr_gate<kBlend>(kEdge ? get8(rr, j) : glr_r(rr, j, live), rb, A2);
       a[j] = g.a;
       u[j] = g.n * get8(xr, j);
     }
@@ -104,7 +113,8 @@ __global__ __launch_bounds__(1024) void glr_fwd_kernel(GlrParams p) {
       }
       // Past the caches where whole lines are written at once; 4-byte outputs take two stores a line.  20480 rows,
       // L = 2048, fp32 out: 94.8 us past the caches, 89.6 through them; 4096 rows, L = 32768, bf16: 250, 260.
-      store8<O, sizeof(O) == 2>(y + t, o, live, clamp8(t1 - t));
+      if constexpr (kEdge) store_share<O, sizeof(O) == 2>(y, o, q);
+      else store8<O, sizeof(O) == 2>(y + t, o, live, clamp8(t1 - t));
       carry = __builtin_fmaf(tile_total.P, carry, tile_total.H);
     }
   }
@@ -154,8 +164,8 @@ __global__ __launch_bounds__(256) void glr_update_kernel(GlrParams p) {
 template <typename T>
 hipError_t summary_t(const GlrParams& p, hipStream_t s) {
   const dim3 grid((unsigned)(p.B * p.D * (p.S - 1))), block(64u * p.waves);
-  if (p.blend) hipLaunchKernelGGL((glr_fwd_kernel<T, T, true, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((glr_fwd_kernel<T, T, false, true>), grid, block, 0, s, p);
+  if (p.blend) hipLaunchKernelGGL((glr_fwd_kernel<T, T, true, true, false>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((glr_fwd_kernel<T, T, false, true, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -166,7 +176,13 @@ hipError_t fwd_b(const GlrParams& p, hipStream_t s) {
     const hipError_t e = summary_t<T>(p, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((glr_fwd_kernel<T, O, kBlend, false>), dim3(rows * (unsigned)p.S), dim3(threads), 0, s, p);
+  if constexpr (sizeof(T) == 2) {
+    if (p.L % kGlrLane > 3 && p.waves <= 8) {
+      hipLaunchKernelGGL((glr_fwd_kernel<T, O, kBlend, false, true>), dim3(rows * (unsigned)p.S), dim3(threads), 0, s, p);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((glr_fwd_kernel<T, O, kBlend, false, false>), dim3(rows * (unsigned)p.S), dim3(threads), 0, s, p);
   return hipGetLastError();
 }
 

@@ -21,8 +21,9 @@
 namespace mamba {
 namespace {
 
-// kSummary: only the (P, H, C) of each tile.  kLoop: more than one tile a workgroup.
-template <typename T, typename Gr, bool kBlend, bool kSummary, bool kLoop, int kThreads>
+// kSummary: only the (P, H, C) of each tile.  kLoop: more than one tile a workgroup.  kEdge: rows that do not end with a
+// whole lane, through Share (the others go without its registers: 20480 rows, L = 2048, bf16: 148 us, with it 168).
+template <typename T, typename Gr, bool kBlend, bool kSummary, bool kLoop, bool kEdge, int kThreads>
 __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
   __shared__ float totals[2][3][16];
   __shared__ float sums[3][16];
@@ -59,17 +60,23 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
     const int64_t t0 = seg * p.seg_len;
     const int64_t t1 = p.L - t0 < p.seg_len ? p.L : t0 + p.seg_len;
     const int64_t t = t0 + (int64_t)threadIdx.x * kGlrLane;
+    Share q;
     const int live = clamp8((len < t1 ? len : t1) - t);
-    Raw8<T> xr = load_raw8(x + t, live), rr = load_raw8(r + t, live);
-    Raw8<Gr> yr = load_raw8(dy + t, live);
+    if constexpr (kEdge) q = glr_share(p.L, t1, len, t);
+    auto load = [&](const auto* from, uint32_t dead) {
+      if constexpr (kEdge) return load_share(from, p.L, q, dead);
+      else return load_raw8(from + t, live);
+    };
+    Raw8<T> xr = load(x, 0), rr = load(r, kMinusInf<T>);
+    Raw8<Gr> yr = load(dy, 0);
     Raw8<T> ir, zr;
-    if (ig) ir = load_raw8(ig + t, live);
-    if (zg) zr = load_raw8(zg + t, live);
+    if (ig) ir = load(ig, 0);
+    if (zg) zr = load(zg, 0);
 
     float a[8], n[8], s[8], ra[8], g[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const GlrGate k = glr_gate<kBlend>(glr_r(rr, j, live), rb, A2);
+      const GlrGate k = glr_gate<kBlend>(kEdge ? get8(rr, j) : glr_r(rr, j, live), rb, A2);
       a[j] = k.a; n[j] = k.n; s[j] = k.s; ra[j] = k.ra;
     }
     if (ig) {
@@ -136,7 +143,11 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
     c = __builtin_fmaf(ke.P, c, ke.H);
 
     const int there = clamp8(t1 - t);
-    const int64_t at = row * p.L + t;
+    const int64_t at = row * p.L + (kEdge ? 0 : t);
+    auto store = [&](void* to, const float (&v)[8]) {
+      if constexpr (kEdge) store_share<Gr, true>(static_cast<Gr*>(to) + at, v, q);
+      else store8(static_cast<Gr*>(to) + at, v, live, there);
+    };
     float hp[8];                               // state in front of each token
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -150,33 +161,33 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
         const float hj = j < 7 ? hp[j < 7 ? j + 1 : 7] : h;
         o[j] = get8(yr, j) * hj * sz[j] * __builtin_fmaf(get8(zr, j), 1.0f - sz[j], 1.0f);
       }
-      store8(static_cast<Gr*>(p.dz) + at, o, live, there);
+      store(p.dz, o);
     }
     float dx[8], dr[8];
 #pragma unroll
     for (int j = 7; j >= 0; --j) {
-      const float q = e[j] + c;
-      c = a[j] * q;
-      dx[j] = q * n[j] * g[j];
+      const float v = e[j] + c;
+      c = a[j] * v;
+      dx[j] = v * n[j] * g[j];
       const float gx = g[j] * get8(xr, j);
       if constexpr (kBlend) {
-        dr[j] = q * (gx - hp[j]) * s[j] * a[j];
+        dr[j] = v * (gx - hp[j]) * s[j] * a[j];
       } else {
-        const float ds = q * __builtin_fmaf(a[j], hp[j], -gx * ra[j]) * s[j];
+        const float ds = v * __builtin_fmaf(a[j], hp[j], -gx * ra[j]) * s[j];
         sA += ds;
         dr[j] = ds * A * (1.0f - s[j]);
       }
       sr += dr[j];
     }
-    store8(static_cast<Gr*>(p.dx) + at, dx, live, there);
-    store8(static_cast<Gr*>(p.dr) + at, dr, live, there);
+    store(p.dx, dx);
+    store(p.dr, dr);
     if (ig) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dx[j] *= get8(xr, j) * (1.0f - g[j]);
         si += dx[j];
       }
-      store8(static_cast<Gr*>(p.di) + at, dx, live, there);
+      store(p.di, dx);
     }
   }
   if constexpr (kSummary) return;
@@ -219,7 +230,7 @@ __global__ __launch_bounds__(256) void glr_sum_kernel(GlrParams p) {
   if (dst) dst[d] = o;
 }
 
-template <typename T, typename Gr, bool kBlend, int kThreads>
+template <typename T, typename Gr, bool kBlend, bool kEdge, int kThreads>
 hipError_t bwd_n(const GlrParams& p, hipStream_t s) {
   const unsigned rows = (unsigned)(p.B * p.D);
   const dim3 block(64u * p.waves), grid(rows * (unsigned)p.groups);
@@ -227,25 +238,30 @@ hipError_t bwd_n(const GlrParams& p, hipStream_t s) {
   if (p.groups > 1) {
     GlrParams one = p;
     one.group = 1;
-    hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, true, false, kThreads>), dim3(rows * (unsigned)p.S), block, 0, s, one);
+    hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, true, false, kEdge, kThreads>), dim3(rows * (unsigned)p.S), block, 0, s, one);
     e = hipGetLastError();
   } else if (p.S > 1) {
     e = launch_glr_summary(p, sizeof(T) == 2 ? Dt::BF16 : Dt::F32, s);
   }
   if (e != hipSuccess) return e;
   if constexpr (kThreads == 512) {             // more waves are only taken for one tile
-    if (p.group > 1) hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, true, 512>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, false, 512>), grid, block, 0, s, p);
+    if (p.group > 1) hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, true, kEdge, 512>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, false, kEdge, 512>), grid, block, 0, s, p);
   } else {
-    hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, false, kThreads>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((glr_bwd_kernel<T, Gr, kBlend, false, false, kEdge, kThreads>), grid, block, 0, s, p);
   }
   return hipGetLastError();
 }
 
+template <typename T, typename Gr, int kThreads>
+hipError_t bwd_e(const GlrParams& p, hipStream_t s) {
+  if (p.L % kGlrLane) return p.blend ? bwd_n<T, Gr, true, true, kThreads>(p, s) : bwd_n<T, Gr, false, true, kThreads>(p, s);
+  return p.blend ? bwd_n<T, Gr, true, false, kThreads>(p, s) : bwd_n<T, Gr, false, false, kThreads>(p, s);
+}
+
 template <typename T, typename Gr>
 hipError_t bwd_t(const GlrParams& p, hipStream_t s) {
-  if (p.waves <= 8) return p.blend ? bwd_n<T, Gr, true, 512>(p, s) : bwd_n<T, Gr, false, 512>(p, s);
-  return p.blend ? bwd_n<T, Gr, true, 1024>(p, s) : bwd_n<T, Gr, false, 1024>(p, s);
+  return p.waves <= 8 ? bwd_e<T, Gr, 512>(p, s) : bwd_e<T, Gr, 1024>(p, s);
 }
 
 }  // namespace

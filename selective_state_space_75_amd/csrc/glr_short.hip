@@ -3,23 +3,19 @@
 // The mathematics of glr.hip and glr_bwd.hip, with several rows in a wave: a row has `p.lanes` neighbouring lanes (a power
 // of two, 8 tokens each), scans and sums run over those, and a workgroup of four waves takes 256 / lanes rows.
 // A wave per row would leave most lanes without a token, and the chip waiting for workgroups that do next to nothing.
-// The last lane of a row of 8 tokens or more takes its last 8 with one load; those that the lane before it has too (the
-// first `lo`) are left out there like tokens behind the row's end: s = 0, a = 1, and zeros in the other inputs.
 #include "glr.hpp"
 
 namespace mamba {
 namespace {
 
-// A lane's share of a row.
-struct Share {
-  int64_t b, d, row, t;         // its 8 tokens begin at t
-  int sub, lo, there, live;     // lane of the row; its own tokens are lo .. lo + there, the first `live` of them count
-  uint32_t on;                  // a bit for each token that counts
+struct Lane : Share {
+  int64_t b, d, row;
+  int sub;                      // lane of the row
   bool mine;                    // there is such a row
 };
 
-__device__ __forceinline__ Share glr_share(const GlrParams& p) {
-  Share o;
+__device__ __forceinline__ Lane glr_lane(const GlrParams& p) {
+  Lane o;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = p.B * p.D;
   o.row = id / p.lanes;
   o.sub = threadIdx.x & (p.lanes - 1);
@@ -27,54 +23,8 @@ __device__ __forceinline__ Share glr_share(const GlrParams& p) {
   if (!o.mine) o.row = rows - 1;
   o.b = o.row / p.D;
   o.d = o.row - o.b * p.D;
-  const int64_t first = o.sub * kGlrLane, last = p.L - kGlrLane, len = glr_length(p, o.b);
-  o.t = last < 0 ? 0 : first < last ? first : last;
-  o.there = o.mine ? clamp8(p.L - first) : 0;
-  o.lo = o.there ? (int)(first - o.t) : 0;
-  o.live = o.there < clamp8(len - first) ? o.there : clamp8(len - first);
-  o.on = ((1u << o.live) - 1) << o.lo;
+  static_cast<Share&>(o) = glr_share(p.L, o.mine ? p.L : 0, glr_length(p, o.b), o.sub * kGlrLane);
   return o;
-}
-
-// The lane's 8 tokens of a row of n, `dead` (its bits) in the place of those that do not count.
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_share(const T* row, int64_t n, const Share& q, uint32_t dead) {
-  Raw8<T> o;
-  if (n >= 8) {
-#pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k) o.w[k] = *(reinterpret_cast<const u32x4_u*>(row + q.t) + k);
-  } else {
-    o = load_raw8(row, (int)n);
-  }
-  if (q.on != 0xff) {
-#pragma unroll
-    for (int j = 0; j < 4 * (int)sizeof(T); j += 2) {
-      const int e = sizeof(T) == 2 ? j : j / 2;          // the word's first (or only) token
-      uint32_t w = o.w[j / 8][j / 2 & 3];
-      if constexpr (sizeof(T) == 2) {
-        const uint32_t m = (q.on >> e & 1 ? 0xffffu : 0u) | (q.on >> (e + 1) & 1 ? 0xffff0000u : 0u);
-        w = (w & m) | (dead & ~m);
-      } else {
-        w = q.on >> e & 1 ? w : dead;
-      }
-      o.w[j / 8][j / 2 & 3] = w;
-    }
-  }
-  return o;
-}
-template <typename T>
-constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-
-// The lane's own tokens, zeros for those that do not count.
-template <typename O>
-__device__ __forceinline__ void store_share(O* row, const float (&v)[8], const Share& q) {
-  if (q.lo == 0) {
-    store8<O, false>(row + q.t, v, q.live, q.there);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j >= q.lo) put1(row + q.t + j, j < q.lo + q.live ? v[j] : 0.0f);
-  }
 }
 
 // (P, H) of the row's lanes up to this one, and from this one on (composed from the last to the first).
@@ -101,7 +51,7 @@ __device__ __forceinline__ Affine share_down(Affine v, int sub, int lanes) {
 
 template <typename T, typename O, bool kBlend>
 __global__ __launch_bounds__(256) void glr_short_fwd_kernel(GlrParams p) {
-  const Share q = glr_share(p);
+  const Lane q = glr_lane(p);
   const int64_t at = q.d * p.L;
   const Raw8<T> xr = load_share(static_cast<const T*>(p.x) + q.b * p.x_stride + at, p.L, q, 0);
   const Raw8<T> rr = load_share(static_cast<const T*>(p.r) + q.b * p.r_stride + at, p.L, q, kMinusInf<T>);
@@ -141,13 +91,13 @@ __global__ __launch_bounds__(256) void glr_short_fwd_kernel(GlrParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] *= silu(get8(zr, j));
   }
-  store_share(static_cast<O*>(p.y) + q.row * p.L, o, q);
+  store_share<O, false>(static_cast<O*>(p.y) + q.row * p.L, o, q);
   if (p.final_state && q.mine && q.sub == p.lanes - 1) p.final_state[q.row] = __builtin_fmaf(v.P, before, v.H);
 }
 
 template <typename T, typename Gr, bool kBlend>
 __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
-  const Share q = glr_share(p);
+  const Lane q = glr_lane(p);
   const int64_t at = q.d * p.L, out = q.row * p.L;
   Raw8<T> xr = load_share(static_cast<const T*>(p.x) + q.b * p.x_stride + at, p.L, q, 0);
   const Raw8<T> rr = load_share(static_cast<const T*>(p.r) + q.b * p.r_stride + at, p.L, q, kMinusInf<T>);
@@ -196,7 +146,7 @@ __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
       const float hj = j < 7 ? hp[j < 7 ? j + 1 : 7] : h;
       o[j] = get8(yr, j) * hj * sz[j] * __builtin_fmaf(get8(zr, j), 1.0f - sz[j], 1.0f);
     }
-    store_share(static_cast<Gr*>(p.dz) + out, o, q);
+    store_share<Gr, false>(static_cast<Gr*>(p.dz) + out, o, q);
   }
   float dr[8], sums[3] = {0.0f, 0.0f, 0.0f};   // of A, r_bias, i_bias
 #pragma unroll
@@ -213,15 +163,15 @@ __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
     }
     sums[1] += dr[j];
   }
-  store_share(static_cast<Gr*>(p.dx) + out, o, q);
-  store_share(static_cast<Gr*>(p.dr) + out, dr, q);
+  store_share<Gr, false>(static_cast<Gr*>(p.dx) + out, o, q);
+  store_share<Gr, false>(static_cast<Gr*>(p.dr) + out, dr, q);
   if (p.i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       o[j] *= get8(xr, j) * (1.0f - g[j]);
       sums[2] += o[j];
     }
-    store_share(static_cast<Gr*>(p.di) + out, o, q);
+    store_share<Gr, false>(static_cast<Gr*>(p.di) + out, o, q);
   }
   for (int m = 1; m < p.lanes; m *= 2) {
 #pragma unroll
