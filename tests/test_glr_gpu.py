@@ -167,6 +167,17 @@ def test_every_split_of_every_type(dtype, out, blend, with_i, with_z, dev):
             test(B, D, L, dtype, out, blend, with_i, with_z, True, [L - 5 * b for b in range(B)], False, waves, 0, dev)
 
 
+@pytest.mark.parametrize("L", [1, 3, 7, 8, 9, 15, 16, 17, 31, 33, 64, 65, 100, 127, 129, 250, 255, 256, 257, 511, 519])
+def test_short_rows_and_their_last_lanes(L, dev):
+    """Rows share waves; a row's last lane has the tokens of the one before it too; lengths that end in either, before
+    both, or at once."""
+    lengths = [L, max(0, L - 3), max(0, L - 9), 0, L // 2]
+    for dtype, out, blend, ranges in (("bf16", "bf16", False, False), ("f32", "f32", False, True), ("bf16", "f32", True, True)):
+        for ln in (None, lengths):
+            for test in (test_forward, test_backward):
+                test(5, 37, L, dtype, out, blend, True, True, True, ln, ranges, 0, 0, dev)
+
+
 @pytest.mark.parametrize("with_init,with_final", [(True, False), (False, True)])
 @pytest.mark.parametrize("waves,segments", [(0, 0), (1, 3)])
 def test_one_of_the_two_states(with_init, with_final, waves, segments, dev):
@@ -266,12 +277,34 @@ def test_behind_a_rows_end_nothing_is_looked_at_or_lost(dev):
         assert torch.equal(c[0], a[0]) and torch.equal(c[1], a[1])
 
 
+@pytest.mark.parametrize("L", [4, 12, 100, 255, 511, 1207])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nothing_comes_from_behind_a_rows_length(L, bad, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    ends = [L - 1, L // 2, 0]
+    x = make(3, 9, L, "bf16", 12, False, True, True, True)
+    t = put(x, dev, NAMES)
+    ln = torch.tensor(ends, dtype=torch.int32, device=dev)
+    q = {k: v.clone() for k, v in t.items()}
+    for k in ("x", "r", "i", "z", "dy"):
+        for b, n in enumerate(ends):
+            q[k][b, :, n:] = bad
+    call = lambda v: m.glr_fwd(*args(v), initial_state=v["initial_state"], lengths=ln, return_final_state=True)  # noqa: E731
+    a, b = call(t), call(q)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga, gb = gradients(t, t["dy"], False, ln), gradients(q, q["dy"], False, ln)
+    for n in ga:
+        assert torch.equal(ga[n], gb[n]), n
+
+
+@pytest.mark.parametrize("L", [5, 99, 603, 1999])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_alignment_and_neighbours(dtype, dev):
+def test_alignment_and_neighbours(dtype, L, dev):
     """Arrays that begin at any element: the same bits, and nothing written around the outputs."""
     import torch
     import selective_state_space_75_amd as m
-    B, D, L = 2, 3, 603
+    B, D = 2, 3
     n = B * D * L
     x = make(B, D, L, dtype, 10, False, True, True, True)
     t = put(x, dev, NAMES)

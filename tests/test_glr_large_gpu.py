@@ -44,6 +44,26 @@ def test_recurrence_past_32_bit_offsets(dev):
     near(h, hr, E, "final state")
 
 
+def test_short_rows_past_32_bit_offsets(dev):
+    """The last rows have the bits that they have alone."""
+    import torch
+    import selective_state_space_75_amd as m
+    D, L = 23000000, 99
+    torch.manual_seed(3)
+    x, r, dy = (torch.randn(1, 1000, L, device=dev).bfloat16().repeat(1, D // 1000, 1) for _ in range(3))
+    A = -torch.rand(D, device=dev) - 0.1
+    cut = lambda t: t[:, D - 300:].contiguous()  # noqa: E731
+    y, h = m.glr_fwd(x, r, x, A, return_final_state=True)
+    y1, h1 = m.glr_fwd(cut(x), cut(r), cut(x), A[D - 300:].contiguous(), return_final_state=True)
+    assert torch.equal(cut(y), y1) and torch.equal(h[:, D - 300:], h1)
+    del y
+    g = m.glr_bwd(x, r, None, A, None, None, None, dy)
+    g1 = m.glr_bwd(cut(x), cut(r), None, A[D - 300:].contiguous(), None, None, None, cut(dy))
+    for n in ("dx", "dr"):
+        assert torch.equal(cut(g[n]), g1[n]), n
+    assert torch.equal(g["dA"][D - 300:], g1["dA"])
+
+
 def test_norm_past_32_bit_offsets(dev):
     import torch
     import selective_state_space_75_amd as m
