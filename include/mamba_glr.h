@@ -42,7 +42,7 @@
  * infinite.  In the backward pass any gradient of such a channel may be NaN, in the batch row
  * that holds it, and that channel's sums.
  * State, gates and sums are fp32.  The results are deterministic (sums in a fixed order, no
- * atomics): the same call gives the same bits.  B, like every other size, takes part in
+ * atomics): the same call gives the same bits.  Past 256 tokens, B, like every other size, takes part in
  * the choice of how a row is cut over waves and segments, and those agree to fp32 rounding only.
  */
 #ifndef MAMBA_GLR_H_

@@ -1,4 +1,5 @@
-// glr.hip -- the gated linear recurrence over sequences and one token at a time (gfx950).
+// glr.hip -- the gated linear recurrence over sequences and one token at a time (gfx950).  Rows of up to 256 tokens:
+// glr_short.hip.
 //
 // Per channel, one state h: h_t = a_t h_(t-1) + u_t with the gates of glr.hpp, y_t = h_t silu(z_t).
 // A stretch of tokens takes the state in front of it, h, to P h + H with P the product of its
@@ -11,8 +12,8 @@
 // Every input is read once and every output written once, and HBM bounds it where there are rows enough: 20480 rows,
 // L = 2048, bf16 with both gates, 76 us for 419 MB, 5.5 TB/s where a plain copy reaches 5.1; 4096 rows,
 // L = 32768, 248 us for 1.34 GB, 5.4 TB/s.  Vector instructions take 0.8 to 0.9 of the issue cycles beside that (the
-// exponentials of three gates a token), so there is little left on either side.  Few short rows wait for one
-// tile's latency: 16 rows of 256 tokens 4 us, one token of 4096 channels 3 us on the GPU.
+// exponentials of three gates a token), so there is little left on either side.  One token of 4096 channels takes
+// 3 us on the GPU.
 #include "glr.hpp"
 
 namespace mamba {
