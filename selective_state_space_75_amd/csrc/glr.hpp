@@ -17,16 +17,12 @@ struct Raw8 {
 };
 
 // n < 8: only the first n are there, the others read as zero.
-template <typename T, bool kNT = false>
+template <typename T>
 __device__ __forceinline__ Raw8<T> load_raw8(const T* p, int n) {
   Raw8<T> o;
   if (n >= 8) {
 #pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
-      const u32x4_u* q = reinterpret_cast<const u32x4_u*>(p) + k;
-      if constexpr (kNT) o.w[k] = __builtin_nontemporal_load(q);
-      else o.w[k] = *q;
-    }
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) o.w[k] = *(reinterpret_cast<const u32x4_u*>(p) + k);
   } else {
 #pragma unroll
     for (int k = 0; k < (int)sizeof(T) / 2; ++k) o.w[k] = u32x4{0, 0, 0, 0};
