@@ -18,13 +18,15 @@ struct Lane : Share {
 
 __device__ __forceinline__ Lane glr_lane(const GlrParams& p) {
   Lane o;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = p.B * p.D;
-  o.row = id / p.lanes;
+  const int shift = __builtin_ctz(p.lanes);
+  const uint32_t rows = (uint32_t)(p.B * p.D), D = (uint32_t)p.D;                  // below 2^26: a wave per row would be a launch
+  uint32_t row = blockIdx.x * (256u >> shift) + (threadIdx.x >> shift);
   o.sub = threadIdx.x & (p.lanes - 1);
-  o.mine = o.row < rows;
-  if (!o.mine) o.row = rows - 1;
-  o.b = o.row / p.D;
-  o.d = o.row - o.b * p.D;
+  o.mine = row < rows;
+  if (!o.mine) row = rows - 1;
+  o.row = row;
+  o.b = row / D;
+  o.d = row - (uint32_t)o.b * D;
   static_cast<Share&>(o) = glr_share(p.L, o.mine ? p.L : 0, glr_length(p, o.b), o.sub * kGlrLane);
   return o;
 }
