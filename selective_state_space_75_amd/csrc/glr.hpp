@@ -240,7 +240,7 @@ __device__ __forceinline__ GlrGate glr_gate(float r, float nb, float A2) {
   GlrGate o;
   float e = hw_exp2(__builtin_fmaf(r, -kLog2e, nb));
   if constexpr (kBlend) {
-    e = __builtin_fminf(e, 0x1p126f);
+    e = e > 0x1p126f ? 0x1p126f : e;           // a comparison, so that a NaN stays one (the hardware's minimum drops it)
     o.s = hw_rcp(1.0f + e);
     o.a = e * o.s;
     o.n = o.s;

@@ -1,0 +1,92 @@
+"""NaN among the inputs of the gated linear recurrence, both rules, on every way that a row is laid out (short rows,
+the last lane's overlap, waves, segments, one token): where the definition gives NaN, so do the outputs, the states and the
+gradients, and what it does not reach keeps the bits that it has without it."""
+import numpy as np
+import pytest
+
+from helpers import f64, from_dev, log
+from oracle import glr as O
+from test_glr_gpu import NAMES, args, gradients, make, oracle_args, put
+
+pytestmark = pytest.mark.gpu
+
+B, D, ROW, CH = 2, 5, 1, 2
+NAN = float("nan")
+#       L    waves segments: a short row; of bf16, a last lane that overlaps; one wave; segments
+LAYOUTS = [(1, 0, 0), (7, 0, 0), (100, 0, 0), (255, 0, 0), (1500, 0, 0), (1503, 0, 0), (1503, 1, 0), (1100, 2, 3)]
+
+
+def nan_where(ref, got, what):
+    """Where the definition gives NaN, the GPU does."""
+    bad = np.isnan(ref) & ~np.isnan(from_dev(got))
+    assert not bad.any(), "%s: %d numbers are not NaN" % (what, bad.sum())
+
+
+def planted(x, t, name, at):
+    """The inputs with a NaN at one token of one channel (or in the channel's bias)."""
+    q, v = {**t, name: t[name].clone()}, dict(x)
+    v[name] = x[name].copy()
+    where = (CH,) if name.endswith("bias") else (ROW, CH, at)
+    q[name][where] = NAN
+    v[name][where] = 0x7fc0 if v[name].dtype == np.uint16 else NAN
+    return v, q
+
+
+@pytest.mark.parametrize("L,waves,segments", LAYOUTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("blend", [True, False])
+@pytest.mark.parametrize("name", ["x", "r", "i", "z", "r_bias", "i_bias"])
+def test_nan_is_not_lost(name, blend, dtype, L, waves, segments, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    log("[glr nan] %s" % ((name, blend, dtype, L, waves, segments),))
+    x = make(B, D, L, dtype, 30 + L, blend, True, True, True)
+    t = put(x, dev, NAMES)
+    v, q = planted(x, t, name, L // 2)
+    kw = dict(blend=blend, return_final_state=True)
+    with m.glr_test_knobs(waves=waves, segments=segments):
+        clean = m.glr_fwd(*args(t), initial_state=t["initial_state"], **kw)
+        y, h = m.glr_fwd(*args(q), initial_state=q["initial_state"], **kw)
+        gc, g = gradients(t, t["dy"], blend, None), gradients(q, q["dy"], blend, None)
+        torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        yr, hr = O.glr(*oracle_args(v), blend=blend, initial_state=x["initial_state"])
+        ref = O.glr_bwd(*oracle_args(v), f64(x["dy"]), blend=blend, initial_state=x["initial_state"],
+                        dfinal_state=x["dfinal_state"])
+    assert np.isnan(yr).any()
+    for a, r, n in ((y, yr, "y"), (h, hr, "final state")):
+        nan_where(r, a, n)
+        assert not (np.isnan(from_dev(a)) & ~np.isnan(r)).any(), n
+    assert torch.equal(y[torch.from_numpy(~np.isnan(yr)).to(dev)], clean[0][torch.from_numpy(~np.isnan(yr)).to(dev)])
+    assert torch.equal(h[torch.from_numpy(~np.isnan(hr)).to(dev)], clean[1][torch.from_numpy(~np.isnan(hr)).to(dev)])
+    own = torch.zeros((B, D), dtype=torch.bool, device=dev)
+    own[slice(None) if name.endswith("bias") else ROW, CH] = True
+    for n in g:
+        if g[n] is None:
+            continue
+        nan_where(ref[n], g[n], n)
+        keep = ~(own.any(0) if g[n].dim() == 1 else own)
+        assert torch.equal(g[n][keep], gc[n][keep]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("blend", [True, False])
+@pytest.mark.parametrize("name", ["x", "r", "i", "z", "r_bias", "i_bias"])
+def test_nan_in_one_token(name, blend, dtype, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    x = make(B, D, 1, dtype, 60, blend, True, True, True)
+    t = put(x, dev, NAMES)
+    v, q = planted(x, t, name, 0)
+    got = []
+    for s in (t, q):
+        pool = s["initial_state"].clone()
+        one = {k: s[k].squeeze(2) for k in ("x", "r", "i", "z")}
+        got.append((m.glr_update(pool, *args({**s, **one}), blend=blend), pool))
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        ref = O.glr(*oracle_args(v), blend=blend, initial_state=x["initial_state"])
+    for clean, a, r, n in zip(got[0], got[1], (ref[0][..., 0], ref[1]), ("y", "state")):
+        assert np.array_equal(np.isnan(from_dev(a)), np.isnan(r)), n
+        keep = torch.from_numpy(~np.isnan(r)).to(dev)
+        assert torch.equal(a[keep], clean[keep]), n
