@@ -250,7 +250,8 @@ __device__ __forceinline__ GlrGate glr_gate(float r, float nb, float A2) {
     const float x2 = A2 * o.s;
     o.a = hw_exp2(x2);
     float q = glr_rest(x2, o.a);
-    q = q < 1e-37f ? 1e-37f : q;               // a comparison, so that a NaN stays one
+    // a comparison, so that a NaN stays one; of the size, so that A > 0 (below zero by 2 A s) gives a NaN
+    q = __builtin_fabsf(q) < 1e-37f ? 1e-37f : q;
     const float rs = __builtin_amdgcn_rsqf(q);
     o.n = q * rs;
     o.ra = o.a * o.a * rs;

@@ -90,3 +90,50 @@ def test_nan_in_one_token(name, blend, dtype, dev):
         assert np.array_equal(np.isnan(from_dev(a)), np.isnan(r)), n
         keep = torch.from_numpy(~np.isnan(r)).to(dev)
         assert torch.equal(a[keep], clean[keep]), n
+
+
+@pytest.mark.parametrize("L,waves,segments", LAYOUTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_growing_decay_gives_nan(dtype, L, waves, segments, dev):
+    """A above zero: sqrt(1 - a^2) has no value.  A row without tokens keeps its state all the same."""
+    import torch
+    import selective_state_space_75_amd as m
+    x = make(3, D, L, dtype, 70 + L, False, True, True, True)
+    t = put(x, dev, NAMES)
+    lengths = [L, L - L // 3, 0]
+    ln = torch.tensor(lengths, dtype=torch.int32, device=dev)
+    up = np.float32([0.0, 0.01, 0.5, 3.0, 90.0])                 # added in: channel 0 stays as it is
+    q = {**t, "A": t["A"].clone()}
+    q["A"][1:] = torch.from_numpy(up[1:]).to(dev)
+    with m.glr_test_knobs(waves=waves, segments=segments):
+        kw = dict(lengths=ln, return_final_state=True)
+        clean = m.glr_fwd(*args(t), initial_state=t["initial_state"], **kw)
+        y, h = m.glr_fwd(*args(q), initial_state=q["initial_state"], **kw)
+        gc, g = gradients(t, t["dy"], False, ln), gradients(q, q["dy"], False, ln)
+        torch.cuda.synchronize()
+    for b, n in enumerate(lengths):
+        assert torch.isnan(y[b, 1:, :n]).all() and not y[b, :, n:].any()
+        assert torch.isnan(h[b, 1:]).all() if n else torch.equal(h[b], t["initial_state"][b])
+    assert torch.equal(y[:, 0], clean[0][:, 0]) and torch.equal(h[:, 0], clean[1][:, 0])
+    for n in g:
+        assert torch.equal(g[n][..., 0] if g[n].dim() < 3 else g[n][:, 0], gc[n][..., 0] if g[n].dim() < 3 else gc[n][:, 0]), n
+    live = torch.arange(L, device=dev) < ln[:, None]
+    for n in ("dx", "dr", "di", "dz"):
+        assert torch.isnan(g[n][:, 1:].transpose(1, 2)[live]).all(), n
+    for n in ("dA", "dr_bias", "di_bias"):
+        assert torch.isnan(g[n][1:]).all(), n
+    assert torch.equal(g["dinitial_state"][2], t["dfinal_state"][2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_growing_decay_gives_nan_in_one_token(dtype, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    x = make(B, D, 1, dtype, 71, False, True, True, True)
+    t = put(x, dev, NAMES)
+    t["A"][1:] = torch.tensor([0.01, 0.5, 3.0, 90.0], device=dev)
+    pool = t["initial_state"].clone()
+    y = m.glr_update(pool, *args({**t, **{k: t[k].squeeze(2) for k in ("x", "r", "i", "z")}}))
+    torch.cuda.synchronize()
+    assert torch.isnan(y[:, 1:]).all() and torch.isnan(pool[:, 1:]).all()
+    assert torch.isfinite(y[:, 0]).all() and torch.isfinite(pool[:, 0]).all()
