@@ -38,9 +38,8 @@ __global__ __launch_bounds__(1024) void glr_fwd_kernel(GlrParams p) {
   const T* ig = p.i ? static_cast<const T*>(p.i) + b * p.i_stride + d * p.L : nullptr;
   const T* z = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + d * p.L : nullptr;
   O* y = static_cast<O*>(p.y) + row * p.L;
-  const float A2 = kBlend ? 0.0f : p.A[d] * kLog2e;
-  const float rb = p.r_bias ? -p.r_bias[d] * kLog2e : 0.0f;
-  const float ib = p.i_bias ? -p.i_bias[d] * kLog2e : 0.0f;
+  const GlrChannel channel = glr_channel<kBlend>(p, d, len);
+  const float A2 = channel.A2, rb = channel.rb, ib = channel.ib;
 
   Affine all;                         // kSummary: the segment so far
   float carry = 0.0f;                 // state in front of the tile

@@ -266,6 +266,26 @@ __device__ __forceinline__ int64_t glr_length(const GlrParams& p, int64_t b) {
   return n < 0 ? 0 : n > p.L ? p.L : n;
 }
 
+// A channel's parameters as the gates of a row of `len` tokens take them: A, A log2(e), -bias log2(e).  Kept finite, so that a token
+// that is not there (r = -inf, zeros) stays absent, s = 0 and a = 1, for gates that an infinite bias holds open and for A = -inf.
+// A row without tokens looks at none of them.
+struct GlrChannel {
+  float A = 0.0f, A2 = 0.0f, rb = 0.0f, ib = 0.0f;
+};
+template <bool kBlend>
+__device__ __forceinline__ GlrChannel glr_channel(const GlrParams& p, int64_t d, int64_t len) {
+  GlrChannel o;
+  if (len == 0) return o;
+  auto held = [](float v) { return v < -2e38f ? -2e38f : v; };     // a comparison, so that a NaN stays one
+  if constexpr (!kBlend) {
+    o.A = held(p.A[d]);
+    o.A2 = o.A * kLog2e;
+  }
+  if (p.r_bias) o.rb = held(-p.r_bias[d] * kLog2e);
+  if (p.i_bias) o.ib = -p.i_bias[d] * kLog2e;
+  return o;
+}
+
 __device__ __forceinline__ int clamp8(int64_t n) { return n < 0 ? 0 : n > 8 ? 8 : (int)n; }
 
 // r of a token that is not there.

@@ -37,9 +37,8 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
   const T* ig = p.i ? static_cast<const T*>(p.i) + b * p.i_stride + d * p.L : nullptr;
   const T* zg = p.z ? static_cast<const T*>(p.z) + b * p.z_stride + d * p.L : nullptr;
   const Gr* dy = static_cast<const Gr*>(p.dy) + row * p.L;
-  const float A = kBlend ? 0.0f : p.A[d], A2 = A * kLog2e;
-  const float rb = p.r_bias ? -p.r_bias[d] * kLog2e : 0.0f;
-  const float ib = p.i_bias ? -p.i_bias[d] * kLog2e : 0.0f;
+  const GlrChannel channel = glr_channel<kBlend>(p, d, len);
+  const float A = channel.A, A2 = channel.A2, rb = channel.rb, ib = channel.ib;
   const int width = p.groups > 1 ? 3 : 2;                                   // numbers of a tile's summary
   const float* sum = p.S > 1 ? p.sum + row * p.S * width : nullptr;
   const int64_t lo = own * p.group, hi = p.S < lo + p.group ? p.S : lo + p.group;

@@ -11,7 +11,7 @@ namespace mamba {
 namespace {
 
 struct Lane : Share {
-  int64_t b, d, row;
+  int64_t b, d, row, len;       // len: tokens of the row that count
   int sub;                      // lane of the row
   bool mine;                    // there is such a row
 };
@@ -27,7 +27,8 @@ __device__ __forceinline__ Lane glr_lane(const GlrParams& p) {
   o.row = row;
   o.b = row / D;
   o.d = row - (uint32_t)o.b * D;
-  static_cast<Share&>(o) = glr_share(p.L, o.mine ? p.L : 0, glr_length(p, o.b), o.sub * kGlrLane);
+  o.len = glr_length(p, o.b);
+  static_cast<Share&>(o) = glr_share(p.L, o.mine ? p.L : 0, o.len, o.sub * kGlrLane);
   return o;
 }
 
@@ -62,8 +63,8 @@ __global__ __launch_bounds__(256) void glr_short_fwd_kernel(GlrParams p) {
   Raw8<T> ir, zr;
   if (p.i) ir = load_share(static_cast<const T*>(p.i) + q.b * p.i_stride + at, p.L, q, 0);
   if (p.z) zr = load_share(static_cast<const T*>(p.z) + q.b * p.z_stride + at, p.L, q, 0);
-  const float A2 = kBlend ? 0.0f : p.A[q.d] * kLog2e;
-  const float rb = p.r_bias ? -p.r_bias[q.d] * kLog2e : 0.0f, ib = p.i_bias ? -p.i_bias[q.d] * kLog2e : 0.0f;
+  const GlrChannel channel = glr_channel<kBlend>(p, q.d, q.len);
+  const float A2 = channel.A2, rb = channel.rb, ib = channel.ib;
   const float before = p.init ? p.init[q.row] : 0.0f;
   float a[8], u[8];
 #pragma unroll
@@ -109,8 +110,8 @@ __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
   Raw8<T> ir, zr;
   if (p.i) ir = load_share(static_cast<const T*>(p.i) + q.b * p.i_stride + at, p.L, q, 0);
   if (p.z) zr = load_share(static_cast<const T*>(p.z) + q.b * p.z_stride + at, p.L, q, 0);
-  const float A = kBlend ? 0.0f : p.A[q.d], A2 = A * kLog2e;
-  const float rb = p.r_bias ? -p.r_bias[q.d] * kLog2e : 0.0f, ib = p.i_bias ? -p.i_bias[q.d] * kLog2e : 0.0f;
+  const GlrChannel channel = glr_channel<kBlend>(p, q.d, q.len);
+  const float A = channel.A, A2 = channel.A2, rb = channel.rb, ib = channel.ib;
   const float before = p.init ? p.init[q.row] : 0.0f, after = p.dfinal ? p.dfinal[q.row] : 0.0f;
   float a[8], n[8], s[8], ra[8], g[8], e[8], sz[8];
 #pragma unroll

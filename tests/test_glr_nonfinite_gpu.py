@@ -137,3 +137,58 @@ def test_a_growing_decay_gives_nan_in_one_token(dtype, dev):
     torch.cuda.synchronize()
     assert torch.isnan(y[:, 1:]).all() and torch.isnan(pool[:, 1:]).all()
     assert torch.isfinite(y[:, 0]).all() and torch.isfinite(pool[:, 0]).all()
+
+
+@pytest.mark.parametrize("L,waves,segments", LAYOUTS)
+@pytest.mark.parametrize("blend", [True, False])
+@pytest.mark.parametrize("name,value", [("r_bias", np.inf), ("r_bias", -np.inf), ("i_bias", np.inf), ("i_bias", -np.inf),
+                                        ("A", -np.inf), ("A", -3.4e38)])
+def test_infinite_parameters_are_gates_held_open_or_closed(name, value, blend, L, waves, segments, dev):
+    """Absent tokens, behind a length or behind L in a wave's last lanes, are absent for such a channel too.  The bars are
+    those of the finite gates.  (dr of A = -inf is 0 * inf.)"""
+    import torch
+    import selective_state_space_75_amd as m
+    if blend and name == "A":
+        pytest.skip("no A")
+    from test_glr_gpu import E, near
+    x = make(3, D, L, "f32", 90 + L, blend, True, True, True)
+    x[name][CH] = value
+    t = put(x, dev, NAMES)
+    for lengths in (None, [L, L - L // 3, 0]):
+        ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=dev)
+        with m.glr_test_knobs(waves=waves, segments=segments):
+            y, h = m.glr_fwd(*args(t), blend=blend, initial_state=t["initial_state"], lengths=ln, return_final_state=True)
+            g = gradients(t, t["dy"], blend, ln)
+            torch.cuda.synchronize()
+        with np.errstate(all="ignore"):
+            yr, hr = O.glr(*oracle_args(x), blend=blend, initial_state=x["initial_state"], lengths=lengths)
+            ref = O.glr_bwd(*oracle_args(x), f64(x["dy"]), blend=blend, initial_state=x["initial_state"],
+                            dfinal_state=x["dfinal_state"], lengths=lengths)
+        near(y, yr, E, "y")
+        near(h, hr, E, "final state")
+        for n in ("dx", "dr", "di", "dz", "dA", "dr_bias", "di_bias", "dinitial_state"):
+            if g[n] is None or name == "A" and n in ("dr", "dr_bias"):
+                continue
+            near(g[n], ref[n], 2 * E, n, ref["scale"].get(n))
+
+
+@pytest.mark.parametrize("L,waves,segments", LAYOUTS)
+@pytest.mark.parametrize("blend", [True, False])
+@pytest.mark.parametrize("name", ["r_bias", "i_bias", "A"])
+def test_a_row_without_tokens_looks_at_no_parameter(name, blend, L, waves, segments, dev):
+    import torch
+    import selective_state_space_75_amd as m
+    if blend and name == "A":
+        pytest.skip("no A")
+    x = make(2, D, L, "bf16", 110 + L, blend, True, True, True)
+    t = put(x, dev, NAMES)
+    t[name][CH] = NAN
+    ln = torch.tensor([0, 0], dtype=torch.int32, device=dev)
+    with m.glr_test_knobs(waves=waves, segments=segments):
+        y, h = m.glr_fwd(*args(t), blend=blend, initial_state=t["initial_state"], lengths=ln, return_final_state=True)
+        g = gradients(t, t["dy"], blend, ln)
+        torch.cuda.synchronize()
+    assert torch.equal(h, t["initial_state"]) and torch.equal(g["dinitial_state"], t["dfinal_state"])
+    assert not y.any()
+    for n in ("dx", "dr", "di", "dz", "dA", "dr_bias", "di_bias"):
+        assert g[n] is None or torch.isfinite(g[n]).all() and g[n].abs().max() < 1e-30, n
