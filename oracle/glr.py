@@ -31,13 +31,16 @@ def _prepare(x, r, i, z, A, r_bias, i_bias, blend, lengths):
         live = (np.arange(L)[:, None] < np.clip(np.asarray(lengths), 0, L)[None, :])[:, :, None]
     v = {"live": live, "x": _tokens(x, live), "z": _tokens(z, live), "L": L}
     pre = _tokens(r, live) + (0.0 if r_bias is None else _f64(r_bias))
-    v["s"] = sigmoid(pre)
+    v["s"], v["not_s"] = sigmoid(pre), sigmoid(-pre)          # 1 - s, also where s is 1 to the last bit
     if blend:
-        v["a"], v["n"] = sigmoid(-pre), v["s"]
+        v["a"], v["n"] = v["not_s"], v["s"]
     else:
         l = _f64(A) * v["s"]
         v["a"], v["n"] = np.exp(l), np.sqrt(-np.expm1(2.0 * l))
-    v["g"] = np.ones_like(v["x"]) if i is None else sigmoid(_tokens(i, live) + (0.0 if i_bias is None else _f64(i_bias)))
+    v["g"], v["not_g"] = np.ones_like(v["x"]), np.zeros_like(v["x"])
+    if i is not None:
+        pre = _tokens(i, live) + (0.0 if i_bias is None else _f64(i_bias))
+        v["g"], v["not_g"] = sigmoid(pre), sigmoid(-pre)
     return v
 
 
@@ -69,7 +72,7 @@ def glr_bwd(x, r, i, A, r_bias, i_bias, z, dy, *, blend=False, initial_state=Non
     v = _prepare(x, r, i, z, A, r_bias, i_bias, blend, lengths)
     h0 = np.zeros((B, D)) if initial_state is None else _f64(initial_state)
     h = _states(v, h0)
-    live, a, n, s, g, xs = (v[k] for k in ("live", "a", "n", "s", "g", "x"))
+    live, a, n, s, not_s, g, xs = (v[k] for k in ("live", "a", "n", "s", "not_s", "g", "x"))
     dys = _tokens(dy, live)
     e = dys
     dz = None
@@ -85,17 +88,17 @@ def glr_bwd(x, r, i, A, r_bias, i_bias, z, dy, *, blend=False, initial_state=Non
     q = np.where(live, q, 0.0)
     hp = np.concatenate([h0[None], h[:-1]])
     dx = q * n * g
-    di = q * n * xs * g * (1.0 - g)
+    di = q * n * xs * g * v["not_g"]
     out, scale = {}, {}
     if blend:
-        dr = q * (g * xs - hp) * s * (1.0 - s)
-        scale["dr"] = np.abs(q) * (np.abs(g * xs) + np.abs(hp)) * s * (1.0 - s)
+        dr = q * (g * xs - hp) * s * not_s
+        scale["dr"] = np.abs(q) * (np.abs(g * xs) + np.abs(hp)) * s * not_s
         out["dA"] = None
     else:
         with np.errstate(divide="ignore", invalid="ignore"):
             ra = np.where(n > 0, a * a / n, 0.0)
         dl, sl = q * (a * hp - g * xs * ra), np.abs(q) * (np.abs(a * hp) + np.abs(g * xs * ra))
-        f = _f64(A) * s * (1.0 - s)
+        f = _f64(A) * s * not_s
         dr, scale["dr"] = dl * f, sl * np.abs(f)
         out["dA"], scale["dA"] = (dl * s).sum((0, 1)), (sl * s).sum((0, 1))
     out["dr_bias"], scale["dr_bias"] = dr.sum((0, 1)), scale["dr"].sum((0, 1))

@@ -227,9 +227,13 @@ __device__ __forceinline__ float glr_rest(float x2, float a) {
   return y > -0.125f ? -y * p : __builtin_fmaf(-a, a, 1.0f);
 }
 
+// 1 - s of a sigmoid s = 1 / (1 + e), as e s: right to its own last bits where the difference would have 2^-24 of 1.  e may be
+// infinite where s is 0.
+__device__ __forceinline__ float one_less(float s, float e) { return s == 0.0f ? 1.0f : e * s; }
+
 // The gates of a token.
 struct GlrGate {
-  float a, n, s;      // decay, input factor, sigmoid of r
+  float a, n, s, c;   // decay, input factor, sigmoid of r and one less it
   float ra;           // a^2 / n: minus the derivative of n with respect to log a (decay rule)
 };
 
@@ -242,11 +246,12 @@ __device__ __forceinline__ GlrGate glr_gate(float r, float nb, float A2) {
   if constexpr (kBlend) {
     e = e > 0x1p126f ? 0x1p126f : e;           // a comparison, so that a NaN stays one (the hardware's minimum drops it)
     o.s = hw_rcp(1.0f + e);
-    o.a = e * o.s;
+    o.a = o.c = e * o.s;
     o.n = o.s;
     o.ra = 0.0f;
   } else {
     o.s = hw_rcp(1.0f + e);
+    o.c = one_less(o.s, e);
     const float x2 = A2 * o.s;
     o.a = hw_exp2(x2);
     float q = glr_rest(x2, o.a);

@@ -72,18 +72,21 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
     if (ig) ir = load(ig, 0);
     if (zg) zr = load(zg, 0);
 
-    float a[8], n[8], s[8], ra[8], g[8];
+    // Of n, g and a^2 / n only the products with g are needed.  one: 1 - g
+    float a[8], s[8], c1[8], ng[8], ra[8], one[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const GlrGate k = glr_gate<kBlend>(kEdge ? get8(rr, j) : glr_r(rr, j, live), rb, A2);
-      a[j] = k.a; n[j] = k.n; s[j] = k.s; ra[j] = k.ra;
+      a[j] = k.a; s[j] = k.s; c1[j] = k.c; ng[j] = k.n; ra[j] = k.ra;
     }
     if (ig) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = hw_rcp(1.0f + hw_exp2(__builtin_fmaf(get8(ir, j), -kLog2e, ib)));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+      for (int j = 0; j < 8; ++j) {
+        const float ei = hw_exp2(__builtin_fmaf(get8(ir, j), -kLog2e, ib)), g = hw_rcp(1.0f + ei);
+        ng[j] *= g;
+        ra[j] *= g;
+        one[j] = one_less(g, ei);
+      }
     }
     float e[8], sz[8];
     if (zg) {
@@ -100,7 +103,7 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       f.P *= a[j];
-      f.H = __builtin_fmaf(a[j], f.H, n[j] * g[j] * get8(xr, j));
+      f.H = __builtin_fmaf(a[j], f.H, ng[j] * get8(xr, j));
     }
 #pragma unroll
     for (int j = 7; j >= 0; --j) k.H = a[j] * (k.H + e[j]);
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       hp[j] = h;
-      h = __builtin_fmaf(a[j], h, n[j] * g[j] * get8(xr, j));
+      h = __builtin_fmaf(a[j], h, ng[j] * get8(xr, j));
     }
     if (zg) {
       float o[8];
@@ -167,14 +170,14 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
     for (int j = 7; j >= 0; --j) {
       const float v = e[j] + c;
       c = a[j] * v;
-      dx[j] = v * n[j] * g[j];
-      const float gx = g[j] * get8(xr, j);
+      dx[j] = v * ng[j];
+      const float xj = get8(xr, j);
       if constexpr (kBlend) {
-        dr[j] = v * (gx - hp[j]) * s[j] * a[j];
+        dr[j] = v * __builtin_fmaf(ng[j], xj, -s[j] * hp[j]) * a[j];     // n = s
       } else {
-        const float ds = v * __builtin_fmaf(a[j], hp[j], -gx * ra[j]) * s[j];
+        const float ds = v * __builtin_fmaf(a[j], hp[j], -xj * ra[j]) * s[j];
         sA += ds;
-        dr[j] = ds * A * (1.0f - s[j]);
+        dr[j] = ds * A * c1[j];
       }
       sr += dr[j];
     }
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
     if (ig) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dx[j] *= get8(xr, j) * (1.0f - g[j]);
+        dx[j] *= get8(xr, j) * one[j];
         si += dx[j];
       }
       store(p.di, dx);

@@ -113,12 +113,17 @@ __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
   const GlrChannel channel = glr_channel<kBlend>(p, q.d, q.len);
   const float A = channel.A, A2 = channel.A2, rb = channel.rb, ib = channel.ib;
   const float before = p.init ? p.init[q.row] : 0.0f, after = p.dfinal ? p.dfinal[q.row] : 0.0f;
-  float a[8], n[8], s[8], ra[8], g[8], e[8], sz[8];
+  float a[8], s[8], c1[8], ng[8], ra[8], one[8], e[8], sz[8];      // as in glr_bwd.hip
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const GlrGate k = glr_gate<kBlend>(get8(rr, j), rb, A2);
-    a[j] = k.a; n[j] = k.n; s[j] = k.s; ra[j] = k.ra;
-    g[j] = p.i ? hw_rcp(1.0f + hw_exp2(__builtin_fmaf(get8(ir, j), -kLog2e, ib))) : 1.0f;
+    a[j] = k.a; s[j] = k.s; c1[j] = k.c; ng[j] = k.n; ra[j] = k.ra;
+    if (p.i) {
+      const float ei = hw_exp2(__builtin_fmaf(get8(ir, j), -kLog2e, ib)), g = hw_rcp(1.0f + ei);
+      ng[j] *= g;
+      ra[j] *= g;
+      one[j] = one_less(g, ei);
+    }
     sz[j] = p.z ? sigmoid(get8(zr, j)) : 1.0f;
     e[j] = get8(yr, j);
     if (p.z) e[j] *= get8(zr, j) * sz[j];
@@ -127,7 +132,7 @@ __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     f.P *= a[j];
-    f.H = __builtin_fmaf(a[j], f.H, n[j] * g[j] * get8(xr, j));
+    f.H = __builtin_fmaf(a[j], f.H, ng[j] * get8(xr, j));
   }
 #pragma unroll
   for (int j = 7; j >= 0; --j) k.H = a[j] * (k.H + e[j]);
@@ -143,7 +148,7 @@ __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     hp[j] = h;
-    h = __builtin_fmaf(a[j], h, n[j] * g[j] * get8(xr, j));
+    h = __builtin_fmaf(a[j], h, ng[j] * get8(xr, j));
   }
   if (p.z) {
 #pragma unroll
@@ -156,15 +161,15 @@ __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
   float dr[8], sums[3] = {0.0f, 0.0f, 0.0f};   // of A, r_bias, i_bias
 #pragma unroll
   for (int j = 7; j >= 0; --j) {
-    const float y = e[j] + c, gx = g[j] * get8(xr, j);
+    const float y = e[j] + c, xj = get8(xr, j);
     c = a[j] * y;
-    o[j] = y * n[j] * g[j];
+    o[j] = y * ng[j];
     if constexpr (kBlend) {
-      dr[j] = y * (gx - hp[j]) * s[j] * a[j];
+      dr[j] = y * __builtin_fmaf(ng[j], xj, -s[j] * hp[j]) * a[j];       // n = s
     } else {
-      const float ds = y * __builtin_fmaf(a[j], hp[j], -gx * ra[j]) * s[j];
+      const float ds = y * __builtin_fmaf(a[j], hp[j], -xj * ra[j]) * s[j];
       sums[0] += ds;
-      dr[j] = ds * A * (1.0f - s[j]);
+      dr[j] = ds * A * c1[j];
     }
     sums[1] += dr[j];
   }
@@ -173,7 +178,7 @@ __global__ __launch_bounds__(256) void glr_short_bwd_kernel(GlrParams p) {
   if (p.i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      o[j] *= get8(xr, j) * (1.0f - g[j]);
+      o[j] *= get8(xr, j) * one[j];
       sums[2] += o[j];
     }
     store_share<Gr, false>(static_cast<Gr*>(p.di) + out, o, q);
