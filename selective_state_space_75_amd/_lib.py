@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import itertools
 import os
 import threading
 
@@ -865,15 +866,17 @@ def _like(x, dtype):
     return torch.empty(x.shape, dtype=dtype, device=x.device)
 
 
-def _apart(y, name, ins, strides):
-    """The caller's y, which must not lie over an input: tiles are read more than once."""
-    lo = y.data_ptr()
-    hi = lo + y.numel() * y.element_size()
-    for t, s in zip(ins, strides):
+def _apart(out, name, ins, strides, dense):
+    """The caller's output, which must not lie over an input (batch rows `strides` apart), nor over the `dense`
+    parameters, states and outputs of the call: workgroups read and write in no order."""
+    lo = out.data_ptr()
+    hi = lo + out.numel() * out.element_size()
+    for t, s in itertools.chain(zip(ins, strides), zip(dense, itertools.repeat(None))):
         if t is not None and t.numel():
             at, B = t.data_ptr(), t.shape[0]
-            if at < hi and lo < at + ((B - 1) * s + t.numel() // B) * t.element_size():
-                raise ValueError("%s must not overlap the inputs" % name)
+            n = t.numel() if s is None else (B - 1) * s + t.numel() // B
+            if at < hi and lo < at + n * t.element_size():
+                raise ValueError("%s must not overlap the inputs or another output" % name)
 
 
 _HERE = contextlib.nullcontext()
@@ -942,7 +945,8 @@ def glr_fwd(x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *, blend=Fal
     of a wider tensor.  A (below zero), r_bias, i_bias: (D) fp32.  initial_state: (B, D) fp32;
     lengths: (B) int32, tokens per row.
 
-    Returns y (B, D, L), or (y, final_state (B, D) fp32) when return_final_state.
+    Returns y (B, D, L), or (y, final_state (B, D) fp32) when return_final_state.  A y or final_state
+    passed in must lie apart from the inputs, initial_state among them (ValueError).
     """
     torch = _torch()
     dev, in_dt, code = _first(x, (3,), "(B, D, L)")
@@ -957,12 +961,15 @@ def glr_fwd(x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *, blend=Fal
             yp = y.data_ptr()
         else:
             yp = _plain(y, "y", shape, out_dt, dev)
-            _apart(y, "y", (x, r, i, z), strides)
+            _apart(y, "y", (x, r, i, z), strides, (A, r_bias, i_bias, initial_state, lengths))
         last = None
         if return_final_state:
             if final_state is None:
                 final_state = torch.empty((B, D), dtype=torch.float32, device=dev)
-            last = _plain(final_state, "final_state", (B, D), torch.float32, dev)
+                last = final_state.data_ptr()
+            else:
+                last = _plain(final_state, "final_state", (B, D), torch.float32, dev)
+                _apart(final_state, "final_state", (x, r, i, z), strides, (A, r_bias, i_bias, initial_state, lengths, y))
         workspace = _workspace(workspace, glr_workspace_size(B, D, L), dev)
         st = lib().mamba_glr_fwd(*ins, init, ends, yp, last, B, D, L, *strides, code, _dtype_code(y),
                                  FLAG_BLEND if blend else 0, _addr(workspace), _nbytes(workspace),
@@ -1028,6 +1035,11 @@ def glr_update(state, x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *,
     ins, strides = _glr_inputs(x, r, i, z, A, r_bias, i_bias, blend)
     S = state.shape[0]
     pool = _plain(state, "state", (S, D), torch.float32, dev)
+    if code == MAMBA_F32:                      # as _apart, by the addresses at hand; inputs of another type are no states
+        hi = pool + 4 * S * D
+        for at, s in zip(ins, strides):
+            if at is not None and at < hi and pool < at + 4 * ((B - 1) * s + D):
+                raise ValueError("state must not overlap the inputs")
     rows = _plain(slots, "slots", (B,), torch.int32, dev)
     out_dt = in_dt if out_dtype is None else out_dtype
     with _there(dev, stream):
@@ -1036,7 +1048,7 @@ def glr_update(state, x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *,
             yp = y.data_ptr()
         else:
             yp = _plain(y, "y", shape, out_dt, dev)
-            _apart(y, "y", (x, r, i, z), strides)
+            _apart(y, "y", (x, r, i, z), strides, (state, A, r_bias, i_bias, slots))
         st = lib().mamba_glr_update(pool, rows, *ins, yp, B, D, S, *strides, code,
                                     _dtype_code(y), FLAG_BLEND if blend else 0, _raw_stream(dev, stream))
     if st != 0:
@@ -1084,7 +1096,7 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms
             yp = y.data_ptr()
         else:
             yp = _plain(y, "y", x.shape, out_dt, dev)
-            _apart(y, "y", (x, z), sizes[4:])
+            _apart(y, "y", (x, z), sizes[4:], (weight, bias))
         workspace = _workspace(workspace, layer_norm_workspace_size(*sizes[:4]), dev)
         st = lib().mamba_layer_norm_fwd(*ins, yp, *sizes, eps, code, _dtype_code(y),
                                         FLAG_RMS if rms else 0, _addr(workspace), _nbytes(workspace),
