@@ -128,37 +128,31 @@ __global__ __launch_bounds__(1024) void glr_fwd_kernel(GlrParams p) {
   }
 }
 
-// One token: kV consecutive channels of a row per thread.
-template <typename T, typename O, bool kBlend, int kV>
+// One token: a channel of a row per thread.
+template <typename T, typename O, bool kBlend>
 __global__ __launch_bounds__(256) void glr_update_kernel(GlrParams p) {
-  const int64_t per_row = (p.D + 256 * kV - 1) / (256 * kV);
+  const int64_t per_row = (p.D + 255) / 256;
   const int64_t b = blockIdx.x / per_row;
-  const int64_t d0 = (blockIdx.x - b * per_row) * (256 * kV) + (int64_t)threadIdx.x * kV;
-  if (d0 >= p.D) return;
+  const int64_t d = (blockIdx.x - b * per_row) * 256 + threadIdx.x;
+  if (d >= p.D) return;
   const int64_t slot = p.slots ? (int64_t)p.slots[b] : b;
   const bool on = slot >= 0 && slot < p.n_slots;          // uniform over the workgroup
   const T* x = static_cast<const T*>(p.x) + b * p.x_stride;
   const T* r = static_cast<const T*>(p.r) + b * p.r_stride;
   const T* ig = static_cast<const T*>(p.i) + b * p.i_stride;
   const T* z = static_cast<const T*>(p.z) + b * p.z_stride;
-  O* y = static_cast<O*>(p.y) + b * p.D;
-  float* st = p.final_state + (on ? slot : 0) * p.D;
-#pragma unroll
-  for (int k = 0; k < kV; ++k) {
-    const int64_t d = d0 + k;
-    if (d >= p.D) break;
-    float o = 0.0f;
-    if (on) {
-      const GlrGate g = glr_gate<kBlend>(get1(r + d), p.r_bias ? -p.r_bias[d] * kLog2e : 0.0f,
-                                         kBlend ? 0.0f : p.A[d] * kLog2e);
-      float u = g.n * get1(x + d);
-      if (p.i) u *= sigmoid(get1(ig + d) + (p.i_bias ? p.i_bias[d] : 0.0f));
-      const float h = __builtin_fmaf(g.a, st[d], u);
-      st[d] = h;
-      o = p.z ? h * silu(get1(z + d)) : h;
-    }
-    put1(y + d, o);
+  float o = 0.0f;
+  if (on) {
+    float* st = p.final_state + slot * p.D;
+    const GlrGate g = glr_gate<kBlend>(get1(r + d), p.r_bias ? -p.r_bias[d] * kLog2e : 0.0f,
+                                       kBlend ? 0.0f : p.A[d] * kLog2e);
+    float u = g.n * get1(x + d);
+    if (p.i) u *= sigmoid(get1(ig + d) + (p.i_bias ? p.i_bias[d] : 0.0f));
+    const float h = __builtin_fmaf(g.a, st[d], u);
+    st[d] = h;
+    o = p.z ? h * silu(get1(z + d)) : h;
   }
+  put1(static_cast<O*>(p.y) + b * p.D + d, o);
 }
 
 template <typename T>
@@ -194,8 +188,8 @@ hipError_t fwd_t(const GlrParams& p, hipStream_t s) {
 template <typename T, typename O>
 hipError_t upd_t(const GlrParams& p, hipStream_t s) {
   const unsigned wgs = (unsigned)(p.B * ((p.D + 255) / 256));
-  if (p.blend) hipLaunchKernelGGL((glr_update_kernel<T, O, true, 1>), dim3(wgs), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((glr_update_kernel<T, O, false, 1>), dim3(wgs), dim3(256), 0, s, p);
+  if (p.blend) hipLaunchKernelGGL((glr_update_kernel<T, O, true>), dim3(wgs), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((glr_update_kernel<T, O, false>), dim3(wgs), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
