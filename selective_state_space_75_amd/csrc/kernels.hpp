@@ -278,16 +278,20 @@ struct NormParams {
 //   kNormColLong  channel-major, fewer than 8 tokens
 //   kNormRowTeam  token-major, 8 to 512 channels: teams of 2^k <= 64 lanes, 8 channels each
 //   kNormRowBlock token-major, up to 8192 channels: a workgroup, 8 channels a thread
+//   kNormRowWide  token-major, up to 16384 channels: a workgroup, 2 x 8 channels a thread
 //   kNormRowLong  token-major, any group
 enum NormKind : int { kNormShapes = 4, kNormBwdShapes = 3, kNormColTwo = 4, kNormColLong, kNormRowTeam, kNormRowBlock,
                       kNormRowWide, kNormRowLong };
 
 struct NormShape {
   int threads, lanes, chans;                    // workgroup, token lanes of 8 tokens, channels of a thread
-  int cu, cu_gate;                              // backward: workgroups that a CU's registers hold, without and with z
+  int cu, cu_gate;                              // backward: workgroups of a CU that the plan counts on, without and with z
 };
 // Token lanes make whole cache lines of 128 bytes.  For 2-byte and 4-byte inputs (backward: with a 4-byte
-// array among them).
+// array among them).  cu and cu_gate are what the registers of the shape's types hold, the fewest of them, with one
+// exception: {256, 4, 2} with z, all arrays fp32, has 130 registers, so a CU holds three, and four are counted on.  Four against three, in
+// us: 12 heads of 80, 3 x 1003 tokens: 21.3, 21.4; 4 x 5120 channels, L = 2048, in 40 groups: 178, 202, in 64: 227, 208; 8 x 2000 in
+// 25, L = 777: 52.7, 50.0 (with bf16 x or dy, where four fit: 138, 142; 150, 144; 37.6, 40.8).
 constexpr NormShape kNormFwd2[kNormShapes] = {{256, 8, 4}, {256, 8, 16}, {512, 8, 16}, {1024, 8, 16}};
 constexpr NormShape kNormFwd4[kNormShapes] = {{256, 4, 4}, {256, 4, 8}, {512, 4, 8}, {512, 4, 20}};
 constexpr NormShape kNormBwd2[kNormBwdShapes] = {{256, 8, 4, 4, 3}, {256, 8, 8, 3, 2}, {512, 8, 8, 1, 1}};
