@@ -24,23 +24,25 @@
  *              projection's output.  Those of absent inputs are not looked at.
  *   A        : (D) fp32, below zero; NULL with MAMBA_FLAG_BLEND.  (A = 0 keeps the state
  *              and takes no input; the gradient of A is infinite there, and comes out as very
- *              large numbers.  A > 0 gives NaN.)
- *   r_bias, i_bias : (D) fp32 or NULL (zeros).
+ *              large numbers.  A below -2e38, -inf too, counts as -2e38: nothing of the state is kept.
+ *              A > 0 gives NaN.)
+ *   r_bias, i_bias : (D) fp32 or NULL (zeros).  An infinite one holds its gate open or closed.
  *   states   : (B, D) fp32.
  *   lengths  : (B) int32 on the device, or NULL (every row has L tokens).
  *              Row b ends after lengths[b] tokens (values are held to 0 .. L):
  *              what its inputs hold behind that is not looked at, be it NaN,
  *              its outputs and gradients there are zero, and its final state is
- *              the one after lengths[b] tokens.
+ *              the one after lengths[b] tokens (of none: the initial state, whatever the
+ *              channel's parameters hold).
  *
  * Sizes: B, D, L >= 1; B*D*L < 2^46, strides < 2^46 / B; and no launch of 2^32 threads or more:
  * B*D*(ceil(L/512) + ceil(L/2048)) < 2^26 is enough (mamba_glr_update: B*ceil(D/256) < 2^24).  in_dtype and the
  * output dtypes may each be MAMBA_F32 or MAMBA_BF16.  Alignment: every array to its element
  * size; workspaces 256 bytes.
- * A NaN or an infinity among the inputs of a token leaves the outputs of the tokens before it
- * as they are; from that token on, every output and state that it reaches is NaN or
- * infinite.  In the backward pass any gradient of such a channel may be NaN, in the batch row
- * that holds it, and that channel's sums.
+ * A NaN among the inputs of a token leaves the outputs of the tokens before it as they are;
+ * from that token on, every output and state that it reaches is NaN.  So does an infinite x or z, with
+ * NaN or infinities; an infinite r or i is a gate wholly open or closed.  In the backward pass any
+ * gradient of such a channel may be NaN, in the batch row that holds it, and that channel's sums.
  * State, gates and sums are fp32.  The results are deterministic (sums in a fixed order, no
  * atomics): the same call gives the same bits.  Past 256 tokens, B, like every other size, takes part in
  * the choice of how a row is cut over waves and segments, and those agree to fp32 rounding only.
@@ -66,7 +68,8 @@ size_t mamba_glr_workspace_size(int64_t B, int64_t D, int64_t L);
  * The recurrence over whole sequences.
  *   initial_state : (B, D) fp32 or NULL (zeros).
  *   y             : (B, D, L) out_dtype, written, dense.
- *   final_state   : (B, D) fp32, written, or NULL.
+ *   final_state   : (B, D) fp32, written, or NULL.  Not the initial state's array: where a row is
+ *                   cut into segments, some read the one while another writes the other.
  */
 int mamba_glr_fwd(const void* x, const void* r, const void* i, const void* z, const float* A,
                   const float* r_bias, const float* i_bias, const float* initial_state,

@@ -1,8 +1,8 @@
 /*
  * mamba_norm.h -- C ABI of the layer norm over channels: the norm in front of a
- * block, and the norm per head of a layer's output with the output gate that
- * mamba_gdr_fwd and mamba_ssd_fwd leave to what follows them.  The conventions of
- * mamba_scan.h hold.
+ * block, and the norm per head of a layer's output with an output gate, which
+ * mamba_gdr_fwd leaves to what follows it (mamba_ssd_fwd and mamba_glr_fwd take a z of
+ * their own, in front of the norm, or none).  The conventions of mamba_scan.h hold.
  *
  * For every token (b, t) and group of Dg = D / groups consecutive channels:
  *     xh = (x - mean) / sqrt(var + eps)          (var: the mean of (x - mean)^2)
@@ -18,7 +18,8 @@
  * threads or more: D < 2^27, B*groups*ceil(L/32) < 2^22 and B*D*ceil(L/64) < 2^29 are enough.
  * in_dtype and the output dtypes may each be MAMBA_F32 or MAMBA_BF16.  eps >= 0.  Alignment: every array to
  * its element size; workspaces 256 bytes.  Statistics and sums are fp32; the variance is taken
- * around the mean, or around one of the numbers for a few of them, never as a difference of large squares.  A NaN
+ * around the mean, or around one of the numbers for a few of them, never as a difference of large squares.  (The mean is
+ * rounded to fp32, so x - mean is off by 2^-24 of a large offset; numbers more than 1e17 from the mean may overflow the variance.)  A NaN
  * or an infinity stays in its own token and group (dweight and dbias aside).  Deterministic: sums in a
  * fixed order, no atomics: the same call gives the same bits.  B takes part in how channel-major groups of more
  * than 256 channels are cut, which agrees to fp32 rounding; token-major rows and smaller groups have the

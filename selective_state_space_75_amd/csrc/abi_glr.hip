@@ -33,7 +33,7 @@ bool all_aligned(std::initializer_list<const void*> ptrs, size_t a) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Test knobs (mamba_glr_set_test_knobs), read once per call.
+// Test knobs (mamba_glr_set_test_knobs), read while a call's plan is made.
 std::atomic<int> g_waves{0};
 std::atomic<int64_t> g_segments{0};
 

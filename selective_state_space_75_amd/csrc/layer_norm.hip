@@ -384,9 +384,11 @@ NormPlan norm_plan(int64_t B, int64_t D, int64_t L, int64_t G, int in_width, int
     return q;
   }
   // Backward, workgroups that fill the chip and no more: every part of the weight's sums is written and read.
-  // Token-major that is one a CU, or two where the registers hold two (a group's one team of up to 640 threads, no gate,
+  // Token-major that is one a CU, or two for one team of up to 640 threads (4097 to 5120 channels), no gate,
   // 2-byte numbers: 8192 tokens of 5120 channels, bf16, 66 us, with one 76; fp32 110, 105; gated 109, 108; of 512
-  // channels, where one workgroup holds 1024 threads, 17.5, 13.6; of 7168, 99, 92).  Forward (kNormRowBlock,
+  // channels, where one workgroup holds 1024 threads, 17.5, 13.6; of 7168, 99, 92.  The registers hold two of 704 or 768
+  // threads as well, which is faster for many tokens and slower for few (one, two; one set of arrays: 8192 tokens of 2816
+  // channels 34.8, 31.7, of 5632 63.9, 55.1, of 6144 64.2, 57.4; 1000 tokens 17.6, 17.4; 19.8, 22.0; 19.8, 22.3).  Forward (kNormRowBlock,
   // kNormRowWide) a CU gets the power of two that makes up to 2048 threads: two workgroups of 640 for 5120 channels
   // 33 us, three 38; two of 896 for 7168 channels 51 us, one 68.
   const bool two = q.kind == kNormRowBlock && q.threads <= 640 && !gate && in_width + grad_width == 4;
