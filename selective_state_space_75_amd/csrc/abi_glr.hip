@@ -54,7 +54,7 @@ void cut(GlrPlan& q, int64_t L, int64_t S) {
 
 // Short rows go several to a wave (unless a test asks for waves or segments).  32768 rows, bf16, forward and backward in us,
 // with a wave a row before: 8 tokens 6 (30) and 10 (63), 64: 11 (30), 18 (62), 100: 15 (46), 28 (90), 256: 24 (30),
-// 47 (62); with a row a wave, 512: 48 (36), 84 (66), so not past 256.
+// 45 (62); with a row a wave, 512: 48 (36), 84 (66), so not past 256.
 constexpr int64_t kShort = 256;
 bool short_rows(GlrPlan& q, int64_t L) {
   if (L > kShort || g_waves.load() > 0 || g_segments.load() > 0) return false;

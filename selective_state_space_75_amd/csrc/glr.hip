@@ -11,7 +11,7 @@
 //
 // Every input is read once and every output written once, and HBM bounds it where there are rows enough: 20480 rows,
 // L = 2048, bf16 with both gates, 76 us for 419 MB, 5.5 TB/s where a plain copy reaches 5.1; 4096 rows,
-// L = 32768, 248 us for 1.34 GB, 5.4 TB/s.  Vector instructions take 0.8 to 0.9 of the issue cycles beside that (the
+// L = 32768, 248 us for 1.34 GB, 5.4 TB/s.  Vector instructions take 0.75 to 0.86 of the issue cycles beside that (the
 // exponentials of three gates a token), so there is little left on either side.  One token of 4096 channels takes
 // 3 us on the GPU.
 #include "glr.hpp"

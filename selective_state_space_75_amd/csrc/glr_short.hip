@@ -3,7 +3,7 @@
 // The mathematics of glr.hip and glr_bwd.hip, with several rows in a wave: a row has `p.lanes` neighbouring lanes (a power
 // of two, 8 tokens each), scans and sums run over those, and a workgroup of four waves takes 256 / lanes rows.
 // A wave per row would leave most lanes without a token, and the chip waiting for workgroups that do next to nothing:
-// 32768 rows of 8 tokens, bf16: forward 30 us so, 6 here, backward 63, 10; of 256 tokens 30, 24 and 62, 47 (HBM 16, 30).
+// 32768 rows of 8 tokens, bf16: forward 30 us so, 6 here, backward 63, 10; of 256 tokens 30, 24 and 62, 45 (HBM 16, 30).
 // Up to 64 tokens a row the launch and one round trip to memory bound it, then the shuffles of the scans beside HBM.
 #include "glr.hpp"
 
