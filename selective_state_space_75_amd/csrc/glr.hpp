@@ -242,16 +242,14 @@ struct GlrGate {
 template <bool kBlend>
 __device__ __forceinline__ GlrGate glr_gate(float r, float nb, float A2) {
   GlrGate o;
-  float e = hw_exp2(__builtin_fmaf(r, -kLog2e, nb));
+  const float e = hw_exp2(__builtin_fmaf(r, -kLog2e, nb));
+  o.s = hw_rcp(1.0f + e);
+  o.c = one_less(o.s, e);
   if constexpr (kBlend) {
-    e = e > 0x1p126f ? 0x1p126f : e;           // a comparison, so that a NaN stays one (the hardware's minimum drops it)
-    o.s = hw_rcp(1.0f + e);
-    o.a = o.c = e * o.s;
+    o.a = o.c;
     o.n = o.s;
     o.ra = 0.0f;
   } else {
-    o.s = hw_rcp(1.0f + e);
-    o.c = one_less(o.s, e);
     const float x2 = A2 * o.s;
     o.a = hw_exp2(x2);
     float q = glr_rest(x2, o.a);
