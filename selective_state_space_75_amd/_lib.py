@@ -1026,7 +1026,8 @@ def glr_update(state, x, r, i=None, A=None, r_bias=None, i_bias=None, z=None, *,
                out_dtype=None, y=None, stream=None):
     """One token of the gated linear recurrence for every row; `state` (S, D) fp32 is updated in
     place at the rows' slots (int32 (B); None: row b has state b; negative: an empty row, y = 0).
-    x, r, i, z: (B, D).  Returns y (B, D)."""
+    x, r, i, z: (B, D).  Returns y (B, D).  A y passed in must lie apart from state and the inputs, and
+    those apart from state (ValueError)."""
     torch = _torch()
     dev, in_dt, code = _first(x, (2,), "(B, D)")
     B, D = shape = x.shape
@@ -1086,7 +1087,7 @@ def layer_norm_fwd(x, weight=None, bias=None, z=None, *, groups=1, eps=1e-5, rms
     with the output gate (include/mamba_norm.h): (xh weight + bias) silu(z), xh = (x - mean) /
     sqrt(var + eps), or x / sqrt(mean x^2 + eps) with rms=True.  x, z: (B, D, L), or (rows, D) for
     token-major rows; both may be channel ranges of a wider tensor.  weight, bias: (D) fp32 or None.
-    Returns y like x, in out_dtype."""
+    Returns y like x, in out_dtype.  A y passed in must lie apart from the inputs (ValueError)."""
     torch = _torch()
     dev, code, ins, sizes = _norm_inputs(x, weight, bias, z, groups)
     out_dt = x.dtype if out_dtype is None else out_dtype

@@ -144,8 +144,8 @@ __global__ __launch_bounds__(256) void glr_update_kernel(GlrParams p) {
   float o = 0.0f;
   if (on) {
     float* st = p.final_state + slot * p.D;
-    const GlrGate g = glr_gate<kBlend>(get1(r + d), p.r_bias ? -p.r_bias[d] * kLog2e : 0.0f,
-                                       kBlend ? 0.0f : p.A[d] * kLog2e);
+    const GlrChannel channel = glr_channel<kBlend>(p, d, 1);
+    const GlrGate g = glr_gate<kBlend>(get1(r + d), channel.rb, channel.A2);
     float u = g.n * get1(x + d);
     if (p.i) u *= sigmoid(get1(ig + d) + (p.i_bias ? p.i_bias[d] : 0.0f));
     const float h = __builtin_fmaf(g.a, st[d], u);

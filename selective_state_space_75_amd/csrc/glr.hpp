@@ -238,7 +238,7 @@ struct GlrGate {
 };
 
 // nb: -bias log2(e); A2: A log2(e), both as glr_channel holds them.  r = -inf stands for a token that is not there: s = 0, a = 1.
-// n is held to 3e-19 or more, so that its reciprocal stays finite where s underflows.
+// Decay rule: n is held to 3e-19 or more, so that its reciprocal stays finite where s underflows.
 template <bool kBlend>
 __device__ __forceinline__ GlrGate glr_gate(float r, float nb, float A2) {
   GlrGate o;

@@ -207,3 +207,22 @@ def test_absent_tokens_leave_nothing_in_the_sums(blend, L, waves, segments, dev)
         assert torch.equal(g["dinitial_state"], t["dfinal_state"])
         for n in ("dr", "dA", "dr_bias"):
             assert g[n] is None or not g[n].any(), n
+
+
+@pytest.mark.parametrize("name,value,blend", [(n, v, blend) for n in ("r_bias", "i_bias") for v in (np.inf, -np.inf)
+                                              for blend in (True, False)] + [("A", -np.inf, False), ("A", -3.4e38, False)])
+def test_infinite_parameters_in_one_token(name, value, blend, dev):
+    """As in a sequence of one token, also where r closes the gate to its last bit."""
+    import torch
+    import selective_state_space_75_amd as m
+    from test_glr_gpu import E, near
+    x = make(4, D, 1, "f32", 150, blend, True, True, True)
+    x[name][CH] = value
+    x["r"][2] = -200.0
+    t = put(x, dev, NAMES)
+    y, h = m.glr_fwd(*args(t), blend=blend, initial_state=t["initial_state"], return_final_state=True)
+    pool = t["initial_state"].clone()
+    y1 = m.glr_update(pool, *args({**t, **{k: t[k].squeeze(2) for k in ("x", "r", "i", "z")}}), blend=blend)
+    torch.cuda.synchronize()
+    near(y1, from_dev(y)[..., 0], E, "y")
+    near(pool, from_dev(h), E, "state")
